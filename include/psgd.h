@@ -57,6 +57,7 @@ typedef enum { PSGD_F32 = 0, PSGD_F16 = 1, PSGD_BF16 = 2 } psgd_dtype;
 
 #define PSGD_OK 0
 #define PSGD_SKIPPED_NONFINITE 1 /* [AMP] inf/NaN seen: step skipped, state kept   */
+#define PSGD_BAD_TOKEN 2         /* an embedding met an id outside its table       */
 #define PSGD_EINVAL (-1)         /* bad argument                                   */
 #define PSGD_ENOMEM (-2)         /* device or host allocation failed               */
 #define PSGD_ECUDA (-3)          /* a CUDA call failed                             */
@@ -503,6 +504,160 @@ int psgd_dp_project(psgd_state* s, void* stream, float** exchange, int64_t* coun
  * order), PSGD_ECUDA.
  */
 int psgd_dp_finish(psgd_state* s, void* stream);
+
+/*
+ * Training operators -- what fills the buckets.
+ *
+ * The gradients that psgd_step compresses come from a training step.  These
+ * operators compute the parts of one that hang on a vocabulary and on the
+ * normalisations between the matrix products: the embedding's lookup and the
+ * dense gradient of its table, layer norm forward and backward, and
+ * distillation from a teacher's top logits.  Each writes parameter gradients
+ * straight into a caller's bucket: at any element offset, in the bucket's
+ * type, replacing what is there or adding to it.
+ *
+ * Common to all of them:
+ *   - dtype arguments name the type of the elements (F32, F16, BF16); all
+ *     arithmetic and every sum is fp32, rounded once into an output.
+ *   - strides are in elements and non-negative; rows are contiguous inside.
+ *     Outputs may have any element alignment; operands whose addresses and
+ *     strides are multiples of 16 bytes are accessed 16 bytes at a time.
+ *   - an output may overlap no other operand unless the call says so.
+ *   - calls enqueue on `stream` and never synchronise; results are the same
+ *     bits on every run on the same GPU model.
+ */
+
+/*
+ * Embedding -- a table of `vocab` rows of `dim` elements.
+ *
+ * The handle holds the workspace of the gradient (the sorted tokens and the
+ * partial rows) for up to max_tokens tokens a call; calls on one handle must
+ * not overlap on the GPU (order them on one stream, or with events).
+ */
+typedef struct psgd_embedding psgd_embedding; /* opaque, library-owned */
+
+/* Errors: PSGD_EINVAL (vocab outside [1, 2^31 - 2], dim outside [1, 2^20],
+ * max_tokens outside [0, 2^31 - 256], device above 63), PSGD_ENOMEM,
+ * PSGD_ECUDA.  *out is NULL on failure. */
+int psgd_embedding_create(int64_t vocab, int64_t dim, int64_t max_tokens, int32_t device, psgd_embedding** out);
+void psgd_embedding_destroy(psgd_embedding* e); /* NULL is a no-op */
+size_t psgd_embedding_workspace_bytes(const psgd_embedding* e);
+
+/*
+ * psgd_embedding_forward -- out_i = scale * weight[id_i].
+ *
+ *   weight : vocab rows, weight_stride apart.
+ *   ids    : id_bits (32 or 64) bit signed integers, an (outer, inner) array:
+ *            token (o, n) at o * ids_outer_stride + n * ids_inner_stride.
+ *            An id outside [0, vocab) gives a row of zeros and is reported by
+ *            psgd_embedding_status.
+ *   out    : the tokens' rows, in the same (outer, inner) layout with strides
+ *            of its own; rows must not overlap.
+ * Errors: PSGD_EINVAL, PSGD_ECUDA.
+ */
+int psgd_embedding_forward(psgd_embedding* e, const void* weight, psgd_dtype weight_dtype, int64_t weight_stride,
+                           const void* ids, int32_t id_bits, int64_t outer, int64_t inner,
+                           int64_t ids_outer_stride, int64_t ids_inner_stride, float scale, void* out,
+                           psgd_dtype out_dtype, int64_t out_outer_stride, int64_t out_inner_stride, void* stream);
+
+/*
+ * psgd_embedding_backward -- the gradient of the whole table:
+ *   dweight_v = [dweight_v +] scale * sum over the tokens i with id_i = v of grad_i,
+ * zero (or unchanged, with accumulate) for a row that no token names.
+ *
+ *   ids, grad   : as psgd_embedding_forward's ids and out; grad rows may
+ *                 overlap (a broadcast gradient has stride 0).
+ *   padding_idx : tokens with this id add nothing; -1: none.  Neither does an
+ *                 id outside [0, vocab), which psgd_embedding_status reports.
+ *   accumulate  : 0: dweight is overwritten; 1: added to.
+ * The tokens are sorted by id; each row's sum runs over them in position
+ * order, in chunks of fixed length.
+ * Errors: PSGD_EINVAL (more than max_tokens tokens among them), PSGD_ECUDA.
+ */
+int psgd_embedding_backward(psgd_embedding* e, const void* ids, int32_t id_bits, int64_t outer, int64_t inner,
+                            int64_t ids_outer_stride, int64_t ids_inner_stride, const void* grad,
+                            psgd_dtype grad_dtype, int64_t grad_outer_stride, int64_t grad_inner_stride,
+                            float scale, int64_t padding_idx, int32_t accumulate, void* dweight,
+                            psgd_dtype dweight_dtype, int64_t dweight_stride, void* stream);
+
+/* Synchronises `stream`; PSGD_BAD_TOKEN if a call enqueued on it since the last
+ * status call (or creation) met an id outside the table, else PSGD_OK. */
+int psgd_embedding_status(psgd_embedding* e, void* stream);
+
+/*
+ * Layer norm over rows of `dim` elements.  The handle holds the partial sums
+ * of the parameters' gradients; backward calls on one handle must not overlap
+ * on the GPU, forward calls may.
+ */
+typedef struct psgd_layernorm psgd_layernorm; /* opaque, library-owned */
+
+/* Errors: PSGD_EINVAL (dim outside [1, 2^20], device above 63), PSGD_ENOMEM,
+ * PSGD_ECUDA.  *out is NULL on failure. */
+int psgd_layernorm_create(int64_t dim, int32_t device, psgd_layernorm** out);
+void psgd_layernorm_destroy(psgd_layernorm* n); /* NULL is a no-op */
+size_t psgd_layernorm_workspace_bytes(const psgd_layernorm* n);
+
+/*
+ * psgd_layernorm_forward -- y = (x - mean) rstd weight + bias per row, with
+ * rstd = (mean((x - mean)^2) + eps)^-1/2.
+ *
+ *   x, y         : `rows` rows of `dtype`, x_stride / y_stride apart.
+ *   weight, bias : dim elements of param_dtype; NULL: 1 and 0.
+ *   mean, rstd   : out, one float a row (what the backward pass takes); may be
+ *                  NULL.
+ * Errors: PSGD_EINVAL, PSGD_ECUDA.
+ */
+int psgd_layernorm_forward(psgd_layernorm* n, const void* x, psgd_dtype dtype, int64_t x_stride, int64_t rows,
+                           const void* weight, const void* bias, psgd_dtype param_dtype, float eps, void* y,
+                           int64_t y_stride, float* mean, float* rstd, void* stream);
+
+/*
+ * psgd_layernorm_backward -- with xh = (x - mean) rstd and a = grad weight:
+ *   dx      = rstd (a - mean(a) - xh mean(a xh))
+ *   dweight = [dweight +] sum over rows of grad xh
+ *   dbias   = [dbias +]   sum over rows of grad
+ *
+ *   grad, x, dx    : `rows` rows of `dtype`; dx may be NULL.
+ *   weight         : dim elements of param_dtype; NULL: 1.
+ *   dweight, dbias : dim elements of dparam_dtype; either may be NULL.  With
+ *                    no rows they become 0 (unchanged with accumulate).
+ * Errors: PSGD_EINVAL, PSGD_ECUDA.
+ */
+int psgd_layernorm_backward(psgd_layernorm* n, const void* grad, int64_t grad_stride, const void* x,
+                            psgd_dtype dtype, int64_t x_stride, int64_t rows, const float* mean, const float* rstd,
+                            const void* weight, psgd_dtype param_dtype, void* dx, int64_t dx_stride, void* dweight,
+                            void* dbias, psgd_dtype dparam_dtype, int32_t accumulate, void* stream);
+
+#define PSGD_DISTILL_MAX_K 1024 /* teacher entries per row */
+
+/*
+ * psgd_distill -- distillation of a student from a teacher's top logits.
+ * For every row, with T = temperature:
+ *   p_k     = softmax over the row's valid entries of teacher_k / T,
+ *   q       = softmax over the vocabulary of logits / T,
+ *   loss    = w T^2 sum_k p_k (log p_k - log q[index_k]),
+ *   dlogits = grad_scale w T (q_j - sum over the k with index_k = j of p_k).
+ *
+ *   logits  : `rows` rows of `vocab` elements of `dtype`.
+ *   teacher, index : `rows` rows of k teacher logits and of the vocabulary
+ *             entries (index_bits 32 or 64) they belong to.  An entry whose
+ *             index lies outside [0, vocab) is not valid: a row with fewer
+ *             than k entries is filled up with -1.  Equal indices add up.
+ *   weights : w, one float a row (a loss mask, or 1 / tokens); NULL: 1.
+ *   losses  : out, one float a row.
+ *   dlogits : out, rows of `dtype`; NULL: the losses only.  May be logits
+ *             itself (same stride).
+ * A row with w = 0, or with no valid entry whose teacher logit is above
+ * -infinity, has loss 0 and gradient 0 whatever its logits hold.  Otherwise
+ * a logit of -infinity has q_j = 0 (the loss is infinite if the teacher wants
+ * it), and NaN, +infinity or a row of nothing but -infinity gives NaN.
+ * Runs on the calling thread's current CUDA device.
+ * Errors: PSGD_EINVAL, PSGD_ECUDA.
+ */
+int psgd_distill(const void* logits, psgd_dtype dtype, int64_t logits_stride, int64_t rows, int64_t vocab,
+                 const void* teacher, psgd_dtype teacher_dtype, int64_t teacher_stride, const void* index,
+                 int32_t index_bits, int64_t index_stride, int32_t k, float temperature, const float* weights,
+                 float grad_scale, float* losses, void* dlogits, int64_t dlogits_stride, void* stream);
 
 /*
  * psgd_build_id -- "psgd-source-hash:" followed by the SHA-256 (32 hex

@@ -16,4 +16,8 @@ def __getattr__(name):
         from . import dp
 
         return getattr(dp, name)
+    if name in ("Embedding", "LayerNorm", "distill_loss"):
+        from . import training
+
+        return getattr(training, name)
     raise AttributeError(name)

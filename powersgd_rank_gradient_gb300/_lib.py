@@ -13,6 +13,7 @@ LIB_PATH = os.path.join(HERE, "libpsgd.so")
 
 PSGD_OK = 0
 PSGD_SKIPPED_NONFINITE = 1
+PSGD_BAD_TOKEN = 2
 PSGD_EINVAL = -1
 PSGD_ENOMEM = -2
 PSGD_ECUDA = -3
@@ -23,6 +24,7 @@ PSGD_BF16 = 2
 PSGD_MAX_RANK = 32
 PSGD_MAX_WORLD = 64
 PSGD_MAX_GROUP_STREAMS = 16
+PSGD_DISTILL_MAX_K = 1024
 
 # every symbol include/psgd.h declares
 EXPORTS = [
@@ -35,6 +37,10 @@ EXPORTS = [
     "psgd_group_create", "psgd_group_destroy", "psgd_group_step", "psgd_group_wait",
     "psgd_group_status", "psgd_group_bucket", "psgd_group_size", "psgd_set_graph", "psgd_graph_stats",
     "psgd_dp_create", "psgd_dp_begin", "psgd_dp_project", "psgd_dp_finish", "psgd_build_id",
+    "psgd_embedding_create", "psgd_embedding_destroy", "psgd_embedding_workspace_bytes",
+    "psgd_embedding_forward", "psgd_embedding_backward", "psgd_embedding_status",
+    "psgd_layernorm_create", "psgd_layernorm_destroy", "psgd_layernorm_workspace_bytes",
+    "psgd_layernorm_forward", "psgd_layernorm_backward", "psgd_distill",
 ]
 
 _lib = None
@@ -136,6 +142,35 @@ def lib():
     L.psgd_dp_project.restype = ctypes.c_int
     L.psgd_dp_finish.argtypes = [P, P]
     L.psgd_dp_finish.restype = ctypes.c_int
+    f32 = ctypes.c_float
+    L.psgd_embedding_create.argtypes = [c_i64, c_i64, c_i64, c_i32, ctypes.POINTER(P)]
+    L.psgd_embedding_create.restype = ctypes.c_int
+    L.psgd_embedding_destroy.argtypes = [P]
+    L.psgd_embedding_destroy.restype = None
+    L.psgd_embedding_workspace_bytes.argtypes = [P]
+    L.psgd_embedding_workspace_bytes.restype = ctypes.c_size_t
+    L.psgd_embedding_forward.argtypes = [P, P, c_i32, c_i64, P, c_i32, c_i64, c_i64, c_i64, c_i64, f32, P, c_i32,
+                                         c_i64, c_i64, P]
+    L.psgd_embedding_forward.restype = ctypes.c_int
+    L.psgd_embedding_backward.argtypes = [P, P, c_i32, c_i64, c_i64, c_i64, c_i64, P, c_i32, c_i64, c_i64, f32,
+                                          c_i64, c_i32, P, c_i32, c_i64, P]
+    L.psgd_embedding_backward.restype = ctypes.c_int
+    L.psgd_embedding_status.argtypes = [P, P]
+    L.psgd_embedding_status.restype = ctypes.c_int
+    L.psgd_layernorm_create.argtypes = [c_i64, c_i32, ctypes.POINTER(P)]
+    L.psgd_layernorm_create.restype = ctypes.c_int
+    L.psgd_layernorm_destroy.argtypes = [P]
+    L.psgd_layernorm_destroy.restype = None
+    L.psgd_layernorm_workspace_bytes.argtypes = [P]
+    L.psgd_layernorm_workspace_bytes.restype = ctypes.c_size_t
+    L.psgd_layernorm_forward.argtypes = [P, P, c_i32, c_i64, c_i64, P, P, c_i32, f32, P, c_i64, P, P, P]
+    L.psgd_layernorm_forward.restype = ctypes.c_int
+    L.psgd_layernorm_backward.argtypes = [P, P, c_i64, P, c_i32, c_i64, c_i64, P, P, P, c_i32, P, c_i64, P, P, c_i32,
+                                          c_i32, P]
+    L.psgd_layernorm_backward.restype = ctypes.c_int
+    L.psgd_distill.argtypes = [P, c_i32, c_i64, c_i64, c_i64, P, c_i32, c_i64, P, c_i32, c_i64, c_i32, f32, P, f32, P,
+                               P, c_i64, P]
+    L.psgd_distill.restype = ctypes.c_int
     L.psgd_build_id.argtypes = []
     L.psgd_build_id.restype = ctypes.c_char_p
     L.psgd_last_error.argtypes = []

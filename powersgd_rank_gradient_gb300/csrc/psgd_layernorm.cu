@@ -1,0 +1,596 @@
+// Layer norm over the last dimension, forward and backward.
+//
+//   forward   mu = mean(x), r = (mean((x - mu)^2) + eps)^-1/2, y = (x - mu) r w + b
+//   backward  xh = (x - mu) r, a = g w
+//             dx = r (a - mean(a) - xh mean(a xh)),  dw = sum_rows g xh,  db = sum_rows g
+//
+// One group of threads holds a whole row in registers, so every operand is
+// read once.  The variance is the mean of the squared deviations from the
+// mean (a second reduction over registers, no cancellation).  In the backward
+// pass each thread owns the same columns of every row it meets and keeps their
+// dw and db sums in fp32 registers; a CTA leaves one partial row and a second
+// kernel adds the partial rows in a fixed order.
+#include <algorithm>
+#include <new>
+
+#include "psgd_ops.cuh"
+
+struct psgd_layernorm {
+  int device = 0;
+  int sms = 0;
+  long long dim = 0;
+  int max_ctas = 0;       // partial rows
+  float* part = nullptr;  // max_ctas x 2 x dim
+  size_t bytes = 0;
+};
+
+namespace psgd {
+namespace ops {
+namespace {
+
+constexpr int kMaxThreads = 512;  // of a register kernel's CTA
+
+struct RowsArgs {
+  const void* x;
+  const void* g;   // backward
+  const void* w;
+  const void* b;
+  void* y;         // y (forward) or dx (backward)
+  float* mean;
+  float* rstd;
+  float* part;     // backward
+  long long xs, gs, ys;
+  long long rows;
+  int dim;
+  int pdtype;
+  float eps;
+};
+
+// Sums of N values over the `warps` warps of one thread group, returned to all
+// of its threads.  `buf` holds warps * N floats of this group; the caller
+// alternates between two of them, so one barrier per call suffices.
+template <int N>
+__device__ __forceinline__ void group_sum(float (&v)[N], float* buf, int warps, int warp, int lane, int group,
+                                          int threads) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) v[i] = warp_sum(v[i]);
+  if (warps == 1) return;
+  if (lane == 0) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) buf[warp * N + i] = v[i];
+  }
+  asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "r"(threads) : "memory");
+#pragma unroll
+  for (int i = 0; i < N; ++i) v[i] = 0.f;
+  for (int w = 0; w < warps; ++w) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] += buf[w * N + i];
+  }
+}
+
+// blockDim = (threads of a group, groups).  A group takes R rows at a time;
+// thread t owns the vectors t, t + threads, ... (NV of them) of each row.
+template <typename T, int VEC, int NV, int R>
+__global__ void __launch_bounds__(kMaxThreads) k_norm_forward(RowsArgs a) {
+  __shared__ float red[2][kMaxThreads / 32 * R];
+  const int t = threadIdx.x, group = threadIdx.y, threads = blockDim.x;
+  const int warps = threads / 32, warp = t >> 5, lane = t & 31;
+  float* buf[2] = {red[0] + group * warps * R, red[1] + group * warps * R};
+  const int nvec = a.dim / VEC;
+  const float inv = 1.f / (float)a.dim;
+  const long long step = (long long)gridDim.x * blockDim.y * R;
+  for (long long row0 = ((long long)blockIdx.x * blockDim.y + group) * R; row0 < a.rows; row0 += step) {
+    Pack<T, VEC> x[R][NV];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const T* src = (const T*)a.x + (row0 + r) * a.xs;
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        const int v = t + j * threads;
+        if (row0 + r < a.rows && v < nvec) x[r][j] = load_pack<T, VEC>(src + (long long)v * VEC);
+      }
+    }
+    float s[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      s[r] = 0.f;
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        if (row0 + r < a.rows && t + j * threads < nvec) {
+#pragma unroll
+          for (int k = 0; k < VEC; ++k) s[r] += to_f(x[r][j].v[k]);
+        }
+      }
+    }
+    group_sum<R>(s, buf[0], warps, warp, lane, group, threads);
+    float mean[R], q[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      mean[r] = s[r] * inv;
+      q[r] = 0.f;
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        if (row0 + r < a.rows && t + j * threads < nvec) {
+#pragma unroll
+          for (int k = 0; k < VEC; ++k) {
+            const float d = to_f(x[r][j].v[k]) - mean[r];
+            q[r] = fmaf(d, d, q[r]);
+          }
+        }
+      }
+    }
+    group_sum<R>(q, buf[1], warps, warp, lane, group, threads);
+    float rstd[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      rstd[r] = rsqrtf(fmaf(q[r], inv, a.eps));
+      if (t == 0 && row0 + r < a.rows) {
+        if (a.mean) a.mean[row0 + r] = mean[r];
+        if (a.rstd) a.rstd[row0 + r] = rstd[r];
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int v = t + j * threads;
+      if (v >= nvec) continue;
+      float w[VEC], b[VEC];
+#pragma unroll
+      for (int k = 0; k < VEC; ++k) {
+        w[k] = a.w ? load_any(a.w, a.pdtype, (long long)v * VEC + k) : 1.f;
+        b[k] = a.b ? load_any(a.b, a.pdtype, (long long)v * VEC + k) : 0.f;
+      }
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        if (row0 + r >= a.rows) continue;
+        float f[VEC];
+#pragma unroll
+        for (int k = 0; k < VEC; ++k) f[k] = fmaf((to_f(x[r][j].v[k]) - mean[r]) * rstd[r], w[k], b[k]);
+        store_pack<T, VEC>((T*)a.y + (row0 + r) * a.ys + (long long)v * VEC, f);
+      }
+    }
+  }
+}
+
+template <typename T, int VEC, int NV, int R>
+__global__ void __launch_bounds__(kMaxThreads) k_norm_backward(RowsArgs a) {
+  extern __shared__ float cols[];  // 2 x dim: the CTA's dw and db (more than one group only)
+  __shared__ float red[2][kMaxThreads / 32 * 2 * R];
+  const int t = threadIdx.x, group = threadIdx.y, threads = blockDim.x;
+  const int warps = threads / 32, warp = t >> 5, lane = t & 31;
+  const int nvec = a.dim / VEC;
+  const float inv = 1.f / (float)a.dim;
+  float dw[NV][VEC], db[NV][VEC], w[NV][VEC];
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    const int v = t + j * threads;
+#pragma unroll
+    for (int k = 0; k < VEC; ++k) {
+      dw[j][k] = db[j][k] = 0.f;
+      w[j][k] = v < nvec ? (a.w ? load_any(a.w, a.pdtype, (long long)v * VEC + k) : 1.f) : 0.f;
+    }
+  }
+  const long long step = (long long)gridDim.x * blockDim.y * R;
+  int flip = 0;
+  for (long long row0 = ((long long)blockIdx.x * blockDim.y + group) * R; row0 < a.rows; row0 += step) {
+    Pack<T, VEC> x[R][NV], g[R][NV];
+    float mean[R], rstd[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const bool in = row0 + r < a.rows;
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        const int v = t + j * threads;
+        if (in && v < nvec) {
+          x[r][j] = load_pack<T, VEC>((const T*)a.x + (row0 + r) * a.xs + (long long)v * VEC);
+          g[r][j] = load_pack<T, VEC>((const T*)a.g + (row0 + r) * a.gs + (long long)v * VEC);
+        }
+      }
+      mean[r] = in ? __ldg(a.mean + row0 + r) : 0.f;
+      rstd[r] = in ? __ldg(a.rstd + row0 + r) : 0.f;
+    }
+    float s[2 * R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      s[2 * r] = s[2 * r + 1] = 0.f;
+      const bool in = row0 + r < a.rows;
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        if (in && t + j * threads < nvec) {
+#pragma unroll
+          for (int k = 0; k < VEC; ++k) {
+            const float gv = to_f(g[r][j].v[k]);
+            const float xh = (to_f(x[r][j].v[k]) - mean[r]) * rstd[r];
+            const float av = gv * w[j][k];
+            s[2 * r] += av;
+            s[2 * r + 1] = fmaf(av, xh, s[2 * r + 1]);
+            dw[j][k] = fmaf(gv, xh, dw[j][k]);
+            db[j][k] += gv;
+          }
+        }
+      }
+    }
+    group_sum<2 * R>(s, red[flip] + group * warps * 2 * R, warps, warp, lane, group, threads);
+    flip ^= 1;
+    if (a.y) {
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        if (row0 + r >= a.rows) continue;
+        const float m0 = s[2 * r] * inv, m1 = s[2 * r + 1] * inv;
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+          const int v = t + j * threads;
+          if (v >= nvec) continue;
+          float f[VEC];
+#pragma unroll
+          for (int k = 0; k < VEC; ++k) {
+            const float xh = (to_f(x[r][j].v[k]) - mean[r]) * rstd[r];
+            f[k] = (to_f(g[r][j].v[k]) * w[j][k] - m0 - xh * m1) * rstd[r];
+          }
+          store_pack<T, VEC>((T*)a.y + (row0 + r) * a.ys + (long long)v * VEC, f);
+        }
+      }
+    }
+  }
+  if (!a.part) return;
+  float* out = a.part + (long long)blockIdx.x * 2 * a.dim;
+  if (blockDim.y > 1) {
+    // the groups' sums in group order
+    for (int y = 0; y < (int)blockDim.y; ++y) {
+      if (group == y) {
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+          const int v = t + j * threads;
+          if (v >= nvec) continue;
+#pragma unroll
+          for (int k = 0; k < VEC; ++k) {
+            const int c = v * VEC + k;
+            cols[c] = (y ? cols[c] : 0.f) + dw[j][k];
+            cols[a.dim + c] = (y ? cols[a.dim + c] : 0.f) + db[j][k];
+          }
+        }
+      }
+      __syncthreads();
+    }
+    for (int c = group * threads + t; c < 2 * a.dim; c += threads * blockDim.y) out[c] = cols[c];
+  } else {
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int v = t + j * threads;
+      if (v >= nvec) continue;
+#pragma unroll
+      for (int k = 0; k < VEC; ++k) {
+        out[v * VEC + k] = dw[j][k];
+        out[a.dim + v * VEC + k] = db[j][k];
+      }
+    }
+  }
+}
+
+// Rows too long for registers: one CTA a row, the row read once per reduction.
+__device__ __forceinline__ float block_sum(float v, float* buf) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  v = warp_sum(v);
+  __syncthreads();
+  if (lane == 0) buf[warp] = v;
+  __syncthreads();
+  v = 0.f;
+  for (int w = 0; w < (int)blockDim.x / 32; ++w) v += buf[w];
+  return v;
+}
+
+template <typename T> __global__ void __launch_bounds__(kMaxThreads) k_norm_forward_long(RowsArgs a) {
+  __shared__ float buf[kMaxThreads / 32];
+  const float inv = 1.f / (float)a.dim;
+  for (long long row = blockIdx.x; row < a.rows; row += gridDim.x) {
+    const T* x = (const T*)a.x + row * a.xs;
+    float s = 0.f;
+    for (int c = threadIdx.x; c < a.dim; c += blockDim.x) s += to_f(__ldg(x + c));
+    const float mean = block_sum(s, buf) * inv;
+    s = 0.f;
+    for (int c = threadIdx.x; c < a.dim; c += blockDim.x) {
+      const float d = to_f(__ldg(x + c)) - mean;
+      s = fmaf(d, d, s);
+    }
+    const float rstd = rsqrtf(fmaf(block_sum(s, buf), inv, a.eps));
+    if (threadIdx.x == 0) {
+      if (a.mean) a.mean[row] = mean;
+      if (a.rstd) a.rstd[row] = rstd;
+    }
+    T* y = (T*)a.y + row * a.ys;
+    for (int c = threadIdx.x; c < a.dim; c += blockDim.x)
+      y[c] = from_f<T>(fmaf((to_f(__ldg(x + c)) - mean) * rstd, a.w ? load_any(a.w, a.pdtype, c) : 1.f,
+                            a.b ? load_any(a.b, a.pdtype, c) : 0.f));
+  }
+}
+
+template <typename T> __global__ void __launch_bounds__(kMaxThreads) k_norm_dx_long(RowsArgs a) {
+  __shared__ float buf[kMaxThreads / 32];
+  const float inv = 1.f / (float)a.dim;
+  for (long long row = blockIdx.x; row < a.rows; row += gridDim.x) {
+    const T* x = (const T*)a.x + row * a.xs;
+    const T* g = (const T*)a.g + row * a.gs;
+    const float mean = a.mean[row], rstd = a.rstd[row];
+    float s0 = 0.f, s1 = 0.f;
+    for (int c = threadIdx.x; c < a.dim; c += blockDim.x) {
+      const float av = to_f(__ldg(g + c)) * (a.w ? load_any(a.w, a.pdtype, c) : 1.f);
+      s0 += av;
+      s1 = fmaf(av, (to_f(__ldg(x + c)) - mean) * rstd, s1);
+    }
+    const float m0 = block_sum(s0, buf) * inv, m1 = block_sum(s1, buf) * inv;
+    T* y = (T*)a.y + row * a.ys;
+    for (int c = threadIdx.x; c < a.dim; c += blockDim.x) {
+      const float xh = (to_f(__ldg(x + c)) - mean) * rstd;
+      y[c] = from_f<T>((to_f(__ldg(g + c)) * (a.w ? load_any(a.w, a.pdtype, c) : 1.f) - m0 - xh * m1) * rstd);
+    }
+  }
+}
+
+// dw and db of long rows: gridDim.y partial rows, each the sum of a
+// contiguous share of the rows in row order.
+template <typename T> __global__ void __launch_bounds__(256) k_norm_columns_long(RowsArgs a) {
+  const int c = blockIdx.x * blockDim.x + threadIdx.x;
+  if (c >= a.dim) return;
+  const long long per = (a.rows + gridDim.y - 1) / gridDim.y;
+  const long long r0 = blockIdx.y * per, r1 = min(a.rows, r0 + per);
+  float dw = 0.f, db = 0.f;
+  for (long long r = r0; r < r1; ++r) {
+    const float g = to_f(__ldg((const T*)a.g + r * a.gs + c));
+    const float xh = (to_f(__ldg((const T*)a.x + r * a.xs + c)) - __ldg(a.mean + r)) * __ldg(a.rstd + r);
+    dw = fmaf(g, xh, dw);
+    db += g;
+  }
+  a.part[(long long)blockIdx.y * 2 * a.dim + c] = dw;
+  a.part[(long long)blockIdx.y * 2 * a.dim + a.dim + c] = db;
+}
+
+// dw and db: the partial rows' sums, 32 columns a CTA, its warps over
+// interleaved partial rows, then the warps' sums in order.
+__global__ void __launch_bounds__(512) k_norm_columns(const float* __restrict__ part, int parts, int dim, void* dw,
+                                                      void* db, int dtype, int accumulate) {
+  __shared__ float sums[16][33];
+  const int x = threadIdx.x & 31, y = threadIdx.x >> 5;
+  const long long c = (long long)blockIdx.x * 32 + x;
+  float s = 0.f;
+  if (c < 2LL * dim)
+    for (int p = y; p < parts; p += 16) s += part[(long long)p * 2 * dim + c];
+  sums[y][x] = s;
+  __syncthreads();
+  if (y != 0 || c >= 2LL * dim) return;
+  s = sums[0][x];
+#pragma unroll
+  for (int w = 1; w < 16; ++w) s += sums[w][x];
+  void* out = c < dim ? dw : db;
+  if (!out) return;
+  const long long i = c < dim ? c : c - dim;
+  if (accumulate) s += read_any(out, dtype, i);
+  store_any(out, dtype, i, s);
+}
+
+// How a row is spread over threads.
+struct RowPlan {
+  int vec;      // elements per access: 16 bytes' worth, or 1
+  int nv;       // accesses per thread and row; 0: the row does not fit into registers
+  int threads;  // of a group
+  int groups;   // of a CTA
+};
+
+RowPlan plan_rows(long long dim, int vec) {
+  const int max_nv = vec == 1 ? 16 : 4;
+  const long long nvec = dim / vec;
+  RowPlan p{vec, 0, 0, 1};
+  for (int nv = vec == 1 ? 4 : 1; nv <= max_nv; nv *= 2) {
+    const long long threads = ((nvec + nv - 1) / nv + 31) / 32 * 32;
+    if (threads <= kMaxThreads) {
+      p.nv = nv;
+      p.threads = (int)threads;
+      p.groups = std::max(1, std::min(8, 256 / p.threads));
+      break;
+    }
+  }
+  return p;
+}
+
+// f(VEC, NV, R) for a plan, as compile-time constants.
+template <int V> struct Int {
+  static constexpr int value = V;
+};
+template <typename T, typename F> void with_plan(const RowPlan& p, bool few, F&& f) {
+  constexpr int V = Vec16<T>::N;
+  if (p.vec != 1) {
+    if (p.nv == 1) {
+      if (few) f(Int<V>(), Int<1>(), Int<1>());
+      else f(Int<V>(), Int<1>(), Int<4>());
+    } else if (p.nv == 2) {
+      f(Int<V>(), Int<2>(), Int<1>());
+    } else {
+      f(Int<V>(), Int<4>(), Int<1>());
+    }
+  } else {
+    if (p.nv == 4) f(Int<1>(), Int<4>(), Int<2>());
+    else if (p.nv == 8) f(Int<1>(), Int<8>(), Int<1>());
+    else f(Int<1>(), Int<16>(), Int<1>());
+  }
+}
+int rows_per_group(const RowPlan& p, bool few) { return p.vec != 1 ? (p.nv == 1 && !few ? 4 : 1) : (p.nv == 4 ? 2 : 1); }
+
+template <typename F> void by_dtype(int32_t d, F&& f) {
+  switch (d) {
+    case PSGD_F32: f((float*)nullptr); break;
+    case PSGD_F16: f((__half*)nullptr); break;
+    default: f((__nv_bfloat16*)nullptr); break;
+  }
+}
+
+bool vec_ok(const void* p, long long stride, int dtype) {
+  return !p || (aligned16(p) && (stride * dtype_size(dtype)) % 16 == 0);
+}
+
+int check_common(const char* who, const psgd_layernorm* h, int32_t dtype, int32_t pdtype, int64_t rows) {
+  const std::string w(who);
+  if (!h) return fail(PSGD_EINVAL, w + ": NULL layer norm");
+  if (!dtype_ok(dtype) || !dtype_ok(pdtype)) return fail(PSGD_EINVAL, w + ": unknown dtype");
+  if (rows < 0 || rows > kMaxElems) return fail(PSGD_EINVAL, w + ": bad row count");
+  return PSGD_OK;
+}
+
+int check_operand(const char* who, const char* what, const void* p, int64_t rows, int64_t dim, int64_t stride,
+                  bool written) {
+  const std::string w = std::string(who) + ": " + what;
+  if (rows > 0 && !p) return fail(PSGD_EINVAL, w + " is NULL");
+  if (!span_ok(rows, stride)) return fail(PSGD_EINVAL, w + ": bad row stride");
+  if (written && rows > 1 && stride < dim) return fail(PSGD_EINVAL, w + ": rows overlap");
+  return PSGD_OK;
+}
+
+}  // namespace
+}  // namespace ops
+}  // namespace psgd
+
+using namespace psgd;
+using namespace psgd::ops;
+
+extern "C" int psgd_layernorm_create(int64_t dim, int32_t device, psgd_layernorm** out) {
+  if (!out) return fail(PSGD_EINVAL, "psgd_layernorm_create: out is NULL");
+  *out = nullptr;
+  if (dim < 1 || dim > (1 << 20)) return fail(PSGD_EINVAL, "psgd_layernorm_create: dim must be in [1, 2^20]");
+  if (device < 0 || device >= 64) return fail(PSGD_EINVAL, "psgd_layernorm_create: device ordinal must be in [0, 63]");
+  int count = 0;
+  cudaError_t e = cudaGetDeviceCount(&count);
+  if (e != cudaSuccess) return cuda_fail("psgd_layernorm_create: cudaGetDeviceCount", e);
+  if (device >= count) return fail(PSGD_ECUDA, "psgd_layernorm_create: no such device");
+  psgd_layernorm* h = new (std::nothrow) psgd_layernorm;
+  if (!h) return fail(PSGD_ENOMEM, "psgd_layernorm_create: out of host memory");
+  DeviceScope scope(device);
+  h->device = device;
+  h->dim = dim;
+  e = cudaDeviceGetAttribute(&h->sms, cudaDevAttrMultiProcessorCount, device);
+  if (e == cudaSuccess) {
+    h->max_ctas = h->sms * 4;
+    h->bytes = (size_t)h->max_ctas * 2 * dim * 4;
+    e = cudaMalloc((void**)&h->part, h->bytes);
+  }
+  if (e != cudaSuccess) {
+    const int rc = cuda_fail("psgd_layernorm_create", e);
+    h->part = nullptr;
+    psgd_layernorm_destroy(h);
+    return rc;
+  }
+  *out = h;
+  return PSGD_OK;
+}
+
+extern "C" void psgd_layernorm_destroy(psgd_layernorm* h) {
+  if (!h) return;
+  {
+    DeviceScope scope(h->device);
+    if (h->part) cudaFree(h->part);
+  }
+  delete h;
+}
+
+extern "C" size_t psgd_layernorm_workspace_bytes(const psgd_layernorm* h) { return h ? h->bytes : 0; }
+
+extern "C" int psgd_layernorm_forward(psgd_layernorm* h, const void* x, psgd_dtype dtype, int64_t x_stride,
+                                      int64_t rows, const void* weight, const void* bias, psgd_dtype param_dtype,
+                                      float eps, void* y, int64_t y_stride, float* mean, float* rstd, void* stream) {
+  const char* who = "psgd_layernorm_forward";
+  int rc = check_common(who, h, dtype, param_dtype, rows);
+  if (!rc) rc = check_operand(who, "x", x, rows, h->dim, x_stride, false);
+  if (!rc) rc = check_operand(who, "y", y, rows, h->dim, y_stride, true);
+  if (rc) return rc;
+  if (!(eps >= 0.f) || !isfinite(eps)) return fail(PSGD_EINVAL, "psgd_layernorm_forward: eps must be finite and >= 0");
+  if (rows == 0) return PSGD_OK;
+  const long long yb = extent(rows, h->dim, y_stride, dtype), pb = h->dim * dtype_size(param_dtype);
+  if (overlap(y, yb, x, extent(rows, h->dim, x_stride, dtype)) || overlap(y, yb, weight, pb) ||
+      overlap(y, yb, bias, pb) || overlap(y, yb, mean, rows * 4) || overlap(y, yb, rstd, rows * 4))
+    return fail(PSGD_EINVAL, "psgd_layernorm_forward: y overlaps another operand");
+  DeviceScope scope(h->device);
+  const cudaStream_t st = (cudaStream_t)stream;
+  RowsArgs a{x, nullptr, weight, bias, y, mean, rstd, nullptr, x_stride, 0, y_stride, rows, (int)h->dim,
+             (int)param_dtype, eps};
+  const int full = 16 / dtype_size(dtype);
+  const bool vec = h->dim % full == 0 && vec_ok(x, x_stride, dtype) && vec_ok(y, y_stride, dtype);
+  const RowPlan p = plan_rows(h->dim, vec ? full : 1);
+  by_dtype(dtype, [&](auto* tt) {
+    using T = std::remove_pointer_t<decltype(tt)>;
+    if (p.nv == 0) {
+      k_norm_forward_long<T><<<(unsigned)std::min<long long>(rows, h->sms * 4), kMaxThreads, 0, st>>>(a);
+      return;
+    }
+    const bool few = rows <= (long long)h->sms * 4 * p.groups;
+    const long long ctas = (rows + (long long)p.groups * rows_per_group(p, few) - 1) / (p.groups * rows_per_group(p, few));
+    const unsigned grid = (unsigned)std::min<long long>(ctas, (long long)h->sms * std::max(1, 1024 / (p.threads * p.groups)));
+    with_plan<T>(p, few, [&](auto v, auto nv, auto r) {
+      k_norm_forward<T, decltype(v)::value, decltype(nv)::value, decltype(r)::value>
+          <<<grid, dim3(p.threads, p.groups), 0, st>>>(a);
+    });
+  });
+  const cudaError_t e = cudaGetLastError();
+  return e == cudaSuccess ? PSGD_OK : cuda_fail(who, e);
+}
+
+extern "C" int psgd_layernorm_backward(psgd_layernorm* h, const void* grad, int64_t grad_stride, const void* x,
+                                       psgd_dtype dtype, int64_t x_stride, int64_t rows, const float* mean,
+                                       const float* rstd, const void* weight, psgd_dtype param_dtype, void* dx,
+                                       int64_t dx_stride, void* dweight, void* dbias, psgd_dtype dparam_dtype,
+                                       int32_t accumulate, void* stream) {
+  const char* who = "psgd_layernorm_backward";
+  int rc = check_common(who, h, dtype, param_dtype, rows);
+  if (!rc) rc = check_operand(who, "grad", grad, rows, h->dim, grad_stride, false);
+  if (!rc) rc = check_operand(who, "x", x, rows, h->dim, x_stride, false);
+  if (!rc && dx) rc = check_operand(who, "dx", dx, rows, h->dim, dx_stride, true);
+  if (rc) return rc;
+  if (!dtype_ok(dparam_dtype)) return fail(PSGD_EINVAL, "psgd_layernorm_backward: unknown dtype");
+  if (rows > 0 && (!mean || !rstd)) return fail(PSGD_EINVAL, "psgd_layernorm_backward: mean or rstd is NULL");
+  const long long gb = extent(rows, h->dim, grad_stride, dtype), xb = extent(rows, h->dim, x_stride, dtype);
+  const long long db = dx ? extent(rows, h->dim, dx_stride, dtype) : 0, wb = h->dim * dtype_size(param_dtype);
+  const long long ob = h->dim * dtype_size(dparam_dtype);
+  for (const auto& o : {std::pair<const void*, long long>(dx, db), {dweight, ob}, {dbias, ob}})
+    if (overlap(o.first, o.second, grad, gb) || overlap(o.first, o.second, x, xb) ||
+        overlap(o.first, o.second, mean, rows * 4) || overlap(o.first, o.second, rstd, rows * 4) ||
+        overlap(o.first, o.second, weight, wb))
+      return fail(PSGD_EINVAL, "psgd_layernorm_backward: an output overlaps an input");
+  if (overlap(dx, db, dweight, ob) || overlap(dx, db, dbias, ob) || overlap(dweight, ob, dbias, ob))
+    return fail(PSGD_EINVAL, "psgd_layernorm_backward: the outputs overlap");
+  const bool params = dweight || dbias;
+  if (!params && (!dx || rows == 0)) return PSGD_OK;
+  DeviceScope scope(h->device);
+  const cudaStream_t st = (cudaStream_t)stream;
+  RowsArgs a{x, grad, weight, nullptr, dx, const_cast<float*>(mean), const_cast<float*>(rstd),
+             params ? h->part : nullptr, x_stride, grad_stride, dx_stride, rows, (int)h->dim, (int)param_dtype, 0.f};
+  const int full = 16 / dtype_size(dtype);
+  const bool vec = h->dim % full == 0 && vec_ok(x, x_stride, dtype) && vec_ok(grad, grad_stride, dtype) &&
+                   vec_ok(dx, dx_stride, dtype);
+  const RowPlan p = plan_rows(h->dim, vec ? full : 1);
+  int parts = 0;
+  if (rows > 0)
+    by_dtype(dtype, [&](auto* tt) {
+      using T = std::remove_pointer_t<decltype(tt)>;
+      if (p.nv == 0) {
+        if (dx) k_norm_dx_long<T><<<(unsigned)std::min<long long>(rows, h->sms * 4), kMaxThreads, 0, st>>>(a);
+        if (params) {
+          parts = (int)std::min<long long>((rows + 31) / 32, h->max_ctas);
+          k_norm_columns_long<T><<<dim3((unsigned)((h->dim + 255) / 256), parts), 256, 0, st>>>(a);
+        }
+        return;
+      }
+      const bool few = rows <= (long long)h->sms * 4 * p.groups;
+      const long long ctas =
+          (rows + (long long)p.groups * rows_per_group(p, few) - 1) / (p.groups * rows_per_group(p, few));
+      const unsigned grid =
+          (unsigned)std::min<long long>(ctas, (long long)h->sms * std::min(4, std::max(1, 1024 / (p.threads * p.groups))));
+      parts = (int)grid;
+      const size_t smem = p.groups > 1 ? (size_t)h->dim * 8 : 0;
+      with_plan<T>(p, few, [&](auto v, auto nv, auto r) {
+        k_norm_backward<T, decltype(v)::value, decltype(nv)::value, decltype(r)::value>
+            <<<grid, dim3(p.threads, p.groups), smem, st>>>(a);
+      });
+    });
+  cudaError_t e = cudaGetLastError();
+  if (e == cudaSuccess && params) {
+    k_norm_columns<<<(unsigned)((2 * h->dim + 31) / 32), 512, 0, st>>>(h->part, parts, (int)h->dim, dweight, dbias,
+                                                                      dparam_dtype, accumulate);
+    e = cudaGetLastError();
+  }
+  return e == cudaSuccess ? PSGD_OK : cuda_fail(who, e);
+}

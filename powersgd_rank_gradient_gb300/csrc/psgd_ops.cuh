@@ -1,0 +1,146 @@
+// Shared pieces of the training operators (embedding, layer norm,
+// distillation): element types, vector accesses, host-side argument checks.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+#include <math.h>
+#include <stdint.h>
+
+#include <string>
+
+#include "../../include/psgd.h"
+
+int psgd_internal_set_error(int code, const char* msg);
+
+namespace psgd {
+namespace ops {
+
+// ---- host side ---------------------------------------------------------------
+
+inline int fail(int code, const std::string& msg) { return psgd_internal_set_error(code, msg.c_str()); }
+
+inline int cuda_fail(const char* where, cudaError_t e) {
+  cudaGetLastError();
+  return fail(e == cudaErrorMemoryAllocation ? PSGD_ENOMEM : PSGD_ECUDA,
+              std::string(where) + ": " + cudaGetErrorString(e));
+}
+
+// Makes `dev` current for the enclosing scope.
+struct DeviceScope {
+  int prev = -1;
+  explicit DeviceScope(int dev) {
+    if (cudaGetDevice(&prev) != cudaSuccess) prev = -1;
+    if (prev != dev) cudaSetDevice(dev);
+    else prev = -1;
+  }
+  ~DeviceScope() {
+    if (prev >= 0) cudaSetDevice(prev);
+  }
+};
+
+inline bool dtype_ok(int32_t d) { return d == PSGD_F32 || d == PSGD_F16 || d == PSGD_BF16; }
+inline int dtype_size(int32_t d) { return d == PSGD_F32 ? 4 : 2; }
+inline bool aligned16(const void* p) { return ((uintptr_t)p & 15) == 0; }
+
+// Whether [a, a + an) and [b, b + bn) share a byte (NULL ranges share none).
+inline bool overlap(const void* a, long long an, const void* b, long long bn) {
+  if (!a || !b || an <= 0 || bn <= 0) return false;
+  const uintptr_t x = (uintptr_t)a, y = (uintptr_t)b;
+  return x < y + (uintptr_t)bn && y < x + (uintptr_t)an;
+}
+
+// Bytes from the first to one past the last element of `rows` rows of `cols`
+// elements, `stride` elements apart.
+inline long long extent(long long rows, long long cols, long long stride, int32_t dtype) {
+  return rows > 0 && cols > 0 ? ((rows - 1) * stride + cols) * dtype_size(dtype) : 0;
+}
+
+// Largest element count of one operand that the checks accept: extents in
+// bytes and row x stride products then stay far inside 64 bits.
+constexpr long long kMaxElems = 1LL << 46;
+
+// rows x stride stays inside kMaxElems (both non-negative).
+inline bool span_ok(long long rows, long long stride) {
+  return rows >= 0 && stride >= 0 && (rows == 0 || stride <= kMaxElems / rows);
+}
+
+// ---- device side -------------------------------------------------------------
+
+template <typename T> __device__ __forceinline__ float to_f(T v);
+template <> __device__ __forceinline__ float to_f<float>(float v) { return v; }
+template <> __device__ __forceinline__ float to_f<__half>(__half v) { return __half2float(v); }
+template <> __device__ __forceinline__ float to_f<__nv_bfloat16>(__nv_bfloat16 v) { return __bfloat162float(v); }
+
+template <typename T> __device__ __forceinline__ T from_f(float v);
+template <> __device__ __forceinline__ float from_f<float>(float v) { return v; }
+template <> __device__ __forceinline__ __half from_f<__half>(float v) { return __float2half_rn(v); }
+template <> __device__ __forceinline__ __nv_bfloat16 from_f<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
+
+// Elements of T in 16 bytes.
+template <typename T> struct Vec16 { static constexpr int N = 16 / (int)sizeof(T); };
+
+// V consecutive elements: V * sizeof(T) bytes in one access (V = 1: one
+// element of any alignment; otherwise the address is a multiple of the size).
+template <typename T, int V> struct Pack {
+  T v[V];
+};
+template <> struct __align__(16) Pack<float, 4> { float v[4]; };
+template <> struct __align__(16) Pack<__half, 8> { __half v[8]; };
+template <> struct __align__(16) Pack<__nv_bfloat16, 8> { __nv_bfloat16 v[8]; };
+
+template <typename T, int V> __device__ __forceinline__ Pack<T, V> load_pack(const T* p) {
+  Pack<T, V> r;
+  if constexpr (V == 1) {
+    r.v[0] = __ldg(p);
+  } else {
+    static_assert(V * sizeof(T) == 16, "one 16-byte access");
+    const uint4 u = __ldg(reinterpret_cast<const uint4*>(p));
+    r = *reinterpret_cast<const Pack<T, V>*>(&u);
+  }
+  return r;
+}
+
+template <typename T, int V> __device__ __forceinline__ void store_pack(T* p, const float* f) {
+  if constexpr (V == 1) {
+    p[0] = from_f<T>(f[0]);
+  } else {
+    Pack<T, V> r;
+#pragma unroll
+    for (int i = 0; i < V; ++i) r.v[i] = from_f<T>(f[i]);
+    *reinterpret_cast<uint4*>(p) = *reinterpret_cast<const uint4*>(&r);
+  }
+}
+
+// Element i of an array of runtime type.
+__device__ __forceinline__ float load_any(const void* p, int dtype, long long i) {
+  if (dtype == PSGD_F32) return __ldg((const float*)p + i);
+  if (dtype == PSGD_F16) return __half2float(__ldg((const __half*)p + i));
+  return __bfloat162float(__ldg((const __nv_bfloat16*)p + i));
+}
+// Its current value, where the kernel itself writes the array.
+__device__ __forceinline__ float read_any(const void* p, int dtype, long long i) {
+  if (dtype == PSGD_F32) return ((const float*)p)[i];
+  if (dtype == PSGD_F16) return __half2float(((const __half*)p)[i]);
+  return __bfloat162float(((const __nv_bfloat16*)p)[i]);
+}
+__device__ __forceinline__ void store_any(void* p, int dtype, long long i, float v) {
+  if (dtype == PSGD_F32) ((float*)p)[i] = v;
+  else if (dtype == PSGD_F16) ((__half*)p)[i] = __float2half_rn(v);
+  else ((__nv_bfloat16*)p)[i] = __float2bfloat16_rn(v);
+}
+
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+__device__ __forceinline__ float warp_max(float v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+  return v;
+}
+
+}  // namespace ops
+}  // namespace psgd
