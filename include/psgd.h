@@ -651,13 +651,13 @@ int psgd_layernorm_backward(psgd_layernorm* n, const void* grad, int64_t grad_st
  * -infinity, has loss 0 and gradient 0 whatever its logits hold.  Otherwise
  * a logit of -infinity has q_j = 0 (the loss is infinite if the teacher wants
  * it), and NaN, +infinity or a row of nothing but -infinity gives NaN.
- * Runs on the calling thread's current CUDA device.
+ *   device  : the CUDA device that holds the operands.
  * Errors: PSGD_EINVAL, PSGD_ECUDA.
  */
 int psgd_distill(const void* logits, psgd_dtype dtype, int64_t logits_stride, int64_t rows, int64_t vocab,
                  const void* teacher, psgd_dtype teacher_dtype, int64_t teacher_stride, const void* index,
                  int32_t index_bits, int64_t index_stride, int32_t k, float temperature, const float* weights,
-                 float grad_scale, float* losses, void* dlogits, int64_t dlogits_stride, void* stream);
+                 float grad_scale, float* losses, void* dlogits, int64_t dlogits_stride, int32_t device, void* stream);
 
 /*
  * psgd_build_id -- "psgd-source-hash:" followed by the SHA-256 (32 hex

@@ -169,7 +169,7 @@ def lib():
                                           c_i32, P]
     L.psgd_layernorm_backward.restype = ctypes.c_int
     L.psgd_distill.argtypes = [P, c_i32, c_i64, c_i64, c_i64, P, c_i32, c_i64, P, c_i32, c_i64, c_i32, f32, P, f32, P,
-                               P, c_i64, P]
+                               P, c_i64, c_i32, P]
     L.psgd_distill.restype = ctypes.c_int
     L.psgd_build_id.argtypes = []
     L.psgd_build_id.restype = ctypes.c_char_p

@@ -49,17 +49,17 @@ def test_null_handles():
 
 
 def distill(dtype=F32, stride=50, rows=4, vocab=50, tdtype=F32, bits=64, k=6, t=1.0, null=(), dz=False, dz_at=1 << 24,
-            dz_stride=50):
+            dz_stride=50, device=0):
     """psgd_distill with made-up addresses, which only calls that are refused (or have no rows) may be given."""
     at = dict(logits=1 << 20, teacher=1 << 21, index=1 << 22, losses=1 << 23)
     at.update({n: None for n in null})
     return _lib.lib().psgd_distill(at["logits"], dtype, stride, rows, vocab, at["teacher"], tdtype, 6, at["index"], bits, 6, k,
-                                   t, None, 1.0, at["losses"], dz_at if dz else None, dz_stride, None)
+                                   t, None, 1.0, at["losses"], dz_at if dz else None, dz_stride, device, None)
 
 
 @pytest.mark.parametrize("kw,words", [
     (dict(dtype=9), "dtype"), (dict(tdtype=-1), "dtype"), (dict(bits=16), "index_bits"), (dict(rows=-1), "rows"),
-    (dict(rows=2**31), "rows"), (dict(vocab=0), "vocab"), (dict(vocab=2**30 + 1), "vocab"), (dict(k=0), "k must"),
+    (dict(rows=2**31), "rows"), (dict(vocab=0), "vocab"), (dict(vocab=2**30 + 1), "vocab"), (dict(k=0), "k must"), (dict(device=64), "device"), (dict(device=-1), "device"),
     (dict(k=_lib.PSGD_DISTILL_MAX_K + 1), "k must"), (dict(t=0.0), "temperature"), (dict(t=float("nan")), "temperature"),
     (dict(null=["logits"]), "NULL"), (dict(null=["teacher"]), "NULL"), (dict(null=["index"]), "NULL"),
     (dict(null=["losses"]), "NULL"), (dict(stride=-1), "stride"), (dict(stride=2**60), "stride"),
