@@ -15,6 +15,7 @@
 
 #include <algorithm>
 #include <atomic>
+#include <type_traits>
 
 #include "psgd_ops.cuh"
 
@@ -26,9 +27,10 @@ namespace {
 
 constexpr int kDistillThreads = 512;
 constexpr int kDistillWarps = kDistillThreads / 32;
+constexpr int kStages = 4;               // groups of copies a slice arrives in
 constexpr int kMaxCluster = 8;           // CTAs of a row
-constexpr int kHalfSmem = 104 * 1024;    // of a row in one CTA, two of which fit an SM beside their static arrays
-constexpr int kFullSmem = 212 * 1024;    // of a row in one CTA, alone on its SM
+constexpr int kHalfSmem = 112 * 1024;    // of a CTA, two of which fit an SM
+constexpr int kFullSmem = 224 * 1024;    // of a CTA alone on its SM
 
 struct DistillArgs {
   const void* z;
@@ -122,171 +124,351 @@ __device__ __forceinline__ float mass_at(const float* p, const int* at, int n, i
   return sum;
 }
 
-// A 16-byte granule of a row as floats.
-template <typename Z> __device__ __forceinline__ void unpack(const uint4& u, float* f) {
-  const Z* v = reinterpret_cast<const Z*>(&u);
+// Two fp32 lanes of one register pair: one instruction for both.
+struct F2 {
+  unsigned long long v;
+};
+__device__ __forceinline__ F2 f2(float x, float y) {
+  F2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(x), "f"(y));
+  return r;
+}
+__device__ __forceinline__ void split(F2 a, float& x, float& y) { asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(a.v)); }
+__device__ __forceinline__ F2 add(F2 a, F2 b) {
+  F2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ F2 mul(F2 a, F2 b) {
+  F2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+
+// A 16-byte granule of a row as pairs of floats, and its largest element.
+template <typename Z> struct Granule;
+template <> struct Granule<float> {
+  static __device__ __forceinline__ void pairs(const uint4& u, F2* f) {
+    f[0] = f2(__uint_as_float(u.x), __uint_as_float(u.y));
+    f[1] = f2(__uint_as_float(u.z), __uint_as_float(u.w));
+  }
+  static __device__ __forceinline__ float top(const uint4& u) {
+    return fmaxf(fmaxf(__uint_as_float(u.x), __uint_as_float(u.y)), fmaxf(__uint_as_float(u.z), __uint_as_float(u.w)));
+  }
+};
+template <> struct Granule<__half> {
+  static __device__ __forceinline__ void pairs(const uint4& u, F2* f) {
+    const __half2* h = reinterpret_cast<const __half2*>(&u);
 #pragma unroll
-  for (int i = 0; i < Vec16<Z>::N; ++i) f[i] = to_f(v[i]);
+    for (int i = 0; i < 4; ++i) {
+      const float2 x = __half22float2(h[i]);
+      f[i] = f2(x.x, x.y);
+    }
+  }
+  static __device__ __forceinline__ float top(const uint4& u) {
+    const __half2* h = reinterpret_cast<const __half2*>(&u);
+    const __half2 m = __hmax2(__hmax2(h[0], h[1]), __hmax2(h[2], h[3]));
+    return fmaxf(__low2float(m), __high2float(m));
+  }
+};
+template <> struct Granule<__nv_bfloat16> {
+  static __device__ __forceinline__ void pairs(const uint4& u, F2* f) {
+    const unsigned w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f[i] = f2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
+  }
+  static __device__ __forceinline__ float top(const uint4& u) {
+    const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(&u);
+    const __nv_bfloat162 m = __hmax2(__hmax2(h[0], h[1]), __hmax2(h[2], h[3]));
+    return fmaxf(__low2float(m), __high2float(m));
+  }
+};
+
+__device__ __forceinline__ void copy16(uint4* dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((unsigned)__cvta_generic_to_shared(dst)), "l"(src)
+               : "memory");
+}
+// Waits for the first q + 1 of LAST + 1 groups of copies (q known when unrolled).
+template <int LAST> __device__ __forceinline__ void wait_copies(int q) {
+  if (q == LAST) asm volatile("cp.async.wait_group 0;" ::: "memory");
+  else if (q == LAST - 1) asm volatile("cp.async.wait_group 1;" ::: "memory");
+  else if (q == LAST - 2) asm volatile("cp.async.wait_group 2;" ::: "memory");
+  else asm volatile("cp.async.wait_group 3;" ::: "memory");
+}
+
+// Slots of the table in which a row's entries look for equal indices: a power
+// of two, at least twice the entries.
+__host__ __device__ constexpr int table_slots(int k) {
+  int n = 64;
+  while (n < 2 * k) n *= 2;
+  return n;
+}
+
+// One warp's work on a row's teacher entries: validity (at[k], -1 where not),
+// their softmax p[k], whether the row counts (state bit 0) and whether two of
+// its indices are equal (bit 1).
+__device__ __forceinline__ int teacher_warp(const DistillArgs& a, long long row, float* p, int* at, int* table) {
+  const int lane = threadIdx.x & 31;
+  const float inv_t = 1.f / a.temperature;
+  const int slots = table_slots(a.k);
+  for (int i = lane; i < slots; i += 32) table[i] = -1;
+  __syncwarp();
+  float m = -INFINITY;
+  bool mass = false, twice = false;
+  for (int k = lane; k < a.k; k += 32) {
+    const long long i = a.index64 ? __ldg((const long long*)a.index + row * a.is + k)
+                                  : (long long)__ldg((const int*)a.index + row * a.is + k);
+    const float tk = load_any(a.t, a.tdtype, row * a.ts + k);
+    const bool valid = i >= 0 && i < a.vocab;
+    const float t = valid ? tk * inv_t : -INFINITY;
+    at[k] = valid ? (int)i : -1;
+    p[k] = t;
+    m = fmaxf(m, t);
+    mass |= t != -INFINITY;
+    if (valid) {
+      // open addressing: there are more slots than entries, so a free one or the index itself is met
+      unsigned h = ((unsigned)i * 2654435761u) & (slots - 1);
+      for (;;) {
+        const int old = atomicCAS(&table[h], -1, (int)i);
+        if (old == (int)i) twice = true;
+        if (old == -1 || old == (int)i) break;
+        h = (h + 1) & (slots - 1);
+      }
+    }
+  }
+  mass = __any_sync(0xffffffffu, mass);
+  twice = __any_sync(0xffffffffu, twice);
+  if (!mass) return 0;
+  m = warp_max(m);
+  float s = 0.f;
+  for (int k = lane; k < a.k; k += 32) {
+    const float e = at[k] >= 0 ? expf(p[k] - m) : 0.f;
+    p[k] = e;
+    s += e;
+  }
+  const float inv_p = 1.f / warp_sum(s);
+  for (int k = lane; k < a.k; k += 32) p[k] *= inv_p;
+  return twice ? 3 : 1;
 }
 
 // One cluster per row; CTA r of C holds the row's granules [r n / C, (r + 1) n / C)
 // in shared memory, n the number of aligned 16-byte granules that the row
-// touches (its first and last may be shared with the neighbouring rows).
-// ALIGNED: the gradient's rows start at the same place of a granule as the
-// logits' do, so whole granules are stored.
+// touches (its first and last may be shared with the neighbouring rows).  The
+// last warp of a CTA works on the teacher's entries while the others take the
+// softmax's sums, so neither waits for the other's loads.  ALIGNED: the
+// gradient's rows start at the same place of a granule as the logits' do, so
+// whole granules are stored.
 template <typename Z, bool ALIGNED>
-__global__ void __launch_bounds__(kDistillThreads, 2) k_distill_chip(DistillArgs a, int ctas) {
+__global__ void __launch_bounds__(kDistillThreads + 32, 2) k_distill_chip(DistillArgs a, int ctas, int slice_granules) {
   constexpr int NE = Vec16<Z>::N;
-  constexpr int U = 4;  // granules in flight per thread
+  constexpr int NP = NE / 2;
+  constexpr int U = NE == 8 ? 2 : 4;  // granules a thread takes at a time
   extern __shared__ uint4 slice[];
-  __shared__ float buf[kDistillWarps], bufs[kDistillWarps], bufp[kDistillWarps];
-  __shared__ float p[PSGD_DISTILL_MAX_K];
-  __shared__ int at[PSGD_DISTILL_MAX_K];
+  __shared__ float bufm[kDistillWarps], bufs[kDistillWarps];
   __shared__ float2 peers[kMaxCluster];
   __shared__ float parts[kMaxCluster];
-  const int tid = threadIdx.x, threads = blockDim.x, lane = tid & 31, warp = tid >> 5, warps = threads >> 5;
+  __shared__ int state_shared;
+  float* p = reinterpret_cast<float*>(slice + slice_granules);  // k each, and the table
+  float* pm = p + a.k;
+  int* at = reinterpret_cast<int*>(pm + a.k);
+  int* table = at + a.k;
+  const int threads = blockDim.x - 32;  // of the row's warps
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, warps = threads >> 5;
+  const bool entries = warp == warps;
   const long long row = blockIdx.x / ctas;
   const int rank = blockIdx.x - (int)row * ctas;
   const Z* z = (const Z*)a.z + row * a.zs;
   Z* dz = a.dz ? (Z*)a.dz + row * a.dzs : nullptr;
   const int head = (int)(((uintptr_t)z & 15) / sizeof(Z));  // elements of the first granule before the row
   const int granules = (head + a.vocab + NE - 1) / NE;
-  const int g0 = (int)((long long)granules * rank / ctas), g1 = (int)((long long)granules * (rank + 1) / ctas);
+  const int g0 = (int)((long long)granules * rank / ctas), n = (int)((long long)granules * (rank + 1) / ctas) - g0;
+  // granules of the slice that lie inside the row: [whole0, whole0 + whole)
+  const int whole0 = max(0, (head ? 1 : 0) - g0);
+  const unsigned whole = (unsigned)max(0, min(n, (head + a.vocab) / NE - g0) - whole0);
+  const Z* zs = z + ((long long)g0 * NE - head);  // the slice's first granule (its first elements may lie before the row)
+  const int j0 = g0 * NE - head;                  // its first element
   const float w = a.weights ? __ldg(a.weights + row) : 1.f;
   if (ctas > 1) cluster_arrive();  // a peer's shared memory is written once all have started
-  const bool live = teacher_softmax(a, row, w, p, at, buf);
 
   auto store = [&](int g, const float* f) {
-    const int j0 = g * NE - head;
-    if (ALIGNED && j0 >= 0 && j0 + NE <= a.vocab) {
-      store_pack<Z, NE>(dz + j0, f);
+    if (ALIGNED && (unsigned)(g - whole0) < whole) {
+      store_pack<Z, NE>(dz + j0 + g * NE, f);
     } else {
 #pragma unroll
       for (int i = 0; i < NE; ++i)
-        if (j0 + i >= 0 && j0 + i < a.vocab) dz[j0 + i] = from_f<Z>(f[i]);
+        if (j0 + g * NE + i >= 0 && j0 + g * NE + i < a.vocab) dz[j0 + g * NE + i] = from_f<Z>(f[i]);
     }
   };
-
-  if (!live) {  // the same for every CTA of the cluster
-    if (rank == 0 && tid == 0) a.losses[row] = 0.f;
-    if (dz) {
-      float zero[NE];
+  auto store_zeros = [&]() {
+    float zero[NE];
 #pragma unroll
-      for (int i = 0; i < NE; ++i) zero[i] = 0.f;
-      for (int g = g0 + tid; g < g1; g += threads) store(g, zero);
-    }
+    for (int i = 0; i < NE; ++i) zero[i] = 0.f;
+    if (dz && !entries)
+      for (int g = tid; g < n; g += threads) store(g, zero);
+    if (rank == 0 && tid == 0) a.losses[row] = 0.f;
+  };
+
+  if (w == 0.f) {  // the same for every CTA of the cluster
+    store_zeros();
     if (ctas > 1) cluster_wait();
     return;
   }
 
   const float c = kLog2e / a.temperature;
-  float r = -INFINITY, s = 0.f;
-  for (int g = g0 + tid; g < g1; g += threads * U) {
-    uint4 v[U];
+  if (entries) {
+    const int state = teacher_warp(a, row, p, at, table);
+    if (lane == 0) state_shared = state;
+  } else {
+    // The slice is copied by the threads that will use it (granule tid, tid +
+    // threads, ...), in kStages groups of copies that are all under way at once.
+    const int per = ((n + threads - 1) / threads + kStages - 1) / kStages;  // granules per thread and stage
 #pragma unroll
-    for (int n = 0; n < U; ++n) {
-      const int gg = g + n * threads;
-      const int j0 = gg * NE - head;
-      if (gg < g1 && j0 >= 0 && j0 + NE <= a.vocab) {
-        v[n] = *reinterpret_cast<const uint4*>(z + j0);
-      } else {
-        Z* e = reinterpret_cast<Z*>(&v[n]);
+    for (int q = 0; q < kStages; ++q) {
+      const int last = min(n, (q + 1) * per * threads);
+      for (int g = q * per * threads + tid; g < last; g += threads) {
+        if ((unsigned)(g - whole0) < whole) {
+          copy16(&slice[g], zs + (long long)g * NE);
+        } else {
+          uint4 v;
+          Z* e = reinterpret_cast<Z*>(&v);
 #pragma unroll
-        for (int i = 0; i < NE; ++i)
-          e[i] = gg < g1 && j0 + i >= 0 && j0 + i < a.vocab ? z[j0 + i] : from_f<Z>(-INFINITY);
+          for (int i = 0; i < NE; ++i) {
+            const int j = j0 + g * NE + i;
+            e[i] = j >= 0 && j < a.vocab ? z[j] : from_f<Z>(-INFINITY);
+          }
+          slice[g] = v;
+        }
       }
+      asm volatile("cp.async.commit_group;" ::: "memory");
     }
-    float top = -INFINITY;
+    float r = -INFINITY;
+    F2 sums[2] = {f2(0.f, 0.f), f2(0.f, 0.f)};
+    const F2 cc = f2(c, c);
+    auto take = [&](const uint4* v, auto count) {
+      constexpr int N = decltype(count)::value;
+      float top = Granule<Z>::top(v[0]);
 #pragma unroll
-    for (int n = 0; n < U; ++n) {
-      if (g + n * threads < g1) slice[g + n * threads - g0] = v[n];
-      float f[NE];
-      unpack<Z>(v[n], f);
+      for (int i = 1; i < N; ++i) top = fmaxf(top, Granule<Z>::top(v[i]));
+      if (top > r) {
+        const float down = exp2_fast((r - top) * c);
+        sums[0] = mul(sums[0], f2(down, down));
+        sums[1] = mul(sums[1], f2(down, down));
+        r = top;
+      }
+      const float base = r == -INFINITY ? 0.f : -r;
+      const F2 bb = f2(base, base);
 #pragma unroll
-      for (int i = 0; i < NE; ++i) top = fmaxf(top, f[i]);
+      for (int i = 0; i < N; ++i) {
+        F2 f[NP];
+        Granule<Z>::pairs(v[i], f);
+#pragma unroll
+        for (int h = 0; h < NP; ++h) {
+          float x, y;
+          split(mul(add(f[h], bb), cc), x, y);
+          sums[h & 1] = add(sums[h & 1], f2(exp2_fast(x), exp2_fast(y)));
+        }
+      }
+    };
+#pragma unroll
+    for (int q = 0; q < kStages; ++q) {
+      wait_copies<kStages - 1>(q);
+      const int last = min(n, (q + 1) * per * threads);
+      int g = q * per * threads + tid;
+      for (; g + (U - 1) * threads < last; g += threads * U) {
+        uint4 v[U];
+#pragma unroll
+        for (int i = 0; i < U; ++i) v[i] = slice[g + i * threads];
+        take(v, std::integral_constant<int, U>());
+      }
+      for (; g < last; g += threads) take(&slice[g], std::integral_constant<int, 1>());
     }
-    if (top > r) {
-      s *= exp2_fast((r - top) * c);
-      r = top;
+    float x, y;
+    split(add(sums[0], sums[1]), x, y);
+    float s = x + y;
+    // over the warp
+    const float top = warp_max(r);
+    s = warp_sum(r == -INFINITY ? s : s * exp2_fast((r - top) * c));
+    if (lane == 0) {
+      bufm[warp] = top;
+      bufs[warp] = s;
     }
-    const float base = r == -INFINITY ? 0.f : r;
-#pragma unroll
-    for (int n = 0; n < U; ++n) {
-      float f[NE];
-      unpack<Z>(v[n], f);
-#pragma unroll
-      for (int i = 0; i < NE; ++i) s += exp2_fast((f[i] - base) * c);
-    }
-  }
-  // over the warp, the CTA, the cluster
-  auto shifted = [c](float s, float r, float to) { return r == -INFINITY ? s : s * exp2_fast((r - to) * c); };
-  float top = warp_max(r);
-  s = warp_sum(shifted(s, r, top));
-  if (lane == 0) {
-    buf[warp] = top;
-    bufs[warp] = s;
   }
   __syncthreads();
-  r = lane < warps ? buf[lane] : -INFINITY;
-  s = lane < warps ? bufs[lane] : 0.f;
-  top = warp_max(r);
-  s = warp_sum(shifted(s, r, top));
+  // over the CTA, then the cluster
+  auto join = [c](float r, float s, float& top, float& sum) {
+    top = warp_max(r);
+    sum = warp_sum(r == -INFINITY ? s : s * exp2_fast((r - top) * c));
+  };
+  float top, s;
+  join(lane < warps ? bufm[lane] : -INFINITY, lane < warps ? bufs[lane] : 0.f, top, s);
   if (ctas > 1) {
     cg::cluster_group cluster = cg::this_cluster();
     cluster_wait();
     if (tid < ctas) *cluster.map_shared_rank(&peers[rank], tid) = make_float2(top, s);
     cluster.sync();
-    r = lane < ctas ? peers[lane].x : -INFINITY;
-    s = lane < ctas ? peers[lane].y : 0.f;
-    top = warp_max(r);
-    s = warp_sum(shifted(s, r, top));
+    join(lane < ctas ? peers[lane].x : -INFINITY, lane < ctas ? peers[lane].y : 0.f, top, s);
+  }
+  const int state = state_shared;
+  if (state == 0) {  // the same for every CTA of the cluster
+    store_zeros();
+    return;
   }
   const float base = top == -INFINITY ? 0.f : top;
-  const float log2_s = log2f(s);
   const float f = w * a.temperature * a.scale, fq = f / s;
-  // the entries that fall into this CTA's slice: their part of the loss, and their gradients
-  const Z* held = reinterpret_cast<const Z*>(slice) + head - (long long)g0 * NE;
-  float part = 0.f;
-  for (int k = tid; k < a.k; k += threads) {
-    const int j = at[k];
-    const bool mine = j >= 0 && (j + head) / NE >= g0 && (j + head) / NE < g1;
-    if (mine) {
-      const float x = (to_f(held[j]) - base) * c;
-      if (!(p[k] == 0.f)) part += p[k] * (logf(p[k]) - kLn2 * (x - log2_s));
-    }
+  if (state & 2) {
+    for (int k = tid; k < a.k; k += blockDim.x) pm[k] = mass_at(p, at, a.k, k);
+    __syncthreads();
   }
-  part = warp_sum(part);
-  if (lane == 0) bufp[warp] = part;
-  if (dz) {
-    for (int g = g0 + tid; g < g1; g += threads) {
+  const Z* held = reinterpret_cast<const Z*>(slice) - j0;
+  if (entries) {
+    // the entries that fall into this CTA's slice: their part of the loss, and their gradients
+    const float log2_s = log2f(s);
+    float part = 0.f;
+    for (int k = lane; k < a.k; k += 32) {
+      const int j = at[k];
+      const float pk = p[k];
+      if (j >= 0 && (unsigned)(j - j0) < (unsigned)(n * NE)) {
+        const float x = (to_f(held[j]) - base) * c;
+        if (!(pk == 0.f)) part += pk * (logf(pk) - kLn2 * (x - log2_s));
+        pm[k] = exp2_fast(x) * fq - (state & 2 ? pm[k] : pk) * f;
+      } else {
+        at[k] = -1;
+      }
+    }
+    part = warp_sum(part);
+    if (ctas == 1) {
+      if (lane == 0) a.losses[row] = w * (a.temperature * a.temperature) * part;
+    } else if (lane == 0) {
+      *cg::this_cluster().map_shared_rank(&parts[rank], 0) = part;
+    }
+  } else if (dz) {
+    const F2 cc = f2(c, c), bb = f2(-base, -base), ff = f2(fq, fq);
+    for (int g = tid; g < n; g += threads) {
+      F2 x[NP];
       float q[NE];
-      unpack<Z>(slice[g - g0], q);
+      Granule<Z>::pairs(slice[g], x);
 #pragma unroll
-      for (int i = 0; i < NE; ++i) q[i] = exp2_fast((q[i] - base) * c) * fq;
+      for (int h = 0; h < NP; ++h) {
+        float u, v;
+        split(mul(add(x[h], bb), cc), u, v);
+        split(mul(f2(exp2_fast(u), exp2_fast(v)), ff), q[2 * h], q[2 * h + 1]);
+      }
       store(g, q);
     }
   }
-  __syncthreads();
-  if (dz) {
-    for (int k = tid; k < a.k; k += threads) {
-      const int j = at[k];
-      if (j >= 0 && (j + head) / NE >= g0 && (j + head) / NE < g1)
-        dz[j] = from_f<Z>(exp2_fast((to_f(held[j]) - base) * c) * fq - mass_at(p, at, a.k, k) * f);
-    }
-  }
-  part = 0.f;
-  if (tid == 0)
-    for (int v = 0; v < warps; ++v) part += bufp[v];
   if (ctas > 1) {
-    cg::cluster_group cluster = cg::this_cluster();
-    if (tid == 0) *cluster.map_shared_rank(&parts[rank], 0) = part;
-    cluster.sync();
+    cg::this_cluster().sync();
     if (rank == 0 && tid == 0) {
-      part = 0.f;
+      float part = 0.f;
       for (int v = 0; v < ctas; ++v) part += parts[v];
+      a.losses[row] = w * (a.temperature * a.temperature) * part;
     }
+  } else if (dz) {
+    __syncthreads();
   }
-  if (rank == 0 && tid == 0) a.losses[row] = w * (a.temperature * a.temperature) * part;
+  if (dz && entries)
+    for (int k = lane; k < a.k; k += 32)
+      if (at[k] >= 0) dz[at[k]] = from_f<Z>(pm[k]);
 }
 
 // Rows larger than a cluster's shared memory: one CTA per row, which reads the
@@ -347,23 +529,27 @@ template <typename Z> __global__ void __launch_bounds__(kDistillThreads) k_disti
   }
 }
 
-// How a row is spread: CTAs of its cluster (0: too long for one), threads.
+// How a row is spread: CTAs of its cluster (0: too long for one), threads of
+// the row's warps, granules of a slice, shared memory with the entries'.
 struct RowPlan {
   int ctas;
   int threads;
+  int granules;
   size_t smem;
 };
 
-RowPlan plan_row(long long vocab, int size, long long rows, int sms) {
+RowPlan plan_row(long long vocab, int size, int k, long long rows, int sms) {
+  const long long extra = 12LL * k + 4LL * table_slots(k) + 16;
   const long long bytes = vocab * size + 32;  // with both ends' granules
-  RowPlan p{1, 0, 0};
-  while (p.ctas < kMaxCluster && bytes / p.ctas > kHalfSmem) p.ctas *= 2;
-  if (bytes / p.ctas > kFullSmem) return RowPlan{0, kDistillThreads, 0};
+  RowPlan p{1, kDistillThreads, 0, 0};
+  while (p.ctas < kMaxCluster && bytes / p.ctas + extra > kHalfSmem) p.ctas *= 2;
+  if (bytes / p.ctas + extra > kFullSmem) return RowPlan{0, kDistillThreads, 0, 0};
   // few rows: more CTAs a row, as long as each keeps a few granules per thread
   while (p.ctas < kMaxCluster && rows * p.ctas * 2 <= sms && bytes / p.ctas >= 16 * 1024) p.ctas *= 2;
-  const long long granules = bytes / 16 / p.ctas + 2;
-  p.smem = (size_t)granules * 16;
-  p.threads = (int)std::min<long long>(kDistillThreads, std::max<long long>(64, (granules / 4 + 31) / 32 * 32));
+  p.granules = (int)(bytes / 16 / p.ctas + 2);
+  p.smem = (size_t)p.granules * 16 + extra;
+  const int most = p.smem > 72 * 1024 ? kDistillThreads : kDistillThreads / 2;  // three and more slices to an SM: 256 each
+  p.threads = (int)std::min<long long>(most, std::max<long long>(64, (p.granules / 4 + 31) / 32 * 32));
   return p;
 }
 
@@ -378,7 +564,7 @@ template <typename Z, bool ALIGNED> cudaError_t launch_chip(const DistillArgs& a
   }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(a.rows * p.ctas));
-  cfg.blockDim = dim3(p.threads);
+  cfg.blockDim = dim3(p.threads + 32);
   cfg.dynamicSmemBytes = p.smem;
   cfg.stream = st;
   cudaLaunchAttribute attr;
@@ -387,11 +573,11 @@ template <typename Z, bool ALIGNED> cudaError_t launch_chip(const DistillArgs& a
   attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = p.ctas > 1 ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, k_distill_chip<Z, ALIGNED>, a, p.ctas);
+  return cudaLaunchKernelEx(&cfg, k_distill_chip<Z, ALIGNED>, a, p.ctas, p.granules);
 }
 
 template <typename Z> cudaError_t launch_distill(const DistillArgs& a, int device, int sms, cudaStream_t st) {
-  const RowPlan p = plan_row(a.vocab, (int)sizeof(Z), a.rows, sms);
+  const RowPlan p = plan_row(a.vocab, (int)sizeof(Z), a.k, a.rows, sms);
   if (p.ctas == 0) {
     k_distill_long<Z><<<(unsigned)a.rows, kDistillThreads, 0, st>>>(a);
     return cudaGetLastError();

@@ -285,11 +285,11 @@ class LayerNorm:
             out, ys = _new_like(x, stream), self.dim
         else:
             ys = self._like(out, x, "out")
-        mean, rstd = _new((2, *x.shape[:-1]), torch.float32, self.device, stream).unbind(0)
-        at = mean.data_ptr()
+        lead = x.shape[:-1]
+        mean, rstd = _new(lead, torch.float32, self.device, stream), _new(lead, torch.float32, self.device, stream)
         check(self._lib.psgd_layernorm_forward(
-            self._h, x.data_ptr(), xd, xs, rows, w, b, pd, self.eps, out.data_ptr(), ys, at, at + 4 * rows,
-            _stream(stream, self._index)))
+            self._h, x.data_ptr(), xd, xs, rows, w, b, pd, self.eps, out.data_ptr(), ys, mean.data_ptr(),
+            rstd.data_ptr(), _stream(stream, self._index)))
         return out, mean, rstd
 
     def backward(self, grad, x, mean, rstd, weight=None, dx=None, dweight=None, dbias=None, accumulate=False,
