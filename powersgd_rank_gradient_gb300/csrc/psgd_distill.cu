@@ -57,6 +57,7 @@ __device__ __forceinline__ float exp2_fast(float x) {
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kFar = 1048576.f;  // 2^20
 
 // Sums or maxima over a CTA of any whole number of warps, returned to all of
 // its threads; `buf` holds one float a warp.
@@ -81,9 +82,11 @@ __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.aligned;" ::: "memory"); }
 
 // Everything below works in powers of two: with c = log2(e) / T the softmax is
-// 2^((z_j - r) c) over its sum, r the largest logit.  The difference comes
-// first: c z_j - c r in one fused operation would leave c r's rounding error in
-// the exponent, which is without bound for masks of the type's lowest value.
+// 2^(c z_j - r) over its sum, r the largest c z_j, rounded.  One fused operation
+// gives an exponent; r's rounding is in every term and cancels, as long as it
+// is small: up to |r| = kFar it is below 2^-4.  A row further out (masks of the
+// type's lowest value and nothing else, or enormous logits) takes its sums
+// again with the difference first, 2^(c (z_j - max)).
 //
 // The teacher's entries of one row: validity (at[k], -1 where not), and their
 // softmax p[k].  Returns whether the row counts at all.
@@ -137,6 +140,11 @@ __device__ __forceinline__ void split(F2 a, float& x, float& y) { asm("mov.b64 {
 __device__ __forceinline__ F2 add(F2 a, F2 b) {
   F2 r;
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ F2 fma(F2 a, F2 b, F2 c) {
+  F2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
   return r;
 }
 __device__ __forceinline__ F2 mul(F2 a, F2 b) {
@@ -251,6 +259,35 @@ __device__ __forceinline__ int teacher_warp(const DistillArgs& a, long long row,
   return twice ? 3 : 1;
 }
 
+// Maximum and sum over all warps of a CTA, the same in every thread.
+__device__ __forceinline__ float cta_max(float v, float* buf, int warps) {
+  const int lane = threadIdx.x & 31;
+  v = warp_max(v);
+  __syncthreads();
+  if (lane == 0) buf[threadIdx.x >> 5] = v;
+  __syncthreads();
+  return warp_max(lane < warps ? buf[lane] : -INFINITY);
+}
+__device__ __forceinline__ float cta_sum(float v, float* buf, int warps) {
+  const int lane = threadIdx.x & 31;
+  v = warp_sum(v);
+  __syncthreads();
+  if (lane == 0) buf[threadIdx.x >> 5] = v;
+  __syncthreads();
+  return warp_sum(lane < warps ? buf[lane] : 0.f);
+}
+// A CTA's value joined over the cluster by `join`, a reduction over a warp.
+template <typename J>
+__device__ __forceinline__ float cluster_join(float v, float2* peers, int ctas, int rank, J join, float none) {
+  if (ctas == 1) return v;
+  cg::cluster_group cluster = cg::this_cluster();
+  cluster.sync();  // nobody reads `peers` any more
+  if ((int)threadIdx.x < ctas) *cluster.map_shared_rank(&peers[rank].x, threadIdx.x) = v;
+  cluster.sync();
+  const int lane = threadIdx.x & 31;
+  return join(lane < ctas ? peers[lane].x : none);
+}
+
 // One cluster per row; CTA r of C holds the row's granules [r n / C, (r + 1) n / C)
 // in shared memory, n the number of aligned 16-byte granules that the row
 // touches (its first and last may be shared with the neighbouring rows).  The
@@ -264,7 +301,7 @@ __global__ void __launch_bounds__(kDistillThreads + 32, 2) k_distill_chip(Distil
   constexpr int NP = NE / 2;
   constexpr int U = NE == 8 ? 2 : 4;  // granules a thread takes at a time
   extern __shared__ uint4 slice[];
-  __shared__ float bufm[kDistillWarps], bufs[kDistillWarps];
+  __shared__ float bufm[kDistillWarps + 1], bufs[kDistillWarps + 1];
   __shared__ float2 peers[kMaxCluster];
   __shared__ float parts[kMaxCluster];
   __shared__ int state_shared;
@@ -341,7 +378,7 @@ __global__ void __launch_bounds__(kDistillThreads + 32, 2) k_distill_chip(Distil
       }
       asm volatile("cp.async.commit_group;" ::: "memory");
     }
-    float r = -INFINITY;
+    float r = -kFar;
     F2 sums[2] = {f2(0.f, 0.f), f2(0.f, 0.f)};
     const F2 cc = f2(c, c);
     auto take = [&](const uint4* v, auto count) {
@@ -349,14 +386,13 @@ __global__ void __launch_bounds__(kDistillThreads + 32, 2) k_distill_chip(Distil
       float top = Granule<Z>::top(v[0]);
 #pragma unroll
       for (int i = 1; i < N; ++i) top = fmaxf(top, Granule<Z>::top(v[i]));
-      if (top > r) {
-        const float down = exp2_fast((r - top) * c);
+      if (top * c > r) {
+        const float down = exp2_fast(r - top * c);
         sums[0] = mul(sums[0], f2(down, down));
         sums[1] = mul(sums[1], f2(down, down));
-        r = top;
+        r = top * c;
       }
-      const float base = r == -INFINITY ? 0.f : -r;
-      const F2 bb = f2(base, base);
+      const F2 bb = f2(-r, -r);
 #pragma unroll
       for (int i = 0; i < N; ++i) {
         F2 f[NP];
@@ -364,7 +400,7 @@ __global__ void __launch_bounds__(kDistillThreads + 32, 2) k_distill_chip(Distil
 #pragma unroll
         for (int h = 0; h < NP; ++h) {
           float x, y;
-          split(mul(add(f[h], bb), cc), x, y);
+          split(fma(f[h], cc, bb), x, y);
           sums[h & 1] = add(sums[h & 1], f2(exp2_fast(x), exp2_fast(y)));
         }
       }
@@ -387,7 +423,7 @@ __global__ void __launch_bounds__(kDistillThreads + 32, 2) k_distill_chip(Distil
     float s = x + y;
     // over the warp
     const float top = warp_max(r);
-    s = warp_sum(r == -INFINITY ? s : s * exp2_fast((r - top) * c));
+    s = warp_sum(s * exp2_fast(r - top));
     if (lane == 0) {
       bufm[warp] = top;
       bufs[warp] = s;
@@ -395,25 +431,45 @@ __global__ void __launch_bounds__(kDistillThreads + 32, 2) k_distill_chip(Distil
   }
   __syncthreads();
   // over the CTA, then the cluster
-  auto join = [c](float r, float s, float& top, float& sum) {
-    top = warp_max(r);
-    sum = warp_sum(r == -INFINITY ? s : s * exp2_fast((r - top) * c));
-  };
   float top, s;
-  join(lane < warps ? bufm[lane] : -INFINITY, lane < warps ? bufs[lane] : 0.f, top, s);
+  top = warp_max(lane < warps ? bufm[lane] : -kFar);
+  s = warp_sum(lane < warps ? bufs[lane] * exp2_fast(bufm[lane] - top) : 0.f);
   if (ctas > 1) {
     cg::cluster_group cluster = cg::this_cluster();
     cluster_wait();
     if (tid < ctas) *cluster.map_shared_rank(&peers[rank], tid) = make_float2(top, s);
     cluster.sync();
-    join(lane < ctas ? peers[lane].x : -INFINITY, lane < ctas ? peers[lane].y : 0.f, top, s);
+    top = warp_max(lane < ctas ? peers[lane].x : -kFar);
+    s = warp_sum(lane < ctas ? peers[lane].y * exp2_fast(peers[lane].x - top) : 0.f);
   }
   const int state = state_shared;
   if (state == 0) {  // the same for every CTA of the cluster
     store_zeros();
     return;
   }
-  const float base = top == -INFINITY ? 0.f : top;
+  // the exponent of a logit is c (z - shift) - base; one of shift and base is 0
+  float shift = 0.f, base = top;
+  if (!(fabsf(top) < kFar)) {  // the same for every CTA of the cluster
+    float m = -INFINITY;
+    for (int g = tid; g < n; g += blockDim.x) m = fmaxf(m, Granule<Z>::top(slice[g]));
+    m = cta_max(m, bufm, warps + 1);
+    m = cluster_join(m, peers, ctas, rank, [](float v) { return warp_max(v); }, -INFINITY);
+    shift = m == -INFINITY ? 0.f : m;
+    base = 0.f;
+    s = 0.f;
+    for (int g = tid; g < n; g += blockDim.x) {
+      F2 x[NP];
+      Granule<Z>::pairs(slice[g], x);
+#pragma unroll
+      for (int h = 0; h < NP; ++h) {
+        float u, v;
+        split(x[h], u, v);
+        s += exp2_fast((u - shift) * c) + exp2_fast((v - shift) * c);
+      }
+    }
+    s = cta_sum(s, bufs, warps + 1);
+    s = cluster_join(s, peers, ctas, rank, [](float v) { return warp_sum(v); }, 0.f);
+  }
   const float f = w * a.temperature * a.scale, fq = f / s;
   if (state & 2) {
     for (int k = tid; k < a.k; k += blockDim.x) pm[k] = mass_at(p, at, a.k, k);
@@ -428,7 +484,7 @@ __global__ void __launch_bounds__(kDistillThreads + 32, 2) k_distill_chip(Distil
       const int j = at[k];
       const float pk = p[k];
       if (j >= 0 && (unsigned)(j - j0) < (unsigned)(n * NE)) {
-        const float x = (to_f(held[j]) - base) * c;
+        const float x = fmaf(to_f(held[j]) - shift, c, -base);
         if (!(pk == 0.f)) part += pk * (logf(pk) - kLn2 * (x - log2_s));
         pm[k] = exp2_fast(x) * fq - (state & 2 ? pm[k] : pk) * f;
       } else {
@@ -442,19 +498,23 @@ __global__ void __launch_bounds__(kDistillThreads + 32, 2) k_distill_chip(Distil
       *cg::this_cluster().map_shared_rank(&parts[rank], 0) = part;
     }
   } else if (dz) {
-    const F2 cc = f2(c, c), bb = f2(-base, -base), ff = f2(fq, fq);
-    for (int g = tid; g < n; g += threads) {
-      F2 x[NP];
-      float q[NE];
-      Granule<Z>::pairs(slice[g], x);
+    const F2 cc = f2(c, c), ff = f2(fq, fq), bb = f2(-base, -base), ss = f2(-shift, -shift);
+    auto gradient = [&](auto far) {
+      for (int g = tid; g < n; g += threads) {
+        F2 x[NP];
+        float q[NE];
+        Granule<Z>::pairs(slice[g], x);
 #pragma unroll
-      for (int h = 0; h < NP; ++h) {
-        float u, v;
-        split(mul(add(x[h], bb), cc), u, v);
-        split(mul(f2(exp2_fast(u), exp2_fast(v)), ff), q[2 * h], q[2 * h + 1]);
+        for (int h = 0; h < NP; ++h) {
+          float u, v;
+          split(decltype(far)::value ? mul(add(x[h], ss), cc) : fma(x[h], cc, bb), u, v);
+          split(mul(f2(exp2_fast(u), exp2_fast(v)), ff), q[2 * h], q[2 * h + 1]);
+        }
+        store(g, q);
       }
-      store(g, q);
-    }
+    };
+    if (fabsf(top) < kFar) gradient(std::false_type());
+    else gradient(std::true_type());
   }
   if (ctas > 1) {
     cg::this_cluster().sync();

@@ -102,14 +102,25 @@ template <typename T, int V> __device__ __forceinline__ Pack<T, V> load_pack(con
   return r;
 }
 
+// Two values rounded to T, as the 32 bits of a pair (one conversion for both).
+template <typename T> __device__ __forceinline__ unsigned pack2(float x, float y);
+template <> __device__ __forceinline__ unsigned pack2<__half>(float x, float y) {
+  const __half2 h = __floats2half2_rn(x, y);
+  return *reinterpret_cast<const unsigned*>(&h);
+}
+template <> __device__ __forceinline__ unsigned pack2<__nv_bfloat16>(float x, float y) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
+  return *reinterpret_cast<const unsigned*>(&h);
+}
+
 template <typename T, int V> __device__ __forceinline__ void store_pack(T* p, const float* f) {
   if constexpr (V == 1) {
     p[0] = from_f<T>(f[0]);
+  } else if constexpr (sizeof(T) == 4) {
+    *reinterpret_cast<float4*>(p) = make_float4(f[0], f[1], f[2], f[3]);
   } else {
-    Pack<T, V> r;
-#pragma unroll
-    for (int i = 0; i < V; ++i) r.v[i] = from_f<T>(f[i]);
-    *reinterpret_cast<uint4*>(p) = *reinterpret_cast<const uint4*>(&r);
+    *reinterpret_cast<uint4*>(p) =
+        make_uint4(pack2<T>(f[0], f[1]), pack2<T>(f[2], f[3]), pack2<T>(f[4], f[5]), pack2<T>(f[6], f[7]));
   }
 }
 

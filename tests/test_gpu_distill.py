@@ -173,6 +173,23 @@ def test_far_logits():
     verify(z, t * 50, at, 3.0)
 
 
+@pytest.mark.parametrize("vocab,rows", [(100, 8), (60001, 8), (60001, 400)])
+def test_rows_far_from_zero(vocab, rows):
+    """Rows whose largest logit is enormous, on either side, beside ordinary ones."""
+    z, t, at = inputs(rows, vocab, 7, F32, F32, torch.int64, 11, ragged=False)
+    z[0] += 1e7
+    z[1] -= 1e7
+    z[2] = torch.finfo(F32).min
+    z[3, 1:] -= 3e38
+    z[4, ::3] = 1e30
+    z[5, 7] = 2.0 ** 20
+    z[6] = -torch.inf
+    z[6, 9] = -1e9
+    at[6] = 9
+    at[3, 1:] = 0
+    verify(z, t, at, 1.3)
+
+
 def test_gradient_against_differences():
     """<dz, v> is the slope of the losses' sum along v, taken from the 64-bit losses."""
     z, t, at = inputs(6, 61, 9, F32, F32, torch.int64, 10)
