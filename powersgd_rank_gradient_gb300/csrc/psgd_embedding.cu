@@ -56,127 +56,228 @@ __device__ __forceinline__ long long load_id(const void* ids, int id64, long lon
   return id64 ? __ldg((const long long*)ids + at) : (long long)__ldg((const int*)ids + at);
 }
 
-// One CTA per token: its row of W times the scale.
-template <typename W, typename O, int VEC>
+// A group of threads (blockDim = (threads of a group, groups)) takes kLookup
+// tokens at a time, so that as many row loads are in flight per thread; thread
+// t owns the vectors t, t + threads, ... (NV of them) of a tile of columns.
+template <typename W, typename O, int VEC, int NV>
 __global__ void __launch_bounds__(256) k_lookup(const W* __restrict__ weight, long long wstride, long long vocab,
                                                 int dim, const void* __restrict__ ids, int id64, Layout2 il, int n,
                                                 float scale, O* __restrict__ out, Layout2 ol, int* flag) {
-  for (int i = blockIdx.x; i < n; i += gridDim.x) {
-    const long long id = load_id(ids, id64, il.at(i));
-    const bool ok = id >= 0 && id < vocab;
-    if (!ok && threadIdx.x == 0) *flag = 1;
-    const W* src = weight + (ok ? id : 0) * wstride;
-    O* dst = out + ol.at(i);
-    for (int c = threadIdx.x * VEC; c < dim; c += blockDim.x * VEC) {
-      float f[VEC];
+  constexpr int T = VEC == 1 ? 2 : 4;  // tokens at a time
+  const int c0 = (blockIdx.y * blockDim.x * NV + threadIdx.x) * VEC, step = blockDim.x * VEC;
+  const int group = blockIdx.x * blockDim.y + threadIdx.y, groups = gridDim.x * blockDim.y;
+  for (long long i0 = (long long)group * T; i0 < n; i0 += groups * T) {
+    long long id[T];
+    bool ok[T];
 #pragma unroll
-      for (int k = 0; k < VEC; ++k) f[k] = 0.f;
-      if (ok) {
+    for (int k = 0; k < T; ++k) {
+      id[k] = i0 + k < n ? load_id(ids, id64, il.at((int)i0 + k)) : 0;
+      ok[k] = id[k] >= 0 && id[k] < vocab;
+      if (!ok[k] && threadIdx.x == 0) *flag = 1;
+    }
+    Pack<W, VEC> v[T][NV];
 #pragma unroll
-        for (int k = 0; k < VEC; ++k) f[k] = to_f(__ldg(src + c + k)) * scale;
+    for (int k = 0; k < T; ++k) {
+      const W* src = weight + (ok[k] ? id[k] : 0) * wstride;
+#pragma unroll
+      for (int j = 0; j < NV; ++j)
+        if (c0 + j * step < dim) v[k][j] = load_pack<W, VEC>(src + c0 + j * step);
+    }
+#pragma unroll
+    for (int k = 0; k < T; ++k) {
+      if (i0 + k >= n) break;
+      O* dst = out + ol.at((int)i0 + k);
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        if (c0 + j * step >= dim) continue;
+        float f[VEC];
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) f[e] = ok[k] ? to_f(v[k][j].v[e]) * scale : 0.f;
+        store_run<O, VEC>(dst + c0 + j * step, f);
       }
-#pragma unroll
-      for (int k = 0; k < VEC; ++k) dst[c + k] = from_f<O>(f[k]);
     }
   }
 }
+
+struct SortArgs {
+  const void* ids;
+  int id64;
+  Layout2 il;
+  int n, vocab;
+  long long padding;
+  int passes;
+  int *key[2], *pos[2];  // pass p writes buffer p & 1
+  int* flag;
+  // the table to zero beside the sort (NULL: none): a run of bytes
+  void* zero;
+  long long zero_bytes;
+};
+
+struct SortShared {
+  int cnt[kSortWarps][kDigits];
+  int quarter[4][kDigits];
+  int totals[kSortCtas][kDigits];  // every CTA's digit totals, pushed by the peers
+  int base[kDigits];
+  int scan[kDigits / 32];
+};
 
 // Stable least-significant-digit radix sort of (key, position) by one cluster:
 // key = id, or `vocab` for a token without a gradient (padding, or an id
 // outside the table), which sorts behind every row.  Each warp owns a
 // contiguous share of the list, so that digit counts per (CTA, warp), scanned
-// in list order, give every element its place; the CTAs read one another's
-// digit totals through distributed shared memory.
-__global__ void __cluster_dims__(kSortCtas, 1, 1) __launch_bounds__(kSortThreads)
-    k_sort_tokens(const void* __restrict__ ids, int id64, Layout2 il, int n, int vocab, long long padding, int passes,
-                  int* keyA, int* posA, int* keyB, int* posB, int* flag) {
-  __shared__ int cnt[kSortWarps][kDigits];
-  __shared__ int total[kDigits];
-  __shared__ int base[kDigits];
-  __shared__ int scan[kDigits / 32];
+// in list order, give every element its place; each CTA writes its digit totals
+// into its peers' shared memory.  A share of at most 32 x ITEMS elements stays
+// in registers between counting and placing (ITEMS = 0: any share, read twice).
+template <int ITEMS> __device__ __forceinline__ void sort_tokens(const SortArgs& a, SortShared& s) {
   cg::cluster_group cluster = cg::this_cluster();
   const int rank = (int)cluster.block_rank();
   const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
   const unsigned below = (1u << lane) - 1u;
-  // elements per warp: a multiple of 32
-  const long long per = ((n + (long long)kSortCtas * kSortThreads - 1) / ((long long)kSortCtas * kSortThreads)) * 32;
+  const int per = (int)((a.n + (long long)kSortCtas * kSortThreads - 1) / ((long long)kSortCtas * kSortThreads)) * 32;
   const long long first = ((long long)rank * kSortWarps + warp) * per;
-  const long long last = min((long long)n, first + per);
-  int *sk = keyB, *sp = posB, *dk = keyA, *dp = posA;
-  for (int p = 0; p < passes; ++p) {
+  const int share = (int)max(0LL, min((long long)a.n - first, (long long)per));  // of this warp
+  for (int p = 0; p < a.passes; ++p) {
     const int shift = 8 * p;
+    const int *sk = p & 1 ? a.key[0] : a.key[1], *sp = p & 1 ? a.pos[0] : a.pos[1];
+    int *dk = p & 1 ? a.key[1] : a.key[0], *dp = p & 1 ? a.pos[1] : a.pos[0];
     auto key_at = [&](long long i) -> int {
       if (p > 0) return __ldcg(sk + i);
-      const long long id = load_id(ids, id64, il.at((int)i));
-      if (id < 0 || id >= vocab) {
-        *flag = 1;
-        return vocab;
+      const long long id = load_id(a.ids, a.id64, a.il.at((int)i));
+      if (id < 0 || id >= a.vocab) {
+        *a.flag = 1;
+        return a.vocab;
       }
-      return id == padding ? vocab : (int)id;
+      return id == a.padding ? a.vocab : (int)id;
     };
-    for (int i = t; i < kSortWarps * kDigits; i += kSortThreads) (&cnt[0][0])[i] = 0;
-    __syncthreads();
-    for (long long i0 = first; i0 < last; i0 += 32) {
-      const long long i = i0 + lane;
-      const int d = i < last ? (key_at(i) >> shift) & (kDigits - 1) : kDigits;
+    auto count = [&](int d) {
       const unsigned same = __match_any_sync(0xffffffffu, d);
-      if (d < kDigits && (same & below) == 0) cnt[warp][d] += __popc(same);
+      if (d < kDigits && (same & below) == 0) s.cnt[warp][d] += __popc(same);
       __syncwarp();
+    };
+    auto place = [&](int d, int key, int pos) {
+      const unsigned same = __match_any_sync(0xffffffffu, d);
+      int at = 0;
+      if (d < kDigits) {
+        at = s.base[d] + s.cnt[warp][d] + __popc(same & below);
+        dk[at] = key;
+        dp[at] = pos;
+      }
+      __syncwarp();
+      if (d < kDigits && (same & below) == 0) s.cnt[warp][d] += __popc(same);
+      __syncwarp();
+    };
+    int key[ITEMS > 0 ? ITEMS : 1], pos[ITEMS > 0 ? ITEMS : 1];
+    if constexpr (ITEMS > 0) {
+#pragma unroll
+      for (int i = 0; i < ITEMS; ++i) {
+        const int e = i * 32 + lane;
+        key[i] = e < share ? key_at(first + e) : 0;
+        pos[i] = e < share ? (p > 0 ? __ldcg(sp + first + e) : (int)first + e) : 0;
+      }
+    }
+    for (int i = t; i < kSortWarps * kDigits; i += kSortThreads) (&s.cnt[0][0])[i] = 0;
+    __syncthreads();
+    if constexpr (ITEMS > 0) {
+#pragma unroll
+      for (int i = 0; i < ITEMS; ++i)
+        if (i * 32 < share) count(i * 32 + lane < share ? (key[i] >> shift) & (kDigits - 1) : kDigits);
+    } else {
+      for (int e = lane; e - lane < share; e += 32)
+        count(e < share ? (key_at(first + e) >> shift) & (kDigits - 1) : kDigits);
     }
     __syncthreads();
-    if (t < kDigits) {
-      int run = 0;
-      for (int w = 0; w < kSortWarps; ++w) {
-        const int c = cnt[w][t];
-        cnt[w][t] = run;
-        run += c;
+    // exclusive counts over the warps, a quarter of them per thread
+    const int d = t & (kDigits - 1), q = t / kDigits;
+    {
+      int sum = 0;
+#pragma unroll
+      for (int w = 0; w < kSortWarps / 4; ++w) {
+        const int c = s.cnt[q * (kSortWarps / 4) + w][d];
+        s.cnt[q * (kSortWarps / 4) + w][d] = sum;
+        sum += c;
       }
-      total[t] = run;
+      s.quarter[q][d] = sum;
+    }
+    __syncthreads();
+    int ahead = 0, total = 0;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int c = s.quarter[k][d];
+      if (k < q) ahead += c;
+      total += c;
+    }
+    if (q > 0) {
+#pragma unroll
+      for (int w = 0; w < kSortWarps / 4; ++w) s.cnt[q * (kSortWarps / 4) + w][d] += ahead;
+    }
+    // two of the peers each
+#pragma unroll
+    for (int k = 0; k < kSortCtas / 4; ++k) {
+      const int peer = q * (kSortCtas / 4) + k;
+      cluster.map_shared_rank(&s.totals[rank][0], peer)[d] = total;
     }
     cluster.sync();
-    int before = 0, all = 0;
     if (t < kDigits) {
+      int before = 0, all = 0;
+#pragma unroll
       for (int r = 0; r < kSortCtas; ++r) {
-        const int c = cluster.map_shared_rank(total, r)[t];
+        const int c = s.totals[r][t];
         if (r < rank) before += c;
         all += c;
       }
-      // exclusive scan of `all` over the digits
-      int inc = all;
+      int inc = all;  // inclusive scan over the digits
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const int v = __shfl_up_sync(0xffffffffu, inc, o);
         if (lane >= o) inc += v;
       }
-      if (lane == 31) scan[warp] = inc;
-      base[t] = inc - all + before;
+      if (lane == 31) s.scan[warp] = inc;
+      s.base[t] = inc - all + before;
     }
     __syncthreads();
     if (t < kDigits) {
       int add = 0;
-      for (int w = 0; w < warp; ++w) add += scan[w];
-      base[t] += add;
+      for (int w = 0; w < warp; ++w) add += s.scan[w];
+      s.base[t] += add;
     }
     __syncthreads();
-    for (long long i0 = first; i0 < last; i0 += 32) {
-      const long long i = i0 + lane;
-      const int key = i < last ? key_at(i) : 0;
-      const int ps = i < last ? (p > 0 ? __ldcg(sp + i) : (int)i) : 0;
-      const int d = i < last ? (key >> shift) & (kDigits - 1) : kDigits;
-      const unsigned same = __match_any_sync(0xffffffffu, d);
-      if (d < kDigits) {
-        const int at = base[d] + cnt[warp][d] + __popc(same & below);
-        dk[at] = key;
-        dp[at] = ps;
+    if constexpr (ITEMS > 0) {
+#pragma unroll
+      for (int i = 0; i < ITEMS; ++i)
+        if (i * 32 < share)
+          place(i * 32 + lane < share ? (key[i] >> shift) & (kDigits - 1) : kDigits, key[i], pos[i]);
+    } else {
+      for (int e = lane; e - lane < share; e += 32) {
+        const bool in = e < share;
+        const int k = in ? key_at(first + e) : 0;
+        place(in ? (k >> shift) & (kDigits - 1) : kDigits, k,
+              in ? (p > 0 ? __ldcg(sp + first + e) : (int)first + e) : 0);
       }
-      __syncwarp();
-      if (d < kDigits && (same & below) == 0) cnt[warp][d] += __popc(same);
-      __syncwarp();
     }
-    cluster.sync();  // this pass's output, for every CTA of the cluster; its totals are free again
-    int* x = sk; sk = dk; dk = x;
-    x = sp; sp = dp; dp = x;
+    cluster.sync();  // this pass's output, for every CTA of the cluster; the totals are free again
   }
+}
+
+// The first cluster sorts the tokens; the others, if any, zero the table.
+template <int ITEMS>
+__global__ void __cluster_dims__(kSortCtas, 1, 1) __launch_bounds__(kSortThreads) k_sort_and_zero(SortArgs a) {
+  __shared__ SortShared s;
+  next_may_launch();
+  if (blockIdx.x < kSortCtas) {
+    cg::this_cluster().sync();  // all have started: their shared memory may be written
+    sort_tokens<ITEMS>(a, s);
+    return;
+  }
+  // 16 bytes at a time between the first and the last boundary, the ends by bytes
+  const long long t = (long long)(blockIdx.x - kSortCtas) * kSortThreads + threadIdx.x;
+  const long long step = (long long)(gridDim.x - kSortCtas) * kSortThreads;
+  char* p = (char*)a.zero;
+  const long long head = min(a.zero_bytes, (long long)((16 - ((uintptr_t)p & 15)) & 15));
+  const long long vecs = (a.zero_bytes - head) / 16, tail = a.zero_bytes - head - vecs * 16;
+  uint4* v = reinterpret_cast<uint4*>(p + head);
+  for (long long i = t; i < vecs; i += step) v[i] = make_uint4(0, 0, 0, 0);
+  if (t < head) p[t] = 0;
+  if (t < tail) p[head + vecs * 16 + t] = 0;
 }
 
 // Zeroes `rows` rows of `dim` elements, `stride` apart.
@@ -187,33 +288,96 @@ __global__ void __launch_bounds__(256) k_zero_rows(O* __restrict__ w, long long 
     for (long long c = threadIdx.x; c < dim; c += blockDim.x) w[r * stride + c] = zero;
 }
 
-// The rows of one chunk of sorted tokens, for one tile of columns.
-template <typename G, typename O>
+// A finished sum into its row of the table: as VEC elements if they are
+// aligned for that, else one by one.
+template <typename O, int VEC>
+__device__ __forceinline__ void write_row(O* dst, const float* acc, float scale, int accumulate, bool aligned) {
+  float f[VEC];
+#pragma unroll
+  for (int i = 0; i < VEC; ++i) {
+    f[i] = acc[i] * scale;
+    if (accumulate) f[i] += to_f(dst[i]);
+  }
+  if (VEC > 1 && aligned) {
+    store_run<O, VEC>(dst, f);
+  } else {
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) dst[i] = from_f<O>(f[i]);
+  }
+}
+
+// The rows of one chunk of sorted tokens, for one tile of columns: thread t
+// owns the vectors t, t + threads, ... (NV of them).  kBatch rows are loaded at
+// a time, then added in order; a sum ends with its id's last token.
+template <typename G, typename O, int VEC, int NV>
 __global__ void __launch_bounds__(256) k_row_sums(const int* __restrict__ key, const int* __restrict__ pos, int n,
                                                   int vocab, const G* __restrict__ grad, Layout2 gl, int dim,
                                                   float scale, int accumulate, O* __restrict__ dw, long long stride,
-                                                  float* __restrict__ part) {
-  const int e0 = blockIdx.x * kChunk, e1 = min(n, e0 + kChunk);
-  const int c = blockIdx.y * blockDim.x + threadIdx.x;
-  if (c >= dim) return;
-  float acc = 0.f;
-  bool open = e0 > 0 && key[e0 - 1] == key[e0];  // the first id's tokens began in an earlier chunk
-  for (int e = e0; e < e1; ++e) {
-    const int k = key[e];
-    if (k >= vocab) return;
-    acc += to_f(__ldg(grad + gl.at(pos[e]) + c));
-    const bool more = e + 1 < n && key[e + 1] == k;
-    if (more && e + 1 < e1) continue;
-    if (open || more) {
-      part[((long long)blockIdx.x * 2 + (open ? 0 : 1)) * dim + c] = acc;
-    } else {
-      O* dst = dw + (long long)k * stride + c;
-      float v = acc * scale;
-      if (accumulate) v += to_f(*dst);
-      *dst = from_f<O>(v);
+                                                  int dw_aligned, float* __restrict__ part) {
+  constexpr int kBatch = 8;
+  __shared__ long long s_off[kChunk];
+  __shared__ int s_key[kChunk + 2];  // with the tokens on both sides (-1: none)
+  after_previous();
+  next_may_launch();
+  const int e0 = blockIdx.x * kChunk, m = min(n - e0, kChunk);
+  const int t = threadIdx.x;
+  if (t < kChunk + 2) {
+    const int e = e0 + t - 1;
+    s_key[t] = t <= m + 1 && e >= 0 && e < n ? __ldcg(key + e) : -1;
+  }
+  if (t < m) s_off[t] = gl.at(__ldcg(pos + e0 + t));
+  __syncthreads();
+  const int c0 = (blockIdx.y * blockDim.x * NV + t) * VEC, step = blockDim.x * VEC;
+  if (c0 >= dim) return;
+  float acc[NV][VEC];
+#pragma unroll
+  for (int j = 0; j < NV; ++j)
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) acc[j][i] = 0.f;
+  bool open = s_key[0] == s_key[1];  // the first id's tokens began in an earlier chunk
+  for (int b = 0; b < m; b += kBatch) {
+    if (s_key[b + 1] >= vocab) return;  // only tokens without a gradient from here on
+    Pack<G, VEC> v[kBatch][NV];
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      if (b + k < m && s_key[b + k + 1] < vocab) {
+#pragma unroll
+        for (int j = 0; j < NV; ++j)
+          if (c0 + j * step < dim) v[k][j] = load_pack<G, VEC>(grad + s_off[b + k] + c0 + j * step);
+      }
     }
-    acc = 0.f;
-    open = false;
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      const int e = b + k;
+      if (e >= m || s_key[e + 1] >= vocab) break;
+#pragma unroll
+      for (int j = 0; j < NV; ++j)
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) acc[j][i] += to_f(v[k][j].v[i]);
+      const bool more = s_key[e + 2] == s_key[e + 1];
+      if (more && e + 1 < m) continue;
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        const int c = c0 + j * step;
+        if (c < dim) {
+          if (open || more) {
+            float* dst = part + ((long long)blockIdx.x * 2 + (open ? 0 : 1)) * dim + c;
+            if (VEC > 1 && dim % 4 == 0) {
+#pragma unroll
+              for (int i = 0; i < VEC; i += 4) store_pack<float, 4>(dst + i, acc[j] + i);
+            } else {
+#pragma unroll
+              for (int i = 0; i < VEC; ++i) dst[i] = acc[j][i];
+            }
+          } else {
+            write_row<O, VEC>(dw + (long long)s_key[e + 1] * stride + c, acc[j], scale, accumulate, dw_aligned);
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) acc[j][i] = 0.f;
+      }
+      open = false;
+    }
   }
 }
 
@@ -222,43 +386,71 @@ __device__ __forceinline__ int upper_bound(const int* __restrict__ key, int lo, 
   int hi = n;
   while (lo < hi) {
     const int mid = lo + (hi - lo) / 2;
-    if (key[mid] <= k) lo = mid + 1;
+    if (__ldcg(key + mid) <= k) lo = mid + 1;
     else hi = mid;
   }
   return lo;
 }
 
+constexpr int kJoinGroups = 8;
+
 // The rows that cross a chunk's end: the chunk where such a row begins adds
-// its partials in chunk order (eight interleaved sums, then those in order).
+// its partials in chunk order (kJoinGroups interleaved sums, then those in
+// order).  blockDim = (32 lanes of 4 columns, kJoinGroups); a CTA looks at the
+// chunk ends blockIdx.x, blockIdx.x + gridDim.x, ...
 template <typename O>
-__global__ void __launch_bounds__(256) k_join_rows(const int* __restrict__ key, int n, int vocab, int dim, float scale,
-                                                   int accumulate, O* __restrict__ dw, long long stride,
-                                                   const float* __restrict__ part) {
-  __shared__ float sums[8][32];
-  const int e0 = blockIdx.x * kChunk, e1 = min(n, e0 + kChunk);
-  if (e1 >= n) return;
-  const int k = key[e1 - 1];
-  if (k >= vocab || key[e1] != k) return;                       // nothing crosses this end
-  if (key[e0] == k && e0 > 0 && key[e0 - 1] == k) return;       // began earlier: not this chunk's
-  const int end = upper_bound(key, e1, n, k);
-  const int chunks = (end - 1) / kChunk - (int)blockIdx.x;      // chunks after this one
-  const int x = threadIdx.x & 31, y = threadIdx.x >> 5;
-  const int c = blockIdx.y * 32 + x;
-  float acc = 0.f;
-  if (c < dim) {
-    if (y == 0) acc = part[((long long)blockIdx.x * 2 + 1) * dim + c];
-    for (int j = 1 + y; j <= chunks; j += 8) acc += part[((long long)blockIdx.x + j) * 2 * dim + c];
-  }
-  sums[y][x] = acc;
-  __syncthreads();
-  if (y != 0 || c >= dim) return;
-  acc = sums[0][x];
+__global__ void __launch_bounds__(32 * kJoinGroups) k_join_rows(const int* __restrict__ key, int n, int vocab, int dim,
+                                                                float scale, int accumulate, O* __restrict__ dw,
+                                                                long long stride, const float* __restrict__ part) {
+  __shared__ float sums[kJoinGroups][32][4];
+  after_previous();
+  const int x = threadIdx.x, y = threadIdx.y;
+  const int c = (blockIdx.y * 32 + x) * 4;
+  const bool vec = dim % 4 == 0;
+  for (int chunk = blockIdx.x; (chunk + 1) * (long long)kChunk < n; chunk += gridDim.x) {
+    const int e0 = chunk * kChunk, e1 = e0 + kChunk;
+    const int k = __ldcg(key + e1 - 1);
+    const bool crosses = k < vocab && __ldcg(key + e1) == k;
+    const bool began = !(e0 > 0 && __ldcg(key + e0) == k && __ldcg(key + e0 - 1) == k);
+    if (!crosses || !began) continue;  // the same for the whole CTA
+    const int end = upper_bound(key, e1, n, k);
+    const int chunks = (end - 1) / kChunk - chunk;  // chunks after this one
+    float acc[4] = {0.f, 0.f, 0.f, 0.f};
+    auto take = [&](const float* src) {
+      if (vec && c < dim) {
+        const float4 v = __ldcg(reinterpret_cast<const float4*>(src));
+        acc[0] += v.x;
+        acc[1] += v.y;
+        acc[2] += v.z;
+        acc[3] += v.w;
+      } else {
 #pragma unroll
-  for (int w = 1; w < 8; ++w) acc += sums[w][x];
-  O* dst = dw + (long long)k * stride + c;
-  float v = acc * scale;
-  if (accumulate) v += to_f(*dst);
-  *dst = from_f<O>(v);
+        for (int i = 0; i < 4; ++i)
+          if (c + i < dim) acc[i] += __ldcg(src + i);
+      }
+    };
+    if (y == 0) take(part + ((long long)chunk * 2 + 1) * dim + c);
+#pragma unroll 4
+    for (int j = 1 + y; j <= chunks; j += kJoinGroups) take(part + ((long long)chunk + j) * 2 * dim + c);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) sums[y][x][i] = acc[i];
+    __syncthreads();
+    if (y == 0) {
+#pragma unroll
+      for (int w = 1; w < kJoinGroups; ++w)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[i] += sums[w][x][i];
+      O* dst = dw + (long long)k * stride + c;
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (c + i < dim) {
+          float v = acc[i] * scale;
+          if (accumulate) v += to_f(dst[i]);
+          dst[i] = from_f<O>(v);
+        }
+    }
+    __syncthreads();
+  }
 }
 
 template <typename F> int by_dtype(int32_t d, F&& f) {
@@ -267,6 +459,27 @@ template <typename F> int by_dtype(int32_t d, F&& f) {
     case PSGD_F16: return f((__half*)nullptr);
     default: return f((__nv_bfloat16*)nullptr);
   }
+}
+
+// Whether rows at two strides all begin at multiples of `to` bytes.
+bool aligned_rows(const void* p, long long s0, long long s1, int size, int to) {
+  return (uintptr_t)p % to == 0 && s0 * size % to == 0 && s1 * size % to == 0;
+}
+
+// How a row is spread over threads: tiles of columns (grid.y), threads of a
+// group, groups of a CTA.
+constexpr int kScalarNv = 4;  // elements per thread and row where accesses are single elements
+struct TilePlan {
+  int threads, groups, tiles;
+};
+TilePlan plan_tile(long long dim, int vec) {
+  const long long per = vec > 1 ? vec : kScalarNv;  // elements per thread
+  const long long want = ((dim + per - 1) / per + 31) / 32 * 32;
+  TilePlan p;
+  p.threads = (int)std::min<long long>(256, want);
+  p.groups = std::max(1, 128 / p.threads);
+  p.tiles = (int)((dim + p.threads * per - 1) / (p.threads * per));
+  return p;
 }
 
 int check_ids(const char* who, const psgd_embedding* e, const void* ids, int32_t id_bits, int64_t outer, int64_t inner,
@@ -396,9 +609,20 @@ extern "C" int psgd_embedding_forward(psgd_embedding* h, const void* weight, psg
     using W = std::remove_pointer_t<decltype(wt)>;
     return by_dtype(out_dtype, [&](auto* ot) {
       using O = std::remove_pointer_t<decltype(ot)>;
-      const int grid = (int)std::min<long long>(n, (long long)h->sms * 8);
-      k_lookup<W, O, 1><<<grid, 256, 0, st>>>((const W*)weight, weight_stride, h->vocab, (int)h->dim, ids,
-                                              id_bits == 64, il, n, scale, (O*)out, ol, h->d_flag);
+      constexpr int V = Vec16<W>::N;
+      const int align = run_alignment(V, sizeof(O));
+      const bool vec = h->dim % V == 0 && aligned_rows(weight, weight_stride, 0, sizeof(W), 16) &&
+                       aligned_rows(out, out_outer_stride, out_inner_stride, sizeof(O), align);
+      const TilePlan p = plan_tile(h->dim, vec ? V : 1);
+      const int tokens = (vec ? 4 : 2) * p.groups;
+      const dim3 grid((unsigned)std::min<long long>((n + tokens - 1) / tokens, (long long)h->sms * 8), p.tiles);
+      const dim3 block(p.threads, p.groups);
+      if (vec)
+        k_lookup<W, O, V, 1><<<grid, block, 0, st>>>((const W*)weight, weight_stride, h->vocab, (int)h->dim, ids,
+                                                     id_bits == 64, il, n, scale, (O*)out, ol, h->d_flag);
+      else
+        k_lookup<W, O, 1, kScalarNv><<<grid, block, 0, st>>>((const W*)weight, weight_stride, h->vocab, (int)h->dim,
+                                                             ids, id_bits == 64, il, n, scale, (O*)out, ol, h->d_flag);
       return 0;
     });
   });
@@ -434,36 +658,58 @@ extern "C" int psgd_embedding_backward(psgd_embedding* h, const void* ids, int32
   const int dim = (int)h->dim, vocab = (int)h->vocab;
   int passes = 1;
   while (passes < 4 && (vocab >> (8 * passes)) != 0) ++passes;
-  // pass p writes buffer p % 2
-  const int last = (passes - 1) & 1;
-  if (!accumulate) {
+  cudaError_t e = cudaSuccess;
+  // A table without gaps is zeroed beside the sort, in one launch.
+  const bool beside = !accumulate && n > 0 && (dweight_stride == dim || vocab == 1);
+  if (!accumulate && !beside) {
     by_dtype(dweight_dtype, [&](auto* ot) {
       using O = std::remove_pointer_t<decltype(ot)>;
       k_zero_rows<O><<<(unsigned)std::min<long long>(vocab, h->sms * 8), 256, 0, st>>>((O*)dweight, vocab, dim,
                                                                                      dweight_stride);
       return 0;
     });
+    e = cudaGetLastError();
   }
-  if (n > 0) {
-    k_sort_tokens<<<kSortCtas, kSortThreads, 0, st>>>(ids, id_bits == 64, il, n, vocab, padding_idx, passes, h->key[0],
-                                                      h->pos[0], h->key[1], h->pos[1], h->d_flag);
+  if (n > 0 && e == cudaSuccess) {
+    SortArgs a{ids, id_bits == 64, il, n, vocab, padding_idx, passes, {h->key[0], h->key[1]}, {h->pos[0], h->pos[1]},
+               h->d_flag, beside ? dweight : nullptr, beside ? wb : 0};
+    // a cluster of zeroing CTAs per 512 KB, up to one wave of them
+    const unsigned zero = beside ? (unsigned)std::min<long long>((wb + (1 << 19) - 1) >> 19, (h->sms - kSortCtas) / kSortCtas) : 0;
+    const unsigned grid = kSortCtas * (1 + zero);
+    if (n <= kSortCtas * kSortThreads * 2) k_sort_and_zero<2><<<grid, kSortThreads, 0, st>>>(a);
+    else k_sort_and_zero<0><<<grid, kSortThreads, 0, st>>>(a);
+    e = cudaGetLastError();
     const unsigned chunks = (unsigned)((n + kChunk - 1) / kChunk);
-    const int *key = h->key[last], *pos = h->pos[last];
+    const int *key = h->key[(passes - 1) & 1], *pos = h->pos[(passes - 1) & 1];
+    cudaLaunchAttribute early = early_launch();
+    cudaLaunchConfig_t cfg = {};
+    cfg.stream = st;
+    cfg.attrs = &early;
+    cfg.numAttrs = 1;
     by_dtype(grad_dtype, [&](auto* gt) {
       using G = std::remove_pointer_t<decltype(gt)>;
       return by_dtype(dweight_dtype, [&](auto* ot) {
         using O = std::remove_pointer_t<decltype(ot)>;
-        k_row_sums<G, O><<<dim3(chunks, (dim + 255) / 256), 256, 0, st>>>(key, pos, n, vocab, (const G*)grad, gl, dim,
-                                                                         scale, accumulate, (O*)dweight,
-                                                                         dweight_stride, h->part);
-        if (chunks > 1)
-          k_join_rows<O><<<dim3(chunks, (dim + 31) / 32), 256, 0, st>>>(key, n, vocab, dim, scale, accumulate,
-                                                                       (O*)dweight, dweight_stride, h->part);
+        constexpr int V = Vec16<G>::N;
+        const bool vec = dim % V == 0 && aligned_rows(grad, grad_outer_stride, grad_inner_stride, sizeof(G), 16);
+        const int dw_aligned = aligned_rows(dweight, dweight_stride, 0, sizeof(O), run_alignment(V, sizeof(O)));
+        const TilePlan p = plan_tile(dim, vec ? V : 1);
+        cfg.gridDim = dim3(chunks, p.tiles);
+        cfg.blockDim = dim3(std::max(p.threads, 64));
+        if (e == cudaSuccess)
+          e = cudaLaunchKernelEx(&cfg, vec ? k_row_sums<G, O, V, 1> : k_row_sums<G, O, 1, kScalarNv>, key, pos, n, vocab,
+                                 (const G*)grad, gl, dim, scale, (int)accumulate, (O*)dweight, (long long)dweight_stride,
+                                 dw_aligned, h->part);
+        if (chunks > 1 && e == cudaSuccess) {
+          cfg.gridDim = dim3(std::min(chunks - 1, (unsigned)h->sms), (dim + 127) / 128);
+          cfg.blockDim = dim3(32, kJoinGroups);
+          e = cudaLaunchKernelEx(&cfg, k_join_rows<O>, key, n, vocab, dim, scale, (int)accumulate, (O*)dweight,
+                                 (long long)dweight_stride, (const float*)h->part);
+        }
         return 0;
       });
     });
   }
-  const cudaError_t e = cudaGetLastError();
   return e == cudaSuccess ? PSGD_OK : cuda_fail(who, e);
 }
 

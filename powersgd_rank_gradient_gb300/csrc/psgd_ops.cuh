@@ -124,6 +124,36 @@ template <typename T, int V> __device__ __forceinline__ void store_pack(T* p, co
   }
 }
 
+// V values into V consecutive elements, 16 bytes at a time (8 where they are
+// no more): the address is a multiple of that.
+template <typename T, int V> __device__ __forceinline__ void store_run(T* p, const float* f) {
+  constexpr int N = Vec16<T>::N;
+  if constexpr (V == 1) {
+    p[0] = from_f<T>(f[0]);
+  } else if constexpr (V >= N) {
+#pragma unroll
+    for (int i = 0; i < V; i += N) store_pack<T, N>(p + i, f + i);
+  } else {
+    static_assert(V == 4 && sizeof(T) == 2, "8 bytes");
+    *reinterpret_cast<uint2*>(p) = make_uint2(pack2<T>(f[0], f[1]), pack2<T>(f[2], f[3]));
+  }
+}
+// The alignment in bytes that store_run of V elements of `size` bytes asks for.
+inline int run_alignment(int v, int size) { return v == 1 ? size : (v * size >= 16 ? 16 : v * size); }
+
+// The kernel launch attribute that lets a kernel be set up while the one before
+// it in the stream still runs; it then begins with after_previous().
+inline cudaLaunchAttribute early_launch() {
+  cudaLaunchAttribute a;
+  a.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  a.val.programmaticStreamSerializationAllowed = 1;
+  return a;
+}
+// Waits until everything the previous kernel of the stream wrote is visible.
+__device__ __forceinline__ void after_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+// Lets the next kernel of the stream be set up.
+__device__ __forceinline__ void next_may_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
 // Element i of an array of runtime type.
 __device__ __forceinline__ float load_any(const void* p, int dtype, long long i) {
   if (dtype == PSGD_F32) return __ldg((const float*)p + i);
