@@ -12,7 +12,9 @@
 #include <cooperative_groups.h>
 
 #include <algorithm>
+#include <atomic>
 #include <new>
+#include <type_traits>
 
 #include "psgd_ops.cuh"
 
@@ -26,6 +28,8 @@ struct psgd_embedding {
   int* key[2] = {nullptr, nullptr};
   int* pos[2] = {nullptr, nullptr};
   float* part = nullptr;  // per chunk: the partial rows of its first and its last id
+  int2* crossing = nullptr;  // rows that cross a chunk's end: (chunk where they begin, id)
+  int* counts = nullptr;     // how many of those; sorted tokens
   int* d_flag = nullptr;  // an id outside [0, vocab) was seen
   int* h_flag = nullptr;  // pinned
   size_t bytes = 0;
@@ -35,11 +39,10 @@ namespace psgd {
 namespace ops {
 namespace {
 
-constexpr int kChunk = 32;          // sorted tokens per CTA of the row sums
+constexpr int kMaxChunk = 32;       // sorted tokens per CTA of the row sums, at most
 constexpr int kSortCtas = 8;        // CTAs of the sort's cluster
 constexpr int kSortThreads = 1024;
 constexpr int kSortWarps = kSortThreads / 32;
-constexpr int kDigits = 256;        // 8 bits a radix pass
 
 // Tokens in an (outer, inner) layout: token i = o * inner + n, at
 // o * os + n * is in units of the operand's elements.
@@ -56,17 +59,19 @@ __device__ __forceinline__ long long load_id(const void* ids, int id64, long lon
   return id64 ? __ldg((const long long*)ids + at) : (long long)__ldg((const int*)ids + at);
 }
 
+constexpr int kLookup = 2;
+
 // A group of threads (blockDim = (threads of a group, groups)) takes kLookup
 // tokens at a time, so that as many row loads are in flight per thread; thread
 // t owns the vectors t, t + threads, ... (NV of them) of a tile of columns.
 template <typename W, typename O, int VEC, int NV>
-__global__ void __launch_bounds__(256) k_lookup(const W* __restrict__ weight, long long wstride, long long vocab,
+__global__ void __launch_bounds__(256, VEC == 8 ? 6 : 8) k_lookup(const W* __restrict__ weight, long long wstride, long long vocab,
                                                 int dim, const void* __restrict__ ids, int id64, Layout2 il, int n,
                                                 float scale, O* __restrict__ out, Layout2 ol, int* flag) {
-  constexpr int T = VEC == 1 ? 2 : 4;  // tokens at a time
+  constexpr int T = kLookup;
   const int c0 = (blockIdx.y * blockDim.x * NV + threadIdx.x) * VEC, step = blockDim.x * VEC;
-  const int group = blockIdx.x * blockDim.y + threadIdx.y, groups = gridDim.x * blockDim.y;
-  for (long long i0 = (long long)group * T; i0 < n; i0 += groups * T) {
+  const long long i0 = ((long long)blockIdx.x * blockDim.y + threadIdx.y) * T;
+  if (i0 < n) {
     long long id[T];
     bool ok[T];
 #pragma unroll
@@ -108,62 +113,76 @@ struct SortArgs {
   int passes;
   int *key[2], *pos[2];  // pass p writes buffer p & 1
   int* flag;
-  // the table to zero beside the sort (NULL: none): a run of bytes
-  void* zero;
-  long long zero_bytes;
+  int* counts;           // out: [0] = 0 (crossing rows found so far), [1] = tokens with a gradient
 };
 
-struct SortShared {
-  int cnt[kSortWarps][kDigits];
-  int quarter[4][kDigits];
+template <int BITS> struct SortShared {
+  // a CTA's counts fit 16 bits where a digit has 10 (the host sees to it)
+  using Count = typename std::conditional<(BITS > 8), unsigned short, int>::type;
+  static constexpr int kDigits = 1 << BITS;
+  static constexpr int kParts = kSortThreads / kDigits;  // threads per digit of the scan over the warps
+  Count cnt[kSortWarps][kDigits];
+  int part[kParts][kDigits];
   int totals[kSortCtas][kDigits];  // every CTA's digit totals, pushed by the peers
   int base[kDigits];
-  int scan[kDigits / 32];
+  int scan[32];
+  int all;
 };
 
-// Stable least-significant-digit radix sort of (key, position) by one cluster:
-// key = id, or `vocab` for a token without a gradient (padding, or an id
-// outside the table), which sorts behind every row.  Each warp owns a
-// contiguous share of the list, so that digit counts per (CTA, warp), scanned
-// in list order, give every element its place; each CTA writes its digit totals
-// into its peers' shared memory.  A share of at most 32 x ITEMS elements stays
-// in registers between counting and placing (ITEMS = 0: any share, read twice).
-template <int ITEMS> __device__ __forceinline__ void sort_tokens(const SortArgs& a, SortShared& s) {
+// Stable least-significant-digit radix sort of (id, position) by one cluster of
+// CTAS.  Tokens without a gradient (padding, or an id outside the table) are
+// dropped by the first pass.  Each warp owns a contiguous share of the list, so
+// that digit counts per (CTA, warp), scanned in list order, give every element
+// its place; each CTA writes its digit totals into its peers' shared memory.  A
+// share of at most 32 x ITEMS elements stays in registers between counting and
+// placing (ITEMS = 0: any share, read twice).  The time is the chain of
+// latencies of a pass (a load, the barriers, a scan, a scattered store), so
+// tables of up to 1024 rows take one pass of 10 bits in place of two of 8, and
+// up to 2048 tokens one CTA without a cluster's barriers.
+template <int CTAS, int ITEMS, int BITS> __global__ void __launch_bounds__(kSortThreads) k_sort_tokens(SortArgs a) {
+  using Shared = SortShared<BITS>;
+  constexpr int D = Shared::kDigits, PARTS = Shared::kParts, PER = kSortWarps / PARTS;
+  extern __shared__ __align__(16) unsigned char raw[];
+  Shared& s = *reinterpret_cast<Shared*>(raw);
+  next_may_launch();
   cg::cluster_group cluster = cg::this_cluster();
-  const int rank = (int)cluster.block_rank();
+  const int rank = CTAS > 1 ? (int)cluster.block_rank() : 0;
+  if (CTAS > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
   const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
   const unsigned below = (1u << lane) - 1u;
-  const int per = (int)((a.n + (long long)kSortCtas * kSortThreads - 1) / ((long long)kSortCtas * kSortThreads)) * 32;
-  const long long first = ((long long)rank * kSortWarps + warp) * per;
-  const int share = (int)max(0LL, min((long long)a.n - first, (long long)per));  // of this warp
+  int n = a.n;
   for (int p = 0; p < a.passes; ++p) {
-    const int shift = 8 * p;
+    const int shift = BITS * p;
     const int *sk = p & 1 ? a.key[0] : a.key[1], *sp = p & 1 ? a.pos[0] : a.pos[1];
     int *dk = p & 1 ? a.key[1] : a.key[0], *dp = p & 1 ? a.pos[1] : a.pos[0];
+    const int per = (int)((n + (long long)CTAS * kSortThreads - 1) / ((long long)CTAS * kSortThreads)) * 32;
+    const long long first = ((long long)rank * kSortWarps + warp) * per;
+    const int share = (int)max(0LL, min((long long)n - first, (long long)per));  // of this warp
+    // a token's id, or -1 if it has no gradient
     auto key_at = [&](long long i) -> int {
       if (p > 0) return __ldcg(sk + i);
       const long long id = load_id(a.ids, a.id64, a.il.at((int)i));
       if (id < 0 || id >= a.vocab) {
         *a.flag = 1;
-        return a.vocab;
+        return -1;
       }
-      return id == a.padding ? a.vocab : (int)id;
+      return id == a.padding ? -1 : (int)id;
     };
+    auto digit = [&](int key) { return key < 0 ? D : (key >> shift) & (D - 1); };
     auto count = [&](int d) {
       const unsigned same = __match_any_sync(0xffffffffu, d);
-      if (d < kDigits && (same & below) == 0) s.cnt[warp][d] += __popc(same);
+      if (d < D && (same & below) == 0) s.cnt[warp][d] += __popc(same);
       __syncwarp();
     };
     auto place = [&](int d, int key, int pos) {
       const unsigned same = __match_any_sync(0xffffffffu, d);
-      int at = 0;
-      if (d < kDigits) {
-        at = s.base[d] + s.cnt[warp][d] + __popc(same & below);
+      if (d < D) {
+        const int at = s.base[d] + s.cnt[warp][d] + __popc(same & below);
         dk[at] = key;
         dp[at] = pos;
       }
       __syncwarp();
-      if (d < kDigits && (same & below) == 0) s.cnt[warp][d] += __popc(same);
+      if (d < D && (same & below) == 0) s.cnt[warp][d] += __popc(same);
       __syncwarp();
     };
     int key[ITEMS > 0 ? ITEMS : 1], pos[ITEMS > 0 ? ITEMS : 1];
@@ -171,121 +190,124 @@ template <int ITEMS> __device__ __forceinline__ void sort_tokens(const SortArgs&
 #pragma unroll
       for (int i = 0; i < ITEMS; ++i) {
         const int e = i * 32 + lane;
-        key[i] = e < share ? key_at(first + e) : 0;
+        key[i] = e < share ? key_at(first + e) : -1;
         pos[i] = e < share ? (p > 0 ? __ldcg(sp + first + e) : (int)first + e) : 0;
       }
     }
-    for (int i = t; i < kSortWarps * kDigits; i += kSortThreads) (&s.cnt[0][0])[i] = 0;
+    {
+      uint4* z = reinterpret_cast<uint4*>(&s.cnt[0][0]);
+      for (int i = t; i < (int)(sizeof(s.cnt) / 16); i += kSortThreads) z[i] = make_uint4(0, 0, 0, 0);
+    }
     __syncthreads();
     if constexpr (ITEMS > 0) {
 #pragma unroll
       for (int i = 0; i < ITEMS; ++i)
-        if (i * 32 < share) count(i * 32 + lane < share ? (key[i] >> shift) & (kDigits - 1) : kDigits);
+        if (i * 32 < share) count(digit(key[i]));
     } else {
-      for (int e = lane; e - lane < share; e += 32)
-        count(e < share ? (key_at(first + e) >> shift) & (kDigits - 1) : kDigits);
+      for (int e = lane; e - lane < share; e += 32) count(e < share ? digit(key_at(first + e)) : D);
     }
     __syncthreads();
-    // exclusive counts over the warps, a quarter of them per thread
-    const int d = t & (kDigits - 1), q = t / kDigits;
-    {
-      int sum = 0;
+    // exclusive counts over the warps, PER of them per thread
+    const int d = t & (D - 1), q = t / D;
+    int total = 0;
 #pragma unroll
-      for (int w = 0; w < kSortWarps / 4; ++w) {
-        const int c = s.cnt[q * (kSortWarps / 4) + w][d];
-        s.cnt[q * (kSortWarps / 4) + w][d] = sum;
-        sum += c;
-      }
-      s.quarter[q][d] = sum;
-    }
-    __syncthreads();
-    int ahead = 0, total = 0;
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const int c = s.quarter[k][d];
-      if (k < q) ahead += c;
+    for (int w = 0; w < PER; ++w) {
+      const int c = s.cnt[q * PER + w][d];
+      s.cnt[q * PER + w][d] = total;
       total += c;
     }
-    if (q > 0) {
+    if constexpr (PARTS > 1) {
+      s.part[q][d] = total;
+      __syncthreads();
+      int ahead = 0;
+      total = 0;
 #pragma unroll
-      for (int w = 0; w < kSortWarps / 4; ++w) s.cnt[q * (kSortWarps / 4) + w][d] += ahead;
-    }
-    // two of the peers each
-#pragma unroll
-    for (int k = 0; k < kSortCtas / 4; ++k) {
-      const int peer = q * (kSortCtas / 4) + k;
-      cluster.map_shared_rank(&s.totals[rank][0], peer)[d] = total;
-    }
-    cluster.sync();
-    if (t < kDigits) {
-      int before = 0, all = 0;
-#pragma unroll
-      for (int r = 0; r < kSortCtas; ++r) {
-        const int c = s.totals[r][t];
-        if (r < rank) before += c;
-        all += c;
+      for (int k = 0; k < PARTS; ++k) {
+        const int c = s.part[k][d];
+        if (k < q) ahead += c;
+        total += c;
       }
-      int inc = all;  // inclusive scan over the digits
+      if (q > 0) {
+#pragma unroll
+        for (int w = 0; w < PER; ++w) s.cnt[q * PER + w][d] += ahead;
+      }
+    }
+    if constexpr (CTAS > 1) {
+      if (p == 0) asm volatile("barrier.cluster.wait.aligned;" ::: "memory");  // all have started
+#pragma unroll
+      for (int k = 0; k < CTAS / PARTS; ++k)
+        cluster.map_shared_rank(&s.totals[rank][0], q * (CTAS / PARTS) + k)[d] = total;
+      cluster.sync();
+    }
+    int before = 0, all = 0, inc = 0;
+    if (t < D) {
+      if constexpr (CTAS > 1) {
+#pragma unroll
+        for (int r = 0; r < CTAS; ++r) {
+          const int c = s.totals[r][t];
+          if (r < rank) before += c;
+          all += c;
+        }
+      } else {
+        all = total;
+      }
+      inc = all;  // inclusive scan over the digits of a warp
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const int v = __shfl_up_sync(0xffffffffu, inc, o);
         if (lane >= o) inc += v;
       }
       if (lane == 31) s.scan[warp] = inc;
-      s.base[t] = inc - all + before;
     }
     __syncthreads();
-    if (t < kDigits) {
-      int add = 0;
-      for (int w = 0; w < warp; ++w) add += s.scan[w];
-      s.base[t] += add;
+    if (t < D) {
+      const int mine = lane < D / 32 ? s.scan[lane] : 0;
+      const int ahead = __reduce_add_sync(0xffffffffu, lane < warp ? mine : 0);
+      s.base[t] = ahead + inc - all + before;
+      if (t == D - 1) s.all = ahead + inc;
     }
     __syncthreads();
     if constexpr (ITEMS > 0) {
 #pragma unroll
       for (int i = 0; i < ITEMS; ++i)
-        if (i * 32 < share)
-          place(i * 32 + lane < share ? (key[i] >> shift) & (kDigits - 1) : kDigits, key[i], pos[i]);
+        if (i * 32 < share) place(digit(key[i]), key[i], pos[i]);
     } else {
       for (int e = lane; e - lane < share; e += 32) {
-        const bool in = e < share;
-        const int k = in ? key_at(first + e) : 0;
-        place(in ? (k >> shift) & (kDigits - 1) : kDigits, k,
-              in ? (p > 0 ? __ldcg(sp + first + e) : (int)first + e) : 0);
+        const int k = e < share ? key_at(first + e) : -1;
+        place(digit(k), k, e < share ? (p > 0 ? __ldcg(sp + first + e) : (int)first + e) : 0);
       }
     }
-    cluster.sync();  // this pass's output, for every CTA of the cluster; the totals are free again
+    n = s.all;
+    if (p + 1 < a.passes) {
+      // this pass's output, for every CTA of the cluster; the totals are free again
+      if constexpr (CTAS > 1) cluster.sync();
+      else __syncthreads();
+    }
+  }
+  if (rank == 0 && t == 0) {
+    a.counts[0] = 0;
+    a.counts[1] = n;
   }
 }
 
-// The first cluster sorts the tokens; the others, if any, zero the table.
-template <int ITEMS>
-__global__ void __cluster_dims__(kSortCtas, 1, 1) __launch_bounds__(kSortThreads) k_sort_and_zero(SortArgs a) {
-  __shared__ SortShared s;
-  next_may_launch();
-  if (blockIdx.x < kSortCtas) {
-    cg::this_cluster().sync();  // all have started: their shared memory may be written
-    sort_tokens<ITEMS>(a, s);
-    return;
+// Zeroes `rows` rows of `bytes` bytes, `stride` bytes apart (one row: a whole
+// table without gaps), 16 bytes at a time between the first and the last
+// boundary, the ends by bytes.  Started beside the sort (EARLY), it ends only
+// when that has.
+template <bool EARLY>
+__global__ void __launch_bounds__(256) k_zero(char* __restrict__ w, long long rows, long long bytes, long long stride) {
+  if (EARLY) next_may_launch();
+  const long long t = (long long)blockIdx.x * blockDim.x + threadIdx.x, step = (long long)gridDim.x * blockDim.x;
+  for (long long r = blockIdx.y; r < rows; r += gridDim.y) {
+    char* p = w + r * stride;
+    const long long head = min(bytes, (long long)((16 - ((uintptr_t)p & 15)) & 15));
+    const long long vecs = (bytes - head) / 16, tail = bytes - head - vecs * 16;
+    uint4* v = reinterpret_cast<uint4*>(p + head);
+    for (long long i = t; i < vecs; i += step) v[i] = make_uint4(0, 0, 0, 0);
+    if (t < head) p[t] = 0;
+    if (t < tail) p[head + vecs * 16 + t] = 0;
   }
-  // 16 bytes at a time between the first and the last boundary, the ends by bytes
-  const long long t = (long long)(blockIdx.x - kSortCtas) * kSortThreads + threadIdx.x;
-  const long long step = (long long)(gridDim.x - kSortCtas) * kSortThreads;
-  char* p = (char*)a.zero;
-  const long long head = min(a.zero_bytes, (long long)((16 - ((uintptr_t)p & 15)) & 15));
-  const long long vecs = (a.zero_bytes - head) / 16, tail = a.zero_bytes - head - vecs * 16;
-  uint4* v = reinterpret_cast<uint4*>(p + head);
-  for (long long i = t; i < vecs; i += step) v[i] = make_uint4(0, 0, 0, 0);
-  if (t < head) p[t] = 0;
-  if (t < tail) p[head + vecs * 16 + t] = 0;
-}
-
-// Zeroes `rows` rows of `dim` elements, `stride` apart.
-template <typename O>
-__global__ void __launch_bounds__(256) k_zero_rows(O* __restrict__ w, long long rows, long long dim, long long stride) {
-  const O zero = from_f<O>(0.f);
-  for (long long r = blockIdx.x; r < rows; r += gridDim.x)
-    for (long long c = threadIdx.x; c < dim; c += blockDim.x) w[r * stride + c] = zero;
+  if (EARLY) after_previous();
 }
 
 // A finished sum into its row of the table: as VEC elements if they are
@@ -310,23 +332,26 @@ __device__ __forceinline__ void write_row(O* dst, const float* acc, float scale,
 // owns the vectors t, t + threads, ... (NV of them).  kBatch rows are loaded at
 // a time, then added in order; a sum ends with its id's last token.
 template <typename G, typename O, int VEC, int NV>
-__global__ void __launch_bounds__(256) k_row_sums(const int* __restrict__ key, const int* __restrict__ pos, int n,
-                                                  int vocab, const G* __restrict__ grad, Layout2 gl, int dim,
+__global__ void __launch_bounds__(256, VEC == 1 ? 2 : 4) k_row_sums(const int* __restrict__ key, const int* __restrict__ pos, const G* __restrict__ grad, Layout2 gl, int dim,
                                                   float scale, int accumulate, O* __restrict__ dw, long long stride,
-                                                  int dw_aligned, float* __restrict__ part) {
-  constexpr int kBatch = 8;
-  __shared__ long long s_off[kChunk];
-  __shared__ int s_key[kChunk + 2];  // with the tokens on both sides (-1: none)
+                                                  int dw_aligned, float* __restrict__ part, int chunk, int2* __restrict__ crossing, int* __restrict__ counts) {
+  constexpr int kBatch = VEC == 8 ? 4 : 8;
+  __shared__ long long s_off[kMaxChunk];
+  __shared__ int s_key[kMaxChunk + 2];  // with the tokens on both sides (-1: none)
   after_previous();
   next_may_launch();
-  const int e0 = blockIdx.x * kChunk, m = min(n - e0, kChunk);
+  const int n = __ldcg(counts + 1);  // sorted tokens
+  const int e0 = blockIdx.x * chunk, m = min(n - e0, chunk);
+  if (m <= 0) return;
   const int t = threadIdx.x;
-  if (t < kChunk + 2) {
+  if (t < m + 2) {
     const int e = e0 + t - 1;
-    s_key[t] = t <= m + 1 && e >= 0 && e < n ? __ldcg(key + e) : -1;
+    s_key[t] = e >= 0 && e < n ? __ldcg(key + e) : -1;
   }
   if (t < m) s_off[t] = gl.at(__ldcg(pos + e0 + t));
   __syncthreads();
+  if (t == 0 && blockIdx.y == 0 && s_key[m + 1] == s_key[m] && s_key[0] != s_key[m])
+    crossing[atomicAdd(counts, 1)] = make_int2(blockIdx.x, s_key[m]);  // a row begins here and goes on in the next chunk
   const int c0 = (blockIdx.y * blockDim.x * NV + t) * VEC, step = blockDim.x * VEC;
   if (c0 >= dim) return;
   float acc[NV][VEC];
@@ -336,11 +361,10 @@ __global__ void __launch_bounds__(256) k_row_sums(const int* __restrict__ key, c
     for (int i = 0; i < VEC; ++i) acc[j][i] = 0.f;
   bool open = s_key[0] == s_key[1];  // the first id's tokens began in an earlier chunk
   for (int b = 0; b < m; b += kBatch) {
-    if (s_key[b + 1] >= vocab) return;  // only tokens without a gradient from here on
     Pack<G, VEC> v[kBatch][NV];
 #pragma unroll
     for (int k = 0; k < kBatch; ++k) {
-      if (b + k < m && s_key[b + k + 1] < vocab) {
+      if (b + k < m) {
 #pragma unroll
         for (int j = 0; j < NV; ++j)
           if (c0 + j * step < dim) v[k][j] = load_pack<G, VEC>(grad + s_off[b + k] + c0 + j * step);
@@ -349,7 +373,7 @@ __global__ void __launch_bounds__(256) k_row_sums(const int* __restrict__ key, c
 #pragma unroll
     for (int k = 0; k < kBatch; ++k) {
       const int e = b + k;
-      if (e >= m || s_key[e + 1] >= vocab) break;
+      if (e >= m) break;
 #pragma unroll
       for (int j = 0; j < NV; ++j)
 #pragma unroll
@@ -381,40 +405,34 @@ __global__ void __launch_bounds__(256) k_row_sums(const int* __restrict__ key, c
   }
 }
 
-// One past the last sorted token whose key is `k`, known to be >= lo.
-__device__ __forceinline__ int upper_bound(const int* __restrict__ key, int lo, int n, int k) {
-  int hi = n;
-  while (lo < hi) {
-    const int mid = lo + (hi - lo) / 2;
-    if (__ldcg(key + mid) <= k) lo = mid + 1;
-    else hi = mid;
-  }
-  return lo;
-}
-
 constexpr int kJoinGroups = 8;
 
-// The rows that cross a chunk's end: the chunk where such a row begins adds
-// its partials in chunk order (kJoinGroups interleaved sums, then those in
-// order).  blockDim = (32 lanes of 4 columns, kJoinGroups); a CTA looks at the
-// chunk ends blockIdx.x, blockIdx.x + gridDim.x, ...
+// The rows that cross a chunk's end, as listed by the chunks where they begin
+// (chunk, id): each adds its partials in chunk order, kJoinGroups interleaved
+// sums and then those in order, so the list's own order does not matter.
+// blockDim = (32 lanes of 4 columns, kJoinGroups).
 template <typename O>
-__global__ void __launch_bounds__(32 * kJoinGroups) k_join_rows(const int* __restrict__ key, int n, int vocab, int dim,
-                                                                float scale, int accumulate, O* __restrict__ dw,
-                                                                long long stride, const float* __restrict__ part) {
+__global__ void __launch_bounds__(32 * kJoinGroups) k_join_rows(const int* __restrict__ key, int dim, float scale,
+                                                                int accumulate, O* __restrict__ dw, long long stride,
+                                                                const float* __restrict__ part, int chunk,
+                                                                const int2* __restrict__ crossing,
+                                                                const int* __restrict__ counts) {
   __shared__ float sums[kJoinGroups][32][4];
   after_previous();
   const int x = threadIdx.x, y = threadIdx.y;
   const int c = (blockIdx.y * 32 + x) * 4;
   const bool vec = dim % 4 == 0;
-  for (int chunk = blockIdx.x; (chunk + 1) * (long long)kChunk < n; chunk += gridDim.x) {
-    const int e0 = chunk * kChunk, e1 = e0 + kChunk;
-    const int k = __ldcg(key + e1 - 1);
-    const bool crosses = k < vocab && __ldcg(key + e1) == k;
-    const bool began = !(e0 > 0 && __ldcg(key + e0) == k && __ldcg(key + e0 - 1) == k);
-    if (!crosses || !began) continue;  // the same for the whole CTA
-    const int end = upper_bound(key, e1, n, k);
-    const int chunks = (end - 1) / kChunk - chunk;  // chunks after this one
+  const int count = __ldcg(counts), n = __ldcg(counts + 1);
+  for (int i = blockIdx.x; i < count; i += gridDim.x) {
+    const int2 who = __ldcg(crossing + i);
+    // the chunks after this one that begin with the row's id
+    int chunks = 0;
+    for (;;) {
+      const long long e = ((long long)who.x + 1 + chunks + y * 32 + x) * chunk;
+      const int more = __syncthreads_count(e < n && __ldcg(key + e) == who.y);
+      chunks += more;
+      if (more < 32 * kJoinGroups) break;
+    }
     float acc[4] = {0.f, 0.f, 0.f, 0.f};
     auto take = [&](const float* src) {
       if (vec && c < dim) {
@@ -425,28 +443,28 @@ __global__ void __launch_bounds__(32 * kJoinGroups) k_join_rows(const int* __res
         acc[3] += v.w;
       } else {
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          if (c + i < dim) acc[i] += __ldcg(src + i);
+        for (int k = 0; k < 4; ++k)
+          if (c + k < dim) acc[k] += __ldcg(src + k);
       }
     };
-    if (y == 0) take(part + ((long long)chunk * 2 + 1) * dim + c);
-#pragma unroll 4
-    for (int j = 1 + y; j <= chunks; j += kJoinGroups) take(part + ((long long)chunk + j) * 2 * dim + c);
+    if (y == 0) take(part + ((long long)who.x * 2 + 1) * dim + c);
+#pragma unroll 8
+    for (int j = 1 + y; j <= chunks; j += kJoinGroups) take(part + ((long long)who.x + j) * 2 * dim + c);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) sums[y][x][i] = acc[i];
+    for (int k = 0; k < 4; ++k) sums[y][x][k] = acc[k];
     __syncthreads();
     if (y == 0) {
 #pragma unroll
       for (int w = 1; w < kJoinGroups; ++w)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) acc[i] += sums[w][x][i];
-      O* dst = dw + (long long)k * stride + c;
+        for (int k = 0; k < 4; ++k) acc[k] += sums[w][x][k];
+      O* dst = dw + (long long)who.y * stride + c;
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (c + i < dim) {
-          float v = acc[i] * scale;
-          if (accumulate) v += to_f(dst[i]);
-          dst[i] = from_f<O>(v);
+      for (int k = 0; k < 4; ++k)
+        if (c + k < dim) {
+          float v = acc[k] * scale;
+          if (accumulate) v += to_f(dst[k]);
+          dst[k] = from_f<O>(v);
         }
     }
     __syncthreads();
@@ -459,6 +477,49 @@ template <typename F> int by_dtype(int32_t d, F&& f) {
     case PSGD_F16: return f((__half*)nullptr);
     default: return f((__nv_bfloat16*)nullptr);
   }
+}
+
+template <int CTAS, int ITEMS, int BITS> cudaError_t launch_sort(const SortArgs& a, int device, cudaStream_t st) {
+  constexpr int bytes = (int)sizeof(SortShared<BITS>);
+  static std::atomic<unsigned long long> raised{0};  // devices whose shared-memory limit is raised
+  const unsigned long long bit = 1ull << device;
+  if (!(raised.load(std::memory_order_acquire) & bit)) {
+    const cudaError_t e =
+        cudaFuncSetAttribute(k_sort_tokens<CTAS, ITEMS, BITS>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e != cudaSuccess) return e;
+    raised.fetch_or(bit, std::memory_order_release);
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(CTAS);
+  cfg.blockDim = dim3(kSortThreads);
+  cfg.dynamicSmemBytes = bytes;
+  cfg.stream = st;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = CTAS;
+  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = CTAS > 1 ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, k_sort_tokens<CTAS, ITEMS, BITS>, a);
+}
+
+// Sorted tokens per CTA of the row sums: 32, or 8 to 16 where that would leave
+// multiprocessors idle.
+int chunk_for(long long n, int sms) {
+  int c = kMaxChunk;
+  while (c > 8 && n < (long long)c * sms * 2) c /= 2;
+  return c;
+}
+
+// The most chunks that up to n tokens make.
+long long max_chunks(long long n, int sms) {
+  long long most = (n + chunk_for(n, sms) - 1) / chunk_for(n, sms);
+  // fewer tokens in smaller chunks can make more of them: at the sizes where the length halves
+  for (int c = kMaxChunk / 2; c >= 8; c /= 2) {
+    const long long last = std::min(n, (long long)2 * c * sms * 2 - 1);  // the most tokens that get chunks of c or less
+    if (last > 0) most = std::max(most, (last + c - 1) / c);
+  }
+  return std::max<long long>(most, 1);
 }
 
 // Whether rows at two strides all begin at multiples of `to` bytes.
@@ -539,20 +600,22 @@ extern "C" int psgd_embedding_create(int64_t vocab, int64_t dim, int64_t max_tok
   h->vocab = vocab;
   h->dim = dim;
   h->max_tokens = max_tokens;
+  e = cudaDeviceGetAttribute(&h->sms, cudaDevAttrMultiProcessorCount, device);
   const long long n = std::max<long long>(1, max_tokens);
-  const long long chunks = (n + kChunk - 1) / kChunk;
+  const long long chunks = max_chunks(n, h->sms);
   auto alloc = [&](void** p, long long bytes) {
     if (e != cudaSuccess) return;
     e = cudaMalloc(p, (size_t)bytes);
     if (e == cudaSuccess) h->bytes += (size_t)bytes;
     else *p = nullptr;
   };
-  e = cudaDeviceGetAttribute(&h->sms, cudaDevAttrMultiProcessorCount, device);
   for (int i = 0; i < 2; ++i) {
     alloc((void**)&h->key[i], n * 4);
     alloc((void**)&h->pos[i], n * 4);
   }
   alloc((void**)&h->part, chunks * 2 * dim * 4);
+  alloc((void**)&h->crossing, chunks * 8);
+  alloc((void**)&h->counts, 8);
   alloc((void**)&h->d_flag, 4);
   if (e == cudaSuccess) e = cudaMemset(h->d_flag, 0, 4);
   if (e == cudaSuccess) e = cudaMallocHost((void**)&h->h_flag, 4);
@@ -574,6 +637,8 @@ extern "C" void psgd_embedding_destroy(psgd_embedding* h) {
       if (h->pos[i]) cudaFree(h->pos[i]);
     }
     if (h->part) cudaFree(h->part);
+    if (h->crossing) cudaFree(h->crossing);
+    if (h->counts) cudaFree(h->counts);
     if (h->d_flag) cudaFree(h->d_flag);
     if (h->h_flag) cudaFreeHost(h->h_flag);
   }
@@ -614,8 +679,8 @@ extern "C" int psgd_embedding_forward(psgd_embedding* h, const void* weight, psg
       const bool vec = h->dim % V == 0 && aligned_rows(weight, weight_stride, 0, sizeof(W), 16) &&
                        aligned_rows(out, out_outer_stride, out_inner_stride, sizeof(O), align);
       const TilePlan p = plan_tile(h->dim, vec ? V : 1);
-      const int tokens = (vec ? 4 : 2) * p.groups;
-      const dim3 grid((unsigned)std::min<long long>((n + tokens - 1) / tokens, (long long)h->sms * 8), p.tiles);
+      const int tokens = kLookup * p.groups;
+      const dim3 grid((unsigned)((n + (long long)tokens - 1) / tokens), p.tiles);
       const dim3 block(p.threads, p.groups);
       if (vec)
         k_lookup<W, O, V, 1><<<grid, block, 0, st>>>((const W*)weight, weight_stride, h->vocab, (int)h->dim, ids,
@@ -656,36 +721,40 @@ extern "C" int psgd_embedding_backward(psgd_embedding* h, const void* ids, int32
   const cudaStream_t st = (cudaStream_t)stream;
   const Layout2 il{ids_outer_stride, ids_inner_stride, (int)inner}, gl{grad_outer_stride, grad_inner_stride, (int)inner};
   const int dim = (int)h->dim, vocab = (int)h->vocab;
-  int passes = 1;
-  while (passes < 4 && (vocab >> (8 * passes)) != 0) ++passes;
+  // dweight is zeroed as one row where its rows have no gaps
+  const bool dense = dweight_stride == dim || vocab == 1;
+  const int osize = dtype_size(dweight_dtype);
+  const long long zrows = dense ? 1 : vocab, zbytes = dense ? wb : (long long)dim * osize;
+  const dim3 zgrid((unsigned)std::min<long long>((zbytes + 4095) / 4096, (long long)h->sms * 8),
+                   (unsigned)std::min<long long>(zrows, (long long)h->sms * 8));
   cudaError_t e = cudaSuccess;
-  // A table without gaps is zeroed beside the sort, in one launch.
-  const bool beside = !accumulate && n > 0 && (dweight_stride == dim || vocab == 1);
-  if (!accumulate && !beside) {
-    by_dtype(dweight_dtype, [&](auto* ot) {
-      using O = std::remove_pointer_t<decltype(ot)>;
-      k_zero_rows<O><<<(unsigned)std::min<long long>(vocab, h->sms * 8), 256, 0, st>>>((O*)dweight, vocab, dim,
-                                                                                     dweight_stride);
-      return 0;
-    });
+  if (n == 0) {
+    if (!accumulate) k_zero<false><<<zgrid, 256, 0, st>>>((char*)dweight, zrows, zbytes, dweight_stride * osize);
     e = cudaGetLastError();
-  }
-  if (n > 0 && e == cudaSuccess) {
+  } else {
+    const bool wide = vocab > 256 && vocab <= 1024 && n <= (1 << 18);  // one pass of 10 bits; a CTA's counts fit 16
+    int passes = 1;
+    while (!wide && passes < 4 && ((vocab - 1) >> (8 * passes)) != 0) ++passes;
     SortArgs a{ids, id_bits == 64, il, n, vocab, padding_idx, passes, {h->key[0], h->key[1]}, {h->pos[0], h->pos[1]},
-               h->d_flag, beside ? dweight : nullptr, beside ? wb : 0};
-    // a cluster of zeroing CTAs per 512 KB, up to one wave of them
-    const unsigned zero = beside ? (unsigned)std::min<long long>((wb + (1 << 19) - 1) >> 19, (h->sms - kSortCtas) / kSortCtas) : 0;
-    const unsigned grid = kSortCtas * (1 + zero);
-    if (n <= kSortCtas * kSortThreads * 2) k_sort_and_zero<2><<<grid, kSortThreads, 0, st>>>(a);
-    else k_sort_and_zero<0><<<grid, kSortThreads, 0, st>>>(a);
-    e = cudaGetLastError();
-    const unsigned chunks = (unsigned)((n + kChunk - 1) / kChunk);
+               h->d_flag, h->counts};
+    e = n <= 2 * kSortThreads               ? (wide ? launch_sort<1, 2, 10>(a, h->device, st) : launch_sort<1, 2, 8>(a, h->device, st))
+        : n <= 2 * kSortThreads * kSortCtas ? (wide ? launch_sort<kSortCtas, 2, 10>(a, h->device, st)
+                                                    : launch_sort<kSortCtas, 2, 8>(a, h->device, st))
+                                            : (wide ? launch_sort<kSortCtas, 0, 10>(a, h->device, st)
+                                                    : launch_sort<kSortCtas, 0, 8>(a, h->device, st));
+    const int chunk = chunk_for(n, h->sms);
+    const unsigned chunks = (unsigned)((n + (long long)chunk - 1) / chunk);
     const int *key = h->key[(passes - 1) & 1], *pos = h->pos[(passes - 1) & 1];
     cudaLaunchAttribute early = early_launch();
     cudaLaunchConfig_t cfg = {};
     cfg.stream = st;
     cfg.attrs = &early;
     cfg.numAttrs = 1;
+    if (!accumulate && e == cudaSuccess) {
+      cfg.gridDim = zgrid;
+      cfg.blockDim = dim3(256);
+      e = cudaLaunchKernelEx(&cfg, k_zero<true>, (char*)dweight, zrows, zbytes, (long long)dweight_stride * osize);
+    }
     by_dtype(grad_dtype, [&](auto* gt) {
       using G = std::remove_pointer_t<decltype(gt)>;
       return by_dtype(dweight_dtype, [&](auto* ot) {
@@ -697,14 +766,15 @@ extern "C" int psgd_embedding_backward(psgd_embedding* h, const void* ids, int32
         cfg.gridDim = dim3(chunks, p.tiles);
         cfg.blockDim = dim3(std::max(p.threads, 64));
         if (e == cudaSuccess)
-          e = cudaLaunchKernelEx(&cfg, vec ? k_row_sums<G, O, V, 1> : k_row_sums<G, O, 1, kScalarNv>, key, pos, n, vocab,
+          e = cudaLaunchKernelEx(&cfg, vec ? k_row_sums<G, O, V, 1> : k_row_sums<G, O, 1, kScalarNv>, key, pos,
                                  (const G*)grad, gl, dim, scale, (int)accumulate, (O*)dweight, (long long)dweight_stride,
-                                 dw_aligned, h->part);
+                                 dw_aligned, h->part, chunk, h->crossing, h->counts);
         if (chunks > 1 && e == cudaSuccess) {
-          cfg.gridDim = dim3(std::min(chunks - 1, (unsigned)h->sms), (dim + 127) / 128);
+          cfg.gridDim = dim3(std::min(chunks - 1, (unsigned)h->sms * 4), (dim + 127) / 128);
           cfg.blockDim = dim3(32, kJoinGroups);
-          e = cudaLaunchKernelEx(&cfg, k_join_rows<O>, key, n, vocab, dim, scale, (int)accumulate, (O*)dweight,
-                                 (long long)dweight_stride, (const float*)h->part);
+          e = cudaLaunchKernelEx(&cfg, k_join_rows<O>, key, dim, scale, (int)accumulate, (O*)dweight,
+                                 (long long)dweight_stride, (const float*)h->part, chunk, (const int2*)h->crossing,
+                                 (const int*)h->counts);
         }
         return 0;
       });

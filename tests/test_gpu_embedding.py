@@ -159,10 +159,11 @@ def test_grad_widths_and_bucket_offsets(dim, offset, odtype):
     run_grad(77, dim, (5, 53), BF16, odtype, dim + offset, offset=offset, hot=0.3)
 
 
-@pytest.mark.parametrize("vocab", [255, 256, 257, 65535, 65536, 70001])
-def test_grad_table_sizes(vocab):
-    """One, two and three radix passes."""
-    run_grad(vocab, 16, (9, 301), F16, F32, vocab)
+@pytest.mark.parametrize("vocab", [255, 256, 257, 1023, 1024, 1025, 65535, 65536, 65537, 70001])
+@pytest.mark.parametrize("tokens", [700, 2047, 2048, 2049, 9 * 301, 16384, 16385, 20000])
+def test_grad_table_sizes(vocab, tokens):
+    """One, two and three radix passes, of 8 bits and of 10, on one CTA and on a cluster, in registers and not."""
+    run_grad(vocab, 8, (tokens,), F16, F32, vocab, padding=vocab // 3)
 
 
 @pytest.mark.parametrize("hot", [0.5, 1.0])
@@ -179,6 +180,15 @@ def test_grad_large():
 
 def test_grad_many_tokens():
     run_grad(5000, 8, (300, 1001), F16, F32, 4, hot=0.05)
+    run_grad(1000, 4, (300, 1001), F16, F32, 5, hot=0.9)
+    run_grad(777, 8, (262, 1001), F16, F32, 6, hot=0.5, padding=5)
+    run_grad(2, 8, (1, 200001), F32, F32, 7)
+
+
+def test_grad_of_padding_only():
+    run_grad(300, 24, (3, 50), F32, F32, 1, hot=1.0, padding=150)
+    run_grad(300, 24, (3000,), F32, F32, 1, hot=1.0, padding=150)
+    run_grad(30000, 24, (3000,), F32, F32, 1, hot=1.0, padding=15000, accumulate=True)
 
 
 def test_grad_strides_and_broadcast():
