@@ -28,8 +28,8 @@ struct psgd_embedding {
   int* key[2] = {nullptr, nullptr};
   int* pos[2] = {nullptr, nullptr};
   float* part = nullptr;  // per chunk: the partial rows of its first and its last id
-  int2* crossing = nullptr;  // rows that cross a chunk's end: (chunk where they begin, id)
-  int* counts = nullptr;     // how many of those; sorted tokens
+  int4* crossing = nullptr;  // rows that cross a chunk's end: (chunk where they begin, id, chunks that follow)
+  int* counts = nullptr;     // of few partials; sorted tokens; of many partials
   int* d_flag = nullptr;  // an id outside [0, vocab) was seen
   int* h_flag = nullptr;  // pinned
   size_t bytes = 0;
@@ -40,16 +40,22 @@ namespace ops {
 namespace {
 
 constexpr int kMaxChunk = 32;       // sorted tokens per CTA of the row sums, at most
+constexpr int kFewParts = 8;        // partials of a row that one warp adds
+constexpr int kJoinWarps = 8;
 constexpr int kSortCtas = 8;        // CTAs of the sort's cluster
 constexpr int kSortThreads = 1024;
 constexpr int kSortWarps = kSortThreads / 32;
 
-// Tokens in an (outer, inner) layout: token i = o * inner + n, at
-// o * os + n * is in units of the operand's elements.
+// Tokens in an (outer, inner) layout: token i = o * inner + n at o * os + n * is,
+// in units of the operand's elements.  inner = 0: all tokens are `is` apart,
+// and no division is needed to find one.
 struct Layout2 {
   long long os, is;
   int inner;
+  Layout2(int64_t outer, int64_t inner_, int64_t os_, int64_t is_)
+      : os(os_), is(inner_ == 1 ? os_ : is_), inner(outer == 1 || inner_ == 1 || os_ == inner_ * is_ ? 0 : (int)inner_) {}
   __device__ __forceinline__ long long at(int i) const {
+    if (inner == 0) return i * is;
     const int o = i / inner;
     return o * os + (i - o * inner) * is;
   }
@@ -113,7 +119,7 @@ struct SortArgs {
   int passes;
   int *key[2], *pos[2];  // pass p writes buffer p & 1
   int* flag;
-  int* counts;           // out: [0] = 0 (crossing rows found so far), [1] = tokens with a gradient
+  int* counts;           // out: [0] = [2] = 0 (crossing rows found so far), [1] = tokens with a gradient
 };
 
 template <int BITS> struct SortShared {
@@ -285,7 +291,7 @@ template <int CTAS, int ITEMS, int BITS> __global__ void __launch_bounds__(kSort
     }
   }
   if (rank == 0 && t == 0) {
-    a.counts[0] = 0;
+    a.counts[0] = a.counts[2] = 0;
     a.counts[1] = n;
   }
 }
@@ -334,7 +340,7 @@ __device__ __forceinline__ void write_row(O* dst, const float* acc, float scale,
 template <typename G, typename O, int VEC, int NV>
 __global__ void __launch_bounds__(256, VEC == 1 ? 2 : 4) k_row_sums(const int* __restrict__ key, const int* __restrict__ pos, const G* __restrict__ grad, Layout2 gl, int dim,
                                                   float scale, int accumulate, O* __restrict__ dw, long long stride,
-                                                  int dw_aligned, float* __restrict__ part, int chunk, int2* __restrict__ crossing, int* __restrict__ counts) {
+                                                  int dw_aligned, float* __restrict__ part, int chunk, int4* __restrict__ crossing, int* __restrict__ counts) {
   constexpr int kBatch = VEC == 8 ? 4 : 8;
   __shared__ long long s_off[kMaxChunk];
   __shared__ int s_key[kMaxChunk + 2];  // with the tokens on both sides (-1: none)
@@ -350,8 +356,21 @@ __global__ void __launch_bounds__(256, VEC == 1 ? 2 : 4) k_row_sums(const int* _
   }
   if (t < m) s_off[t] = gl.at(__ldcg(pos + e0 + t));
   __syncthreads();
-  if (t == 0 && blockIdx.y == 0 && s_key[m + 1] == s_key[m] && s_key[0] != s_key[m])
-    crossing[atomicAdd(counts, 1)] = make_int2(blockIdx.x, s_key[m]);  // a row begins here and goes on in the next chunk
+  if (t < 32 && blockIdx.y == 0 && s_key[m + 1] == s_key[m] && s_key[0] != s_key[m]) {
+    // a row begins here and goes on: into how many chunks, each of which begins with its id
+    int more = 0;
+    for (;;) {
+      const long long e = ((long long)blockIdx.x + 1 + more + t) * chunk;
+      const int found = __popc(__ballot_sync(0xffffffffu, e < n && __ldcg(key + e) == s_key[m]));
+      more += found;
+      if (found < 32) break;
+    }
+    if (t == 0) {
+      const bool few = more <= kFewParts - 1;
+      const int at = atomicAdd(counts + (few ? 0 : 2), 1);
+      crossing[few ? at : (int)gridDim.x - 1 - at] = make_int4(blockIdx.x, s_key[m], more, 0);
+    }
+  }
   const int c0 = (blockIdx.y * blockDim.x * NV + t) * VEC, step = blockDim.x * VEC;
   if (c0 >= dim) return;
   float acc[NV][VEC];
@@ -405,69 +424,87 @@ __global__ void __launch_bounds__(256, VEC == 1 ? 2 : 4) k_row_sums(const int* _
   }
 }
 
-constexpr int kJoinGroups = 8;
-
-// The rows that cross a chunk's end, as listed by the chunks where they begin
-// (chunk, id): each adds its partials in chunk order, kJoinGroups interleaved
-// sums and then those in order, so the list's own order does not matter.
-// blockDim = (32 lanes of 4 columns, kJoinGroups).
+// The rows that cross a chunk's end, as listed by the chunks where they begin:
+// (chunk, id, chunks that follow), those of at most kFewParts partials from the
+// list's front, the others from its back.  A row's partials are added in chunk
+// order, by one warp per 128 columns if they are few (all loaded at once), else
+// by a CTA, whose warps take interleaved partials and whose sums are then added
+// in order: the list's own order does not matter.
 template <typename O>
-__global__ void __launch_bounds__(32 * kJoinGroups) k_join_rows(const int* __restrict__ key, int dim, float scale,
-                                                                int accumulate, O* __restrict__ dw, long long stride,
-                                                                const float* __restrict__ part, int chunk,
-                                                                const int2* __restrict__ crossing,
-                                                                const int* __restrict__ counts) {
-  __shared__ float sums[kJoinGroups][32][4];
+__global__ void __launch_bounds__(32 * kJoinWarps) k_join_rows(int dim, float scale, int accumulate,
+                                                               O* __restrict__ dw, long long stride,
+                                                               const float* __restrict__ part,
+                                                               const int4* __restrict__ crossing, int chunks,
+                                                               const int* __restrict__ counts) {
+  __shared__ float sums[kJoinWarps][32][4];
   after_previous();
-  const int x = threadIdx.x, y = threadIdx.y;
-  const int c = (blockIdx.y * 32 + x) * 4;
+  const int lane = threadIdx.x, warp = threadIdx.y;
   const bool vec = dim % 4 == 0;
-  const int count = __ldcg(counts), n = __ldcg(counts + 1);
-  for (int i = blockIdx.x; i < count; i += gridDim.x) {
-    const int2 who = __ldcg(crossing + i);
-    // the chunks after this one that begin with the row's id
-    int chunks = 0;
-    for (;;) {
-      const long long e = ((long long)who.x + 1 + chunks + y * 32 + x) * chunk;
-      const int more = __syncthreads_count(e < n && __ldcg(key + e) == who.y);
-      chunks += more;
-      if (more < 32 * kJoinGroups) break;
-    }
-    float acc[4] = {0.f, 0.f, 0.f, 0.f};
-    auto take = [&](const float* src) {
-      if (vec && c < dim) {
-        const float4 v = __ldcg(reinterpret_cast<const float4*>(src));
-        acc[0] += v.x;
-        acc[1] += v.y;
-        acc[2] += v.z;
-        acc[3] += v.w;
-      } else {
+  const int tiles = (dim + 127) / 128;
+  const int few = __ldcg(counts), many = __ldcg(counts + 2);
+  auto load = [&](const float* src, int c, float (&v)[4]) {
+    if (vec && c < dim) {
+      const float4 u = __ldcg(reinterpret_cast<const float4*>(src + c));
+      v[0] = u.x;
+      v[1] = u.y;
+      v[2] = u.z;
+      v[3] = u.w;
+    } else {
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-          if (c + k < dim) acc[k] += __ldcg(src + k);
+      for (int k = 0; k < 4; ++k) v[k] = c + k < dim ? __ldcg(src + c + k) : 0.f;
+    }
+  };
+  auto write = [&](int id, int c, const float (&acc)[4]) {
+    O* dst = dw + (long long)id * stride + c;
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (c + k < dim) {
+        float v = acc[k] * scale;
+        if (accumulate) v += to_f(dst[k]);
+        dst[k] = from_f<O>(v);
       }
-    };
-    if (y == 0) take(part + ((long long)who.x * 2 + 1) * dim + c);
+  };
+  // (items x 1 KB of partials fit a GPU's memory: 32 bits count them)
+  for (int i = blockIdx.x; i < many * tiles; i += gridDim.x) {
+    const int4 who = __ldcg(crossing + (chunks - 1 - i / tiles));
+    const int c = (i % tiles * 32 + lane) * 4;
+    const float* first = part + (long long)who.x * 2 * dim;
+    float acc[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll 8
-    for (int j = 1 + y; j <= chunks; j += kJoinGroups) take(part + ((long long)who.x + j) * 2 * dim + c);
+    for (int j = warp; j <= who.z; j += kJoinWarps) {
+      float v[4];
+      load(first + (j == 0 ? dim : (long long)j * 2 * dim), c, v);
 #pragma unroll
-    for (int k = 0; k < 4; ++k) sums[y][x][k] = acc[k];
+      for (int k = 0; k < 4; ++k) acc[k] += v[k];
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) sums[warp][lane][k] = acc[k];
     __syncthreads();
-    if (y == 0) {
+    if (warp == 0) {
 #pragma unroll
-      for (int w = 1; w < kJoinGroups; ++w)
+      for (int w = 1; w < kJoinWarps; ++w)
 #pragma unroll
-        for (int k = 0; k < 4; ++k) acc[k] += sums[w][x][k];
-      O* dst = dw + (long long)who.y * stride + c;
-#pragma unroll
-      for (int k = 0; k < 4; ++k)
-        if (c + k < dim) {
-          float v = acc[k] * scale;
-          if (accumulate) v += to_f(dst[k]);
-          dst[k] = from_f<O>(v);
-        }
+        for (int k = 0; k < 4; ++k) acc[k] += sums[w][lane][k];
+      write(who.y, c, acc);
     }
     __syncthreads();
+  }
+  for (int i = blockIdx.x * kJoinWarps + warp; i < few * tiles; i += gridDim.x * kJoinWarps) {
+    const int4 who = __ldcg(crossing + i / tiles);
+    const int c = (i % tiles * 32 + lane) * 4;
+    const float* first = part + (long long)who.x * 2 * dim;
+    float v[kFewParts][4];
+#pragma unroll
+    for (int j = 0; j < kFewParts; ++j)
+      if (j <= who.z) load(first + (j == 0 ? dim : (long long)j * 2 * dim), c, v[j]);
+    float acc[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int j = 0; j < kFewParts; ++j)
+      if (j <= who.z) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) acc[k] += v[j][k];
+      }
+    write(who.y, c, acc);
   }
 }
 
@@ -614,8 +651,8 @@ extern "C" int psgd_embedding_create(int64_t vocab, int64_t dim, int64_t max_tok
     alloc((void**)&h->pos[i], n * 4);
   }
   alloc((void**)&h->part, chunks * 2 * dim * 4);
-  alloc((void**)&h->crossing, chunks * 8);
-  alloc((void**)&h->counts, 8);
+  alloc((void**)&h->crossing, chunks * 16);
+  alloc((void**)&h->counts, 12);
   alloc((void**)&h->d_flag, 4);
   if (e == cudaSuccess) e = cudaMemset(h->d_flag, 0, 4);
   if (e == cudaSuccess) e = cudaMallocHost((void**)&h->h_flag, 4);
@@ -668,7 +705,7 @@ extern "C" int psgd_embedding_forward(psgd_embedding* h, const void* weight, psg
       overlap(out, ob, ids, ((outer - 1) * ids_outer_stride + (inner - 1) * ids_inner_stride + 1) * (id_bits / 8)))
     return fail(PSGD_EINVAL, "psgd_embedding_forward: out overlaps an input");
   DeviceScope scope(h->device);
-  const Layout2 il{ids_outer_stride, ids_inner_stride, (int)inner}, ol{out_outer_stride, out_inner_stride, (int)inner};
+  const Layout2 il(outer, inner, ids_outer_stride, ids_inner_stride), ol(outer, inner, out_outer_stride, out_inner_stride);
   const cudaStream_t st = (cudaStream_t)stream;
   by_dtype(weight_dtype, [&](auto* wt) {
     using W = std::remove_pointer_t<decltype(wt)>;
@@ -719,7 +756,7 @@ extern "C" int psgd_embedding_backward(psgd_embedding* h, const void* ids, int32
     return fail(PSGD_EINVAL, "psgd_embedding_backward: dweight overlaps an input");
   DeviceScope scope(h->device);
   const cudaStream_t st = (cudaStream_t)stream;
-  const Layout2 il{ids_outer_stride, ids_inner_stride, (int)inner}, gl{grad_outer_stride, grad_inner_stride, (int)inner};
+  const Layout2 il(outer, inner, ids_outer_stride, ids_inner_stride), gl(outer, inner, grad_outer_stride, grad_inner_stride);
   const int dim = (int)h->dim, vocab = (int)h->vocab;
   // dweight is zeroed as one row where its rows have no gaps
   const bool dense = dweight_stride == dim || vocab == 1;
@@ -770,10 +807,11 @@ extern "C" int psgd_embedding_backward(psgd_embedding* h, const void* ids, int32
                                  (const G*)grad, gl, dim, scale, (int)accumulate, (O*)dweight, (long long)dweight_stride,
                                  dw_aligned, h->part, chunk, h->crossing, h->counts);
         if (chunks > 1 && e == cudaSuccess) {
-          cfg.gridDim = dim3(std::min(chunks - 1, (unsigned)h->sms * 4), (dim + 127) / 128);
-          cfg.blockDim = dim3(32, kJoinGroups);
-          e = cudaLaunchKernelEx(&cfg, k_join_rows<O>, key, dim, scale, (int)accumulate, (O*)dweight,
-                                 (long long)dweight_stride, (const float*)h->part, chunk, (const int2*)h->crossing,
+          const long long items = (long long)(chunks - 1) * ((dim + 127) / 128);
+          cfg.gridDim = dim3((unsigned)std::min<long long>((items + kJoinWarps - 1) / kJoinWarps, h->sms * 4));
+          cfg.blockDim = dim3(32, kJoinWarps);
+          e = cudaLaunchKernelEx(&cfg, k_join_rows<O>, dim, scale, (int)accumulate, (O*)dweight,
+                                 (long long)dweight_stride, (const float*)h->part, (const int4*)h->crossing, (int)chunks,
                                  (const int*)h->counts);
         }
         return 0;
