@@ -30,6 +30,8 @@ struct psgd_embedding {
   float* part = nullptr;  // per chunk: the partial rows of its first and its last id
   int4* crossing = nullptr;  // rows that cross a chunk's end: (chunk where they begin, id, chunks that follow)
   int* counts = nullptr;     // of few partials; sorted tokens; of many partials
+  unsigned char* named = nullptr;  // per row of the table: a token names it
+  int* ready = nullptr;            // the map is complete (0 between calls)
   int* d_flag = nullptr;  // an id outside [0, vocab) was seen
   int* h_flag = nullptr;  // pinned
   size_t bytes = 0;
@@ -42,6 +44,11 @@ namespace {
 constexpr int kMaxChunk = 32;       // sorted tokens per CTA of the row sums, at most
 constexpr int kFewParts = 8;        // partials of a row that one warp adds
 constexpr int kJoinWarps = 8;
+// Zeroing CTAs of 256 threads to an SM, at most.  BERT-large's table (125 MB,
+// 16384 tokens) takes 45.8, 44.4 and 44.0 us with 1, 2 and 4 of them, with 32
+// tokens 34.8, 29.7 and 27.2: fewer leave room for the row sums' CTAs, but do
+// not reach the write rate alone.
+constexpr int kZeroCtas = 4;
 constexpr int kSortCtas = 8;        // CTAs of the sort's cluster
 constexpr int kSortThreads = 1024;
 constexpr int kSortWarps = kSortThreads / 32;
@@ -120,6 +127,10 @@ struct SortArgs {
   int *key[2], *pos[2];  // pass p writes buffer p & 1
   int* flag;
   int* counts;           // out: [0] = [2] = 0 (crossing rows found so far), [1] = tokens with a gradient
+  // NULL, or one byte a row: 1 where a token with a gradient names it.  It is
+  // complete once *ready is 1, early in the first pass.
+  unsigned char* named;
+  int* ready;
 };
 
 template <int BITS> struct SortShared {
@@ -150,11 +161,14 @@ template <int CTAS, int ITEMS, int BITS> __global__ void __launch_bounds__(kSort
   constexpr int D = Shared::kDigits, PARTS = Shared::kParts, PER = kSortWarps / PARTS;
   extern __shared__ __align__(16) unsigned char raw[];
   Shared& s = *reinterpret_cast<Shared*>(raw);
-  next_may_launch();
   cg::cluster_group cluster = cg::this_cluster();
   const int rank = CTAS > 1 ? (int)cluster.block_rank() : 0;
-  if (CTAS > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
   const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
+  if (a.named) {  // (its size is rounded up to 16 bytes)
+    uint4* v = reinterpret_cast<uint4*>(a.named);
+    for (int i = rank * kSortThreads + t; i < (a.vocab + 15) / 16; i += CTAS * kSortThreads) v[i] = make_uint4(0, 0, 0, 0);
+  }
+  if constexpr (CTAS > 1) asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
   const unsigned below = (1u << lane) - 1u;
   int n = a.n;
   for (int p = 0; p < a.passes; ++p) {
@@ -204,13 +218,25 @@ template <int CTAS, int ITEMS, int BITS> __global__ void __launch_bounds__(kSort
       uint4* z = reinterpret_cast<uint4*>(&s.cnt[0][0]);
       for (int i = t; i < (int)(sizeof(s.cnt) / 16); i += kSortThreads) z[i] = make_uint4(0, 0, 0, 0);
     }
+    if constexpr (CTAS > 1) {
+      // all have started, and the map is clear
+      if (p == 0) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+    }
     __syncthreads();
+    const bool mark = p == 0 && a.named;
     if constexpr (ITEMS > 0) {
 #pragma unroll
       for (int i = 0; i < ITEMS; ++i)
-        if (i * 32 < share) count(digit(key[i]));
+        if (i * 32 < share) {
+          if (mark && key[i] >= 0) a.named[key[i]] = 1;
+          count(digit(key[i]));
+        }
     } else {
-      for (int e = lane; e - lane < share; e += 32) count(e < share ? digit(key_at(first + e)) : D);
+      for (int e = lane; e - lane < share; e += 32) {
+        const int k = e < share ? key_at(first + e) : -1;
+        if (mark && k >= 0) a.named[k] = 1;
+        count(digit(k));
+      }
     }
     __syncthreads();
     // exclusive counts over the warps, PER of them per thread
@@ -239,11 +265,16 @@ template <int CTAS, int ITEMS, int BITS> __global__ void __launch_bounds__(kSort
       }
     }
     if constexpr (CTAS > 1) {
-      if (p == 0) asm volatile("barrier.cluster.wait.aligned;" ::: "memory");  // all have started
 #pragma unroll
       for (int k = 0; k < CTAS / PARTS; ++k)
         cluster.map_shared_rank(&s.totals[rank][0], q * (CTAS / PARTS) + k)[d] = total;
       cluster.sync();
+    }
+    if (p == 0) {
+      if (CTAS == 1) __syncthreads();
+      if (mark && rank == 0 && t == 0)
+        asm volatile("st.release.gpu.global.s32 [%0], 1;" ::"l"(a.ready) : "memory");
+      next_may_launch();
     }
     int before = 0, all = 0, inc = 0;
     if (t < D) {
@@ -296,24 +327,55 @@ template <int CTAS, int ITEMS, int BITS> __global__ void __launch_bounds__(kSort
   }
 }
 
-// Zeroes `rows` rows of `bytes` bytes, `stride` bytes apart (one row: a whole
-// table without gaps), 16 bytes at a time between the first and the last
-// boundary, the ends by bytes.  Started beside the sort (EARLY), it ends only
-// when that has.
-template <bool EARLY>
-__global__ void __launch_bounds__(256) k_zero(char* __restrict__ w, long long rows, long long bytes, long long stride) {
-  if (EARLY) next_may_launch();
-  const long long t = (long long)blockIdx.x * blockDim.x + threadIdx.x, step = (long long)gridDim.x * blockDim.x;
-  for (long long r = blockIdx.y; r < rows; r += gridDim.y) {
-    char* p = w + r * stride;
-    const long long head = min(bytes, (long long)((16 - ((uintptr_t)p & 15)) & 15));
-    const long long vecs = (bytes - head) / 16, tail = bytes - head - vecs * 16;
-    uint4* v = reinterpret_cast<uint4*>(p + head);
-    for (long long i = t; i < vecs; i += step) v[i] = make_uint4(0, 0, 0, 0);
-    if (t < head) p[t] = 0;
-    if (t < tail) p[head + vecs * 16 + t] = 0;
+// One warp zeroes `bytes` bytes, 16 at a time between the first and the last boundary.
+__device__ __forceinline__ void zero_bytes(char* p, long long bytes, int lane) {
+  const long long head = min(bytes, (long long)((16 - ((uintptr_t)p & 15)) & 15));
+  const long long vecs = (bytes - head) / 16, tail = bytes - head - vecs * 16;
+  uint4* v = reinterpret_cast<uint4*>(p + head);
+  for (long long i = lane; i < vecs; i += 32) v[i] = make_uint4(0, 0, 0, 0);
+  if (lane < head) p[lane] = 0;
+  if (lane < tail) p[head + vecs * 16 + lane] = 0;
+}
+
+// The whole table, where there is no token.
+__global__ void __launch_bounds__(256) k_zero_table(char* __restrict__ w, long long rows, long long bytes, long long stride) {
+  const int warps = blockDim.x / 32;
+  for (long long r = (long long)blockIdx.x * warps + threadIdx.x / 32; r < rows; r += (long long)gridDim.x * warps)
+    zero_bytes(w + r * stride, bytes, threadIdx.x & 31);
+}
+
+// The rows that no token names, which the CTAs before the row sums' zero while
+// the sort runs.
+struct ZeroArgs {
+  int ctas;                 // 0: rows without a token keep what they hold
+  char* table;
+  long long bytes, stride;  // of a row
+  int vocab;
+  const unsigned char* named;
+  const int* ready;
+};
+
+__device__ __forceinline__ void zero_unnamed(const ZeroArgs& z) {
+  // This kernel starts once the sort has let it, after it set *ready: seen as
+  // 1, the map is complete and visible.  If it is not seen, the sort's end is
+  // waited for, which makes everything visible.
+  int ready;
+  asm volatile("ld.acquire.gpu.global.s32 %0, [%1];" : "=r"(ready) : "l"(z.ready) : "memory");
+  if (!ready) after_previous();
+  // a contiguous share of the table, 32 flags at a time and one step ahead
+  const int lane = threadIdx.x & 31, warps = blockDim.x >> 5, warp = threadIdx.x >> 5;
+  const int first = (int)((long long)z.vocab * blockIdx.x / z.ctas), last = (int)((long long)z.vocab * (blockIdx.x + 1) / z.ctas);
+  auto unnamed = [&](long long r0) { return r0 + lane < last && __ldcg(z.named + r0 + lane) == 0; };
+  bool next = unnamed(first);
+  int turn = 0;  // a row per warp
+  for (long long r0 = first; r0 < last; r0 += 32) {
+    unsigned todo = __ballot_sync(0xffffffffu, next);
+    next = unnamed(r0 + 32);
+    for (; todo; todo &= todo - 1) {
+      if (turn == warp) zero_bytes(z.table + (r0 + __ffs(todo) - 1) * z.stride, z.bytes, lane);
+      turn = turn + 1 == warps ? 0 : turn + 1;
+    }
   }
-  if (EARLY) after_previous();
 }
 
 // A finished sum into its row of the table: as VEC elements if they are
@@ -334,20 +396,25 @@ __device__ __forceinline__ void write_row(O* dst, const float* acc, float scale,
   }
 }
 
-// The rows of one chunk of sorted tokens, for one tile of columns: thread t
+// The rows of one chunk of sorted tokens (CTAs zero.ctas + chunk), for one tile of columns: thread t
 // owns the vectors t, t + threads, ... (NV of them).  kBatch rows are loaded at
 // a time, then added in order; a sum ends with its id's last token.
 template <typename G, typename O, int VEC, int NV>
 __global__ void __launch_bounds__(256, VEC == 1 ? 2 : 4) k_row_sums(const int* __restrict__ key, const int* __restrict__ pos, const G* __restrict__ grad, Layout2 gl, int dim,
                                                   float scale, int accumulate, O* __restrict__ dw, long long stride,
-                                                  int dw_aligned, float* __restrict__ part, int chunk, int4* __restrict__ crossing, int* __restrict__ counts) {
+                                                  int dw_aligned, float* __restrict__ part, int chunk, int4* __restrict__ crossing, int* __restrict__ counts, ZeroArgs zero) {
   constexpr int kBatch = VEC == 8 ? 4 : 8;
   __shared__ long long s_off[kMaxChunk];
   __shared__ int s_key[kMaxChunk + 2];  // with the tokens on both sides (-1: none)
-  after_previous();
   next_may_launch();
+  if ((int)blockIdx.x < zero.ctas) {
+    if (blockIdx.y == 0) zero_unnamed(zero);
+    return;
+  }
+  const int block = blockIdx.x - zero.ctas;  // the chunk
+  after_previous();
   const int n = __ldcg(counts + 1);  // sorted tokens
-  const int e0 = blockIdx.x * chunk, m = min(n - e0, chunk);
+  const int e0 = block * chunk, m = min(n - e0, chunk);
   if (m <= 0) return;
   const int t = threadIdx.x;
   if (t < m + 2) {
@@ -360,7 +427,7 @@ __global__ void __launch_bounds__(256, VEC == 1 ? 2 : 4) k_row_sums(const int* _
     // a row begins here and goes on: into how many chunks, each of which begins with its id
     int more = 0;
     for (;;) {
-      const long long e = ((long long)blockIdx.x + 1 + more + t) * chunk;
+      const long long e = ((long long)block + 1 + more + t) * chunk;
       const int found = __popc(__ballot_sync(0xffffffffu, e < n && __ldcg(key + e) == s_key[m]));
       more += found;
       if (found < 32) break;
@@ -368,7 +435,7 @@ __global__ void __launch_bounds__(256, VEC == 1 ? 2 : 4) k_row_sums(const int* _
     if (t == 0) {
       const bool few = more <= kFewParts - 1;
       const int at = atomicAdd(counts + (few ? 0 : 2), 1);
-      crossing[few ? at : (int)gridDim.x - 1 - at] = make_int4(blockIdx.x, s_key[m], more, 0);
+      crossing[few ? at : (int)gridDim.x - zero.ctas - 1 - at] = make_int4(block, s_key[m], more, 0);
     }
   }
   const int c0 = (blockIdx.y * blockDim.x * NV + t) * VEC, step = blockDim.x * VEC;
@@ -404,7 +471,7 @@ __global__ void __launch_bounds__(256, VEC == 1 ? 2 : 4) k_row_sums(const int* _
         const int c = c0 + j * step;
         if (c < dim) {
           if (open || more) {
-            float* dst = part + ((long long)blockIdx.x * 2 + (open ? 0 : 1)) * dim + c;
+            float* dst = part + ((long long)block * 2 + (open ? 0 : 1)) * dim + c;
             if (VEC > 1 && dim % 4 == 0) {
 #pragma unroll
               for (int i = 0; i < VEC; i += 4) store_pack<float, 4>(dst + i, acc[j] + i);
@@ -435,9 +502,10 @@ __global__ void __launch_bounds__(32 * kJoinWarps) k_join_rows(int dim, float sc
                                                                O* __restrict__ dw, long long stride,
                                                                const float* __restrict__ part,
                                                                const int4* __restrict__ crossing, int chunks,
-                                                               const int* __restrict__ counts) {
+                                                               const int* __restrict__ counts, int* ready) {
   __shared__ float sums[kJoinWarps][32][4];
   after_previous();
+  if (blockIdx.x == 0 && threadIdx.x == 0 && threadIdx.y == 0) *ready = 0;  // for the next call
   const int lane = threadIdx.x, warp = threadIdx.y;
   const bool vec = dim % 4 == 0;
   const int tiles = (dim + 127) / 128;
@@ -653,6 +721,9 @@ extern "C" int psgd_embedding_create(int64_t vocab, int64_t dim, int64_t max_tok
   alloc((void**)&h->part, chunks * 2 * dim * 4);
   alloc((void**)&h->crossing, chunks * 16);
   alloc((void**)&h->counts, 12);
+  alloc((void**)&h->named, (vocab + 15) / 16 * 16);
+  alloc((void**)&h->ready, 4);
+  if (e == cudaSuccess) e = cudaMemset(h->ready, 0, 4);
   alloc((void**)&h->d_flag, 4);
   if (e == cudaSuccess) e = cudaMemset(h->d_flag, 0, 4);
   if (e == cudaSuccess) e = cudaMallocHost((void**)&h->h_flag, 4);
@@ -676,6 +747,8 @@ extern "C" void psgd_embedding_destroy(psgd_embedding* h) {
     if (h->part) cudaFree(h->part);
     if (h->crossing) cudaFree(h->crossing);
     if (h->counts) cudaFree(h->counts);
+    if (h->named) cudaFree(h->named);
+    if (h->ready) cudaFree(h->ready);
     if (h->d_flag) cudaFree(h->d_flag);
     if (h->h_flag) cudaFreeHost(h->h_flag);
   }
@@ -758,22 +831,19 @@ extern "C" int psgd_embedding_backward(psgd_embedding* h, const void* ids, int32
   const cudaStream_t st = (cudaStream_t)stream;
   const Layout2 il(outer, inner, ids_outer_stride, ids_inner_stride), gl(outer, inner, grad_outer_stride, grad_inner_stride);
   const int dim = (int)h->dim, vocab = (int)h->vocab;
-  // dweight is zeroed as one row where its rows have no gaps
-  const bool dense = dweight_stride == dim || vocab == 1;
   const int osize = dtype_size(dweight_dtype);
-  const long long zrows = dense ? 1 : vocab, zbytes = dense ? wb : (long long)dim * osize;
-  const dim3 zgrid((unsigned)std::min<long long>((zbytes + 4095) / 4096, (long long)h->sms * 8),
-                   (unsigned)std::min<long long>(zrows, (long long)h->sms * 8));
   cudaError_t e = cudaSuccess;
   if (n == 0) {
-    if (!accumulate) k_zero<false><<<zgrid, 256, 0, st>>>((char*)dweight, zrows, zbytes, dweight_stride * osize);
+    if (!accumulate)
+      k_zero_table<<<(unsigned)std::min<long long>((vocab + 7) / 8, h->sms * 8), 256, 0, st>>>(
+          (char*)dweight, vocab, (long long)dim * osize, dweight_stride * osize);
     e = cudaGetLastError();
   } else {
     const bool wide = vocab > 256 && vocab <= 1024 && n <= (1 << 18);  // one pass of 10 bits; a CTA's counts fit 16
     int passes = 1;
     while (!wide && passes < 4 && ((vocab - 1) >> (8 * passes)) != 0) ++passes;
     SortArgs a{ids, id_bits == 64, il, n, vocab, padding_idx, passes, {h->key[0], h->key[1]}, {h->pos[0], h->pos[1]},
-               h->d_flag, h->counts};
+               h->d_flag, h->counts, accumulate ? nullptr : h->named, h->ready};
     e = n <= 2 * kSortThreads               ? (wide ? launch_sort<1, 2, 10>(a, h->device, st) : launch_sort<1, 2, 8>(a, h->device, st))
         : n <= 2 * kSortThreads * kSortCtas ? (wide ? launch_sort<kSortCtas, 2, 10>(a, h->device, st)
                                                     : launch_sort<kSortCtas, 2, 8>(a, h->device, st))
@@ -787,11 +857,6 @@ extern "C" int psgd_embedding_backward(psgd_embedding* h, const void* ids, int32
     cfg.stream = st;
     cfg.attrs = &early;
     cfg.numAttrs = 1;
-    if (!accumulate && e == cudaSuccess) {
-      cfg.gridDim = zgrid;
-      cfg.blockDim = dim3(256);
-      e = cudaLaunchKernelEx(&cfg, k_zero<true>, (char*)dweight, zrows, zbytes, (long long)dweight_stride * osize);
-    }
     by_dtype(grad_dtype, [&](auto* gt) {
       using G = std::remove_pointer_t<decltype(gt)>;
       return by_dtype(dweight_dtype, [&](auto* ot) {
@@ -800,23 +865,30 @@ extern "C" int psgd_embedding_backward(psgd_embedding* h, const void* ids, int32
         const bool vec = dim % V == 0 && aligned_rows(grad, grad_outer_stride, grad_inner_stride, sizeof(G), 16);
         const int dw_aligned = aligned_rows(dweight, dweight_stride, 0, sizeof(O), run_alignment(V, sizeof(O)));
         const TilePlan p = plan_tile(dim, vec ? V : 1);
-        cfg.gridDim = dim3(chunks, p.tiles);
-        cfg.blockDim = dim3(std::max(p.threads, 64));
+        const int threads = std::max(p.threads, 64);
+        // zeroing: about 64 KB a CTA, up to kZeroCtas CTAs of 256 threads to an SM
+        ZeroArgs zero{0, (char*)dweight, (long long)dim * osize, dweight_stride * osize, vocab, h->named, h->ready};
+        if (!accumulate)
+          zero.ctas = (int)std::max<long long>(
+              1, std::min<long long>(vocab * zero.bytes / 65536, (long long)h->sms * kZeroCtas * (256 / threads)));
+        cfg.gridDim = dim3(zero.ctas + chunks, p.tiles);
+        cfg.blockDim = dim3(threads);
         if (e == cudaSuccess)
           e = cudaLaunchKernelEx(&cfg, vec ? k_row_sums<G, O, V, 1> : k_row_sums<G, O, 1, kScalarNv>, key, pos,
                                  (const G*)grad, gl, dim, scale, (int)accumulate, (O*)dweight, (long long)dweight_stride,
-                                 dw_aligned, h->part, chunk, h->crossing, h->counts);
-        if (chunks > 1 && e == cudaSuccess) {
-          const long long items = (long long)(chunks - 1) * ((dim + 127) / 128);
+                                 dw_aligned, h->part, chunk, h->crossing, h->counts, zero);
+        if ((chunks > 1 || !accumulate) && e == cudaSuccess) {
+          const long long items = std::max<long long>(1, chunks - 1) * ((dim + 127) / 128);
           cfg.gridDim = dim3((unsigned)std::min<long long>((items + kJoinWarps - 1) / kJoinWarps, h->sms * 4));
           cfg.blockDim = dim3(32, kJoinWarps);
           e = cudaLaunchKernelEx(&cfg, k_join_rows<O>, dim, scale, (int)accumulate, (O*)dweight,
                                  (long long)dweight_stride, (const float*)h->part, (const int4*)h->crossing, (int)chunks,
-                                 (const int*)h->counts);
+                                 (const int*)h->counts, h->ready);
         }
         return 0;
       });
     });
+    if (e != cudaSuccess) cudaMemsetAsync(h->ready, 0, 4, st);  // the kernel that does so may not have been launched
   }
   return e == cudaSuccess ? PSGD_OK : cuda_fail(who, e);
 }

@@ -185,6 +185,14 @@ def test_grad_many_tokens():
     run_grad(2, 8, (1, 200001), F32, F32, 7)
 
 
+@pytest.mark.parametrize("tokens", [3000, 65536, 65537, 150000])
+def test_grad_of_tall_tables(tokens):
+    """Tables of far more rows than tokens, and rows of one element: every row that no token names is zero."""
+    run_grad(200003, 1, (tokens,), F32, F32, 1, offset=1)
+    run_grad(70001, 3, (tokens,), BF16, F16, 2, offset=3, hot=0.4, padding=0)
+    run_grad(30522, 40, (tokens,), F32, F32, 3, iddtype=torch.int32)
+
+
 def test_grad_of_padding_only():
     run_grad(300, 24, (3, 50), F32, F32, 1, hot=1.0, padding=150)
     run_grad(300, 24, (3000,), F32, F32, 1, hot=1.0, padding=150)
