@@ -127,75 +127,22 @@ __device__ __forceinline__ float mass_at(const float* p, const int* at, int n, i
   return sum;
 }
 
-// Two fp32 lanes of one register pair: one instruction for both.
-struct F2 {
-  unsigned long long v;
-};
-__device__ __forceinline__ F2 f2(float x, float y) {
-  F2 r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(x), "f"(y));
-  return r;
+// The largest element of a 16-byte granule.
+template <typename Z> __device__ __forceinline__ float top_of(const uint4& u);
+template <> __device__ __forceinline__ float top_of<float>(const uint4& u) {
+  return fmaxf(fmaxf(__uint_as_float(u.x), __uint_as_float(u.y)), fmaxf(__uint_as_float(u.z), __uint_as_float(u.w)));
 }
-__device__ __forceinline__ void split(F2 a, float& x, float& y) { asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(a.v)); }
-__device__ __forceinline__ F2 add(F2 a, F2 b) {
-  F2 r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
-  return r;
+template <> __device__ __forceinline__ float top_of<__half>(const uint4& u) {
+  const __half2* h = reinterpret_cast<const __half2*>(&u);
+  const __half2 m = __hmax2(__hmax2(h[0], h[1]), __hmax2(h[2], h[3]));
+  return fmaxf(__low2float(m), __high2float(m));
 }
-__device__ __forceinline__ F2 fma(F2 a, F2 b, F2 c) {
-  F2 r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
-  return r;
-}
-__device__ __forceinline__ F2 mul(F2 a, F2 b) {
-  F2 r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
-  return r;
+template <> __device__ __forceinline__ float top_of<__nv_bfloat16>(const uint4& u) {
+  const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(&u);
+  const __nv_bfloat162 m = __hmax2(__hmax2(h[0], h[1]), __hmax2(h[2], h[3]));
+  return fmaxf(__low2float(m), __high2float(m));
 }
 
-// A 16-byte granule of a row as pairs of floats, and its largest element.
-template <typename Z> struct Granule;
-template <> struct Granule<float> {
-  static __device__ __forceinline__ void pairs(const uint4& u, F2* f) {
-    f[0] = f2(__uint_as_float(u.x), __uint_as_float(u.y));
-    f[1] = f2(__uint_as_float(u.z), __uint_as_float(u.w));
-  }
-  static __device__ __forceinline__ float top(const uint4& u) {
-    return fmaxf(fmaxf(__uint_as_float(u.x), __uint_as_float(u.y)), fmaxf(__uint_as_float(u.z), __uint_as_float(u.w)));
-  }
-};
-template <> struct Granule<__half> {
-  static __device__ __forceinline__ void pairs(const uint4& u, F2* f) {
-    const __half2* h = reinterpret_cast<const __half2*>(&u);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float2 x = __half22float2(h[i]);
-      f[i] = f2(x.x, x.y);
-    }
-  }
-  static __device__ __forceinline__ float top(const uint4& u) {
-    const __half2* h = reinterpret_cast<const __half2*>(&u);
-    const __half2 m = __hmax2(__hmax2(h[0], h[1]), __hmax2(h[2], h[3]));
-    return fmaxf(__low2float(m), __high2float(m));
-  }
-};
-template <> struct Granule<__nv_bfloat16> {
-  static __device__ __forceinline__ void pairs(const uint4& u, F2* f) {
-    const unsigned w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) f[i] = f2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
-  }
-  static __device__ __forceinline__ float top(const uint4& u) {
-    const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(&u);
-    const __nv_bfloat162 m = __hmax2(__hmax2(h[0], h[1]), __hmax2(h[2], h[3]));
-    return fmaxf(__low2float(m), __high2float(m));
-  }
-};
-
-__device__ __forceinline__ void copy16(uint4* dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((unsigned)__cvta_generic_to_shared(dst)), "l"(src)
-               : "memory");
-}
 // Waits for the first q + 1 of LAST + 1 groups of copies (q known when unrolled).
 template <int LAST> __device__ __forceinline__ void wait_copies(int q) {
   if (q == LAST) asm volatile("cp.async.wait_group 0;" ::: "memory");
@@ -383,9 +330,9 @@ __global__ void __launch_bounds__(kDistillThreads + 32, 2) k_distill_chip(Distil
     const F2 cc = f2(c, c);
     auto take = [&](const uint4* v, auto count) {
       constexpr int N = decltype(count)::value;
-      float top = Granule<Z>::top(v[0]);
+      float top = top_of<Z>(v[0]);
 #pragma unroll
-      for (int i = 1; i < N; ++i) top = fmaxf(top, Granule<Z>::top(v[i]));
+      for (int i = 1; i < N; ++i) top = fmaxf(top, top_of<Z>(v[i]));
       if (top * c > r) {
         const float down = exp2_fast(r - top * c);
         sums[0] = mul(sums[0], f2(down, down));
@@ -396,7 +343,7 @@ __global__ void __launch_bounds__(kDistillThreads + 32, 2) k_distill_chip(Distil
 #pragma unroll
       for (int i = 0; i < N; ++i) {
         F2 f[NP];
-        Granule<Z>::pairs(v[i], f);
+        to_pairs<Z>(v[i], f);
 #pragma unroll
         for (int h = 0; h < NP; ++h) {
           float x, y;
@@ -451,7 +398,7 @@ __global__ void __launch_bounds__(kDistillThreads + 32, 2) k_distill_chip(Distil
   float shift = 0.f, base = top;
   if (!(fabsf(top) < kFar)) {  // the same for every CTA of the cluster
     float m = -INFINITY;
-    for (int g = tid; g < n; g += blockDim.x) m = fmaxf(m, Granule<Z>::top(slice[g]));
+    for (int g = tid; g < n; g += blockDim.x) m = fmaxf(m, top_of<Z>(slice[g]));
     m = cta_max(m, bufm, warps + 1);
     m = cluster_join(m, peers, ctas, rank, [](float v) { return warp_max(v); }, -INFINITY);
     shift = m == -INFINITY ? 0.f : m;
@@ -459,7 +406,7 @@ __global__ void __launch_bounds__(kDistillThreads + 32, 2) k_distill_chip(Distil
     s = 0.f;
     for (int g = tid; g < n; g += blockDim.x) {
       F2 x[NP];
-      Granule<Z>::pairs(slice[g], x);
+      to_pairs<Z>(slice[g], x);
 #pragma unroll
       for (int h = 0; h < NP; ++h) {
         float u, v;
@@ -503,7 +450,7 @@ __global__ void __launch_bounds__(kDistillThreads + 32, 2) k_distill_chip(Distil
       for (int g = tid; g < n; g += threads) {
         F2 x[NP];
         float q[NE];
-        Granule<Z>::pairs(slice[g], x);
+        to_pairs<Z>(slice[g], x);
 #pragma unroll
         for (int h = 0; h < NP; ++h) {
           float u, v;

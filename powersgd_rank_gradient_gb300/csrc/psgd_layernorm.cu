@@ -11,7 +11,9 @@
 // dw and db sums in fp32 registers; a CTA leaves one partial row and a second
 // kernel adds the partial rows in a fixed order.
 #include <algorithm>
+#include <atomic>
 #include <new>
+#include <type_traits>
 
 #include "psgd_ops.cuh"
 
@@ -46,30 +48,334 @@ struct RowsArgs {
   float eps;
 };
 
+// N values (a power of two up to 8) summed over a warp with N - 1 + log2(32 / N)
+// shuffles: while there is more than one value, half of the lanes keep one half
+// of them and send the other.  Returns the sum of value fold_index(lane).
+template <int N> __device__ __forceinline__ float fold_sum(float (&v)[N], int lane) {
+  int off = 16;
+#pragma unroll
+  for (int n = N / 2; n >= 1; n /= 2, off /= 2) {
+    const bool upper = lane & off;
+#pragma unroll
+    for (int i = 0; i < n; ++i) {
+      const float send = upper ? v[i] : v[i + n], keep = upper ? v[i + n] : v[i];
+      v[i] = keep + __shfl_xor_sync(0xffffffffu, send, off);
+    }
+  }
+#pragma unroll
+  for (; off > 0; off /= 2) v[0] += __shfl_xor_sync(0xffffffffu, v[0], off);
+  return v[0];
+}
+template <int N> __device__ __forceinline__ int fold_index(int lane) {
+  return N == 8 ? (lane >> 2) : N == 4 ? (lane >> 3) : N == 2 ? (lane >> 4) : 0;
+}
+
 // Sums of N values over the `warps` warps of one thread group, returned to all
 // of its threads.  `buf` holds warps * N floats of this group; the caller
 // alternates between two of them, so one barrier per call suffices.
 template <int N>
 __device__ __forceinline__ void group_sum(float (&v)[N], float* buf, int warps, int warp, int lane, int group,
                                           int threads) {
+  float x = fold_sum<N>(v, lane);
+  if (warps == 1) {
 #pragma unroll
-  for (int i = 0; i < N; ++i) v[i] = warp_sum(v[i]);
-  if (warps == 1) return;
-  if (lane == 0) {
-#pragma unroll
-    for (int i = 0; i < N; ++i) buf[warp * N + i] = v[i];
+    for (int i = 0; i < N; ++i) v[i] = __shfl_sync(0xffffffffu, x, i * (32 / N));
+    return;
   }
+  if ((lane & (32 / N - 1)) == 0) buf[warp * N + fold_index<N>(lane)] = x;
   asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "r"(threads) : "memory");
+  x = 0.f;
+  for (int w = lane / N; w < warps; w += 32 / N) x += buf[w * N + lane % N];
 #pragma unroll
-  for (int i = 0; i < N; ++i) v[i] = 0.f;
-  for (int w = 0; w < warps; ++w) {
+  for (int off = N; off < 32; off *= 2) x += __shfl_xor_sync(0xffffffffu, x, off);
 #pragma unroll
-    for (int i = 0; i < N; ++i) v[i] += buf[w * N + i];
+  for (int i = 0; i < N; ++i) v[i] = __shfl_sync(0xffffffffu, x, i);
+}
+
+// N elements of a parameter from column c on, `none` where there is no
+// parameter or no column.  One branch on the type, so that all loads are under
+// way together.
+template <int N> __device__ __forceinline__ void load_param(const void* w, int dtype, long long c, bool in, float none, float (&f)[N]) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) f[i] = in ? none : 0.f;
+  if (!w || !in) return;
+  if (dtype == PSGD_F32) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) f[i] = __ldg((const float*)w + c + i);
+  } else if (dtype == PSGD_F16) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) f[i] = __half2float(__ldg((const __half*)w + c + i));
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i) f[i] = __bfloat162float(__ldg((const __nv_bfloat16*)w + c + i));
+  }
+}
+template <int NE> __device__ __forceinline__ void load_param(const void* w, int dtype, long long c, bool in, float none, F2 (&f)[NE]) {
+  float v[2 * NE];
+  load_param<2 * NE>(w, dtype, c, in, none, v);
+#pragma unroll
+  for (int h = 0; h < NE; ++h) f[h] = f2(v[2 * h], v[2 * h + 1]);
+}
+
+// The kernels for rows of whole 16-byte units.  blockDim = (threads of a group,
+// groups); a group takes R rows at a time, thread t the vectors t, t + threads,
+// ... (NV of them) of each.  The rows are copied kStages - 1 steps ahead into
+// shared memory, by the thread that will use them, so no barrier is needed for
+// them and no register holds what is under way.
+constexpr int kStages = 3;
+
+template <typename T, int NV, int R>
+__global__ void __launch_bounds__(kMaxThreads, NV == 1 ? 2 : 1) k_norm_forward_vec(RowsArgs a) {
+  constexpr int NE = Vec16<T>::N, NP = NE / 2;
+  constexpr int kStep = R * NV;  // vectors of a stage per thread, kMaxThreads apart
+  extern __shared__ __align__(16) uint4 staged[];
+  __shared__ float red[2][kMaxThreads / 32 * R];
+  const int t = threadIdx.x, group = threadIdx.y, threads = blockDim.x;
+  const int warps = threads / 32, warp = t >> 5, lane = t & 31;
+  float* buf[2] = {red[0] + group * warps * R, red[1] + group * warps * R};
+  const int nvec = a.dim / NE;
+  const float inv = 1.f / (float)a.dim;
+  const long long batches = (a.rows + R - 1) / R, step = (long long)gridDim.x * blockDim.y;
+  uint4* mine = staged + group * threads + t;
+  bool in[NV];
+#pragma unroll
+  for (int j = 0; j < NV; ++j) in[j] = t + j * threads < nvec;
+  long long b = (long long)blockIdx.x * blockDim.y + group;
+  // the next batch to copy, and this thread's first vector of its rows
+  long long ahead = b;
+  const T* from = (const T*)a.x + b * R * a.xs + t * NE;
+  auto issue = [&](int stage) {
+    const long long left = a.rows - ahead * R;
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+      for (int j = 0; j < NV; ++j)
+        if (r < left && in[j])
+          copy16(mine + ((stage * R + r) * NV + j) * kMaxThreads, from + r * a.xs + j * threads * NE);
+    commit_copies();
+    ahead += step;
+    from += step * R * a.xs;
+  };
+#pragma unroll
+  for (int k = 0; k < kStages - 1; ++k) issue(k);
+  F2 w[NV][NP], bias[NV][NP];
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    const int v = t + j * threads;
+    load_param<NP>(a.w, a.pdtype, (long long)v * NE, in[j], 1.f, w[j]);
+    load_param<NP>(a.b, a.pdtype, (long long)v * NE, in[j], 0.f, bias[j]);
+  }
+  T* to = (T*)a.y + b * R * a.ys + t * NE;
+  int stage = 0;
+  for (; b < batches; b += step, to += step * R * a.ys) {
+    asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
+    issue(stage == 0 ? kStages - 1 : stage - 1);
+    const int rows = (int)min((long long)R, a.rows - b * R);
+    F2 x[R][NV][NP];
+    float s[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      F2 sum = f2(0.f, 0.f);
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        to_pairs<T>(in[j] ? mine[((stage * R + r) * NV + j) * kMaxThreads] : make_uint4(0, 0, 0, 0), x[r][j]);
+#pragma unroll
+        for (int h = 0; h < NP; ++h) sum = add(sum, x[r][j][h]);
+      }
+      float u, v;
+      split(sum, u, v);
+      s[r] = u + v;
+    }
+    stage = stage + 1 == kStages ? 0 : stage + 1;
+    group_sum<R>(s, buf[0], warps, warp, lane, group, threads);
+    float mean[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      mean[r] = s[r] * inv;
+      const F2 nm = f2(-mean[r], -mean[r]);
+      F2 sum = f2(0.f, 0.f);
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+#pragma unroll
+        for (int h = 0; h < NP; ++h) {
+          x[r][j][h] = add(x[r][j][h], nm);
+          if (in[j]) sum = fma(x[r][j][h], x[r][j][h], sum);
+        }
+      }
+      float u, v;
+      split(sum, u, v);
+      s[r] = u + v;
+    }
+    group_sum<R>(s, buf[1], warps, warp, lane, group, threads);
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      if (r >= rows) break;
+      const float rstd = rsqrtf(fmaf(s[r], inv, a.eps));
+      if (t == 0) {
+        if (a.mean) a.mean[b * R + r] = mean[r];
+        if (a.rstd) a.rstd[b * R + r] = rstd;
+      }
+      const F2 rs = f2(rstd, rstd);
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        float f[NE];
+#pragma unroll
+        for (int h = 0; h < NP; ++h) split(fma(mul(x[r][j][h], rs), w[j][h], bias[j][h]), f[2 * h], f[2 * h + 1]);
+        if (in[j]) store_pack<T, NE>(to + r * a.ys + j * threads * NE, f);
+      }
+    }
   }
 }
 
-// blockDim = (threads of a group, groups).  A group takes R rows at a time;
-// thread t owns the vectors t, t + threads, ... (NV of them) of each row.
+// dx = rstd a - rstd m0 - (x - mu) rstd^2 m1, with m0 = mean(a) and m1 = rstd mean(a (x - mu)):
+// the mean comes off x first, so rows far from zero lose nothing.
+template <typename T, int NV, int R>
+__global__ void __launch_bounds__(kMaxThreads, 1) k_norm_backward_vec(RowsArgs a) {
+  constexpr int NE = Vec16<T>::N, NP = NE / 2;
+  extern __shared__ __align__(16) uint4 staged[];
+  __shared__ float red[2][kMaxThreads / 32 * 2 * R];
+  __shared__ float stats[kStages][kMaxThreads / 32][2 * R];  // each warp's own copy of the rows' mean and rstd
+  const int t = threadIdx.x, group = threadIdx.y, threads = blockDim.x;
+  const int warps = threads / 32, warp = t >> 5, lane = t & 31, cta_warp = group * warps + warp;
+  const int nvec = a.dim / NE;
+  const float inv = 1.f / (float)a.dim;
+  const long long batches = (a.rows + R - 1) / R, step = (long long)gridDim.x * blockDim.y;
+  uint4* mine = staged + group * threads + t;
+  bool in[NV];
+#pragma unroll
+  for (int j = 0; j < NV; ++j) in[j] = t + j * threads < nvec;
+  long long b = (long long)blockIdx.x * blockDim.y + group;
+  // the next batch to copy, and this thread's first vectors of its rows
+  long long ahead = b;
+  const T* from_x = (const T*)a.x + b * R * a.xs + t * NE;
+  const T* from_g = (const T*)a.g + b * R * a.gs + t * NE;
+  const float* from_s = (lane & 1 ? a.rstd : a.mean) + b * R + lane / 2;
+  auto issue = [&](int stage) {
+    const long long left = a.rows - ahead * R;
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+      for (int j = 0; j < NV; ++j)
+        if (r < left && in[j]) {
+          uint4* dst = mine + ((stage * R + r) * NV + j) * 2 * kMaxThreads;
+          copy16(dst, from_x + r * a.xs + j * threads * NE);
+          copy16(dst + kMaxThreads, from_g + r * a.gs + j * threads * NE);
+        }
+    if (lane < 2 * R && lane / 2 < left) copy4(&stats[stage][cta_warp][lane], from_s);
+    commit_copies();
+    ahead += step;
+    from_x += step * R * a.xs;
+    from_g += step * R * a.gs;
+    from_s += step * R;
+  };
+#pragma unroll
+  for (int k = 0; k < kStages - 1; ++k) issue(k);
+  F2 dw[NV][NP], db[NV][NP], w[NV][NP];
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    const int v = t + j * threads;
+    load_param<NP>(a.w, a.pdtype, (long long)v * NE, in[j], 1.f, w[j]);
+#pragma unroll
+    for (int h = 0; h < NP; ++h) dw[j][h] = db[j][h] = f2(0.f, 0.f);
+  }
+  T* to = (T*)a.y + b * R * a.ys + t * NE;
+  int stage = 0, flip = 0;
+  for (; b < batches; b += step, to += step * R * a.ys) {
+    asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
+    __syncwarp();  // the other lanes' copies of the statistics
+    issue(stage == 0 ? kStages - 1 : stage - 1);
+    const uint4* data = mine + stage * R * NV * 2 * kMaxThreads;
+    const float* stat = stats[stage][cta_warp];
+    auto rows_of = [&](auto full) {
+      const int rows = decltype(full)::value ? R : (int)(a.rows - b * R);
+      float s[2 * R];
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        F2 s0 = f2(0.f, 0.f), s1 = f2(0.f, 0.f);
+        if (r < rows) {
+          const F2 nm = f2(-stat[2 * r], -stat[2 * r]), rs = f2(stat[2 * r + 1], stat[2 * r + 1]);
+#pragma unroll
+          for (int j = 0; j < NV; ++j) {
+            if (!in[j]) continue;
+            F2 x[NP], g[NP];
+            to_pairs<T>(data[(r * NV + j) * 2 * kMaxThreads], x);
+            to_pairs<T>(data[((r * NV + j) * 2 + 1) * kMaxThreads], g);
+#pragma unroll
+            for (int h = 0; h < NP; ++h) {
+              const F2 gd = mul(g[h], add(x[h], nm));
+              s0 = fma(g[h], w[j][h], s0);
+              s1 = fma(gd, w[j][h], s1);
+              dw[j][h] = fma(gd, rs, dw[j][h]);
+              db[j][h] = add(db[j][h], g[h]);
+            }
+          }
+        }
+        float u, v;
+        split(s0, u, v);
+        s[2 * r] = u + v;
+        split(s1, u, v);
+        s[2 * r + 1] = u + v;
+      }
+      if (!a.y) return;
+      group_sum<2 * R>(s, red[flip] + group * warps * 2 * R, warps, warp, lane, group, threads);
+      flip ^= 1;
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        if (r >= rows) break;
+        const float mean = stat[2 * r], rstd = stat[2 * r + 1];
+        const float c0 = -s[2 * r] * inv * rstd, c1 = -s[2 * r + 1] * inv * rstd * rstd * rstd;
+        const F2 nm = f2(-mean, -mean), rs = f2(rstd, rstd), k0 = f2(c0, c0), k1 = f2(c1, c1);
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+          if (!in[j]) continue;
+          F2 x[NP], g[NP];
+          to_pairs<T>(data[(r * NV + j) * 2 * kMaxThreads], x);
+          to_pairs<T>(data[((r * NV + j) * 2 + 1) * kMaxThreads], g);
+          float f[NE];
+#pragma unroll
+          for (int h = 0; h < NP; ++h)
+            split(fma(mul(g[h], w[j][h]), rs, fma(add(x[h], nm), k1, k0)), f[2 * h], f[2 * h + 1]);
+          store_pack<T, NE>(to + r * a.ys + j * threads * NE, f);
+        }
+      }
+    };
+    if ((b + 1) * R <= a.rows) rows_of(std::true_type());
+    else rows_of(std::false_type());
+    stage = stage + 1 == kStages ? 0 : stage + 1;
+  }
+  next_may_launch();
+  if (!a.part) return;
+  float* out = a.part + (long long)blockIdx.x * 2 * a.dim;
+  // the groups' sums in group order, through the staging memory
+  float* cols = reinterpret_cast<float*>(staged);
+  asm volatile("cp.async.wait_group 0;" ::: "memory");
+  for (int y = 0; y < (int)blockDim.y; ++y) {
+    __syncthreads();
+    if (group != y) continue;
+    float* dst = y + 1 < (int)blockDim.y ? cols : out;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int v = t + j * threads;
+      if (v >= nvec) continue;
+#pragma unroll
+      for (int h = 0; h < NP; ++h) {
+        float u0, u1, v0, v1;
+        split(dw[j][h], u0, u1);
+        split(db[j][h], v0, v1);
+        const int c = v * NE + 2 * h;
+        if (y > 0) {
+          u0 += cols[c];
+          u1 += cols[c + 1];
+          v0 += cols[a.dim + c];
+          v1 += cols[a.dim + c + 1];
+        }
+        *reinterpret_cast<float2*>(dst + c) = make_float2(u0, u1);
+        *reinterpret_cast<float2*>(dst + a.dim + c) = make_float2(v0, v1);
+      }
+    }
+  }
+}
+
 template <typename T, int VEC, int NV, int R>
 __global__ void __launch_bounds__(kMaxThreads) k_norm_forward(RowsArgs a) {
   __shared__ float red[2][kMaxThreads / 32 * R];
@@ -79,6 +385,13 @@ __global__ void __launch_bounds__(kMaxThreads) k_norm_forward(RowsArgs a) {
   const int nvec = a.dim / VEC;
   const float inv = 1.f / (float)a.dim;
   const long long step = (long long)gridDim.x * blockDim.y * R;
+  float w[NV][VEC], b[NV][VEC];
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    const int v = t + j * threads;
+    load_param<VEC>(a.w, a.pdtype, (long long)v * VEC, v < nvec, 1.f, w[j]);
+    load_param<VEC>(a.b, a.pdtype, (long long)v * VEC, v < nvec, 0.f, b[j]);
+  }
   for (long long row0 = ((long long)blockIdx.x * blockDim.y + group) * R; row0 < a.rows; row0 += step) {
     Pack<T, VEC> x[R][NV];
 #pragma unroll
@@ -133,18 +446,12 @@ __global__ void __launch_bounds__(kMaxThreads) k_norm_forward(RowsArgs a) {
     for (int j = 0; j < NV; ++j) {
       const int v = t + j * threads;
       if (v >= nvec) continue;
-      float w[VEC], b[VEC];
-#pragma unroll
-      for (int k = 0; k < VEC; ++k) {
-        w[k] = a.w ? load_any(a.w, a.pdtype, (long long)v * VEC + k) : 1.f;
-        b[k] = a.b ? load_any(a.b, a.pdtype, (long long)v * VEC + k) : 0.f;
-      }
 #pragma unroll
       for (int r = 0; r < R; ++r) {
         if (row0 + r >= a.rows) continue;
         float f[VEC];
 #pragma unroll
-        for (int k = 0; k < VEC; ++k) f[k] = fmaf((to_f(x[r][j].v[k]) - mean[r]) * rstd[r], w[k], b[k]);
+        for (int k = 0; k < VEC; ++k) f[k] = fmaf((to_f(x[r][j].v[k]) - mean[r]) * rstd[r], w[j][k], b[j][k]);
         store_pack<T, VEC>((T*)a.y + (row0 + r) * a.ys + (long long)v * VEC, f);
       }
     }
@@ -163,11 +470,9 @@ __global__ void __launch_bounds__(kMaxThreads) k_norm_backward(RowsArgs a) {
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
     const int v = t + j * threads;
+    load_param<VEC>(a.w, a.pdtype, (long long)v * VEC, v < nvec, 1.f, w[j]);
 #pragma unroll
-    for (int k = 0; k < VEC; ++k) {
-      dw[j][k] = db[j][k] = 0.f;
-      w[j][k] = v < nvec ? (a.w ? load_any(a.w, a.pdtype, (long long)v * VEC + k) : 1.f) : 0.f;
-    }
+    for (int k = 0; k < VEC; ++k) dw[j][k] = db[j][k] = 0.f;
   }
   const long long step = (long long)gridDim.x * blockDim.y * R;
   int flip = 0;
@@ -345,20 +650,33 @@ template <typename T> __global__ void __launch_bounds__(256) k_norm_columns_long
 
 // dw and db: the partial rows' sums, 32 columns a CTA, its warps over
 // interleaved partial rows, then the warps' sums in order.
-__global__ void __launch_bounds__(512) k_norm_columns(const float* __restrict__ part, int parts, int dim, void* dw,
-                                                      void* db, int dtype, int accumulate) {
-  __shared__ float sums[16][33];
+constexpr int kColumnWarps = 16;
+__global__ void __launch_bounds__(32 * kColumnWarps) k_norm_columns(const float* __restrict__ part, int parts, int dim,
+                                                                    void* dw, void* db, int dtype, int accumulate) {
+  __shared__ float sums[kColumnWarps][33];
   const int x = threadIdx.x & 31, y = threadIdx.x >> 5;
   const long long c = (long long)blockIdx.x * 32 + x;
+  after_previous();
   float s = 0.f;
-  if (c < 2LL * dim)
-    for (int p = y; p < parts; p += 16) s += part[(long long)p * 2 * dim + c];
+  if (c < 2LL * dim) {
+    constexpr int kAtOnce = 10;
+    for (int p0 = y; p0 < parts; p0 += kAtOnce * kColumnWarps) {
+      float v[kAtOnce];
+#pragma unroll
+      for (int k = 0; k < kAtOnce; ++k) {
+        const int p = p0 + k * kColumnWarps;
+        v[k] = p < parts ? __ldcg(part + (long long)p * 2 * dim + c) : 0.f;
+      }
+#pragma unroll
+      for (int k = 0; k < kAtOnce; ++k) s += v[k];
+    }
+  }
   sums[y][x] = s;
   __syncthreads();
   if (y != 0 || c >= 2LL * dim) return;
   s = sums[0][x];
 #pragma unroll
-  for (int w = 1; w < 16; ++w) s += sums[w][x];
+  for (int w = 1; w < kColumnWarps; ++w) s += sums[w][x];
   void* out = c < dim ? dw : db;
   if (!out) return;
   const long long i = c < dim ? c : c - dim;
@@ -368,50 +686,79 @@ __global__ void __launch_bounds__(512) k_norm_columns(const float* __restrict__ 
 
 // How a row is spread over threads.
 struct RowPlan {
-  int vec;      // elements per access: 16 bytes' worth, or 1
-  int nv;       // accesses per thread and row; 0: the row does not fit into registers
+  int nv;       // accesses per thread and row; 0: the row does not fit
   int threads;  // of a group
   int groups;   // of a CTA
 };
 
-RowPlan plan_rows(long long dim, int vec) {
+// vec: elements per access; groups fill a CTA of up to `most` threads.  The
+// fewest accesses per thread that leave at most a quarter of those without work.
+RowPlan plan_rows(long long dim, int vec, int most) {
   const int max_nv = vec == 1 ? 16 : 4;
   const long long nvec = dim / vec;
-  RowPlan p{vec, 0, 0, 1};
+  RowPlan best{0, 0, 1};
+  double best_share = 0.0;
   for (int nv = vec == 1 ? 4 : 1; nv <= max_nv; nv *= 2) {
     const long long threads = ((nvec + nv - 1) / nv + 31) / 32 * 32;
-    if (threads <= kMaxThreads) {
-      p.nv = nv;
-      p.threads = (int)threads;
-      p.groups = std::max(1, std::min(8, 256 / p.threads));
-      break;
+    if (threads > kMaxThreads) continue;
+    RowPlan p{nv, (int)threads, 0};
+    p.groups = std::max(1, std::min(8, most / p.threads));
+    const double share = (double)nvec * p.groups / ((double)nv * most);
+    if (share > best_share) {
+      best = p;
+      best_share = share;
     }
+    if (share >= 0.75) break;
   }
-  return p;
+  return best;
 }
 
-// f(VEC, NV, R) for a plan, as compile-time constants.
 template <int V> struct Int {
   static constexpr int value = V;
 };
-template <typename T, typename F> void with_plan(const RowPlan& p, bool few, F&& f) {
-  constexpr int V = Vec16<T>::N;
-  if (p.vec != 1) {
-    if (p.nv == 1) {
-      if (few) f(Int<V>(), Int<1>(), Int<1>());
-      else f(Int<V>(), Int<1>(), Int<4>());
-    } else if (p.nv == 2) {
-      f(Int<V>(), Int<2>(), Int<1>());
-    } else {
-      f(Int<V>(), Int<4>(), Int<1>());
-    }
-  } else {
-    if (p.nv == 4) f(Int<1>(), Int<4>(), Int<2>());
-    else if (p.nv == 8) f(Int<1>(), Int<8>(), Int<1>());
-    else f(Int<1>(), Int<16>(), Int<1>());
-  }
+// f(NV, R) as compile-time constants: R1 rows at a time where a thread has one
+// vector of each, fewer where it has more, one where there are few rows.
+template <int R1, typename F> void with_vec_plan(const RowPlan& p, bool few, F&& f) {
+  if (p.nv == 1 && few) f(Int<1>(), Int<1>());
+  else if (p.nv == 1) f(Int<1>(), Int<R1>());
+  else if (p.nv == 2) f(Int<2>(), Int<2>());
+  else f(Int<4>(), Int<1>());
 }
-int rows_per_group(const RowPlan& p, bool few) { return p.vec != 1 ? (p.nv == 1 && !few ? 4 : 1) : (p.nv == 4 ? 2 : 1); }
+int vec_rows(const RowPlan& p, int r1, bool few) { return p.nv == 1 ? (few ? 1 : r1) : p.nv == 2 ? 2 : 1; }
+template <typename F> void with_scalar_plan(const RowPlan& p, F&& f) {
+  if (p.nv == 4) f(Int<4>(), Int<2>());
+  else if (p.nv == 8) f(Int<8>(), Int<1>());
+  else f(Int<16>(), Int<1>());
+}
+int scalar_rows(const RowPlan& p) { return p.nv == 4 ? 2 : 1; }
+
+// Raises a kernel's shared-memory limit, once per device.
+template <typename K> cudaError_t raise_smem(K kernel, std::atomic<unsigned long long>& raised, int device, int bytes) {
+  const unsigned long long bit = 1ull << device;
+  if (raised.load(std::memory_order_acquire) & bit) return cudaSuccess;
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess) raised.fetch_or(bit, std::memory_order_release);
+  return e;
+}
+
+template <typename T, int NV, int R>
+cudaError_t launch_forward(const RowsArgs& a, const RowPlan& p, unsigned grid, int device, cudaStream_t st) {
+  static std::atomic<unsigned long long> raised{0};
+  const cudaError_t e = raise_smem(k_norm_forward_vec<T, NV, R>, raised, device, kStages * R * NV * kMaxThreads * 16);
+  if (e != cudaSuccess) return e;
+  k_norm_forward_vec<T, NV, R>
+      <<<grid, dim3(p.threads, p.groups), (size_t)kStages * R * NV * kMaxThreads * 16, st>>>(a);
+  return cudaGetLastError();
+}
+template <typename T, int NV, int R>
+cudaError_t launch_backward(const RowsArgs& a, const RowPlan& p, unsigned grid, int device, cudaStream_t st) {
+  static std::atomic<unsigned long long> raised{0};
+  const cudaError_t e = raise_smem(k_norm_backward_vec<T, NV, R>, raised, device, kStages * R * NV * kMaxThreads * 32);
+  if (e != cudaSuccess) return e;
+  k_norm_backward_vec<T, NV, R>
+      <<<grid, dim3(p.threads, p.groups), (size_t)kStages * R * NV * kMaxThreads * 32, st>>>(a);
+  return cudaGetLastError();
+}
 
 template <typename F> void by_dtype(int32_t d, F&& f) {
   switch (d) {
@@ -510,22 +857,29 @@ extern "C" int psgd_layernorm_forward(psgd_layernorm* h, const void* x, psgd_dty
              (int)param_dtype, eps};
   const int full = 16 / dtype_size(dtype);
   const bool vec = h->dim % full == 0 && vec_ok(x, x_stride, dtype) && vec_ok(y, y_stride, dtype);
-  const RowPlan p = plan_rows(h->dim, vec ? full : 1);
+  const RowPlan p = plan_rows(h->dim, vec ? full : 1, vec ? kMaxThreads : 256);
+  cudaError_t e = cudaSuccess;
   by_dtype(dtype, [&](auto* tt) {
     using T = std::remove_pointer_t<decltype(tt)>;
     if (p.nv == 0) {
       k_norm_forward_long<T><<<(unsigned)std::min<long long>(rows, h->sms * 4), kMaxThreads, 0, st>>>(a);
-      return;
+      e = cudaGetLastError();
+    } else if (vec) {
+      const bool few = rows < (long long)h->sms * 8 * p.groups;
+      const long long per = (long long)p.groups * vec_rows(p, 2, few);
+      const unsigned grid = (unsigned)std::min<long long>((rows + per - 1) / per, h->sms * (p.nv == 1 ? 2 : 1));
+      with_vec_plan<2>(p, few, [&](auto nv, auto r) {
+        e = launch_forward<T, decltype(nv)::value, decltype(r)::value>(a, p, grid, h->device, st);
+      });
+    } else {
+      const long long per = (long long)p.groups * scalar_rows(p);
+      const unsigned grid = (unsigned)std::min<long long>((rows + per - 1) / per, (long long)h->sms * std::max(1, 1024 / (p.threads * p.groups)));
+      with_scalar_plan(p, [&](auto nv, auto r) {
+        k_norm_forward<T, 1, decltype(nv)::value, decltype(r)::value><<<grid, dim3(p.threads, p.groups), 0, st>>>(a);
+      });
+      e = cudaGetLastError();
     }
-    const bool few = rows <= (long long)h->sms * 4 * p.groups;
-    const long long ctas = (rows + (long long)p.groups * rows_per_group(p, few) - 1) / (p.groups * rows_per_group(p, few));
-    const unsigned grid = (unsigned)std::min<long long>(ctas, (long long)h->sms * std::max(1, 1024 / (p.threads * p.groups)));
-    with_plan<T>(p, few, [&](auto v, auto nv, auto r) {
-      k_norm_forward<T, decltype(v)::value, decltype(nv)::value, decltype(r)::value>
-          <<<grid, dim3(p.threads, p.groups), 0, st>>>(a);
-    });
   });
-  const cudaError_t e = cudaGetLastError();
   return e == cudaSuccess ? PSGD_OK : cuda_fail(who, e);
 }
 
@@ -561,8 +915,9 @@ extern "C" int psgd_layernorm_backward(psgd_layernorm* h, const void* grad, int6
   const int full = 16 / dtype_size(dtype);
   const bool vec = h->dim % full == 0 && vec_ok(x, x_stride, dtype) && vec_ok(grad, grad_stride, dtype) &&
                    vec_ok(dx, dx_stride, dtype);
-  const RowPlan p = plan_rows(h->dim, vec ? full : 1);
+  const RowPlan p = plan_rows(h->dim, vec ? full : 1, vec ? kMaxThreads : 256);
   int parts = 0;
+  cudaError_t e = cudaSuccess;
   if (rows > 0)
     by_dtype(dtype, [&](auto* tt) {
       using T = std::remove_pointer_t<decltype(tt)>;
@@ -572,25 +927,36 @@ extern "C" int psgd_layernorm_backward(psgd_layernorm* h, const void* grad, int6
           parts = (int)std::min<long long>((rows + 31) / 32, h->max_ctas);
           k_norm_columns_long<T><<<dim3((unsigned)((h->dim + 255) / 256), parts), 256, 0, st>>>(a);
         }
-        return;
+        e = cudaGetLastError();
+      } else if (vec) {
+        const bool few = rows < (long long)h->sms * 8 * p.groups;
+        const long long per = (long long)p.groups * vec_rows(p, 4, few);
+        parts = (int)std::min<long long>((rows + per - 1) / per, h->sms);
+        with_vec_plan<4>(p, few, [&](auto nv, auto r) {
+          e = launch_backward<T, decltype(nv)::value, decltype(r)::value>(a, p, (unsigned)parts, h->device, st);
+        });
+      } else {
+        const long long per = (long long)p.groups * scalar_rows(p);
+        parts = (int)std::min<long long>((rows + per - 1) / per,
+                                         (long long)h->sms * std::min(4, std::max(1, 1024 / (p.threads * p.groups))));
+        const size_t smem = p.groups > 1 ? (size_t)h->dim * 8 : 0;
+        with_scalar_plan(p, [&](auto nv, auto r) {
+          k_norm_backward<T, 1, decltype(nv)::value, decltype(r)::value>
+              <<<(unsigned)parts, dim3(p.threads, p.groups), smem, st>>>(a);
+        });
+        e = cudaGetLastError();
       }
-      const bool few = rows <= (long long)h->sms * 4 * p.groups;
-      const long long ctas =
-          (rows + (long long)p.groups * rows_per_group(p, few) - 1) / (p.groups * rows_per_group(p, few));
-      const unsigned grid =
-          (unsigned)std::min<long long>(ctas, (long long)h->sms * std::min(4, std::max(1, 1024 / (p.threads * p.groups))));
-      parts = (int)grid;
-      const size_t smem = p.groups > 1 ? (size_t)h->dim * 8 : 0;
-      with_plan<T>(p, few, [&](auto v, auto nv, auto r) {
-        k_norm_backward<T, decltype(v)::value, decltype(nv)::value, decltype(r)::value>
-            <<<grid, dim3(p.threads, p.groups), smem, st>>>(a);
-      });
     });
-  cudaError_t e = cudaGetLastError();
   if (e == cudaSuccess && params) {
-    k_norm_columns<<<(unsigned)((2 * h->dim + 31) / 32), 512, 0, st>>>(h->part, parts, (int)h->dim, dweight, dbias,
-                                                                      dparam_dtype, accumulate);
-    e = cudaGetLastError();
+    cudaLaunchAttribute early = early_launch();
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)((2 * h->dim + 31) / 32));
+    cfg.blockDim = dim3(32 * kColumnWarps);
+    cfg.stream = st;
+    cfg.attrs = &early;
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, k_norm_columns, (const float*)h->part, parts, (int)h->dim, dweight, dbias,
+                           (int)dparam_dtype, (int)accumulate);
   }
   return e == cudaSuccess ? PSGD_OK : cuda_fail(who, e);
 }
