@@ -601,7 +601,8 @@ size_t psgd_layernorm_workspace_bytes(const psgd_layernorm* n);
  * psgd_layernorm_forward -- y = (x - mean) rstd weight + bias per row, with
  * rstd = (mean((x - mean)^2) + eps)^-1/2.
  *
- *   x, y         : `rows` rows of `dtype`, x_stride / y_stride apart.
+ *   x, y         : `rows` rows (at most 2^30) of `dtype`, x_stride / y_stride
+ *                  apart.
  *   weight, bias : dim elements of param_dtype; NULL: 1 and 0.
  *   mean, rstd   : out, one float a row (what the backward pass takes); may be
  *                  NULL.
@@ -638,7 +639,8 @@ int psgd_layernorm_backward(psgd_layernorm* n, const void* grad, int64_t grad_st
  *   loss    = w T^2 sum_k p_k (log p_k - log q[index_k]),
  *   dlogits = grad_scale w T (q_j - sum over the k with index_k = j of p_k).
  *
- *   logits  : `rows` rows of `vocab` elements of `dtype`.
+ *   logits  : `rows` rows (below 2^28) of `vocab` elements (at most 2^30) of
+ *             `dtype`.
  *   teacher, index : `rows` rows of k teacher logits and of the vocabulary
  *             entries (index_bits 32 or 64) they belong to.  An entry whose
  *             index lies outside [0, vocab) is not valid: a row with fewer

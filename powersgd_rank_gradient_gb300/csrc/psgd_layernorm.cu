@@ -52,18 +52,20 @@ struct RowsArgs {
 // shuffles: while there is more than one value, half of the lanes keep one half
 // of them and send the other.  Returns the sum of value fold_index(lane).
 template <int N> __device__ __forceinline__ float fold_sum(float (&v)[N], int lane) {
-  int off = 16;
 #pragma unroll
-  for (int n = N / 2; n >= 1; n /= 2, off /= 2) {
-    const bool upper = lane & off;
+  for (int k = 0; k < 5; ++k) {
+    const int off = 16 >> k, n = N >> (k + 1);
+    if (n >= 1) {
+      const bool upper = lane & off;
 #pragma unroll
-    for (int i = 0; i < n; ++i) {
-      const float send = upper ? v[i] : v[i + n], keep = upper ? v[i + n] : v[i];
-      v[i] = keep + __shfl_xor_sync(0xffffffffu, send, off);
+      for (int i = 0; i < n; ++i) {
+        const float send = upper ? v[i] : v[i + n], keep = upper ? v[i + n] : v[i];
+        v[i] = keep + __shfl_xor_sync(0xffffffffu, send, off);
+      }
+    } else {
+      v[0] += __shfl_xor_sync(0xffffffffu, v[0], off);
     }
   }
-#pragma unroll
-  for (; off > 0; off /= 2) v[0] += __shfl_xor_sync(0xffffffffu, v[0], off);
   return v[0];
 }
 template <int N> __device__ __forceinline__ int fold_index(int lane) {
@@ -85,7 +87,10 @@ __device__ __forceinline__ void group_sum(float (&v)[N], float* buf, int warps, 
   if ((lane & (32 / N - 1)) == 0) buf[warp * N + fold_index<N>(lane)] = x;
   asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "r"(threads) : "memory");
   x = 0.f;
-  for (int w = lane / N; w < warps; w += 32 / N) x += buf[w * N + lane % N];
+  constexpr int kMaxWarps = kMaxThreads / 32;
+#pragma unroll
+  for (int k = 0; k < (kMaxWarps * N + 31) / 32; ++k)  // value lane % N of warp lane / N + k * 32 / N
+    if (k * 32 + lane < warps * N) x += buf[k * 32 + lane];
 #pragma unroll
   for (int off = N; off < 32; off *= 2) x += __shfl_xor_sync(0xffffffffu, x, off);
 #pragma unroll
@@ -135,17 +140,17 @@ __global__ void __launch_bounds__(kMaxThreads, NV == 1 ? 2 : 1) k_norm_forward_v
   float* buf[2] = {red[0] + group * warps * R, red[1] + group * warps * R};
   const int nvec = a.dim / NE;
   const float inv = 1.f / (float)a.dim;
-  const long long batches = (a.rows + R - 1) / R, step = (long long)gridDim.x * blockDim.y;
+  const int step = gridDim.x * blockDim.y * R;
   uint4* mine = staged + group * threads + t;
   bool in[NV];
 #pragma unroll
   for (int j = 0; j < NV; ++j) in[j] = t + j * threads < nvec;
-  long long b = (long long)blockIdx.x * blockDim.y + group;
-  // the next batch to copy, and this thread's first vector of its rows
-  long long ahead = b;
-  const T* from = (const T*)a.x + b * R * a.xs + t * NE;
+  int row = ((int)blockIdx.x * blockDim.y + group) * R;  // the batch's first row
+  // rows left from the next batch to copy on, and this thread's first vector of it
+  int left = (int)a.rows - row;
+  const T* from = (const T*)a.x + row * a.xs + t * NE;
+  const long long from_step = step * a.xs, to_step = step * a.ys;
   auto issue = [&](int stage) {
-    const long long left = a.rows - ahead * R;
 #pragma unroll
     for (int r = 0; r < R; ++r)
 #pragma unroll
@@ -153,8 +158,8 @@ __global__ void __launch_bounds__(kMaxThreads, NV == 1 ? 2 : 1) k_norm_forward_v
         if (r < left && in[j])
           copy16(mine + ((stage * R + r) * NV + j) * kMaxThreads, from + r * a.xs + j * threads * NE);
     commit_copies();
-    ahead += step;
-    from += step * R * a.xs;
+    left -= step;
+    from += from_step;
   };
 #pragma unroll
   for (int k = 0; k < kStages - 1; ++k) issue(k);
@@ -165,12 +170,12 @@ __global__ void __launch_bounds__(kMaxThreads, NV == 1 ? 2 : 1) k_norm_forward_v
     load_param<NP>(a.w, a.pdtype, (long long)v * NE, in[j], 1.f, w[j]);
     load_param<NP>(a.b, a.pdtype, (long long)v * NE, in[j], 0.f, bias[j]);
   }
-  T* to = (T*)a.y + b * R * a.ys + t * NE;
+  T* to = (T*)a.y + row * a.ys + t * NE;
   int stage = 0;
-  for (; b < batches; b += step, to += step * R * a.ys) {
+  for (; row < (int)a.rows; row += step, to += to_step) {
     asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
     issue(stage == 0 ? kStages - 1 : stage - 1);
-    const int rows = (int)min((long long)R, a.rows - b * R);
+    const int rows = min(R, (int)a.rows - row);
     F2 x[R][NV][NP];
     float s[R];
 #pragma unroll
@@ -212,8 +217,8 @@ __global__ void __launch_bounds__(kMaxThreads, NV == 1 ? 2 : 1) k_norm_forward_v
       if (r >= rows) break;
       const float rstd = rsqrtf(fmaf(s[r], inv, a.eps));
       if (t == 0) {
-        if (a.mean) a.mean[b * R + r] = mean[r];
-        if (a.rstd) a.rstd[b * R + r] = rstd;
+        if (a.mean) a.mean[row + r] = mean[r];
+        if (a.rstd) a.rstd[row + r] = rstd;
       }
       const F2 rs = f2(rstd, rstd);
 #pragma unroll
@@ -239,19 +244,19 @@ __global__ void __launch_bounds__(kMaxThreads, 1) k_norm_backward_vec(RowsArgs a
   const int warps = threads / 32, warp = t >> 5, lane = t & 31, cta_warp = group * warps + warp;
   const int nvec = a.dim / NE;
   const float inv = 1.f / (float)a.dim;
-  const long long batches = (a.rows + R - 1) / R, step = (long long)gridDim.x * blockDim.y;
+  const int step = gridDim.x * blockDim.y * R;
   uint4* mine = staged + group * threads + t;
   bool in[NV];
 #pragma unroll
   for (int j = 0; j < NV; ++j) in[j] = t + j * threads < nvec;
-  long long b = (long long)blockIdx.x * blockDim.y + group;
-  // the next batch to copy, and this thread's first vectors of its rows
-  long long ahead = b;
-  const T* from_x = (const T*)a.x + b * R * a.xs + t * NE;
-  const T* from_g = (const T*)a.g + b * R * a.gs + t * NE;
-  const float* from_s = (lane & 1 ? a.rstd : a.mean) + b * R + lane / 2;
+  int row = ((int)blockIdx.x * blockDim.y + group) * R;  // the batch's first row
+  // rows left from the next batch to copy on, and this thread's first vectors of it
+  int left = (int)a.rows - row;
+  const T* from_x = (const T*)a.x + row * a.xs + t * NE;
+  const T* from_g = (const T*)a.g + row * a.gs + t * NE;
+  const float* from_s = (lane & 1 ? a.rstd : a.mean) + row + lane / 2;
+  const long long x_step = step * a.xs, g_step = step * a.gs, y_step = step * a.ys;
   auto issue = [&](int stage) {
-    const long long left = a.rows - ahead * R;
 #pragma unroll
     for (int r = 0; r < R; ++r)
 #pragma unroll
@@ -263,10 +268,10 @@ __global__ void __launch_bounds__(kMaxThreads, 1) k_norm_backward_vec(RowsArgs a
         }
     if (lane < 2 * R && lane / 2 < left) copy4(&stats[stage][cta_warp][lane], from_s);
     commit_copies();
-    ahead += step;
-    from_x += step * R * a.xs;
-    from_g += step * R * a.gs;
-    from_s += step * R;
+    left -= step;
+    from_x += x_step;
+    from_g += g_step;
+    from_s += step;
   };
 #pragma unroll
   for (int k = 0; k < kStages - 1; ++k) issue(k);
@@ -278,16 +283,16 @@ __global__ void __launch_bounds__(kMaxThreads, 1) k_norm_backward_vec(RowsArgs a
 #pragma unroll
     for (int h = 0; h < NP; ++h) dw[j][h] = db[j][h] = f2(0.f, 0.f);
   }
-  T* to = (T*)a.y + b * R * a.ys + t * NE;
+  T* to = (T*)a.y + row * a.ys + t * NE;
   int stage = 0, flip = 0;
-  for (; b < batches; b += step, to += step * R * a.ys) {
+  for (; row < (int)a.rows; row += step, to += y_step) {
     asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
     __syncwarp();  // the other lanes' copies of the statistics
     issue(stage == 0 ? kStages - 1 : stage - 1);
     const uint4* data = mine + stage * R * NV * 2 * kMaxThreads;
     const float* stat = stats[stage][cta_warp];
     auto rows_of = [&](auto full) {
-      const int rows = decltype(full)::value ? R : (int)(a.rows - b * R);
+      const int rows = decltype(full)::value ? R : (int)a.rows - row;
       float s[2 * R];
 #pragma unroll
       for (int r = 0; r < R; ++r) {
@@ -339,7 +344,7 @@ __global__ void __launch_bounds__(kMaxThreads, 1) k_norm_backward_vec(RowsArgs a
         }
       }
     };
-    if ((b + 1) * R <= a.rows) rows_of(std::true_type());
+    if (row + R <= (int)a.rows) rows_of(std::true_type());
     else rows_of(std::false_type());
     stage = stage + 1 == kStages ? 0 : stage + 1;
   }
@@ -776,7 +781,7 @@ int check_common(const char* who, const psgd_layernorm* h, int32_t dtype, int32_
   const std::string w(who);
   if (!h) return fail(PSGD_EINVAL, w + ": NULL layer norm");
   if (!dtype_ok(dtype) || !dtype_ok(pdtype)) return fail(PSGD_EINVAL, w + ": unknown dtype");
-  if (rows < 0 || rows > kMaxElems) return fail(PSGD_EINVAL, w + ": bad row count");
+  if (rows < 0 || rows > (1 << 30)) return fail(PSGD_EINVAL, w + ": rows must be in [0, 2^30]");
   return PSGD_OK;
 }
 
