@@ -130,7 +130,7 @@ template <int NE> __device__ __forceinline__ void load_param(const void* w, int 
 constexpr int kStages = 3;
 
 template <typename T, int NV, int R>
-__global__ void __launch_bounds__(kMaxThreads, NV == 1 ? 2 : 1) k_norm_forward_vec(RowsArgs a) {
+__global__ void __launch_bounds__(kMaxThreads, NV == 1 && R == 1 ? 2 : 1) k_norm_forward_vec(RowsArgs a) {
   constexpr int NE = Vec16<T>::N, NP = NE / 2;
   constexpr int kStep = R * NV;  // vectors of a stage per thread, kMaxThreads apart
   extern __shared__ __align__(16) uint4 staged[];
@@ -381,197 +381,212 @@ __global__ void __launch_bounds__(kMaxThreads, 1) k_norm_backward_vec(RowsArgs a
   }
 }
 
-template <typename T, int VEC, int NV, int R>
-__global__ void __launch_bounds__(kMaxThreads) k_norm_forward(RowsArgs a) {
+// The kernels for rows of any length and alignment.  A row's aligned 16-byte
+// granules are copied ahead into shared memory at the row's own place within
+// its first granule, and read from there element by element: thread t owns the
+// columns t, t + threads, ... (NV of them).  A barrier of the group follows
+// each wait, as a granule is used by other threads than the one that copied it.
+//
+// Starts the copy of row `index` of an array: granule t, t + threads, ... into
+// `slot`.  The bytes in front of a row within its first granule are the array's
+// own where the row begins that far into it; elsewhere there may be nothing to
+// read, and the granule's elements are copied one by one.
+template <typename T>
+__device__ __forceinline__ void copy_row(unsigned char* slot, const T* base, int index, long long stride, int dim, int t,
+                                         int threads) {
+  const T* row = base + index * stride;
+  const int before = (int)((uintptr_t)row & 15);
+  const bool first = index * stride * (long long)sizeof(T) < before;
+  const int bytes = before + dim * (int)sizeof(T);
+  const unsigned char* src = (const unsigned char*)row - before;
+  for (int o = t * 16; o < bytes; o += threads * 16) {
+    if (first && o == 0) {
+      for (int e = before; e < min(16, bytes); e += (int)sizeof(T))
+        *(T*)(slot + e) = *(const T*)(src + e);
+    } else {
+      const int n = min(16, bytes - o);
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"((unsigned)__cvta_generic_to_shared(slot + o)),
+                   "l"(src + o), "r"(n)
+                   : "memory");
+    }
+  }
+}
+// Bytes of a row's place in shared memory.
+__host__ __device__ inline int slot_bytes(int dim, int size) { return (dim * size + 15 + 15) / 16 * 16; }
+
+__device__ __forceinline__ void group_barrier(int group, int threads) {
+  asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "r"(threads) : "memory");
+}
+
+template <typename T, int NV, int R>
+__global__ void __launch_bounds__(kMaxThreads, NV == 4 ? 2 : 1) k_norm_forward_any(RowsArgs a) {
+  extern __shared__ __align__(16) unsigned char slots[];
   __shared__ float red[2][kMaxThreads / 32 * R];
   const int t = threadIdx.x, group = threadIdx.y, threads = blockDim.x;
   const int warps = threads / 32, warp = t >> 5, lane = t & 31;
   float* buf[2] = {red[0] + group * warps * R, red[1] + group * warps * R};
-  const int nvec = a.dim / VEC;
+  const int slot = slot_bytes(a.dim, sizeof(T));
+  unsigned char* mine = slots + (size_t)group * kStages * R * slot;
   const float inv = 1.f / (float)a.dim;
-  const long long step = (long long)gridDim.x * blockDim.y * R;
-  float w[NV][VEC], b[NV][VEC];
+  const int step = gridDim.x * blockDim.y * R;
+  int row = ((int)blockIdx.x * blockDim.y + group) * R, ahead = row;
+  auto issue = [&](int stage) {
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+      if (ahead + r < (int)a.rows)
+        copy_row(mine + (stage * R + r) * slot, (const T*)a.x, ahead + r, a.xs, a.dim, t, threads);
+    commit_copies();
+    ahead = ahead < (int)a.rows ? ahead + step : ahead;
+  };
+#pragma unroll
+  for (int k = 0; k < kStages - 1; ++k) issue(k);
+  float w[NV], bias[NV];
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
-    const int v = t + j * threads;
-    load_param<VEC>(a.w, a.pdtype, (long long)v * VEC, v < nvec, 1.f, w[j]);
-    load_param<VEC>(a.b, a.pdtype, (long long)v * VEC, v < nvec, 0.f, b[j]);
+    float v[1];
+    load_param<1>(a.w, a.pdtype, t + j * threads, t + j * threads < a.dim, 1.f, v);
+    w[j] = v[0];
+    load_param<1>(a.b, a.pdtype, t + j * threads, t + j * threads < a.dim, 0.f, v);
+    bias[j] = v[0];
   }
-  for (long long row0 = ((long long)blockIdx.x * blockDim.y + group) * R; row0 < a.rows; row0 += step) {
-    Pack<T, VEC> x[R][NV];
-#pragma unroll
-    for (int r = 0; r < R; ++r) {
-      const T* src = (const T*)a.x + (row0 + r) * a.xs;
-#pragma unroll
-      for (int j = 0; j < NV; ++j) {
-        const int v = t + j * threads;
-        if (row0 + r < a.rows && v < nvec) x[r][j] = load_pack<T, VEC>(src + (long long)v * VEC);
-      }
-    }
-    float s[R];
+  int stage = 0;
+  for (; row < (int)a.rows; row += step) {
+    asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
+    group_barrier(group, threads);
+    issue(stage == 0 ? kStages - 1 : stage - 1);
+    float x[R][NV], s[R], mean[R];
 #pragma unroll
     for (int r = 0; r < R; ++r) {
       s[r] = 0.f;
+      const T* src = (const T*)(mine + (stage * R + r) * slot + ((uintptr_t)((const T*)a.x + (row + r) * a.xs) & 15));
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
-        if (row0 + r < a.rows && t + j * threads < nvec) {
-#pragma unroll
-          for (int k = 0; k < VEC; ++k) s[r] += to_f(x[r][j].v[k]);
-        }
+        x[r][j] = row + r < (int)a.rows && t + j * threads < a.dim ? to_f(src[t + j * threads]) : 0.f;
+        s[r] += x[r][j];
       }
     }
+    stage = stage + 1 == kStages ? 0 : stage + 1;
     group_sum<R>(s, buf[0], warps, warp, lane, group, threads);
-    float mean[R], q[R];
 #pragma unroll
     for (int r = 0; r < R; ++r) {
       mean[r] = s[r] * inv;
-      q[r] = 0.f;
+      s[r] = 0.f;
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
-        if (row0 + r < a.rows && t + j * threads < nvec) {
-#pragma unroll
-          for (int k = 0; k < VEC; ++k) {
-            const float d = to_f(x[r][j].v[k]) - mean[r];
-            q[r] = fmaf(d, d, q[r]);
-          }
-        }
+        x[r][j] -= mean[r];
+        if (t + j * threads < a.dim) s[r] = fmaf(x[r][j], x[r][j], s[r]);
       }
     }
-    group_sum<R>(q, buf[1], warps, warp, lane, group, threads);
-    float rstd[R];
+    group_sum<R>(s, buf[1], warps, warp, lane, group, threads);
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-      rstd[r] = rsqrtf(fmaf(q[r], inv, a.eps));
-      if (t == 0 && row0 + r < a.rows) {
-        if (a.mean) a.mean[row0 + r] = mean[r];
-        if (a.rstd) a.rstd[row0 + r] = rstd[r];
+      if (row + r >= (int)a.rows) break;
+      const float rstd = rsqrtf(fmaf(s[r], inv, a.eps));
+      if (t == 0) {
+        if (a.mean) a.mean[row + r] = mean[r];
+        if (a.rstd) a.rstd[row + r] = rstd;
       }
-    }
+      T* dst = (T*)a.y + (row + r) * a.ys;
 #pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      const int v = t + j * threads;
-      if (v >= nvec) continue;
-#pragma unroll
-      for (int r = 0; r < R; ++r) {
-        if (row0 + r >= a.rows) continue;
-        float f[VEC];
-#pragma unroll
-        for (int k = 0; k < VEC; ++k) f[k] = fmaf((to_f(x[r][j].v[k]) - mean[r]) * rstd[r], w[j][k], b[j][k]);
-        store_pack<T, VEC>((T*)a.y + (row0 + r) * a.ys + (long long)v * VEC, f);
-      }
+      for (int j = 0; j < NV; ++j)
+        if (t + j * threads < a.dim) dst[t + j * threads] = from_f<T>(fmaf(x[r][j] * rstd, w[j], bias[j]));
     }
   }
 }
 
-template <typename T, int VEC, int NV, int R>
-__global__ void __launch_bounds__(kMaxThreads) k_norm_backward(RowsArgs a) {
-  extern __shared__ float cols[];  // 2 x dim: the CTA's dw and db (more than one group only)
+template <typename T, int NV, int R>
+__global__ void __launch_bounds__(kMaxThreads, NV == 4 ? 2 : 1) k_norm_backward_any(RowsArgs a) {
+  extern __shared__ __align__(16) unsigned char slots[];
   __shared__ float red[2][kMaxThreads / 32 * 2 * R];
+  __shared__ float stats[kStages][kMaxThreads / 32][2 * R];  // a group's
   const int t = threadIdx.x, group = threadIdx.y, threads = blockDim.x;
   const int warps = threads / 32, warp = t >> 5, lane = t & 31;
-  const int nvec = a.dim / VEC;
+  const int slot = slot_bytes(a.dim, sizeof(T));
+  unsigned char* mine = slots + (size_t)group * kStages * R * 2 * slot;
   const float inv = 1.f / (float)a.dim;
-  float dw[NV][VEC], db[NV][VEC], w[NV][VEC];
+  const int step = gridDim.x * blockDim.y * R;
+  int row = ((int)blockIdx.x * blockDim.y + group) * R, ahead = row;
+  auto issue = [&](int stage) {
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+      if (ahead + r < (int)a.rows) {
+        copy_row(mine + (stage * R + r) * 2 * slot, (const T*)a.x, ahead + r, a.xs, a.dim, t, threads);
+        copy_row(mine + ((stage * R + r) * 2 + 1) * slot, (const T*)a.g, ahead + r, a.gs, a.dim, t, threads);
+      }
+    if (t < 2 * R && ahead + t / 2 < (int)a.rows) copy4(&stats[stage][group][t], (t & 1 ? a.rstd : a.mean) + ahead + t / 2);
+    commit_copies();
+    ahead = ahead < (int)a.rows ? ahead + step : ahead;
+  };
+#pragma unroll
+  for (int k = 0; k < kStages - 1; ++k) issue(k);
+  float dw[NV], db[NV], w[NV];
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
-    const int v = t + j * threads;
-    load_param<VEC>(a.w, a.pdtype, (long long)v * VEC, v < nvec, 1.f, w[j]);
-#pragma unroll
-    for (int k = 0; k < VEC; ++k) dw[j][k] = db[j][k] = 0.f;
+    float v[1];
+    load_param<1>(a.w, a.pdtype, t + j * threads, t + j * threads < a.dim, 1.f, v);
+    w[j] = v[0];
+    dw[j] = db[j] = 0.f;
   }
-  const long long step = (long long)gridDim.x * blockDim.y * R;
-  int flip = 0;
-  for (long long row0 = ((long long)blockIdx.x * blockDim.y + group) * R; row0 < a.rows; row0 += step) {
-    Pack<T, VEC> x[R][NV], g[R][NV];
-    float mean[R], rstd[R];
-#pragma unroll
-    for (int r = 0; r < R; ++r) {
-      const bool in = row0 + r < a.rows;
-#pragma unroll
-      for (int j = 0; j < NV; ++j) {
-        const int v = t + j * threads;
-        if (in && v < nvec) {
-          x[r][j] = load_pack<T, VEC>((const T*)a.x + (row0 + r) * a.xs + (long long)v * VEC);
-          g[r][j] = load_pack<T, VEC>((const T*)a.g + (row0 + r) * a.gs + (long long)v * VEC);
-        }
-      }
-      mean[r] = in ? __ldg(a.mean + row0 + r) : 0.f;
-      rstd[r] = in ? __ldg(a.rstd + row0 + r) : 0.f;
-    }
-    float s[2 * R];
+  int stage = 0, flip = 0;
+  for (; row < (int)a.rows; row += step) {
+    asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
+    group_barrier(group, threads);
+    issue(stage == 0 ? kStages - 1 : stage - 1);
+    const float* stat = stats[stage][group];
+    const int rows = min(R, (int)a.rows - row);
+    float d[R][NV], g[R][NV], s[2 * R];
 #pragma unroll
     for (int r = 0; r < R; ++r) {
       s[2 * r] = s[2 * r + 1] = 0.f;
-      const bool in = row0 + r < a.rows;
+      if (r >= rows) continue;
+      const unsigned char* at = mine + (stage * R + r) * 2 * slot;
+      const T* x = (const T*)(at + ((uintptr_t)((const T*)a.x + (row + r) * a.xs) & 15));
+      const T* y = (const T*)(at + slot + ((uintptr_t)((const T*)a.g + (row + r) * a.gs) & 15));
+      const float mean = stat[2 * r], rstd = stat[2 * r + 1];
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
-        if (in && t + j * threads < nvec) {
-#pragma unroll
-          for (int k = 0; k < VEC; ++k) {
-            const float gv = to_f(g[r][j].v[k]);
-            const float xh = (to_f(x[r][j].v[k]) - mean[r]) * rstd[r];
-            const float av = gv * w[j][k];
-            s[2 * r] += av;
-            s[2 * r + 1] = fmaf(av, xh, s[2 * r + 1]);
-            dw[j][k] = fmaf(gv, xh, dw[j][k]);
-            db[j][k] += gv;
-          }
-        }
+        const bool in = t + j * threads < a.dim;
+        d[r][j] = in ? to_f(x[t + j * threads]) - mean : 0.f;
+        g[r][j] = in ? to_f(y[t + j * threads]) : 0.f;
+        const float gd = g[r][j] * d[r][j];
+        s[2 * r] = fmaf(g[r][j], w[j], s[2 * r]);
+        s[2 * r + 1] = fmaf(gd, w[j], s[2 * r + 1]);
+        dw[j] = fmaf(gd, rstd, dw[j]);
+        db[j] += g[r][j];
       }
     }
+    stage = stage + 1 == kStages ? 0 : stage + 1;
+    if (!a.y) continue;
     group_sum<2 * R>(s, red[flip] + group * warps * 2 * R, warps, warp, lane, group, threads);
     flip ^= 1;
-    if (a.y) {
 #pragma unroll
-      for (int r = 0; r < R; ++r) {
-        if (row0 + r >= a.rows) continue;
-        const float m0 = s[2 * r] * inv, m1 = s[2 * r + 1] * inv;
+    for (int r = 0; r < R; ++r) {
+      if (r >= rows) break;
+      const float rstd = stat[2 * r + 1];
+      const float c0 = -s[2 * r] * inv * rstd, c1 = -s[2 * r + 1] * inv * rstd * rstd * rstd;
+      T* dst = (T*)a.y + (row + r) * a.ys;
 #pragma unroll
-        for (int j = 0; j < NV; ++j) {
-          const int v = t + j * threads;
-          if (v >= nvec) continue;
-          float f[VEC];
-#pragma unroll
-          for (int k = 0; k < VEC; ++k) {
-            const float xh = (to_f(x[r][j].v[k]) - mean[r]) * rstd[r];
-            f[k] = (to_f(g[r][j].v[k]) * w[j][k] - m0 - xh * m1) * rstd[r];
-          }
-          store_pack<T, VEC>((T*)a.y + (row0 + r) * a.ys + (long long)v * VEC, f);
-        }
-      }
+      for (int j = 0; j < NV; ++j)
+        if (t + j * threads < a.dim)
+          dst[t + j * threads] = from_f<T>(fmaf(g[r][j] * w[j], rstd, fmaf(d[r][j], c1, c0)));
     }
   }
+  next_may_launch();
   if (!a.part) return;
   float* out = a.part + (long long)blockIdx.x * 2 * a.dim;
-  if (blockDim.y > 1) {
-    // the groups' sums in group order
-    for (int y = 0; y < (int)blockDim.y; ++y) {
-      if (group == y) {
-#pragma unroll
-        for (int j = 0; j < NV; ++j) {
-          const int v = t + j * threads;
-          if (v >= nvec) continue;
-#pragma unroll
-          for (int k = 0; k < VEC; ++k) {
-            const int c = v * VEC + k;
-            cols[c] = (y ? cols[c] : 0.f) + dw[j][k];
-            cols[a.dim + c] = (y ? cols[a.dim + c] : 0.f) + db[j][k];
-          }
-        }
-      }
-      __syncthreads();
-    }
-    for (int c = group * threads + t; c < 2 * a.dim; c += threads * blockDim.y) out[c] = cols[c];
-  } else {
+  // the groups' sums in group order, through the rows' memory
+  float* cols = reinterpret_cast<float*>(slots);
+  asm volatile("cp.async.wait_group 0;" ::: "memory");
+  for (int y = 0; y < (int)blockDim.y; ++y) {
+    __syncthreads();
+    if (group != y) continue;
+    float* dst = y + 1 < (int)blockDim.y ? cols : out;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      const int v = t + j * threads;
-      if (v >= nvec) continue;
-#pragma unroll
-      for (int k = 0; k < VEC; ++k) {
-        out[v * VEC + k] = dw[j][k];
-        out[a.dim + v * VEC + k] = db[j][k];
-      }
+      const int c = t + j * threads;
+      if (c >= a.dim) continue;
+      dst[c] = (y ? cols[c] : 0.f) + dw[j];
+      dst[a.dim + c] = (y ? cols[a.dim + c] : 0.f) + db[j];
     }
   }
 }
@@ -696,9 +711,9 @@ struct RowPlan {
   int groups;   // of a CTA
 };
 
-// vec: elements per access; groups fill a CTA of up to `most` threads.  The
+// vec: elements per access; groups fill a CTA of up to kMaxThreads.  The
 // fewest accesses per thread that leave at most a quarter of those without work.
-RowPlan plan_rows(long long dim, int vec, int most) {
+RowPlan plan_rows(long long dim, int vec) {
   const int max_nv = vec == 1 ? 16 : 4;
   const long long nvec = dim / vec;
   RowPlan best{0, 0, 1};
@@ -707,8 +722,8 @@ RowPlan plan_rows(long long dim, int vec, int most) {
     const long long threads = ((nvec + nv - 1) / nv + 31) / 32 * 32;
     if (threads > kMaxThreads) continue;
     RowPlan p{nv, (int)threads, 0};
-    p.groups = std::max(1, std::min(8, most / p.threads));
-    const double share = (double)nvec * p.groups / ((double)nv * most);
+    p.groups = std::max(1, std::min(8, kMaxThreads / p.threads));
+    const double share = (double)nvec * p.groups / ((double)nv * kMaxThreads);
     if (share > best_share) {
       best = p;
       best_share = share;
@@ -744,6 +759,32 @@ template <typename K> cudaError_t raise_smem(K kernel, std::atomic<unsigned long
   const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
   if (e == cudaSuccess) raised.fetch_or(bit, std::memory_order_release);
   return e;
+}
+
+// Shared memory of the kernels for any rows, and how many of their CTAs an SM
+// gets (at most two: more would leave more partial rows to add).
+size_t any_smem(const RowPlan& p, long long dim, int size, int arrays) {
+  return (size_t)p.groups * kStages * scalar_rows(p) * arrays * slot_bytes((int)dim, size);
+}
+int any_ctas(const RowPlan& p, size_t smem) {
+  return smem <= 100 * 1024 && p.nv == 4 ? 2 : 1;
+}
+
+template <typename T, int NV, int R>
+cudaError_t launch_forward_any(const RowsArgs& a, const RowPlan& p, unsigned grid, size_t smem, int device, cudaStream_t st) {
+  static std::atomic<unsigned long long> raised{0};
+  const cudaError_t e = raise_smem(k_norm_forward_any<T, NV, R>, raised, device, 220 * 1024);
+  if (e != cudaSuccess) return e;
+  k_norm_forward_any<T, NV, R><<<grid, dim3(p.threads, p.groups), smem, st>>>(a);
+  return cudaGetLastError();
+}
+template <typename T, int NV, int R>
+cudaError_t launch_backward_any(const RowsArgs& a, const RowPlan& p, unsigned grid, size_t smem, int device, cudaStream_t st) {
+  static std::atomic<unsigned long long> raised{0};
+  const cudaError_t e = raise_smem(k_norm_backward_any<T, NV, R>, raised, device, 220 * 1024);
+  if (e != cudaSuccess) return e;
+  k_norm_backward_any<T, NV, R><<<grid, dim3(p.threads, p.groups), smem, st>>>(a);
+  return cudaGetLastError();
 }
 
 template <typename T, int NV, int R>
@@ -862,7 +903,7 @@ extern "C" int psgd_layernorm_forward(psgd_layernorm* h, const void* x, psgd_dty
              (int)param_dtype, eps};
   const int full = 16 / dtype_size(dtype);
   const bool vec = h->dim % full == 0 && vec_ok(x, x_stride, dtype) && vec_ok(y, y_stride, dtype);
-  const RowPlan p = plan_rows(h->dim, vec ? full : 1, vec ? kMaxThreads : 256);
+  const RowPlan p = plan_rows(h->dim, vec ? full : 1);
   cudaError_t e = cudaSuccess;
   by_dtype(dtype, [&](auto* tt) {
     using T = std::remove_pointer_t<decltype(tt)>;
@@ -871,18 +912,18 @@ extern "C" int psgd_layernorm_forward(psgd_layernorm* h, const void* x, psgd_dty
       e = cudaGetLastError();
     } else if (vec) {
       const bool few = rows < (long long)h->sms * 8 * p.groups;
-      const long long per = (long long)p.groups * vec_rows(p, 2, few);
-      const unsigned grid = (unsigned)std::min<long long>((rows + per - 1) / per, h->sms * (p.nv == 1 ? 2 : 1));
-      with_vec_plan<2>(p, few, [&](auto nv, auto r) {
+      const long long per = (long long)p.groups * vec_rows(p, 4, few);
+      const unsigned grid = (unsigned)std::min<long long>((rows + per - 1) / per, h->sms * (p.nv == 1 && few ? 2 : 1));
+      with_vec_plan<4>(p, few, [&](auto nv, auto r) {
         e = launch_forward<T, decltype(nv)::value, decltype(r)::value>(a, p, grid, h->device, st);
       });
     } else {
       const long long per = (long long)p.groups * scalar_rows(p);
-      const unsigned grid = (unsigned)std::min<long long>((rows + per - 1) / per, (long long)h->sms * std::max(1, 1024 / (p.threads * p.groups)));
+      const size_t smem = any_smem(p, h->dim, (int)sizeof(T), 1);
+      const unsigned grid = (unsigned)std::min<long long>((rows + per - 1) / per, h->sms * any_ctas(p, smem));
       with_scalar_plan(p, [&](auto nv, auto r) {
-        k_norm_forward<T, 1, decltype(nv)::value, decltype(r)::value><<<grid, dim3(p.threads, p.groups), 0, st>>>(a);
+        e = launch_forward_any<T, decltype(nv)::value, decltype(r)::value>(a, p, grid, smem, h->device, st);
       });
-      e = cudaGetLastError();
     }
   });
   return e == cudaSuccess ? PSGD_OK : cuda_fail(who, e);
@@ -920,7 +961,7 @@ extern "C" int psgd_layernorm_backward(psgd_layernorm* h, const void* grad, int6
   const int full = 16 / dtype_size(dtype);
   const bool vec = h->dim % full == 0 && vec_ok(x, x_stride, dtype) && vec_ok(grad, grad_stride, dtype) &&
                    vec_ok(dx, dx_stride, dtype);
-  const RowPlan p = plan_rows(h->dim, vec ? full : 1, vec ? kMaxThreads : 256);
+  const RowPlan p = plan_rows(h->dim, vec ? full : 1);
   int parts = 0;
   cudaError_t e = cudaSuccess;
   if (rows > 0)
@@ -942,14 +983,11 @@ extern "C" int psgd_layernorm_backward(psgd_layernorm* h, const void* grad, int6
         });
       } else {
         const long long per = (long long)p.groups * scalar_rows(p);
-        parts = (int)std::min<long long>((rows + per - 1) / per,
-                                         (long long)h->sms * std::min(4, std::max(1, 1024 / (p.threads * p.groups))));
-        const size_t smem = p.groups > 1 ? (size_t)h->dim * 8 : 0;
+        const size_t smem = any_smem(p, h->dim, (int)sizeof(T), 2);
+        parts = (int)std::min<long long>((rows + per - 1) / per, h->sms * any_ctas(p, smem));
         with_scalar_plan(p, [&](auto nv, auto r) {
-          k_norm_backward<T, 1, decltype(nv)::value, decltype(r)::value>
-              <<<(unsigned)parts, dim3(p.threads, p.groups), smem, st>>>(a);
+          e = launch_backward_any<T, decltype(nv)::value, decltype(r)::value>(a, p, (unsigned)parts, smem, h->device, st);
         });
-        e = cudaGetLastError();
       }
     });
   if (e == cudaSuccess && params) {

@@ -145,6 +145,7 @@ class Embedding:
         check(self._lib.psgd_embedding_create(self.num_embeddings, self.embedding_dim, self.max_tokens,
                                               self.device.index, ctypes.byref(handle)))
         self._h = handle
+        self._forward, self._backward = self._lib.psgd_embedding_forward, self._lib.psgd_embedding_backward
 
     def close(self):
         if getattr(self, "_h", None) and self._h.value:
@@ -188,10 +189,16 @@ class Embedding:
         shape = (*shape, self.embedding_dim)
         if out is None:
             out = _new(shape, out_dtype or weight.dtype, self.device, stream)
-        od, oos, ois = self._token_rows(out, shape, "out")
-        check(self._lib.psgd_embedding_forward(
+            od, oos, ois = _DTYPE.get(out.dtype), inner * self.embedding_dim, self.embedding_dim
+            if od is None:
+                raise ValueError(f"out_dtype must be float32, float16 or bfloat16, got {out.dtype}")
+        else:
+            od, oos, ois = self._token_rows(out, shape, "out")
+        rc = self._forward(
             self._h, weight.data_ptr(), wd, ws, ids.data_ptr(), bits, outer, inner, os, is_, self.scale,
-            out.data_ptr(), od, oos, ois, _stream(stream, self._index)))
+            out.data_ptr(), od, oos, ois, _stream(stream, self._index))
+        if rc:
+            check(rc)
         return out
 
     def backward(self, ids, grad, out=None, accumulate=False, stream=None):
@@ -207,9 +214,11 @@ class Embedding:
                 raise ValueError("accumulate needs an out to add to")
             out = _new(self._shape, torch.float32, self.device, stream)
         wd, ws = self._table(out, "out")
-        check(self._lib.psgd_embedding_backward(
+        rc = self._backward(
             self._h, ids.data_ptr(), bits, outer, inner, os, is_, grad.data_ptr(), gd, gos, gis, self.scale,
-            self._padding, 1 if accumulate else 0, out.data_ptr(), wd, ws, _stream(stream, self._index)))
+            self._padding, 1 if accumulate else 0, out.data_ptr(), wd, ws, _stream(stream, self._index))
+        if rc:
+            check(rc)
         return out
 
     def status(self, stream=None):
@@ -227,12 +236,14 @@ class LayerNorm:
 
     def __init__(self, normalized_size, eps=1e-5, device=None):
         self.dim, self.eps = int(normalized_size), float(eps)
+        self._shape = (self.dim,)
         self.device = _device(device)
         self._index = self.device.index
         self._lib = _lib.lib()
         handle = ctypes.c_void_p()
         check(self._lib.psgd_layernorm_create(self.dim, self.device.index, ctypes.byref(handle)))
         self._h = handle
+        self._forward, self._backward = self._lib.psgd_layernorm_forward, self._lib.psgd_layernorm_backward
 
     def close(self):
         if getattr(self, "_h", None) and self._h.value:
@@ -249,11 +260,11 @@ class LayerNorm:
         """(type, addresses) of two optional vectors of one type."""
         d = pa = pb = None
         if a is not None:
-            if a.shape != (self.dim,) or not a.is_contiguous():
+            if a.shape != self._shape or not a.is_contiguous():
                 raise ValueError(f"{name_a} must be a contiguous vector of {self.dim} elements")
             d, pa = _dtype(a, self._index, name_a), a.data_ptr()
         if b is not None:
-            if b.shape != (self.dim,) or not b.is_contiguous():
+            if b.shape != self._shape or not b.is_contiguous():
                 raise ValueError(f"{name_b} must be a contiguous vector of {self.dim} elements")
             e, pb = _dtype(b, self._index, name_b), b.data_ptr()
             if d is not None and d != e:
@@ -278,18 +289,26 @@ class LayerNorm:
 
     def forward(self, x, weight=None, bias=None, out=None, stream=None):
         """(y, mean, rstd); mean and rstd (fp32, one a row) are what backward takes."""
-        xd = _dtype(x, self._index, "x")
+        index, device = self._index, self.device
+        xd = _dtype(x, index, "x")
         rows, xs = _rows(x, self.dim, "x")
         pd, w, b = self._pair(weight, bias, "weight", "bias")
         if out is None:
             out, ys = _new_like(x, stream), self.dim
         else:
             ys = self._like(out, x, "out")
-        lead = x.shape[:-1]
-        mean, rstd = _new(lead, torch.float32, self.device, stream), _new(lead, torch.float32, self.device, stream)
-        check(self._lib.psgd_layernorm_forward(
+        shape = x.shape
+        lead = (shape[0],) if len(shape) == 2 else shape[:-1]
+        if stream is None:
+            mean, rstd = (torch.empty(lead, dtype=torch.float32, device=device),
+                          torch.empty(lead, dtype=torch.float32, device=device))
+        else:
+            mean, rstd = _new(lead, torch.float32, device, stream), _new(lead, torch.float32, device, stream)
+        rc = self._forward(
             self._h, x.data_ptr(), xd, xs, rows, w, b, pd, self.eps, out.data_ptr(), ys, mean.data_ptr(),
-            rstd.data_ptr(), _stream(stream, self._index)))
+            rstd.data_ptr(), _stream(stream, index))
+        if rc:
+            check(rc)
         return out, mean, rstd
 
     def backward(self, grad, x, mean, rstd, weight=None, dx=None, dweight=None, dbias=None, accumulate=False,
@@ -315,9 +334,11 @@ class LayerNorm:
             if dbias is None:
                 dbias = _new((self.dim,), dtype, self.device, stream)
         od, dw, db = self._pair(dweight, dbias, "dweight", "dbias")
-        check(self._lib.psgd_layernorm_backward(
+        rc = self._backward(
             self._h, grad.data_ptr(), gs, x.data_ptr(), xd, xs, rows, m, r, w, pd, dx.data_ptr(), ds, dw, db, od,
-            1 if accumulate else 0, _stream(stream, self._index)))
+            1 if accumulate else 0, _stream(stream, self._index))
+        if rc:
+            check(rc)
         return dx, dweight, dbias
 
     def workspace_bytes(self):
