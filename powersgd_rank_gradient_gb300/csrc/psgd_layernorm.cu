@@ -387,30 +387,42 @@ __global__ void __launch_bounds__(kMaxThreads, 1) k_norm_backward_vec(RowsArgs a
 // columns t, t + threads, ... (NV of them).  A barrier of the group follows
 // each wait, as a granule is used by other threads than the one that copied it.
 //
-// Starts the copy of row `index` of an array: granule t, t + threads, ... into
+// Starts the copy of row `index` of an array: granule u, u + step, ... into
 // `slot`.  The bytes in front of a row within its first granule are the array's
 // own where the row begins that far into it; elsewhere there may be nothing to
 // read, and the granule's elements are copied one by one.
 template <typename T>
-__device__ __forceinline__ void copy_row(unsigned char* slot, const T* base, int index, long long stride, int dim, int t,
-                                         int threads) {
+__device__ __forceinline__ void copy_row(unsigned char* slot, const T* base, int index, long long stride, int dim, int u,
+                                         int step) {
   const T* row = base + index * stride;
   const int before = (int)((uintptr_t)row & 15);
-  const bool first = index * stride * (long long)sizeof(T) < before;
   const int bytes = before + dim * (int)sizeof(T);
   const unsigned char* src = (const unsigned char*)row - before;
-  for (int o = t * 16; o < bytes; o += threads * 16) {
-    if (first && o == 0) {
-      for (int e = before; e < min(16, bytes); e += (int)sizeof(T))
-        *(T*)(slot + e) = *(const T*)(src + e);
-    } else {
-      const int n = min(16, bytes - o);
-      asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"((unsigned)__cvta_generic_to_shared(slot + o)),
-                   "l"(src + o), "r"(n)
-                   : "memory");
-    }
+  if (u == 0 && index * stride * (long long)sizeof(T) < before) {
+    for (int e = before; e < min(16, bytes); e += (int)sizeof(T)) *(T*)(slot + e) = *(const T*)(src + e);
+    u += step;
+  }
+  unsigned to = (unsigned)__cvta_generic_to_shared(slot) + u * 16;
+  src += u * 16;
+  for (int left = bytes - u * 16; left > 0; left -= step * 16) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(src), "r"(min(16, left)) : "memory");
+    to += step * 16;
+    src += step * 16;
   }
 }
+
+// How the warps of a group share the copies of `items` rows: warp w takes the
+// items first, first + step, ..., and of each the granules of part `part` of
+// `parts`.
+struct CopyShare {
+  int first, step, part, parts;
+  __device__ __forceinline__ CopyShare(int items, int warps, int warp) {
+    parts = warps >= items ? warps / items : 1;
+    first = parts > 1 ? warp / parts : warp;
+    part = parts > 1 ? warp - first * parts : 0;
+    step = parts > 1 ? items : warps;  // (with parts, warps that are left over have first >= items)
+  }
+};
 // Bytes of a row's place in shared memory.
 __host__ __device__ inline int slot_bytes(int dim, int size) { return (dim * size + 15 + 15) / 16 * 16; }
 
@@ -430,11 +442,11 @@ __global__ void __launch_bounds__(kMaxThreads, NV == 4 ? 2 : 1) k_norm_forward_a
   const float inv = 1.f / (float)a.dim;
   const int step = gridDim.x * blockDim.y * R;
   int row = ((int)blockIdx.x * blockDim.y + group) * R, ahead = row;
+  const CopyShare share(R, warps, warp);
   auto issue = [&](int stage) {
-#pragma unroll
-    for (int r = 0; r < R; ++r)
+    for (int r = share.first; r < R; r += share.step)
       if (ahead + r < (int)a.rows)
-        copy_row(mine + (stage * R + r) * slot, (const T*)a.x, ahead + r, a.xs, a.dim, t, threads);
+        copy_row(mine + (stage * R + r) * slot, (const T*)a.x, ahead + r, a.xs, a.dim, share.part * 32 + lane, share.parts * 32);
     commit_copies();
     ahead = ahead < (int)a.rows ? ahead + step : ahead;
   };
@@ -506,13 +518,12 @@ __global__ void __launch_bounds__(kMaxThreads, NV == 4 ? 2 : 1) k_norm_backward_
   const float inv = 1.f / (float)a.dim;
   const int step = gridDim.x * blockDim.y * R;
   int row = ((int)blockIdx.x * blockDim.y + group) * R, ahead = row;
+  const CopyShare share(2 * R, warps, warp);
   auto issue = [&](int stage) {
-#pragma unroll
-    for (int r = 0; r < R; ++r)
-      if (ahead + r < (int)a.rows) {
-        copy_row(mine + (stage * R + r) * 2 * slot, (const T*)a.x, ahead + r, a.xs, a.dim, t, threads);
-        copy_row(mine + ((stage * R + r) * 2 + 1) * slot, (const T*)a.g, ahead + r, a.gs, a.dim, t, threads);
-      }
+    for (int i = share.first; i < 2 * R; i += share.step)
+      if (ahead + i / 2 < (int)a.rows)
+        copy_row(mine + (stage * 2 * R + i) * slot, (const T*)(i & 1 ? a.g : a.x), ahead + i / 2, i & 1 ? a.gs : a.xs,
+                 a.dim, share.part * 32 + lane, share.parts * 32);
     if (t < 2 * R && ahead + t / 2 < (int)a.rows) copy4(&stats[stage][group][t], (t & 1 ? a.rstd : a.mean) + ahead + t / 2);
     commit_copies();
     ahead = ahead < (int)a.rows ? ahead + step : ahead;
