@@ -383,8 +383,7 @@ __global__ void __launch_bounds__(kMaxThreads, 1) k_norm_backward_vec(RowsArgs a
 
 // The kernels for rows of any length and alignment.  A row's aligned 16-byte
 // granules are copied ahead into shared memory at the row's own place within
-// its first granule, and read from there element by element: thread t owns the
-// columns t, t + threads, ... (NV of them).  A barrier of the group follows
+// its first granule, and read from there element by element.  A barrier of the group follows
 // each wait, as a granule is used by other threads than the one that copied it.
 //
 // Starts the copy of row `index` of an array: granule u, u + step, ... into
@@ -423,22 +422,43 @@ struct CopyShare {
     step = parts > 1 ? items : warps;  // (with parts, warps that are left over have first >= items)
   }
 };
-// Bytes of a row's place in shared memory.
-__host__ __device__ inline int slot_bytes(int dim, int size) { return (dim * size + 15 + 15) / 16 * 16; }
+// Bytes of a row's place in shared memory: `columns` elements (the columns of
+// all threads) from any place of the first granule on.
+__host__ __device__ inline int slot_bytes(int columns, int size) { return (columns * size + 15 + 15) / 16 * 16; }
+
+// `a` where `keep` is not 0, else 0 (not a product: what lies behind a row may
+// be anything).
+__device__ __forceinline__ F2 only(F2 a, F2 keep) {
+  float x, y, k, l;
+  split(a, x, y);
+  split(keep, k, l);
+  return f2(k != 0.f ? x : 0.f, l != 0.f ? y : 0.f);
+}
 
 __device__ __forceinline__ void group_barrier(int group, int threads) {
   asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "r"(threads) : "memory");
 }
 
+// Where in its first granule row `index` of an array begins, in bytes.
+__device__ __forceinline__ int row_phase(const void* base, int index, long long stride, int size) {
+  return ((unsigned)(uintptr_t)base + (unsigned)index * ((unsigned)stride * (unsigned)size)) & 15;
+}
+// Elements 0 and 32 from a place in a row in shared memory, as a pair; they may
+// lie behind the row's end, where the slot's last bytes are read.
+template <typename T> __device__ __forceinline__ F2 pair_at(const T* row) { return f2(to_f(row[0]), to_f(row[32])); }
+
 template <typename T, int NV, int R>
 __global__ void __launch_bounds__(kMaxThreads, NV == 4 ? 2 : 1) k_norm_forward_any(RowsArgs a) {
+  constexpr int NP = NV / 2;  // pairs of columns
   extern __shared__ __align__(16) unsigned char slots[];
   __shared__ float red[2][kMaxThreads / 32 * R];
   const int t = threadIdx.x, group = threadIdx.y, threads = blockDim.x;
   const int warps = threads / 32, warp = t >> 5, lane = t & 31;
   float* buf[2] = {red[0] + group * warps * R, red[1] + group * warps * R};
-  const int slot = slot_bytes(a.dim, sizeof(T));
-  unsigned char* mine = slots + (size_t)group * kStages * R * slot;
+  // a warp owns 32 NV columns, lane by lane: first, first + 32, ...; `left` of them and of what follows are in the row
+  const int first = warp * 32 * NV + lane, left = a.dim - warp * 32 * NV;
+  const int slot = slot_bytes(threads * NV, sizeof(T));
+  unsigned char* mine = slots + group * kStages * R * slot;
   const float inv = 1.f / (float)a.dim;
   const int step = gridDim.x * blockDim.y * R;
   int row = ((int)blockIdx.x * blockDim.y + group) * R, ahead = row;
@@ -452,69 +472,98 @@ __global__ void __launch_bounds__(kMaxThreads, NV == 4 ? 2 : 1) k_norm_forward_a
   };
 #pragma unroll
   for (int k = 0; k < kStages - 1; ++k) issue(k);
-  float w[NV], bias[NV];
+  F2 w[NP], bias[NP], keep[NP];  // keep: 1 in a column of the row, 0 behind its end
 #pragma unroll
-  for (int j = 0; j < NV; ++j) {
-    float v[1];
-    load_param<1>(a.w, a.pdtype, t + j * threads, t + j * threads < a.dim, 1.f, v);
-    w[j] = v[0];
-    load_param<1>(a.b, a.pdtype, t + j * threads, t + j * threads < a.dim, 0.f, v);
-    bias[j] = v[0];
+  for (int j = 0; j < NP; ++j) {
+    float v[2], u[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int c = first + (2 * j + i) * 32;
+      float one[1];
+      load_param<1>(a.w, a.pdtype, c, c < a.dim, 1.f, one);
+      v[i] = one[0];
+      load_param<1>(a.b, a.pdtype, c, c < a.dim, 0.f, one);
+      u[i] = one[0];
+    }
+    w[j] = f2(v[0], v[1]);
+    bias[j] = f2(u[0], u[1]);
+    keep[j] = f2(first + 2 * j * 32 < a.dim ? 1.f : 0.f, first + (2 * j + 1) * 32 < a.dim ? 1.f : 0.f);
   }
+  T* to = (T*)a.y + row * a.ys + first;
+  const long long to_step = step * a.ys;
   int stage = 0;
-  for (; row < (int)a.rows; row += step) {
+  for (; row < (int)a.rows; row += step, to += to_step) {
     asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
     group_barrier(group, threads);
     issue(stage == 0 ? kStages - 1 : stage - 1);
-    float x[R][NV], s[R], mean[R];
+    const int rows = min(R, (int)a.rows - row);
+    F2 x[R][NP];
+    float s[R], mean[R];
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-      s[r] = 0.f;
-      const T* src = (const T*)(mine + (stage * R + r) * slot + ((uintptr_t)((const T*)a.x + (row + r) * a.xs) & 15));
+      const T* src = (const T*)(mine + (stage * R + r) * slot + row_phase(a.x, row + r, a.xs, sizeof(T))) + first;
+      F2 sum = f2(0.f, 0.f);
 #pragma unroll
-      for (int j = 0; j < NV; ++j) {
-        x[r][j] = row + r < (int)a.rows && t + j * threads < a.dim ? to_f(src[t + j * threads]) : 0.f;
-        s[r] += x[r][j];
+      for (int j = 0; j < NP; ++j) {
+        x[r][j] = pair_at(src + 2 * j * 32);
+        if ((2 * j + 2) * 32 > left) x[r][j] = only(x[r][j], keep[j]);
+        sum = add(sum, x[r][j]);
       }
+      float u, v;
+      split(sum, u, v);
+      s[r] = u + v;
     }
     stage = stage + 1 == kStages ? 0 : stage + 1;
     group_sum<R>(s, buf[0], warps, warp, lane, group, threads);
 #pragma unroll
     for (int r = 0; r < R; ++r) {
       mean[r] = s[r] * inv;
-      s[r] = 0.f;
+      const F2 nm = f2(-mean[r], -mean[r]);
+      F2 sum = f2(0.f, 0.f);
 #pragma unroll
-      for (int j = 0; j < NV; ++j) {
-        x[r][j] -= mean[r];
-        if (t + j * threads < a.dim) s[r] = fmaf(x[r][j], x[r][j], s[r]);
+      for (int j = 0; j < NP; ++j) {
+        x[r][j] = add(x[r][j], nm);
+        if ((2 * j + 2) * 32 > left) x[r][j] = only(x[r][j], keep[j]);
+        sum = fma(x[r][j], x[r][j], sum);
       }
+      float u, v;
+      split(sum, u, v);
+      s[r] = u + v;
     }
     group_sum<R>(s, buf[1], warps, warp, lane, group, threads);
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-      if (row + r >= (int)a.rows) break;
+      if (r >= rows) break;
       const float rstd = rsqrtf(fmaf(s[r], inv, a.eps));
       if (t == 0) {
         if (a.mean) a.mean[row + r] = mean[r];
         if (a.rstd) a.rstd[row + r] = rstd;
       }
-      T* dst = (T*)a.y + (row + r) * a.ys;
+      const F2 rs = f2(rstd, rstd);
+      T* dst = to + r * a.ys;
 #pragma unroll
-      for (int j = 0; j < NV; ++j)
-        if (t + j * threads < a.dim) dst[t + j * threads] = from_f<T>(fmaf(x[r][j] * rstd, w[j], bias[j]));
+      for (int j = 0; j < NP; ++j) {
+        float u, v;
+        split(fma(mul(x[r][j], rs), w[j], bias[j]), u, v);
+        if (lane + 2 * j * 32 < left) dst[2 * j * 32] = from_f<T>(u);
+        if (lane + (2 * j + 1) * 32 < left) dst[(2 * j + 1) * 32] = from_f<T>(v);
+      }
     }
   }
 }
 
 template <typename T, int NV, int R>
 __global__ void __launch_bounds__(kMaxThreads, NV == 4 ? 2 : 1) k_norm_backward_any(RowsArgs a) {
+  constexpr int NP = NV / 2;
   extern __shared__ __align__(16) unsigned char slots[];
   __shared__ float red[2][kMaxThreads / 32 * 2 * R];
   __shared__ float stats[kStages][kMaxThreads / 32][2 * R];  // a group's
   const int t = threadIdx.x, group = threadIdx.y, threads = blockDim.x;
   const int warps = threads / 32, warp = t >> 5, lane = t & 31;
-  const int slot = slot_bytes(a.dim, sizeof(T));
-  unsigned char* mine = slots + (size_t)group * kStages * R * 2 * slot;
+  // a warp owns 32 NV columns, lane by lane: first, first + 32, ...; `left` of them and of what follows are in the row
+  const int first = warp * 32 * NV + lane, left = a.dim - warp * 32 * NV;
+  const int slot = slot_bytes(threads * NV, sizeof(T));
+  unsigned char* mine = slots + group * kStages * R * 2 * slot;
   const float inv = 1.f / (float)a.dim;
   const int step = gridDim.x * blockDim.y * R;
   int row = ((int)blockIdx.x * blockDim.y + group) * R, ahead = row;
@@ -530,41 +579,60 @@ __global__ void __launch_bounds__(kMaxThreads, NV == 4 ? 2 : 1) k_norm_backward_
   };
 #pragma unroll
   for (int k = 0; k < kStages - 1; ++k) issue(k);
-  float dw[NV], db[NV], w[NV];
+  F2 dw[NP], db[NP], w[NP], keep[NP];
 #pragma unroll
-  for (int j = 0; j < NV; ++j) {
-    float v[1];
-    load_param<1>(a.w, a.pdtype, t + j * threads, t + j * threads < a.dim, 1.f, v);
-    w[j] = v[0];
-    dw[j] = db[j] = 0.f;
+  for (int j = 0; j < NP; ++j) {
+    float v[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int c = first + (2 * j + i) * 32;
+      float one[1];
+      load_param<1>(a.w, a.pdtype, c, c < a.dim, 1.f, one);
+      v[i] = one[0];
+    }
+    w[j] = f2(v[0], v[1]);
+    dw[j] = db[j] = f2(0.f, 0.f);
+    keep[j] = f2(first + 2 * j * 32 < a.dim ? 1.f : 0.f, first + (2 * j + 1) * 32 < a.dim ? 1.f : 0.f);
   }
+  T* to = (T*)a.y + row * a.ys + first;
+  const long long to_step = step * a.ys;
   int stage = 0, flip = 0;
-  for (; row < (int)a.rows; row += step) {
+  for (; row < (int)a.rows; row += step, to += to_step) {
     asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
     group_barrier(group, threads);
     issue(stage == 0 ? kStages - 1 : stage - 1);
     const float* stat = stats[stage][group];
     const int rows = min(R, (int)a.rows - row);
-    float d[R][NV], g[R][NV], s[2 * R];
+    F2 d[R][NP], g[R][NP];
+    float s[2 * R];
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-      s[2 * r] = s[2 * r + 1] = 0.f;
-      if (r >= rows) continue;
-      const unsigned char* at = mine + (stage * R + r) * 2 * slot;
-      const T* x = (const T*)(at + ((uintptr_t)((const T*)a.x + (row + r) * a.xs) & 15));
-      const T* y = (const T*)(at + slot + ((uintptr_t)((const T*)a.g + (row + r) * a.gs) & 15));
-      const float mean = stat[2 * r], rstd = stat[2 * r + 1];
+      F2 s0 = f2(0.f, 0.f), s1 = f2(0.f, 0.f);
+      if (r < rows) {
+        const unsigned char* at = mine + (stage * R + r) * 2 * slot;
+        const T* x = (const T*)(at + row_phase(a.x, row + r, a.xs, sizeof(T))) + first;
+        const T* y = (const T*)(at + slot + row_phase(a.g, row + r, a.gs, sizeof(T))) + first;
+        const F2 nm = f2(-stat[2 * r], -stat[2 * r]), rs = f2(stat[2 * r + 1], stat[2 * r + 1]);
 #pragma unroll
-      for (int j = 0; j < NV; ++j) {
-        const bool in = t + j * threads < a.dim;
-        d[r][j] = in ? to_f(x[t + j * threads]) - mean : 0.f;
-        g[r][j] = in ? to_f(y[t + j * threads]) : 0.f;
-        const float gd = g[r][j] * d[r][j];
-        s[2 * r] = fmaf(g[r][j], w[j], s[2 * r]);
-        s[2 * r + 1] = fmaf(gd, w[j], s[2 * r + 1]);
-        dw[j] = fmaf(gd, rstd, dw[j]);
-        db[j] += g[r][j];
+        for (int j = 0; j < NP; ++j) {
+          d[r][j] = add(pair_at(x + 2 * j * 32), nm);
+          g[r][j] = pair_at(y + 2 * j * 32);
+          if ((2 * j + 2) * 32 > left) {
+            d[r][j] = only(d[r][j], keep[j]);
+            g[r][j] = only(g[r][j], keep[j]);
+          }
+          const F2 gd = mul(g[r][j], d[r][j]);
+          s0 = fma(g[r][j], w[j], s0);
+          s1 = fma(gd, w[j], s1);
+          dw[j] = fma(gd, rs, dw[j]);
+          db[j] = add(db[j], g[r][j]);
+        }
       }
+      float u, v;
+      split(s0, u, v);
+      s[2 * r] = u + v;
+      split(s1, u, v);
+      s[2 * r + 1] = u + v;
     }
     stage = stage + 1 == kStages ? 0 : stage + 1;
     if (!a.y) continue;
@@ -575,11 +643,15 @@ __global__ void __launch_bounds__(kMaxThreads, NV == 4 ? 2 : 1) k_norm_backward_
       if (r >= rows) break;
       const float rstd = stat[2 * r + 1];
       const float c0 = -s[2 * r] * inv * rstd, c1 = -s[2 * r + 1] * inv * rstd * rstd * rstd;
-      T* dst = (T*)a.y + (row + r) * a.ys;
+      const F2 rs = f2(rstd, rstd), k0 = f2(c0, c0), k1 = f2(c1, c1);
+      T* dst = to + r * a.ys;
 #pragma unroll
-      for (int j = 0; j < NV; ++j)
-        if (t + j * threads < a.dim)
-          dst[t + j * threads] = from_f<T>(fmaf(g[r][j] * w[j], rstd, fmaf(d[r][j], c1, c0)));
+      for (int j = 0; j < NP; ++j) {
+        float u, v;
+        split(fma(mul(g[r][j], w[j]), rs, fma(d[r][j], k1, k0)), u, v);
+        if (lane + 2 * j * 32 < left) dst[2 * j * 32] = from_f<T>(u);
+        if (lane + (2 * j + 1) * 32 < left) dst[(2 * j + 1) * 32] = from_f<T>(v);
+      }
     }
   }
   next_may_launch();
@@ -594,10 +666,13 @@ __global__ void __launch_bounds__(kMaxThreads, NV == 4 ? 2 : 1) k_norm_backward_
     float* dst = y + 1 < (int)blockDim.y ? cols : out;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      const int c = t + j * threads;
+      const int c = first + j * 32;
       if (c >= a.dim) continue;
-      dst[c] = (y ? cols[c] : 0.f) + dw[j];
-      dst[a.dim + c] = (y ? cols[a.dim + c] : 0.f) + db[j];
+      float u[2], v[2];
+      split(dw[j / 2], u[0], u[1]);
+      split(db[j / 2], v[0], v[1]);
+      dst[c] = (y ? cols[c] : 0.f) + u[j & 1];
+      dst[a.dim + c] = (y ? cols[a.dim + c] : 0.f) + v[j & 1];
     }
   }
 }
@@ -727,9 +802,10 @@ struct RowPlan {
 RowPlan plan_rows(long long dim, int vec) {
   const int max_nv = vec == 1 ? 16 : 4;
   const long long nvec = dim / vec;
+  const int min_nv = vec == 1 ? 4 : 1;
   RowPlan best{0, 0, 1};
   double best_share = 0.0;
-  for (int nv = vec == 1 ? 4 : 1; nv <= max_nv; nv *= 2) {
+  for (int nv = min_nv; nv <= max_nv; nv *= 2) {
     const long long threads = ((nvec + nv - 1) / nv + 31) / 32 * 32;
     if (threads > kMaxThreads) continue;
     RowPlan p{nv, (int)threads, 0};
@@ -774,8 +850,8 @@ template <typename K> cudaError_t raise_smem(K kernel, std::atomic<unsigned long
 
 // Shared memory of the kernels for any rows, and how many of their CTAs an SM
 // gets (at most two: more would leave more partial rows to add).
-size_t any_smem(const RowPlan& p, long long dim, int size, int arrays) {
-  return (size_t)p.groups * kStages * scalar_rows(p) * arrays * slot_bytes((int)dim, size);
+size_t any_smem(const RowPlan& p, int size, int arrays) {
+  return (size_t)p.groups * kStages * scalar_rows(p) * arrays * slot_bytes(p.threads * p.nv, size);
 }
 int any_ctas(const RowPlan& p, size_t smem) {
   return smem <= 100 * 1024 && p.nv == 4 ? 2 : 1;
@@ -930,7 +1006,7 @@ extern "C" int psgd_layernorm_forward(psgd_layernorm* h, const void* x, psgd_dty
       });
     } else {
       const long long per = (long long)p.groups * scalar_rows(p);
-      const size_t smem = any_smem(p, h->dim, (int)sizeof(T), 1);
+      const size_t smem = any_smem(p, (int)sizeof(T), 1);
       const unsigned grid = (unsigned)std::min<long long>((rows + per - 1) / per, h->sms * any_ctas(p, smem));
       with_scalar_plan(p, [&](auto nv, auto r) {
         e = launch_forward_any<T, decltype(nv)::value, decltype(r)::value>(a, p, grid, smem, h->device, st);
@@ -994,7 +1070,7 @@ extern "C" int psgd_layernorm_backward(psgd_layernorm* h, const void* grad, int6
         });
       } else {
         const long long per = (long long)p.groups * scalar_rows(p);
-        const size_t smem = any_smem(p, h->dim, (int)sizeof(T), 2);
+        const size_t smem = any_smem(p, (int)sizeof(T), 2);
         parts = (int)std::min<long long>((rows + per - 1) / per, h->sms * any_ctas(p, smem));
         with_scalar_plan(p, [&](auto nv, auto r) {
           e = launch_backward_any<T, decltype(nv)::value, decltype(r)::value>(a, p, (unsigned)parts, smem, h->device, st);
