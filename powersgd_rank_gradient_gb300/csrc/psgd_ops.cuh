@@ -172,31 +172,15 @@ __device__ __forceinline__ void store_any(void* p, int dtype, long long i, float
   else ((__nv_bfloat16*)p)[i] = __float2bfloat16_rn(v);
 }
 
-// Two fp32 lanes of one register pair: one instruction for both.
+// Two floats in one register pair: one instruction for both.
 struct F2 {
-  unsigned long long v;
+  float2 p;
 };
-__device__ __forceinline__ F2 f2(float x, float y) {
-  F2 r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(x), "f"(y));
-  return r;
-}
-__device__ __forceinline__ void split(F2 a, float& x, float& y) { asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(a.v)); }
-__device__ __forceinline__ F2 add(F2 a, F2 b) {
-  F2 r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
-  return r;
-}
-__device__ __forceinline__ F2 fma(F2 a, F2 b, F2 c) {
-  F2 r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
-  return r;
-}
-__device__ __forceinline__ F2 mul(F2 a, F2 b) {
-  F2 r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
-  return r;
-}
+__device__ __forceinline__ F2 f2(float x, float y) { F2 r; r.p = make_float2(x, y); return r; }
+__device__ __forceinline__ void split(F2 a, float& x, float& y) { x = a.p.x; y = a.p.y; }
+__device__ __forceinline__ F2 add(F2 a, F2 b) { F2 r; r.p = __fadd2_rn(a.p, b.p); return r; }
+__device__ __forceinline__ F2 fma(F2 a, F2 b, F2 c) { F2 r; r.p = __ffma2_rn(a.p, b.p, c.p); return r; }
+__device__ __forceinline__ F2 mul(F2 a, F2 b) { F2 r; r.p = __fmul2_rn(a.p, b.p); return r; }
 
 // 16 bytes of elements as pairs of floats.
 template <typename T> __device__ __forceinline__ void to_pairs(const uint4& u, F2* f);
