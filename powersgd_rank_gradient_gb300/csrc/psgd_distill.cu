@@ -47,6 +47,8 @@ struct DistillArgs {
   int vocab, k;
   int tdtype, index64;
   float temperature, scale;
+  float inv_t;  // 1 / temperature
+  float c;      // log2(e) / temperature
 };
 
 __device__ __forceinline__ float exp2_fast(float x) {
@@ -92,7 +94,7 @@ __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.w
 // softmax p[k].  Returns whether the row counts at all.
 __device__ __forceinline__ bool teacher_softmax(const DistillArgs& a, long long row, float w, float* p, int* at,
                                                 float* buf) {
-  const float inv_t = 1.f / a.temperature;
+  const float inv_t = a.inv_t;
   float m = -INFINITY;
   bool mass = false;
   for (int k = threadIdx.x; k < a.k; k += blockDim.x) {
@@ -164,7 +166,7 @@ __host__ __device__ constexpr int table_slots(int k) {
 // its indices are equal (bit 1).
 __device__ __forceinline__ int teacher_warp(const DistillArgs& a, long long row, float* p, int* at, int* table) {
   const int lane = threadIdx.x & 31;
-  const float inv_t = 1.f / a.temperature;
+  const float inv_t = a.inv_t;
   const int slots = table_slots(a.k);
   for (int i = lane; i < slots; i += 32) table[i] = -1;
   __syncwarp();
@@ -243,7 +245,8 @@ __device__ __forceinline__ float cluster_join(float v, float2* peers, int ctas, 
 // gradient's rows start at the same place of a granule as the logits' do, so
 // whole granules are stored.
 template <typename Z, bool ALIGNED>
-__global__ void __launch_bounds__(kDistillThreads + 32, 2) k_distill_chip(DistillArgs a, int ctas, int slice_granules) {
+__global__ void __launch_bounds__(kDistillThreads + 32, 2) k_distill_chip(DistillArgs a, int log_ctas, int slice_granules,
+                                                                         int per) {
   constexpr int NE = Vec16<Z>::N;
   constexpr int NP = NE / 2;
   constexpr int U = NE == 8 ? 2 : 4;  // granules a thread takes at a time
@@ -259,13 +262,14 @@ __global__ void __launch_bounds__(kDistillThreads + 32, 2) k_distill_chip(Distil
   const int threads = blockDim.x - 32;  // of the row's warps
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, warps = threads >> 5;
   const bool entries = warp == warps;
-  const long long row = blockIdx.x / ctas;
-  const int rank = blockIdx.x - (int)row * ctas;
+  const int ctas = 1 << log_ctas;
+  const int row = blockIdx.x >> log_ctas, rank = blockIdx.x & (ctas - 1);
   const Z* z = (const Z*)a.z + row * a.zs;
   Z* dz = a.dz ? (Z*)a.dz + row * a.dzs : nullptr;
   const int head = (int)(((uintptr_t)z & 15) / sizeof(Z));  // elements of the first granule before the row
   const int granules = (head + a.vocab + NE - 1) / NE;
-  const int g0 = (int)((long long)granules * rank / ctas), n = (int)((long long)granules * (rank + 1) / ctas) - g0;
+  // (a row's granules times 8 fit 32 bits: its CTAs hold at most 8 x 224 KB of them)
+  const int g0 = granules * rank >> log_ctas, n = (granules * (rank + 1) >> log_ctas) - g0;
   // granules of the slice that lie inside the row: [whole0, whole0 + whole)
   const int whole0 = max(0, (head ? 1 : 0) - g0);
   const unsigned whole = (unsigned)max(0, min(n, (head + a.vocab) / NE - g0) - whole0);
@@ -298,14 +302,13 @@ __global__ void __launch_bounds__(kDistillThreads + 32, 2) k_distill_chip(Distil
     return;
   }
 
-  const float c = kLog2e / a.temperature;
+  const float c = a.c;
   if (entries) {
     const int state = teacher_warp(a, row, p, at, table);
     if (lane == 0) state_shared = state;
   } else {
     // The slice is copied by the threads that will use it (granule tid, tid +
-    // threads, ...), in kStages groups of copies that are all under way at once.
-    const int per = ((n + threads - 1) / threads + kStages - 1) / kStages;  // granules per thread and stage
+    // threads, ...), in kStages groups of `per` copies that are all under way at once.
 #pragma unroll
     for (int q = 0; q < kStages; ++q) {
       const int last = min(n, (q + 1) * per * threads);
@@ -495,7 +498,7 @@ template <typename Z> __global__ void __launch_bounds__(kDistillThreads) k_disti
       for (int j = tid; j < a.vocab; j += kDistillThreads) dz[j] = from_f<Z>(0.f);
     return;
   }
-  const float c = kLog2e / a.temperature;
+  const float c = a.c;
   float r = -INFINITY, s = 0.f;
   for (int j = tid; j < a.vocab; j += kDistillThreads) {
     const float v = to_f(z[j]);
@@ -540,6 +543,7 @@ template <typename Z> __global__ void __launch_bounds__(kDistillThreads) k_disti
 // the row's warps, granules of a slice, shared memory with the entries'.
 struct RowPlan {
   int ctas;
+  int log_ctas;
   int threads;
   int granules;
   size_t smem;
@@ -548,11 +552,12 @@ struct RowPlan {
 RowPlan plan_row(long long vocab, int size, int k, long long rows, int sms) {
   const long long extra = 12LL * k + 4LL * table_slots(k) + 16;
   const long long bytes = vocab * size + 32;  // with both ends' granules
-  RowPlan p{1, kDistillThreads, 0, 0};
+  RowPlan p{1, 0, kDistillThreads, 0, 0};
   while (p.ctas < kMaxCluster && bytes / p.ctas + extra > kHalfSmem) p.ctas *= 2;
-  if (bytes / p.ctas + extra > kFullSmem) return RowPlan{0, kDistillThreads, 0, 0};
+  if (bytes / p.ctas + extra > kFullSmem) return RowPlan{0, 0, kDistillThreads, 0, 0};
   // few rows: more CTAs a row, as long as each keeps a few granules per thread
   while (p.ctas < kMaxCluster && rows * p.ctas * 2 <= sms && bytes / p.ctas >= 16 * 1024) p.ctas *= 2;
+  while (1 << p.log_ctas < p.ctas) ++p.log_ctas;
   p.granules = (int)(bytes / 16 / p.ctas + 2);
   p.smem = (size_t)p.granules * 16 + extra;
   const int most = p.smem > 72 * 1024 ? kDistillThreads : kDistillThreads / 2;  // three and more slices to an SM: 256 each
@@ -580,7 +585,8 @@ template <typename Z, bool ALIGNED> cudaError_t launch_chip(const DistillArgs& a
   attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = p.ctas > 1 ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, k_distill_chip<Z, ALIGNED>, a, p.ctas, p.granules);
+  const int per = ((p.granules + p.threads - 1) / p.threads + kStages - 1) / kStages;  // granules per thread and group of copies
+  return cudaLaunchKernelEx(&cfg, k_distill_chip<Z, ALIGNED>, a, p.log_ctas, p.granules, per);
 }
 
 template <typename Z> cudaError_t launch_distill(const DistillArgs& a, int device, int sms, cudaStream_t st) {
@@ -646,7 +652,8 @@ extern "C" int psgd_distill(const void* logits, psgd_dtype dtype, int64_t logits
       overlap(losses, rows * 4, weights, rows * 4))
     return fail(PSGD_EINVAL, "psgd_distill: an output overlaps another operand (dlogits may be logits itself)");
   DistillArgs a{logits, logits_stride, teacher, teacher_stride, index, index_stride, weights, dlogits, dlogits_stride,
-                losses, rows, (int)vocab, k, (int)teacher_dtype, index_bits == 64, temperature, grad_scale};
+                losses, rows, (int)vocab, k, (int)teacher_dtype, index_bits == 64, temperature, grad_scale, 1.f / temperature,
+                kLog2e / temperature};
   DeviceScope scope(device);
   const cudaStream_t st = (cudaStream_t)stream;
   const int sms = sm_count(device);
