@@ -130,6 +130,14 @@ at::Tensor fresh(at::IntArrayRef shape, at::ScalarType type, int index) {
   return at::empty(shape, at::TensorOptions().dtype(type).device(at::kCUDA, static_cast<c10::DeviceIndex>(index)));
 }
 
+// A contiguous tensor of `shape` in the memory of `t`, `offset` elements in.
+at::Tensor part_of(const at::Tensor& t, at::IntArrayRef shape, int64_t offset) {
+  at::Tensor p = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(t.storage()), t.key_set(), t.dtype());
+  p.unsafeGetTensorImpl()->set_storage_offset(offset);
+  p.unsafeGetTensorImpl()->set_sizes_contiguous(shape);
+  return p;
+}
+
 void* stream_of(int index) { return c10::cuda::getCurrentCUDAStream(static_cast<c10::DeviceIndex>(index)).stream(); }
 
 // Raises the library's error of a failed call, as every other binding does.
@@ -382,7 +390,9 @@ PyObject* py_layernorm_forward(PyObject*, PyObject* const* a, Py_ssize_t n) {
       ys = stride_like(s, out, x, "out");
     }
     const auto lead = x.sizes().slice(0, x.sizes().size() - 1);
-    at::Tensor mean = fresh(lead, at::kFloat, s.index), rstd = fresh(lead, at::kFloat, s.index);
+    // one allocation for both statistics
+    const at::Tensor stats = fresh({2 * r.rows}, at::kFloat, s.index);
+    at::Tensor mean = part_of(stats, lead, 0), rstd = part_of(stats, lead, r.rows);
     void* stream = stream_of(s.index);
     check(call([&] {
       return psgd_layernorm_forward(static_cast<psgd_layernorm*>(s.handle), x.const_data_ptr(), d, r.stride, r.rows,

@@ -491,6 +491,169 @@ __global__ void __launch_bounds__(256, VEC == 1 ? 2 : 4) k_row_sums(const int* _
   }
 }
 
+// The whole gradient in one launch, for few tokens: each CTA owns `span` rows of
+// the table, looks at every token's id itself, and lists the tokens of its rows
+// by row and position.  A row of up to kAlone tokens is summed by one group of
+// threads, the others by all groups, each over a contiguous part of the row's
+// tokens.  blockDim = (threads of a group, groups).  Shared memory: per token a
+// byte and two integers, and the groups' partial sums.
+constexpr int kAlone = 16;
+constexpr int kMaxSpan = 32;
+
+__host__ __device__ inline int direct_bytes(int n) { return (n + 15) / 16 * 16; }
+
+template <typename G, typename O, int VEC, int NV>
+__global__ void __launch_bounds__(512) k_rows_direct(const void* __restrict__ ids, int id64, Layout2 il, int n, int vocab,
+                                                     long long padding, int* flag, const G* __restrict__ grad, Layout2 gl,
+                                                     int dim, float scale, int accumulate, O* __restrict__ dw,
+                                                     long long stride, int dw_aligned, int span) {
+  constexpr int kBatch = VEC == 8 ? 4 : 8;
+  extern __shared__ __align__(16) unsigned char mark[];  // row within the span, 255: another's token
+  __shared__ int count[kMaxSpan], first[kMaxSpan + 1], warp_total[16];
+  int* found = reinterpret_cast<int*>(mark + direct_bytes(n));  // position | row << 16, by position
+  int* list = found + n;                                        // positions, by row and position
+  float* sums = reinterpret_cast<float*>(list + n);
+  const int threads = blockDim.x, groups = blockDim.y, group = threadIdx.y;
+  const int all = threads * groups, t = group * threads + threadIdx.x, lane = t & 31, warp = t >> 5, warps = all >> 5;
+  const int base = blockIdx.x * span, rows = min(span, vocab - base);
+  if (t < kMaxSpan) count[t] = 0;
+  __syncthreads();
+  for (int i0 = t; i0 < n; i0 += all * 8) {
+    long long id[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) id[k] = i0 + k * all < n ? load_id(ids, id64, il.at(i0 + k * all)) : padding;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      if (i0 + k * all >= n) break;
+      const bool mine = id[k] >= base && id[k] < base + rows && id[k] != padding;
+      mark[i0 + k * all] = mine ? (unsigned char)(id[k] - base) : 255;
+      if (mine) atomicAdd(&count[id[k] - base], 1);
+      if ((id[k] < 0 || id[k] >= vocab) && blockIdx.x == 0) *flag = 1;
+    }
+  }
+  __syncthreads();
+  // first place of each row in the list (one warp's scan)
+  if (warp == 0) {
+    const int c = count[lane];
+    int inc = c;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += v;
+    }
+    first[lane] = inc - c;
+    if (lane == 31) first[32] = inc;
+  }
+  __syncthreads();
+  const int total = first[kMaxSpan];
+  if (total > 0) {
+    // the tokens found, by position: each thread's share of the marks in order
+    const int share = ((n + all - 1) / all + 3) / 4 * 4, b = min(n, t * share), e = min(n, b + share);
+    int mine = 0;
+    for (int i = b; i < e; ++i) mine += mark[i] != 255;
+    int inc = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += v;
+    }
+    if (lane == 31) warp_total[warp] = inc;
+    __syncthreads();
+    int at = inc - mine;
+    for (int w = 0; w < warp; ++w) at += warp_total[w];
+    if (mine)
+      for (int i = b; i < e; ++i)
+        if (mark[i] != 255) found[at++] = i | mark[i] << 16;
+    __syncthreads();
+    // then by row, one warp keeping the order within each
+    if (warp == 0) {
+      for (int i0 = 0; i0 < total; i0 += 32) {
+        const int v = i0 + lane < total ? found[i0 + lane] : -1;
+        const int row = v >= 0 ? v >> 16 : kMaxSpan;
+        const unsigned same = __match_any_sync(0xffffffffu, row);
+        const int ahead = __popc(same & ((1u << lane) - 1));
+        int start = 0;
+        if (v >= 0) start = first[row];
+        __syncwarp();
+        if (v >= 0) {
+          list[start + ahead] = v & 0xffff;
+          if (ahead == 0) first[row] = start + __popc(same);  // (ends at the row's end)
+        }
+        __syncwarp();
+      }
+    }
+    __syncthreads();
+  }
+  const int c0 = (blockIdx.y * threads * NV + threadIdx.x) * VEC, step = threads * VEC;
+  float acc[NV][VEC];
+  auto clear = [&]() {
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) acc[j][i] = 0.f;
+  };
+  // adds the tokens list[b, e) in order
+  auto sum = [&](int b, int e) {
+    for (int i0 = b; i0 < e; i0 += kBatch) {
+      Pack<G, VEC> v[kBatch][NV];
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) {
+        if (i0 + k >= e) continue;
+        const G* src = grad + gl.at(list[i0 + k]);
+#pragma unroll
+        for (int j = 0; j < NV; ++j)
+          if (c0 + j * step < dim) v[k][j] = load_pack<G, VEC>(src + c0 + j * step);
+      }
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) {
+        if (i0 + k >= e) continue;
+#pragma unroll
+        for (int j = 0; j < NV; ++j)
+#pragma unroll
+          for (int i = 0; i < VEC; ++i) acc[j][i] += to_f(v[k][j].v[i]);
+      }
+    }
+  };
+  auto write = [&](int u) {
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+      if (c0 + j * step < dim)
+        write_row<O, VEC>(dw + (long long)(base + u) * stride + c0 + j * step, acc[j], scale, accumulate, dw_aligned);
+  };
+  // (first[u] is now the end of row u's tokens)
+  for (int u = group; u < rows; u += groups) {
+    const int m = count[u];
+    if (m > kAlone || (m == 0 && accumulate)) continue;
+    clear();
+    sum(first[u] - m, first[u]);
+    write(u);
+  }
+  if (total <= kAlone) return;
+  for (int u = 0; u < rows; ++u) {
+    const int m = count[u];
+    if (m <= kAlone) continue;  // the same for the whole CTA
+    const int b = first[u] - m;
+    clear();
+    sum(b + (int)((long long)m * group / groups), b + (int)((long long)m * (group + 1) / groups));
+    if (groups > 1) {
+      __syncthreads();
+#pragma unroll
+      for (int j = 0; j < NV; ++j)
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) sums[(group * NV * VEC + j * VEC + i) * threads + threadIdx.x] = acc[j][i];
+      __syncthreads();
+      if (group == 0) {
+        for (int g = 1; g < groups; ++g)
+#pragma unroll
+          for (int j = 0; j < NV; ++j)
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) acc[j][i] += sums[(g * NV * VEC + j * VEC + i) * threads + threadIdx.x];
+      }
+    }
+    if (group == 0) write(u);
+  }
+}
+
 // The rows that cross a chunk's end, as listed by the chunks where they begin:
 // (chunk, id, chunks that follow), those of at most kFewParts partials from the
 // list's front, the others from its back.  A row's partials are added in chunk
@@ -646,6 +809,18 @@ TilePlan plan_tile(long long dim, int vec) {
   p.groups = std::max(1, 128 / p.threads);
   p.tiles = (int)((dim + p.threads * per - 1) / (p.threads * per));
   return p;
+}
+
+// Rows of the table per CTA of the one-launch gradient, or 0 where the sorted
+// one is used: every CTA looks at all ids, and a row's tokens are not split
+// over CTAs.  GPU time of one launch against the sorted three, 1024 fp32
+// columns: 16 tokens of a 300-row table 3.6 and 7.5 us, 512 7.5 and 10.6, 2048
+// 19.1 and 16.1; 256 tokens of 30522 rows 24.3 and 28.0 (with 640 bf16 columns
+// 17.3 and 15.1).
+int direct_span(int n, int vocab) {
+  if (n > 1024 || n > 16LL * vocab) return 0;
+  const int span = std::min(kMaxSpan, (vocab + 1215) / 1216);
+  return (long long)((vocab + span - 1) / span) * n <= (1 << 18) ? span : 0;
 }
 
 int check_ids(const char* who, const psgd_embedding* e, const void* ids, int32_t id_bits, int64_t outer, int64_t inner,
@@ -838,6 +1013,36 @@ extern "C" int psgd_embedding_backward(psgd_embedding* h, const void* ids, int32
       k_zero_table<<<(unsigned)std::min<long long>((vocab + 7) / 8, h->sms * 8), 256, 0, st>>>(
           (char*)dweight, vocab, (long long)dim * osize, dweight_stride * osize);
     e = cudaGetLastError();
+  } else if (const int span = direct_span(n, vocab)) {
+    by_dtype(grad_dtype, [&](auto* gt) {
+      using G = std::remove_pointer_t<decltype(gt)>;
+      return by_dtype(dweight_dtype, [&](auto* ot) {
+        using O = std::remove_pointer_t<decltype(ot)>;
+        constexpr int V = Vec16<G>::N;
+        const bool vec = dim % V == 0 && aligned_rows(grad, grad_outer_stride, grad_inner_stride, sizeof(G), 16);
+        const int dw_aligned = aligned_rows(dweight, dweight_stride, 0, sizeof(O), run_alignment(V, sizeof(O)));
+        const TilePlan p = plan_tile(dim, vec ? V : 1);
+        const int groups = std::min(8, 512 / p.threads);
+        const size_t smem = direct_bytes(n) + 8 * (size_t)n + (size_t)groups * p.threads * (vec ? V : kScalarNv) * 4;
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3((vocab + span - 1) / span, p.tiles);
+        cfg.blockDim = dim3(p.threads, groups);
+        cfg.dynamicSmemBytes = smem;
+        cfg.stream = st;
+        auto kernel = vec ? k_rows_direct<G, O, V, 1> : k_rows_direct<G, O, 1, kScalarNv>;
+        static std::atomic<unsigned long long> raised[2];  // devices whose shared-memory limit is raised
+        const unsigned long long bit = 1ull << h->device;
+        if (!(raised[vec].load(std::memory_order_acquire) & bit)) {
+          e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 100 * 1024);
+          if (e == cudaSuccess) raised[vec].fetch_or(bit, std::memory_order_release);
+        }
+        if (e == cudaSuccess)
+          e = cudaLaunchKernelEx(&cfg, kernel, ids, (int)(id_bits == 64), il, n, vocab, (long long)padding_idx, h->d_flag,
+                                 (const G*)grad, gl, dim, scale, (int)accumulate, (O*)dweight, (long long)dweight_stride,
+                                 dw_aligned, span);
+        return 0;
+      });
+    });
   } else {
     const bool wide = vocab > 256 && vocab <= 1024 && n <= (1 << 18);  // one pass of 10 bits; a CTA's counts fit 16
     int passes = 1;

@@ -178,6 +178,14 @@ def test_grad_large():
     run_grad(50257, 1600, (4, 1024), BF16, BF16, 9, iddtype=torch.int32, offset=1)
 
 
+@pytest.mark.parametrize("vocab", [1, 33, 300, 512, 1217, 2500, 30522, 50257])
+@pytest.mark.parametrize("tokens,hot", [(1, 0), (15, 0.5), (17, 1.0), (100, 0.9), (1000, 0.3), (4096, 0.05), (8192, 0.6)])
+def test_grad_few_tokens(vocab, tokens, hot):
+    """One launch or the sorted list, rows of one token and of most of them."""
+    run_grad(vocab, 24, (tokens,), BF16, F32, vocab, hot=hot, padding=vocab - 1 if vocab > 1 else None, offset=3)
+    run_grad(vocab, 17, (tokens,), F32, F16, vocab, hot=hot, accumulate=True)
+
+
 def test_grad_many_tokens():
     run_grad(5000, 8, (300, 1001), F16, F32, 4, hot=0.05)
     run_grad(1000, 4, (300, 1001), F16, F32, 5, hot=0.9)
@@ -221,6 +229,22 @@ def test_grad_out_of_range_ids_add_nothing_and_are_reported():
     dw, mag, count = tu.table_grad(ids, grad, 10, 1.0)
     tu.check(out, dw, tu.table_grad_tol(dw, mag, count, F32))
     assert e.status() and not e.status()
+
+
+@pytest.mark.parametrize("bad", [-1, 10, 2**32, -2**31])
+@pytest.mark.parametrize("tokens", [9, 5000])
+def test_grad_reports_a_single_bad_id(bad, tokens):
+    for padding in (None, 4):
+        e = embedding(10, 8, tokens, padding_idx=padding)
+        ids = make_ids((tokens,), 10, 1)
+        grad = randn((tokens, 8), F32, 2)
+        e.backward(ids, grad)
+        assert not e.status()
+        ids[tokens // 2] = bad
+        out = e.backward(ids, grad)
+        dw, mag, count = tu.table_grad(ids, grad, 10, 1.0, padding)
+        tu.check(out, dw, tu.table_grad_tol(dw, mag, count, F32))
+        assert e.status()
 
 
 def test_grad_keeps_nonfinite_rows_apart():
