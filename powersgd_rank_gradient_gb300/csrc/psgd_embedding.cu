@@ -24,6 +24,7 @@ struct psgd_embedding {
   int device = 0;
   int sms = 0;
   long long vocab = 0, dim = 0, max_tokens = 0;
+  void* memory = nullptr;  // all of the following
   // the sorted tokens: two (key, position) buffers the radix passes alternate between
   int* key[2] = {nullptr, nullptr};
   int* pos[2] = {nullptr, nullptr};
@@ -33,7 +34,6 @@ struct psgd_embedding {
   unsigned char* named = nullptr;  // per row of the table: a token names it
   int* ready = nullptr;            // the map is complete (0 between calls)
   int* d_flag = nullptr;  // an id outside [0, vocab) was seen
-  int* h_flag = nullptr;  // pinned
   size_t bytes = 0;
 };
 
@@ -72,48 +72,34 @@ __device__ __forceinline__ long long load_id(const void* ids, int id64, long lon
   return id64 ? __ldg((const long long*)ids + at) : (long long)__ldg((const int*)ids + at);
 }
 
-constexpr int kLookup = 2;
-
-// A group of threads (blockDim = (threads of a group, groups)) takes kLookup
-// tokens at a time, so that as many row loads are in flight per thread; thread
-// t owns the vectors t, t + threads, ... (NV of them) of a tile of columns.
+// A group of threads (blockDim = (threads of a group, groups)) takes one token;
+// thread t owns the vectors t, t + threads, ... (NV of them) of a tile of
+// columns, all of them under way at once.  What finding a token's row costs is
+// paid once per NV vectors.
 template <typename W, typename O, int VEC, int NV>
-__global__ void __launch_bounds__(256, VEC == 8 ? 6 : 8) k_lookup(const W* __restrict__ weight, long long wstride, long long vocab,
+__global__ void __launch_bounds__(256) k_lookup(const W* __restrict__ weight, long long wstride, long long vocab,
                                                 int dim, const void* __restrict__ ids, int id64, Layout2 il, int n,
                                                 float scale, O* __restrict__ out, Layout2 ol, int* flag) {
-  constexpr int T = kLookup;
   const int c0 = (blockIdx.y * blockDim.x * NV + threadIdx.x) * VEC, step = blockDim.x * VEC;
-  const long long i0 = ((long long)blockIdx.x * blockDim.y + threadIdx.y) * T;
-  if (i0 < n) {
-    long long id[T];
-    bool ok[T];
+  const long long token = (long long)blockIdx.x * blockDim.y + threadIdx.y;
+  if (token >= n) return;
+  const int i = (int)token;
+  const long long id = load_id(ids, id64, il.at(i));
+  const bool ok = id >= 0 && id < vocab;
+  if (!ok && threadIdx.x == 0) *flag = 1;
+  const W* src = weight + (ok ? id : 0) * wstride + c0;
+  O* dst = out + ol.at(i) + c0;
+  Pack<W, VEC> v[NV];
 #pragma unroll
-    for (int k = 0; k < T; ++k) {
-      id[k] = i0 + k < n ? load_id(ids, id64, il.at((int)i0 + k)) : 0;
-      ok[k] = id[k] >= 0 && id[k] < vocab;
-      if (!ok[k] && threadIdx.x == 0) *flag = 1;
-    }
-    Pack<W, VEC> v[T][NV];
+  for (int j = 0; j < NV; ++j)
+    if (c0 + j * step < dim) v[j] = load_pack<W, VEC>(src + j * step);
 #pragma unroll
-    for (int k = 0; k < T; ++k) {
-      const W* src = weight + (ok[k] ? id[k] : 0) * wstride;
+  for (int j = 0; j < NV; ++j) {
+    if (c0 + j * step >= dim) continue;
+    float f[VEC];
 #pragma unroll
-      for (int j = 0; j < NV; ++j)
-        if (c0 + j * step < dim) v[k][j] = load_pack<W, VEC>(src + c0 + j * step);
-    }
-#pragma unroll
-    for (int k = 0; k < T; ++k) {
-      if (i0 + k >= n) break;
-      O* dst = out + ol.at((int)i0 + k);
-#pragma unroll
-      for (int j = 0; j < NV; ++j) {
-        if (c0 + j * step >= dim) continue;
-        float f[VEC];
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) f[e] = ok[k] ? to_f(v[k][j].v[e]) * scale : 0.f;
-        store_run<O, VEC>(dst + c0 + j * step, f);
-      }
-    }
+    for (int e = 0; e < VEC; ++e) f[e] = ok ? to_f(v[j].v[e]) * scale : 0.f;
+    store_run<O, VEC>(dst + j * step, f);
   }
 }
 
@@ -801,12 +787,12 @@ constexpr int kScalarNv = 4;  // elements per thread and row where accesses are 
 struct TilePlan {
   int threads, groups, tiles;
 };
-TilePlan plan_tile(long long dim, int vec) {
-  const long long per = vec > 1 ? vec : kScalarNv;  // elements per thread
+TilePlan plan_tile(long long dim, int vec, int nv = 1) {
+  const long long per = vec > 1 ? vec * nv : kScalarNv;  // elements per thread
   const long long want = ((dim + per - 1) / per + 31) / 32 * 32;
   TilePlan p;
   p.threads = (int)std::min<long long>(256, want);
-  p.groups = std::max(1, 128 / p.threads);
+  p.groups = std::max(1, 256 / p.threads);
   p.tiles = (int)((dim + p.threads * per - 1) / (p.threads * per));
   return p;
 }
@@ -883,30 +869,37 @@ extern "C" int psgd_embedding_create(int64_t vocab, int64_t dim, int64_t max_tok
   e = cudaDeviceGetAttribute(&h->sms, cudaDevAttrMultiProcessorCount, device);
   const long long n = std::max<long long>(1, max_tokens);
   const long long chunks = max_chunks(n, h->sms);
-  auto alloc = [&](void** p, long long bytes) {
-    if (e != cudaSuccess) return;
-    e = cudaMalloc(p, (size_t)bytes);
-    if (e == cudaSuccess) h->bytes += (size_t)bytes;
-    else *p = nullptr;
+  // one allocation, cut into 256-byte aligned parts
+  long long bytes = 0;
+  auto part = [&](long long size) {
+    const long long at = bytes;
+    bytes += (size + 255) / 256 * 256;
+    return at;
   };
-  for (int i = 0; i < 2; ++i) {
-    alloc((void**)&h->key[i], n * 4);
-    alloc((void**)&h->pos[i], n * 4);
-  }
-  alloc((void**)&h->part, chunks * 2 * dim * 4);
-  alloc((void**)&h->crossing, chunks * 16);
-  alloc((void**)&h->counts, 12);
-  alloc((void**)&h->named, (vocab + 15) / 16 * 16);
-  alloc((void**)&h->ready, 4);
-  if (e == cudaSuccess) e = cudaMemset(h->ready, 0, 4);
-  alloc((void**)&h->d_flag, 4);
-  if (e == cudaSuccess) e = cudaMemset(h->d_flag, 0, 4);
-  if (e == cudaSuccess) e = cudaMallocHost((void**)&h->h_flag, 4);
+  const long long words = part(16), key0 = part(n * 4), key1 = part(n * 4), pos0 = part(n * 4), pos1 = part(n * 4),
+                  sums = part(chunks * 2 * dim * 4), crossing = part(chunks * 16), counts = part(12),
+                  named = part((vocab + 15) / 16 * 16);
+  if (e == cudaSuccess) e = cudaMalloc(&h->memory, (size_t)bytes);
+  if (e != cudaSuccess) h->memory = nullptr;
+  if (e == cudaSuccess) e = cudaMemset(h->memory, 0, 16);
+  if (e == cudaSuccess) e = cudaStreamSynchronize(nullptr);  // before any stream may use the handle
   if (e != cudaSuccess) {
     const int rc = cuda_fail("psgd_embedding_create", e);
     psgd_embedding_destroy(h);
     return rc;
   }
+  char* base = (char*)h->memory;
+  h->bytes = (size_t)bytes;
+  h->d_flag = (int*)(base + words);
+  h->ready = h->d_flag + 1;
+  h->key[0] = (int*)(base + key0);
+  h->key[1] = (int*)(base + key1);
+  h->pos[0] = (int*)(base + pos0);
+  h->pos[1] = (int*)(base + pos1);
+  h->part = (float*)(base + sums);
+  h->crossing = (int4*)(base + crossing);
+  h->counts = (int*)(base + counts);
+  h->named = (unsigned char*)(base + named);
   *out = h;
   return PSGD_OK;
 }
@@ -915,17 +908,7 @@ extern "C" void psgd_embedding_destroy(psgd_embedding* h) {
   if (!h) return;
   {
     DeviceScope scope(h->device);
-    for (int i = 0; i < 2; ++i) {
-      if (h->key[i]) cudaFree(h->key[i]);
-      if (h->pos[i]) cudaFree(h->pos[i]);
-    }
-    if (h->part) cudaFree(h->part);
-    if (h->crossing) cudaFree(h->crossing);
-    if (h->counts) cudaFree(h->counts);
-    if (h->named) cudaFree(h->named);
-    if (h->ready) cudaFree(h->ready);
-    if (h->d_flag) cudaFree(h->d_flag);
-    if (h->h_flag) cudaFreeHost(h->h_flag);
+    if (h->memory) cudaFree(h->memory);
   }
   delete h;
 }
@@ -963,11 +946,15 @@ extern "C" int psgd_embedding_forward(psgd_embedding* h, const void* weight, psg
       const int align = run_alignment(V, sizeof(O));
       const bool vec = h->dim % V == 0 && aligned_rows(weight, weight_stride, 0, sizeof(W), 16) &&
                        aligned_rows(out, out_outer_stride, out_inner_stride, sizeof(O), align);
-      const TilePlan p = plan_tile(h->dim, vec ? V : 1);
-      const int tokens = kLookup * p.groups;
-      const dim3 grid((unsigned)((n + (long long)tokens - 1) / tokens), p.tiles);
+      // rows of 64 vectors and more: four of them to a thread
+      const bool wide = vec && h->dim >= 64 * V;
+      const TilePlan p = plan_tile(h->dim, vec ? V : 1, wide ? 4 : 1);
+      const dim3 grid((unsigned)((n + (long long)p.groups - 1) / p.groups), p.tiles);
       const dim3 block(p.threads, p.groups);
-      if (vec)
+      if (wide)
+        k_lookup<W, O, V, 4><<<grid, block, 0, st>>>((const W*)weight, weight_stride, h->vocab, (int)h->dim, ids,
+                                                     id_bits == 64, il, n, scale, (O*)out, ol, h->d_flag);
+      else if (vec)
         k_lookup<W, O, V, 1><<<grid, block, 0, st>>>((const W*)weight, weight_stride, h->vocab, (int)h->dim, ids,
                                                      id_bits == 64, il, n, scale, (O*)out, ol, h->d_flag);
       else
@@ -1102,9 +1089,10 @@ extern "C" int psgd_embedding_status(psgd_embedding* h, void* stream) {
   if (!h) return fail(PSGD_EINVAL, "psgd_embedding_status: NULL embedding");
   DeviceScope scope(h->device);
   const cudaStream_t st = (cudaStream_t)stream;
-  cudaError_t e = cudaMemcpyAsync(h->h_flag, h->d_flag, 4, cudaMemcpyDeviceToHost, st);
+  int flag = 0;
+  cudaError_t e = cudaMemcpyAsync(&flag, h->d_flag, 4, cudaMemcpyDeviceToHost, st);
   if (e == cudaSuccess) e = cudaMemsetAsync(h->d_flag, 0, 4, st);
   if (e == cudaSuccess) e = cudaStreamSynchronize(st);
   if (e != cudaSuccess) return cuda_fail("psgd_embedding_status", e);
-  return *h->h_flag ? PSGD_BAD_TOKEN : PSGD_OK;
+  return flag ? PSGD_BAD_TOKEN : PSGD_OK;
 }

@@ -945,7 +945,7 @@ extern "C" int psgd_layernorm_create(int64_t dim, int32_t device, psgd_layernorm
   h->dim = dim;
   e = cudaDeviceGetAttribute(&h->sms, cudaDevAttrMultiProcessorCount, device);
   if (e == cudaSuccess) {
-    h->max_ctas = h->sms * 4;
+    h->max_ctas = h->sms * 2;
     h->bytes = (size_t)h->max_ctas * 2 * dim * 4;
     e = cudaMalloc((void**)&h->part, h->bytes);
   }
