@@ -448,7 +448,7 @@ __device__ __forceinline__ int row_phase(const void* base, int index, long long 
 template <typename T> __device__ __forceinline__ F2 pair_at(const T* row) { return f2(to_f(row[0]), to_f(row[32])); }
 
 template <typename T, int NV, int R>
-__global__ void __launch_bounds__(kMaxThreads, NV == 4 ? 2 : 1) k_norm_forward_any(RowsArgs a) {
+__global__ void __launch_bounds__(kMaxThreads, 1) k_norm_forward_any(RowsArgs a) {
   constexpr int NP = NV / 2;  // pairs of columns
   extern __shared__ __align__(16) unsigned char slots[];
   __shared__ float red[2][kMaxThreads / 32 * R];
@@ -553,7 +553,7 @@ __global__ void __launch_bounds__(kMaxThreads, NV == 4 ? 2 : 1) k_norm_forward_a
 }
 
 template <typename T, int NV, int R>
-__global__ void __launch_bounds__(kMaxThreads, NV == 4 ? 2 : 1) k_norm_backward_any(RowsArgs a) {
+__global__ void __launch_bounds__(kMaxThreads, 1) k_norm_backward_any(RowsArgs a) {
   constexpr int NP = NV / 2;
   extern __shared__ __align__(16) unsigned char slots[];
   __shared__ float red[2][kMaxThreads / 32 * 2 * R];
@@ -802,7 +802,10 @@ struct RowPlan {
 RowPlan plan_rows(long long dim, int vec) {
   const int max_nv = vec == 1 ? 16 : 4;
   const long long nvec = dim / vec;
-  const int min_nv = vec == 1 ? 4 : 1;
+  // (single elements: 4 a thread and 4 rows at a time, or 8 and 2.  Backward,
+  // fp16: 1023 columns 51 us so and 45, 30001 rows; 333 columns 19 and 23, 20000
+  // rows)
+  const int min_nv = vec != 1 ? 1 : dim > 768 ? 8 : 4;
   RowPlan best{0, 0, 1};
   double best_share = 0.0;
   for (int nv = min_nv; nv <= max_nv; nv *= 2) {
@@ -833,11 +836,11 @@ template <int R1, typename F> void with_vec_plan(const RowPlan& p, bool few, F&&
 }
 int vec_rows(const RowPlan& p, int r1, bool few) { return p.nv == 1 ? (few ? 1 : r1) : p.nv == 2 ? 2 : 1; }
 template <typename F> void with_scalar_plan(const RowPlan& p, F&& f) {
-  if (p.nv == 4) f(Int<4>(), Int<2>());
-  else if (p.nv == 8) f(Int<8>(), Int<1>());
+  if (p.nv == 4) f(Int<4>(), Int<4>());
+  else if (p.nv == 8) f(Int<8>(), Int<2>());
   else f(Int<16>(), Int<1>());
 }
-int scalar_rows(const RowPlan& p) { return p.nv == 4 ? 2 : 1; }
+int scalar_rows(const RowPlan& p) { return 16 / p.nv; }
 
 // Raises a kernel's shared-memory limit, once per device.
 template <typename K> cudaError_t raise_smem(K kernel, std::atomic<unsigned long long>& raised, int device, int bytes) {
@@ -848,13 +851,9 @@ template <typename K> cudaError_t raise_smem(K kernel, std::atomic<unsigned long
   return e;
 }
 
-// Shared memory of the kernels for any rows, and how many of their CTAs an SM
-// gets (at most two: more would leave more partial rows to add).
+// Shared memory of the kernels for any rows, one CTA of which an SM gets.
 size_t any_smem(const RowPlan& p, int size, int arrays) {
   return (size_t)p.groups * kStages * scalar_rows(p) * arrays * slot_bytes(p.threads * p.nv, size);
-}
-int any_ctas(const RowPlan& p, size_t smem) {
-  return smem <= 100 * 1024 && p.nv == 4 ? 2 : 1;
 }
 
 template <typename T, int NV, int R>
@@ -1007,7 +1006,7 @@ extern "C" int psgd_layernorm_forward(psgd_layernorm* h, const void* x, psgd_dty
     } else {
       const long long per = (long long)p.groups * scalar_rows(p);
       const size_t smem = any_smem(p, (int)sizeof(T), 1);
-      const unsigned grid = (unsigned)std::min<long long>((rows + per - 1) / per, h->sms * any_ctas(p, smem));
+      const unsigned grid = (unsigned)std::min<long long>((rows + per - 1) / per, h->sms);
       with_scalar_plan(p, [&](auto nv, auto r) {
         e = launch_forward_any<T, decltype(nv)::value, decltype(r)::value>(a, p, grid, smem, h->device, st);
       });
@@ -1071,7 +1070,7 @@ extern "C" int psgd_layernorm_backward(psgd_layernorm* h, const void* grad, int6
       } else {
         const long long per = (long long)p.groups * scalar_rows(p);
         const size_t smem = any_smem(p, (int)sizeof(T), 2);
-        parts = (int)std::min<long long>((rows + per - 1) / per, h->sms * any_ctas(p, smem));
+        parts = (int)std::min<long long>((rows + per - 1) / per, h->sms);
         with_scalar_plan(p, [&](auto nv, auto r) {
           e = launch_backward_any<T, decltype(nv)::value, decltype(r)::value>(a, p, (unsigned)parts, smem, h->device, st);
         });
