@@ -244,6 +244,14 @@ __device__ __forceinline__ float cluster_join(float v, float2* peers, int ctas, 
 // softmax's sums, so neither waits for the other's loads.  ALIGNED: the
 // gradient's rows start at the same place of a granule as the logits' do, so
 // whole granules are stored.
+//
+// Two slices of about 100 KB to an SM (rows of more than that are cut over a
+// cluster), one CTA's loads and stores under the other's arithmetic.  8192 rows
+// of 50257 bf16 logits take 282 us (5.85 TB/s, 86 % of the copy bandwidth), 2458
+// rows of 30522 fp32 ones 104 us (5.5 TB/s, 81 %); with the logits read twice
+// from memory 995 and 202 us.  What is left is the instructions (about 16 an
+// element, the issue slots 60 % full) in the phases that both CTAs of an SM meet
+// in.  Few rows: a row over up to 8 CTAs, five rows of 50257 fp32 5.5 us.
 template <typename Z, bool ALIGNED>
 __global__ void __launch_bounds__(kDistillThreads + 32, 2) k_distill_chip(DistillArgs a, int log_ctas, int slice_granules,
                                                                          int per) {
@@ -481,8 +489,8 @@ __global__ void __launch_bounds__(kDistillThreads + 32, 2) k_distill_chip(Distil
       if (at[k] >= 0) dz[at[k]] = from_f<Z>(pm[k]);
 }
 
-// Rows larger than a cluster's shared memory: one CTA per row, which reads the
-// logits twice.
+// Rows larger than a cluster's shared memory (1.7 MB): one CTA per row, which
+// reads the logits twice, element by element: bound by its one SM's loads.
 template <typename Z> __global__ void __launch_bounds__(kDistillThreads) k_distill_long(DistillArgs a) {
   __shared__ float buf[kDistillWarps];
   __shared__ float p[PSGD_DISTILL_MAX_K];
