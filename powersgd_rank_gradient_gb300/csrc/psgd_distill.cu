@@ -640,8 +640,8 @@ extern "C" int psgd_distill(const void* logits, psgd_dtype dtype, int64_t logits
   if (rows < 0 || rows > 0xfffffff) return fail(PSGD_EINVAL, "psgd_distill: rows must be in [0, 2^28 - 1]");
   if (vocab < 1 || vocab > (1 << 30)) return fail(PSGD_EINVAL, "psgd_distill: vocab must be in [1, 2^30]");
   if (k < 1 || k > PSGD_DISTILL_MAX_K) return fail(PSGD_EINVAL, "psgd_distill: k must be in [1, PSGD_DISTILL_MAX_K]");
-  if (!(temperature > 0.f) || !isfinite(temperature))
-    return fail(PSGD_EINVAL, "psgd_distill: temperature must be finite and > 0");
+  if (!(temperature > 0.f) || !isfinite(temperature) || !isfinite(kLog2e / temperature))
+    return fail(PSGD_EINVAL, "psgd_distill: temperature must be finite and > 0, and so must its reciprocal");
   if (device < 0 || device >= 64) return fail(PSGD_EINVAL, "psgd_distill: device ordinal must be in [0, 63]");
   if (rows == 0) return PSGD_OK;
   if (!logits || !teacher || !index || !losses) return fail(PSGD_EINVAL, "psgd_distill: NULL pointer");

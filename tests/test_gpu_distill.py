@@ -207,6 +207,24 @@ def test_gradient_against_differences():
         assert abs(float((dz.double() * v).sum() - slope)) <= float(bound)
 
 
+def test_offsets_beyond_32_bits():
+    """More than 2^31 logits, in place; rows from both ends and the middle."""
+    rows, vocab, k = 43001, 50257, 3
+    z = torch.zeros((rows, vocab), dtype=BF16, device=DEV)
+    part, t, at = inputs(90, vocab, k, BF16, F32, torch.int64, 15, ragged=False)
+    places = torch.cat([torch.arange(30), torch.arange(21000, 21030), torch.arange(rows - 30, rows)]).to(DEV)
+    z[places] = part
+    teacher, index = torch.zeros((rows, k), device=DEV), torch.full((rows, k), -1, device=DEV)
+    teacher[places], index[places] = t, at
+    losses, dz = distill(z, teacher, index, dlogits=z)
+    (wl, wz), (el, ez) = tu.distill(part, t, at, 1.0)
+    tu.check(losses[places], wl, tu.out_tol(el, wl, F32))
+    tu.check(dz[places], wz, tu.out_tol(ez, wz, BF16))
+    others = torch.ones(rows, dtype=torch.bool, device=DEV)
+    others[places] = False
+    assert bool((losses[others] == 0).all()) and int(torch.count_nonzero(z[others.nonzero()[::400, 0]])) == 0
+
+
 def test_side_stream():
     s = torch.cuda.Stream()
     z, t, at = inputs(300, 3000, 9, F32, F32, torch.int64, 11)
@@ -255,7 +273,7 @@ def test_refusals():
     with pytest.raises(PsgdError, match="k must"):
         distill(z, t[:, :1].expand(4, PSGD_DISTILL_MAX_K + 1).contiguous(),
                 at[:, :1].expand(4, PSGD_DISTILL_MAX_K + 1).contiguous())
-    for bad in (0.0, -1.0, float("inf"), float("nan")):
+    for bad in (0.0, -1.0, float("inf"), float("nan"), 1e-39):
         with pytest.raises(PsgdError, match="temperature"):
             distill(z, t, at, temperature=bad)
     with pytest.raises(ValueError, match="weights"):

@@ -111,6 +111,27 @@ def test_lookup_one_large_table():
     assert torch.equal(e.forward(w, ids[:1, 77:78]), w[ids[:1, 77:78]])
 
 
+@pytest.mark.parametrize("dim", [1024, 1031])
+@pytest.mark.parametrize("tokens", [100, 3000])
+def test_offsets_beyond_32_bits(dim, tokens):
+    """A table of more than 2^31 elements, read and written at both ends and in the middle."""
+    vocab = 2**31 // dim + 77
+    e = embedding(vocab, dim, tokens)
+    w = torch.zeros((vocab, dim), dtype=BF16, device=DEV)
+    rows = torch.cat([torch.arange(9), torch.arange(vocab // 2, vocab // 2 + 9), torch.arange(vocab - 9, vocab)]).to(DEV)
+    w[rows] = randn((27, dim), BF16, 1)
+    pick = torch.randint(0, 27, (tokens,), device=DEV, generator=gen(2))
+    out = e.forward(w, rows[pick])
+    assert torch.equal(out, w[rows][pick])
+    grad = randn((tokens, dim), BF16, 3)
+    w.fill_(3.0)
+    e.backward(rows[pick], grad, out=w)
+    dw, mag, count = tu.table_grad(pick, grad, 27, 1.0)
+    tu.check(w[rows], dw, tu.table_grad_tol(dw, mag, count, BF16))
+    assert int(torch.count_nonzero(w[9:vocab // 2:97])) == 0 and int(torch.count_nonzero(w[vocab // 2 + 9:vocab - 9:97])) == 0
+    assert not e.status()
+
+
 # -- gradient ------------------------------------------------------------------------
 
 def run_grad(vocab, dim, shape, gdtype, odtype, seed, iddtype=torch.int64, hot=0.0, padding=None, scale=1.0, offset=0,

@@ -100,6 +100,27 @@ def test_strides(dtype, dim):
     run_both(20, dim, dtype, F32, 4, x=big[:20, :dim], grad=grads[:1, :dim].expand(20, dim))
 
 
+@pytest.mark.parametrize("dim", [1024, 1023])
+def test_offsets_beyond_32_bits(dim):
+    """More than 2^31 elements; rows from both ends and the middle, and the columns' sums of all of them."""
+    rows = 2**31 // dim + 999
+    n = norm(dim)
+    x, g = torch.zeros((rows, dim), dtype=BF16, device=DEV), torch.zeros((rows, dim), dtype=BF16, device=DEV)
+    places = torch.cat([torch.arange(40), torch.arange(rows // 2, rows // 2 + 40), torch.arange(rows - 40, rows)]).to(DEV)
+    x[places], g[places] = randn((120, dim), BF16, 1, 1.5), randn((120, dim), BF16, 2)
+    w = randn((dim,), F32, 3)
+    y, mean, rstd = n.forward(x, w)
+    part, pg = x[places], g[places]
+    (wy, _, _), (ey, _, _) = tu.norm_forward(part, w, None, EPS)
+    tu.check(y[places], wy, tu.out_tol(ey, wy, BF16))
+    dx, dw, db = n.backward(g, x, mean, rstd, w, dx=y)
+    (wx, ww, wb), (ex, ew, eb) = tu.norm_backward(pg, part, mean[places], rstd[places], w)
+    tu.check(dx[places], wx, tu.out_tol(ex, wx, BF16))
+    # the other rows add zeros to the columns' sums
+    tu.check(dw, ww, tu.out_tol(ew, ww, F32))
+    tu.check(db, wb, tu.out_tol(eb, wb, F32))
+
+
 def test_three_dimensions_and_outputs():
     n = norm(48)
     x = randn((3, 5, 48), BF16, 1)
