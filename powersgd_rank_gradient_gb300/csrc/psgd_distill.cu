@@ -283,6 +283,8 @@ __global__ void __launch_bounds__(kDistillThreads + 32, 2) k_distill_chip(Distil
   const unsigned whole = (unsigned)max(0, min(n, (head + a.vocab) / NE - g0) - whole0);
   const Z* zs = z + ((long long)g0 * NE - head);  // the slice's first granule (its first elements may lie before the row)
   const int j0 = g0 * NE - head;                  // its first element
+  after_previous();
+  next_may_launch();
   const float w = a.weights ? __ldg(a.weights + row) : 1.f;
   if (ctas > 1) cluster_arrive();  // a peer's shared memory is written once all have started
 
@@ -499,6 +501,8 @@ template <typename Z> __global__ void __launch_bounds__(kDistillThreads) k_disti
   const long long row = blockIdx.x;
   const Z* z = (const Z*)a.z + row * a.zs;
   Z* dz = a.dz ? (Z*)a.dz + row * a.dzs : nullptr;
+  after_previous();
+  next_may_launch();
   const float w = a.weights ? __ldg(a.weights + row) : 1.f;
   if (!teacher_softmax(a, row, w, p, at, buf)) {
     if (tid == 0) a.losses[row] = 0.f;
@@ -574,34 +578,18 @@ RowPlan plan_row(long long vocab, int size, int k, long long rows, int sms) {
 }
 
 template <typename Z, bool ALIGNED> cudaError_t launch_chip(const DistillArgs& a, const RowPlan& p, int device, cudaStream_t st) {
-  static std::atomic<unsigned long long> raised{0};  // devices whose shared-memory limit is raised
-  const unsigned long long bit = 1ull << device;
-  cudaError_t e = cudaSuccess;
-  if (!(raised.load(std::memory_order_acquire) & bit)) {
-    e = cudaFuncSetAttribute(k_distill_chip<Z, ALIGNED>, cudaFuncAttributeMaxDynamicSharedMemorySize, kFullSmem + 64);
-    if (e != cudaSuccess) return e;
-    raised.fetch_or(bit, std::memory_order_release);
-  }
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(a.rows * p.ctas));
-  cfg.blockDim = dim3(p.threads + 32);
-  cfg.dynamicSmemBytes = p.smem;
-  cfg.stream = st;
-  cudaLaunchAttribute attr;
-  attr.id = cudaLaunchAttributeClusterDimension;
-  attr.val.clusterDim.x = p.ctas;
-  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = p.ctas > 1 ? 1 : 0;
+  static std::atomic<unsigned long long> raised{0};
+  const cudaError_t e = raise_smem(k_distill_chip<Z, ALIGNED>, raised, device, kFullSmem + 64);
+  if (e != cudaSuccess) return e;
   const int per = ((p.granules + p.threads - 1) / p.threads + kStages - 1) / kStages;  // granules per thread and group of copies
-  return cudaLaunchKernelEx(&cfg, k_distill_chip<Z, ALIGNED>, a, p.log_ctas, p.granules, per);
+  return launch_early(k_distill_chip<Z, ALIGNED>, (unsigned)(a.rows * p.ctas), p.threads + 32, p.smem, p.ctas, st, a,
+                      p.log_ctas, p.granules, per);
 }
 
 template <typename Z> cudaError_t launch_distill(const DistillArgs& a, int device, int sms, cudaStream_t st) {
   const RowPlan p = plan_row(a.vocab, (int)sizeof(Z), a.k, a.rows, sms);
   if (p.ctas == 0) {
-    k_distill_long<Z><<<(unsigned)a.rows, kDistillThreads, 0, st>>>(a);
-    return cudaGetLastError();
+    return launch_early(k_distill_long<Z>, (unsigned)a.rows, kDistillThreads, 0, 1, st, a);
   }
   const bool aligned = !a.dz || ((((uintptr_t)a.z ^ (uintptr_t)a.dz) & 15) == 0 &&
                                  (a.rows == 1 || ((a.zs - a.dzs) * (long long)sizeof(Z)) % 16 == 0));

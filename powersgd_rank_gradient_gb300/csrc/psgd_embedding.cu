@@ -86,6 +86,8 @@ __global__ void __launch_bounds__(256) k_lookup(const W* __restrict__ weight, lo
   const int c0 = (blockIdx.y * blockDim.x * NV + threadIdx.x) * VEC, step = blockDim.x * VEC;
   const long long token = (long long)blockIdx.x * blockDim.y + threadIdx.y;
   if (token >= n) return;
+  after_previous();
+  next_may_launch();
   const int i = (int)token;
   const long long id = load_id(ids, id64, il.at(i));
   const bool ok = id >= 0 && id < vocab;
@@ -155,6 +157,7 @@ template <int CTAS, int ITEMS, int BITS> __global__ void __launch_bounds__(kSort
   cg::cluster_group cluster = cg::this_cluster();
   const int rank = CTAS > 1 ? (int)cluster.block_rank() : 0;
   const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
+  after_previous();  // and with it the row sums' kernel, which starts when this one lets it
   if (a.named) {  // (its size is rounded up to 16 bytes)
     uint4* v = reinterpret_cast<uint4*>(a.named);
     for (int i = rank * kSortThreads + t; i < (a.vocab + 15) / 16; i += CTAS * kSortThreads) v[i] = make_uint4(0, 0, 0, 0);
@@ -330,6 +333,8 @@ __device__ __forceinline__ void zero_bytes(char* p, long long bytes, int lane) {
 
 // The whole table, where there is no token.
 __global__ void __launch_bounds__(256) k_zero_table(char* __restrict__ w, long long rows, long long bytes, long long stride) {
+  after_previous();
+  next_may_launch();
   const int warps = blockDim.x / 32;
   for (long long r = (long long)blockIdx.x * warps + threadIdx.x / 32; r < rows; r += (long long)gridDim.x * warps)
     zero_bytes(w + r * stride, bytes, threadIdx.x & 31);
@@ -513,6 +518,8 @@ __global__ void __launch_bounds__(512) k_rows_direct(const void* __restrict__ id
   const int threads = blockDim.x, groups = blockDim.y, group = threadIdx.y;
   const int all = threads * groups, t = group * threads + threadIdx.x, lane = t & 31, warp = t >> 5, warps = all >> 5;
   const int base = blockIdx.x * span, rows = min(span, vocab - base);
+  after_previous();
+  next_may_launch();
   if (t < kMaxSpan) count[t] = 0;
   __syncthreads();
   for (int i0 = t; i0 < n; i0 += all * 8) {
@@ -667,6 +674,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) k_join_rows(int dim, float sc
                                                                const int* __restrict__ counts, int* ready) {
   __shared__ float sums[kJoinWarps][32][4];
   after_previous();
+  next_may_launch();
   if (blockIdx.x == 0 && threadIdx.x == 0 && threadIdx.y == 0) *ready = 0;  // for the next call
   const int lane = threadIdx.x, warp = threadIdx.y;
   const bool vec = dim % 4 == 0;
@@ -748,26 +756,9 @@ template <typename F> int by_dtype(int32_t d, F&& f) {
 
 template <int CTAS, int ITEMS, int BITS> cudaError_t launch_sort(const SortArgs& a, int device, cudaStream_t st) {
   constexpr int bytes = (int)sizeof(SortShared<BITS>);
-  static std::atomic<unsigned long long> raised{0};  // devices whose shared-memory limit is raised
-  const unsigned long long bit = 1ull << device;
-  if (!(raised.load(std::memory_order_acquire) & bit)) {
-    const cudaError_t e =
-        cudaFuncSetAttribute(k_sort_tokens<CTAS, ITEMS, BITS>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-    if (e != cudaSuccess) return e;
-    raised.fetch_or(bit, std::memory_order_release);
-  }
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(CTAS);
-  cfg.blockDim = dim3(kSortThreads);
-  cfg.dynamicSmemBytes = bytes;
-  cfg.stream = st;
-  cudaLaunchAttribute attr;
-  attr.id = cudaLaunchAttributeClusterDimension;
-  attr.val.clusterDim.x = CTAS;
-  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = CTAS > 1 ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, k_sort_tokens<CTAS, ITEMS, BITS>, a);
+  static std::atomic<unsigned long long> raised{0};
+  const cudaError_t e = raise_smem(k_sort_tokens<CTAS, ITEMS, BITS>, raised, device, bytes);
+  return e != cudaSuccess ? e : launch_early(k_sort_tokens<CTAS, ITEMS, BITS>, CTAS, kSortThreads, bytes, CTAS, st, a);
 }
 
 // Sorted tokens per CTA of the row sums: 32, or 8 to 16 where that would leave
@@ -951,6 +942,7 @@ extern "C" int psgd_embedding_forward(psgd_embedding* h, const void* weight, psg
   DeviceScope scope(h->device);
   const Layout2 il(outer, inner, ids_outer_stride, ids_inner_stride), ol(outer, inner, out_outer_stride, out_inner_stride);
   const cudaStream_t st = (cudaStream_t)stream;
+  cudaError_t e = cudaSuccess;
   by_dtype(weight_dtype, [&](auto* wt) {
     using W = std::remove_pointer_t<decltype(wt)>;
     return by_dtype(out_dtype, [&](auto* ot) {
@@ -964,19 +956,12 @@ extern "C" int psgd_embedding_forward(psgd_embedding* h, const void* weight, psg
       const TilePlan p = plan_tile(h->dim, vec ? V : 1, wide ? 4 : 1);
       const dim3 grid((unsigned)((n + (long long)p.groups - 1) / p.groups), p.tiles);
       const dim3 block(p.threads, p.groups);
-      if (wide)
-        k_lookup<W, O, V, 4><<<grid, block, 0, st>>>((const W*)weight, weight_stride, h->vocab, (int)h->dim, ids,
-                                                     id_bits == 64, il, n, scale, (O*)out, ol, h->d_flag);
-      else if (vec)
-        k_lookup<W, O, V, 1><<<grid, block, 0, st>>>((const W*)weight, weight_stride, h->vocab, (int)h->dim, ids,
-                                                     id_bits == 64, il, n, scale, (O*)out, ol, h->d_flag);
-      else
-        k_lookup<W, O, 1, kScalarNv><<<grid, block, 0, st>>>((const W*)weight, weight_stride, h->vocab, (int)h->dim,
-                                                             ids, id_bits == 64, il, n, scale, (O*)out, ol, h->d_flag);
+      auto kernel = wide ? k_lookup<W, O, V, 4> : vec ? k_lookup<W, O, V, 1> : k_lookup<W, O, 1, kScalarNv>;
+      e = launch_early(kernel, grid, block, 0, 1, st, (const W*)weight, weight_stride, h->vocab, h->dim, ids,
+                       id_bits == 64, il, n, scale, (O*)out, ol, h->d_flag);
       return 0;
     });
   });
-  const cudaError_t e = cudaGetLastError();
   return e == cudaSuccess ? PSGD_OK : cuda_fail(who, e);
 }
 
@@ -1010,9 +995,8 @@ extern "C" int psgd_embedding_backward(psgd_embedding* h, const void* ids, int32
   cudaError_t e = cudaSuccess;
   if (n == 0) {
     if (!accumulate)
-      k_zero_table<<<(unsigned)std::min<long long>((vocab + 7) / 8, h->sms * 8), 256, 0, st>>>(
-          (char*)dweight, vocab, (long long)dim * osize, dweight_stride * osize);
-    e = cudaGetLastError();
+      e = launch_early(k_zero_table, (unsigned)std::min<long long>((vocab + 7) / 8, h->sms * 8), 256, 0, 1, st,
+                       (char*)dweight, vocab, (long long)dim * osize, dweight_stride * osize);
   } else if (const int span = direct_span(n, vocab)) {
     by_dtype(grad_dtype, [&](auto* gt) {
       using G = std::remove_pointer_t<decltype(gt)>;
@@ -1024,22 +1008,13 @@ extern "C" int psgd_embedding_backward(psgd_embedding* h, const void* ids, int32
         const TilePlan p = plan_tile(dim, vec ? V : 1);
         const int groups = std::min(8, 512 / p.threads);
         const size_t smem = direct_bytes(n) + 8 * (size_t)n + (size_t)groups * p.threads * (vec ? V : kScalarNv) * 4;
-        cudaLaunchConfig_t cfg = {};
-        cfg.gridDim = dim3((vocab + span - 1) / span, p.tiles);
-        cfg.blockDim = dim3(p.threads, groups);
-        cfg.dynamicSmemBytes = smem;
-        cfg.stream = st;
         auto kernel = vec ? k_rows_direct<G, O, V, 1> : k_rows_direct<G, O, 1, kScalarNv>;
-        static std::atomic<unsigned long long> raised[2];  // devices whose shared-memory limit is raised
-        const unsigned long long bit = 1ull << h->device;
-        if (!(raised[vec].load(std::memory_order_acquire) & bit)) {
-          e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 100 * 1024);
-          if (e == cudaSuccess) raised[vec].fetch_or(bit, std::memory_order_release);
-        }
+        static std::atomic<unsigned long long> raised[2];
+        e = raise_smem(kernel, raised[vec], h->device, 64 * 1024);
         if (e == cudaSuccess)
-          e = cudaLaunchKernelEx(&cfg, kernel, ids, (int)(id_bits == 64), il, n, vocab, (long long)padding_idx, h->d_flag,
-                                 (const G*)grad, gl, dim, scale, (int)accumulate, (O*)dweight, (long long)dweight_stride,
-                                 dw_aligned, span);
+          e = launch_early(kernel, dim3((vocab + span - 1) / span, p.tiles), dim3(p.threads, groups), smem, 1, st, ids,
+                           id_bits == 64, il, n, vocab, padding_idx, h->d_flag, (const G*)grad, gl, dim, scale, accumulate,
+                           (O*)dweight, dweight_stride, dw_aligned, span);
         return 0;
       });
     });
@@ -1057,11 +1032,6 @@ extern "C" int psgd_embedding_backward(psgd_embedding* h, const void* ids, int32
     const int chunk = chunk_for(n, h->sms);
     const unsigned chunks = (unsigned)((n + (long long)chunk - 1) / chunk);
     const int *key = h->key[(passes - 1) & 1], *pos = h->pos[(passes - 1) & 1];
-    cudaLaunchAttribute early = early_launch();
-    cudaLaunchConfig_t cfg = {};
-    cfg.stream = st;
-    cfg.attrs = &early;
-    cfg.numAttrs = 1;
     by_dtype(grad_dtype, [&](auto* gt) {
       using G = std::remove_pointer_t<decltype(gt)>;
       return by_dtype(dweight_dtype, [&](auto* ot) {
@@ -1076,19 +1046,16 @@ extern "C" int psgd_embedding_backward(psgd_embedding* h, const void* ids, int32
         if (!accumulate)
           zero.ctas = (int)std::max<long long>(
               1, std::min<long long>(vocab * zero.bytes / 65536, (long long)h->sms * kZeroCtas * (256 / threads)));
-        cfg.gridDim = dim3(zero.ctas + chunks, p.tiles);
-        cfg.blockDim = dim3(threads);
         if (e == cudaSuccess)
-          e = cudaLaunchKernelEx(&cfg, vec ? k_row_sums<G, O, V, 1> : k_row_sums<G, O, 1, kScalarNv>, key, pos,
-                                 (const G*)grad, gl, dim, scale, (int)accumulate, (O*)dweight, (long long)dweight_stride,
-                                 dw_aligned, h->part, chunk, h->crossing, h->counts, zero);
+          e = launch_early(vec ? k_row_sums<G, O, V, 1> : k_row_sums<G, O, 1, kScalarNv>, dim3(zero.ctas + chunks, p.tiles),
+                           threads, 0, 1, st, key, pos, (const G*)grad, gl, dim, scale, accumulate, (O*)dweight,
+                           dweight_stride, dw_aligned, h->part, chunk, h->crossing, h->counts, zero);
         if ((chunks > 1 || !accumulate) && e == cudaSuccess) {
           const long long items = std::max<long long>(1, chunks - 1) * ((dim + 127) / 128);
-          cfg.gridDim = dim3((unsigned)std::min<long long>((items + kJoinWarps - 1) / kJoinWarps, h->sms * 4));
-          cfg.blockDim = dim3(32, kJoinWarps);
-          e = cudaLaunchKernelEx(&cfg, k_join_rows<O>, dim, scale, (int)accumulate, (O*)dweight,
-                                 (long long)dweight_stride, (const float*)h->part, (const int4*)h->crossing, (int)chunks,
-                                 (const int*)h->counts, h->ready);
+          e = launch_early(k_join_rows<O>,
+                           (unsigned)std::min<long long>((items + kJoinWarps - 1) / kJoinWarps, h->sms * 4),
+                           dim3(32, kJoinWarps), 0, 1, st, dim, scale, accumulate, (O*)dweight, dweight_stride, h->part,
+                           h->crossing, chunks, h->counts, h->ready);
         }
         return 0;
       });

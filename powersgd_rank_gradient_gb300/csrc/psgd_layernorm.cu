@@ -167,6 +167,8 @@ __global__ void __launch_bounds__(kMaxThreads, NV == 1 && R == 1 ? 2 : 1) k_norm
     left -= step;
     from += from_step;
   };
+  after_previous();
+  next_may_launch();
 #pragma unroll
   for (int k = 0; k < kStages - 1; ++k) issue(k);
   F2 w[NV][NP], bias[NV][NP];
@@ -279,6 +281,7 @@ __global__ void __launch_bounds__(kMaxThreads, 1) k_norm_backward_vec(RowsArgs a
     from_g += g_step;
     from_s += step;
   };
+  after_previous();
 #pragma unroll
   for (int k = 0; k < kStages - 1; ++k) issue(k);
   F2 dw[NV][NP], db[NV][NP], w[NV][NP];
@@ -478,6 +481,8 @@ __global__ void __launch_bounds__(kMaxThreads, 1) k_norm_forward_any(RowsArgs a)
     commit_copies();
     ahead = ahead < (int)a.rows ? ahead + step : ahead;
   };
+  after_previous();
+  next_may_launch();
 #pragma unroll
   for (int k = 0; k < kStages - 1; ++k) issue(k);
   F2 w[NP], bias[NP], keep[NP];  // keep: 1 in a column of the row, 0 behind its end
@@ -585,6 +590,7 @@ __global__ void __launch_bounds__(kMaxThreads, 1) k_norm_backward_any(RowsArgs a
     commit_copies();
     ahead = ahead < (int)a.rows ? ahead + step : ahead;
   };
+  after_previous();
 #pragma unroll
   for (int k = 0; k < kStages - 1; ++k) issue(k);
   F2 dw[NP], db[NP], w[NP], keep[NP];
@@ -773,6 +779,7 @@ __global__ void __launch_bounds__(32 * kColumnWarps) k_norm_columns(const float*
   const int x = threadIdx.x & 31, y = threadIdx.x >> 5;
   const long long c = (long long)blockIdx.x * 32 + x;
   after_previous();
+  next_may_launch();
   float s = 0.f;
   if (c < 2LL * dim) {
     constexpr int kAtOnce = 10;
@@ -852,15 +859,6 @@ template <typename F> void with_scalar_plan(const RowPlan& p, F&& f) {
 }
 int scalar_rows(const RowPlan& p) { return 16 / p.nv; }
 
-// Raises a kernel's shared-memory limit, once per device.
-template <typename K> cudaError_t raise_smem(K kernel, std::atomic<unsigned long long>& raised, int device, int bytes) {
-  const unsigned long long bit = 1ull << device;
-  if (raised.load(std::memory_order_acquire) & bit) return cudaSuccess;
-  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-  if (e == cudaSuccess) raised.fetch_or(bit, std::memory_order_release);
-  return e;
-}
-
 // Shared memory of the kernels for any rows, one CTA of which an SM gets.
 size_t any_smem(const RowPlan& p, int size, int arrays) {
   return (size_t)p.groups * kStages * scalar_rows(p) * arrays * slot_bytes(p.threads * p.nv, size);
@@ -871,16 +869,14 @@ cudaError_t launch_forward_any(const RowsArgs& a, const RowPlan& p, unsigned gri
   static std::atomic<unsigned long long> raised{0};
   const cudaError_t e = raise_smem(k_norm_forward_any<T, NV, R>, raised, device, 220 * 1024);
   if (e != cudaSuccess) return e;
-  k_norm_forward_any<T, NV, R><<<grid, dim3(p.threads, p.groups), smem, st>>>(a);
-  return cudaGetLastError();
+  return launch_early(k_norm_forward_any<T, NV, R>, grid, dim3(p.threads, p.groups), smem, 1, st, a);
 }
 template <typename T, int NV, int R>
 cudaError_t launch_backward_any(const RowsArgs& a, const RowPlan& p, unsigned grid, size_t smem, int device, cudaStream_t st) {
   static std::atomic<unsigned long long> raised{0};
   const cudaError_t e = raise_smem(k_norm_backward_any<T, NV, R>, raised, device, 220 * 1024);
   if (e != cudaSuccess) return e;
-  k_norm_backward_any<T, NV, R><<<grid, dim3(p.threads, p.groups), smem, st>>>(a);
-  return cudaGetLastError();
+  return launch_early(k_norm_backward_any<T, NV, R>, grid, dim3(p.threads, p.groups), smem, 1, st, a);
 }
 
 template <typename T, int NV, int R>
@@ -888,18 +884,16 @@ cudaError_t launch_forward(const RowsArgs& a, const RowPlan& p, unsigned grid, i
   static std::atomic<unsigned long long> raised{0};
   const cudaError_t e = raise_smem(k_norm_forward_vec<T, NV, R>, raised, device, kStages * R * NV * kMaxThreads * 16);
   if (e != cudaSuccess) return e;
-  k_norm_forward_vec<T, NV, R>
-      <<<grid, dim3(p.threads, p.groups), (size_t)kStages * R * NV * kMaxThreads * 16, st>>>(a);
-  return cudaGetLastError();
+  return launch_early(k_norm_forward_vec<T, NV, R>, grid, dim3(p.threads, p.groups),
+                      (size_t)kStages * R * NV * kMaxThreads * 16, 1, st, a);
 }
 template <typename T, int NV, int R>
 cudaError_t launch_backward(const RowsArgs& a, const RowPlan& p, unsigned grid, int device, cudaStream_t st) {
   static std::atomic<unsigned long long> raised{0};
   const cudaError_t e = raise_smem(k_norm_backward_vec<T, NV, R>, raised, device, kStages * R * NV * kMaxThreads * 32);
   if (e != cudaSuccess) return e;
-  k_norm_backward_vec<T, NV, R>
-      <<<grid, dim3(p.threads, p.groups), (size_t)kStages * R * NV * kMaxThreads * 32, st>>>(a);
-  return cudaGetLastError();
+  return launch_early(k_norm_backward_vec<T, NV, R>, grid, dim3(p.threads, p.groups),
+                      (size_t)kStages * R * NV * kMaxThreads * 32, 1, st, a);
 }
 
 template <typename F> void by_dtype(int32_t d, F&& f) {
@@ -1087,15 +1081,8 @@ extern "C" int psgd_layernorm_backward(psgd_layernorm* h, const void* grad, int6
       }
     });
   if (e == cudaSuccess && params) {
-    cudaLaunchAttribute early = early_launch();
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)((2 * h->dim + 31) / 32));
-    cfg.blockDim = dim3(32 * kColumnWarps);
-    cfg.stream = st;
-    cfg.attrs = &early;
-    cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, k_norm_columns, (const float*)h->part, parts, (int)h->dim, dweight, dbias,
-                           (int)dparam_dtype, (int)accumulate);
+    e = launch_early(k_norm_columns, (unsigned)((2 * h->dim + 31) / 32), 32 * kColumnWarps, 0, 1, st, h->part, parts, h->dim,
+                     dweight, dbias, dparam_dtype, accumulate);
   }
   return e == cudaSuccess ? PSGD_OK : cuda_fail(who, e);
 }

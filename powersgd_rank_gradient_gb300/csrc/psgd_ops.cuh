@@ -8,6 +8,7 @@
 #include <math.h>
 #include <stdint.h>
 
+#include <atomic>
 #include <string>
 
 #include "../../include/psgd.h"
@@ -141,13 +142,33 @@ template <typename T, int V> __device__ __forceinline__ void store_run(T* p, con
 // The alignment in bytes that store_run of V elements of `size` bytes asks for.
 inline int run_alignment(int v, int size) { return v == 1 ? size : (v * size >= 16 ? 16 : v * size); }
 
-// The kernel launch attribute that lets a kernel be set up while the one before
-// it in the stream still runs; it then begins with after_previous().
-inline cudaLaunchAttribute early_launch() {
-  cudaLaunchAttribute a;
-  a.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  a.val.programmaticStreamSerializationAllowed = 1;
-  return a;
+// Launches a kernel that may be set up while the one before it in the stream
+// still runs: it must begin with after_previous(), before it touches any memory
+// (the kernel before may be anyone's).  cluster: CTAs of a cluster, 1: none.
+template <typename... P, typename... A>
+cudaError_t launch_early(void (*kernel)(P...), dim3 grid, dim3 block, size_t smem, int cluster, cudaStream_t st, A&&... args) {
+  cudaLaunchAttribute attrs[2];
+  attrs[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attrs[0].val.programmaticStreamSerializationAllowed = 1;
+  attrs[1].id = cudaLaunchAttributeClusterDimension;
+  attrs[1].val.clusterDim.x = cluster;
+  attrs[1].val.clusterDim.y = attrs[1].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cfg.attrs = attrs;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
+}
+// Raises a kernel's shared-memory limit, once per device.
+template <typename K> cudaError_t raise_smem(K kernel, std::atomic<unsigned long long>& raised, int device, int bytes) {
+  const unsigned long long bit = 1ull << device;
+  if (raised.load(std::memory_order_acquire) & bit) return cudaSuccess;
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess) raised.fetch_or(bit, std::memory_order_release);
+  return e;
 }
 // Waits until everything the previous kernel of the stream wrote is visible.
 __device__ __forceinline__ void after_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
