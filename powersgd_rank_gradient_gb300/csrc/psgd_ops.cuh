@@ -144,23 +144,35 @@ inline int run_alignment(int v, int size) { return v == 1 ? size : (v * size >= 
 
 // Launches a kernel that may be set up while the one before it in the stream
 // still runs: it must begin with after_previous(), before it touches any memory
-// (the kernel before may be anyone's).  cluster: CTAs of a cluster, 1: none.
+// (the kernel before may be anyone's).  cluster: CTAs of a cluster, 1: none;
+// early = false: after the kernel before, as usual.
 template <typename... P, typename... A>
-cudaError_t launch_early(void (*kernel)(P...), dim3 grid, dim3 block, size_t smem, int cluster, cudaStream_t st, A&&... args) {
+cudaError_t launch(bool early, void (*kernel)(P...), dim3 grid, dim3 block, size_t smem, int cluster, cudaStream_t st,
+                   A&&... args) {
   cudaLaunchAttribute attrs[2];
-  attrs[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attrs[0].val.programmaticStreamSerializationAllowed = 1;
-  attrs[1].id = cudaLaunchAttributeClusterDimension;
-  attrs[1].val.clusterDim.x = cluster;
-  attrs[1].val.clusterDim.y = attrs[1].val.clusterDim.z = 1;
+  int n = 0;
+  if (early) {
+    attrs[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attrs[n++].val.programmaticStreamSerializationAllowed = 1;
+  }
+  if (cluster > 1) {
+    attrs[n].id = cudaLaunchAttributeClusterDimension;
+    attrs[n].val.clusterDim.x = cluster;
+    attrs[n].val.clusterDim.y = 1;
+    attrs[n++].val.clusterDim.z = 1;
+  }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = block;
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
   cfg.attrs = attrs;
-  cfg.numAttrs = cluster > 1 ? 2 : 1;
+  cfg.numAttrs = n;
   return cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
+}
+template <typename... P, typename... A>
+cudaError_t launch_early(void (*kernel)(P...), dim3 grid, dim3 block, size_t smem, int cluster, cudaStream_t st, A&&... args) {
+  return launch(true, kernel, grid, block, smem, cluster, st, static_cast<A&&>(args)...);
 }
 // Raises a kernel's shared-memory limit, once per device.
 template <typename K> cudaError_t raise_smem(K kernel, std::atomic<unsigned long long>& raised, int device, int bytes) {
