@@ -574,8 +574,12 @@ RowPlan plan_row(long long vocab, int size, int k, long long rows, int sms) {
   while (1 << p.log_ctas < p.ctas) ++p.log_ctas;
   p.granules = (int)(bytes / 16 / p.ctas + 2);
   p.smem = (size_t)p.granules * 16 + extra;
-  const int most = p.smem > 72 * 1024 ? kDistillThreads : kDistillThreads / 2;  // three and more slices to an SM: 256 each
-  p.threads = (int)std::min<long long>(most, std::max<long long>(64, (p.granules / 4 + 31) / 32 * 32));
+  // threads: 512 where two slices fill an SM, 256 where three and more do, and
+  // half as many for short rows, of which an SM then has more, each waiting for
+  // its own loads (4000 rows of 8000 bf16 logits 34 us so, 41 with 288 threads)
+  const int most = p.smem > 72 * 1024 ? kDistillThreads : kDistillThreads / 2;
+  const int share = p.smem > 48 * 1024 ? 4 : 8;  // granules per thread
+  p.threads = (int)std::min<long long>(most, std::max<long long>(64, (p.granules / share + 31) / 32 * 32));
   return p;
 }
 

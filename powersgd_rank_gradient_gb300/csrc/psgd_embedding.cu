@@ -83,7 +83,10 @@ template <typename W, typename O, int VEC, int NV>
 __global__ void __launch_bounds__(256) k_lookup(const W* __restrict__ weight, long long wstride, long long vocab,
                                                 int dim, const void* __restrict__ ids, int id64, Layout2 il, int n,
                                                 float scale, O* __restrict__ out, Layout2 ol, int* flag) {
-  const int c0 = (blockIdx.y * blockDim.x * NV + threadIdx.x) * VEC, step = blockDim.x * VEC;
+  // (single elements: a warp's are next to each other, at constant distances)
+  const int c0 = VEC > 1 ? (blockIdx.y * blockDim.x * NV + threadIdx.x) * VEC
+                         : (blockIdx.y * blockDim.x + threadIdx.x / 32 * 32) * NV + threadIdx.x % 32;
+  const int step = VEC > 1 ? blockDim.x * VEC : 32;
   const long long token = (long long)blockIdx.x * blockDim.y + threadIdx.y;
   if (token >= n) return;
   after_previous();
@@ -142,8 +145,8 @@ template <int BITS> struct SortShared {
 // dropped by the first pass.  Each warp owns a contiguous share of the list, so
 // that digit counts per (CTA, warp), scanned in list order, give every element
 // its place; each CTA writes its digit totals into its peers' shared memory.  A
-// share of at most 32 x ITEMS elements stays in registers between counting and
-// placing (ITEMS = 0: any share, read twice).  The time is the chain of
+// warp loads 32 x ITEMS elements of its share at a time; a share of no more stays
+// in registers between counting and placing.  The time is the chain of
 // latencies of a pass (a load, the barriers, a scan, a scattered store), so
 // tables of up to 1024 rows take one pass of 10 bits in place of two of 8, and
 // up to 2048 tokens one CTA without a cluster's barriers.  16384 tokens of
@@ -199,15 +202,16 @@ template <int CTAS, int ITEMS, int BITS> __global__ void __launch_bounds__(kSort
       if (d < D && (same & below) == 0) s.cnt[warp][d] += __popc(same);
       __syncwarp();
     };
-    int key[ITEMS > 0 ? ITEMS : 1], pos[ITEMS > 0 ? ITEMS : 1];
-    if constexpr (ITEMS > 0) {
+    int key[ITEMS], pos[ITEMS];
+    auto load = [&](int e0) {  // the elements e0 .. e0 + 32 ITEMS of the share
 #pragma unroll
       for (int i = 0; i < ITEMS; ++i) {
-        const int e = i * 32 + lane;
+        const int e = e0 + i * 32 + lane;
         key[i] = e < share ? key_at(first + e) : -1;
         pos[i] = e < share ? (p > 0 ? __ldcg(sp + first + e) : (int)first + e) : 0;
       }
-    }
+    };
+    load(0);
     {
       uint4* z = reinterpret_cast<uint4*>(&s.cnt[0][0]);
       for (int i = t; i < (int)(sizeof(s.cnt) / 16); i += kSortThreads) z[i] = make_uint4(0, 0, 0, 0);
@@ -218,19 +222,14 @@ template <int CTAS, int ITEMS, int BITS> __global__ void __launch_bounds__(kSort
     }
     __syncthreads();
     const bool mark = p == 0 && a.named;
-    if constexpr (ITEMS > 0) {
+    for (int e0 = 0; e0 < share; e0 += 32 * ITEMS) {
+      if (e0 > 0) load(e0);
 #pragma unroll
       for (int i = 0; i < ITEMS; ++i)
-        if (i * 32 < share) {
+        if (e0 + i * 32 < share) {
           if (mark && key[i] >= 0) a.named[key[i]] = 1;
           count(digit(key[i]));
         }
-    } else {
-      for (int e = lane; e - lane < share; e += 32) {
-        const int k = e < share ? key_at(first + e) : -1;
-        if (mark && k >= 0) a.named[k] = 1;
-        count(digit(k));
-      }
     }
     __syncthreads();
     // exclusive counts over the warps, PER of them per thread
@@ -298,15 +297,11 @@ template <int CTAS, int ITEMS, int BITS> __global__ void __launch_bounds__(kSort
       if (t == D - 1) s.all = ahead + inc;
     }
     __syncthreads();
-    if constexpr (ITEMS > 0) {
+    for (int e0 = 0; e0 < share; e0 += 32 * ITEMS) {
+      if (share > 32 * ITEMS) load(e0);
 #pragma unroll
       for (int i = 0; i < ITEMS; ++i)
-        if (i * 32 < share) place(digit(key[i]), key[i], pos[i]);
-    } else {
-      for (int e = lane; e - lane < share; e += 32) {
-        const int k = e < share ? key_at(first + e) : -1;
-        place(digit(k), k, e < share ? (p > 0 ? __ldcg(sp + first + e) : (int)first + e) : 0);
-      }
+        if (e0 + i * 32 < share) place(digit(key[i]), key[i], pos[i]);
     }
     n = s.all;
     if (p + 1 < a.passes) {
@@ -787,12 +782,13 @@ bool aligned_rows(const void* p, long long s0, long long s1, int size, int to) {
 
 // How a row is spread over threads: tiles of columns (grid.y), threads of a
 // group, groups of a CTA.
-constexpr int kScalarNv = 4;  // elements per thread and row where accesses are single elements
+constexpr int kScalarNv = 4;   // elements per thread and row where accesses are single elements
+constexpr int kLookupNv = 16;  // the same in a lookup
 struct TilePlan {
   int threads, groups, tiles;
 };
-TilePlan plan_tile(long long dim, int vec, int nv = 1) {
-  const long long per = vec > 1 ? vec * nv : kScalarNv;  // elements per thread
+TilePlan plan_tile(long long dim, int vec, int nv) {
+  const long long per = (long long)vec * nv;  // elements per thread
   const long long want = ((dim + per - 1) / per + 31) / 32 * 32;
   TilePlan p;
   p.threads = (int)std::min<long long>(256, want);
@@ -953,10 +949,10 @@ extern "C" int psgd_embedding_forward(psgd_embedding* h, const void* weight, psg
                        aligned_rows(out, out_outer_stride, out_inner_stride, sizeof(O), align);
       // rows of 64 vectors and more: four of them to a thread
       const bool wide = vec && h->dim >= 64 * V;
-      const TilePlan p = plan_tile(h->dim, vec ? V : 1, wide ? 4 : 1);
+      const TilePlan p = plan_tile(h->dim, vec ? V : 1, wide ? 4 : vec ? 1 : kLookupNv);
       const dim3 grid((unsigned)((n + (long long)p.groups - 1) / p.groups), p.tiles);
       const dim3 block(p.threads, p.groups);
-      auto kernel = wide ? k_lookup<W, O, V, 4> : vec ? k_lookup<W, O, V, 1> : k_lookup<W, O, 1, kScalarNv>;
+      auto kernel = wide ? k_lookup<W, O, V, 4> : vec ? k_lookup<W, O, V, 1> : k_lookup<W, O, 1, kLookupNv>;
       e = launch_early(kernel, grid, block, 0, 1, st, (const W*)weight, weight_stride, h->vocab, h->dim, ids,
                        id_bits == 64, il, n, scale, (O*)out, ol, h->d_flag);
       return 0;
@@ -1005,7 +1001,7 @@ extern "C" int psgd_embedding_backward(psgd_embedding* h, const void* ids, int32
         constexpr int V = Vec16<G>::N;
         const bool vec = dim % V == 0 && aligned_rows(grad, grad_outer_stride, grad_inner_stride, sizeof(G), 16);
         const int dw_aligned = aligned_rows(dweight, dweight_stride, 0, sizeof(O), run_alignment(V, sizeof(O)));
-        const TilePlan p = plan_tile(dim, vec ? V : 1);
+        const TilePlan p = plan_tile(dim, vec ? V : 1, vec ? 1 : kScalarNv);
         const int groups = std::min(8, 512 / p.threads);
         const size_t smem = direct_bytes(n) + 8 * (size_t)n + (size_t)groups * p.threads * (vec ? V : kScalarNv) * 4;
         auto kernel = vec ? k_rows_direct<G, O, V, 1> : k_rows_direct<G, O, 1, kScalarNv>;
@@ -1027,8 +1023,8 @@ extern "C" int psgd_embedding_backward(psgd_embedding* h, const void* ids, int32
     e = n <= 2 * kSortThreads               ? (wide ? launch_sort<1, 2, 10>(a, h->device, st) : launch_sort<1, 2, 8>(a, h->device, st))
         : n <= 2 * kSortThreads * kSortCtas ? (wide ? launch_sort<kSortCtas, 2, 10>(a, h->device, st)
                                                     : launch_sort<kSortCtas, 2, 8>(a, h->device, st))
-                                            : (wide ? launch_sort<kSortCtas, 0, 10>(a, h->device, st)
-                                                    : launch_sort<kSortCtas, 0, 8>(a, h->device, st));
+                                            : (wide ? launch_sort<kSortCtas, 8, 10>(a, h->device, st)
+                                                    : launch_sort<kSortCtas, 8, 8>(a, h->device, st));
     const int chunk = chunk_for(n, h->sms);
     const unsigned chunks = (unsigned)((n + (long long)chunk - 1) / chunk);
     const int *key = h->key[(passes - 1) & 1], *pos = h->pos[(passes - 1) & 1];
@@ -1039,13 +1035,13 @@ extern "C" int psgd_embedding_backward(psgd_embedding* h, const void* ids, int32
         constexpr int V = Vec16<G>::N;
         const bool vec = dim % V == 0 && aligned_rows(grad, grad_outer_stride, grad_inner_stride, sizeof(G), 16);
         const int dw_aligned = aligned_rows(dweight, dweight_stride, 0, sizeof(O), run_alignment(V, sizeof(O)));
-        const TilePlan p = plan_tile(dim, vec ? V : 1);
+        const TilePlan p = plan_tile(dim, vec ? V : 1, vec ? 1 : kScalarNv);
         const int threads = std::max(p.threads, 64);
-        // zeroing: about 64 KB a CTA, up to kZeroCtas CTAs of 256 threads to an SM
+        // zeroing: about 64 KB or 32 rows a CTA, up to kZeroCtas CTAs of 256 threads to an SM
         ZeroArgs zero{0, (char*)dweight, (long long)dim * osize, dweight_stride * osize, vocab, h->named, h->ready};
         if (!accumulate)
-          zero.ctas = (int)std::max<long long>(
-              1, std::min<long long>(vocab * zero.bytes / 65536, (long long)h->sms * kZeroCtas * (256 / threads)));
+          zero.ctas = (int)std::min<long long>(std::max<long long>(vocab * zero.bytes / 65536, (vocab + 31) / 32),
+                                               (long long)h->sms * kZeroCtas * (256 / threads));
         if (e == cudaSuccess)
           e = launch_early(vec ? k_row_sums<G, O, V, 1> : k_row_sums<G, O, 1, kScalarNv>, dim3(zero.ctas + chunks, p.tiles),
                            threads, 0, 1, st, key, pos, (const G*)grad, gl, dim, scale, accumulate, (O*)dweight,
