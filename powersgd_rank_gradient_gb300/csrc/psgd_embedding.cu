@@ -25,9 +25,8 @@ struct psgd_embedding {
   int sms = 0;
   long long vocab = 0, dim = 0, max_tokens = 0;
   void* memory = nullptr;  // all of the following
-  // the sorted tokens: two (key, position) buffers the radix passes alternate between
-  int* key[2] = {nullptr, nullptr};
-  int* pos[2] = {nullptr, nullptr};
+  // the sorted tokens: two (id, position) buffers the radix passes alternate between
+  int2* sorted[2] = {nullptr, nullptr};
   float* part = nullptr;  // per chunk: the partial rows of its first and its last id
   int4* crossing = nullptr;  // rows that cross a chunk's end: (chunk where they begin, id, chunks that follow)
   int* counts = nullptr;     // of few partials; sorted tokens; of many partials
@@ -118,7 +117,7 @@ struct SortArgs {
   int n, vocab;
   long long padding;
   int passes;
-  int *key[2], *pos[2];  // pass p writes buffer p & 1
+  int2* sorted[2];       // (id, position); pass p writes buffer p & 1
   int* flag;
   int* counts;           // out: [0] = [2] = 0 (crossing rows found so far), [1] = tokens with a gradient
   // NULL, or one byte a row: 1 where a token with a gradient names it.  It is
@@ -170,14 +169,13 @@ template <int CTAS, int ITEMS, int BITS> __global__ void __launch_bounds__(kSort
   int n = a.n;
   for (int p = 0; p < a.passes; ++p) {
     const int shift = BITS * p;
-    const int *sk = p & 1 ? a.key[0] : a.key[1], *sp = p & 1 ? a.pos[0] : a.pos[1];
-    int *dk = p & 1 ? a.key[1] : a.key[0], *dp = p & 1 ? a.pos[1] : a.pos[0];
+    const int2* src = p & 1 ? a.sorted[0] : a.sorted[1];
+    int2* dst = p & 1 ? a.sorted[1] : a.sorted[0];
     const int per = (int)((n + (long long)CTAS * kSortThreads - 1) / ((long long)CTAS * kSortThreads)) * 32;
     const long long first = ((long long)rank * kSortWarps + warp) * per;
     const int share = (int)max(0LL, min((long long)n - first, (long long)per));  // of this warp
-    // a token's id, or -1 if it has no gradient
-    auto key_at = [&](long long i) -> int {
-      if (p > 0) return __ldcg(sk + i);
+    // a token's id, or -1 if it has no gradient, and its position
+    auto id_at = [&](long long i) -> int {
       const long long id = load_id(a.ids, a.id64, a.il.at((int)i));
       if (id < 0 || id >= a.vocab) {
         *a.flag = 1;
@@ -195,8 +193,7 @@ template <int CTAS, int ITEMS, int BITS> __global__ void __launch_bounds__(kSort
       const unsigned same = __match_any_sync(0xffffffffu, d);
       if (d < D) {
         const int at = s.base[d] + s.cnt[warp][d] + __popc(same & below);
-        dk[at] = key;
-        dp[at] = pos;
+        dst[at] = make_int2(key, pos);
       }
       __syncwarp();
       if (d < D && (same & below) == 0) s.cnt[warp][d] += __popc(same);
@@ -207,8 +204,16 @@ template <int CTAS, int ITEMS, int BITS> __global__ void __launch_bounds__(kSort
 #pragma unroll
       for (int i = 0; i < ITEMS; ++i) {
         const int e = e0 + i * 32 + lane;
-        key[i] = e < share ? key_at(first + e) : -1;
-        pos[i] = e < share ? (p > 0 ? __ldcg(sp + first + e) : (int)first + e) : 0;
+        if (e >= share) {
+          key[i] = -1;
+        } else if (p == 0) {
+          key[i] = id_at(first + e);
+          pos[i] = (int)first + e;
+        } else {
+          const int2 v = __ldcg(src + first + e);
+          key[i] = v.x;
+          pos[i] = v.y;
+        }
       }
     };
     load(0);
@@ -395,7 +400,7 @@ __device__ __forceinline__ void write_row(O* dst, const float* acc, float scale,
 // it took 48 us for the sums alone.  32 tokens a chunk: a row's partials then
 // cost at most two fp32 rows for 32 read.
 template <typename G, typename O, int VEC, int NV>
-__global__ void __launch_bounds__(256, VEC == 1 ? 2 : 4) k_row_sums(const int* __restrict__ key, const int* __restrict__ pos, const G* __restrict__ grad, Layout2 gl, int dim,
+__global__ void __launch_bounds__(256, VEC == 1 ? 2 : 4) k_row_sums(const int2* __restrict__ sorted, const G* __restrict__ grad, Layout2 gl, int dim,
                                                   float scale, int accumulate, O* __restrict__ dw, long long stride,
                                                   int dw_aligned, float* __restrict__ part, int chunk, int4* __restrict__ crossing, int* __restrict__ counts, ZeroArgs zero) {
   constexpr int kBatch = VEC == 8 ? 4 : 8;
@@ -414,16 +419,17 @@ __global__ void __launch_bounds__(256, VEC == 1 ? 2 : 4) k_row_sums(const int* _
   const int t = threadIdx.x;
   if (t < m + 2) {
     const int e = e0 + t - 1;
-    s_key[t] = e >= 0 && e < n ? __ldcg(key + e) : -1;
+    const int2 v = e >= 0 && e < n ? __ldcg(sorted + e) : make_int2(-1, 0);
+    s_key[t] = v.x;
+    if (t >= 1 && t <= m) s_off[t - 1] = gl.at(v.y);
   }
-  if (t < m) s_off[t] = gl.at(__ldcg(pos + e0 + t));
   __syncthreads();
   if (t < 32 && blockIdx.y == 0 && s_key[m + 1] == s_key[m] && s_key[0] != s_key[m]) {
     // a row begins here and goes on: into how many chunks, each of which begins with its id
     int more = 0;
     for (;;) {
       const long long e = ((long long)block + 1 + more + t) * chunk;
-      const int found = __popc(__ballot_sync(0xffffffffu, e < n && __ldcg(key + e) == s_key[m]));
+      const int found = __popc(__ballot_sync(0xffffffffu, e < n && __ldcg(sorted + e).x == s_key[m]));
       more += found;
       if (found < 32) break;
     }
@@ -876,8 +882,7 @@ extern "C" int psgd_embedding_create(int64_t vocab, int64_t dim, int64_t max_tok
     bytes += (size + 255) / 256 * 256;
     return at;
   };
-  const long long words = part(16), key0 = part(n * 4), key1 = part(n * 4), pos0 = part(n * 4), pos1 = part(n * 4),
-                  sums = part(chunks * 2 * dim * 4), crossing = part(chunks * 16), counts = part(12),
+  const long long words = part(16), sorted0 = part(n * 8), sorted1 = part(n * 8), sums = part(chunks * 2 * dim * 4), crossing = part(chunks * 16), counts = part(12),
                   named = part((vocab + 15) / 16 * 16);
   if (e == cudaSuccess) e = cudaMalloc(&h->memory, (size_t)bytes);
   if (e != cudaSuccess) h->memory = nullptr;
@@ -892,10 +897,8 @@ extern "C" int psgd_embedding_create(int64_t vocab, int64_t dim, int64_t max_tok
   h->bytes = (size_t)bytes;
   h->d_flag = (int*)(base + words);
   h->ready = h->d_flag + 1;
-  h->key[0] = (int*)(base + key0);
-  h->key[1] = (int*)(base + key1);
-  h->pos[0] = (int*)(base + pos0);
-  h->pos[1] = (int*)(base + pos1);
+  h->sorted[0] = (int2*)(base + sorted0);
+  h->sorted[1] = (int2*)(base + sorted1);
   h->part = (float*)(base + sums);
   h->crossing = (int4*)(base + crossing);
   h->counts = (int*)(base + counts);
@@ -1018,7 +1021,7 @@ extern "C" int psgd_embedding_backward(psgd_embedding* h, const void* ids, int32
     const bool wide = vocab > 256 && vocab <= 1024 && n <= (1 << 18);  // one pass of 10 bits; a CTA's counts fit 16
     int passes = 1;
     while (!wide && passes < 4 && ((vocab - 1) >> (8 * passes)) != 0) ++passes;
-    SortArgs a{ids, id_bits == 64, il, n, vocab, padding_idx, passes, {h->key[0], h->key[1]}, {h->pos[0], h->pos[1]},
+    SortArgs a{ids, id_bits == 64, il, n, vocab, padding_idx, passes, {h->sorted[0], h->sorted[1]},
                h->d_flag, h->counts, accumulate ? nullptr : h->named, h->ready};
     e = n <= 2 * kSortThreads               ? (wide ? launch_sort<1, 2, 10>(a, h->device, st) : launch_sort<1, 2, 8>(a, h->device, st))
         : n <= 2 * kSortThreads * kSortCtas ? (wide ? launch_sort<kSortCtas, 2, 10>(a, h->device, st)
@@ -1027,7 +1030,7 @@ extern "C" int psgd_embedding_backward(psgd_embedding* h, const void* ids, int32
                                                     : launch_sort<kSortCtas, 8, 8>(a, h->device, st));
     const int chunk = chunk_for(n, h->sms);
     const unsigned chunks = (unsigned)((n + (long long)chunk - 1) / chunk);
-    const int *key = h->key[(passes - 1) & 1], *pos = h->pos[(passes - 1) & 1];
+    const int2* sorted = h->sorted[(passes - 1) & 1];
     by_dtype(grad_dtype, [&](auto* gt) {
       using G = std::remove_pointer_t<decltype(gt)>;
       return by_dtype(dweight_dtype, [&](auto* ot) {
@@ -1044,7 +1047,7 @@ extern "C" int psgd_embedding_backward(psgd_embedding* h, const void* ids, int32
                                                (long long)h->sms * kZeroCtas * (256 / threads));
         if (e == cudaSuccess)
           e = launch_early(vec ? k_row_sums<G, O, V, 1> : k_row_sums<G, O, 1, kScalarNv>, dim3(zero.ctas + chunks, p.tiles),
-                           threads, 0, 1, st, key, pos, (const G*)grad, gl, dim, scale, accumulate, (O*)dweight,
+                           threads, 0, 1, st, sorted, (const G*)grad, gl, dim, scale, accumulate, (O*)dweight,
                            dweight_stride, dw_aligned, h->part, chunk, h->crossing, h->counts, zero);
         if ((chunks > 1 || !accumulate) && e == cudaSuccess) {
           const long long items = std::max<long long>(1, chunks - 1) * ((dim + 127) / 128);
