@@ -184,19 +184,34 @@ template <int CTAS, int ITEMS, int BITS> __global__ void __launch_bounds__(kSort
       return id == a.padding ? -1 : (int)id;
     };
     auto digit = [&](int key) { return key < 0 ? D : (key >> shift) & (D - 1); };
-    auto count = [&](int d) {
-      const unsigned same = __match_any_sync(0xffffffffu, d);
-      if (d < D && (same & below) == 0) s.cnt[warp][d] += __popc(same);
-      __syncwarp();
+    auto count = [&](int d) {  // (a warp's own counts; two of 16 bits to a word)
+      if (d >= D) return;
+      if constexpr (sizeof(typename Shared::Count) == 2)
+        atomicAdd(reinterpret_cast<unsigned*>(&s.cnt[warp][d & ~1]), 1u << (16 * (d & 1)));
+      else
+        atomicAdd(&s.cnt[warp][d], 1);
+    };
+    // the lanes with the same digit, bit by bit (__match_any_sync takes several times as long)
+    auto same_digit = [&](int d) {
+      unsigned same = 0xffffffffu;
+#pragma unroll
+      for (int b = 0; b <= BITS; ++b) {
+        const bool bit = d >> b & 1;
+        const unsigned set = __ballot_sync(0xffffffffu, bit);
+        same &= bit ? set : ~set;
+      }
+      return same;
     };
     auto place = [&](int d, int key, int pos) {
-      const unsigned same = __match_any_sync(0xffffffffu, d);
+      const unsigned same = same_digit(d);
+      const int ahead = __popc(same & below);
+      int at = 0;
       if (d < D) {
-        const int at = s.base[d] + s.cnt[warp][d] + __popc(same & below);
-        dst[at] = make_int2(key, pos);
+        at = s.cnt[warp][d];
+        dst[s.base[d] + at + ahead] = make_int2(key, pos);
       }
       __syncwarp();
-      if (d < D && (same & below) == 0) s.cnt[warp][d] += __popc(same);
+      if (d < D && ahead == 0) s.cnt[warp][d] = at + __popc(same);
       __syncwarp();
     };
     int key[ITEMS], pos[ITEMS];
