@@ -145,14 +145,6 @@ template <> __device__ __forceinline__ float top_of<__nv_bfloat16>(const uint4& 
   return fmaxf(__low2float(m), __high2float(m));
 }
 
-// Waits for the first q + 1 of LAST + 1 groups of copies (q known when unrolled).
-template <int LAST> __device__ __forceinline__ void wait_copies(int q) {
-  if (q == LAST) asm volatile("cp.async.wait_group 0;" ::: "memory");
-  else if (q == LAST - 1) asm volatile("cp.async.wait_group 1;" ::: "memory");
-  else if (q == LAST - 2) asm volatile("cp.async.wait_group 2;" ::: "memory");
-  else asm volatile("cp.async.wait_group 3;" ::: "memory");
-}
-
 // Slots of the table in which a row's entries look for equal indices: a power
 // of two, at least twice the entries.
 __host__ __device__ constexpr int table_slots(int k) {
@@ -247,11 +239,11 @@ __device__ __forceinline__ float cluster_join(float v, float2* peers, int ctas, 
 //
 // Two slices of about 100 KB to an SM (rows of more than that are cut over a
 // cluster), one CTA's loads and stores under the other's arithmetic.  8192 rows
-// of 50257 bf16 logits take 282 us (5.85 TB/s, 86 % of the copy bandwidth), 2458
-// rows of 30522 fp32 ones 104 us (5.5 TB/s, 81 %); with the logits read twice
+// of 50257 bf16 logits take 285 us (5.79 TB/s, 86 % of the copy bandwidth), 2458
+// rows of 30522 fp32 ones 105 us (5.4 TB/s, 80 %); with the logits read twice
 // from memory 995 and 202 us.  What is left is the instructions (about 16 an
 // element, the issue slots 60 % full) in the phases that both CTAs of an SM meet
-// in.  Few rows: a row over up to 8 CTAs, five rows of 50257 fp32 5.5 us.
+// in.  Few rows: a row over up to 8 CTAs, five rows of 50257 fp32 5.1 us.
 template <typename Z, bool ALIGNED>
 __global__ void __launch_bounds__(kDistillThreads + 32, 2) k_distill_chip(DistillArgs a, int log_ctas, int slice_granules,
                                                                          int per, int early) {

@@ -75,8 +75,8 @@ __device__ __forceinline__ long long load_id(const void* ids, int id64, long lon
 // thread t owns the vectors t, t + threads, ... (NV of them) of a tile of
 // columns, all of them under way at once.  What finding a token's row costs is
 // paid once per NV vectors.  Bound by the rows' way from L2 and the output's to
-// it: 16384 tokens of a 30522 x 1024 fp32 table 16.1 us (89 MB from and to HBM,
-// 82 % of the copy bandwidth; 134 MB through L2); with one vector a thread and
+// it: 16384 tokens of a 30522 x 1024 fp32 table 15.5 us (89 MB from and to HBM,
+// 85 % of the copy bandwidth; 134 MB through L2); with one vector a thread and
 // four tokens at a time 25 us, with two tokens 17.5.
 template <typename W, typename O, int VEC, int NV>
 __global__ void __launch_bounds__(256) k_lookup(const W* __restrict__ weight, long long wstride, long long vocab,
@@ -148,9 +148,11 @@ template <int BITS> struct SortShared {
 // in registers between counting and placing.  The time is the chain of
 // latencies of a pass (a load, the barriers, a scan, a scattered store), so
 // tables of up to 1024 rows take one pass of 10 bits in place of two of 8, and
-// up to 2048 tokens one CTA without a cluster's barriers.  16384 tokens of
-// 30522 rows take about 12 us on 8 of the SMs while the others zero the rows
-// that no token names; 4491 tokens of 512 rows 6 us (9 in two passes).
+// up to 2048 tokens one CTA without a cluster's barriers.  Digits are counted by
+// shared-memory atomics; when elements are placed, a warp's equal digits are
+// found by a ballot per bit.  16384 tokens of 30522 rows take 17 us profiled
+// alone from a cold cache, on 8 of the SMs while the others zero the rows that
+// no token names.
 template <int CTAS, int ITEMS, int BITS> __global__ void __launch_bounds__(kSortThreads) k_sort_tokens(SortArgs a) {
   using Shared = SortShared<BITS>;
   constexpr int D = Shared::kDigits, PARTS = Shared::kParts, PER = kSortWarps / PARTS;
@@ -413,12 +415,16 @@ __device__ __forceinline__ void write_row(O* dst, const float* acc, float scale,
 // HBM: with the zeroing, 192 MB of BERT-large's table gradient in 31 us (6.2
 // TB/s, 92 % of the copy bandwidth).  One column a thread and one row at a time
 // it took 48 us for the sums alone.  32 tokens a chunk: a row's partials then
-// cost at most two fp32 rows for 32 read.
+// cost at most two fp32 rows for 32 read.  Rows at any alignment (VEC 1): all
+// granules of the chunk's rows are copied into shared memory at once, and read
+// from there element by element: 32768 tokens of 30000 x 1601 bf16 80 us with
+// the sort, 109 with single loads into registers, which leave too few under way.
 template <typename G, typename O, int VEC, int NV>
-__global__ void __launch_bounds__(256, VEC == 1 ? 2 : 4) k_row_sums(const int2* __restrict__ sorted, const G* __restrict__ grad, Layout2 gl, int dim,
+__global__ void __launch_bounds__(256, VEC == 1 ? 3 : 4) k_row_sums(const int2* __restrict__ sorted, const G* __restrict__ grad, Layout2 gl, int dim,
                                                   float scale, int accumulate, O* __restrict__ dw, long long stride,
                                                   int dw_aligned, float* __restrict__ part, int chunk, int4* __restrict__ crossing, int* __restrict__ counts, ZeroArgs zero) {
   constexpr int kBatch = VEC == 8 ? 4 : 8;
+  extern __shared__ __align__(16) unsigned char slots[];  // the chunk's rows, if VEC is 1
   __shared__ long long s_off[kMaxChunk];
   __shared__ int s_key[kMaxChunk + 2];  // with the tokens on both sides (-1: none)
   next_may_launch();
@@ -439,6 +445,16 @@ __global__ void __launch_bounds__(256, VEC == 1 ? 2 : 4) k_row_sums(const int2* 
     if (t >= 1 && t <= m) s_off[t - 1] = gl.at(v.y);
   }
   __syncthreads();
+  const int tile = blockIdx.y * blockDim.x * NV, slot = slot_bytes(blockDim.x * NV, sizeof(G));
+  if constexpr (VEC == 1) {
+    const int columns = min((int)blockDim.x * NV, dim - tile);
+#pragma unroll
+    for (int b = 0; b < kMaxChunk; b += kBatch) {
+      for (int k = b + t / 32; k < min(b + kBatch, m); k += blockDim.x / 32)
+        copy_row(slots + k * slot, grad, 1, s_off[k] + tile, columns, t & 31, 32);
+      commit_copies();
+    }
+  }
   if (t < 32 && blockIdx.y == 0 && s_key[m + 1] == s_key[m] && s_key[0] != s_key[m]) {
     // a row begins here and goes on: into how many chunks, each of which begins with its id
     int more = 0;
@@ -455,7 +471,7 @@ __global__ void __launch_bounds__(256, VEC == 1 ? 2 : 4) k_row_sums(const int2* 
     }
   }
   const int c0 = (blockIdx.y * blockDim.x * NV + t) * VEC, step = blockDim.x * VEC;
-  if (c0 >= dim) return;
+  if (VEC > 1 && c0 >= dim) return;
   float acc[NV][VEC];
 #pragma unroll
   for (int j = 0; j < NV; ++j)
@@ -464,12 +480,23 @@ __global__ void __launch_bounds__(256, VEC == 1 ? 2 : 4) k_row_sums(const int2* 
   bool open = s_key[0] == s_key[1];  // the first id's tokens began in an earlier chunk
   for (int b = 0; b < m; b += kBatch) {
     Pack<G, VEC> v[kBatch][NV];
+    if constexpr (VEC == 1) {
+      wait_copies<kMaxChunk / kBatch - 1>(b / kBatch);
+      __syncthreads();
+    }
 #pragma unroll
     for (int k = 0; k < kBatch; ++k) {
       if (b + k < m) {
+        const G* row = grad + s_off[b + k];
+        if constexpr (VEC == 1) {
+          const G* mine = (const G*)(slots + (b + k) * slot + ((uintptr_t)(row + tile) & 15)) + t;
 #pragma unroll
-        for (int j = 0; j < NV; ++j)
-          if (c0 + j * step < dim) v[k][j] = load_pack<G, VEC>(grad + s_off[b + k] + c0 + j * step);
+          for (int j = 0; j < NV; ++j) v[k][j].v[0] = mine[j * step];
+        } else {
+#pragma unroll
+          for (int j = 0; j < NV; ++j)
+            if (c0 + j * step < dim) v[k][j] = load_pack<G, VEC>(row + c0 + j * step);
+        }
       }
     }
 #pragma unroll
@@ -513,8 +540,8 @@ __global__ void __launch_bounds__(256, VEC == 1 ? 2 : 4) k_row_sums(const int2* 
 // threads, the others by all groups, each over a contiguous part of the row's
 // tokens.  blockDim = (threads of a group, groups).  Shared memory: per token a
 // byte and two integers, and the groups' partial sums.  Bound by latency, or by
-// writing the table: 64 tokens of 300 rows of 1024 fp32 columns 4.0 us, of 30522
-// rows 22.7 us (125 MB, 5.5 TB/s).
+// writing the table: 64 tokens of 300 rows of 1024 fp32 columns 3.5 us, of 30522
+// rows 22.1 us (125 MB, 5.7 TB/s).
 constexpr int kAlone = 16;
 constexpr int kMaxSpan = 32;
 
@@ -803,7 +830,7 @@ bool aligned_rows(const void* p, long long s0, long long s1, int size, int to) {
 
 // How a row is spread over threads: tiles of columns (grid.y), threads of a
 // group, groups of a CTA.
-constexpr int kScalarNv = 4;   // elements per thread and row where accesses are single elements
+constexpr int kScalarNv = 4;   // elements per thread and row of the one-launch gradient where accesses are single elements
 constexpr int kLookupNv = 16;  // the same in a lookup
 struct TilePlan {
   int threads, groups, tiles;
@@ -821,9 +848,9 @@ TilePlan plan_tile(long long dim, int vec, int nv) {
 // Rows of the table per CTA of the one-launch gradient, or 0 where the sorted
 // one is used: every CTA looks at all ids, and a row's tokens are not split
 // over CTAs.  GPU time of one launch against the sorted three, 1024 fp32
-// columns: 16 tokens of a 300-row table 3.6 and 7.5 us, 512 7.5 and 10.6, 2048
-// 19.1 and 16.1; 256 tokens of 30522 rows 24.3 and 28.0 (with 640 bf16 columns
-// 17.3 and 15.1).
+// columns: 16 tokens of a 300-row table 3.1 and 7.2 us, 512 6.8 and 9.3, 2048
+// 19.1 and 13.5; 256 tokens of 3000 rows 8.9 and 10.8; 64 tokens of 30522 rows
+// 22.1 and 26.3 (with 640 bf16 columns 12.6 and 14.3).
 int direct_span(int n, int vocab) {
   if (n > 1024 || n > 16LL * vocab) return 0;
   const int span = std::min(kMaxSpan, (vocab + 1215) / 1216);
@@ -1053,16 +1080,21 @@ extern "C" int psgd_embedding_backward(psgd_embedding* h, const void* ids, int32
         constexpr int V = Vec16<G>::N;
         const bool vec = dim % V == 0 && aligned_rows(grad, grad_outer_stride, grad_inner_stride, sizeof(G), 16);
         const int dw_aligned = aligned_rows(dweight, dweight_stride, 0, sizeof(O), run_alignment(V, sizeof(O)));
-        const TilePlan p = plan_tile(dim, vec ? V : 1, vec ? 1 : kScalarNv);
+        constexpr int NV = 8 / sizeof(G);  // columns per thread, if single: a slot is about 2 KB then
+        TilePlan p = plan_tile(dim, vec ? V : 1, vec ? 1 : NV);
+        if (!vec) p.threads = (int)(((long long)(dim + p.tiles - 1) / p.tiles + 32 * NV - 1) / (32 * NV)) * 32;  // even tiles
         const int threads = std::max(p.threads, 64);
+        const size_t smem = vec ? 0 : (size_t)chunk * slot_bytes(threads * NV, sizeof(G));
+        auto kernel = vec ? k_row_sums<G, O, V, 1> : k_row_sums<G, O, 1, NV>;
+        static std::atomic<unsigned long long> raised{0};
+        if (e == cudaSuccess && !vec) e = raise_smem(kernel, raised, h->device, kMaxChunk * slot_bytes(256 * NV, sizeof(G)));
         // zeroing: about 64 KB or 32 rows a CTA, up to kZeroCtas CTAs of 256 threads to an SM
         ZeroArgs zero{0, (char*)dweight, (long long)dim * osize, dweight_stride * osize, vocab, h->named, h->ready};
         if (!accumulate)
           zero.ctas = (int)std::min<long long>(std::max<long long>(vocab * zero.bytes / 65536, (vocab + 31) / 32),
                                                (long long)h->sms * kZeroCtas * (256 / threads));
         if (e == cudaSuccess)
-          e = launch_early(vec ? k_row_sums<G, O, V, 1> : k_row_sums<G, O, 1, kScalarNv>, dim3(zero.ctas + chunks, p.tiles),
-                           threads, 0, 1, st, sorted, (const G*)grad, gl, dim, scale, accumulate, (O*)dweight,
+          e = launch_early(kernel, dim3(zero.ctas + chunks, p.tiles), threads, smem, 1, st, sorted, (const G*)grad, gl, dim, scale, accumulate, (O*)dweight,
                            dweight_stride, dw_aligned, h->part, chunk, h->crossing, h->counts, zero);
         if ((chunks > 1 || !accumulate) && e == cudaSuccess) {
           const long long items = std::max<long long>(1, chunks - 1) * ((dim + 127) / 128);

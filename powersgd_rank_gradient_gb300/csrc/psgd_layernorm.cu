@@ -128,7 +128,7 @@ template <int NE> __device__ __forceinline__ void load_param(const void* w, int 
 // shared memory, by the thread that will use them, so no barrier is needed for
 // them and no register holds what is under way.  Both are bound by HBM once
 // there is enough of it: forward 65536 x 1024 bf16 41 us (6.5 TB/s), 16384 rows
-// 13.7 us, three of which are the launch and the first rows' way; backward 65536
+// 12.9 us, three of which are the launch and the first rows' way; backward 65536
 // x 1600 bf16 94 us with the columns' sums (6.7 TB/s, 99 % of the copy
 // bandwidth; 173 us with plain loads one batch at a time, whose instructions and
 // latency bound it).  Four rows at a time share the barriers and shuffles of one
@@ -394,33 +394,9 @@ __global__ void __launch_bounds__(kMaxThreads, 1) k_norm_backward_vec(RowsArgs a
 // granules are copied ahead into shared memory at the row's own place within
 // its first granule, and read from there element by element.  Bound by the
 // instructions that takes: backward 30001 x 1023 fp16 45 us (4.1 TB/s), fp32 67 us
-// (5.5 TB/s).  A barrier of the group follows
-// each wait, as a granule is used by other threads than the one that copied it.
+// (5.5 TB/s).  A barrier of the group follows each wait, as a granule is used by
+// other threads than the one that copied it.
 //
-// Starts the copy of row `index` of an array: granule u, u + step, ... into
-// `slot`.  The bytes in front of a row within its first granule are the array's
-// own where the row begins that far into it; elsewhere there may be nothing to
-// read, and the granule's elements are copied one by one.
-template <typename T>
-__device__ __forceinline__ void copy_row(unsigned char* slot, const T* base, int index, long long stride, int dim, int u,
-                                         int step) {
-  const T* row = base + index * stride;
-  const int before = (int)((uintptr_t)row & 15);
-  const int bytes = before + dim * (int)sizeof(T);
-  const unsigned char* src = (const unsigned char*)row - before;
-  if (u == 0 && index * stride * (long long)sizeof(T) < before) {
-    for (int e = before; e < min(16, bytes); e += (int)sizeof(T)) *(T*)(slot + e) = *(const T*)(src + e);
-    u += step;
-  }
-  unsigned to = (unsigned)__cvta_generic_to_shared(slot) + u * 16;
-  src += u * 16;
-  for (int left = bytes - u * 16; left > 0; left -= step * 16) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(src), "r"(min(16, left)) : "memory");
-    to += step * 16;
-    src += step * 16;
-  }
-}
-
 // How the warps of a group share the copies of `items` rows: warp w takes the
 // items first, first + step, ..., and of each the granules of part `part` of
 // `parts`.
@@ -433,9 +409,6 @@ struct CopyShare {
     step = parts > 1 ? items : warps;  // (with parts, warps that are left over have first >= items)
   }
 };
-// Bytes of a row's place in shared memory: `columns` elements (the columns of
-// all threads) from any place of the first granule on.
-__host__ __device__ inline int slot_bytes(int columns, int size) { return (columns * size + 15 + 15) / 16 * 16; }
 
 // `a` where `keep` is not 0, else 0 (not a product: what lies behind a row may
 // be anything).

@@ -246,6 +246,41 @@ __device__ __forceinline__ void copy4(void* dst, const void* src) {
 }
 __device__ __forceinline__ void commit_copies() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 
+// Waits for the first q + 1 of LAST + 1 groups of copies.
+template <int LAST> __device__ __forceinline__ void wait_copies(int q) {
+  if (q == LAST) asm volatile("cp.async.wait_group 0;" ::: "memory");
+  else if (q == LAST - 1) asm volatile("cp.async.wait_group 1;" ::: "memory");
+  else if (q == LAST - 2) asm volatile("cp.async.wait_group 2;" ::: "memory");
+  else asm volatile("cp.async.wait_group 3;" ::: "memory");
+}
+
+// Starts the copy of row `index` of an array: granule u, u + step, ... into
+// `slot`.  The bytes in front of a row within its first granule are the array's
+// own where the row begins that far into it; elsewhere there may be nothing to
+// read, and the granule's elements are copied one by one.
+template <typename T>
+__device__ __forceinline__ void copy_row(unsigned char* slot, const T* base, int index, long long stride, int dim, int u,
+                                         int step) {
+  const T* row = base + index * stride;
+  const int before = (int)((uintptr_t)row & 15);
+  const int bytes = before + dim * (int)sizeof(T);
+  const unsigned char* src = (const unsigned char*)row - before;
+  if (u == 0 && index * stride * (long long)sizeof(T) < before) {
+    for (int e = before; e < min(16, bytes); e += (int)sizeof(T)) *(T*)(slot + e) = *(const T*)(src + e);
+    u += step;
+  }
+  unsigned to = (unsigned)__cvta_generic_to_shared(slot) + u * 16;
+  src += u * 16;
+  for (int left = bytes - u * 16; left > 0; left -= step * 16) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(src), "r"(min(16, left)) : "memory");
+    to += step * 16;
+    src += step * 16;
+  }
+}
+// Bytes of a row's place in shared memory: `columns` elements (the columns of
+// all threads) from any place of the first granule on.
+__host__ __device__ inline int slot_bytes(int columns, int size) { return (columns * size + 15 + 15) / 16 * 16; }
+
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);

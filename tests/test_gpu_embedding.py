@@ -242,6 +242,29 @@ def test_grad_strides_and_broadcast():
         assert bool((room[:, :7] == 5.0).all()) and bool((room[:, 39:] == 5.0).all())
 
 
+@pytest.mark.parametrize("gdtype", tu.DTYPES)
+@pytest.mark.parametrize("dim", [5, 33, 513, 1025, 2100])
+@pytest.mark.parametrize("tokens", [1300, 12000])
+def test_grad_rows_between_other_values(gdtype, dim, tokens):
+    """Gradient rows of every alignment, as columns of an array whose other columns are NaN."""
+    e = embedding(1500, dim, tokens)
+    ids = make_ids((tokens,), 1500, 1, hot=0.1)
+    for first in (1, 7):
+        room = torch.full((tokens + 1, dim + 10), float("nan"), dtype=gdtype, device=DEV)
+        grad = room[1:, first:first + dim]
+        grad.copy_(randn((tokens, dim), gdtype, 2 + first))
+        bucket, view = guarded(1500, dim, F32, 1)
+        e.backward(ids, grad, out=view)
+        dw, mag, count = tu.table_grad(ids, grad, 1500, 1.0)
+        tu.check(view, dw, tu.table_grad_tol(dw, mag, count, F32))
+        untouched(bucket, 1, 1500 * dim)
+    flat = torch.full((tokens * dim + 9,), float("nan"), dtype=gdtype, device=DEV)
+    grad = flat[1:1 + tokens * dim].view(tokens, dim)  # the first row begins within the first granule
+    grad.copy_(randn((tokens, dim), gdtype, 5))
+    dw, mag, count = tu.table_grad(ids, grad, 1500, 1.0)
+    tu.check(e.backward(ids, grad), dw, tu.table_grad_tol(dw, mag, count, F32))
+
+
 def test_grad_out_of_range_ids_add_nothing_and_are_reported():
     e = embedding(10, 16, 100)
     ids = torch.tensor([3, -1, 9, 10, 2**33 + 3, -2**31 - 1, 0, 3], device=DEV)
