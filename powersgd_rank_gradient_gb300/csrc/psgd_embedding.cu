@@ -23,6 +23,7 @@ namespace cg = cooperative_groups;
 struct psgd_embedding {
   int device = 0;
   int sms = 0;
+  bool many_sort_ctas = false;  // this device runs clusters of 16 CTAs
   long long vocab = 0, dim = 0, max_tokens = 0;
   void* memory = nullptr;  // all of the following
   // the sorted tokens: two (id, position) buffers the radix passes alternate between
@@ -49,6 +50,7 @@ constexpr int kJoinWarps = 8;
 // not reach the write rate alone.
 constexpr int kZeroCtas = 4;
 constexpr int kSortCtas = 8;        // CTAs of the sort's cluster
+constexpr int kManySortCtas = 16;   // the same for many tokens: more than 8 is not portable
 constexpr int kSortThreads = 1024;
 constexpr int kSortWarps = kSortThreads / 32;
 
@@ -126,14 +128,14 @@ struct SortArgs {
   int* ready;
 };
 
-template <int BITS> struct SortShared {
+template <int CTAS, int BITS> struct SortShared {
   // a CTA's counts fit 16 bits where a digit has 10 (the host sees to it)
   using Count = typename std::conditional<(BITS > 8), unsigned short, int>::type;
   static constexpr int kDigits = 1 << BITS;
   static constexpr int kParts = kSortThreads / kDigits;  // threads per digit of the scan over the warps
   Count cnt[kSortWarps][kDigits];
   int part[kParts][kDigits];
-  int totals[kSortCtas][kDigits];  // every CTA's digit totals, pushed by the peers
+  int totals[CTAS][kDigits];  // every CTA's digit totals, pushed by the peers
   int base[kDigits];
   int scan[32];
   int all;
@@ -152,9 +154,9 @@ template <int BITS> struct SortShared {
 // shared-memory atomics; when elements are placed, a warp's equal digits are
 // found by a ballot per bit.  16384 tokens of 30522 rows take 17 us profiled
 // alone from a cold cache, on 8 of the SMs while the others zero the rows that
-// no token names.
+// no token names (with 16 CTAs the whole gradient takes 1 to 3 us less).
 template <int CTAS, int ITEMS, int BITS> __global__ void __launch_bounds__(kSortThreads) k_sort_tokens(SortArgs a) {
-  using Shared = SortShared<BITS>;
+  using Shared = SortShared<CTAS, BITS>;
   constexpr int D = Shared::kDigits, PARTS = Shared::kParts, PER = kSortWarps / PARTS;
   extern __shared__ __align__(16) unsigned char raw[];
   Shared& s = *reinterpret_cast<Shared*>(raw);
@@ -417,8 +419,9 @@ __device__ __forceinline__ void write_row(O* dst, const float* acc, float scale,
 // it took 48 us for the sums alone.  32 tokens a chunk: a row's partials then
 // cost at most two fp32 rows for 32 read.  Rows at any alignment (VEC 1): all
 // granules of the chunk's rows are copied into shared memory at once, and read
-// from there element by element: 32768 tokens of 30000 x 1601 bf16 80 us with
-// the sort, 109 with single loads into registers, which leave too few under way.
+// from there element by element: 32768 tokens of 30000 x 1601 bf16 77 us with
+// the sort (80 before its cluster had 16 CTAs, 109 then with single loads into
+// registers, which leave too few under way).
 template <typename G, typename O, int VEC, int NV>
 __global__ void __launch_bounds__(256, VEC == 1 ? 3 : 4) k_row_sums(const int2* __restrict__ sorted, const G* __restrict__ grad, Layout2 gl, int dim,
                                                   float scale, int accumulate, O* __restrict__ dw, long long stride,
@@ -797,11 +800,40 @@ template <typename F> int by_dtype(int32_t d, F&& f) {
   }
 }
 
+template <int CTAS, int ITEMS, int BITS> cudaError_t allow_sort(int device) {
+  static std::atomic<unsigned long long> raised{0}, large{0};
+  cudaError_t e = raise_smem(k_sort_tokens<CTAS, ITEMS, BITS>, raised, device, (int)sizeof(SortShared<CTAS, BITS>));
+  const unsigned long long bit = 1ull << device;
+  if (CTAS > 8 && e == cudaSuccess && !(large.load(std::memory_order_acquire) & bit)) {
+    e = cudaFuncSetAttribute(k_sort_tokens<CTAS, ITEMS, BITS>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e == cudaSuccess) large.fetch_or(bit, std::memory_order_release);
+  }
+  return e;
+}
+
 template <int CTAS, int ITEMS, int BITS> cudaError_t launch_sort(const SortArgs& a, int device, cudaStream_t st) {
-  constexpr int bytes = (int)sizeof(SortShared<BITS>);
-  static std::atomic<unsigned long long> raised{0};
-  const cudaError_t e = raise_smem(k_sort_tokens<CTAS, ITEMS, BITS>, raised, device, bytes);
+  constexpr int bytes = (int)sizeof(SortShared<CTAS, BITS>);
+  const cudaError_t e = allow_sort<CTAS, ITEMS, BITS>(device);
   return e != cudaSuccess ? e : launch_early(k_sort_tokens<CTAS, ITEMS, BITS>, CTAS, kSortThreads, bytes, CTAS, st, a);
+}
+
+// Whether a cluster of kManySortCtas of the sort's largest CTAs can run.
+bool runs_many_sort_ctas(int device) {
+  cudaLaunchAttribute attr = {};
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = kManySortCtas;
+  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = kManySortCtas;
+  cfg.blockDim = kSortThreads;
+  cfg.dynamicSmemBytes = sizeof(SortShared<kManySortCtas, 10>);
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  int clusters = 0;
+  const bool ok = allow_sort<kManySortCtas, 8, 10>(device) == cudaSuccess &&
+                  cudaOccupancyMaxActiveClusters(&clusters, k_sort_tokens<kManySortCtas, 8, 10>, &cfg) == cudaSuccess;
+  if (!ok) cudaGetLastError();  // not an error: clusters of 8 do it too
+  return ok && clusters > 0;
 }
 
 // Sorted tokens per CTA of the row sums: 32, or 8 to 16 where that would leave
@@ -915,6 +947,7 @@ extern "C" int psgd_embedding_create(int64_t vocab, int64_t dim, int64_t max_tok
   h->dim = dim;
   h->max_tokens = max_tokens;
   e = cudaDeviceGetAttribute(&h->sms, cudaDevAttrMultiProcessorCount, device);
+  if (e == cudaSuccess) h->many_sort_ctas = runs_many_sort_ctas(device);
   const long long n = std::max<long long>(1, max_tokens);
   const long long chunks = max_chunks(n, h->sms);
   // one allocation, cut into 256-byte aligned parts
@@ -1065,11 +1098,19 @@ extern "C" int psgd_embedding_backward(psgd_embedding* h, const void* ids, int32
     while (!wide && passes < 4 && ((vocab - 1) >> (8 * passes)) != 0) ++passes;
     SortArgs a{ids, id_bits == 64, il, n, vocab, padding_idx, passes, {h->sorted[0], h->sorted[1]},
                h->d_flag, h->counts, accumulate ? nullptr : h->named, h->ready};
-    e = n <= 2 * kSortThreads               ? (wide ? launch_sort<1, 2, 10>(a, h->device, st) : launch_sort<1, 2, 8>(a, h->device, st))
-        : n <= 2 * kSortThreads * kSortCtas ? (wide ? launch_sort<kSortCtas, 2, 10>(a, h->device, st)
-                                                    : launch_sort<kSortCtas, 2, 8>(a, h->device, st))
-                                            : (wide ? launch_sort<kSortCtas, 8, 10>(a, h->device, st)
-                                                    : launch_sort<kSortCtas, 8, 8>(a, h->device, st));
+    // A cluster of 16 where each CTA has enough to do.  GPU time of the gradient
+    // with 8 and 16: 4491 tokens of 512 rows 13.9 and 15.4 us, 16384 of 600 x 64
+    // bf16 18.0 and 18.9, 65536 34.2 and 33.0; of 30000 x 64 4096 18.1 and 17.6,
+    // 16384 24.8 and 21.8, 65536 46.0 and 38.5.
+    const bool many = h->many_sort_ctas && n > (wide ? 16384 : 8192);
+    auto sort = [&](auto bits) {
+      constexpr int BITS = decltype(bits)::value;
+      if (n <= 2 * kSortThreads) return launch_sort<1, 2, BITS>(a, h->device, st);
+      if (!many) return launch_sort<kSortCtas, 2, BITS>(a, h->device, st);
+      return n <= 2 * kSortThreads * kManySortCtas ? launch_sort<kManySortCtas, 2, BITS>(a, h->device, st)
+                                                   : launch_sort<kManySortCtas, 8, BITS>(a, h->device, st);
+    };
+    e = wide ? sort(std::integral_constant<int, 10>{}) : sort(std::integral_constant<int, 8>{});
     const int chunk = chunk_for(n, h->sms);
     const unsigned chunks = (unsigned)((n + (long long)chunk - 1) / chunk);
     const int2* sorted = h->sorted[(passes - 1) & 1];

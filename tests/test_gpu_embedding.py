@@ -242,6 +242,12 @@ def test_grad_strides_and_broadcast():
         assert bool((room[:, :7] == 5.0).all()) and bool((room[:, 39:] == 5.0).all())
 
 
+@pytest.mark.parametrize("vocab", [513, 1025, 66000])
+@pytest.mark.parametrize("tokens", [8192, 8193, 32768, 32769, 100000])
+def test_grad_sort_sizes(vocab, tokens):
+    run_grad(vocab, 12, (tokens,), F32, F32, 1, hot=0.1, padding=3)
+
+
 @pytest.mark.parametrize("gdtype", tu.DTYPES)
 @pytest.mark.parametrize("dim", [5, 33, 513, 1025, 2100])
 @pytest.mark.parametrize("tokens", [1300, 12000])
