@@ -152,9 +152,9 @@ template <int CTAS, int BITS> struct SortShared {
 // tables of up to 1024 rows take one pass of 10 bits in place of two of 8, and
 // up to 2048 tokens one CTA without a cluster's barriers.  Digits are counted by
 // shared-memory atomics; when elements are placed, a warp's equal digits are
-// found by a ballot per bit.  16384 tokens of 30522 rows take 17 us profiled
-// alone from a cold cache, on 8 of the SMs while the others zero the rows that
-// no token names (with 16 CTAs the whole gradient takes 1 to 3 us less).
+// found by a ballot per bit.  16384 tokens of 30522 rows take 14 us profiled
+// alone from a cold cache, on 16 of the SMs while the others zero the rows that
+// no token names (17 us on 8 SMs).
 template <int CTAS, int ITEMS, int BITS> __global__ void __launch_bounds__(kSortThreads) k_sort_tokens(SortArgs a) {
   using Shared = SortShared<CTAS, BITS>;
   constexpr int D = Shared::kDigits, PARTS = Shared::kParts, PER = kSortWarps / PARTS;
