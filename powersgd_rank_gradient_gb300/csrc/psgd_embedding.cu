@@ -166,7 +166,7 @@ template <int CTAS, int ITEMS, int BITS> __global__ void __launch_bounds__(kSort
   after_previous();  // and with it the row sums' kernel, which starts when this one lets it
   if (a.named) {  // (its size is rounded up to 16 bytes)
     uint4* v = reinterpret_cast<uint4*>(a.named);
-    for (int i = rank * kSortThreads + t; i < (a.vocab + 15) / 16; i += CTAS * kSortThreads) v[i] = make_uint4(0, 0, 0, 0);
+    for (int i = rank * kSortThreads + t; i < (int)units(a.vocab, 16); i += CTAS * kSortThreads) v[i] = make_uint4(0, 0, 0, 0);
   }
   if constexpr (CTAS > 1) asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
   const unsigned below = (1u << lane) - 1u;
@@ -885,8 +885,8 @@ TilePlan plan_tile(long long dim, int vec, int nv) {
 // 22.1 and 26.3 (with 640 bf16 columns 12.6 and 14.3).
 int direct_span(int n, int vocab) {
   if (n > 1024 || n > 16LL * vocab) return 0;
-  const int span = std::min(kMaxSpan, (vocab + 1215) / 1216);
-  return (long long)((vocab + span - 1) / span) * n <= (1 << 18) ? span : 0;
+  const int span = (int)std::min<long long>(kMaxSpan, units(vocab, 1216));
+  return units(vocab, span) * n <= (1 << 18) ? span : 0;
 }
 
 int check_ids(const char* who, const psgd_embedding* e, const void* ids, int32_t id_bits, int64_t outer, int64_t inner,
@@ -1069,7 +1069,7 @@ extern "C" int psgd_embedding_backward(psgd_embedding* h, const void* ids, int32
   cudaError_t e = cudaSuccess;
   if (n == 0) {
     if (!accumulate)
-      e = launch_early(k_zero_table, (unsigned)std::min<long long>((vocab + 7) / 8, h->sms * 8), 256, 0, 1, st,
+      e = launch_early(k_zero_table, (unsigned)std::min<long long>(units(vocab, 8), h->sms * 8), 256, 0, 1, st,
                        (char*)dweight, vocab, (long long)dim * osize, dweight_stride * osize);
   } else if (const int span = direct_span(n, vocab)) {
     by_dtype(grad_dtype, [&](auto* gt) {
@@ -1086,7 +1086,7 @@ extern "C" int psgd_embedding_backward(psgd_embedding* h, const void* ids, int32
         static std::atomic<unsigned long long> raised[2];
         e = raise_smem(kernel, raised[vec], h->device, 64 * 1024);
         if (e == cudaSuccess)
-          e = launch_early(kernel, dim3((vocab + span - 1) / span, p.tiles), dim3(p.threads, groups), smem, 1, st, ids,
+          e = launch_early(kernel, dim3((unsigned)units(vocab, span), p.tiles), dim3(p.threads, groups), smem, 1, st, ids,
                            id_bits == 64, il, n, vocab, padding_idx, h->d_flag, (const G*)grad, gl, dim, scale, accumulate,
                            (O*)dweight, dweight_stride, dw_aligned, span);
         return 0;
@@ -1132,7 +1132,7 @@ extern "C" int psgd_embedding_backward(psgd_embedding* h, const void* ids, int32
         // zeroing: about 64 KB or 32 rows a CTA, up to kZeroCtas CTAs of 256 threads to an SM
         ZeroArgs zero{0, (char*)dweight, (long long)dim * osize, dweight_stride * osize, vocab, h->named, h->ready};
         if (!accumulate)
-          zero.ctas = (int)std::min<long long>(std::max<long long>(vocab * zero.bytes / 65536, (vocab + 31) / 32),
+          zero.ctas = (int)std::min<long long>(std::max<long long>(vocab * zero.bytes / 65536, units(vocab, 32)),
                                                (long long)h->sms * kZeroCtas * (256 / threads));
         if (e == cudaSuccess)
           e = launch_early(kernel, dim3(zero.ctas + chunks, p.tiles), threads, smem, 1, st, sorted, (const G*)grad, gl, dim, scale, accumulate, (O*)dweight,

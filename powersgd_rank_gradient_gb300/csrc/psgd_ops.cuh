@@ -45,6 +45,10 @@ inline bool dtype_ok(int32_t d) { return d == PSGD_F32 || d == PSGD_F16 || d == 
 inline int dtype_size(int32_t d) { return d == PSGD_F32 ? 4 : 2; }
 inline bool aligned16(const void* p) { return ((uintptr_t)p & 15) == 0; }
 
+// How many units of `of` hold n (of both at least 1).  In 64 bits: n may be as
+// large as its type, and n + of - 1 then needs more.
+__host__ __device__ inline long long units(long long n, long long of) { return (n + of - 1) / of; }
+
 // Whether [a, a + an) and [b, b + bn) share a byte (NULL ranges share none).
 inline bool overlap(const void* a, long long an, const void* b, long long bn) {
   if (!a || !b || an <= 0 || bn <= 0) return false;
