@@ -91,7 +91,9 @@ __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.w
 // again with the difference first, 2^(c (z_j - max)).
 //
 // The teacher's entries of one row: validity (at[k], -1 where not), and their
-// softmax p[k].  Returns whether the row counts at all.
+// softmax p[k].  Returns whether the row counts at all.  The largest logit comes
+// off before the temperature: a rounding is then relative to the distance
+// between two logits, however far from zero both are, and none overflows.
 __device__ __forceinline__ bool teacher_softmax(const DistillArgs& a, long long row, float w, float* p, int* at,
                                                 float* buf) {
   const float inv_t = a.inv_t;
@@ -101,7 +103,7 @@ __device__ __forceinline__ bool teacher_softmax(const DistillArgs& a, long long 
     const long long i = a.index64 ? __ldg((const long long*)a.index + row * a.is + k)
                                   : (long long)__ldg((const int*)a.index + row * a.is + k);
     const bool valid = i >= 0 && i < a.vocab;
-    const float t = valid ? load_any(a.t, a.tdtype, row * a.ts + k) * inv_t : -INFINITY;
+    const float t = valid ? load_any(a.t, a.tdtype, row * a.ts + k) : -INFINITY;
     at[k] = valid ? (int)i : -1;
     p[k] = t;
     m = fmaxf(m, t);
@@ -111,7 +113,7 @@ __device__ __forceinline__ bool teacher_softmax(const DistillArgs& a, long long 
   m = block_max(m, buf);
   float s = 0.f;
   for (int k = threadIdx.x; k < a.k; k += blockDim.x) {
-    const float e = at[k] >= 0 ? expf(p[k] - m) : 0.f;
+    const float e = at[k] >= 0 ? expf((p[k] - m) * inv_t) : 0.f;
     p[k] = e;
     s += e;
   }
@@ -169,7 +171,7 @@ __device__ __forceinline__ int teacher_warp(const DistillArgs& a, long long row,
                                   : (long long)__ldg((const int*)a.index + row * a.is + k);
     const float tk = load_any(a.t, a.tdtype, row * a.ts + k);
     const bool valid = i >= 0 && i < a.vocab;
-    const float t = valid ? tk * inv_t : -INFINITY;
+    const float t = valid ? tk : -INFINITY;
     at[k] = valid ? (int)i : -1;
     p[k] = t;
     m = fmaxf(m, t);
@@ -191,7 +193,7 @@ __device__ __forceinline__ int teacher_warp(const DistillArgs& a, long long row,
   m = warp_max(m);
   float s = 0.f;
   for (int k = lane; k < a.k; k += 32) {
-    const float e = at[k] >= 0 ? expf(p[k] - m) : 0.f;
+    const float e = at[k] >= 0 ? expf((p[k] - m) * inv_t) : 0.f;
     p[k] = e;
     s += e;
   }
