@@ -129,7 +129,7 @@ template <int NE> __device__ __forceinline__ void load_param(const void* w, int 
 // them and no register holds what is under way.  Both are bound by HBM once
 // there is enough of it: forward 65536 x 1024 bf16 41 us (6.5 TB/s), 16384 rows
 // 12.9 us, three of which are the launch and the first rows' way; backward 65536
-// x 1600 bf16 94 us with the columns' sums (6.7 TB/s, 99 % of the copy
+// x 1600 bf16 96 us with the columns' sums (6.6 TB/s, 97 % of the copy
 // bandwidth; 173 us with plain loads one batch at a time, whose instructions and
 // latency bound it).  Four rows at a time share the barriers and shuffles of one
 // reduction (forward: 14.8 us with two).
@@ -240,8 +240,11 @@ __global__ void __launch_bounds__(kMaxThreads, NV == 1 && R == 1 ? 2 : 1) k_norm
   }
 }
 
-// dx = rstd a - rstd m0 - (x - mu) rstd^2 m1, with m0 = mean(a) and m1 = rstd mean(a (x - mu)):
-// the mean comes off x first, so rows far from zero lose nothing.
+// dx = rstd a - rstd m0 - xh rstd m1, with m0 = mean(a) and m1 = mean(a xh).  The
+// mean comes off x first, so rows far from zero lose nothing, and rstd meets each
+// deviation before anything else does: products of gradients and deviations, or
+// powers of rstd, would leave fp32's range where the result does not (rstd is
+// 1e19 and more where eps is 0 and a row hardly varies).
 template <typename T, int NV, int R>
 __global__ void __launch_bounds__(kMaxThreads, 1) k_norm_backward_vec(RowsArgs a) {
   constexpr int NE = Vec16<T>::N, NP = NE / 2;
@@ -316,10 +319,10 @@ __global__ void __launch_bounds__(kMaxThreads, 1) k_norm_backward_vec(RowsArgs a
             to_pairs<T>(data[((r * NV + j) * 2 + 1) * kMaxThreads], g);
 #pragma unroll
             for (int h = 0; h < NP; ++h) {
-              const F2 gd = mul(g[h], add(x[h], nm));
+              const F2 gx = mul(g[h], mul(add(x[h], nm), rs));
               s0 = fma(g[h], w[j][h], s0);
-              s1 = fma(gd, w[j][h], s1);
-              dw[j][h] = fma(gd, rs, dw[j][h]);
+              s1 = fma(gx, w[j][h], s1);
+              dw[j][h] = add(dw[j][h], gx);
               db[j][h] = add(db[j][h], g[h]);
             }
           }
@@ -337,7 +340,7 @@ __global__ void __launch_bounds__(kMaxThreads, 1) k_norm_backward_vec(RowsArgs a
       for (int r = 0; r < R; ++r) {
         if (r >= rows) break;
         const float mean = stat[2 * r], rstd = stat[2 * r + 1];
-        const float c0 = -s[2 * r] * inv * rstd, c1 = -s[2 * r + 1] * inv * rstd * rstd * rstd;
+        const float c0 = -s[2 * r] * inv * rstd, c1 = -s[2 * r + 1] * inv * rstd;
         const F2 nm = f2(-mean, -mean), rs = f2(rstd, rstd), k0 = f2(c0, c0), k1 = f2(c1, c1);
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
@@ -348,7 +351,7 @@ __global__ void __launch_bounds__(kMaxThreads, 1) k_norm_backward_vec(RowsArgs a
           float f[NE];
 #pragma unroll
           for (int h = 0; h < NP; ++h)
-            split(fma(mul(g[h], w[j][h]), rs, fma(add(x[h], nm), k1, k0)), f[2 * h], f[2 * h + 1]);
+            split(fma(mul(g[h], w[j][h]), rs, fma(mul(add(x[h], nm), rs), k1, k0)), f[2 * h], f[2 * h + 1]);
           store_pack<T, NE>(to + r * a.ys + j * threads * NE, f);
         }
       }
@@ -590,7 +593,7 @@ __global__ void __launch_bounds__(kMaxThreads, 1) k_norm_backward_any(RowsArgs a
     issue(stage == 0 ? kStages - 1 : stage - 1);
     const float* stat = stats[stage][group];
     const int rows = min(R, (int)a.rows - row);
-    F2 d[R][NP], g[R][NP];
+    F2 xh[R][NP], g[R][NP];
     float s[2 * R];
 #pragma unroll
     for (int r = 0; r < R; ++r) {
@@ -602,16 +605,16 @@ __global__ void __launch_bounds__(kMaxThreads, 1) k_norm_backward_any(RowsArgs a
         const F2 nm = f2(-stat[2 * r], -stat[2 * r]), rs = f2(stat[2 * r + 1], stat[2 * r + 1]);
 #pragma unroll
         for (int j = 0; j < NP; ++j) {
-          d[r][j] = add(pair_at(x + 2 * j * 32), nm);
+          xh[r][j] = mul(add(pair_at(x + 2 * j * 32), nm), rs);
           g[r][j] = pair_at(y + 2 * j * 32);
           if ((2 * j + 2) * 32 > left) {
-            d[r][j] = only(d[r][j], keep[j]);
+            xh[r][j] = only(xh[r][j], keep[j]);
             g[r][j] = only(g[r][j], keep[j]);
           }
-          const F2 gd = mul(g[r][j], d[r][j]);
+          const F2 gx = mul(g[r][j], xh[r][j]);
           s0 = fma(g[r][j], w[j], s0);
-          s1 = fma(gd, w[j], s1);
-          dw[j] = fma(gd, rs, dw[j]);
+          s1 = fma(gx, w[j], s1);
+          dw[j] = add(dw[j], gx);
           db[j] = add(db[j], g[r][j]);
         }
       }
@@ -629,13 +632,13 @@ __global__ void __launch_bounds__(kMaxThreads, 1) k_norm_backward_any(RowsArgs a
     for (int r = 0; r < R; ++r) {
       if (r >= rows) break;
       const float rstd = stat[2 * r + 1];
-      const float c0 = -s[2 * r] * inv * rstd, c1 = -s[2 * r + 1] * inv * rstd * rstd * rstd;
+      const float c0 = -s[2 * r] * inv * rstd, c1 = -s[2 * r + 1] * inv * rstd;
       const F2 rs = f2(rstd, rstd), k0 = f2(c0, c0), k1 = f2(c1, c1);
       T* dst = to + r * a.ys;
 #pragma unroll
       for (int j = 0; j < NP; ++j) {
         float u, v;
-        split(fma(mul(g[r][j], w[j]), rs, fma(d[r][j], k1, k0)), u, v);
+        split(fma(mul(g[r][j], w[j]), rs, fma(xh[r][j], k1, k0)), u, v);
         if (lane + 2 * j * 32 < left) dst[2 * j * 32] = from_f<T>(u);
         if (lane + (2 * j + 1) * 32 < left) dst[(2 * j + 1) * 32] = from_f<T>(v);
       }
