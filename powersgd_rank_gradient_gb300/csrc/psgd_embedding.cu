@@ -910,8 +910,11 @@ int check_rows(const char* who, const char* what, const void* p, int32_t dtype, 
   if (!dtype_ok(dtype)) return fail(PSGD_EINVAL, w + ": unknown dtype");
   if (outer * inner > 0 && !p) return fail(PSGD_EINVAL, w + " is NULL");
   if (!span_ok(outer, os) || !span_ok(inner, is)) return fail(PSGD_EINVAL, w + ": bad stride");
-  if (written && ((inner > 1 && is < dim) || (outer > 1 && os < (inner - 1) * is + dim)))
-    return fail(PSGD_EINVAL, w + ": rows overlap");
+  if (!written || outer == 0 || inner == 0) return PSGD_OK;
+  // rows apart: all inner ones before the next outer one, or all outer ones before the next inner one
+  const bool inner_first = (inner == 1 || is >= dim) && (outer == 1 || os >= (inner - 1) * is + dim);
+  const bool outer_first = (outer == 1 || os >= dim) && (inner == 1 || is >= (outer - 1) * os + dim);
+  if (!inner_first && !outer_first) return fail(PSGD_EINVAL, w + ": rows overlap");
   return PSGD_OK;
 }
 
