@@ -959,10 +959,13 @@ extern "C" int psgd_layernorm_forward(psgd_layernorm* h, const void* x, psgd_dty
   if (rc) return rc;
   if (!(eps >= 0.f) || !isfinite(eps)) return fail(PSGD_EINVAL, "psgd_layernorm_forward: eps must be finite and >= 0");
   if (rows == 0) return PSGD_OK;
-  const long long yb = extent(rows, h->dim, y_stride, dtype), pb = h->dim * dtype_size(param_dtype);
-  if (overlap(y, yb, x, extent(rows, h->dim, x_stride, dtype)) || overlap(y, yb, weight, pb) ||
-      overlap(y, yb, bias, pb) || overlap(y, yb, mean, rows * 4) || overlap(y, yb, rstd, rows * 4))
-    return fail(PSGD_EINVAL, "psgd_layernorm_forward: y overlaps another operand");
+  const long long yb = extent(rows, h->dim, y_stride, dtype), xb = extent(rows, h->dim, x_stride, dtype);
+  const long long pb = h->dim * dtype_size(param_dtype), sb = rows * 4;
+  for (const auto& o : {std::pair<const void*, long long>(y, yb), {mean, sb}, {rstd, sb}})
+    if (overlap(o.first, o.second, x, xb) || overlap(o.first, o.second, weight, pb) || overlap(o.first, o.second, bias, pb))
+      return fail(PSGD_EINVAL, "psgd_layernorm_forward: an output overlaps an input");
+  if (overlap(y, yb, mean, sb) || overlap(y, yb, rstd, sb) || overlap(mean, sb, rstd, sb))
+    return fail(PSGD_EINVAL, "psgd_layernorm_forward: the outputs overlap");
   DeviceScope scope(h->device);
   const cudaStream_t st = (cudaStream_t)stream;
   RowsArgs a{x, nullptr, weight, bias, y, mean, rstd, nullptr, x_stride, 0, y_stride, rows, (int)h->dim,
