@@ -9,8 +9,11 @@ every source file, the public header, this script, the compiler flags and
 existing ``libpsgd.so`` is reused only when it carries that exact hash and was
 built for this machine's architecture.  The training operators' Python binding
 ``_bind.so`` (host code only, against torch's and Python's headers) is built
-beside it and carries the same hash with torch's and Python's versions.  ``-Xptxas -v`` register, spill and
-shared-memory lines of every kernel are written to ``_build/ptxas.log``.
+beside it and carries the same hash with torch's and Python's versions.  The
+library needs nvcc alone: where torch, its CUDA headers, Python's headers or g++
+are missing the binding is left out with a note, and where the binding does not
+compile the library is in place before that is raised.  ``-Xptxas -v`` register,
+spill and shared-memory lines of every kernel are written to ``_build/ptxas.log``.
 """
 
 from __future__ import annotations
@@ -116,12 +119,26 @@ def _bind_command(obj):
             sysconfig.get_paths()["include"], "-c", os.path.join(CSRC, BIND_SOURCE), "-o", obj]
 
 
-def build(force: bool = False, verbose: bool = False) -> str:
-    import torch
+def _binding_obstacle():
+    """Why this machine cannot build the binding, or None."""
+    try:
+        import torch
+    except Exception as e:  # ImportError, or a library that torch itself misses
+        return f"torch cannot be imported ({e})"
+    for header in (os.path.join(os.path.dirname(torch.__file__), "include", "c10", "cuda", "CUDAStream.h"),
+                   os.path.join(sysconfig.get_paths()["include"], "Python.h")):
+        if not os.path.exists(header):
+            return f"{header} is missing"
+    return None if shutil.which("g++") else "g++ is missing"
 
-    want, want_bind = source_hash(), bind_hash()
+
+def build(force: bool = False, verbose: bool = False) -> str:
+    obstacle = _binding_obstacle()
+    want, want_bind = source_hash(), None if obstacle else bind_hash()
     lib_ok = not force and library_hash() == want
-    bind_ok = not force and library_hash(BIND, BIND_MARKER) == want_bind
+    bind_ok = bool(obstacle) or (not force and library_hash(BIND, BIND_MARKER) == want_bind)
+    if obstacle:
+        print(f"the training operators' Python binding is not built: {obstacle}", file=sys.stderr)
     if lib_ok and bind_ok:
         return LIB
     os.makedirs(BUILD, exist_ok=True)
@@ -142,13 +159,13 @@ def build(force: bool = False, verbose: bool = False) -> str:
     sources = ([] if bind_ok else [BIND_SOURCE]) + ([] if lib_ok else SOURCES)
     workers = min(len(sources), max(1, os.cpu_count() or 1))
     with concurrent.futures.ThreadPoolExecutor(max_workers=workers) as ex:
-        results = list(ex.map(compile_one, sources))
+        jobs = {src: ex.submit(compile_one, src) for src in sources}
     if not lib_ok:
+        results = [jobs[src].result() for src in SOURCES]
         with open(PTXAS_LOG, "w") as log:
             log.write(f"source hash {want}\n")
             for src, err in results:
-                if src != BIND_SOURCE:
-                    log.write(f"==== {src}\n{err}")
+                log.write(f"==== {src}\n{err}")
         if verbose:
             for src, err in results:
                 spills = [ln for ln in err.splitlines() if "spill" in ln and not ln.strip().startswith("0 bytes")]
@@ -160,6 +177,9 @@ def build(force: bool = False, verbose: bool = False) -> str:
         if library_hash() != want:
             raise RuntimeError("the built library does not carry its source hash")
     if not bind_ok:
+        import torch
+
+        jobs[BIND_SOURCE].result()
         torch_lib = os.path.join(os.path.dirname(torch.__file__), "lib")
         _link(["g++", "-shared"], [os.path.join(BUILD, "psgd_bind.o"), "-L", HERE, "-l:libpsgd.so", "-Wl,-rpath,$ORIGIN",
                                   "-L", torch_lib, "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"], BIND)

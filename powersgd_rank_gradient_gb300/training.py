@@ -23,7 +23,8 @@ from ._lib import PSGD_BAD_TOKEN, check
 _lib.lib()  # the library itself; raises with how to build it where it is missing
 if not os.path.exists(os.path.join(_lib.HERE, "_bind.so")):
     raise RuntimeError(f"{_lib.HERE}/_bind.so is missing: build it with "
-                       "`python -c 'import __graft_entry__ as g; g.build()'`")
+                       "`python -c 'import __graft_entry__ as g; g.build()'` "
+                       "(it needs a CUDA build of torch, Python's headers and g++)")
 from . import _bind  # noqa: E402  (argument checks and calls, compiled: psgd_bind.cpp)
 
 
