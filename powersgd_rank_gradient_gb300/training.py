@@ -37,8 +37,15 @@ def _device(device):
     return torch.device("cuda", torch.cuda.current_device()) if device.index is None else device
 
 
-def _stream(stream, index):
-    return (torch.cuda.current_stream(index) if stream is None else stream).cuda_stream
+def _of_device(stream, index):
+    """``stream``, which must belong to CUDA device ``index``."""
+    if stream.device.index != index:
+        raise ValueError(f"stream must be on cuda:{index}, got {stream.device}")
+    return stream
+
+
+def _on(stream, index):
+    return torch.cuda.stream(_of_device(stream, index))
 
 
 class Embedding:
@@ -85,7 +92,7 @@ class Embedding:
         ``out`` or a new tensor of ``out_dtype`` (default: the weight's)."""
         if stream is None:
             return _bind.embedding_forward(self._spec, weight, ids, out, out_dtype)
-        with torch.cuda.stream(stream):
+        with _on(stream, self.device.index):
             return _bind.embedding_forward(self._spec, weight, ids, out, out_dtype)
 
     def backward(self, ids, grad, out=None, accumulate=False, stream=None):
@@ -94,12 +101,14 @@ class Embedding:
         new fp32 tensor), over what it holds or, with ``accumulate``, added to it."""
         if stream is None:
             return _bind.embedding_backward(self._spec, ids, grad, out, accumulate)
-        with torch.cuda.stream(stream):
+        with _on(stream, self.device.index):
             return _bind.embedding_backward(self._spec, ids, grad, out, accumulate)
 
     def status(self, stream=None):
         """Synchronises; True when an id outside the table was met since the last status()."""
-        return check(self._lib.psgd_embedding_status(self._h, _stream(stream, self.device.index))) == PSGD_BAD_TOKEN
+        index = self.device.index
+        stream = torch.cuda.current_stream(index) if stream is None else _of_device(stream, index)
+        return check(self._lib.psgd_embedding_status(self._h, stream.cuda_stream)) == PSGD_BAD_TOKEN
 
     def workspace_bytes(self):
         return int(self._lib.psgd_embedding_workspace_bytes(self._h))
@@ -136,7 +145,7 @@ class LayerNorm:
         """(y, mean, rstd); mean and rstd (fp32, one a row) are what backward takes."""
         if stream is None:
             return _bind.layernorm_forward(self._spec, x, weight, bias, out)
-        with torch.cuda.stream(stream):
+        with _on(stream, self.device.index):
             return _bind.layernorm_forward(self._spec, x, weight, bias, out)
 
     def backward(self, grad, x, mean, rstd, weight=None, dx=None, dweight=None, dbias=None, accumulate=False,
@@ -145,7 +154,7 @@ class LayerNorm:
         vectors) are overwritten or, with ``accumulate``, added to."""
         if stream is None:
             return _bind.layernorm_backward(self._spec, grad, x, mean, rstd, weight, dx, dweight, dbias, accumulate)
-        with torch.cuda.stream(stream):
+        with _on(stream, self.device.index):
             return _bind.layernorm_backward(self._spec, grad, x, mean, rstd, weight, dx, dweight, dbias, accumulate)
 
     def workspace_bytes(self):
@@ -164,5 +173,6 @@ def distill_loss(logits, teacher_logits, teacher_indices, temperature=1.0, weigh
     itself.  with_grad=False: (losses, None)."""
     if stream is None:
         return _bind.distill(logits, teacher_logits, teacher_indices, temperature, weights, grad_scale, dlogits, with_grad)
-    with torch.cuda.stream(stream):
+    index = logits.get_device() if isinstance(logits, torch.Tensor) and logits.is_cuda else stream.device.index
+    with _on(stream, index):
         return _bind.distill(logits, teacher_logits, teacher_indices, temperature, weights, grad_scale, dlogits, with_grad)
