@@ -1,9 +1,13 @@
 // Python binding of the training operators' calls (include/psgd.h): argument
 // checks, outputs and the current stream for training.py.  A call of one token
 // or one row takes the GPU two or three microseconds, less than the same checks
-// take in Python, so they are compiled; nothing is computed here.
+// take in Python, so they are compiled; nothing is computed here.  Autograd does
+// not see these calls: while it records, operands that require a gradient are
+// refused, and what a call writes advances its tensor's version, so that a value
+// saved before is known to be overwritten.
 #include <Python.h>
 
+#include <ATen/core/grad_mode.h>
 #include <ATen/ops/empty.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Dtype.h>
@@ -51,6 +55,15 @@ std::string str(at::IntArrayRef v) {
 const at::Tensor& tensor(PyObject* o, const char* what) {
   if (!THPVariable_Check(o)) throw ValueError{std::string(what) + " must be a tensor"};
   return THPVariable_Unpack(o);
+}
+
+// A tensor whose values (not indices) a call reads or writes.
+const at::Tensor& values(PyObject* o, const char* what) {
+  const at::Tensor& t = tensor(o, what);
+  if (t.requires_grad() && at::GradMode::is_enabled())
+    throw ValueError{std::string(what) + " requires a gradient, which this call does not record: use torch.no_grad(), and "
+                     "the operator's own gradient"};
+  return t;
 }
 
 void on_device(const at::Tensor& t, int index, const char* what) {
@@ -156,8 +169,10 @@ template <typename F> int call(F&& f) {
   Py_END_ALLOW_THREADS return rc;
 }
 
+// The written tensor as Python's object: the caller's, or a new one.
 PyObject* given_or_new(PyObject* given, at::Tensor made) {
   if (given != Py_None) {
+    if (!made.is_inference()) made.unsafeGetTensorImpl()->bump_version();
     Py_INCREF(given);
     return given;
   }
@@ -282,7 +297,7 @@ TokenRows token_rows_of(const Spec& s, const at::Tensor& t, at::IntArrayRef ids,
 PyObject* py_embedding_forward(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return guarded(n, 5, [&]() -> PyObject* {
     const Spec& s = *spec_of(a[0]);
-    const at::Tensor &weight = tensor(a[1], "weight"), &ids = tensor(a[2], "ids");
+    const at::Tensor &weight = values(a[1], "weight"), &ids = tensor(a[2], "ids");
     const Table w = table_of(s, weight, "weight");
     const int bits = id_bits_of(ids, s.index, "ids");
     const Layout l = layout_of(ids.sizes(), ids.strides(), ids.sizes().size(), "ids");
@@ -302,7 +317,7 @@ PyObject* py_embedding_forward(PyObject*, PyObject* const* a, Py_ssize_t n) {
       out = fresh(shape, type, s.index);
       o = {static_cast<psgd_dtype>(d), l.inner * s.dim, s.dim};
     } else {
-      out = tensor(a[3], "out");
+      out = values(a[3], "out");
       o = token_rows_of(s, out, ids.sizes(), "out");
     }
     void* stream = stream_of(s.index);
@@ -319,13 +334,13 @@ PyObject* py_embedding_forward(PyObject*, PyObject* const* a, Py_ssize_t n) {
 PyObject* py_embedding_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return guarded(n, 5, [&]() -> PyObject* {
     const Spec& s = *spec_of(a[0]);
-    const at::Tensor &ids = tensor(a[1], "ids"), &grad = tensor(a[2], "grad");
+    const at::Tensor &ids = tensor(a[1], "ids"), &grad = values(a[2], "grad");
     const int bits = id_bits_of(ids, s.index, "ids");
     const Layout l = layout_of(ids.sizes(), ids.strides(), ids.sizes().size(), "ids");
     const TokenRows g = token_rows_of(s, grad, ids.sizes(), "grad");
     const bool accumulate = truth(a[4]);
     if (a[3] == Py_None && accumulate) throw ValueError{"accumulate needs an out to add to"};
-    at::Tensor out = a[3] == Py_None ? fresh({s.rows, s.dim}, at::kFloat, s.index) : tensor(a[3], "out");
+    at::Tensor out = a[3] == Py_None ? fresh({s.rows, s.dim}, at::kFloat, s.index) : values(a[3], "out");
     const Table w = table_of(s, out, "out");
     void* stream = stream_of(s.index);
     check(call([&] {
@@ -349,7 +364,7 @@ struct Pair {
 };
 const at::Tensor* vector_of(const Spec& s, PyObject* o, const char* what) {
   if (o == Py_None) return nullptr;
-  const at::Tensor& t = tensor(o, what);
+  const at::Tensor& t = values(o, what);
   if (t.dim() != 1 || t.size(0) != s.dim || !t.is_contiguous())
     throw ValueError{std::string(what) + " must be a contiguous vector of " + std::to_string(s.dim) + " elements"};
   return &t;
@@ -377,7 +392,7 @@ int64_t stride_like(const Spec& s, const at::Tensor& t, const at::Tensor& x, con
 PyObject* py_layernorm_forward(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return guarded(n, 5, [&]() -> PyObject* {
     const Spec& s = *spec_of(a[0]);
-    const at::Tensor& x = tensor(a[1], "x");
+    const at::Tensor& x = values(a[1], "x");
     const psgd_dtype d = dtype_of(x, s.index, "x");
     const Rows r = rows_of(x, s.dim, "x");
     const Pair p = pair_of(s, vector_of(s, a[2], "weight"), vector_of(s, a[3], "bias"), "weight", "bias");
@@ -386,7 +401,7 @@ PyObject* py_layernorm_forward(PyObject*, PyObject* const* a, Py_ssize_t n) {
     if (a[4] == Py_None) {
       out = fresh(x.sizes(), x.scalar_type(), s.index);
     } else {
-      out = tensor(a[4], "out");
+      out = values(a[4], "out");
       ys = stride_like(s, out, x, "out");
     }
     const auto lead = x.sizes().slice(0, x.sizes().size() - 1);
@@ -407,7 +422,7 @@ PyObject* py_layernorm_forward(PyObject*, PyObject* const* a, Py_ssize_t n) {
 }
 
 const float* stat_of(const Spec& s, PyObject* o, int64_t rows, const char* what) {
-  const at::Tensor& t = tensor(o, what);
+  const at::Tensor& t = values(o, what);
   if (t.scalar_type() != at::kFloat || t.numel() != rows || !t.is_contiguous())
     throw ValueError{std::string(what) + " must be a contiguous float32 tensor of " + std::to_string(rows) + " elements"};
   on_device(t, s.index, what);
@@ -418,7 +433,7 @@ const float* stat_of(const Spec& s, PyObject* o, int64_t rows, const char* what)
 PyObject* py_layernorm_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return guarded(n, 10, [&]() -> PyObject* {
     const Spec& s = *spec_of(a[0]);
-    const at::Tensor &grad = tensor(a[1], "grad"), &x = tensor(a[2], "x");
+    const at::Tensor &grad = values(a[1], "grad"), &x = values(a[2], "x");
     const psgd_dtype d = dtype_of(x, s.index, "x");
     const Rows r = rows_of(x, s.dim, "x");
     const int64_t gs = stride_like(s, grad, x, "grad");
@@ -429,7 +444,7 @@ PyObject* py_layernorm_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
     if (a[6] == Py_None) {
       dx = fresh(x.sizes(), x.scalar_type(), s.index);
     } else {
-      dx = tensor(a[6], "dx");
+      dx = values(a[6], "dx");
       ds = stride_like(s, dx, x, "dx");
     }
     const bool accumulate = truth(a[9]);
@@ -455,7 +470,7 @@ PyObject* py_layernorm_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
 // distill(logits, teacher_logits, teacher_indices, temperature, weights, grad_scale, dlogits, with_grad)
 PyObject* py_distill(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return guarded(n, 8, [&]() -> PyObject* {
-    const at::Tensor &z = tensor(a[0], "logits"), &t = tensor(a[1], "teacher_logits"), &at_ = tensor(a[2], "teacher_indices");
+    const at::Tensor &z = values(a[0], "logits"), &t = values(a[1], "teacher_logits"), &at_ = tensor(a[2], "teacher_indices");
     if (!z.is_cuda()) throw ValueError{"logits must be a CUDA tensor"};
     const int index = z.get_device();
     const auto shape = z.sizes();
@@ -473,7 +488,7 @@ PyObject* py_distill(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const int64_t ts = rows_of(t, k, "teacher_logits").stride, ns = rows_of(at_, k, "teacher_indices").stride;
     const float* w = nullptr;
     if (a[4] != Py_None) {
-      const at::Tensor& wt = tensor(a[4], "weights");
+      const at::Tensor& wt = values(a[4], "weights");
       if (wt.scalar_type() != at::kFloat || wt.sizes() != lead || !wt.is_contiguous())
         throw ValueError{"weights must be a contiguous float32 tensor of the logits' leading shape"};
       on_device(wt, index, "weights");
@@ -488,7 +503,7 @@ PyObject* py_distill(PyObject*, PyObject* const* a, Py_ssize_t n) {
       dz = fresh(shape, z.scalar_type(), index);
       ds = vocab;
     } else {
-      dz = tensor(a[6], "dlogits");
+      dz = values(a[6], "dlogits");
       if (dz.sizes() != shape || dz.scalar_type() != z.scalar_type())
         throw ValueError{"dlogits must have the logits' shape and type"};
       on_device(dz, index, "dlogits");

@@ -8,6 +8,10 @@ the caller passes, typically views of a flat replica bucket at any element
 offset and in the bucket's type, so that ``powerSGD_hook`` takes the bucket as
 it is.  torch is used for device memory and streams; the arithmetic runs in the
 CUDA kernels of libpsgd.so.
+
+Autograd does not see these calls: each gradient is a call of its own.  While
+autograd records (outside ``torch.no_grad()``), an operand that requires a
+gradient raises ValueError in place of giving a result without one.
 """
 
 from __future__ import annotations
