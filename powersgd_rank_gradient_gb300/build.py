@@ -113,7 +113,8 @@ def _bind_command(obj):
 
     inc = os.path.join(os.path.dirname(torch.__file__), "include")
     cuda = os.path.join(os.path.dirname(os.path.dirname(_nvcc())), "include")
-    return ["g++", *BIND_FLAGS, f'-DPSGD_BIND_HASH="{bind_hash()}"',
+    return ["g++", *BIND_FLAGS, f'-DPSGD_BIND_HASH="{bind_hash()}"', f'-DPSGD_SOURCE_HASH="{source_hash()}"',
+            f'-DPSGD_BIND_TORCH="{torch.__version__}"',
             f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-isystem", inc, "-isystem",
             os.path.join(inc, "torch", "csrc", "api", "include"), "-isystem", cuda, "-isystem",
             sysconfig.get_paths()["include"], "-c", os.path.join(CSRC, BIND_SOURCE), "-o", obj]

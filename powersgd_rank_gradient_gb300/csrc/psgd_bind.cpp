@@ -22,6 +22,12 @@
 #ifndef PSGD_BIND_HASH
 #define PSGD_BIND_HASH "unknown"
 #endif
+#ifndef PSGD_SOURCE_HASH
+#define PSGD_SOURCE_HASH "unknown"
+#endif
+#ifndef PSGD_BIND_TORCH
+#define PSGD_BIND_TORCH "unknown"
+#endif
 
 namespace {
 
@@ -530,7 +536,12 @@ PyObject* py_distill(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
-PyObject* py_bind_id(PyObject*, PyObject*) { return PyUnicode_FromString("psgd-bind-hash:" PSGD_BIND_HASH); }
+// What this file was built against: the library's build id, torch's version.
+// (The hash is what build.py looks for.)
+PyObject* py_built_with(PyObject*, PyObject*) {
+  static const char hash[] = "psgd-bind-hash:" PSGD_BIND_HASH;
+  return Py_BuildValue("(sss)", "psgd-source-hash:" PSGD_SOURCE_HASH, PSGD_BIND_TORCH, hash);
+}
 
 #define FAST(f) reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(f)), METH_FASTCALL
 PyMethodDef kMethods[] = {
@@ -541,7 +552,7 @@ PyMethodDef kMethods[] = {
     {"layernorm_forward", FAST(py_layernorm_forward), nullptr},
     {"layernorm_backward", FAST(py_layernorm_backward), nullptr},
     {"distill", FAST(py_distill), nullptr},
-    {"bind_id", py_bind_id, METH_NOARGS, nullptr},
+    {"built_with", py_built_with, METH_NOARGS, nullptr},
     {nullptr, nullptr, 0, nullptr},
 };
 PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "_bind", "Calls of the training operators.", -1, kMethods,

@@ -32,6 +32,17 @@ if not os.path.exists(os.path.join(_lib.HERE, "_bind.so")):
 from . import _bind  # noqa: E402  (argument checks and calls, compiled: psgd_bind.cpp)
 
 
+def _check_binding(built_with, library, torch_version):
+    """The binding calls the library and torch through their headers: both must be the ones it was compiled against."""
+    for what, built, found in zip(("library", "torch"), built_with, (library, torch_version)):
+        if built != found:
+            raise RuntimeError(f"_bind.so was built against another {what} ({built}) than the one loaded ({found}): build it again "
+                               "with `python -c 'import __graft_entry__ as g; g.build()'`")
+
+
+_check_binding(_bind.built_with(), _lib.lib().psgd_build_id().decode(), str(torch.__version__))
+
+
 def _device(device):
     if device is None:
         device = torch.cuda.current_device()
