@@ -43,3 +43,34 @@ def test_statistics_overlap_nothing():
         assert forward(n, x, w, b, y, m, r) == _lib.PSGD_EINVAL
         assert "overlap" in _lib.lib().psgd_last_error().decode()
     assert all(torch.equal(s, t) for s, t in zip(before, (x, w, b)))
+
+
+def backward(n, grad, x, mean, rstd, w, dx, dw, db):
+    from powersgd_rank_gradient_gb300 import _lib
+
+    dim = x.shape[1]
+    return _lib.lib().psgd_layernorm_backward(n._h, at(grad), dim, at(x), CODES[x.dtype], dim, x.shape[0], at(mean), at(rstd), at(w),
+                                              0, at(dx), dim, at(dw), at(db), 0, 0, torch.cuda.current_stream().cuda_stream)
+
+
+# rows of whole 16-byte units, of any length, and too long for registers
+@pytest.mark.parametrize("dtype", [F32, F16, BF16])
+@pytest.mark.parametrize("dim", [64, 1600, 333, 1023, 20000])
+@pytest.mark.parametrize("rows", [0, 1, 3, 1300])
+def test_outputs_that_are_left_out(dtype, dim, rows):
+    """Whatever is left out, the others are the same bits."""
+    from powersgd_rank_gradient_gb300 import LayerNorm, _lib
+
+    n = LayerNorm(dim, device=DEV)
+    x, g, w, b = randn((rows, dim), 1, dtype, 1.5), randn((rows, dim), 2, dtype), randn((dim,), 3), randn((dim,), 4)
+    want = n.forward(x, w, b)
+    for keep in ((0, 0), (1, 0), (0, 1)):
+        y = torch.full_like(want[0], 3.0)
+        stats = [torch.full_like(want[1 + i], 3.0) if keep[i] else None for i in range(2)]
+        assert forward(n, x, w, b, y, *stats) == _lib.PSGD_OK
+        assert torch.equal(y, want[0]) and all(s is None or torch.equal(s, want[1 + i]) for i, s in enumerate(stats))
+    grads = n.backward(g, x, want[1], want[2], w)
+    for keep in range(8):
+        outs = [torch.full_like(t, 3.0) if keep >> i & 1 else None for i, t in enumerate(grads)]
+        assert backward(n, g, x, want[1], want[2], w, *outs) == _lib.PSGD_OK
+        assert all(o is None or torch.equal(o, t) for o, t in zip(outs, grads)), keep

@@ -47,3 +47,13 @@ def test_large_gradients_of_large_activations(dim):
     mean = d.mean(1)
     rstd = ((d - mean[:, None]).square().mean(1) + 1e-5).rsqrt()
     verify(x, grad, w, mean.float(), rstd.float(), 1e-5)
+
+
+@pytest.mark.parametrize("dim", [64, 1000, 1023, 9001])
+def test_rows_far_from_zero_and_without_variance(dim):
+    from powersgd_rank_gradient_gb300 import LayerNorm
+
+    x, grad, w = randn((12, dim), 1, 0.1) + 1000.0, randn((12, dim), 2), randn((dim,), 3)
+    x[3], x[4], x[5] = 5.0, 0.0, -1e-30
+    _, mean, rstd = LayerNorm(dim, device=DEV).forward(x, w)
+    verify(x, grad, w, mean, rstd, 1e-5)
