@@ -827,6 +827,14 @@ template <int R1, typename F> void with_vec_plan(const RowPlan& p, bool few, F&&
   else if (p.nv == 2) f(Int<2>(), Int<2>());
   else f(Int<4>(), Int<1>());
 }
+// Few rows: one at a time, so that more CTAs have some.  Forward, one row at a
+// time against four: up to a row for every group of an SM's CTA 0.73 to 0.96 of
+// the time (304 x 1600 bf16 2.4 us, 3.0 with four), at two and more 1.1 to 1.5
+// times (608 x 1600 3.7 and 2.9, 608 x 4096 5.4 and 3.5; 64 columns 1.8 and 2.1
+// at two, 2.3 and 2.1 at four).  Backward: up to two rows 0.8 to 0.98, at four 0.88 to 1.09 (1216 x 1600 7.0 and 7.8, 608 x 2048 fp32 6.1
+// and 5.6), from eight on 1.0 to 1.2 (4864 x 1600 15.6 and 15.0, 4864 x 4096 30 and 25).
+bool few_forward(const RowPlan& p, long long rows, int sms) { return rows <= (long long)sms * p.groups; }
+bool few_backward(const RowPlan& p, long long rows, int sms) { return rows <= 4LL * sms * p.groups; }
 int vec_rows(const RowPlan& p, int r1, bool few) { return p.nv == 1 ? (few ? 1 : r1) : p.nv == 2 ? 2 : 1; }
 template <typename F> void with_scalar_plan(const RowPlan& p, F&& f) {
   if (p.nv == 4) f(Int<4>(), Int<4>());
@@ -980,9 +988,9 @@ extern "C" int psgd_layernorm_forward(psgd_layernorm* h, const void* x, psgd_dty
       k_norm_forward_long<T><<<(unsigned)std::min<long long>(rows, h->sms * 4), kMaxThreads, 0, st>>>(a);
       e = cudaGetLastError();
     } else if (vec) {
-      const bool few = rows < (long long)h->sms * 8 * p.groups;
+      const bool few = few_forward(p, rows, h->sms);
       const long long per = (long long)p.groups * vec_rows(p, 4, few);
-      const unsigned grid = (unsigned)std::min<long long>((rows + per - 1) / per, h->sms * (p.nv == 1 && few ? 2 : 1));
+      const unsigned grid = (unsigned)std::min<long long>((rows + per - 1) / per, h->sms);
       with_vec_plan<4>(p, few, [&](auto nv, auto r) {
         e = launch_forward<T, decltype(nv)::value, decltype(r)::value>(a, p, grid, h->device, st);
       });
@@ -1044,7 +1052,7 @@ extern "C" int psgd_layernorm_backward(psgd_layernorm* h, const void* grad, int6
         }
         e = cudaGetLastError();
       } else if (vec) {
-        const bool few = rows < (long long)h->sms * 8 * p.groups;
+        const bool few = few_backward(p, rows, h->sms);
         const long long per = (long long)p.groups * vec_rows(p, 4, few);
         parts = (int)std::min<long long>((rows + per - 1) / per, h->sms);
         with_vec_plan<4>(p, few, [&](auto nv, auto r) {
