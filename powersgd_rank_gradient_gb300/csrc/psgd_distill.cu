@@ -568,12 +568,14 @@ RowPlan plan_row(long long vocab, int size, int k, long long rows, int sms) {
   while (1 << p.log_ctas < p.ctas) ++p.log_ctas;
   p.granules = (int)(bytes / 16 / p.ctas + 2);
   p.smem = (size_t)p.granules * 16 + extra;
-  // threads: 512 where two slices fill an SM, 256 where three and more do, and
-  // half as many for short rows, of which an SM then has more, each waiting for
-  // its own loads (4000 rows of 8000 bf16 logits 34 us so, 41 with 288 threads)
+  // threads: 512 where two slices fill an SM, 256 where three and more do (4000
+  // bf16 rows of 38000 logits, 76 KB a slice: 113.4 us with 512, 116.0 with 256;
+  // of 35000, 70 KB: 104.9 and 93.4), and fewer for short rows, eight granules
+  // each: an SM then has more rows, each waiting for its own loads (of 8000
+  // logits 33.5 us so, 41.0 with four granules each; from 32 KB a slice on the
+  // limit above is what counts)
   const int most = p.smem > 72 * 1024 ? kDistillThreads : kDistillThreads / 2;
-  const int share = p.smem > 48 * 1024 ? 4 : 8;  // granules per thread
-  p.threads = (int)std::min<long long>(most, std::max<long long>(64, (p.granules / share + 31) / 32 * 32));
+  p.threads = (int)std::min<long long>(most, std::max<long long>(64, (p.granules / 8 + 31) / 32 * 32));
   return p;
 }
 
