@@ -877,15 +877,17 @@ TilePlan plan_tile(long long dim, int vec, int nv) {
   return p;
 }
 
-// Rows of the table per CTA of the one-launch gradient, or 0 where the sorted
-// one is used: every CTA looks at all ids, and a row's tokens are not split
-// over CTAs.  GPU time of one launch against the sorted three, 1024 fp32
+// Rows of the table per CTA of the one-launch gradient (8 CTAs to an SM, or
+// kMaxSpan rows), or 0 where the sorted one is used: every CTA looks at all ids,
+// 2^18 of them together at most, and a row's tokens are not split over CTAs.  On
+// 152 SMs up to 1024 tokens take it where a table has 64 to 256 rows, up to 512
+// of 512 rows, 223 of 30522 and 166 of 50257.  GPU time of one launch against the sorted three, 1024 fp32
 // columns: 16 tokens of a 300-row table 3.1 and 7.2 us, 512 6.8 and 9.3, 2048
 // 19.1 and 13.5; 256 tokens of 3000 rows 8.9 and 10.8; 64 tokens of 30522 rows
 // 22.1 and 26.3 (with 640 bf16 columns 12.6 and 14.3).
-int direct_span(int n, int vocab) {
+int direct_span(int n, int vocab, int sms) {
   if (n > 1024 || n > 16LL * vocab) return 0;
-  const int span = (int)std::min<long long>(kMaxSpan, units(vocab, 1216));
+  const int span = (int)std::min<long long>(kMaxSpan, units(vocab, 8LL * sms));
   return units(vocab, span) * n <= (1 << 18) ? span : 0;
 }
 
@@ -1074,7 +1076,7 @@ extern "C" int psgd_embedding_backward(psgd_embedding* h, const void* ids, int32
     if (!accumulate)
       e = launch_early(k_zero_table, (unsigned)std::min<long long>(units(vocab, 8), h->sms * 8), 256, 0, 1, st,
                        (char*)dweight, vocab, (long long)dim * osize, dweight_stride * osize);
-  } else if (const int span = direct_span(n, vocab)) {
+  } else if (const int span = direct_span(n, vocab, h->sms)) {
     by_dtype(grad_dtype, [&](auto* gt) {
       using G = std::remove_pointer_t<decltype(gt)>;
       return by_dtype(dweight_dtype, [&](auto* ot) {

@@ -758,7 +758,7 @@ __global__ void __launch_bounds__(32 * kColumnWarps) k_norm_columns(const float*
   next_may_launch();
   float s = 0.f;
   if (c < 2LL * dim) {
-    constexpr int kAtOnce = 10;
+    constexpr int kAtOnce = 10;  // loads under way; 152 SMs' partial rows take one turn
     for (int p0 = y; p0 < parts; p0 += kAtOnce * kColumnWarps) {
       float v[kAtOnce];
 #pragma unroll
