@@ -522,7 +522,9 @@ int psgd_dp_finish(psgd_state* s, void* stream);
  *   - strides are in elements and non-negative; rows are contiguous inside.
  *     Outputs may have any element alignment; operands whose addresses and
  *     strides are multiples of 16 bytes are accessed 16 bytes at a time.
- *   - an output may overlap no other operand unless the call says so.
+ *   - an output may overlap no other operand unless the call says so; an
+ *     operand reaches from its first to its last element, what lies between
+ *     its rows included.
  *   - calls enqueue on `stream` and never synchronise; results are the same
  *     bits on every run on the same GPU model.
  */
@@ -531,8 +533,9 @@ int psgd_dp_finish(psgd_state* s, void* stream);
  * Embedding -- a table of `vocab` rows of `dim` elements.
  *
  * The handle holds the workspace of the gradient (the sorted tokens and the
- * partial rows) for up to max_tokens tokens a call; calls on one handle must
- * not overlap on the GPU (order them on one stream, or with events).
+ * partial rows) for up to max_tokens tokens a call, a lookup's among them;
+ * calls on one handle must not overlap on the GPU (order them on one stream, or
+ * with events).
  */
 typedef struct psgd_embedding psgd_embedding; /* opaque, library-owned */
 
@@ -552,7 +555,8 @@ size_t psgd_embedding_workspace_bytes(const psgd_embedding* e);
  *            An id outside [0, vocab) gives a row of zeros and is reported by
  *            psgd_embedding_status.
  *   out    : the tokens' rows, in the same (outer, inner) layout with strides
- *            of its own; rows must not overlap.
+ *            of its own, either of which may be the larger one; rows must not
+ *            overlap.
  * Errors: PSGD_EINVAL, PSGD_ECUDA.
  */
 int psgd_embedding_forward(psgd_embedding* e, const void* weight, psgd_dtype weight_dtype, int64_t weight_stride,
@@ -570,8 +574,9 @@ int psgd_embedding_forward(psgd_embedding* e, const void* weight, psgd_dtype wei
  *   padding_idx : tokens with this id add nothing; -1: none.  Neither does an
  *                 id outside [0, vocab), which psgd_embedding_status reports.
  *   accumulate  : 0: dweight is overwritten; 1: added to.
- * The tokens are sorted by id; each row's sum runs over them in position
- * order, in chunks of fixed length.
+ * Each row's sum runs over its tokens in position order, in pieces whose sums
+ * are then added in a fixed order; where they are cut depends on the ids and the
+ * token count alone (and on the GPU's multiprocessor count).
  * Errors: PSGD_EINVAL (more than max_tokens tokens among them), PSGD_ECUDA.
  */
 int psgd_embedding_backward(psgd_embedding* e, const void* ids, int32_t id_bits, int64_t outer, int64_t inner,
@@ -606,6 +611,9 @@ size_t psgd_layernorm_workspace_bytes(const psgd_layernorm* n);
  *   weight, bias : dim elements of param_dtype; NULL: 1 and 0.
  *   mean, rstd   : out, one float a row (what the backward pass takes); may be
  *                  NULL.
+ * The variance is a sum of squares in fp32: deviations below about 1e-19 count
+ * as none (then rstd is eps^-1/2, infinite without an eps), above 1e19 they
+ * overflow it (rstd 0).  The backward pass takes any mean and rstd.
  * Errors: PSGD_EINVAL, PSGD_ECUDA.
  */
 int psgd_layernorm_forward(psgd_layernorm* n, const void* x, psgd_dtype dtype, int64_t x_stride, int64_t rows,
@@ -645,6 +653,8 @@ int psgd_layernorm_backward(psgd_layernorm* n, const void* grad, int64_t grad_st
  *             entries (index_bits 32 or 64) they belong to.  An entry whose
  *             index lies outside [0, vocab) is not valid: a row with fewer
  *             than k entries is filled up with -1.  Equal indices add up.
+ *             The largest valid logit of a row comes off before the division by
+ *             T: only -infinity has no mass.
  *   weights : w, one float a row (a loss mask, or 1 / tokens); NULL: 1.
  *   losses  : out, one float a row.
  *   dlogits : out, rows of `dtype`; NULL: the losses only.  May be logits

@@ -7,8 +7,9 @@
 // cuts the sorted list into chunks of equal length and lets each CTA add its
 // chunk's rows in order, in fp32.  A row whose tokens lie in one chunk is
 // written there; a row that crosses a chunk's end leaves one fp32 partial per
-// chunk, and a last kernel adds those in chunk order.  No sum depends on the
-// order in which CTAs run.
+// chunk, and a last kernel adds those in chunk order.  Few tokens take one
+// launch without a sort (k_rows_direct).  No sum depends on the order in which
+// CTAs run.
 #include <cooperative_groups.h>
 
 #include <algorithm>

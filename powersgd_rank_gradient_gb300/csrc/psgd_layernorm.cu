@@ -4,12 +4,15 @@
 //   backward  xh = (x - mu) r, a = g w
 //             dx = r (a - mean(a) - xh mean(a xh)),  dw = sum_rows g xh,  db = sum_rows g
 //
-// One group of threads holds a whole row in registers, so every operand is
-// read once.  The variance is the mean of the squared deviations from the
-// mean (a second reduction over registers, no cancellation).  In the backward
-// pass each thread owns the same columns of every row it meets and keeps their
-// dw and db sums in fp32 registers; a CTA leaves one partial row and a second
-// kernel adds the partial rows in a fixed order.
+// One group of threads takes a whole row, which is copied into shared memory
+// ahead of its use, so every operand is read from memory once.  The variance is
+// the mean of the squared deviations from the mean (a second reduction over
+// registers, no cancellation).  In the backward pass each thread owns the same
+// columns of every row it meets and keeps their dw and db sums in fp32
+// registers; a CTA leaves one partial row and a second kernel adds the partial
+// rows in a fixed order.  Rows longer than a CTA's threads can hold (8192
+// elements, 16384 of whole units of a 16-bit type) have kernels of their own,
+// which read a row once per reduction.
 #include <algorithm>
 #include <atomic>
 #include <new>
