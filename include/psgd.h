@@ -55,6 +55,9 @@ typedef struct psgd_state psgd_state; /* opaque, library-owned */
  * the library computes in fp32 and returns fp32 (the cast back). */
 typedef enum { PSGD_F32 = 0, PSGD_F16 = 1, PSGD_BF16 = 2 } psgd_dtype;
 
+/* 8-bit floating point formats: e4m3 (largest value 448, no infinities) and e5m2 (57344). */
+typedef enum { PSGD_E4M3 = 0, PSGD_E5M2 = 1 } psgd_code;
+
 #define PSGD_OK 0
 #define PSGD_SKIPPED_NONFINITE 1 /* [AMP] inf/NaN seen: step skipped, state kept   */
 #define PSGD_BAD_TOKEN 2         /* an embedding met an id outside its table       */
@@ -670,6 +673,88 @@ int psgd_distill(const void* logits, psgd_dtype dtype, int64_t logits_stride, in
                  const void* teacher, psgd_dtype teacher_dtype, int64_t teacher_stride, const void* index,
                  int32_t index_bits, int64_t index_stride, int32_t k, float temperature, const float* weights,
                  float grad_scale, float* losses, void* dlogits, int64_t dlogits_stride, int32_t device, void* stream);
+
+/*
+ * Activations in 8 bits.  Every row is cut into blocks of 128 elements (the last
+ * one may be shorter); a block has one fp32 scale, a power of two:
+ *   scale = the least 2^e, e >= -126, with |x| <= M 2^e for the block's finite
+ *           values (M = 448 for e4m3, 57344 for e5m2); 1 for a block of zeros
+ *   code  = x / scale rounded to the format, ties to even (one rounding of x).
+ * NaN becomes NaN; an infinity stays one in e5m2 and becomes NaN in e4m3.
+ * `codes` are rows of dim bytes, `scales` rows of ceil(dim / 128) floats, both
+ * without gaps.
+ */
+
+/*
+ * psgd_activation_save -- codes and scales of `rows` rows of `dim` elements.
+ * device : the CUDA device that holds the operands.
+ * Errors: PSGD_EINVAL (rows above 2^30, dim above 2^30 among them), PSGD_ECUDA.
+ */
+int psgd_activation_save(const void* x, psgd_dtype dtype, int64_t x_stride, int64_t rows, int64_t dim, void* codes,
+                         psgd_code code, float* scales, int32_t device, void* stream);
+
+/*
+ * psgd_activation_restore -- out = code * scale, rounded to out's type (exact in
+ * fp32, and in bf16 but for its subnormals).  The scales may be any floats.
+ * Errors: PSGD_EINVAL, PSGD_ECUDA.
+ */
+int psgd_activation_restore(const void* codes, psgd_code code, const float* scales, int64_t rows, int64_t dim,
+                            void* out, psgd_dtype dtype, int64_t out_stride, int32_t device, void* stream);
+
+/*
+ * Root-mean-square norm over rows of `dim` elements.  The handle holds the partial
+ * sums of the weight's gradient; backward calls on one handle must not overlap
+ * on the GPU, forward calls may.
+ */
+typedef struct psgd_rmsnorm psgd_rmsnorm; /* opaque, library-owned */
+
+/* Errors: PSGD_EINVAL (dim outside [1, 2^20], device above 63), PSGD_ENOMEM,
+ * PSGD_ECUDA.  *out is NULL on failure. */
+int psgd_rmsnorm_create(int64_t dim, int32_t device, psgd_rmsnorm** out);
+void psgd_rmsnorm_destroy(psgd_rmsnorm* n); /* NULL is a no-op */
+size_t psgd_rmsnorm_workspace_bytes(const psgd_rmsnorm* n);
+
+/*
+ * psgd_rmsnorm_forward -- per row
+ *   s = x + residual, rounded to dtype,   rstd = (mean(s^2) + eps)^-1/2,   y = s rstd weight.
+ *
+ *   x, residual, y, summed : `rows` rows (at most 2^30) of `dtype`, strides of their own.
+ *   residual : NULL: s = x.
+ *   weight   : dim elements of param_dtype; NULL: 1.
+ *   y        : out; or NULL, with
+ *   codes, scales : out, y in 8 bits (from its fp32 value, without a rounding to
+ *              dtype before).
+ *   summed   : out, s (what the backward pass takes); may be NULL, or x or
+ *              residual itself (same stride).
+ *   rstd     : out, one float a row.
+ * The sum of squares is fp32: |s| above 1e19 overflows it (rstd 0).
+ * Errors: PSGD_EINVAL, PSGD_ECUDA.
+ */
+int psgd_rmsnorm_forward(psgd_rmsnorm* n, const void* x, psgd_dtype dtype, int64_t x_stride, int64_t rows,
+                         const void* residual, int64_t residual_stride, const void* weight, psgd_dtype param_dtype,
+                         float eps, void* y, int64_t y_stride, void* codes, psgd_code code, float* scales, void* summed,
+                         int64_t summed_stride, float* rstd, void* stream);
+
+/*
+ * psgd_rmsnorm_backward -- with xh = s rstd and a = grad weight:
+ *   dx      = rstd (a - xh mean(a xh)) [+ grad_summed]
+ *   dweight = [dweight +] sum over rows of grad xh
+ * dx is the gradient of x and of residual.
+ *
+ *   grad, grad_summed, dx : `rows` rows of `dtype`.
+ *   summed        : s, of `dtype`; or NULL, with
+ *   codes, scales : s in 8 bits (psgd_activation_save).
+ *   grad_summed   : the gradient that reaches s past the norm; may be NULL.
+ *   dx            : out; may be NULL, or grad or grad_summed itself (same stride).
+ *   dweight       : out, dim elements of dparam_dtype; may be NULL.  Without rows it
+ *                   becomes 0 (unchanged with accumulate).
+ * Errors: PSGD_EINVAL, PSGD_ECUDA.
+ */
+int psgd_rmsnorm_backward(psgd_rmsnorm* n, const void* grad, psgd_dtype dtype, int64_t grad_stride, int64_t rows,
+                          const void* summed, int64_t summed_stride, const void* codes, psgd_code code,
+                          const float* scales, const float* rstd, const void* weight, psgd_dtype param_dtype,
+                          const void* grad_summed, int64_t grad_summed_stride, void* dx, int64_t dx_stride,
+                          void* dweight, psgd_dtype dparam_dtype, int32_t accumulate, void* stream);
 
 /*
  * psgd_build_id -- "psgd-source-hash:" followed by the SHA-256 (32 hex

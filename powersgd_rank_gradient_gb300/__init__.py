@@ -16,7 +16,7 @@ def __getattr__(name):
         from . import dp
 
         return getattr(dp, name)
-    if name in ("Embedding", "LayerNorm", "distill_loss"):
+    if name in ("Embedding", "LayerNorm", "distill_loss", "RMSNorm", "Activation8", "save_activation"):
         from . import training
 
         return getattr(training, name)

@@ -21,6 +21,8 @@ PSGD_ETIMEOUT = -4
 PSGD_F32 = 0
 PSGD_F16 = 1
 PSGD_BF16 = 2
+PSGD_E4M3 = 0
+PSGD_E5M2 = 1
 PSGD_MAX_RANK = 32
 PSGD_MAX_WORLD = 64
 PSGD_MAX_GROUP_STREAMS = 16
@@ -41,6 +43,9 @@ EXPORTS = [
     "psgd_embedding_forward", "psgd_embedding_backward", "psgd_embedding_status",
     "psgd_layernorm_create", "psgd_layernorm_destroy", "psgd_layernorm_workspace_bytes",
     "psgd_layernorm_forward", "psgd_layernorm_backward", "psgd_distill",
+    "psgd_activation_save", "psgd_activation_restore",
+    "psgd_rmsnorm_create", "psgd_rmsnorm_destroy", "psgd_rmsnorm_workspace_bytes", "psgd_rmsnorm_forward",
+    "psgd_rmsnorm_backward",
 ]
 
 _lib = None
@@ -171,6 +176,22 @@ def lib():
     L.psgd_distill.argtypes = [P, c_i32, c_i64, c_i64, c_i64, P, c_i32, c_i64, P, c_i32, c_i64, c_i32, f32, P, f32, P,
                                P, c_i64, c_i32, P]
     L.psgd_distill.restype = ctypes.c_int
+    L.psgd_activation_save.argtypes = [P, c_i32, c_i64, c_i64, c_i64, P, c_i32, P, c_i32, P]
+    L.psgd_activation_save.restype = ctypes.c_int
+    L.psgd_activation_restore.argtypes = [P, c_i32, P, c_i64, c_i64, P, c_i32, c_i64, c_i32, P]
+    L.psgd_activation_restore.restype = ctypes.c_int
+    L.psgd_rmsnorm_create.argtypes = [c_i64, c_i32, ctypes.POINTER(P)]
+    L.psgd_rmsnorm_create.restype = ctypes.c_int
+    L.psgd_rmsnorm_destroy.argtypes = [P]
+    L.psgd_rmsnorm_destroy.restype = None
+    L.psgd_rmsnorm_workspace_bytes.argtypes = [P]
+    L.psgd_rmsnorm_workspace_bytes.restype = ctypes.c_size_t
+    L.psgd_rmsnorm_forward.argtypes = [P, P, c_i32, c_i64, c_i64, P, c_i64, P, c_i32, f32, P, c_i64, P, c_i32, P, P, c_i64, P,
+                                       P]
+    L.psgd_rmsnorm_forward.restype = ctypes.c_int
+    L.psgd_rmsnorm_backward.argtypes = [P, P, c_i32, c_i64, c_i64, P, c_i64, P, c_i32, P, P, P, c_i32, P, c_i64, P, c_i64, P,
+                                        c_i32, c_i32, P]
+    L.psgd_rmsnorm_backward.restype = ctypes.c_int
     L.psgd_build_id.argtypes = []
     L.psgd_build_id.restype = ctypes.c_char_p
     L.psgd_last_error.argtypes = []

@@ -15,6 +15,7 @@
 
 #include <algorithm>
 #include <string>
+#include <tuple>
 #include <vector>
 
 #include "../../include/psgd.h"
@@ -536,6 +537,241 @@ PyObject* py_distill(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
+// -- activations in 8 bits -------------------------------------------------------------
+
+psgd_code code_of(at::ScalarType t, const char* what) {
+  if (t == at::kFloat8_e4m3fn) return PSGD_E4M3;
+  if (t == at::kFloat8_e5m2) return PSGD_E5M2;
+  throw ValueError{std::string(what) + " must be float8_e4m3fn or float8_e5m2, got " + c10::toString(t)};
+}
+at::ScalarType dtype_arg(PyObject* o, const char* what) {
+  if (!THPDtype_Check(o)) throw ValueError{std::string(what) + " must be a torch.dtype"};
+  return reinterpret_cast<THPDtype*>(o)->scalar_type;
+}
+
+// Codes and scales of rows of `dim` elements, as a caller has them.
+struct Eight {
+  const at::Tensor *codes, *scales;
+  psgd_code code;
+  int64_t rows, dim;
+};
+Eight eight_of(PyObject* codes, PyObject* scales, int index) {
+  const at::Tensor &c = values(codes, "codes"), &s = values(scales, "scales");
+  const psgd_code code = code_of(c.scalar_type(), "codes");
+  on_device(c, index, "codes");
+  on_device(s, index, "scales");
+  const auto shape = c.sizes();
+  if (shape.empty() || shape.back() < 1) throw ValueError{"codes must have a last dimension of at least 1, got " + str(shape)};
+  if (s.scalar_type() != at::kFloat) throw ValueError{std::string("scales must be float32, got ") + c10::toString(s.scalar_type())};
+  c10::SmallVector<int64_t, 8> want(shape.begin(), shape.end());
+  want.back() = (shape.back() + 127) / 128;
+  if (s.sizes() != at::IntArrayRef(want)) throw ValueError{"scales must be " + str(want) + ", got " + str(s.sizes())};
+  if (!c.is_contiguous() || !s.is_contiguous()) throw ValueError{"codes and scales must be contiguous"};
+  return {&c, &s, code, c.numel() / shape.back(), shape.back()};
+}
+int device_of(PyObject* o, const char* what) {
+  const at::Tensor& t = tensor(o, what);
+  if (!t.is_cuda()) throw ValueError{std::string(what) + " must be a CUDA tensor"};
+  return t.get_device();
+}
+// New codes and scales for rows of x's shape.
+std::pair<at::Tensor, at::Tensor> fresh_eight(at::IntArrayRef shape, at::ScalarType type, int index) {
+  c10::SmallVector<int64_t, 8> blocks(shape.begin(), shape.end());
+  blocks.back() = (shape.back() + 127) / 128;
+  return {fresh(shape, type, index), fresh(blocks, at::kFloat, index)};
+}
+
+// activation_check(codes, scales): the checks alone
+PyObject* py_activation_check(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded(n, 2, [&]() -> PyObject* {
+    eight_of(a[0], a[1], device_of(a[0], "codes"));
+    Py_RETURN_NONE;
+  });
+}
+
+// activation_save(x, dtype, codes, scales)
+PyObject* py_activation_save(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded(n, 4, [&]() -> PyObject* {
+    const at::Tensor& x = values(a[0], "x");
+    const int index = device_of(a[0], "x");
+    const psgd_dtype d = dtype_of(x, index, "x");
+    if (x.dim() < 1) throw ValueError{"x must have rows"};
+    const int64_t dim = x.sizes().back();
+    const Rows r = rows_of(x, dim, "x");
+    at::Tensor codes, scales;
+    psgd_code code;
+    if (a[2] == Py_None) {
+      const at::ScalarType type = dtype_arg(a[1], "dtype");
+      code = code_of(type, "dtype");
+      std::tie(codes, scales) = fresh_eight(x.sizes(), type, index);
+    } else {
+      const Eight e = eight_of(a[2], a[3], index);
+      if (e.codes->sizes() != x.sizes()) throw ValueError{"out must have x's shape"};
+      code = e.code;
+      codes = *e.codes;
+      scales = *e.scales;
+    }
+    void* stream = stream_of(index);
+    check(call([&] {
+      return psgd_activation_save(x.const_data_ptr(), d, r.stride, r.rows, dim, codes.mutable_data_ptr(), code,
+                                  static_cast<float*>(scales.mutable_data_ptr()), index, stream);
+    }));
+    Object c(given_or_new(a[2], std::move(codes))), s(given_or_new(a[3], std::move(scales)));
+    return pack({&c, &s});
+  });
+}
+
+// activation_restore(codes, scales, dtype, out)
+PyObject* py_activation_restore(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded(n, 4, [&]() -> PyObject* {
+    const int index = device_of(a[0], "codes");
+    const Eight e = eight_of(a[0], a[1], index);
+    at::Tensor out;
+    int64_t stride = e.dim;
+    if (a[3] == Py_None) {
+      const at::ScalarType type = dtype_arg(a[2], "dtype");
+      if (dtype_code(type) < 0)
+        throw ValueError{std::string("dtype must be float32, float16 or bfloat16, got ") + c10::toString(type)};
+      out = fresh(e.codes->sizes(), type, index);
+    } else {
+      out = values(a[3], "out");
+      if (out.sizes() != e.codes->sizes()) throw ValueError{"out must have the checkpoint's shape"};
+      stride = rows_of(out, e.dim, "out").stride;
+    }
+    const psgd_dtype d = dtype_of(out, index, "out");
+    void* stream = stream_of(index);
+    check(call([&] {
+      return psgd_activation_restore(e.codes->const_data_ptr(), e.code, static_cast<const float*>(e.scales->const_data_ptr()),
+                                     e.rows, e.dim, out.mutable_data_ptr(), d, stride, index, stream);
+    }));
+    return given_or_new(a[3], std::move(out));
+  });
+}
+
+// -- root-mean-square norm ---------------------------------------------------------------
+
+// rmsnorm_forward(spec, x, weight, residual, out, summed, dtype, codes, scales): dtype None: out in x's type, else in 8 bits.
+// (y, summed, rstd) or (codes, scales, summed, rstd)
+PyObject* py_rmsnorm_forward(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded(n, 9, [&]() -> PyObject* {
+    const Spec& s = *spec_of(a[0]);
+    const at::Tensor& x = values(a[1], "x");
+    const psgd_dtype d = dtype_of(x, s.index, "x");
+    const Rows r = rows_of(x, s.dim, "x");
+    const Pair p = pair_of(s, vector_of(s, a[2], "weight"), nullptr, "weight", "");
+    const at::Tensor* residual = a[3] == Py_None ? nullptr : &values(a[3], "residual");
+    const int64_t rs = residual ? stride_like(s, *residual, x, "residual") : 0;
+    const bool eight = a[6] != Py_None;
+    at::Tensor out, codes, scales, summed;
+    int64_t ys = s.dim, ss = s.dim;
+    psgd_code code = PSGD_E4M3;
+    if (eight) {
+      if (a[7] == Py_None) {
+        const at::ScalarType type = dtype_arg(a[6], "dtype");
+        code = code_of(type, "dtype");
+        std::tie(codes, scales) = fresh_eight(x.sizes(), type, s.index);
+      } else {
+        const Eight e = eight_of(a[7], a[8], s.index);
+        if (e.codes->sizes() != x.sizes()) throw ValueError{"out must have x's shape"};
+        code = e.code;
+        codes = *e.codes;
+        scales = *e.scales;
+      }
+    } else if (a[4] == Py_None) {
+      out = fresh(x.sizes(), x.scalar_type(), s.index);
+    } else {
+      out = values(a[4], "out");
+      ys = stride_like(s, out, x, "out");
+    }
+    if (a[5] != Py_None) {
+      summed = values(a[5], "summed");
+      ss = stride_like(s, summed, x, "summed");
+    } else if (residual) {
+      summed = fresh(x.sizes(), x.scalar_type(), s.index);
+    }
+    at::Tensor rstd = fresh(x.sizes().slice(0, x.sizes().size() - 1), at::kFloat, s.index);
+    void* stream = stream_of(s.index);
+    check(call([&] {
+      return psgd_rmsnorm_forward(static_cast<psgd_rmsnorm*>(s.handle), x.const_data_ptr(), d, r.stride, r.rows,
+                                  residual ? residual->const_data_ptr() : nullptr, rs, p.pa(), p.dtype,
+                                  static_cast<float>(s.value), eight ? nullptr : out.mutable_data_ptr(), ys,
+                                  eight ? codes.mutable_data_ptr() : nullptr, code,
+                                  eight ? static_cast<float*>(scales.mutable_data_ptr()) : nullptr,
+                                  summed.defined() ? summed.mutable_data_ptr() : nullptr, ss,
+                                  static_cast<float*>(rstd.mutable_data_ptr()), stream);
+    }));
+    Object z(nullptr);
+    if (summed.defined()) {
+      z.p = given_or_new(a[5], std::move(summed));
+    } else {  // no residual: the sum is x
+      Py_INCREF(a[1]);
+      z.p = a[1];
+    }
+    Object v(given_or_new(Py_None, std::move(rstd)));
+    if (eight) {
+      Object c(given_or_new(a[7], std::move(codes))), k(given_or_new(a[8], std::move(scales)));
+      return pack({&c, &k, &z, &v});
+    }
+    Object y(given_or_new(a[4], std::move(out)));
+    return pack({&y, &z, &v});
+  });
+}
+
+// rmsnorm_backward(spec, grad, summed, codes, scales, rstd, weight, grad_summed, dx, dweight, accumulate); summed None:
+// the codes and scales.  (dx, dweight)
+PyObject* py_rmsnorm_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded(n, 11, [&]() -> PyObject* {
+    const Spec& s = *spec_of(a[0]);
+    const at::Tensor& grad = values(a[1], "grad");
+    const psgd_dtype d = dtype_of(grad, s.index, "grad");
+    const Rows r = rows_of(grad, s.dim, "grad");
+    auto like = [&](const at::Tensor& t, const char* what) {
+      if (t.sizes() != grad.sizes() || t.scalar_type() != grad.scalar_type())
+        throw ValueError{std::string(what) + " must have grad's shape and type"};
+      on_device(t, s.index, what);
+      return rows_of(t, s.dim, what).stride;
+    };
+    const at::Tensor* summed = nullptr;
+    Eight e{};
+    int64_t xs = 0;
+    if (a[2] != Py_None) {
+      summed = &values(a[2], "summed");
+      xs = like(*summed, "summed");
+    } else {
+      e = eight_of(a[3], a[4], s.index);
+      if (e.codes->sizes() != grad.sizes()) throw ValueError{"the checkpoint must have grad's shape"};
+    }
+    const float* rstd = stat_of(s, a[5], r.rows, "rstd");
+    const Pair p = pair_of(s, vector_of(s, a[6], "weight"), nullptr, "weight", "");
+    const at::Tensor* add = a[7] == Py_None ? nullptr : &values(a[7], "grad_summed");
+    const int64_t as = add ? like(*add, "grad_summed") : 0;
+    at::Tensor dx;
+    int64_t ds = s.dim;
+    if (a[8] == Py_None) {
+      dx = fresh(grad.sizes(), grad.scalar_type(), s.index);
+    } else {
+      dx = values(a[8], "dx");
+      ds = like(dx, "dx");
+    }
+    const bool accumulate = truth(a[10]);
+    const at::Tensor* gw = vector_of(s, a[9], "dweight");
+    if (accumulate && !gw) throw ValueError{"accumulate needs a dweight to add to"};
+    at::Tensor dw = gw ? *gw : fresh({s.dim}, at::kFloat, s.index);
+    const psgd_dtype o = dtype_of(dw, s.index, "dweight");
+    void* stream = stream_of(s.index);
+    check(call([&] {
+      return psgd_rmsnorm_backward(static_cast<psgd_rmsnorm*>(s.handle), grad.const_data_ptr(), d, r.stride, r.rows,
+                                   summed ? summed->const_data_ptr() : nullptr, xs,
+                                   summed ? nullptr : e.codes->const_data_ptr(), e.code,
+                                   summed ? nullptr : static_cast<const float*>(e.scales->const_data_ptr()), rstd, p.pa(),
+                                   p.dtype, add ? add->const_data_ptr() : nullptr, as, dx.mutable_data_ptr(), ds,
+                                   dw.mutable_data_ptr(), o, accumulate, stream);
+    }));
+    Object u(given_or_new(a[8], std::move(dx))), v(given_or_new(a[9], std::move(dw)));
+    return pack({&u, &v});
+  });
+}
+
 // What this file was built against: the library's build id, torch's version.
 // (The hash is what build.py looks for.)
 PyObject* py_built_with(PyObject*, PyObject*) {
@@ -552,6 +788,11 @@ PyMethodDef kMethods[] = {
     {"layernorm_forward", FAST(py_layernorm_forward), nullptr},
     {"layernorm_backward", FAST(py_layernorm_backward), nullptr},
     {"distill", FAST(py_distill), nullptr},
+    {"activation_check", FAST(py_activation_check), nullptr},
+    {"activation_save", FAST(py_activation_save), nullptr},
+    {"activation_restore", FAST(py_activation_restore), nullptr},
+    {"rmsnorm_forward", FAST(py_rmsnorm_forward), nullptr},
+    {"rmsnorm_backward", FAST(py_rmsnorm_backward), nullptr},
     {"built_with", py_built_with, METH_NOARGS, nullptr},
     {nullptr, nullptr, 0, nullptr},
 };

@@ -2,8 +2,11 @@
 
 ``Embedding`` (lookup with scaling, and the dense gradient of its table),
 ``LayerNorm`` (forward, and backward with the reduction of the parameters'
-gradients) and ``distill_loss`` (losses and logits' gradient of distillation
-from a teacher's top logits).  Parameter gradients are written into tensors
+gradients), ``distill_loss`` (losses and logits' gradient of distillation
+from a teacher's top logits), and what keeps a step's memory small: ``RMSNorm``
+(with the residual's addition, an output in 8 bits, a backward pass that reads
+one) and activation checkpoints in 8 bits (``save_activation``,
+``Activation8``).  Parameter gradients are written into tensors
 the caller passes, typically views of a flat replica bucket at any element
 offset and in the bucket's type, so that ``powerSGD_hook`` takes the bucket as
 it is.  torch is used for device memory and streams; the arithmetic runs in the
@@ -191,3 +194,127 @@ def distill_loss(logits, teacher_logits, teacher_indices, temperature=1.0, weigh
     index = logits.get_device() if isinstance(logits, torch.Tensor) and logits.is_cuda else stream.device.index
     with _on(stream, index):
         return _bind.distill(logits, teacher_logits, teacher_indices, temperature, weights, grad_scale, dlogits, with_grad)
+
+
+class Activation8:
+    """An activation kept in 8 bits: ``codes`` (float8_e4m3fn or float8_e5m2, of the
+    activation's shape) and ``scales`` (float32, one for each 128 elements of a
+    row: (..., ceil(dim / 128))), both contiguous.  Scales that this package makes
+    are powers of two; it stands for codes times scales."""
+
+    __slots__ = ("codes", "scales")
+
+    def __init__(self, codes, scales):
+        _bind.activation_check(codes, scales)
+        self.codes, self.scales = codes, scales
+
+    @classmethod
+    def _made(cls, codes, scales):
+        a = cls.__new__(cls)
+        a.codes, a.scales = codes, scales
+        return a
+
+    @property
+    def shape(self):
+        return self.codes.shape
+
+    @property
+    def dtype(self):
+        return self.codes.dtype
+
+    @property
+    def device(self):
+        return self.codes.device
+
+    def restore(self, dtype=torch.bfloat16, out=None, stream=None):
+        """The values it stands for, in ``out`` or a new tensor of ``dtype`` (float32, float16 or bfloat16)."""
+        if stream is None:
+            return _bind.activation_restore(self.codes, self.scales, dtype, out)
+        with _on(stream, self.codes.get_device()):
+            return _bind.activation_restore(self.codes, self.scales, dtype, out)
+
+
+def _index_of(t, stream):
+    return t.get_device() if isinstance(t, torch.Tensor) and t.is_cuda else stream.device.index
+
+
+def save_activation(x, dtype=torch.float8_e4m3fn, out=None, stream=None):
+    """``x`` (..., dim) as an ``Activation8`` of ``dtype`` (float8_e4m3fn or
+    float8_e5m2), a new one or ``out``.
+
+    A block of 128 elements of a row has one scale, the least power of two that
+    brings its largest value within the format; a code is its element, rounded
+    once.  Infinities and NaN become NaN (e5m2 keeps infinities)."""
+    codes, scales = (None, None) if out is None else (out.codes, out.scales)
+    if stream is None:
+        codes, scales = _bind.activation_save(x, dtype, codes, scales)
+    else:
+        with _on(stream, _index_of(x, stream)):
+            codes, scales = _bind.activation_save(x, dtype, codes, scales)
+    return Activation8._made(codes, scales) if out is None else out
+
+
+class RMSNorm:
+    """Root-mean-square norm over a last dimension of ``normalized_size`` elements,
+    with the residual's addition.  The handle holds the partial sums of the weight's
+    gradient; backward calls on one handle must not overlap on the GPU."""
+
+    def __init__(self, normalized_size, eps=1e-6, device=None):
+        self.dim, self.eps = int(normalized_size), float(eps)
+        self.device = _device(device)
+        self._lib = _lib.lib()
+        handle = ctypes.c_void_p()
+        check(self._lib.psgd_rmsnorm_create(self.dim, self.device.index, ctypes.byref(handle)))
+        self._h = handle
+        self._spec = _bind.spec(handle.value, 0, self.dim, self.eps, -1, self.device.index)
+
+    def close(self):
+        if getattr(self, "_h", None) and self._h.value:
+            if getattr(self, "_spec", None) is not None:
+                _bind.closed(self._spec)
+            self._lib.psgd_rmsnorm_destroy(self._h)
+            self._h = ctypes.c_void_p()
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+    def forward(self, x, weight=None, residual=None, out=None, summed=None, stream=None):
+        """(y, summed, rstd): ``summed`` is x + residual in x's type (a new tensor, the
+        one given, which may be ``x`` or ``residual`` itself, or without a residual x),
+        rstd = (mean(summed^2) + eps)^-1/2 in fp32, y = summed * rstd * weight.
+        backward takes summed and rstd."""
+        if stream is None:
+            return _bind.rmsnorm_forward(self._spec, x, weight, residual, out, summed, None, None, None)
+        with _on(stream, self.device.index):
+            return _bind.rmsnorm_forward(self._spec, x, weight, residual, out, summed, None, None, None)
+
+    def forward8(self, x, weight=None, residual=None, dtype=torch.float8_e4m3fn, out=None, summed=None, stream=None):
+        """(y, summed, rstd) with y an ``Activation8`` of ``dtype`` (a new one, or ``out``)."""
+        codes, scales = (None, None) if out is None else (out.codes, out.scales)
+        if stream is None:
+            codes, scales, summed, rstd = _bind.rmsnorm_forward(self._spec, x, weight, residual, None, summed, dtype, codes, scales)
+        else:
+            with _on(stream, self.device.index):
+                codes, scales, summed, rstd = _bind.rmsnorm_forward(self._spec, x, weight, residual, None, summed, dtype, codes,
+                                                                    scales)
+        return (Activation8._made(codes, scales) if out is None else out), summed, rstd
+
+    def backward(self, grad, summed, rstd, weight=None, grad_summed=None, dx=None, dweight=None, accumulate=False, stream=None):
+        """(dx, dweight).  ``summed``: as forward gave it, or an ``Activation8`` of it.
+        ``grad_summed``: the gradient that reaches the sum past the norm, added to dx
+        (which is the gradient of both x and the residual); ``dx`` may be ``grad`` or
+        ``grad_summed`` itself.  ``dweight`` (default: a new fp32 vector) is overwritten
+        or, with ``accumulate``, added to."""
+        codes = scales = None
+        if isinstance(summed, Activation8):
+            summed, codes, scales = None, summed.codes, summed.scales
+        if stream is None:
+            return _bind.rmsnorm_backward(self._spec, grad, summed, codes, scales, rstd, weight, grad_summed, dx, dweight, accumulate)
+        with _on(stream, self.device.index):
+            return _bind.rmsnorm_backward(self._spec, grad, summed, codes, scales, rstd, weight, grad_summed, dx, dweight, accumulate)
+
+    def workspace_bytes(self):
+        return int(self._lib.psgd_rmsnorm_workspace_bytes(self._h))
