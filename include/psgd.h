@@ -757,6 +757,41 @@ int psgd_rmsnorm_backward(psgd_rmsnorm* n, const void* grad, psgd_dtype dtype, i
                           void* dweight, psgd_dtype dparam_dtype, int32_t accumulate, void* stream);
 
 /*
+ * The weight gradient of a linear layer y = x W^T from its input's 8-bit
+ * checkpoint, on the tensor cores.  The handle holds the restored checkpoint and a
+ * product's partial sums; calls on one handle must not overlap on the GPU.
+ */
+typedef struct psgd_wgrad psgd_wgrad; /* opaque, library-owned */
+
+/* outs, ins : rows and columns of W.  max_rows : rows of one call at most.
+ * Errors: PSGD_EINVAL (features outside [1, 2^20], max_rows outside [0, 2^24],
+ * device above 63), PSGD_ENOMEM, PSGD_ECUDA.  *out is NULL on failure. */
+int psgd_wgrad_create(int64_t outs, int64_t ins, int64_t max_rows, int32_t device, psgd_wgrad** out);
+void psgd_wgrad_destroy(psgd_wgrad* w); /* NULL is a no-op */
+size_t psgd_wgrad_workspace_bytes(const psgd_wgrad* w);
+
+/*
+ * psgd_wgrad_backward -- dweight = [dweight +] grad^T x, with x = codes * scales
+ * (psgd_activation_save) rounded to grad's type (exact in bf16; in f16 while it is in
+ * range).
+ *
+ *   grad          : `rows` rows of outs elements, F16 or BF16 (the tensor cores
+ *                   multiply 16-bit operands; sums are fp32).
+ *   codes, scales : `rows` rows of ins elements.
+ *   dweight       : outs rows of ins elements, dweight_stride apart, at any
+ *                   element offset.  Without rows it becomes 0 (unchanged with
+ *                   accumulate).
+ * Errors: PSGD_EINVAL, PSGD_ECUDA.
+ */
+int psgd_wgrad_backward(psgd_wgrad* w, const void* grad, psgd_dtype dtype, int64_t grad_stride, int64_t rows,
+                        const void* codes, psgd_code code, const float* scales, void* dweight,
+                        psgd_dtype dweight_dtype, int64_t dweight_stride, int32_t accumulate, void* stream);
+
+/* Synchronises `stream`; PSGD_ETIMEOUT if a bounded wait of a call enqueued on it gave
+ * up since the last status call (its results are not valid), else PSGD_OK. */
+int psgd_wgrad_status(psgd_wgrad* w, void* stream);
+
+/*
  * psgd_build_id -- "psgd-source-hash:" followed by the SHA-256 (32 hex
  * digits) of the sources, header, flags and compiler version this library
  * was built from, so that a caller can check that the loaded binary matches

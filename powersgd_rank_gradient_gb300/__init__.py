@@ -16,7 +16,8 @@ def __getattr__(name):
         from . import dp
 
         return getattr(dp, name)
-    if name in ("Embedding", "LayerNorm", "distill_loss", "RMSNorm", "Activation8", "save_activation"):
+    if name in ("Embedding", "LayerNorm", "distill_loss", "RMSNorm", "Activation8", "save_activation",
+                "LinearWeightGrad"):
         from . import training
 
         return getattr(training, name)

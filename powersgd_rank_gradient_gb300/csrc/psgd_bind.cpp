@@ -772,6 +772,38 @@ PyObject* py_rmsnorm_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
+// -- weight gradient ---------------------------------------------------------------------
+
+// wgrad_backward(spec, grad, codes, scales, out, accumulate); spec.rows: outputs, spec.dim: inputs
+PyObject* py_wgrad_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded(n, 6, [&]() -> PyObject* {
+    const Spec& s = *spec_of(a[0]);
+    const at::Tensor& grad = values(a[1], "grad");
+    if (grad.scalar_type() != at::kHalf && grad.scalar_type() != at::kBFloat16)
+      throw ValueError{std::string("grad must be float16 or bfloat16, got ") + c10::toString(grad.scalar_type())};
+    const psgd_dtype d = dtype_of(grad, s.index, "grad");
+    const Rows r = rows_of(grad, s.rows, "grad");
+    const Eight e = eight_of(a[2], a[3], s.index);
+    const auto lead = grad.sizes().slice(0, grad.sizes().size() - 1), kept = e.codes->sizes();
+    if (e.dim != s.dim || kept.slice(0, kept.size() - 1) != lead) {
+      std::vector<int64_t> want(lead.begin(), lead.end());
+      want.push_back(s.dim);
+      throw ValueError{"the checkpoint must be " + str(want) + ", got " + str(kept)};
+    }
+    const bool accumulate = truth(a[5]);
+    if (a[4] == Py_None && accumulate) throw ValueError{"accumulate needs an out to add to"};
+    at::Tensor out = a[4] == Py_None ? fresh({s.rows, s.dim}, at::kFloat, s.index) : values(a[4], "out");
+    const Table w = table_of(s, out, "out");
+    void* stream = stream_of(s.index);
+    check(call([&] {
+      return psgd_wgrad_backward(static_cast<psgd_wgrad*>(s.handle), grad.const_data_ptr(), d, r.stride, r.rows,
+                                 e.codes->const_data_ptr(), e.code, static_cast<const float*>(e.scales->const_data_ptr()),
+                                 out.mutable_data_ptr(), w.dtype, w.stride, accumulate, stream);
+    }));
+    return given_or_new(a[4], std::move(out));
+  });
+}
+
 // What this file was built against: the library's build id, torch's version.
 // (The hash is what build.py looks for.)
 PyObject* py_built_with(PyObject*, PyObject*) {
@@ -793,6 +825,7 @@ PyMethodDef kMethods[] = {
     {"activation_restore", FAST(py_activation_restore), nullptr},
     {"rmsnorm_forward", FAST(py_rmsnorm_forward), nullptr},
     {"rmsnorm_backward", FAST(py_rmsnorm_backward), nullptr},
+    {"wgrad_backward", FAST(py_wgrad_backward), nullptr},
     {"built_with", py_built_with, METH_NOARGS, nullptr},
     {nullptr, nullptr, 0, nullptr},
 };

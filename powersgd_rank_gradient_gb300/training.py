@@ -318,3 +318,53 @@ class RMSNorm:
 
     def workspace_bytes(self):
         return int(self._lib.psgd_rmsnorm_workspace_bytes(self._h))
+
+
+class LinearWeightGrad:
+    """The weight gradient of a linear layer ``y = x W^T``, W of ``out_features`` rows
+    of ``in_features`` elements, from an 8-bit checkpoint of x.
+
+    ``max_tokens`` bounds the rows of one call (the handle holds the restored
+    checkpoint and a product's partial sums; layers of one shape may share it).
+    Calls on one handle must not overlap on the GPU."""
+
+    def __init__(self, out_features, in_features, max_tokens, device=None):
+        self.out_features, self.in_features, self.max_tokens = int(out_features), int(in_features), int(max_tokens)
+        self.device = _device(device)
+        self._lib = _lib.lib()
+        handle = ctypes.c_void_p()
+        check(self._lib.psgd_wgrad_create(self.out_features, self.in_features, self.max_tokens, self.device.index,
+                                          ctypes.byref(handle)))
+        self._h = handle
+        self._spec = _bind.spec(handle.value, self.out_features, self.in_features, 0.0, -1, self.device.index)
+
+    def close(self):
+        if getattr(self, "_h", None) and self._h.value:
+            if getattr(self, "_spec", None) is not None:
+                _bind.closed(self._spec)
+            self._lib.psgd_wgrad_destroy(self._h)
+            self._h = ctypes.c_void_p()
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+    def backward(self, grad, activation, out=None, accumulate=False, stream=None):
+        """``grad^T x`` with grad (..., out_features) in float16 or bfloat16 and x the values of
+        ``activation`` (an ``Activation8`` of (..., in_features)) in grad's type, into ``out``
+        (default: a new fp32 tensor), over what it holds or, with ``accumulate``, added to it."""
+        if stream is None:
+            return _bind.wgrad_backward(self._spec, grad, activation.codes, activation.scales, out, accumulate)
+        with _on(stream, self.device.index):
+            return _bind.wgrad_backward(self._spec, grad, activation.codes, activation.scales, out, accumulate)
+
+    def status(self, stream=None):
+        """Synchronises; raises PsgdError if a bounded wait on the GPU gave up since the last status()."""
+        index = self.device.index
+        stream = torch.cuda.current_stream(index) if stream is None else _of_device(stream, index)
+        check(self._lib.psgd_wgrad_status(self._h, stream.cuda_stream))
+
+    def workspace_bytes(self):
+        return int(self._lib.psgd_wgrad_workspace_bytes(self._h))

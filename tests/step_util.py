@@ -112,3 +112,14 @@ def rms_backward(grad, s, rstd, weight, add=None, before=None):
     if before is not None:
         dw, mag = dw + before.double(), mag + before.double().abs()
     return (dx, dw), (dx_err, (depth + 4) * u * mag)
+
+
+# -- products ------------------------------------------------------------------------
+
+def product(a, b, scale=1.0, before=None):
+    """(a^T b * scale [+ before], its error where products are exact and sums fp32, whatever their order)."""
+    a, b = a.double(), b.double()
+    d, mag = a.t() @ b * scale, a.abs().t() @ b.abs() * abs(scale)
+    if before is not None:
+        d, mag = d + before.double(), mag + before.double().abs()
+    return d, (a.shape[0] + 4) * u * mag
