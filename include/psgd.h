@@ -792,6 +792,64 @@ int psgd_wgrad_backward(psgd_wgrad* w, const void* grad, psgd_dtype dtype, int64
 int psgd_wgrad_status(psgd_wgrad* w, void* stream);
 
 /*
+ * Softmax cross entropy of a linear output layer, without its logits.
+ *
+ * The handle holds the tokens that count, a bounded piece of the logits' gradient
+ * (256 MB, or 256 columns of the vocabulary where those take more) and partial
+ * sums; calls on one handle must not overlap on the GPU.
+ */
+typedef struct psgd_linear_ce psgd_linear_ce; /* opaque, library-owned */
+
+/* Errors: PSGD_EINVAL (vocab outside [1, 2^24], dim outside [1, 2^20], max_tokens
+ * outside [0, 2^20], device above 63), PSGD_ENOMEM, PSGD_ECUDA.  *out is NULL on failure. */
+int psgd_linear_ce_create(int64_t vocab, int64_t dim, int64_t max_tokens, int32_t device, psgd_linear_ce** out);
+void psgd_linear_ce_destroy(psgd_linear_ce* c); /* NULL is a no-op */
+size_t psgd_linear_ce_workspace_bytes(const psgd_linear_ce* c);
+
+/*
+ * psgd_linear_ce_forward -- for every token t, with z_tv = hidden_t . weight_v:
+ *   lse_t    = log sum_v exp(z_tv),
+ *   losses_t = w_t (lse_t - z_t,target).
+ *
+ *   hidden  : `tokens` rows of dim elements, F16 or BF16 (the tensor cores
+ *             multiply 16-bit operands; sums are fp32).
+ *   weight  : vocab rows of dim elements of the same type.
+ *   targets : target_bits (32 or 64) bit signed integers, without gaps.
+ *   weights : w, one float a token; NULL: 1.
+ *   losses, lse : out, one float a token (lse is what the backward pass takes).
+ * A token with a target outside [0, vocab) or with w = 0 does not count: its
+ * loss and lse are 0 whatever its row holds, and it costs no arithmetic.  NaN or
+ * +infinity among a row's logits gives NaN.
+ * Errors: PSGD_EINVAL, PSGD_ECUDA.
+ */
+int psgd_linear_ce_forward(psgd_linear_ce* c, const void* hidden, psgd_dtype dtype, int64_t hidden_stride, int64_t tokens,
+                           const void* weight, int64_t weight_stride, const void* targets, int32_t target_bits,
+                           const float* weights, float* losses, float* lse, void* stream);
+
+/*
+ * psgd_linear_ce_backward -- with G_tv = grad_scale w_t (exp(z_tv - lse_t) - [v = target_t]):
+ *   dhidden_t = sum_v G_tv weight_v
+ *   dweight_v = [dweight_v +] sum_t G_tv hidden_t
+ * The logits are computed again.  exp(z - lse) - [v = target], times w_t's significand, is
+ * rounded once to the operands' type before both products; hidden_t takes the rest of w_t, a
+ * power of two relative to the largest.
+ *
+ *   hidden, weight, targets, weights : as in the forward pass; lse: its output.
+ *   dhidden : out, rows of the operands' type; may be NULL.  0 for a token that
+ *             does not count.
+ *   dweight : out, vocab rows of dim elements, at any element offset; may be NULL.
+ * Errors: PSGD_EINVAL, PSGD_ECUDA.
+ */
+int psgd_linear_ce_backward(psgd_linear_ce* c, const void* hidden, psgd_dtype dtype, int64_t hidden_stride,
+                            int64_t tokens, const void* weight, int64_t weight_stride, const void* targets,
+                            int32_t target_bits, const float* lse, const float* weights, float grad_scale, void* dhidden,
+                            int64_t dhidden_stride, void* dweight, psgd_dtype dweight_dtype, int64_t dweight_stride,
+                            int32_t accumulate, void* stream);
+
+/* As psgd_wgrad_status. */
+int psgd_linear_ce_status(psgd_linear_ce* c, void* stream);
+
+/*
  * psgd_build_id -- "psgd-source-hash:" followed by the SHA-256 (32 hex
  * digits) of the sources, header, flags and compiler version this library
  * was built from, so that a caller can check that the loaded binary matches

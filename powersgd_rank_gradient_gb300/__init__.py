@@ -17,7 +17,7 @@ def __getattr__(name):
 
         return getattr(dp, name)
     if name in ("Embedding", "LayerNorm", "distill_loss", "RMSNorm", "Activation8", "save_activation",
-                "LinearWeightGrad"):
+                "LinearWeightGrad", "LinearCrossEntropy"):
         from . import training
 
         return getattr(training, name)

@@ -47,6 +47,8 @@ EXPORTS = [
     "psgd_rmsnorm_create", "psgd_rmsnorm_destroy", "psgd_rmsnorm_workspace_bytes", "psgd_rmsnorm_forward",
     "psgd_rmsnorm_backward",
     "psgd_wgrad_create", "psgd_wgrad_destroy", "psgd_wgrad_workspace_bytes", "psgd_wgrad_backward", "psgd_wgrad_status",
+    "psgd_linear_ce_create", "psgd_linear_ce_destroy", "psgd_linear_ce_workspace_bytes", "psgd_linear_ce_forward",
+    "psgd_linear_ce_backward", "psgd_linear_ce_status",
 ]
 
 _lib = None
@@ -203,6 +205,19 @@ def lib():
     L.psgd_wgrad_backward.restype = ctypes.c_int
     L.psgd_wgrad_status.argtypes = [P, P]
     L.psgd_wgrad_status.restype = ctypes.c_int
+    L.psgd_linear_ce_create.argtypes = [c_i64, c_i64, c_i64, c_i32, ctypes.POINTER(P)]
+    L.psgd_linear_ce_create.restype = ctypes.c_int
+    L.psgd_linear_ce_destroy.argtypes = [P]
+    L.psgd_linear_ce_destroy.restype = None
+    L.psgd_linear_ce_workspace_bytes.argtypes = [P]
+    L.psgd_linear_ce_workspace_bytes.restype = ctypes.c_size_t
+    L.psgd_linear_ce_forward.argtypes = [P, P, c_i32, c_i64, c_i64, P, c_i64, P, c_i32, P, P, P, P]
+    L.psgd_linear_ce_forward.restype = ctypes.c_int
+    L.psgd_linear_ce_backward.argtypes = [P, P, c_i32, c_i64, c_i64, P, c_i64, P, c_i32, P, P, f32, P, c_i64, P, c_i32, c_i64,
+                                          c_i32, P]
+    L.psgd_linear_ce_backward.restype = ctypes.c_int
+    L.psgd_linear_ce_status.argtypes = [P, P]
+    L.psgd_linear_ce_status.restype = ctypes.c_int
     L.psgd_build_id.argtypes = []
     L.psgd_build_id.restype = ctypes.c_char_p
     L.psgd_last_error.argtypes = []

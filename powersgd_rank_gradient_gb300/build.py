@@ -37,7 +37,7 @@ PTXAS_LOG = os.path.join(BUILD, "ptxas.log")
 
 SOURCES = ["psgd_api.cu", "psgd_misc.cu", "psgd_static.cu", "psgd_group.cu",
            "psgd_embedding.cu", "psgd_layernorm.cu", "psgd_distill.cu", "psgd_rmsnorm.cu",
-           "psgd_activation.cu", "psgd_gemm.cu", "psgd_wgrad.cu"] + \
+           "psgd_activation.cu", "psgd_gemm.cu", "psgd_wgrad.cu", "psgd_loss.cu"] + \
           [f"kern_rp{r}.cu" for r in (1, 2, 4, 8, 16, 32)]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xptxas", "-v", "-I", INCLUDE]

@@ -804,6 +804,95 @@ PyObject* py_wgrad_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
+// -- cross entropy of a linear layer ----------------------------------------------------------
+
+// What both passes check.  spec.rows: the vocabulary, spec.dim: its rows' length
+struct LossCall {
+  const at::Tensor &hidden, &weight, &targets;
+  psgd_dtype dtype;
+  Rows rows;
+  int64_t weight_stride;
+  int bits;
+  at::IntArrayRef lead;
+  const float* weights = nullptr;
+  LossCall(const Spec& s, PyObject* h, PyObject* w, PyObject* t, PyObject* loss_weights)
+      : hidden(values(h, "hidden")), weight(values(w, "weight")), targets(tensor(t, "targets")) {
+    if (hidden.scalar_type() != at::kHalf && hidden.scalar_type() != at::kBFloat16)
+      throw ValueError{std::string("hidden must be float16 or bfloat16, got ") + c10::toString(hidden.scalar_type())};
+    dtype = dtype_of(hidden, s.index, "hidden");
+    rows = rows_of(hidden, s.dim, "hidden");
+    lead = hidden.sizes().slice(0, hidden.sizes().size() - 1);
+    const Table table = table_of(s, weight, "weight");
+    if (table.dtype != dtype) throw ValueError{"weight must have hidden's type"};
+    weight_stride = table.stride;
+    bits = id_bits_of(targets, s.index, "targets");
+    if (targets.sizes() != lead || !targets.is_contiguous())
+      throw ValueError{"targets must be a contiguous tensor of hidden's leading shape"};
+    if (loss_weights != Py_None) weights = of_tokens(s, loss_weights, "weights");
+  }
+  const float* of_tokens(const Spec& s, PyObject* o, const char* what) const {
+    const at::Tensor& t = values(o, what);
+    if (t.scalar_type() != at::kFloat || t.sizes() != lead || !t.is_contiguous())
+      throw ValueError{std::string(what) + " must be a contiguous float32 tensor of hidden's leading shape"};
+    on_device(t, s.index, what);
+    return static_cast<const float*>(t.const_data_ptr());
+  }
+};
+
+// linear_ce_forward(spec, hidden, weight, targets, weights)
+PyObject* py_linear_ce_forward(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded(n, 5, [&]() -> PyObject* {
+    const Spec& s = *spec_of(a[0]);
+    const LossCall c(s, a[1], a[2], a[3], a[4]);
+    // one allocation for both
+    const at::Tensor both = fresh({2 * c.rows.rows}, at::kFloat, s.index);
+    at::Tensor losses = part_of(both, c.lead, 0), lse = part_of(both, c.lead, c.rows.rows);
+    void* stream = stream_of(s.index);
+    check(call([&] {
+      return psgd_linear_ce_forward(static_cast<psgd_linear_ce*>(s.handle), c.hidden.const_data_ptr(), c.dtype, c.rows.stride,
+                                    c.rows.rows, c.weight.const_data_ptr(), c.weight_stride, c.targets.const_data_ptr(), c.bits,
+                                    c.weights, static_cast<float*>(losses.mutable_data_ptr()),
+                                    static_cast<float*>(lse.mutable_data_ptr()), stream);
+    }));
+    Object u(given_or_new(Py_None, std::move(losses))), v(given_or_new(Py_None, std::move(lse)));
+    return pack({&u, &v});
+  });
+}
+
+// linear_ce_backward(spec, hidden, weight, targets, lse, weights, grad_scale, dhidden, dweight, accumulate)
+PyObject* py_linear_ce_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded(n, 10, [&]() -> PyObject* {
+    const Spec& s = *spec_of(a[0]);
+    const LossCall c(s, a[1], a[2], a[3], a[5]);
+    const float* lse = c.of_tokens(s, a[4], "lse");
+    const double scale = number(a[6]);
+    at::Tensor dh;
+    int64_t ds = s.dim;
+    if (a[7] == Py_None) {
+      dh = fresh(c.hidden.sizes(), c.hidden.scalar_type(), s.index);
+    } else {
+      dh = values(a[7], "dhidden");
+      if (dh.sizes() != c.hidden.sizes() || dh.scalar_type() != c.hidden.scalar_type())
+        throw ValueError{"dhidden must have hidden's shape and type"};
+      on_device(dh, s.index, "dhidden");
+      ds = rows_of(dh, s.dim, "dhidden").stride;
+    }
+    const bool accumulate = truth(a[9]);
+    if (a[8] == Py_None && accumulate) throw ValueError{"accumulate needs a dweight to add to"};
+    at::Tensor dw = a[8] == Py_None ? fresh({s.rows, s.dim}, at::kFloat, s.index) : values(a[8], "dweight");
+    const Table o = table_of(s, dw, "dweight");
+    void* stream = stream_of(s.index);
+    check(call([&] {
+      return psgd_linear_ce_backward(static_cast<psgd_linear_ce*>(s.handle), c.hidden.const_data_ptr(), c.dtype, c.rows.stride,
+                                     c.rows.rows, c.weight.const_data_ptr(), c.weight_stride, c.targets.const_data_ptr(), c.bits,
+                                     lse, c.weights, static_cast<float>(scale), dh.mutable_data_ptr(), ds, dw.mutable_data_ptr(),
+                                     o.dtype, o.stride, accumulate, stream);
+    }));
+    Object u(given_or_new(a[7], std::move(dh))), v(given_or_new(a[8], std::move(dw)));
+    return pack({&u, &v});
+  });
+}
+
 // What this file was built against: the library's build id, torch's version.
 // (The hash is what build.py looks for.)
 PyObject* py_built_with(PyObject*, PyObject*) {
@@ -826,6 +915,8 @@ PyMethodDef kMethods[] = {
     {"rmsnorm_forward", FAST(py_rmsnorm_forward), nullptr},
     {"rmsnorm_backward", FAST(py_rmsnorm_backward), nullptr},
     {"wgrad_backward", FAST(py_wgrad_backward), nullptr},
+    {"linear_ce_forward", FAST(py_linear_ce_forward), nullptr},
+    {"linear_ce_backward", FAST(py_linear_ce_backward), nullptr},
     {"built_with", py_built_with, METH_NOARGS, nullptr},
     {nullptr, nullptr, 0, nullptr},
 };

@@ -5,8 +5,10 @@
 gradients), ``distill_loss`` (losses and logits' gradient of distillation
 from a teacher's top logits), and what keeps a step's memory small: ``RMSNorm``
 (with the residual's addition, an output in 8 bits, a backward pass that reads
-one) and activation checkpoints in 8 bits (``save_activation``,
-``Activation8``).  Parameter gradients are written into tensors
+one), activation checkpoints in 8 bits (``save_activation``, ``Activation8``)
+with the weight gradient of a linear layer from one (``LinearWeightGrad``), and
+``LinearCrossEntropy`` (losses and gradients of an output layer without its
+logits).  Parameter gradients are written into tensors
 the caller passes, typically views of a flat replica bucket at any element
 offset and in the bucket's type, so that ``powerSGD_hook`` takes the bucket as
 it is.  torch is used for device memory and streams; the arithmetic runs in the
@@ -368,3 +370,67 @@ class LinearWeightGrad:
 
     def workspace_bytes(self):
         return int(self._lib.psgd_wgrad_workspace_bytes(self._h))
+
+
+class LinearCrossEntropy:
+    """Softmax cross entropy of an output layer ``hidden @ weight.t()`` over a vocabulary
+    of ``vocab`` rows of ``dim`` elements, without the logits: they are made tile by
+    tile and used where they are made, in the backward pass again.
+
+    ``max_tokens`` bounds the tokens of one call (the handle holds them, a bounded piece of the
+    logits' gradient and partial sums).  Calls on one handle must not overlap on the GPU.
+
+    ``hidden`` (..., dim) and ``weight`` (vocab, dim) are float16 or bfloat16, of one
+    type; ``targets`` (...) int32 or int64; ``weights`` (...) float32, multiplied into
+    losses and gradients.  A token whose target is outside the vocabulary (-100, say) or
+    whose weight is 0 does not count: loss, lse and gradient are 0 whatever its row
+    holds, and it costs no arithmetic."""
+
+    def __init__(self, vocab, dim, max_tokens, device=None):
+        self.vocab, self.dim, self.max_tokens = int(vocab), int(dim), int(max_tokens)
+        self.device = _device(device)
+        self._lib = _lib.lib()
+        handle = ctypes.c_void_p()
+        check(self._lib.psgd_linear_ce_create(self.vocab, self.dim, self.max_tokens, self.device.index, ctypes.byref(handle)))
+        self._h = handle
+        self._spec = _bind.spec(handle.value, self.vocab, self.dim, 0.0, -1, self.device.index)
+
+    def close(self):
+        if getattr(self, "_h", None) and self._h.value:
+            if getattr(self, "_spec", None) is not None:
+                _bind.closed(self._spec)
+            self._lib.psgd_linear_ce_destroy(self._h)
+            self._h = ctypes.c_void_p()
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+    def forward(self, hidden, weight, targets, weights=None, stream=None):
+        """(losses, lse), fp32, of targets' shape: lse = log sum exp of a token's logits, loss = weight * (lse - its
+        target's logit).  backward takes lse."""
+        if stream is None:
+            return _bind.linear_ce_forward(self._spec, hidden, weight, targets, weights)
+        with _on(stream, self.device.index):
+            return _bind.linear_ce_forward(self._spec, hidden, weight, targets, weights)
+
+    def backward(self, hidden, weight, targets, lse, weights=None, grad_scale=1.0, dhidden=None, dweight=None, accumulate=False,
+                 stream=None):
+        """(dhidden, dweight), the gradients of the sum of the losses times ``grad_scale``.
+        ``dhidden`` (default: a new tensor) has hidden's type; ``dweight`` (default: a new
+        fp32 tensor) is overwritten or, with ``accumulate``, added to."""
+        if stream is None:
+            return _bind.linear_ce_backward(self._spec, hidden, weight, targets, lse, weights, grad_scale, dhidden, dweight, accumulate)
+        with _on(stream, self.device.index):
+            return _bind.linear_ce_backward(self._spec, hidden, weight, targets, lse, weights, grad_scale, dhidden, dweight, accumulate)
+
+    def status(self, stream=None):
+        """Synchronises; raises PsgdError if a bounded wait on the GPU gave up since the last status()."""
+        index = self.device.index
+        stream = torch.cuda.current_stream(index) if stream is None else _of_device(stream, index)
+        check(self._lib.psgd_linear_ce_status(self._h, stream.cuda_stream))
+
+    def workspace_bytes(self):
+        return int(self._lib.psgd_linear_ce_workspace_bytes(self._h))

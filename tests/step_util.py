@@ -12,6 +12,17 @@ BITS = {E4: 3, E5: 2}   # of a significand, behind the leading one
 LOW = {E4: -6, E5: -14}  # exponent below which the values are equally spaced
 
 
+def check_out(got, want, err, dtype):
+    """An fp32 result within err of ``want``, rounded to ``dtype``: f16 rounds what is 65520 (the middle of its largest
+    value and the next one that it would have) or more to infinity."""
+    want, err = want.double(), err.double()
+    if dtype == torch.float16:
+        over, may = want.abs() - err >= 65520.0, want.abs() + err >= 65520.0
+        assert torch.equal(got[over].double(), torch.sign(want[over]) * torch.inf)
+        got, want, err = got[~may], want[~may], err[~may]
+    check(got, want, out_tol(err, want, dtype))
+
+
 # -- 8 bits ----------------------------------------------------------------------
 
 def blocks(x):
@@ -123,3 +134,71 @@ def product(a, b, scale=1.0, before=None):
     if before is not None:
         d, mag = d + before.double(), mag + before.double().abs()
     return d, (a.shape[0] + 4) * u * mag
+
+
+# -- cross entropy of a linear layer ---------------------------------------------------
+
+def live_tokens(targets, weights, vocab):
+    t = targets.reshape(-1).long()
+    w = torch.ones(t.shape, dtype=torch.float64, device=t.device) if weights is None else weights.reshape(-1).double()
+    return t, w, (t >= 0) & (t < vocab) & (w != 0)
+
+
+def _logits(h, weight):
+    """(z, the error of each in fp32: exact products, sums in any order)."""
+    h, weight = h.double(), weight.double()
+    return h @ weight.t(), (h.shape[1] + 4) * u * (h.abs() @ weight.abs().t())
+
+
+def loss_forward(hidden, weight, targets, weights):
+    """(losses, lse), (their errors); rows that do not count are 0 with an error of 0."""
+    v = weight.shape[0]
+    t, w, live = live_tokens(targets, weights, v)
+    h = hidden.reshape(-1, hidden.shape[-1])[live]
+    z, ez = _logits(h, weight)
+    lse = torch.logsumexp(z, 1)
+    at = t[live][:, None]
+    zt, et = z.gather(1, at)[:, 0], ez.gather(1, at)[:, 0]
+    # the logits' errors, weighted by the probabilities; an exponential is within 4 u and |x| u of its argument x (|x| e^x < 0.4,
+    # so 90 u in all at most); a chain of 46 additions in 128 columns, then of the columns' pieces
+    p = torch.exp(z - lse[:, None])
+    el = (p * ez).sum(1) * 1.01 + (150 + v / 128 / 32 + 40) * u + 3 * u * lse.abs()
+    out = [torch.zeros(t.shape, dtype=torch.float64, device=t.device) for _ in range(4)]
+    out[0][live] = w[live] * (lse - zt)
+    out[1][live] = lse
+    out[2][live] = w[live].abs() * (el + et + 3 * u * (lse.abs() + zt.abs()))
+    out[3][live] = el
+    return tuple(x.view(targets.shape) for x in out[:2]), tuple(x.view(targets.shape) for x in out[2:])
+
+
+def loss_backward(hidden, weight, targets, lse, weights, scale=1.0, before=None):
+    """(dhidden, dweight), (their errors) for the lse that is given."""
+    v, d, dtype = weight.shape[0], weight.shape[1], hidden.dtype
+    t, w, live = live_tokens(targets, weights, v)
+    h = hidden.reshape(-1, d)[live]
+    z, ez = _logits(h, weight)
+    x = z - lse.reshape(-1).double()[live][:, None]
+    q = torch.exp(x)
+    # q's error: its argument's (the logit's and the difference's), the exponential's; then the difference from 1
+    eq = q * (torch.expm1(ez + 2 * u * (z.abs() + x.abs()) + 4 * u))
+    q.scatter_add_(1, t[live][:, None], torch.full_like(q[:, :1], -1.0))
+    eq += u * q.abs()
+    wl = w[live]
+    size = torch.exp2(torch.floor(torch.log2(wl.abs())))[:, None]  # a weight's power of two
+    # one rounding to the operands' type, of f16 2^14 times the value
+    low = 2.0 ** -39 if dtype == torch.float16 else 0.0
+    eg = (eq + (U[dtype] + 2 * u) * (q.abs() + eq)) * wl.abs()[:, None] + low * size
+    g = q * wl[:, None]
+    dh = torch.zeros((t.shape[0], d), dtype=torch.float64, device=h.device)
+    eh, wd, hd = torch.zeros_like(dh), weight.double(), h.double()
+    dh[live] = g @ wd * scale
+    mag = (g.abs() + eg) @ wd.abs()
+    eh[live] = (eg @ wd.abs() + (v + 40) * u * mag) * abs(scale)
+    dw, mag = g.t() @ hd * scale, (g.abs() + eg).t() @ hd.abs()
+    ew = (eg.t() @ hd.abs() + (h.shape[0] + 40) * u * mag) * abs(scale)
+    if dtype == torch.float16 and h.shape[0]:
+        # a row of h times its weight's power of two relative to the largest may meet f16's smallest step
+        ew = ew + (((g.abs() + eg) / size).sum(0) * 2.0 ** -25 * float(size.max()) * abs(scale))[:, None]
+    if before is not None:
+        dw, ew = dw + before.double(), ew + u * (dw.abs() + before.double().abs())
+    return (dh.view(hidden.shape), dw), (eh.view(hidden.shape), ew)

@@ -60,3 +60,34 @@ def test_restore_refuses_rows_that_overlap():
 @pytest.mark.parametrize("call", [save, restore])
 def test_no_rows_do_nothing(call):
     assert call(rows=0, x=None, codes=None, scales=None) == _lib.PSGD_OK
+
+
+@pytest.mark.parametrize("outs,ins,rows,device", [(0, 8, 8, 0), (8, 0, 8, 0), (2**20 + 1, 8, 8, 0), (8, 2**20 + 1, 8, 0), (8, 8, -1, 0),
+                                                  (8, 8, 2**24 + 1, 0), (8, 8, 8, 64), (8, 8, 8, -1)])
+def test_wgrad_create_refuses(outs, ins, rows, device):
+    h = ctypes.c_void_p(1)
+    assert _lib.lib().psgd_wgrad_create(outs, ins, rows, device, ctypes.byref(h)) == _lib.PSGD_EINVAL
+    assert not h.value and "psgd_wgrad_create" in message()
+
+
+@pytest.mark.parametrize("vocab,dim,tokens,device", [(0, 8, 8, 0), (2**24 + 1, 8, 8, 0), (8, 0, 8, 0), (8, 2**20 + 1, 8, 0), (8, 8, -1, 0),
+                                                     (8, 8, 2**20 + 1, 0), (8, 8, 8, 64), (8, 8, 8, -1)])
+def test_linear_ce_create_refuses(vocab, dim, tokens, device):
+    h = ctypes.c_void_p(1)
+    assert _lib.lib().psgd_linear_ce_create(vocab, dim, tokens, device, ctypes.byref(h)) == _lib.PSGD_EINVAL
+    assert not h.value and "psgd_linear_ce_create" in message()
+
+
+def test_null_product_handles():
+    L = _lib.lib()
+    bf16 = _lib.PSGD_BF16
+    assert L.psgd_wgrad_create(8, 8, 8, 0, None) == _lib.PSGD_EINVAL
+    assert L.psgd_linear_ce_create(8, 8, 8, 0, None) == _lib.PSGD_EINVAL
+    assert L.psgd_wgrad_backward(None, None, bf16, 8, 1, None, 0, None, None, F32, 8, 0, None) == _lib.PSGD_EINVAL
+    assert L.psgd_linear_ce_forward(None, None, bf16, 8, 1, None, 8, None, 64, None, None, None, None) == _lib.PSGD_EINVAL
+    assert L.psgd_linear_ce_backward(None, None, bf16, 8, 1, None, 8, None, 64, None, None, 1.0, None, 8, None, F32, 8, 0,
+                                     None) == _lib.PSGD_EINVAL
+    assert L.psgd_wgrad_status(None, None) == _lib.PSGD_EINVAL and L.psgd_linear_ce_status(None, None) == _lib.PSGD_EINVAL
+    assert L.psgd_wgrad_workspace_bytes(None) == 0 and L.psgd_linear_ce_workspace_bytes(None) == 0
+    L.psgd_wgrad_destroy(None)
+    L.psgd_linear_ce_destroy(None)
