@@ -830,9 +830,10 @@ int psgd_linear_ce_forward(psgd_linear_ce* c, const void* hidden, psgd_dtype dty
  * psgd_linear_ce_backward -- with G_tv = grad_scale w_t (exp(z_tv - lse_t) - [v = target_t]):
  *   dhidden_t = sum_v G_tv weight_v
  *   dweight_v = [dweight_v +] sum_t G_tv hidden_t
- * The logits are computed again.  exp(z - lse) - [v = target], times w_t's significand, is
- * rounded once to the operands' type before both products; hidden_t takes the rest of w_t, a
- * power of two relative to the largest.
+ * The logits are computed again.  exp(z - lse) - [v = target], times r_t, is rounded
+ * once to the operands' type before both products, where w_t = s r_t 2^e with s the
+ * significand of the largest weight and 1 <= |r_t| < 2; hidden_t takes the power of two,
+ * relative to the largest.
  *
  *   hidden, weight, targets, weights : as in the forward pass; lse: its output.
  *   dhidden : out, rows of the operands' type; may be NULL.  0 for a token that

@@ -2,11 +2,12 @@
 // in the same kernel: the pieces of a log-sum-exp, the gradient of a softmax cross
 // entropy, or the sums' rounding into a bucket.
 //
-// Persistent pairs of CTAs.  In each, one thread loads (TMA, six stages of 32 KB), one
-// thread of the first CTA multiplies (tcgen05, both CTAs' tensor memory), eight warps take finished tiles out
-// of tensor memory while the next tile is summed in its other half.
+// Persistent pairs of CTAs.  In each, one thread loads (TMA, five stages of 32 KB),
+// one thread of the first CTA multiplies (tcgen05, both CTAs' tensor memory), and
+// sixteen warps take finished tiles, 32 rows of 64 columns each, out of tensor
+// memory while the next tile is summed in its other half.
 #include <algorithm>
-#include <mutex>
+#include <type_traits>
 
 #include "psgd_mma.cuh"
 
@@ -33,7 +34,7 @@ struct Walk {
   long long at, end;
   int piece;
   __device__ Walk(const Product& p, int m, int k, int pairs_, int pair_)
-      : s(schedule_of(m, p.n, k, pairs_, p.slots != nullptr)), pairs(pairs_), pair(pair_), m_fast(p.m_fast), next(pair_), piece(0) {
+      : s(schedule_of(m, p.n, p.bn, k, pairs_, p.slots != nullptr)), pairs(pairs_), pair(pair_), m_fast(p.m_fast), next(pair_), piece(0) {
     at = pair < s.workers ? first_step(s, pair) : 0;
     end = pair < s.workers ? first_step(s, pair + 1) : 0;
   }
@@ -69,23 +70,76 @@ __device__ __forceinline__ float exp_of(float x) {
   return y;
 }
 
-// A 32 x 32 block (lane = row) through a warp's staging into rows of `out`, 32 elements side by side.
-__device__ __forceinline__ void put_block(const float (&v)[32], float* st, int lane, void* out, int dtype, long long ldo, long long row0,
-                                          int rows, long long col0, int cols, float scale, int accumulate) {
+// Four elements of one row, side by side, at a multiple of their size.
+template <typename T> __device__ __forceinline__ float4 load4(const T* p) {
+  if constexpr (sizeof(T) == 4) {
+    return *reinterpret_cast<const float4*>(p);
+  } else {
+    const uint2 u = *reinterpret_cast<const uint2*>(p);
+    const T* e = reinterpret_cast<const T*>(&u);
+    return make_float4(ops::to_f(e[0]), ops::to_f(e[1]), ops::to_f(e[2]), ops::to_f(e[3]));
+  }
+}
+template <typename T> __device__ __forceinline__ void store4(T* p, float4 v) {
+  if constexpr (sizeof(T) == 4) *reinterpret_cast<float4*>(p) = v;
+  else *reinterpret_cast<uint2*>(p) = make_uint2(ops::pack2<T>(v.x, v.y), ops::pack2<T>(v.z, v.w));
+}
+__device__ __forceinline__ float4 plus(float4 a, float4 b) { return make_float4(a.x + b.x, a.y + b.y, a.z + b.z, a.w + b.w); }
+
+// A staged 32 x 32 block into rows of `to`.  Aligned rows: eight lanes a row, four rows at a time; others: a row at a
+// time.  What is there already is read for several rows together.
+template <typename T>
+__device__ __forceinline__ void put_rows(const float4* st, int lane, T* to, long long ldo, int rows, int cols, bool vec, bool add) {
+  if (vec && cols >= 32) {
+    const int r = lane >> 3, c = lane & 7;
+    T* at = to + r * ldo + 4 * c;
+#pragma unroll 1
+    for (int half = 0; half < 2; ++half) {
+      float4 old[4];
+      if (add) {
 #pragma unroll
-  for (int c = 0; c < 32; ++c) st[lane * 32 + (c ^ lane)] = v[c] * scale;
-  __syncwarp();
-  if (lane < cols) {
-    for (int r = 0; r < rows; ++r) {
-      const long long i = (row0 + r) * ldo + col0 + lane;
-      const float x = st[r * 32 + (lane ^ r)];
-      ops::store_any(out, dtype, i, accumulate ? ops::read_any(out, dtype, i) + x : x);
+        for (int i = 0; i < 4; ++i)
+          if (half * 16 + 4 * i + r < rows) old[i] = load4(at + (half * 16 + 4 * i) * ldo);
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int row = half * 16 + 4 * i + r;
+        const float4 y = st[row * 8 + (c ^ (row & 7))];
+        if (row < rows) store4(at + (half * 16 + 4 * i) * ldo, add ? plus(old[i], y) : y);
+      }
+    }
+  } else if (lane < cols) {
+    const float* s = reinterpret_cast<const float*>(st);
+    T* at = to + lane;
+#pragma unroll 1
+    for (int r0 = 0; r0 < rows; r0 += 8, at += 8 * ldo) {
+      float old[8], y[8];
+#pragma unroll
+      for (int r = 0; r < 8; ++r) {
+        old[r] = add && r0 + r < rows ? ops::to_f(at[r * ldo]) : 0.f;
+        y[r] = s[(r0 + r) * 32 + (((lane >> 2) ^ (r & 7)) << 2 | (lane & 3))];  // (r0 is a multiple of 8)
+      }
+#pragma unroll
+      for (int r = 0; r < 8; ++r)
+        if (r0 + r < rows) at[r * ldo] = ops::from_f<T>(add ? old[r] + y[r] : y[r]);
     }
   }
+}
+// A 32 x 32 block (lane = row) through a warp's staging into `out`, from (row0, col0) on.
+template <typename T>
+__device__ __forceinline__ void put_block(const float* v, float4* st, int lane, const Product& p, int row0, int rows, int col0, int cols,
+                                          float scale) {
+  if (rows <= 0 || cols <= 0) return;
+#pragma unroll
+  for (int c = 0; c < 8; ++c)
+    st[lane * 8 + (c ^ (lane & 7))] = make_float4(v[4 * c] * scale, v[4 * c + 1] * scale, v[4 * c + 2] * scale, v[4 * c + 3] * scale);
+  __syncwarp();
+  put_rows((const float4*)st, lane, (T*)p.out + (long long)row0 * p.ldo + col0, p.ldo, rows, cols, p.vec, p.accumulate);
   __syncwarp();
 }
 
-template <int KIND>
+// T: OUT: out's type, GRAD: the operands', LSE: any.
+template <int KIND, typename T>
 __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) k_product(const __grid_constant__ Product p) {
   extern __shared__ __align__(1024) unsigned char raw[];
   __shared__ Shared sh;
@@ -129,15 +183,24 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) k_produ
       int stage = 0;
       uint32_t phase = 0;
       while (walk.take(run)) {
-        const int row = run.tm * kTile + (int)rank * kHalf, col = run.tn * kTile + (int)rank * kHalf;
+        const int row = run.tm * kTile + (int)rank * kHalf, col = run.tn * p.bn + (int)rank * (p.bn / 2);
+        // Of A with K rows, no more than the rows that there are: what bounds products of few rows is the lines of 128
+        // bytes that an SM can have under way (some 350).  What lies in the others' place gives rows that nobody takes.
+        const int rows_here = min(kHalf, m - row), rows_0 = min(kHalf, m - run.tm * kTile), rows_1 = min(kHalf, m - run.tm * kTile - kHalf);
+        const bool few = !p.a_m_rows && rows_1 < kHalf;
+        const int boxes = (max(rows_here, 0) + kFew - 1) / kFew;
+        const uint32_t bytes =
+            few ? 2 * kOperand + ((rows_0 + kFew - 1) / kFew + (max(rows_1, 0) + kFew - 1) / kFew) * (kFew * kStep * 2) : 2 * kStageBytes;
         for (int kb = run.k0; kb < run.k1; ++kb) {
           if (!bar_wait(&sh.empty[stage], phase ^ 1, dead)) break;
           const uint32_t a = saddr(stages + stage * kStageBytes), b = a + kOperand, bar = at_rank(saddr(&sh.full[stage]), 0);
-          if (rank == 0) bar_expect(&sh.full[stage], 2 * kStageBytes);
+          if (rank == 0) bar_expect(&sh.full[stage], bytes);
           const int x = kb * kStep;
           if (p.a_m_rows) {
             load_box(a, &p.a, row, x, bar);
             load_box(a + kOperand / 2, &p.a, row + 64, x, bar);
+          } else if (few) {
+            for (int i = 0; i < boxes; ++i) load_box(a + i * (kFew * kStep * 2), &p.a_few, x, row + i * kFew, bar);
           } else {
             load_box(a, &p.a, x, row, bar);
           }
@@ -157,137 +220,164 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) k_produ
     }
   } else if (warp == kEpilogueWarps + 1) {
     if (rank == 0 && lane == 0) {
-      const uint32_t idesc = instruction(p.bf16, p.a_m_rows, p.b_m_rows);
+      const uint32_t idesc = instruction(p.bf16, p.a_m_rows, p.b_m_rows, p.bn);
       const uint32_t a_step = step_bytes(p.a_m_rows) >> 4, b_step = step_bytes(p.b_m_rows) >> 4;
       int stage = 0, buf = 0;
       uint32_t phase = 0, turn = 0;
-      while (walk.take(run)) {
-        if (!bar_wait(&sh.drained[buf], turn ^ 1, dead)) break;
-        fence_after();
-        const uint32_t d = tmem + buf * kTile;
-        for (int kb = run.k0; kb < run.k1; ++kb) {
-          if (!bar_wait(&sh.full[stage], phase, dead)) break;
+      while (!*dead && walk.take(run)) {
+        for (int kb = run.k0; kb < run.k1;) {
+          if (!bar_wait(&sh.drained[buf], turn ^ 1, dead)) break;
           fence_after();
-          const uint32_t at = saddr(stages + stage * kStageBytes);
-          const uint64_t a = describe(at, p.a_m_rows), b = describe(at + kOperand, p.b_m_rows);
+          const uint32_t d = tmem + buf * kTile;
+          const int from = kb, to = p.chunk ? min(run.k1, kb + p.chunk) : run.k1;
+          for (; kb < to; ++kb) {
+            if (!bar_wait(&sh.full[stage], phase, dead)) break;
+            fence_after();
+            const uint32_t at = saddr(stages + stage * kStageBytes);
+            const uint64_t a = describe(at, p.a_m_rows), b = describe(at + kOperand, p.b_m_rows);
 #pragma unroll
-          for (int i = 0; i < kStep / 16; ++i) multiply(d, a + i * a_step, b + i * b_step, idesc, kb > run.k0 || i > 0);
-          commit_both(&sh.empty[stage]);
-          if (++stage == kStages) {
-            stage = 0;
-            phase ^= 1;
+            for (int i = 0; i < kStep / 16; ++i) multiply(d, a + i * a_step, b + i * b_step, idesc, kb > from || i > 0);
+            commit_both(&sh.empty[stage]);
+            if (++stage == kStages) {
+              stage = 0;
+              phase ^= 1;
+            }
           }
+          if (*dead) break;
+          commit_both(&sh.done[buf]);
+          buf ^= 1;
+          turn ^= buf == 0;
         }
-        if (*dead) break;
-        commit_both(&sh.done[buf]);
-        buf ^= 1;
-        turn ^= buf == 0;
       }
     }
   } else {
-    const int quarter = warp & 3, half = warp >> 2;
-    float* st = reinterpret_cast<float*>(staging + warp * kStaging);
+    const int quarter = warp & 3, group = warp >> 2;  // 32 lanes of tensor memory, 64 columns
+    float4* st = reinterpret_cast<float4*>(staging + warp * kStaging);
     const float scale = KIND == kOut && p.scale ? *p.scale : 1.f;
     int buf = 0;
-    uint32_t turn = 0;
+    uint32_t turn = 0, flip = 0;
+    bool alive = true;
     while (walk.take(run)) {
-      if (!warp_wait(&sh.done[buf], turn, dead)) break;
-      fence_after();
-      const uint32_t t = tmem + buf * kTile + half * kHalf + ((uint32_t)(quarter * 32) << 16);
       const int row0 = run.tm * kTile + (int)rank * kHalf + quarter * 32, row = row0 + lane;
-      const int col0 = run.tn * kTile + half * kHalf;
-      float v[32];
-      if constexpr (KIND == kOut) {
-        for (int c = 0; c < 4; ++c) {
-          if (run.k1 > run.k0) {
-            tmem_load32(t + c * 32, v);
-          } else {  // a sum of nothing
-#pragma unroll
-            for (int i = 0; i < 32; ++i) v[i] = 0.f;
-          }
-          if (run.slot >= 0) {
-            // groups of four columns, row by row: neighbouring lanes write neighbouring 16 bytes
-            float4* to = reinterpret_cast<float4*>(p.slots + run.slot * kSlotFloats) + (long long)rank * kHalf * kTile / 4 +
-                         (long long)(half * 32 + c * 8) * kHalf + quarter * 32 + lane;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) to[i * kHalf] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
-          } else {
-            put_block(v, st, lane, p.out, p.dtype, p.ldo, row0, min(32, m - row0), col0 + c * 32, min(32, p.n - col0 - c * 32), scale,
-                      p.accumulate);
-          }
-        }
-      } else if constexpr (KIND == kLse) {
-        const int tgt = row < m ? p.target[row] - p.column0 - col0 : -1;
-        const int left = p.vocab - p.column0 - col0;  // columns that are in the vocabulary
-        float top = -INFINITY, sum = 0.f;
-        for (int c = 0; c < 4; ++c) {
-          tmem_load32(t + c * 32, v);
-          if (left < c * 32 + 32) {
-#pragma unroll
-            for (int i = 0; i < 32; ++i)
-              if (c * 32 + i >= left) v[i] = -INFINITY;
-          }
-          float most = v[0];
-#pragma unroll
-          for (int i = 1; i < 32; ++i) most = fmaxf(most, v[i]);
-          if (tgt >= c * 32 && tgt < c * 32 + 32) {
-            float z = 0.f;
-#pragma unroll
-            for (int i = 0; i < 32; ++i) z = tgt - c * 32 == i ? v[i] : z;
-            p.at_target[row] = z;
-          }
-          const float now = fmaxf(top, most), from = now == -INFINITY ? 0.f : now;
-          sum *= top == -INFINITY ? 0.f : exp_of(top - now);
-          top = now;
-          float s[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-          for (int i = 0; i < 32; ++i) s[i & 3] += exp_of(v[i] - from);
-          sum += (s[0] + s[1]) + (s[2] + s[3]);
-        }
-        if (row < m) p.part[(long long)((p.column0 + col0) / kHalf) * p.part_rows + row] = make_float2(top, sum);
-      } else {
-        const bool in = row < m;
-        const float lse = in ? p.lse[row] : 0.f, factor = in ? p.factor[row] : 0.f;
-        const int tgt = in ? p.target[row] - p.column0 - col0 : -1;
-        const int left = in ? p.vocab - p.column0 - col0 : 0;
-        uint4* to = reinterpret_cast<uint4*>(st);
-        for (int box = 0; box < 2; ++box) {
-          if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");  // the staging's last box is out
-          __syncwarp();
-#pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            const int at = box * 64 + c * 32;
-            tmem_load32(t + at, v);
-#pragma unroll
-            for (int i = 0; i < 32; ++i) {
-              // a row or column that is none: 0 whatever was summed there
-              const float g = (exp_of(v[i] - lse) - (at + i == tgt ? 1.f : 0.f)) * factor;
-              v[i] = at + i < left ? g : 0.f;
-            }
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              uint4 u;
-              unsigned* w = &u.x;
-#pragma unroll
-              for (int e = 0; e < 4; ++e)
-                w[e] = p.bf16 ? ops::pack2<__nv_bfloat16>(v[8 * i + 2 * e], v[8 * i + 2 * e + 1])
-                              : ops::pack2<__half>(v[8 * i + 2 * e], v[8 * i + 2 * e + 1]);
-              to[lane * 8 + ((c * 4 + i) ^ (lane & 7))] = u;
-            }
-          }
-          fence_async();
-          __syncwarp();
-          if (lane == 0) {
-            store_box(&p.store, col0 + box * 64, row0, saddr(st));
-            asm volatile("cp.async.bulk.commit_group;" ::: "memory");
-          }
+      const int col0 = run.tn * p.bn + group * kCols;
+      // (loaded while the tile is summed)
+      int tgt = -1;
+      float lse = 0.f, factor = 0.f;
+      if constexpr (KIND != kOut) {
+        if (row < m) tgt = p.target[row] - p.column0 - col0;
+      }
+      if constexpr (KIND == kGrad) {
+        if (row < m) {
+          lse = p.lse[row];
+          factor = p.factor[row];
         }
       }
-      fence_before();
-      __syncwarp();
-      if (lane == 0) bar_arrive_at(at_rank(saddr(&sh.drained[buf]), 0));
-      buf ^= 1;
-      turn ^= buf == 0;
+      float v[kCols];  // this lane's row, 64 columns of it
+#pragma unroll
+      for (int i = 0; i < kCols; ++i) v[i] = 0.f;
+      for (int kb = run.k0; kb < run.k1; kb = p.chunk ? kb + p.chunk : run.k1) {
+        alive = alive && warp_wait(&sh.done[buf], turn, dead);
+        if (!alive) break;
+        fence_after();
+        const uint32_t t = tmem + buf * kTile + group * kCols + ((uint32_t)(quarter * 32) << 16);
+#pragma unroll
+        for (int c = 0; c < kCols; c += 16) {
+          float x[16];
+          tmem_load16(t + c, x);
+          tmem_wait();
+#pragma unroll
+          for (int i = 0; i < 16; ++i) v[c + i] += x[i];
+        }
+        fence_before();
+        __syncwarp();
+        if (lane == 0) bar_arrive_at(at_rank(saddr(&sh.drained[buf]), 0));
+        buf ^= 1;
+        turn ^= buf == 0;
+      }
+      if (KIND != kLse && !alive) break;  // (kLse: on to the barriers that the other warps are at)
+      if constexpr (KIND == kOut) {
+        if (group * kCols >= p.bn) continue;
+        if (run.slot >= 0) {
+          // groups of four columns, row by row: neighbouring lanes write neighbouring 16 bytes
+          float4* to = reinterpret_cast<float4*>(p.slots + run.slot * kSlotFloats) + (long long)rank * kHalf * kTile / 4 +
+                       (long long)(group * (kCols / 4)) * kHalf + quarter * 32 + lane;
+#pragma unroll
+          for (int i = 0; i < kCols / 4; ++i) to[i * kHalf] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+        } else {
+          const int end = min(p.n, run.tn * p.bn + p.bn);
+          put_block<T>(v, st, lane, p, row0, min(32, m - row0), col0, min(32, end - col0), scale);
+          put_block<T>(v + 32, st, lane, p, row0, min(32, m - row0), col0 + 32, min(32, end - col0 - 32), scale);
+        }
+      } else if constexpr (KIND == kLse) {
+        const int left = p.vocab - p.column0 - col0;  // columns that are in the vocabulary
+        if (left < kCols) {
+#pragma unroll
+          for (int i = 0; i < kCols; ++i)
+            if (i >= left) v[i] = -INFINITY;
+        }
+        // without the target's, which is added with more care at the end
+        if (__any_sync(0xffffffffu, tgt >= 0 && tgt < kCols)) {
+#pragma unroll
+          for (int i = 0; i < kCols; ++i) v[i] = tgt == i ? -INFINITY : v[i];
+        }
+        float most[4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          most[c] = v[c];
+#pragma unroll
+          for (int i = 1; i < kCols / 4; ++i) most[c] = fmaxf(most[c], v[4 * i + c]);
+        }
+        const float top = fmaxf(fmaxf(most[0], most[1]), fmaxf(most[2], most[3])), from = top == -INFINITY ? 0.f : top;
+        float s[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int i = 0; i < kCols; ++i) s[i & 3] += exp_of(v[i] - from);
+        // the four warps of these rows join their columns, through each other's staging; two halves of it in turn, so that
+        // one barrier a tile is enough
+        float2* mine = reinterpret_cast<float2*>(staging + warp * kStaging) + flip * 32;
+        mine[lane] = make_float2(top, (s[0] + s[1]) + (s[2] + s[3]));
+        asm volatile("bar.sync %0, 128;" ::"r"(1 + quarter) : "memory");
+        if (group == 0 && row < m) {
+          float2 x[4];
+          float most_of = -INFINITY, sum = 0.f;
+#pragma unroll
+          for (int g = 0; g < 4; ++g) {
+            x[g] = (reinterpret_cast<const float2*>(staging + (g * 4 + quarter) * kStaging) + flip * 32)[lane];
+            most_of = fmaxf(most_of, x[g].x);
+          }
+          // (columns without a logit above -infinity have a sum of 0, or NaN, which stays)
+#pragma unroll
+          for (int g = 0; g < 4; ++g) sum += x[g].y * (x[g].x == -INFINITY ? 0.f : exp_of(x[g].x - most_of));
+          p.part[(long long)((p.column0 + col0) / kPartCols) * p.part_rows + row] = make_float2(most_of, sum);
+        }
+        flip ^= 1;
+      } else {
+        const int left = row < m ? p.vocab - p.column0 - col0 : 0;
+        if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");  // the staging's last box is out
+        __syncwarp();
+        uint4* to = reinterpret_cast<uint4*>(st);
+#pragma unroll
+        for (int i = 0; i < kCols / 8; ++i) {
+          unsigned w[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            float g[2];
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              const int at = 8 * i + 2 * e + k;
+              // a row or column that is none: 0 whatever was summed there
+              g[k] = at < left ? (exp_of(v[at] - lse) - (at == tgt ? 1.f : 0.f)) * factor : 0.f;
+            }
+            w[e] = ops::pack2<T>(g[0], g[1]);
+          }
+          to[lane * 8 + (i ^ (lane & 7))] = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+        fence_async();
+        __syncwarp();
+        if (lane == 0) {
+          store_box(&p.store, col0, row0, saddr(st));
+          asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+        }
+      }
     }
     if (KIND == kGrad && lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
   }
@@ -304,21 +394,22 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) k_produ
 }
 
 // The sum of a split tile's parts, in the order of the summed dimension.  A CTA takes 32 rows of 64 columns.
-__global__ void __launch_bounds__(64) k_join(const __grid_constant__ Product p, int pairs) {
-  __shared__ float st[2][32 * 32];
+template <typename T> __global__ void __launch_bounds__(64) k_join(const __grid_constant__ Product p, int pairs) {
+  __shared__ float4 st[2][32 * 8];
   after_previous();
   next_may_launch();
   const int live = p.live ? *p.live : 0;
   const int m = p.live_is == 1 ? live : p.m, k = p.live_is == 2 ? live : p.k;
-  const Schedule s = schedule_of(m, p.n, k, pairs, true);
+  const Schedule s = schedule_of(m, p.n, p.bn, k, pairs, true);
   const int i = blockIdx.y;  // of the tiles that are cut
   if (i >= s.tiles - s.whole) return;
   const int tile = s.whole + i;
   const int tm = p.m_fast ? tile % s.mt : tile / s.nt, tn = p.m_fast ? tile / s.mt : tile % s.nt;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rows32 = blockIdx.x >> 2, cols64 = blockIdx.x & 3;  // of 8 and of 4
-  const int row0 = tm * kTile + rows32 * 32, col0 = tn * kTile + cols64 * 64 + warp * 32;
-  if (row0 >= m || col0 >= p.n) return;
+  const int row0 = tm * kTile + rows32 * 32, col0 = tn * p.bn + cols64 * 64 + warp * 32;
+  const int end = min(p.n, tn * p.bn + p.bn);
+  if (row0 >= m || col0 >= end) return;
   const long long lo = (long long)i * s.kb, hi = lo + s.kb;
   int w = (int)(lo * s.workers / s.steps);
   while (w > 0 && first_step(s, w) > lo) --w;
@@ -340,8 +431,7 @@ __global__ void __launch_bounds__(64) k_join(const __grid_constant__ Product p, 
       v[4 * c + 3] += x.w;
     }
   }
-  put_block(v, st[warp], lane, p.out, p.dtype, p.ldo, row0, min(32, m - row0), col0, min(32, p.n - col0), p.scale ? *p.scale : 1.f,
-            p.accumulate);
+  put_block<T>(v, st[warp], lane, p, row0, min(32, m - row0), col0, min(32, end - col0), p.scale ? *p.scale : 1.f);
 }
 
 using Encode = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
@@ -373,18 +463,21 @@ cudaError_t make_map(CUtensorMap* map, const void* p, long long rows, long long 
 }
 
 namespace {
-template <int KIND> cudaError_t raise(int device) {
+template <int KIND, typename T> cudaError_t raise(int device) {
   static std::atomic<unsigned long long> raised{0};
-  return ops::raise_smem(k_product<KIND>, raised, device, kSmem);
+  return ops::raise_smem(k_product<KIND, T>, raised, device, kSmem);
 }
-template <int KIND> cudaError_t go(const Product& p, unsigned pairs, int device, cudaStream_t st) {
-  const cudaError_t e = raise<KIND>(device);
-  return e != cudaSuccess ? e : ops::launch_early(k_product<KIND>, 2 * pairs, kThreads, kSmem, 1, st, p);
+template <int KIND, typename T> cudaError_t go(const Product& p, unsigned pairs, int device, cudaStream_t st) {
+  const cudaError_t e = raise<KIND, T>(device);
+  return e != cudaSuccess ? e : ops::launch_early(k_product<KIND, T>, 2 * pairs, kThreads, kSmem, 1, st, p);
+}
+template <typename F> cudaError_t by_type(int dtype, F&& f) {
+  return dtype == PSGD_F32 ? f((float*)nullptr) : dtype == PSGD_F16 ? f((__half*)nullptr) : f((__nv_bfloat16*)nullptr);
 }
 }  // namespace
 
 cudaError_t pairs_of(int device, int* pairs) {
-  cudaError_t e = raise<kOut>(device);
+  cudaError_t e = raise<kOut, float>(device);
   if (e != cudaSuccess) return e;
   int sms = 0;
   e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, device);
@@ -398,25 +491,34 @@ cudaError_t pairs_of(int device, int* pairs) {
   attr.val.clusterDim = {2, 1, 1};
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  e = cudaOccupancyMaxActiveClusters(pairs, k_product<kOut>, &cfg);
+  e = cudaOccupancyMaxActiveClusters(pairs, k_product<kOut, float>, &cfg);
   if (e == cudaSuccess && *pairs < 1) e = cudaErrorLaunchOutOfResources;
   return e;
 }
 
-cudaError_t enqueue(Epilogue kind, const Product& p, int device, int pairs, cudaStream_t st) {
+cudaError_t enqueue(Epilogue kind, Product p, int device, int pairs, cudaStream_t st) {
+  // (the others' columns go by 128)
+  p.bn = kind == kOut ? columns_of(p.n) : kTile;
+  if (kind == kOut) {
+    const int size = 4 * ops::dtype_size(p.dtype);
+    p.vec = (uintptr_t)p.out % size == 0 && (p.ldo % 4 == 0 || p.m == 1);
+  }
   // (extents that the device knows are at most these)
-  const long long tiles = ops::units(p.m, kTile) * ops::units(p.n, kTile);
+  const long long tiles = ops::units(p.m, kTile) * ops::units(p.n, p.bn);
   if (tiles == 0) return cudaSuccess;
   // split tiles want every pair, also where there are few of them
   const unsigned grid = (unsigned)(p.slots ? pairs : std::min<long long>(pairs, tiles));
   cudaError_t e;
-  if (kind == kLse) e = go<kLse>(p, grid, device, st);
-  else if (kind == kGrad) e = go<kGrad>(p, grid, device, st);
-  else e = go<kOut>(p, grid, device, st);
+  if (kind == kLse) e = go<kLse, float>(p, grid, device, st);
+  else if (kind == kGrad) e = p.bf16 ? go<kGrad, __nv_bfloat16>(p, grid, device, st) : go<kGrad, __half>(p, grid, device, st);
+  else e = by_type(p.dtype, [&](auto* t) { return go<kOut, std::remove_pointer_t<decltype(t)>>(p, grid, device, st); });
   if (e != cudaSuccess || kind != kOut || !p.slots) return e;
   // which tiles are cut goes by the extents that the device knows; with those of the host there may be none
-  if (!p.live && schedule_of(p.m, p.n, p.k, pairs, true).workers == 0) return e;
-  return ops::launch_early(k_join, dim3(32, (unsigned)std::min<long long>(tiles, pairs - 1)), 64, 0, 1, st, p, pairs);
+  if (!p.live && schedule_of(p.m, p.n, p.bn, p.k, pairs, true).workers == 0) return e;
+  const dim3 parts(32, (unsigned)std::min<long long>(tiles, pairs - 1));
+  return by_type(p.dtype, [&](auto* t) {
+    return ops::launch_early(k_join<std::remove_pointer_t<decltype(t)>>, parts, 64, 0, 1, st, p, pairs);
+  });
 }
 
 }  // namespace mma

@@ -5,14 +5,14 @@
 //
 // The logits are made tile by tile on the tensor cores and used where they are
 // made (psgd_gemm.cu): the forward pass leaves the largest logit and the sum of
-// exponentials of every 128 columns of a row, the backward pass makes them again
+// exponentials of every 256 columns of a row, the backward pass makes them again
 // and leaves G, rounded to 16 bits, for a piece of the vocabulary at a time; both
 // gradients are products of that piece.  No memory grows with tokens x vocabulary
 // but those pieces, which are bounded.
 //
 // Tokens that count (a target in the vocabulary, a weight that is not 0) are moved
 // together first, so that padding costs nothing, and what its rows hold touches
-// nothing.  A weight is split into its exponent and the rest, w_t = r_t 2^e_t:
+// nothing.  A weight is split, w_t = s r_t 2^e_t with s the largest one's significand and 1 <= |r_t| < 2:
 // G's rows are rounded with r_t (and 2^14 for f16, whose smallest step is 6e-8),
 // dh's rows are multiplied by the power of two at the end, and h's rows by
 // 2^(e_t - max e) for dW, which is exact where the weights are of one size.  So G
@@ -36,12 +36,12 @@ struct psgd_linear_ce {
   void* g = nullptr;
   float* dh = nullptr;       // cap x dp
   float* slots = nullptr;
-  float2* part = nullptr;    // cap for every 128 columns
-  float *at_target = nullptr, *lse = nullptr, *factor = nullptr;
+  float2* part = nullptr;    // cap for every 256 columns
+  float *lse = nullptr, *factor = nullptr;
   int *row = nullptr, *target = nullptr, *exponent = nullptr;  // of the tokens that count
   int* place = nullptr;      // of a token among them, or -1
   int* count = nullptr;      // [0]: tokens that count, [1]: largest exponent, [2]: error
-  float* scale = nullptr;    // dW's
+  float* scale = nullptr;    // [0]: dW's, [1]: a row of dh's without its power of two
   size_t bytes = 0;
 };
 
@@ -69,68 +69,113 @@ __device__ __forceinline__ bool counts(const Tokens& t, int i) {
   return y >= 0 && y < t.vocab && weight_of(t, i) != 0.f;
 }
 
-// Which tokens count, in their order, and the exponents of their weights.  One CTA, 1024 tokens at a time.
-__global__ void __launch_bounds__(1024) k_plan(Tokens t, int* place, int* row, int* target, float* factor, int* exponent, int* count,
-                                               float* scale, float grad_scale, int shift) {
-  __shared__ int sums[32], most[32];
+// Which tokens count, in their order, and their weights: w = r 2^e s with s the largest weight's significand, so that
+// weights that are all the same have r = 1 and lose nothing to a rounding.  One CTA, eight tokens a thread at a time.
+constexpr int kPlanItems = 8;
+__device__ void plan(const Tokens& t, int* place, int* row, int* target, float* factor, int* exponent, int* count, float* scale,
+                     float grad_scale, int shift) {
+  __shared__ int sums[32];
+  __shared__ float most[32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  after_previous();
-  next_may_launch();
-  int before = 0, top = INT_MIN;
-  for (int base = 0; base < t.tokens; base += 1024) {
-    const int i = base + (int)threadIdx.x;
-    const bool in = i < t.tokens && counts(t, i);
-    const unsigned votes = __ballot_sync(0xffffffffu, in);
-    if (lane == 0) sums[warp] = __popc(votes);
+  constexpr int kTurn = 1024 * kPlanItems;
+  // tokens that count among this thread's from `first` on, as bits
+  const auto flags = [&](int first) {
+    unsigned bits = 0;
+#pragma unroll
+    for (int k = 0; k < kPlanItems; ++k)
+      if (first + k < t.tokens && counts(t, first + k)) bits |= 1u << k;
+    return bits;
+  };
+  unsigned mine = 0;
+  float top = 0.f;
+  if (t.weights) {
+    for (int base = 0; base < t.tokens; base += kTurn) {
+      const int first = base + (int)threadIdx.x * kPlanItems;
+      mine = flags(first);
+#pragma unroll
+      for (int k = 0; k < kPlanItems; ++k)
+        if (mine >> k & 1) {
+          const float w = fabsf(weight_of(t, first + k));
+          if (isfinite(w)) top = fmaxf(top, w);
+        }
+    }
+    top = warp_max(top);
+    if (lane == 0) most[warp] = top;
     __syncthreads();
-    int n = sums[lane];
+    top = warp_max(most[lane]);
+  } else {
+    mine = flags((int)threadIdx.x * kPlanItems);
+    top = 1.f;
+  }
+  if (top == 0.f) top = 1.f;  // no token counts, or none whose weight is finite
+  const int e_top = ilogbf(top);
+  const float s = scalbnf(top, -e_top);
+  int before = 0;
+  for (int base = 0; base < t.tokens; base += kTurn) {
+    const int first = base + (int)threadIdx.x * kPlanItems;
+    const unsigned bits = t.tokens <= kTurn ? mine : flags(first);
+    int n = __popc(bits);
 #pragma unroll
     for (int o = 1; o < 32; o *= 2) {
       const int up = __shfl_up_sync(0xffffffffu, n, o);
       if (lane >= o) n += up;
     }
-    const int all = __shfl_sync(0xffffffffu, n, 31), mine = warp ? __shfl_sync(0xffffffffu, n, warp - 1) : 0;
-    const int at = before + mine + __popc(votes & ((1u << lane) - 1));
-    if (i < t.tokens) place[i] = in ? at : -1;
-    if (in) {
+    if (lane == 31) sums[warp] = n;
+    __syncthreads();
+    int all = sums[lane];
+#pragma unroll
+    for (int o = 1; o < 32; o *= 2) {
+      const int up = __shfl_up_sync(0xffffffffu, all, o);
+      if (lane >= o) all += up;
+    }
+    int at = before + n - __popc(bits) + (warp ? __shfl_sync(0xffffffffu, all, warp - 1) : 0);
+    before += __shfl_sync(0xffffffffu, all, 31);
+#pragma unroll
+    for (int k = 0; k < kPlanItems; ++k) {
+      const int i = first + k;
+      if (i >= t.tokens) break;
+      const bool in = bits >> k & 1;
+      place[i] = in ? at : -1;
+      if (!in) continue;
       const float w = weight_of(t, i);
-      const int e = isfinite(w) ? ilogbf(w) : 0;
+      int e = 0;
+      float r = w;
+      if (isfinite(w)) {
+        e = ilogbf(w);
+        r = scalbnf(w, -e) / s;
+        if (fabsf(r) < 1.f) {
+          r *= 2.f;
+          --e;
+        }
+      }
       row[at] = i;
       target[at] = (int)target_of(t, i);
-      factor[at] = scalbnf(w, shift - e);
+      factor[at] = scalbnf(r, shift);
       exponent[at] = e;
-      top = max(top, e);
+      ++at;
     }
-    before += all;
     __syncthreads();
   }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-  if (lane == 0) most[warp] = top;
-  __syncthreads();
   if (threadIdx.x == 0) {
-    for (int w = 1; w < 32; ++w) top = max(top, most[w]);
-    if (before == 0) top = 0;
     count[0] = before;
-    count[1] = top;
-    *scale = scalbnf(grad_scale, top - shift);
+    count[1] = e_top;
+    scale[0] = scalbnf(grad_scale * s, e_top - shift);
+    scale[1] = grad_scale * s;
   }
 }
 
-// The rows of the tokens that count, side by side, then rows of zeros up to a multiple of 256 (the products'
-// tiles read those).  hs (backward): the rows times 2^(e - max e); lse: theirs.
+// The rows of the tokens that count, side by side.  hs (backward): the rows times 2^(e - max e), then rows of zeros up to
+// a whole step of the sum over tokens; lse: theirs.
 template <typename T, int V>
-__global__ void __launch_bounds__(128) k_gather(const T* src, long long stride, int dim, const int* row, const int* exponent, const int* count,
-                                                T* h, T* hs, long long dp, const float* lse_of, float* lse) {
-  after_previous();
-  next_may_launch();
-  const int n = count[0], end = (n + mma::kTile - 1) / mma::kTile * mma::kTile;
-  for (int r = blockIdx.x; r < end; r += gridDim.x) {
+__device__ __forceinline__ void gather_rows(const T* src, long long stride, int dim, const int* row, const int* exponent, const int* count,
+                                            T* h, T* hs, long long dp, const float* lse_of, float* lse, int block, int blocks) {
+  const int n = count[0], end = hs ? (n + mma::kStep - 1) / mma::kStep * mma::kStep : n;
+  for (int r = block; r < end; r += blocks) {
     const bool in = r < n;
     const T* from = src + (in ? (long long)row[r] * stride : 0);
     const float f = in && hs ? scalbnf(1.f, max(exponent[r] - count[1], -200)) : 1.f;
     if (lse && in && threadIdx.x == 0) lse[r] = lse_of[row[r]];
-    for (int c = threadIdx.x * V; c < dim; c += 128 * V) {
+    for (int c = threadIdx.x * V; c < dim; c += blockDim.x * V) {
       if constexpr (V == 1) {
         const T x = in ? from[c] : from_f<T>(0.f);
         h[r * dp + c] = x;
@@ -152,11 +197,68 @@ __global__ void __launch_bounds__(128) k_gather(const T* src, long long stride, 
     }
   }
 }
+template <typename T, int V>
+__global__ void __launch_bounds__(128) k_gather(const T* src, long long stride, int dim, const int* row, const int* exponent, const int* count,
+                                                T* h, T* hs, long long dp, const float* lse_of, float* lse) {
+  after_previous();
+  next_may_launch();
+  gather_rows<T, V>(src, stride, dim, row, exponent, count, h, hs, dp, lse_of, lse, blockIdx.x, gridDim.x);
+}
 
-// Losses and log-sum-exps of 32 tokens a CTA from the pieces of 128 columns, whose order the warps share.
+__global__ void __launch_bounds__(1024) k_plan(Tokens t, int* place, int* row, int* target, float* factor, int* exponent, int* count,
+                                               float* scale, float grad_scale, int shift) {
+  after_previous();
+  next_may_launch();
+  plan(t, place, row, target, factor, exponent, count, scale, grad_scale, shift);
+}
+// Both in one launch, where the rows are little enough for one CTA.
+constexpr long long kFewElements = 32768;
+template <typename T, int V>
+__global__ void __launch_bounds__(1024) k_plan_gather(Tokens t, int* place, int* row, int* target, float* factor, int* exponent, int* count,
+                                                      float* scale, float grad_scale, int shift, const T* src, long long stride, int dim, T* h,
+                                                      T* hs, long long dp, const float* lse_of, float* lse) {
+  after_previous();
+  next_may_launch();
+  plan(t, place, row, target, factor, exponent, count, scale, grad_scale, shift);
+  __syncthreads();
+  gather_rows<T, V>(src, stride, dim, row, exponent, count, h, hs, dp, lse_of, lse, 0, 1);
+}
+
+// A warp's product of two rows of 16-bit elements, of any alignment.
+template <typename T> __device__ __forceinline__ float warp_dot(const T* a, const T* b, int dim, bool vec) {
+  const int lane = threadIdx.x & 31;
+  float sum = 0.f;
+  for (int c = lane * 8; c < dim; c += 256) {
+    F2 x[4], y[4], s = f2(0.f, 0.f);
+    if (vec) {
+      to_pairs<T>(*reinterpret_cast<const uint4*>(a + c), x);
+      to_pairs<T>(*reinterpret_cast<const uint4*>(b + c), y);
+    } else {  // in the same order
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int u = c + 2 * i, v = u + 1;
+        x[i] = f2(u < dim ? to_f(a[u]) : 0.f, v < dim ? to_f(a[v]) : 0.f);
+        y[i] = f2(u < dim ? to_f(b[u]) : 0.f, v < dim ? to_f(b[v]) : 0.f);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) s = fma(x[i], y[i], s);
+    float u, v;
+    split(s, u, v);
+    sum += u + v;
+  }
+  return warp_sum(sum);
+}
+
+// Losses and log-sum-exps of 32 tokens a CTA from the pieces of 256 columns, whose order the warps share, and the
+// targets' logits, a warp each.  Those are summed here, in rounded fp32: where a target is likely, its logit is by far
+// the largest, the loss is the small rest, and the tensor cores' drift on a large sum (2e-6 of it) would be most of it.
+template <typename T>
 __global__ void __launch_bounds__(1024) k_losses(Tokens t, const int* place, const float2* part, long long part_rows, int parts,
-                                                 const float* at_target, float* losses, float* lses) {
+                                                 const T* hidden, long long hidden_stride, const T* weight, long long weight_stride, int dim,
+                                                 bool vec, float* losses, float* lses) {
   __shared__ float2 all[32][33];
+  __shared__ float logit[32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, i = blockIdx.x * 32 + lane;
   after_previous();
   next_may_launch();
@@ -169,30 +271,63 @@ __global__ void __launch_bounds__(1024) k_losses(Tokens t, const int* place, con
     top = now;
   };
   if (at >= 0)
-    for (int p = warp; p < parts; p += 32) add(__ldcg(part + p * part_rows + at));
+    for (int p = warp; p < parts; p += 32 * 8) {  // eight reads under way
+      float2 x[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) x[k] = p + 32 * k < parts ? __ldcg(part + (p + 32 * k) * part_rows + at) : make_float2(-INFINITY, 0.f);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) add(x[k]);
+    }
   all[warp][lane] = make_float2(top, sum);
+  // (all lanes have the CTA's places: token `warp` is lane `warp`'s)
+  if (__shfl_sync(0xffffffffu, at, warp) >= 0) {
+    const long long mine = blockIdx.x * 32 + warp;
+    const float z = warp_dot(hidden + mine * hidden_stride, weight + target_of(t, (int)mine) * weight_stride, dim, vec);
+    if (lane == 0) logit[warp] = z;
+  }
   __syncthreads();
   if (warp || i >= t.tokens) return;
   float loss = 0.f, lse = 0.f;
   if (at >= 0) {
     for (int w = 1; w < 32; ++w) add(all[w][lane]);
-    lse = top + logf(sum);
-    loss = weight_of(t, i) * (lse - at_target[at]);
+    const float z = logit[lane];
+    float rest;
+    if (z >= top) {  // of a target that is nearly certain the loss is what the others add
+      rest = z == INFINITY ? NAN : log1pf(sum * __expf(top - z));
+      lse = z + rest;
+    } else {
+      const float r = logf(sum + __expf(z - top));
+      rest = (top - z) + r;
+      lse = top + r;
+    }
+    loss = weight_of(t, i) * rest;
   }
   losses[i] = loss;
   lses[i] = lse;
 }
 
 // dh of every token: its row of the sums times its power of two, 0 for a token that does not count.
-template <typename T>
+template <typename T, int V>
 __global__ void __launch_bounds__(128) k_dhidden(const float* sums, long long dp, const int* place, const int* exponent, int tokens, int dim,
-                                                 float grad_scale, int shift, T* dh, long long stride) {
+                                                 const float* scale, int shift, T* dh, long long stride) {
   after_previous();
   next_may_launch();
   for (int i = blockIdx.x; i < tokens; i += gridDim.x) {
     const int at = place[i];
-    const float f = at >= 0 ? scalbnf(grad_scale, exponent[at] - shift) : 0.f;
-    for (int c = threadIdx.x; c < dim; c += 128) dh[i * stride + c] = from_f<T>(at >= 0 ? sums[at * dp + c] * f : 0.f);
+    const float f = at >= 0 ? scalbnf(scale[1], exponent[at] - shift) : 0.f;
+    for (int c = threadIdx.x * V; c < dim; c += 128 * V) {
+      float v[V];
+      if constexpr (V == 1) {
+        v[0] = at >= 0 ? sums[at * dp + c] * f : 0.f;
+      } else {
+#pragma unroll
+        for (int k = 0; k < V; k += 4) {
+          const float4 x = at >= 0 ? *reinterpret_cast<const float4*>(sums + at * dp + c + k) : make_float4(0.f, 0.f, 0.f, 0.f);
+          v[k] = x.x * f, v[k + 1] = x.y * f, v[k + 2] = x.z * f, v[k + 3] = x.w * f;
+        }
+      }
+      store_pack<T, V>(dh + i * stride + c, v);
+    }
   }
 }
 
@@ -226,39 +361,45 @@ struct Call {
         in_place(aligned16(weight_) && ws % 8 == 0 && ws >= h_->dim), t{targets, bits, weights, (int)tokens, h_->vocab},
         st((cudaStream_t)stream) {}
 
-  void plan(float grad_scale) {
-    e = launch_early(k_plan, 1, 1024, 0, 1, st, t, h->place, h->row, h->target, h->factor, h->exponent, h->count, h->scale, grad_scale,
-                     bf16 ? 0 : kF16Shift);
-  }
-  void gather(bool backward, const float* lse) {
-    const unsigned grid = (unsigned)std::min<long long>(units(t.tokens, mma::kTile) * mma::kTile, 4096);
-    if (e != cudaSuccess || grid == 0) return;
+  // The tokens that count, side by side.
+  void gather(bool backward, const float* lse, float grad_scale) {
+    const int shift = bf16 ? 0 : kF16Shift;
     const bool vec = h->dim % 8 == 0 && aligned16(hidden) && hidden_stride % 8 == 0;
+    const bool few = (long long)t.tokens * h->dim <= kFewElements;
+    if (!few)
+      e = launch_early(k_plan, 1, 1024, 0, 1, st, t, h->place, h->row, h->target, h->factor, h->exponent, h->count, h->scale, grad_scale, shift);
+    if (e != cudaSuccess) return;
     void* hs = backward ? h->hs : nullptr;
     const auto go = [&](auto* tt, auto v) {
       using T = std::remove_pointer_t<decltype(tt)>;
-      e = launch_early(k_gather<T, decltype(v)::value>, grid, 128, 0, 1, st, (const T*)hidden, hidden_stride, (int)h->dim, h->row, h->exponent,
-                       h->count, (T*)h->h, (T*)hs, h->dp, lse, backward ? h->lse : nullptr);
+      constexpr int V = decltype(v)::value;
+      if (few)
+        e = launch_early(k_plan_gather<T, V>, 1, 1024, 0, 1, st, t, h->place, h->row, h->target, h->factor, h->exponent, h->count, h->scale,
+                         grad_scale, shift, (const T*)hidden, hidden_stride, (int)h->dim, (T*)h->h, (T*)hs, h->dp, lse,
+                         backward ? h->lse : nullptr);
+      else
+        e = launch_early(k_gather<T, V>, (unsigned)std::min(t.tokens + mma::kStep, 4096), 128, 0, 1, st, (const T*)hidden, hidden_stride,
+                         (int)h->dim, h->row, h->exponent, h->count, (T*)h->h, (T*)hs, h->dp, lse, backward ? h->lse : nullptr);
     };
     using One = std::integral_constant<int, 1>;
     using Eight = std::integral_constant<int, 8>;
     if (bf16) vec ? go((__nv_bfloat16*)nullptr, Eight()) : go((__nv_bfloat16*)nullptr, One());
     else vec ? go((__half*)nullptr, Eight()) : go((__half*)nullptr, One());
   }
-  // The rows [v0, v0 + n) of the weight as an operand either way around, and the first row of its map that counts.
-  void weight_map(CUtensorMap* k_rows, CUtensorMap* m_rows, long long v0, long long n, int* y0) {
+  // The rows [v0, v0 + n) of the weight as an operand, either way around.
+  void weight_map(mma::Product& z, CUtensorMap* m_rows, long long v0, long long n) {
     if (e != cudaSuccess) return;
     const void* p = weight;
     long long rows = h->vocab, stride = weight_stride;
-    *y0 = (int)v0;
+    z.b_y0 = (int)v0;
     if (!in_place) {
       e = mma::align_rows((const char*)weight + v0 * weight_stride * 2, weight_stride, n, h->dim, h->w, h->dp, st);
       p = h->w;
       rows = n;
       stride = h->dp;
-      *y0 = 0;
+      z.b_y0 = 0;
     }
-    if (e == cudaSuccess) e = mma::make_map(k_rows, p, rows, h->dim, stride, mma::box_rows(false), bf16);
+    if (e == cudaSuccess) e = mma::make_map(&z.b, p, rows, h->dim, stride, mma::box_rows(false), bf16);
     if (e == cudaSuccess && m_rows) e = mma::make_map(m_rows, p, rows, h->dim, stride, mma::box_rows(true), bf16);
   }
   // What a product over the logits is told: rows are tokens, columns [v0, v0 + n) of the vocabulary.
@@ -270,6 +411,7 @@ struct Call {
     p.column0 = (int)v0, p.vocab = (int)h->vocab;
     p.target = h->target;
     if (e == cudaSuccess) e = mma::make_map(&p.a, h->h, h->cap, h->dim, h->dp, mma::box_rows(false), bf16);
+    if (e == cudaSuccess) e = mma::make_map(&p.a_few, h->h, h->cap, h->dim, h->dp, mma::kFew, bf16);
     return p;
   }
 };
@@ -317,11 +459,11 @@ extern "C" int psgd_linear_ce_create(int64_t vocab, int64_t dim, int64_t max_tok
   get(&h->g, h->cap * h->piece * 2);
   get(&h->dh, h->cap * h->dp * 4);
   get(&h->slots, 2 * h->pairs * mma::kSlotFloats * 4);
-  get(&h->part, tiles * 2 * h->cap * 8);
-  for (float** p : {&h->at_target, &h->lse, &h->factor}) get(p, h->cap * 4);
+  get(&h->part, tiles * h->cap * 8);
+  for (float** p : {&h->lse, &h->factor}) get(p, h->cap * 4);
   for (int** p : {&h->row, &h->target, &h->exponent, &h->place}) get(p, h->cap * 4);
   get(&h->count, 16);
-  get(&h->scale, 4);
+  get(&h->scale, 8);
   if (e == cudaSuccess) e = cudaMemset(h->count, 0, 16);
   if (e == cudaSuccess) e = cudaDeviceSynchronize();
   if (e != cudaSuccess) {
@@ -337,7 +479,7 @@ extern "C" void psgd_linear_ce_destroy(psgd_linear_ce* h) {
   if (!h) return;
   {
     DeviceScope scope(h->device);
-    for (void* p : {h->h, h->hs, h->w, h->g, (void*)h->dh, (void*)h->slots, (void*)h->part, (void*)h->at_target, (void*)h->lse,
+    for (void* p : {h->h, h->hs, h->w, h->g, (void*)h->dh, (void*)h->slots, (void*)h->part, (void*)h->lse,
                     (void*)h->factor, (void*)h->row, (void*)h->target, (void*)h->exponent, (void*)h->place, (void*)h->count,
                     (void*)h->scale})
       cudaFree(p);
@@ -369,19 +511,26 @@ extern "C" int psgd_linear_ce_forward(psgd_linear_ce* h, const void* hidden, psg
   if (tokens == 0) return PSGD_OK;
   DeviceScope scope(h->device);
   Call c(h, hidden, dtype, hidden_stride, weight, weight_stride, targets, target_bits, weights, tokens, stream);
-  c.plan(1.f);
-  c.gather(false, nullptr);
+  c.gather(false, nullptr, 1.f);
   const long long step = c.in_place ? h->vocab : h->piece;
   for (long long v0 = 0; v0 < h->vocab && c.e == cudaSuccess; v0 += step) {
     const long long n = std::min(step, h->vocab - v0);
     mma::Product p = c.logits(v0, n);
-    c.weight_map(&p.b, nullptr, v0, n, &p.b_y0);
-    p.part = h->part, p.part_rows = h->cap, p.at_target = h->at_target;
+    c.weight_map(p, nullptr, v0, n);
+    p.part = h->part, p.part_rows = h->cap;
     if (c.e == cudaSuccess) c.e = mma::enqueue(mma::kLse, p, h->device, h->pairs, c.st);
   }
-  if (c.e == cudaSuccess)
-    c.e = launch_early(k_losses, (unsigned)units(tokens, 32), 1024, 0, 1, c.st, c.t, h->place, h->part, h->cap,
-                       (int)units(h->vocab, mma::kTile) * 2, h->at_target, losses, lse);
+  const auto go = [&](auto* tt) {
+    using T = std::remove_pointer_t<decltype(tt)>;
+    const bool vec = c.in_place && h->dim % 8 == 0 && aligned16(hidden) && hidden_stride % 8 == 0;
+    c.e = launch_early(k_losses<T>, (unsigned)units(tokens, 32), 1024, 0, 1, c.st, c.t, h->place, h->part, h->cap,
+                       (int)units(h->vocab, mma::kPartCols), (const T*)hidden, hidden_stride, (const T*)weight, weight_stride, (int)h->dim,
+                       vec, losses, lse);
+  };
+  if (c.e == cudaSuccess) {
+    if (c.bf16) go((__nv_bfloat16*)nullptr);
+    else go((__half*)nullptr);
+  }
   return c.e == cudaSuccess ? PSGD_OK : cuda_fail(who.c_str(), c.e);
 }
 
@@ -413,17 +562,17 @@ extern "C" int psgd_linear_ce_backward(psgd_linear_ce* h, const void* hidden, ps
   DeviceScope scope(h->device);
   Call c(h, hidden, dtype, hidden_stride, weight, weight_stride, targets, target_bits, weights, tokens, stream);
   const int shift = c.bf16 ? 0 : kF16Shift;
-  c.plan(grad_scale);
-  c.gather(true, lse);
+  c.gather(true, lse, grad_scale);
   for (long long v0 = 0; v0 < h->vocab && c.e == cudaSuccess; v0 += h->piece) {
     const long long n = std::min(h->piece, h->vocab - v0);
     mma::Product z = c.logits(v0, n), dh{}, dw{};
-    c.weight_map(&z.b, &dh.b, v0, n, &z.b_y0);
+    c.weight_map(z, &dh.b, v0, n);
     z.lse = h->lse, z.factor = h->factor;
     if (c.e == cudaSuccess) c.e = mma::make_map(&z.store, h->g, h->cap, h->piece, h->piece, 32, c.bf16);
     if (c.e == cudaSuccess && tokens > 0) c.e = mma::enqueue(mma::kGrad, z, h->device, h->pairs, c.st);
     if (dhidden && tokens > 0) {
       if (c.e == cudaSuccess) c.e = mma::make_map(&dh.a, h->g, h->cap, h->piece, h->piece, mma::box_rows(false), c.bf16);
+      if (c.e == cudaSuccess) c.e = mma::make_map(&dh.a_few, h->g, h->cap, h->piece, h->piece, mma::kFew, c.bf16);
       dh.m = (int)tokens, dh.n = (int)h->dim, dh.k = (int)n;
       dh.live = h->count, dh.live_is = 1;
       dh.b_m_rows = 1, dh.b_y0 = z.b_y0;
@@ -449,7 +598,8 @@ extern "C" int psgd_linear_ce_backward(psgd_linear_ce* h, const void* hidden, ps
     const unsigned grid = (unsigned)std::min<long long>(tokens, 8192);
     const auto go = [&](auto* tt) {
       using T = std::remove_pointer_t<decltype(tt)>;
-      c.e = launch_early(k_dhidden<T>, grid, 128, 0, 1, c.st, h->dh, h->dp, h->place, h->exponent, (int)tokens, (int)h->dim, grad_scale, shift,
+      const bool vec = h->dim % 8 == 0 && aligned16(dhidden) && dhidden_stride % 8 == 0;
+      c.e = launch_early(vec ? k_dhidden<T, 8> : k_dhidden<T, 1>, grid, 128, 0, 1, c.st, h->dh, h->dp, h->place, h->exponent, (int)tokens, (int)h->dim, h->scale, shift,
                          (T*)dhidden, dhidden_stride);
     };
     if (c.bf16) go((__nv_bfloat16*)nullptr);

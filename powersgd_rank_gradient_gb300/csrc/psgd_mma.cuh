@@ -2,7 +2,7 @@
 // pair of CTAs: tensor maps (TMA), barriers with bounded waits, tcgen05 with
 // cta_group::2, tensor memory.
 //
-// A pair computes 256 x 256 results, each CTA 128 rows of them in its own tensor
+// A pair computes 256 x 256 results (or fewer columns), each CTA 128 rows of them in its own tensor
 // memory (256 fp32 columns, of 512: one tile is drained while the next is summed).
 // Of every 64 elements of the summed dimension a CTA loads its own 128 rows of A
 // and 128 of the 256 columns of B, 32 KB together: with both CTAs' shared memory
@@ -25,17 +25,20 @@ namespace mma {
 
 constexpr int kTile = 256;     // rows and columns of a pair's tile
 constexpr int kHalf = 128;     // rows of a CTA's part
+constexpr int kFew = 32;
 constexpr int kStep = 64;      // elements of the summed dimension per stage
-constexpr int kStages = 6;
+constexpr int kStages = 5;
 constexpr int kOperand = kHalf * kStep * 2;  // bytes of one operand's part of a stage
 constexpr int kStageBytes = 2 * kOperand;
-constexpr int kEpilogueWarps = 8;
+constexpr int kEpilogueWarps = 16;
+constexpr int kCols = 64;      // columns of a tile that an epilogue warp takes, of 32 rows
 constexpr int kThreads = 32 * (kEpilogueWarps + 2);  // the last two warps: TMA and MMA
 constexpr int kStaging = 4096;                       // bytes of an epilogue warp's staging
 constexpr int kSmem = 1024 + kStages * kStageBytes + kEpilogueWarps * kStaging;
 
-// A wait gives up after this time, far beyond any normal one (and after so many tries, whatever the clock says).
-constexpr unsigned long long kWaitNs = 4000000000ull;
+// A wait gives up after so many cycles (four seconds), far beyond any normal one, and after so many tries, whatever the
+// clock says.
+constexpr long long kWaitCycles = 8000000000ll;
 constexpr int kWaitTries = 1 << 28;
 
 __device__ __forceinline__ uint32_t saddr(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
@@ -60,24 +63,19 @@ __device__ __forceinline__ void bar_init(uint64_t* bar, int count) {
 }
 __device__ __forceinline__ bool bar_try(uint64_t* bar, uint32_t parity) {
   uint32_t ok;
-  asm volatile("{\n.reg .pred p;\nmbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\nselp.u32 %0, 1, 0, p;\n}"
+  asm volatile("{\n.reg .pred p;\nmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\nselp.u32 %0, 1, 0, p;\n}"
                : "=r"(ok)
                : "r"(saddr(bar)), "r"(parity)
                : "memory");
   return ok;
 }
-__device__ __forceinline__ unsigned long long now_ns() {
-  unsigned long long t;
-  asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
-  return t;
-}
 // Waits for the phase of `parity`; false if its time ran out, or another wait of this CTA has given up.
 __device__ __forceinline__ bool bar_wait(uint64_t* bar, uint32_t parity, volatile int* dead) {
   if (bar_try(bar, parity)) return true;
-  const unsigned long long began = now_ns();
+  const long long began = clock64();
   for (int i = 0; i < kWaitTries; ++i) {
     if (bar_try(bar, parity)) return true;
-    if ((i & 31) == 31 && (*dead || now_ns() - began > kWaitNs)) break;
+    if ((i & 31) == 31 && (*dead || clock64() - began > kWaitCycles)) break;
   }
   *dead = 1;
   return false;
@@ -89,9 +87,11 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volati
 __device__ __forceinline__ void bar_expect(uint64_t* bar, uint32_t bytes) {
   asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(saddr(bar)), "r"(bytes) : "memory");
 }
-// One arrival at a barrier of any CTA of the cluster.
+// One arrival at a barrier of any CTA of the cluster.  (No more than the accumulators' emptiness goes from CTA to CTA by
+// barriers, which tcgen05's fences order: waits that acquire and arrivals that release at the cluster's scope cost a
+// fence each, 0.5 us and more.)
 __device__ __forceinline__ void bar_arrive_at(uint32_t addr) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
 }
 
 // A box of a tensor map at (x, y) into this CTA's shared memory, completing on a barrier of either CTA of the pair.
@@ -123,9 +123,9 @@ __device__ __forceinline__ uint32_t step_bytes(bool m_rows) { return m_rows ? 20
 
 // Instruction descriptor of kind::f16: fp32 sums (bits 4-5 = 1), both operands of one
 // 16-bit type (bits 7-9 and 10-12: 0 f16, 1 bf16), M rows (bit 15: A, bit 16: B), N / 8 at bit 17, M / 16 at bit 24.
-__device__ __forceinline__ uint32_t instruction(bool bf16, bool a_m_rows, bool b_m_rows) {
+__device__ __forceinline__ uint32_t instruction(bool bf16, bool a_m_rows, bool b_m_rows, int n) {
   return (1u << 4) | ((bf16 ? 1u : 0u) << 7) | ((bf16 ? 1u : 0u) << 10) | ((a_m_rows ? 1u : 0u) << 15) | ((b_m_rows ? 1u : 0u) << 16) |
-         ((uint32_t)(kTile >> 3) << 17) | ((uint32_t)(kTile >> 4) << 24);
+         ((uint32_t)(n >> 3) << 17) | ((uint32_t)(kTile >> 4) << 24);
 }
 // D += A B over 16 elements (D = A B where acc is 0), both CTAs' shared memory and tensor memory.
 __device__ __forceinline__ void multiply(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
@@ -153,20 +153,16 @@ __device__ __forceinline__ void tmem_free(uint32_t t) {
   asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(t));
 }
 
-// 32 columns of a warp's 32 lanes.
-__device__ __forceinline__ void tmem_load32(uint32_t t, float (&v)[32]) {
+// 16 columns of a warp's 32 lanes; there after tmem_wait().
+__device__ __forceinline__ void tmem_load16(uint32_t t, float* v) {
   uint32_t* r = reinterpret_cast<uint32_t*>(v);
   asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
-      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
       : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]),
-        "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]),
-        "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]),
-        "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
       : "r"(t));
-  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 }
+__device__ __forceinline__ void tmem_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 
 // ---- products ---------------------------------------------------------------------
 
@@ -176,27 +172,30 @@ constexpr long long kSlotFloats = (long long)kTile * kTile;
 // What a product's kernel is told.  D[m, n] = sum_k A[m, k] B[n, k].
 struct Product {
   CUtensorMap a, b;
+  CUtensorMap a_few;         // A with K rows: in boxes of kFew rows, for a tile that has fewer rows than a CTA's part
   CUtensorMap store;         // GRAD: the gradients' matrix, in boxes of 64 x 32
   int m, n, k;               // extents in elements
+  int bn;                    // columns of a tile (see columns_of)
   const int* live;           // device: takes the place of m (live_is 1) or k (2); or NULL
   int live_is;
   int a_m_rows, b_m_rows;    // how the operands lie
   int b_y0;                  // first row of B's map
   int bf16;
   int m_fast;                // order of the tiles: neighbours share B (else A)
+  int chunk;                 // steps that the tensor cores sum by themselves, 0: all (see k_product)
   int* error;                // device: set to 1 by a wait that gave up
   // OUT: out = [out +] scale * D
   void* out;
   long long ldo;
   int dtype, accumulate;
+  int vec;                   // rows of out begin at multiples of 4 elements' size
   const float* scale;        // device, or NULL: 1
   float* slots;              // partial tiles, two of kSlotFloats per pair; NULL: no tile is split
   // LSE and GRAD: rows are tokens, columns the vocabulary from column0 on
   int column0, vocab;        // columns in all
   const int* target;         // per row
-  float2* part;              // LSE: largest logit and sum of exp(z - it), for every 128 columns: [part][row]
+  float2* part;              // LSE: largest logit but the target's and sum of exp(z - it), for every 256 columns: [part][row]
   long long part_rows;       // rows between parts
-  float* at_target;          // LSE: the target's logit
   const float* lse;          // GRAD
   const float* factor;       // GRAD: multiplies a row's gradient
 };
@@ -207,10 +206,10 @@ struct Schedule {
   int mt, nt, kb, tiles, whole, workers;
   long long steps;  // of the tiles that are cut
 };
-__host__ __device__ inline Schedule schedule_of(int m, int n, int k, int pairs, bool split) {
+__host__ __device__ inline Schedule schedule_of(int m, int n, int bn, int k, int pairs, bool split) {
   Schedule s;
   s.mt = (int)ops::units(m, kTile);
-  s.nt = (int)ops::units(n, kTile);
+  s.nt = (int)ops::units(n, bn);
   s.kb = (int)ops::units(k, kStep);
   s.tiles = s.mt * s.nt;
   s.whole = s.tiles;
@@ -228,6 +227,13 @@ __host__ __device__ inline Schedule schedule_of(int m, int n, int k, int pairs, 
 }
 __host__ __device__ inline long long first_step(const Schedule& s, int worker) { return worker * s.steps / s.workers; }
 
+// Columns of the tiles of n columns: as few tiles as 256 columns allow, of one width, a multiple of 16.  (1600 columns are
+// 7 tiles of 240, not 6 of 256 and one of 64 that costs as much as they.)
+__host__ __device__ inline int columns_of(int n) {
+  const int tiles = (int)ops::units(n < 1 ? 1 : n, kTile);
+  return (int)ops::units(ops::units(n < 1 ? 1 : n, tiles), 16) * 16;
+}
+
 enum Epilogue { kLse = 0, kGrad = 1, kOut = 2 };
 
 // ---- host side ------------------------------------------------------------------
@@ -240,8 +246,10 @@ inline int box_rows(bool m_rows) { return m_rows ? kStep : kHalf; }
 
 // Pairs of CTAs that a device holds at once.
 cudaError_t pairs_of(int device, int* pairs);
+// Columns whose logits one entry of `part` stands for.
+constexpr int kPartCols = kTile;
 // Enqueues a product, and for split tiles the sum of their parts.
-cudaError_t enqueue(Epilogue kind, const Product& p, int device, int pairs, cudaStream_t st);
+cudaError_t enqueue(Epilogue kind, Product p, int device, int pairs, cudaStream_t st);
 // Rows of 16-bit elements of any stride and alignment into rows `to` elements apart.
 cudaError_t align_rows(const void* src, long long stride, long long rows, long long cols, void* dst, long long to, cudaStream_t st);
 // Reads and clears a handle's error word; synchronises the stream.
