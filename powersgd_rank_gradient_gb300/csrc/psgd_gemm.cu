@@ -26,17 +26,18 @@ struct Shared {
 
 // One run of a pair: steps [k0, k1) of tile (tm, tn); slot < 0: the whole tile.
 struct Run {
-  int tm, tn, k0, k1, slot;
+  int tm, tn, k0, k1, slot, width;
 };
 struct Walk {
   Schedule s;
-  int pairs, pair, m_fast, next;
+  int pairs, pair, m_fast, next, n, bn;
   long long at, end;
   int piece;
   __device__ Walk(const Product& p, int m, int k, int pairs_, int pair_)
-      : s(schedule_of(m, p.n, p.bn, k, pairs_, p.slots != nullptr)), pairs(pairs_), pair(pair_), m_fast(p.m_fast), next(pair_), piece(0) {
-    at = pair < s.workers ? first_step(s, pair) : 0;
-    end = pair < s.workers ? first_step(s, pair + 1) : 0;
+      : s(schedule_of(m, p.n, p.bn, k, pairs_, p.slots != nullptr)), pairs(pairs_), pair(pair_), m_fast(p.m_fast), next(pair_), n(p.n), bn(p.bn), piece(0) {
+    const bool works = pair < s.workers;
+    at = works && !s.cuts ? first_step(s, pair) : 0;
+    end = works ? (s.cuts ? 1 : first_step(s, pair + 1)) : 0;
   }
   __device__ bool take(Run& r) {
     int tile;
@@ -46,6 +47,12 @@ struct Walk {
       r.k0 = 0;
       r.k1 = s.kb;
       r.slot = -1;
+    } else if (s.cuts && at < end) {
+      tile = s.whole + pair % s.rest;
+      r.k0 = first_of_cut(s, pair / s.rest);
+      r.k1 = first_of_cut(s, pair / s.rest + 1);
+      r.slot = 2 * pair;
+      at = end;
     } else if (at < end) {
       const int i = (int)(at / s.kb);
       tile = s.whole + i;
@@ -59,6 +66,7 @@ struct Walk {
     }
     r.tm = m_fast ? tile % s.mt : tile / s.nt;
     r.tn = m_fast ? tile / s.mt : tile % s.nt;
+    r.width = width_of(n, bn, r.tn);
     return true;
   }
 };
@@ -183,14 +191,17 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) k_produ
       int stage = 0;
       uint32_t phase = 0;
       while (walk.take(run)) {
-        const int row = run.tm * kTile + (int)rank * kHalf, col = run.tn * p.bn + (int)rank * (p.bn / 2);
+        const int row = run.tm * kTile + (int)rank * kHalf, col = run.tn * p.bn + (int)rank * (run.width / 2);
         // Of A with K rows, no more than the rows that there are: what bounds products of few rows is the lines of 128
         // bytes that an SM can have under way (some 350).  What lies in the others' place gives rows that nobody takes.
         const int rows_here = min(kHalf, m - row), rows_0 = min(kHalf, m - run.tm * kTile), rows_1 = min(kHalf, m - run.tm * kTile - kHalf);
         const bool few = !p.a_m_rows && rows_1 < kHalf;
         const int boxes = (max(rows_here, 0) + kFew - 1) / kFew;
-        const uint32_t bytes =
-            few ? 2 * kOperand + ((rows_0 + kFew - 1) / kFew + (max(rows_1, 0) + kFew - 1) / kFew) * (kFew * kStep * 2) : 2 * kStageBytes;
+        // of B with M rows, 64 columns more or not (with K rows, a box has 128)
+        const bool wide = !p.b_m_rows || run.width > 128;
+        const uint32_t bytes = (wide ? 2 : 1) * kOperand + (few ? ((rows_0 + kFew - 1) / kFew + (max(rows_1, 0) + kFew - 1) / kFew) *
+                                                                     (kFew * kStep * 2)
+                                                               : 2 * kOperand);
         for (int kb = run.k0; kb < run.k1; ++kb) {
           if (!bar_wait(&sh.empty[stage], phase ^ 1, dead)) break;
           const uint32_t a = saddr(stages + stage * kStageBytes), b = a + kOperand, bar = at_rank(saddr(&sh.full[stage]), 0);
@@ -206,7 +217,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) k_produ
           }
           if (p.b_m_rows) {
             load_box(b, &p.b, col, p.b_y0 + x, bar);
-            load_box(b + kOperand / 2, &p.b, col + 64, p.b_y0 + x, bar);
+            if (wide) load_box(b + kOperand / 2, &p.b, col + 64, p.b_y0 + x, bar);
           } else {
             load_box(b, &p.b, x, p.b_y0 + col, bar);
           }
@@ -220,11 +231,11 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) k_produ
     }
   } else if (warp == kEpilogueWarps + 1) {
     if (rank == 0 && lane == 0) {
-      const uint32_t idesc = instruction(p.bf16, p.a_m_rows, p.b_m_rows, p.bn);
       const uint32_t a_step = step_bytes(p.a_m_rows) >> 4, b_step = step_bytes(p.b_m_rows) >> 4;
       int stage = 0, buf = 0;
       uint32_t phase = 0, turn = 0;
       while (!*dead && walk.take(run)) {
+        const uint32_t idesc = instruction(p.bf16, p.a_m_rows, p.b_m_rows, run.width);
         for (int kb = run.k0; kb < run.k1;) {
           if (!bar_wait(&sh.drained[buf], turn ^ 1, dead)) break;
           fence_after();
@@ -296,7 +307,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) k_produ
       }
       if (KIND != kLse && !alive) break;  // (kLse: on to the barriers that the other warps are at)
       if constexpr (KIND == kOut) {
-        if (group * kCols >= p.bn) continue;
+        if (group * kCols >= run.width) continue;
         if (run.slot >= 0) {
           // groups of four columns, row by row: neighbouring lanes write neighbouring 16 bytes
           float4* to = reinterpret_cast<float4*>(p.slots + run.slot * kSlotFloats) + (long long)rank * kHalf * kTile / 4 +
@@ -304,7 +315,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) k_produ
 #pragma unroll
           for (int i = 0; i < kCols / 4; ++i) to[i * kHalf] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
         } else {
-          const int end = min(p.n, run.tn * p.bn + p.bn);
+          const int end = min(p.n, run.tn * p.bn + run.width);
           put_block<T>(v, st, lane, p, row0, min(32, m - row0), col0, min(32, end - col0), scale);
           put_block<T>(v + 32, st, lane, p, row0, min(32, m - row0), col0 + 32, min(32, end - col0 - 32), scale);
         }
@@ -393,9 +404,11 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) k_produ
   if (warp == kEpilogueWarps + 1) tmem_free(tmem);
 }
 
-// The sum of a split tile's parts, in the order of the summed dimension.  A CTA takes 32 rows of 64 columns.
-template <typename T> __global__ void __launch_bounds__(64) k_join(const __grid_constant__ Product p, int pairs) {
-  __shared__ float4 st[2][32 * 8];
+// The sum of a split tile's parts, in the order of the summed dimension.  A CTA takes 32 rows of 64 columns: two warps
+// side by side, in kJoin rows of warps that share the parts.
+constexpr int kJoin = 4;
+template <typename T> __global__ void __launch_bounds__(64 * kJoin) k_join(const __grid_constant__ Product p, int pairs) {
+  __shared__ float4 st[kJoin][2][32 * 8];
   after_previous();
   next_may_launch();
   const int live = p.live ? *p.live : 0;
@@ -405,21 +418,35 @@ template <typename T> __global__ void __launch_bounds__(64) k_join(const __grid_
   if (i >= s.tiles - s.whole) return;
   const int tile = s.whole + i;
   const int tm = p.m_fast ? tile % s.mt : tile / s.nt, tn = p.m_fast ? tile / s.mt : tile % s.nt;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = threadIdx.x >> 5 & 1, turn = threadIdx.x >> 6, lane = threadIdx.x & 31;
   const int rows32 = blockIdx.x >> 2, cols64 = blockIdx.x & 3;  // of 8 and of 4
   const int row0 = tm * kTile + rows32 * 32, col0 = tn * p.bn + cols64 * 64 + warp * 32;
   const int end = min(p.n, tn * p.bn + p.bn);
-  if (row0 >= m || col0 >= end) return;
-  const long long lo = (long long)i * s.kb, hi = lo + s.kb;
-  int w = (int)(lo * s.workers / s.steps);
-  while (w > 0 && first_step(s, w) > lo) --w;
-  while (first_step(s, w + 1) <= lo) ++w;
-  if (first_step(s, w) <= lo && first_step(s, w + 1) >= hi) return;  // one pair did all of it
+  if (cols64 * 64 >= p.bn || row0 >= m || tn * p.bn + cols64 * 64 >= end) return;
+  // the parts: `parts` of them, part j in slot first + j * step, but for the first one's
+  int parts, first, step, slot0;
+  if (s.cuts) {
+    parts = s.cuts;
+    first = slot0 = 2 * i;
+    step = 2 * s.rest;
+  } else {
+    const long long lo = (long long)i * s.kb, hi = lo + s.kb;
+    int w = (int)(lo * s.workers / s.steps);
+    while (w > 0 && first_step(s, w) > lo) --w;
+    while (first_step(s, w + 1) <= lo) ++w;
+    int last = w;
+    while (last + 1 < s.workers && first_step(s, last + 1) < hi) ++last;
+    parts = last - w + 1;
+    if (parts == 1) return;  // one pair did all of it
+    first = 2 * w;
+    slot0 = first + (first_step(s, w) < lo ? 1 : 0);
+    step = 2;
+  }
   float v[32];
 #pragma unroll
   for (int c = 0; c < 32; ++c) v[c] = 0.f;
-  for (; w < s.workers && first_step(s, w) < hi; ++w) {
-    const int slot = 2 * w + (first_step(s, w) < lo ? 1 : 0);
+  for (int j = turn; j < parts; j += kJoin) {
+    const int slot = j == 0 ? slot0 : first + j * step;
     const float4* from = reinterpret_cast<const float4*>(p.slots + slot * kSlotFloats) + (long long)(rows32 >> 2) * kHalf * kTile / 4 +
                          (long long)(cols64 * 16 + warp * 8) * kHalf + (rows32 & 3) * 32 + lane;
 #pragma unroll
@@ -431,7 +458,23 @@ template <typename T> __global__ void __launch_bounds__(64) k_join(const __grid_
       v[4 * c + 3] += x.w;
     }
   }
-  put_block<T>(v, st[warp], lane, p, row0, min(32, m - row0), col0, min(32, end - col0), p.scale ? *p.scale : 1.f);
+  if (turn > 0) {
+#pragma unroll
+    for (int c = 0; c < 8; ++c) st[turn][warp][c * 32 + lane] = make_float4(v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]);
+  }
+  __syncthreads();
+  if (turn > 0) return;
+#pragma unroll
+  for (int t = 1; t < kJoin; ++t)
+#pragma unroll
+    for (int c = 0; c < 8; ++c) {
+      const float4 x = st[t][warp][c * 32 + lane];
+      v[4 * c] += x.x;
+      v[4 * c + 1] += x.y;
+      v[4 * c + 2] += x.z;
+      v[4 * c + 3] += x.w;
+    }
+  put_block<T>(v, st[0][warp], lane, p, row0, min(32, m - row0), col0, min(32, end - col0), p.scale ? *p.scale : 1.f);
 }
 
 using Encode = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
@@ -496,9 +539,29 @@ cudaError_t pairs_of(int device, int* pairs) {
   return e;
 }
 
+// Columns of an OUT product's tiles.  A step costs about as long as its lines take into an SM, 0.33 us for 256 + 256
+// rows and columns, and what is drained after a pair's last step, 2.5 us for 256 columns, is waited for.  So where the tiles
+// do not occupy the pairs (and cannot be cut along k), narrower ones end earlier: 1024 x 1024 from 509 rows, 16 tiles of 256
+// columns 12.2 us, 64 of 64 columns 10.0.
+static int columns_of(const Product& p, int pairs) {
+  int best = kTile;
+  double least = 1e30;
+  for (int bn = kTile; bn >= 64; bn /= 2) {
+    const Schedule s = schedule_of(p.m, p.n, bn, p.k, pairs, p.slots != nullptr);
+    const double step = 0.33 * (kTile + bn) / (2 * kTile), steps = (double)s.kb;
+    double us = (double)(s.whole / pairs + (s.whole % pairs ? 1 : 0)) * steps * step + 2.5 * bn / kTile;
+    if (s.workers) us += (double)s.steps / s.workers * step + 4.0;
+    if (us < 0.95 * least) {
+      least = us;
+      best = bn;
+    }
+  }
+  return best;
+}
+
 cudaError_t enqueue(Epilogue kind, Product p, int device, int pairs, cudaStream_t st) {
   // (the others' columns go by 128)
-  p.bn = kind == kOut ? columns_of(p.n) : kTile;
+  p.bn = kind == kOut ? columns_of(p, pairs) : kTile;
   if (kind == kOut) {
     const int size = 4 * ops::dtype_size(p.dtype);
     p.vec = (uintptr_t)p.out % size == 0 && (p.ldo % 4 == 0 || p.m == 1);
@@ -517,7 +580,7 @@ cudaError_t enqueue(Epilogue kind, Product p, int device, int pairs, cudaStream_
   if (!p.live && schedule_of(p.m, p.n, p.bn, p.k, pairs, true).workers == 0) return e;
   const dim3 parts(32, (unsigned)std::min<long long>(tiles, pairs - 1));
   return by_type(p.dtype, [&](auto* t) {
-    return ops::launch_early(k_join<std::remove_pointer_t<decltype(t)>>, parts, 64, 0, 1, st, p, pairs);
+    return ops::launch_early(k_join<std::remove_pointer_t<decltype(t)>>, parts, 64 * kJoin, 0, 1, st, p, pairs);
   });
 }
 

@@ -64,57 +64,56 @@ __device__ __forceinline__ long long target_of(const Tokens& t, int i) {
   return t.bits == 64 ? __ldg((const long long*)t.targets + i) : (long long)__ldg((const int*)t.targets + i);
 }
 __device__ __forceinline__ float weight_of(const Tokens& t, int i) { return t.weights ? __ldg(t.weights + i) : 1.f; }
-__device__ __forceinline__ bool counts(const Tokens& t, int i) {
-  const long long y = target_of(t, i);
-  return y >= 0 && y < t.vocab && weight_of(t, i) != 0.f;
-}
-
 // Which tokens count, in their order, and their weights: w = r 2^e s with s the largest weight's significand, so that
 // weights that are all the same have r = 1 and lose nothing to a rounding.  One CTA, eight tokens a thread at a time.
 constexpr int kPlanItems = 8;
+struct Items {  // eight tokens' targets (-1 for a token that does not count) and weights
+  int target[kPlanItems];
+  float weight[kPlanItems];
+  __device__ __forceinline__ Items(const Tokens& t, int first) {
+    long long y[kPlanItems];
+#pragma unroll
+    for (int k = 0; k < kPlanItems; ++k) {
+      const bool in = first + k < t.tokens;
+      y[k] = in ? target_of(t, first + k) : -1;
+      weight[k] = in ? weight_of(t, first + k) : 0.f;
+    }
+#pragma unroll
+    for (int k = 0; k < kPlanItems; ++k) target[k] = y[k] >= 0 && y[k] < t.vocab && weight[k] != 0.f ? (int)y[k] : -1;
+  }
+};
 __device__ void plan(const Tokens& t, int* place, int* row, int* target, float* factor, int* exponent, int* count, float* scale,
                      float grad_scale, int shift) {
   __shared__ int sums[32];
   __shared__ float most[32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   constexpr int kTurn = 1024 * kPlanItems;
-  // tokens that count among this thread's from `first` on, as bits
-  const auto flags = [&](int first) {
-    unsigned bits = 0;
+  // the largest weight
+  Items mine(t, (int)threadIdx.x * kPlanItems);
+  float top = 0.f;
+  const auto look = [&](const Items& x) {
 #pragma unroll
     for (int k = 0; k < kPlanItems; ++k)
-      if (first + k < t.tokens && counts(t, first + k)) bits |= 1u << k;
-    return bits;
+      if (x.target[k] >= 0 && isfinite(x.weight[k])) top = fmaxf(top, fabsf(x.weight[k]));
   };
-  unsigned mine = 0;
-  float top = 0.f;
-  if (t.weights) {
-    for (int base = 0; base < t.tokens; base += kTurn) {
-      const int first = base + (int)threadIdx.x * kPlanItems;
-      mine = flags(first);
-#pragma unroll
-      for (int k = 0; k < kPlanItems; ++k)
-        if (mine >> k & 1) {
-          const float w = fabsf(weight_of(t, first + k));
-          if (isfinite(w)) top = fmaxf(top, w);
-        }
-    }
-    top = warp_max(top);
-    if (lane == 0) most[warp] = top;
-    __syncthreads();
-    top = warp_max(most[lane]);
-  } else {
-    mine = flags((int)threadIdx.x * kPlanItems);
-    top = 1.f;
-  }
+  look(mine);
+  if (t.weights)
+    for (int base = kTurn; base < t.tokens; base += kTurn) look(Items(t, base + (int)threadIdx.x * kPlanItems));
+  top = warp_max(top);
+  if (lane == 0) most[warp] = top;
+  __syncthreads();
+  top = warp_max(most[lane]);
   if (top == 0.f) top = 1.f;  // no token counts, or none whose weight is finite
   const int e_top = ilogbf(top);
   const float s = scalbnf(top, -e_top);
   int before = 0;
   for (int base = 0; base < t.tokens; base += kTurn) {
     const int first = base + (int)threadIdx.x * kPlanItems;
-    const unsigned bits = t.tokens <= kTurn ? mine : flags(first);
-    int n = __popc(bits);
+    if (base) mine = Items(t, first);
+    int n = 0;
+#pragma unroll
+    for (int k = 0; k < kPlanItems; ++k) n += mine.target[k] >= 0;
+    const int own = n;
 #pragma unroll
     for (int o = 1; o < 32; o *= 2) {
       const int up = __shfl_up_sync(0xffffffffu, n, o);
@@ -128,19 +127,21 @@ __device__ void plan(const Tokens& t, int* place, int* row, int* target, float* 
       const int up = __shfl_up_sync(0xffffffffu, all, o);
       if (lane >= o) all += up;
     }
-    int at = before + n - __popc(bits) + (warp ? __shfl_sync(0xffffffffu, all, warp - 1) : 0);
+    int at = before + n - own + (warp ? __shfl_sync(0xffffffffu, all, warp - 1) : 0);
     before += __shfl_sync(0xffffffffu, all, 31);
 #pragma unroll
     for (int k = 0; k < kPlanItems; ++k) {
-      const int i = first + k;
-      if (i >= t.tokens) break;
-      const bool in = bits >> k & 1;
-      place[i] = in ? at : -1;
+      if (first + k >= t.tokens) break;
+      const bool in = mine.target[k] >= 0;
+      place[first + k] = in ? at : -1;
       if (!in) continue;
-      const float w = weight_of(t, i);
+      const float w = mine.weight[k];
       int e = 0;
       float r = w;
-      if (isfinite(w)) {
+      if (w == top) {  // (the usual case: all weights are the same)
+        e = e_top;
+        r = 1.f;
+      } else if (isfinite(w)) {
         e = ilogbf(w);
         r = scalbnf(w, -e) / s;
         if (fabsf(r) < 1.f) {
@@ -148,8 +149,8 @@ __device__ void plan(const Tokens& t, int* place, int* row, int* target, float* 
           --e;
         }
       }
-      row[at] = i;
-      target[at] = (int)target_of(t, i);
+      row[at] = first + k;
+      target[at] = mine.target[k];
       factor[at] = scalbnf(r, shift);
       exponent[at] = e;
       ++at;
@@ -228,6 +229,7 @@ __global__ void __launch_bounds__(1024) k_plan_gather(Tokens t, int* place, int*
 template <typename T> __device__ __forceinline__ float warp_dot(const T* a, const T* b, int dim, bool vec) {
   const int lane = threadIdx.x & 31;
   float sum = 0.f;
+#pragma unroll 4
   for (int c = lane * 8; c < dim; c += 256) {
     F2 x[4], y[4], s = f2(0.f, 0.f);
     if (vec) {

@@ -63,9 +63,10 @@ __device__ __forceinline__ void bar_init(uint64_t* bar, int count) {
 }
 __device__ __forceinline__ bool bar_try(uint64_t* bar, uint32_t parity) {
   uint32_t ok;
-  asm volatile("{\n.reg .pred p;\nmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\nselp.u32 %0, 1, 0, p;\n}"
+  // (it may sleep 20 us: sixteen warps that ask all the time cost the tensor cores 5 % of their clock)
+  asm volatile("{\n.reg .pred p;\nmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\nselp.u32 %0, 1, 0, p;\n}"
                : "=r"(ok)
-               : "r"(saddr(bar)), "r"(parity)
+               : "r"(saddr(bar)), "r"(parity), "r"(20000)
                : "memory");
   return ok;
 }
@@ -175,7 +176,7 @@ struct Product {
   CUtensorMap a_few;         // A with K rows: in boxes of kFew rows, for a tile that has fewer rows than a CTA's part
   CUtensorMap store;         // GRAD: the gradients' matrix, in boxes of 64 x 32
   int m, n, k;               // extents in elements
-  int bn;                    // columns of a tile (see columns_of)
+  int bn;                    // columns of a tile but the last (see width_of)
   const int* live;           // device: takes the place of m (live_is 1) or k (2); or NULL
   int live_is;
   int a_m_rows, b_m_rows;    // how the operands lie
@@ -201,9 +202,11 @@ struct Product {
 };
 
 // How a product's tiles go to pairs of CTAs: whole tiles in turns of one for each pair; the tiles of a last turn that
-// would leave pairs idle are cut along k into equal runs of steps, one for each of `workers` pairs.
+// would leave pairs idle are cut along k.  Where that occupies most pairs, each into `cuts` equal pieces, the same pieces of all
+// tiles at the same time, so that they share what they read (8 tiles of 477 steps: 33 us, 25 so); else into equal runs of
+// the steps of all of them, one for each of `workers` pairs.
 struct Schedule {
-  int mt, nt, kb, tiles, whole, workers;
+  int mt, nt, kb, tiles, whole, rest, workers, cuts;
   long long steps;  // of the tiles that are cut
 };
 __host__ __device__ inline Schedule schedule_of(int m, int n, int bn, int k, int pairs, bool split) {
@@ -213,25 +216,34 @@ __host__ __device__ inline Schedule schedule_of(int m, int n, int bn, int k, int
   s.kb = (int)ops::units(k, kStep);
   s.tiles = s.mt * s.nt;
   s.whole = s.tiles;
-  s.workers = 0;
+  s.workers = s.cuts = 0;
   s.steps = 0;
-  const int rest = s.tiles % pairs;
-  if (!split || rest == 0 || s.kb < 2 * kMinSplit) return s;
-  const long long steps = (long long)rest * s.kb;
-  const long long workers = steps / kMinSplit < pairs ? steps / kMinSplit : pairs;
-  if (workers <= rest) return s;
-  s.whole = s.tiles - rest;
-  s.workers = (int)workers;
+  s.rest = s.tiles % pairs;
+  if (!split || s.rest == 0 || s.kb < 2 * kMinSplit) return s;
+  const int most = s.kb / kMinSplit, fit = pairs / s.rest, cuts = fit < most ? fit : most;
+  const long long steps = (long long)s.rest * s.kb;
+  if (cuts >= 2 && (cuts == most || cuts * s.rest * 8 >= pairs * 7)) {
+    s.cuts = cuts;
+    s.workers = cuts * s.rest;
+  } else {
+    const long long workers = steps / kMinSplit < pairs ? steps / kMinSplit : pairs;
+    if (workers <= s.rest) return s;
+    s.workers = (int)workers;
+  }
+  s.whole = s.tiles - s.rest;
   s.steps = steps;
   return s;
 }
+// Equal runs: the first step of a worker's.  Equal pieces: of a cut's.
 __host__ __device__ inline long long first_step(const Schedule& s, int worker) { return worker * s.steps / s.workers; }
+__host__ __device__ inline int first_of_cut(const Schedule& s, int cut) { return (int)((long long)cut * s.kb / s.cuts); }
 
-// Columns of the tiles of n columns: as few tiles as 256 columns allow, of one width, a multiple of 16.  (1600 columns are
-// 7 tiles of 240, not 6 of 256 and one of 64 that costs as much as they.)
-__host__ __device__ inline int columns_of(int n) {
-  const int tiles = (int)ops::units(n < 1 ? 1 : n, kTile);
-  return (int)ops::units(ops::units(n < 1 ? 1 : n, tiles), 16) * 16;
+// Columns of tile tn of n columns: `bn`, or a multiple of 32 that holds what is left.  (A tile begins at a multiple of 64
+// columns of a row, so that its boxes' rows are whole lines of 128 bytes: seven tiles of 240 for 1600 columns, 0.40 us a
+// step, cost more than six of 256 and one of 64, 0.36.)
+__host__ __device__ inline int width_of(int n, int bn, int tn) {
+  const int left = n - tn * bn;
+  return left >= bn ? bn : (left + 31) / 32 * 32;
 }
 
 enum Epilogue { kLse = 0, kGrad = 1, kOut = 2 };
