@@ -19,57 +19,50 @@ using ops::after_previous;
 using ops::next_may_launch;
 
 struct Shared {
-  uint64_t full[kStages], empty[kStages], done[2], drained[2];
+  uint64_t full[kMostStages], empty[kMostStages], done[2], drained[2];
   uint32_t tmem;
   volatile int dead;
+  int m;
+  Schedule schedule;
 };
 
 // One run of a pair: steps [k0, k1) of tile (tm, tn); slot < 0: the whole tile.
 struct Run {
   int tm, tn, k0, k1, slot, width;
 };
-struct Walk {
-  Schedule s;
-  int pairs, pair, m_fast, next, n, bn;
-  long long at, end;
-  int piece;
-  __device__ Walk(const Product& p, int m, int k, int pairs_, int pair_)
-      : s(schedule_of(m, p.n, p.bn, k, pairs_, p.slots != nullptr)), pairs(pairs_), pair(pair_), m_fast(p.m_fast), next(pair_), n(p.n), bn(p.bn), piece(0) {
-    const bool works = pair < s.workers;
-    at = works && !s.cuts ? first_step(s, pair) : 0;
-    end = works ? (s.cuts ? 1 : first_step(s, pair + 1)) : 0;
-  }
-  __device__ bool take(Run& r) {
-    int tile;
-    if (next < s.whole) {
-      tile = next;
-      next += pairs;
-      r.k0 = 0;
-      r.k1 = s.kb;
-      r.slot = -1;
-    } else if (s.cuts && at < end) {
+// A pair's i-th run; false behind the last.  The schedule is in shared memory: in the registers of the warps that drain
+// it pushed some of their 64 sums out into local memory, which cost up to 10 us a tile.
+__device__ __forceinline__ bool run_of(const Product& p, const Schedule& s, int pairs, int pair, int i, Run& r) {
+  int tile = pair + i * pairs;
+  r.k0 = 0;
+  r.k1 = s.kb;
+  r.slot = -1;
+  if (tile >= s.whole) {
+    if (pair >= s.workers) return false;
+    const int j = i - (s.whole > pair ? (s.whole - pair + pairs - 1) / pairs : 0);
+    if (s.cuts) {
+      if (j > 0) return false;
       tile = s.whole + pair % s.rest;
       r.k0 = first_of_cut(s, pair / s.rest);
       r.k1 = first_of_cut(s, pair / s.rest + 1);
       r.slot = 2 * pair;
-      at = end;
-    } else if (at < end) {
-      const int i = (int)(at / s.kb);
-      tile = s.whole + i;
-      r.k0 = (int)(at - (long long)i * s.kb);
-      r.k1 = (int)min((long long)s.kb, r.k0 + (end - at));
-      r.slot = r.k0 == 0 && r.k1 == s.kb ? -1 : 2 * pair + piece;
-      at += r.k1 - r.k0;
-      ++piece;
     } else {
-      return false;
+      // a run of steps reaches into two tiles at most
+      const long long from = first_step(s, pair), to = first_step(s, pair + 1);
+      const int first = (int)(from / s.kb);
+      const long long border = (long long)(first + 1) * s.kb;
+      if (j > 1 || (j == 1 && to <= border)) return false;
+      tile = s.whole + first + j;
+      r.k0 = j ? 0 : (int)(from - (border - s.kb));
+      r.k1 = (int)((j ? to - border : (to < border ? to : border) - (border - s.kb)));
+      r.slot = r.k0 == 0 && r.k1 == s.kb ? -1 : 2 * pair + j;
     }
-    r.tm = m_fast ? tile % s.mt : tile / s.nt;
-    r.tn = m_fast ? tile / s.mt : tile % s.nt;
-    r.width = width_of(n, bn, r.tn);
-    return true;
   }
-};
+  r.tm = p.m_fast ? tile % s.mt : tile / s.nt;
+  r.tn = p.m_fast ? tile / s.mt : tile % s.nt;
+  r.width = width_of(p.n, p.bn, r.tn);
+  return true;
+}
 
 __device__ __forceinline__ float exp_of(float x) {
   // 2 ulp of ex2 and the product's rounding, |x| 2^-24 of the result at most
@@ -102,33 +95,30 @@ __device__ __forceinline__ void put_rows(const float4* st, int lane, T* to, long
     const int r = lane >> 3, c = lane & 7;
     T* at = to + r * ldo + 4 * c;
 #pragma unroll 1
-    for (int half = 0; half < 2; ++half) {
-      float4 old[4];
+    for (int r0 = r; r0 < rows; r0 += 8, at += 8 * ldo) {
+      const bool second = r0 + 4 < rows;
+      float4 y0 = st[r0 * 8 + (c ^ (r0 & 7))], y1 = st[(r0 + 4) * 8 + (c ^ ((r0 + 4) & 7))];
       if (add) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          if (half * 16 + 4 * i + r < rows) old[i] = load4(at + (half * 16 + 4 * i) * ldo);
+        const float4 x0 = load4(at), x1 = second ? load4(at + 4 * ldo) : make_float4(0.f, 0.f, 0.f, 0.f);
+        y0 = plus(x0, y0);
+        y1 = plus(x1, y1);
       }
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int row = half * 16 + 4 * i + r;
-        const float4 y = st[row * 8 + (c ^ (row & 7))];
-        if (row < rows) store4(at + (half * 16 + 4 * i) * ldo, add ? plus(old[i], y) : y);
-      }
+      store4(at, y0);
+      if (second) store4(at + 4 * ldo, y1);
     }
   } else if (lane < cols) {
     const float* s = reinterpret_cast<const float*>(st);
     T* at = to + lane;
 #pragma unroll 1
-    for (int r0 = 0; r0 < rows; r0 += 8, at += 8 * ldo) {
-      float old[8], y[8];
+    for (int r0 = 0; r0 < rows; r0 += 4, at += 4 * ldo) {
+      float old[4], y[4];
 #pragma unroll
-      for (int r = 0; r < 8; ++r) {
+      for (int r = 0; r < 4; ++r) {
         old[r] = add && r0 + r < rows ? ops::to_f(at[r * ldo]) : 0.f;
-        y[r] = s[(r0 + r) * 32 + (((lane >> 2) ^ (r & 7)) << 2 | (lane & 3))];  // (r0 is a multiple of 8)
+        y[r] = s[(r0 + r) * 32 + (((lane >> 2) ^ ((r0 + r) & 7)) << 2 | (lane & 3))];
       }
 #pragma unroll
-      for (int r = 0; r < 8; ++r)
+      for (int r = 0; r < 4; ++r)
         if (r0 + r < rows) at[r * ldo] = ops::from_f<T>(add ? old[r] + y[r] : y[r]);
     }
   }
@@ -158,7 +148,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) k_produ
   unsigned char* stages = raw + ((1024 - (saddr(raw) & 1023)) & 1023);
   unsigned char* staging = stages + kStages * kStageBytes;
   if (threadIdx.x == 0) {
-    for (int i = 0; i < kStages; ++i) {
+    for (int i = 0; i < kMostStages; ++i) {
       bar_init(&sh.full[i], 1);
       bar_init(&sh.empty[i], 1);
     }
@@ -180,9 +170,15 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) k_produ
   const uint32_t tmem = sh.tmem;
   cluster_sync();
   after_previous();
-  const int live = p.live ? *p.live : 0;
-  const int m = p.live_is == 1 ? live : p.m, k = p.live_is == 2 ? live : p.k;
-  Walk walk(p, m, k, pairs, pair);
+  next_may_launch();
+  if (threadIdx.x == 0) {
+    const int live = p.live ? *p.live : 0;
+    sh.m = p.live_is == 1 ? live : p.m;
+    sh.schedule = schedule_of(sh.m, p.n, p.bn, p.live_is == 2 ? live : p.k, pairs, p.slots != nullptr);
+  }
+  __syncthreads();
+  const int m = sh.m;
+  const Schedule& plan = sh.schedule;
   Run run;
   volatile int* dead = &sh.dead;
 
@@ -190,21 +186,21 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) k_produ
     if (lane == 0) {
       int stage = 0;
       uint32_t phase = 0;
-      while (walk.take(run)) {
+      for (int i = 0; run_of(p, plan, pairs, pair, i, run); ++i) {
         const int row = run.tm * kTile + (int)rank * kHalf, col = run.tn * p.bn + (int)rank * (run.width / 2);
         // Of A with K rows, no more than the rows that there are: what bounds products of few rows is the lines of 128
         // bytes that an SM can have under way (some 350).  What lies in the others' place gives rows that nobody takes.
         const int rows_here = min(kHalf, m - row), rows_0 = min(kHalf, m - run.tm * kTile), rows_1 = min(kHalf, m - run.tm * kTile - kHalf);
         const bool few = !p.a_m_rows && rows_1 < kHalf;
         const int boxes = (max(rows_here, 0) + kFew - 1) / kFew;
-        // of B with M rows, 64 columns more or not (with K rows, a box has 128)
-        const bool wide = !p.b_m_rows || run.width > 128;
-        const uint32_t bytes = (wide ? 2 : 1) * kOperand + (few ? ((rows_0 + kFew - 1) / kFew + (max(rows_1, 0) + kFew - 1) / kFew) *
+        // of B with M rows, 64 columns more or not (with K rows, a box has bn / 2)
+        const bool wide = run.width > 128;
+        const uint32_t bytes = (!p.b_m_rows ? p.bn * (kStep * 2) : (wide ? 2 : 1) * kOperand) + (few ? ((rows_0 + kFew - 1) / kFew + (max(rows_1, 0) + kFew - 1) / kFew) *
                                                                      (kFew * kStep * 2)
                                                                : 2 * kOperand);
         for (int kb = run.k0; kb < run.k1; ++kb) {
           if (!bar_wait(&sh.empty[stage], phase ^ 1, dead)) break;
-          const uint32_t a = saddr(stages + stage * kStageBytes), b = a + kOperand, bar = at_rank(saddr(&sh.full[stage]), 0);
+          const uint32_t a = saddr(stages + stage * p.stage_bytes), b = a + p.a_bytes, bar = at_rank(saddr(&sh.full[stage]), 0);
           if (rank == 0) bar_expect(&sh.full[stage], bytes);
           const int x = kb * kStep;
           if (p.a_m_rows) {
@@ -221,7 +217,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) k_produ
           } else {
             load_box(b, &p.b, x, p.b_y0 + col, bar);
           }
-          if (++stage == kStages) {
+          if (++stage == p.stages) {
             stage = 0;
             phase ^= 1;
           }
@@ -234,7 +230,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) k_produ
       const uint32_t a_step = step_bytes(p.a_m_rows) >> 4, b_step = step_bytes(p.b_m_rows) >> 4;
       int stage = 0, buf = 0;
       uint32_t phase = 0, turn = 0;
-      while (!*dead && walk.take(run)) {
+      for (int i = 0; !*dead && run_of(p, plan, pairs, pair, i, run); ++i) {
         const uint32_t idesc = instruction(p.bf16, p.a_m_rows, p.b_m_rows, run.width);
         for (int kb = run.k0; kb < run.k1;) {
           if (!bar_wait(&sh.drained[buf], turn ^ 1, dead)) break;
@@ -244,12 +240,12 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) k_produ
           for (; kb < to; ++kb) {
             if (!bar_wait(&sh.full[stage], phase, dead)) break;
             fence_after();
-            const uint32_t at = saddr(stages + stage * kStageBytes);
-            const uint64_t a = describe(at, p.a_m_rows), b = describe(at + kOperand, p.b_m_rows);
+            const uint32_t at = saddr(stages + stage * p.stage_bytes);
+            const uint64_t a = describe(at, p.a_m_rows), b = describe(at + p.a_bytes, p.b_m_rows);
 #pragma unroll
             for (int i = 0; i < kStep / 16; ++i) multiply(d, a + i * a_step, b + i * b_step, idesc, kb > from || i > 0);
             commit_both(&sh.empty[stage]);
-            if (++stage == kStages) {
+            if (++stage == p.stages) {
               stage = 0;
               phase ^= 1;
             }
@@ -264,11 +260,10 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) k_produ
   } else {
     const int quarter = warp & 3, group = warp >> 2;  // 32 lanes of tensor memory, 64 columns
     float4* st = reinterpret_cast<float4*>(staging + warp * kStaging);
-    const float scale = KIND == kOut && p.scale ? *p.scale : 1.f;
     int buf = 0;
     uint32_t turn = 0, flip = 0;
     bool alive = true;
-    while (walk.take(run)) {
+    for (int i = 0; run_of(p, plan, pairs, pair, i, run); ++i) {
       const int row0 = run.tm * kTile + (int)rank * kHalf + quarter * 32, row = row0 + lane;
       const int col0 = run.tn * p.bn + group * kCols;
       // (loaded while the tile is summed)
@@ -292,12 +287,12 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) k_produ
         fence_after();
         const uint32_t t = tmem + buf * kTile + group * kCols + ((uint32_t)(quarter * 32) << 16);
 #pragma unroll
-        for (int c = 0; c < kCols; c += 16) {
-          float x[16];
-          tmem_load16(t + c, x);
+        for (int c = 0; c < kCols; c += 8) {
+          float x[8];
+          tmem_load8(t + c, x);
           tmem_wait();
 #pragma unroll
-          for (int i = 0; i < 16; ++i) v[c + i] += x[i];
+          for (int e = 0; e < 8; ++e) v[c + e] += x[e];
         }
         fence_before();
         __syncwarp();
@@ -316,11 +311,13 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) k_produ
           for (int i = 0; i < kCols / 4; ++i) to[i * kHalf] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
         } else {
           const int end = min(p.n, run.tn * p.bn + run.width);
+          const float scale = p.scale ? __ldg(p.scale) : 1.f;
           put_block<T>(v, st, lane, p, row0, min(32, m - row0), col0, min(32, end - col0), scale);
           put_block<T>(v + 32, st, lane, p, row0, min(32, m - row0), col0 + 32, min(32, end - col0 - 32), scale);
         }
       } else if constexpr (KIND == kLse) {
-        const int left = p.vocab - p.column0 - col0;  // columns that are in the vocabulary
+        // columns that are in the tile and the vocabulary
+        const int left = min(p.vocab - p.column0 - run.tn * p.bn, run.width) - group * kCols;
         if (left < kCols) {
 #pragma unroll
           for (int i = 0; i < kCols; ++i)
@@ -358,10 +355,11 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) k_produ
           // (columns without a logit above -infinity have a sum of 0, or NaN, which stays)
 #pragma unroll
           for (int g = 0; g < 4; ++g) sum += x[g].y * (x[g].x == -INFINITY ? 0.f : exp_of(x[g].x - most_of));
-          p.part[(long long)((p.column0 + col0) / kPartCols) * p.part_rows + row] = make_float2(most_of, sum);
+          p.part[(long long)run.tn * p.part_rows + row] = make_float2(most_of, sum);
         }
         flip ^= 1;
       } else {
+        if (group * kCols >= run.width) continue;
         const int left = row < m ? p.vocab - p.column0 - col0 : 0;
         if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");  // the staging's last box is out
         __syncwarp();
@@ -399,7 +397,6 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) k_produ
     if (lane == 0) atomicExch(p.error, 1);
   }
   __syncthreads();
-  next_may_launch();
   cluster_sync();
   if (warp == kEpilogueWarps + 1) tmem_free(tmem);
 }
@@ -559,13 +556,32 @@ static int columns_of(const Product& p, int pairs) {
   return best;
 }
 
+// A step costs as its rows and columns; the last turn's pairs without a tile idle.  For a token over 50257 columns, 197 tiles
+// of 256 on 76 pairs are 3 turns, 225 of 224 as many.  GRAD leaves boxes of 64 columns.
+int logits_columns(Epilogue kind, long long rows, long long n, int pairs) {
+  int best = kTile;
+  long long least = 0;
+  for (int bn = kTile; bn >= 128; bn -= kind == kGrad ? 64 : 32) {
+    const long long turns = ops::units(ops::units(rows, kTile) * ops::units(n, bn), pairs), cost = turns * (std::min<long long>(rows, kTile) + bn);
+    if (bn == kTile || cost * 20 < least * 19) {
+      least = cost;
+      best = bn;
+    }
+  }
+  return best;
+}
+
 cudaError_t enqueue(Epilogue kind, Product p, int device, int pairs, cudaStream_t st) {
   // (the others' columns go by 128)
-  p.bn = kind == kOut ? columns_of(p, pairs) : kTile;
+  if (kind == kOut) p.bn = columns_of(p, pairs);
   if (kind == kOut) {
     const int size = 4 * ops::dtype_size(p.dtype);
     p.vec = (uintptr_t)p.out % size == 0 && (p.ldo % 4 == 0 || p.m == 1);
   }
+  // where A with K rows has fewer rows than a CTA's part, or B fewer columns, there are more stages
+  p.a_bytes = p.a_m_rows || p.m > kHalf ? kOperand : (int)ops::units(std::max(p.m, 1), kFew) * kFew * kStep * 2;
+  p.stage_bytes = p.a_bytes + (p.b_m_rows ? (p.bn > 128 ? kOperand : kOperand / 2) : p.bn * kStep);
+  p.stages = std::min(kMostStages, kStages * kStageBytes / p.stage_bytes);
   // (extents that the device knows are at most these)
   const long long tiles = ops::units(p.m, kTile) * ops::units(p.n, p.bn);
   if (tiles == 0) return cudaSuccess;
@@ -576,8 +592,10 @@ cudaError_t enqueue(Epilogue kind, Product p, int device, int pairs, cudaStream_
   else if (kind == kGrad) e = p.bf16 ? go<kGrad, __nv_bfloat16>(p, grid, device, st) : go<kGrad, __half>(p, grid, device, st);
   else e = by_type(p.dtype, [&](auto* t) { return go<kOut, std::remove_pointer_t<decltype(t)>>(p, grid, device, st); });
   if (e != cudaSuccess || kind != kOut || !p.slots) return e;
-  // which tiles are cut goes by the extents that the device knows; with those of the host there may be none
-  if (!p.live && schedule_of(p.m, p.n, p.bn, p.k, pairs, true).workers == 0) return e;
+  // Which tiles are cut goes by the extents that the device knows.  Few steps are never cut, and of one row of tiles there
+  // is either that or nothing.
+  const Schedule s = schedule_of(p.m, p.n, p.bn, p.k, pairs, true);
+  if (s.kb < 2 * kMinSplit || ((!p.live || (p.live_is == 1 && s.mt == 1)) && s.workers == 0)) return e;
   const dim3 parts(32, (unsigned)std::min<long long>(tiles, pairs - 1));
   return by_type(p.dtype, [&](auto* t) {
     return ops::launch_early(k_join<std::remove_pointer_t<decltype(t)>>, parts, 64 * kJoin, 0, 1, st, p, pairs);

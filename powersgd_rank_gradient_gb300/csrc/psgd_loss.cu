@@ -5,7 +5,7 @@
 //
 // The logits are made tile by tile on the tensor cores and used where they are
 // made (psgd_gemm.cu): the forward pass leaves the largest logit and the sum of
-// exponentials of every 256 columns of a row, the backward pass makes them again
+// exponentials of every tile's columns of a row, the backward pass makes them again
 // and leaves G, rounded to 16 bits, for a piece of the vocabulary at a time; both
 // gradients are products of that piece.  No memory grows with tokens x vocabulary
 // but those pieces, which are bounded.
@@ -36,8 +36,8 @@ struct psgd_linear_ce {
   void* g = nullptr;
   float* dh = nullptr;       // cap x dp
   float* slots = nullptr;
-  float2* part = nullptr;    // cap for every 256 columns
-  float *lse = nullptr, *factor = nullptr;
+  float2* part = nullptr;    // cap for every tile's columns
+  float *lse = nullptr, *factor = nullptr, *at_target = nullptr;
   int *row = nullptr, *target = nullptr, *exponent = nullptr;  // of the tokens that count
   int* place = nullptr;      // of a token among them, or -1
   int* count = nullptr;      // [0]: tokens that count, [1]: largest exponent, [2]: error
@@ -165,66 +165,6 @@ __device__ void plan(const Tokens& t, int* place, int* row, int* target, float* 
   }
 }
 
-// The rows of the tokens that count, side by side.  hs (backward): the rows times 2^(e - max e), then rows of zeros up to
-// a whole step of the sum over tokens; lse: theirs.
-template <typename T, int V>
-__device__ __forceinline__ void gather_rows(const T* src, long long stride, int dim, const int* row, const int* exponent, const int* count,
-                                            T* h, T* hs, long long dp, const float* lse_of, float* lse, int block, int blocks) {
-  const int n = count[0], end = hs ? (n + mma::kStep - 1) / mma::kStep * mma::kStep : n;
-  for (int r = block; r < end; r += blocks) {
-    const bool in = r < n;
-    const T* from = src + (in ? (long long)row[r] * stride : 0);
-    const float f = in && hs ? scalbnf(1.f, max(exponent[r] - count[1], -200)) : 1.f;
-    if (lse && in && threadIdx.x == 0) lse[r] = lse_of[row[r]];
-    for (int c = threadIdx.x * V; c < dim; c += blockDim.x * V) {
-      if constexpr (V == 1) {
-        const T x = in ? from[c] : from_f<T>(0.f);
-        h[r * dp + c] = x;
-        if (hs) hs[r * dp + c] = from_f<T>(to_f(x) * f);
-      } else {
-        const uint4 x = in ? *reinterpret_cast<const uint4*>(from + c) : make_uint4(0, 0, 0, 0);
-        *reinterpret_cast<uint4*>(h + r * dp + c) = x;
-        if (hs) {
-          F2 p[V / 2];
-          float v[V];
-          to_pairs<T>(x, p);
-#pragma unroll
-          for (int i = 0; i < V / 2; ++i) split(p[i], v[2 * i], v[2 * i + 1]);
-#pragma unroll
-          for (int i = 0; i < V; ++i) v[i] *= f;
-          store_pack<T, V>(hs + r * dp + c, v);
-        }
-      }
-    }
-  }
-}
-template <typename T, int V>
-__global__ void __launch_bounds__(128) k_gather(const T* src, long long stride, int dim, const int* row, const int* exponent, const int* count,
-                                                T* h, T* hs, long long dp, const float* lse_of, float* lse) {
-  after_previous();
-  next_may_launch();
-  gather_rows<T, V>(src, stride, dim, row, exponent, count, h, hs, dp, lse_of, lse, blockIdx.x, gridDim.x);
-}
-
-__global__ void __launch_bounds__(1024) k_plan(Tokens t, int* place, int* row, int* target, float* factor, int* exponent, int* count,
-                                               float* scale, float grad_scale, int shift) {
-  after_previous();
-  next_may_launch();
-  plan(t, place, row, target, factor, exponent, count, scale, grad_scale, shift);
-}
-// Both in one launch, where the rows are little enough for one CTA.
-constexpr long long kFewElements = 32768;
-template <typename T, int V>
-__global__ void __launch_bounds__(1024) k_plan_gather(Tokens t, int* place, int* row, int* target, float* factor, int* exponent, int* count,
-                                                      float* scale, float grad_scale, int shift, const T* src, long long stride, int dim, T* h,
-                                                      T* hs, long long dp, const float* lse_of, float* lse) {
-  after_previous();
-  next_may_launch();
-  plan(t, place, row, target, factor, exponent, count, scale, grad_scale, shift);
-  __syncthreads();
-  gather_rows<T, V>(src, stride, dim, row, exponent, count, h, hs, dp, lse_of, lse, 0, 1);
-}
-
 // A warp's product of two rows of 16-bit elements, of any alignment.
 template <typename T> __device__ __forceinline__ float warp_dot(const T* a, const T* b, int dim, bool vec) {
   const int lane = threadIdx.x & 31;
@@ -252,15 +192,84 @@ template <typename T> __device__ __forceinline__ float warp_dot(const T* a, cons
   return warp_sum(sum);
 }
 
-// Losses and log-sum-exps of 32 tokens a CTA from the pieces of 256 columns, whose order the warps share, and the
-// targets' logits, a warp each.  Those are summed here, in rounded fp32: where a target is likely, its logit is by far
-// the largest, the loss is the small rest, and the tensor cores' drift on a large sum (2e-6 of it) would be most of it.
-template <typename T>
+// The rows of the tokens that count, side by side.  Forward: and their targets' logits, which are summed here, in rounded
+// fp32: where a target is likely, its logit is by far the largest, the loss is the small rest, and the tensor cores'
+// drift on a large sum (2e-6 of it) would be most of it.  Backward: and the rows times 2^(e - max e), then rows of zeros
+// up to a whole step of the sum over tokens, and the tokens' lse.
+template <typename T> struct Gather {
+  const T* src;
+  long long stride;
+  int dim;
+  const int *row, *target, *exponent, *count;
+  T *h, *hs;  // hs: backward
+  long long dp;
+  const float* lse_of;
+  float* lse;
+  const T* weight;  // forward
+  long long weight_stride;
+  int vec_dot;
+  float* at_target;
+};
+template <typename T, int V> __device__ __forceinline__ void gather_rows(const Gather<T>& a, int first, int step, int thread, int threads) {
+  const int n = a.count[0], end = a.hs ? (n + mma::kStep - 1) / mma::kStep * mma::kStep : n;
+  for (int r = first; r < end; r += step) {
+    const bool in = r < n;
+    const T* from = a.src + (in ? (long long)a.row[r] * a.stride : 0);
+    const float f = in && a.hs ? scalbnf(1.f, max(a.exponent[r] - a.count[1], -200)) : 1.f;
+    if (a.lse && in && thread == 0) a.lse[r] = a.lse_of[a.row[r]];
+    for (int c = thread * V; c < a.dim; c += threads * V) {
+      if constexpr (V == 1) {
+        const T x = in ? from[c] : from_f<T>(0.f);
+        a.h[r * a.dp + c] = x;
+        if (a.hs) a.hs[r * a.dp + c] = from_f<T>(to_f(x) * f);
+      } else {
+        const uint4 x = in ? *reinterpret_cast<const uint4*>(from + c) : make_uint4(0, 0, 0, 0);
+        *reinterpret_cast<uint4*>(a.h + r * a.dp + c) = x;
+        if (a.hs) {
+          F2 p[V / 2];
+          float v[V];
+          to_pairs<T>(x, p);
+#pragma unroll
+          for (int i = 0; i < V / 2; ++i) split(p[i], v[2 * i], v[2 * i + 1]);
+#pragma unroll
+          for (int i = 0; i < V; ++i) v[i] *= f;
+          store_pack<T, V>(a.hs + r * a.dp + c, v);
+        }
+      }
+    }
+    if (a.weight && thread < 32) {  // (the first warp of the row's threads)
+      const float z = warp_dot(from, a.weight + a.target[r] * a.weight_stride, a.dim, a.vec_dot);
+      if (thread == 0) a.at_target[r] = z;
+    }
+  }
+}
+template <typename T, int V> __global__ void __launch_bounds__(128) k_gather(Gather<T> a) {
+  after_previous();
+  next_may_launch();
+  gather_rows<T, V>(a, blockIdx.x, gridDim.x, threadIdx.x, 128);
+}
+__global__ void __launch_bounds__(1024) k_plan(Tokens t, int* place, int* row, int* target, float* factor, int* exponent, int* count,
+                                               float* scale, float grad_scale, int shift) {
+  after_previous();
+  next_may_launch();
+  plan(t, place, row, target, factor, exponent, count, scale, grad_scale, shift);
+}
+// Both in one launch, where the rows are few enough for one CTA, a warp a row.
+constexpr int kFewTokens = 32;
+template <typename T, int V>
+__global__ void __launch_bounds__(1024) k_plan_gather(Tokens t, int* place, int* row, int* target, float* factor, int* exponent, int* count,
+                                                      float* scale, float grad_scale, int shift, Gather<T> a) {
+  after_previous();
+  next_may_launch();
+  plan(t, place, row, target, factor, exponent, count, scale, grad_scale, shift);
+  __syncthreads();
+  gather_rows<T, V>(a, threadIdx.x >> 5, 32, threadIdx.x & 31, 32);
+}
+
+// Losses and log-sum-exps of 32 tokens a CTA from the tiles, whose order the warps share, and the targets' logits.
 __global__ void __launch_bounds__(1024) k_losses(Tokens t, const int* place, const float2* part, long long part_rows, int parts,
-                                                 const T* hidden, long long hidden_stride, const T* weight, long long weight_stride, int dim,
-                                                 bool vec, float* losses, float* lses) {
+                                                 const float* at_target, float* losses, float* lses) {
   __shared__ float2 all[32][33];
-  __shared__ float logit[32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, i = blockIdx.x * 32 + lane;
   after_previous();
   next_may_launch();
@@ -281,18 +290,12 @@ __global__ void __launch_bounds__(1024) k_losses(Tokens t, const int* place, con
       for (int k = 0; k < 8; ++k) add(x[k]);
     }
   all[warp][lane] = make_float2(top, sum);
-  // (all lanes have the CTA's places: token `warp` is lane `warp`'s)
-  if (__shfl_sync(0xffffffffu, at, warp) >= 0) {
-    const long long mine = blockIdx.x * 32 + warp;
-    const float z = warp_dot(hidden + mine * hidden_stride, weight + target_of(t, (int)mine) * weight_stride, dim, vec);
-    if (lane == 0) logit[warp] = z;
-  }
   __syncthreads();
   if (warp || i >= t.tokens) return;
   float loss = 0.f, lse = 0.f;
   if (at >= 0) {
     for (int w = 1; w < 32; ++w) add(all[w][lane]);
-    const float z = logit[lane];
+    const float z = at_target[at];
     float rest;
     if (z >= top) {  // of a target that is nearly certain the loss is what the others add
       rest = z == INFINITY ? NAN : log1pf(sum * __expf(top - z));
@@ -367,21 +370,21 @@ struct Call {
   void gather(bool backward, const float* lse, float grad_scale) {
     const int shift = bf16 ? 0 : kF16Shift;
     const bool vec = h->dim % 8 == 0 && aligned16(hidden) && hidden_stride % 8 == 0;
-    const bool few = (long long)t.tokens * h->dim <= kFewElements;
+    const bool few = t.tokens <= kFewTokens;
     if (!few)
       e = launch_early(k_plan, 1, 1024, 0, 1, st, t, h->place, h->row, h->target, h->factor, h->exponent, h->count, h->scale, grad_scale, shift);
     if (e != cudaSuccess) return;
-    void* hs = backward ? h->hs : nullptr;
     const auto go = [&](auto* tt, auto v) {
       using T = std::remove_pointer_t<decltype(tt)>;
       constexpr int V = decltype(v)::value;
+      const Gather<T> a{(const T*)hidden, hidden_stride, (int)h->dim, h->row, h->target, h->exponent, h->count, (T*)h->h,
+                        backward ? (T*)h->hs : nullptr, h->dp, lse, backward ? h->lse : nullptr, backward ? nullptr : (const T*)weight,
+                        weight_stride, vec && in_place, h->at_target};
       if (few)
         e = launch_early(k_plan_gather<T, V>, 1, 1024, 0, 1, st, t, h->place, h->row, h->target, h->factor, h->exponent, h->count, h->scale,
-                         grad_scale, shift, (const T*)hidden, hidden_stride, (int)h->dim, (T*)h->h, (T*)hs, h->dp, lse,
-                         backward ? h->lse : nullptr);
+                         grad_scale, shift, a);
       else
-        e = launch_early(k_gather<T, V>, (unsigned)std::min(t.tokens + mma::kStep, 4096), 128, 0, 1, st, (const T*)hidden, hidden_stride,
-                         (int)h->dim, h->row, h->exponent, h->count, (T*)h->h, (T*)hs, h->dp, lse, backward ? h->lse : nullptr);
+        e = launch_early(k_gather<T, V>, (unsigned)std::min(t.tokens + mma::kStep, 4096), 128, 0, 1, st, a);
     };
     using One = std::integral_constant<int, 1>;
     using Eight = std::integral_constant<int, 8>;
@@ -389,7 +392,7 @@ struct Call {
     else vec ? go((__half*)nullptr, Eight()) : go((__half*)nullptr, One());
   }
   // The rows [v0, v0 + n) of the weight as an operand, either way around.
-  void weight_map(mma::Product& z, CUtensorMap* m_rows, long long v0, long long n) {
+  void weight_map(mma::Epilogue kind, mma::Product& z, CUtensorMap* m_rows, long long v0, long long n) {
     if (e != cudaSuccess) return;
     const void* p = weight;
     long long rows = h->vocab, stride = weight_stride;
@@ -401,7 +404,8 @@ struct Call {
       stride = h->dp;
       z.b_y0 = 0;
     }
-    if (e == cudaSuccess) e = mma::make_map(&z.b, p, rows, h->dim, stride, mma::box_rows(false), bf16);
+    z.bn = mma::logits_columns(kind, t.tokens, n, h->pairs);
+    if (e == cudaSuccess) e = mma::make_map(&z.b, p, rows, h->dim, stride, z.bn / 2, bf16);
     if (e == cudaSuccess && m_rows) e = mma::make_map(m_rows, p, rows, h->dim, stride, mma::box_rows(true), bf16);
   }
   // What a product over the logits is told: rows are tokens, columns [v0, v0 + n) of the vocabulary.
@@ -461,8 +465,8 @@ extern "C" int psgd_linear_ce_create(int64_t vocab, int64_t dim, int64_t max_tok
   get(&h->g, h->cap * h->piece * 2);
   get(&h->dh, h->cap * h->dp * 4);
   get(&h->slots, 2 * h->pairs * mma::kSlotFloats * 4);
-  get(&h->part, tiles * h->cap * 8);
-  for (float** p : {&h->lse, &h->factor}) get(p, h->cap * 4);
+  get(&h->part, (units(vocab, mma::kTile / 2) + units(vocab, h->piece)) * h->cap * 8);  // (tiles have 128 columns at least)
+  for (float** p : {&h->lse, &h->factor, &h->at_target}) get(p, h->cap * 4);
   for (int** p : {&h->row, &h->target, &h->exponent, &h->place}) get(p, h->cap * 4);
   get(&h->count, 16);
   get(&h->scale, 8);
@@ -481,7 +485,7 @@ extern "C" void psgd_linear_ce_destroy(psgd_linear_ce* h) {
   if (!h) return;
   {
     DeviceScope scope(h->device);
-    for (void* p : {h->h, h->hs, h->w, h->g, (void*)h->dh, (void*)h->slots, (void*)h->part, (void*)h->lse,
+    for (void* p : {h->h, h->hs, h->w, h->g, (void*)h->dh, (void*)h->slots, (void*)h->part, (void*)h->at_target, (void*)h->lse,
                     (void*)h->factor, (void*)h->row, (void*)h->target, (void*)h->exponent, (void*)h->place, (void*)h->count,
                     (void*)h->scale})
       cudaFree(p);
@@ -515,24 +519,17 @@ extern "C" int psgd_linear_ce_forward(psgd_linear_ce* h, const void* hidden, psg
   Call c(h, hidden, dtype, hidden_stride, weight, weight_stride, targets, target_bits, weights, tokens, stream);
   c.gather(false, nullptr, 1.f);
   const long long step = c.in_place ? h->vocab : h->piece;
+  int parts = 0;
   for (long long v0 = 0; v0 < h->vocab && c.e == cudaSuccess; v0 += step) {
     const long long n = std::min(step, h->vocab - v0);
     mma::Product p = c.logits(v0, n);
-    c.weight_map(p, nullptr, v0, n);
-    p.part = h->part, p.part_rows = h->cap;
+    c.weight_map(mma::kLse, p, nullptr, v0, n);
+    p.part = h->part + parts * h->cap, p.part_rows = h->cap;
+    parts += (int)units(n, p.bn);
     if (c.e == cudaSuccess) c.e = mma::enqueue(mma::kLse, p, h->device, h->pairs, c.st);
   }
-  const auto go = [&](auto* tt) {
-    using T = std::remove_pointer_t<decltype(tt)>;
-    const bool vec = c.in_place && h->dim % 8 == 0 && aligned16(hidden) && hidden_stride % 8 == 0;
-    c.e = launch_early(k_losses<T>, (unsigned)units(tokens, 32), 1024, 0, 1, c.st, c.t, h->place, h->part, h->cap,
-                       (int)units(h->vocab, mma::kPartCols), (const T*)hidden, hidden_stride, (const T*)weight, weight_stride, (int)h->dim,
-                       vec, losses, lse);
-  };
-  if (c.e == cudaSuccess) {
-    if (c.bf16) go((__nv_bfloat16*)nullptr);
-    else go((__half*)nullptr);
-  }
+  if (c.e == cudaSuccess)
+    c.e = launch_early(k_losses, (unsigned)units(tokens, 32), 1024, 0, 1, c.st, c.t, h->place, h->part, h->cap, parts, h->at_target, losses, lse);
   return c.e == cudaSuccess ? PSGD_OK : cuda_fail(who.c_str(), c.e);
 }
 
@@ -568,7 +565,7 @@ extern "C" int psgd_linear_ce_backward(psgd_linear_ce* h, const void* hidden, ps
   for (long long v0 = 0; v0 < h->vocab && c.e == cudaSuccess; v0 += h->piece) {
     const long long n = std::min(h->piece, h->vocab - v0);
     mma::Product z = c.logits(v0, n), dh{}, dw{};
-    c.weight_map(z, &dh.b, v0, n);
+    c.weight_map(mma::kGrad, z, &dh.b, v0, n);
     z.lse = h->lse, z.factor = h->factor;
     if (c.e == cudaSuccess) c.e = mma::make_map(&z.store, h->g, h->cap, h->piece, h->piece, 32, c.bf16);
     if (c.e == cudaSuccess && tokens > 0) c.e = mma::enqueue(mma::kGrad, z, h->device, h->pairs, c.st);

@@ -27,7 +27,8 @@ constexpr int kTile = 256;     // rows and columns of a pair's tile
 constexpr int kHalf = 128;     // rows of a CTA's part
 constexpr int kFew = 32;
 constexpr int kStep = 64;      // elements of the summed dimension per stage
-constexpr int kStages = 5;
+constexpr int kStages = 5;     // of whole operands; of fewer rows and columns as many as their room holds
+constexpr int kMostStages = 10;
 constexpr int kOperand = kHalf * kStep * 2;  // bytes of one operand's part of a stage
 constexpr int kStageBytes = 2 * kOperand;
 constexpr int kEpilogueWarps = 16;
@@ -154,14 +155,12 @@ __device__ __forceinline__ void tmem_free(uint32_t t) {
   asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(t));
 }
 
-// 16 columns of a warp's 32 lanes; there after tmem_wait().
-__device__ __forceinline__ void tmem_load16(uint32_t t, float* v) {
+// 8 columns of a warp's 32 lanes; there after tmem_wait().
+__device__ __forceinline__ void tmem_load8(uint32_t t, float* v) {
   uint32_t* r = reinterpret_cast<uint32_t*>(v);
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]),
-        "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-      : "r"(t));
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(t));
 }
 __device__ __forceinline__ void tmem_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 
@@ -177,6 +176,7 @@ struct Product {
   CUtensorMap store;         // GRAD: the gradients' matrix, in boxes of 64 x 32
   int m, n, k;               // extents in elements
   int bn;                    // columns of a tile but the last (see width_of)
+  int stages, a_bytes, stage_bytes;  // room of a stage's A and of a stage in each CTA
   const int* live;           // device: takes the place of m (live_is 1) or k (2); or NULL
   int live_is;
   int a_m_rows, b_m_rows;    // how the operands lie
@@ -195,7 +195,7 @@ struct Product {
   // LSE and GRAD: rows are tokens, columns the vocabulary from column0 on
   int column0, vocab;        // columns in all
   const int* target;         // per row
-  float2* part;              // LSE: largest logit but the target's and sum of exp(z - it), for every 256 columns: [part][row]
+  float2* part;              // LSE: largest logit but the target's and sum of exp(z - it), for every tile's columns: [part][row]
   long long part_rows;       // rows between parts
   const float* lse;          // GRAD
   const float* factor;       // GRAD: multiplies a row's gradient
@@ -258,8 +258,8 @@ inline int box_rows(bool m_rows) { return m_rows ? kStep : kHalf; }
 
 // Pairs of CTAs that a device holds at once.
 cudaError_t pairs_of(int device, int* pairs);
-// Columns whose logits one entry of `part` stands for.
-constexpr int kPartCols = kTile;
+// Columns of the tiles of an LSE or GRAD product over n columns; B's boxes have half as many rows.
+int logits_columns(Epilogue kind, long long rows, long long n, int pairs);
 // Enqueues a product, and for split tiles the sum of their parts.
 cudaError_t enqueue(Epilogue kind, Product p, int device, int pairs, cudaStream_t st);
 // Rows of 16-bit elements of any stride and alignment into rows `to` elements apart.
