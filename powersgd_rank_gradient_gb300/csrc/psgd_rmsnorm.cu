@@ -12,10 +12,12 @@
 // keeps their dw sums in fp32 registers; a CTA leaves one partial row and a
 // second kernel adds the partial rows in a fixed order.
 #include <algorithm>
+#include <atomic>
 #include <new>
 #include <type_traits>
 
 #include "psgd_eight.cuh"
+#include "psgd_rows.cuh"
 
 struct psgd_rmsnorm {
   int device = 0;
@@ -30,7 +32,7 @@ namespace psgd {
 namespace ops {
 namespace {
 
-constexpr int kThreadsMost = 512;  // of a CTA
+constexpr int kThreadsMost = kRowThreads;  // of a CTA
 constexpr int kCtasPerSm = 2;      // at most; one where a thread holds 16 elements of a row
 constexpr int kElements = 16;      // of a row that a thread holds, at most
 
@@ -307,6 +309,274 @@ __global__ void __launch_bounds__(kThreadsMost, (Unit<T, V>::E * NV < kElements 
   }
 }
 
+// The kernels for rows of whole 16-byte units.  A group takes R rows at a time, which share the barriers and shuffles
+// of one reduction; the rows of the next two turns are copied ahead into shared memory, by the thread that will use
+// them, so that neither a register nor a barrier waits for what is under way.
+constexpr int kAhead = 3;  // turns: the one in use and those under way
+
+template <typename T, int NV, int R>
+__global__ void __launch_bounds__(kThreadsMost, 1) k_rms_forward_vec(RmsArgs a) {
+  constexpr int E = Vec16<T>::N, NP = E / 2;
+  extern __shared__ __align__(16) uint4 staged[];
+  __shared__ float red[2][kThreadsMost / 32 * R];
+  const int t = threadIdx.x, group = threadIdx.y, threads = blockDim.x;
+  const int warps = threads / 32, warp = t >> 5, lane = t & 31;
+  const int arrays = a.residual ? 2 : 1;
+  const float inv = 1.f / (float)a.dim;
+  uint4* mine = staged + group * threads + t;
+  bool in[NV];
+#pragma unroll
+  for (int j = 0; j < NV; ++j) in[j] = (t + j * threads) * E < a.dim;
+  const int step = gridDim.x * blockDim.y * R;
+  int row = ((int)blockIdx.x * blockDim.y + group) * R;  // the turn's first row
+  int left = (int)a.rows - row;                          // rows from the next turn to copy on
+  const T* from_x = (const T*)a.x + row * a.xs + t * E;
+  const T* from_r = (const T*)a.residual + row * a.rs + t * E;
+  auto issue = [&](int stage) {
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+      for (int j = 0; j < NV; ++j)
+        if (r < left && in[j]) {
+          uint4* dst = mine + ((stage * R + r) * NV + j) * arrays * kThreadsMost;
+          copy16(dst, from_x + r * a.xs + j * threads * E);
+          if (a.residual) copy16(dst + kThreadsMost, from_r + r * a.rs + j * threads * E);
+        }
+    commit_copies();
+    left -= step;
+    from_x += step * a.xs;
+    from_r += step * a.rs;
+  };
+  after_previous();
+  next_may_launch();
+#pragma unroll
+  for (int k = 0; k < kAhead - 1; ++k) issue(k);
+  F2 w[NV][NP];
+#pragma unroll
+  for (int j = 0; j < NV; ++j) load_param<NP>(a.w, a.pdtype, (long long)(t + j * threads) * E, in[j], 1.f, w[j]);
+  int stage = 0, flip = 0;
+  for (; row < (int)a.rows; row += step, flip ^= 1) {
+    asm volatile("cp.async.wait_group %0;" ::"n"(kAhead - 2) : "memory");
+    // (in the place of the turn before, which is used up)
+    issue(stage == 0 ? kAhead - 1 : stage - 1);
+    const int rows = min(R, (int)a.rows - row);
+    F2 s[R][NV][NP];
+    float sum[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      F2 squares = f2(0.f, 0.f);
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        const uint4* src = mine + ((stage * R + r) * NV + j) * arrays * kThreadsMost;
+        const bool live = in[j] && r < rows;
+        uint4 raw = live ? src[0] : make_uint4(0, 0, 0, 0);
+        to_pairs<T>(raw, s[r][j]);
+        if (a.residual) {
+          F2 add2[NP];
+          to_pairs<T>(live ? src[kThreadsMost] : make_uint4(0, 0, 0, 0), add2);
+          float f[E];
+#pragma unroll
+          for (int h = 0; h < NP; ++h) {
+            s[r][j][h] = add(s[r][j][h], add2[h]);
+            split(s[r][j][h], f[2 * h], f[2 * h + 1]);
+          }
+          // rounded as it is kept
+          if constexpr (sizeof(T) == 2) {
+            raw = make_uint4(pack2<T>(f[0], f[1]), pack2<T>(f[2], f[3]), pack2<T>(f[4], f[5]), pack2<T>(f[6], f[7]));
+            to_pairs<T>(raw, s[r][j]);
+          } else {
+            raw = make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
+          }
+        }
+        if (a.summed && live) *reinterpret_cast<uint4*>((T*)a.summed + (row + r) * a.ss + (t + j * threads) * E) = raw;
+#pragma unroll
+        for (int h = 0; h < NP; ++h) squares = fma(s[r][j][h], s[r][j][h], squares);
+      }
+      float u, v;
+      split(squares, u, v);
+      sum[r] = u + v;
+    }
+    stage = stage + 1 == kAhead ? 0 : stage + 1;
+    group_sum<R>(sum, red[flip] + group * warps * R, warps, warp, lane, group, threads);
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      if (r >= rows) break;
+      const float rstd = rsqrtf(fmaf(sum[r], inv, a.eps));
+      if (t == 0) a.rstd[row + r] = rstd;
+      const F2 rs = f2(rstd, rstd);
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        float y[E];
+#pragma unroll
+        for (int h = 0; h < NP; ++h) split(mul(mul(s[r][j][h], rs), w[j][h]), y[2 * h], y[2 * h + 1]);
+        const int c = (t + j * threads) * E;
+        if (a.codes) {
+          unsigned code[E / 4];
+          float scale;
+          encode<E, kBlock8 / E>(a.e5, y, code, scale);
+          if (!in[j]) continue;
+          unsigned char* to = a.codes + (long long)(row + r) * a.dim + c;
+          if constexpr (E == 8) *reinterpret_cast<uint2*>(to) = make_uint2(code[0], code[1]);
+          else *reinterpret_cast<unsigned*>(to) = code[0];
+          if (c % kBlock8 == 0) a.scales[(long long)(row + r) * a.blocks + c / kBlock8] = scale;
+        } else if (in[j]) {
+          store_pack<T, E>((T*)a.y + (row + r) * a.ys + c, y);
+        }
+      }
+    }
+  }
+}
+
+// SAVED: s is in 8 bits.
+template <typename T, int NV, int R, bool SAVED>
+__global__ void __launch_bounds__(kThreadsMost, 1) k_rms_backward_vec(RmsArgs a) {
+  constexpr int E = Vec16<T>::N, NP = E / 2, LANES = kBlock8 / E;
+  extern __shared__ __align__(16) uint4 staged[];
+  __shared__ float red[2][kThreadsMost / 32 * R];
+  __shared__ float stats[kAhead][kThreadsMost / 32][R];  // each warp's own copy of the rows' rstd
+  __shared__ float scales[kAhead][R * NV][kThreadsMost / LANES];
+  const int t = threadIdx.x, group = threadIdx.y, threads = blockDim.x;
+  const int warps = threads / 32, warp = t >> 5, lane = t & 31, cta_warp = group * warps + warp;
+  const int arrays = a.residual && a.y ? 3 : 2, mine_8 = (group * threads + t) / LANES;
+  const float inv = 1.f / (float)a.dim;
+  uint4* mine = staged + group * threads + t;
+  bool in[NV];
+#pragma unroll
+  for (int j = 0; j < NV; ++j) in[j] = (t + j * threads) * E < a.dim;
+  const int step = gridDim.x * blockDim.y * R;
+  int row = ((int)blockIdx.x * blockDim.y + group) * R, ahead = row;
+  auto issue = [&](int stage) {
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+      for (int j = 0; j < NV; ++j)
+        if (ahead + r < (int)a.rows && in[j]) {
+          const int c = (t + j * threads) * E;
+          uint4* dst = mine + ((stage * R + r) * NV + j) * arrays * kThreadsMost;
+          copy16(dst, (const T*)a.g + (ahead + r) * a.gs + c);
+          if constexpr (SAVED) {
+            const unsigned char* code = a.codes + (long long)(ahead + r) * a.dim + c;
+            if constexpr (E == 8) copy8(dst + kThreadsMost, code);
+            else copy4(dst + kThreadsMost, code);
+            if (t % LANES == 0) copy4(&scales[stage][r * NV + j][mine_8], a.scales + (long long)(ahead + r) * a.blocks + c / kBlock8);
+          } else {
+            copy16(dst + kThreadsMost, (const T*)a.x + (ahead + r) * a.xs + c);
+          }
+          if (arrays == 3) copy16(dst + 2 * kThreadsMost, (const T*)a.residual + (ahead + r) * a.rs + c);
+        }
+    if (lane < R && ahead + lane < (int)a.rows) copy4(&stats[stage][cta_warp][lane], a.rstd + ahead + lane);
+    commit_copies();
+    ahead = ahead < (int)a.rows ? ahead + step : ahead;
+  };
+  after_previous();
+#pragma unroll
+  for (int k = 0; k < kAhead - 1; ++k) issue(k);
+  F2 w[NV][NP], dw[NV][NP];
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    load_param<NP>(a.w, a.pdtype, (long long)(t + j * threads) * E, in[j], 1.f, w[j]);
+#pragma unroll
+    for (int h = 0; h < NP; ++h) dw[j][h] = f2(0.f, 0.f);
+  }
+  int stage = 0, flip = 0;
+  for (; row < (int)a.rows; row += step, flip ^= 1) {
+    asm volatile("cp.async.wait_group %0;" ::"n"(kAhead - 2) : "memory");
+    __syncwarp();  // the other lanes' copies of scales and statistics
+    issue(stage == 0 ? kAhead - 1 : stage - 1);
+    const int rows = min(R, (int)a.rows - row);
+    const uint4* data = mine + stage * R * NV * arrays * kThreadsMost;
+    F2 xh[R][NV][NP], ga[R][NV][NP];
+    float sum[R], rstd[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      F2 along = f2(0.f, 0.f);
+      rstd[r] = stats[stage][cta_warp][r];
+      const F2 rs = f2(rstd[r], rstd[r]);
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        const uint4* src = data + (r * NV + j) * arrays * kThreadsMost;
+        if (!in[j] || r >= rows) {
+#pragma unroll
+          for (int h = 0; h < NP; ++h) xh[r][j][h] = ga[r][j][h] = f2(0.f, 0.f);
+          continue;
+        }
+        to_pairs<T>(src[0], ga[r][j]);
+        if constexpr (SAVED) {
+          const float scale = scales[stage][r * NV + j][mine_8];
+          float f[E];
+          const unsigned* code = reinterpret_cast<const unsigned*>(src + kThreadsMost);
+#pragma unroll
+          for (int k = 0; k < E / 4; ++k) decode4(a.e5, code[k], scale, f + 4 * k);
+#pragma unroll
+          for (int h = 0; h < NP; ++h) xh[r][j][h] = f2(f[2 * h], f[2 * h + 1]);
+        } else {
+          to_pairs<T>(src[kThreadsMost], xh[r][j]);
+        }
+#pragma unroll
+        for (int h = 0; h < NP; ++h) {
+          xh[r][j][h] = mul(xh[r][j][h], rs);
+          dw[j][h] = fma(ga[r][j][h], xh[r][j][h], dw[j][h]);
+          ga[r][j][h] = mul(ga[r][j][h], w[j][h]);
+          along = fma(ga[r][j][h], xh[r][j][h], along);
+        }
+      }
+      float u, v;
+      split(along, u, v);
+      sum[r] = u + v;
+    }
+    if (a.y) {
+      group_sum<R>(sum, red[flip] + group * warps * R, warps, warp, lane, group, threads);
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        if (r >= rows) break;
+        const float m = -sum[r] * inv;
+        const F2 ms = f2(m, m), rs = f2(rstd[r], rstd[r]);
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+          if (!in[j]) continue;
+          F2 more[NP];
+          if (arrays == 3) to_pairs<T>(data[((r * NV + j) * 3 + 2) * kThreadsMost], more);
+          float d[E];
+#pragma unroll
+          for (int h = 0; h < NP; ++h) {
+            F2 x = mul(fma(xh[r][j][h], ms, ga[r][j][h]), rs);
+            if (arrays == 3) x = add(x, more[h]);
+            split(x, d[2 * h], d[2 * h + 1]);
+          }
+          store_pack<T, E>((T*)a.y + (row + r) * a.ys + (t + j * threads) * E, d);
+        }
+      }
+    }
+    stage = stage + 1 == kAhead ? 0 : stage + 1;
+  }
+  next_may_launch();
+  if (!a.part) return;
+  // the groups' sums in group order, through the rows' memory
+  float* out = a.part + (long long)blockIdx.x * a.dim;
+  float* cols = reinterpret_cast<float*>(staged);
+  asm volatile("cp.async.wait_group 0;" ::: "memory");
+  for (int y = 0; y < (int)blockDim.y; ++y) {
+    __syncthreads();
+    if (group != y) continue;
+    float* dst = y + 1 < (int)blockDim.y ? cols : out;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      if (!in[j]) continue;
+      const int c = (t + j * threads) * E;
+#pragma unroll
+      for (int h = 0; h < NP; ++h) {
+        float u, v;
+        split(dw[j][h], u, v);
+        if (y) {
+          u += cols[c + 2 * h];
+          v += cols[c + 2 * h + 1];
+        }
+        *reinterpret_cast<float2*>(dst + c + 2 * h) = make_float2(u, v);
+      }
+    }
+  }
+}
+
 // Rows too long for registers: one CTA a row, a warp a block of 128 at a time; read again (from L2) for the result.
 __device__ __forceinline__ float cta_sum(float v, float* buf) {
   v = warp_sum(v);
@@ -449,6 +719,8 @@ template <typename F> void by_dtype(int32_t d, F&& f) {
   }
 }
 template <int N> using Int = std::integral_constant<int, N>;
+// A turn's memory: at most four units of a row (of 16 bytes), of two arrays or (backward) two of three, for each thread.
+constexpr int kMostStaged = kAhead * 8 * kThreadsMost * 16;
 
 // Threads of a group, groups of a CTA and units of a thread (0: the row is too long).
 struct Plan {
@@ -467,16 +739,37 @@ Plan plan_of(long long dim, int e) {
   }
   return p;
 }
-template <typename T, typename F> void by_plan(bool vec, const Plan& p, F&& f) {
-  constexpr int V = Vec16<T>::N;
-  auto with = [&](auto v) {
-    constexpr int E = decltype(v)::value == 1 ? 4 : decltype(v)::value;
-    if (p.nv == 1) f(v, Int<1>());
-    else if (p.nv == 2) f(v, Int<2>());
-    else if constexpr (E * 4 <= kElements) f(v, Int<4>());
-  };
-  if (vec) with(Int<V>());
-  else with(Int<1>());
+// f(units of a thread, rows of a turn) for rows of whole units: `r1` rows where a thread has one unit of each, or one
+// row where there are few; f(units) for any rows.
+template <typename T, int R1, typename F> void by_vec_plan(const Plan& p, bool few, F&& f) {
+  if (p.nv == 1) few ? f(Int<1>(), Int<1>()) : f(Int<1>(), Int<R1>());
+  else if (p.nv == 2) f(Int<2>(), Int<R1 / 2>());
+  else if constexpr (Vec16<T>::N * 4 <= kElements) f(Int<4>(), Int<1>());
+}
+template <typename F> void by_any_plan(const Plan& p, F&& f) {
+  if (p.nv == 1) f(Int<1>());
+  else if (p.nv == 2) f(Int<2>());
+  else f(Int<4>());
+}
+// Rows in one turn of a launch of one CTA an SM, and its CTAs.
+unsigned turns_of(const Plan& p, int r, long long rows, int sms) {
+  return (unsigned)std::min<long long>(units(rows, (long long)p.groups * r), sms);
+}
+template <typename K> cudaError_t launch_vec(K kernel, std::atomic<unsigned long long>& raised, const Plan& p, int stage_units, unsigned grid,
+                                             int device, cudaStream_t st, const RmsArgs& a) {
+  const cudaError_t e = raise_smem(kernel, raised, device, kMostStaged);
+  if (e != cudaSuccess) return e;
+  return launch_early(kernel, grid, dim3(p.threads, p.groups), (size_t)kAhead * stage_units * kThreadsMost * 16, 1, st, a);
+}
+template <typename T, int NV, int R>
+cudaError_t forward_vec(const RmsArgs& a, const Plan& p, int sms, int device, cudaStream_t st) {
+  static std::atomic<unsigned long long> raised{0};
+  return launch_vec(k_rms_forward_vec<T, NV, R>, raised, p, R * NV * (a.residual ? 2 : 1), turns_of(p, R, a.rows, sms), device, st, a);
+}
+template <typename T, int NV, int R, bool SAVED>
+cudaError_t backward_vec(const RmsArgs& a, const Plan& p, unsigned grid, int device, cudaStream_t st) {
+  static std::atomic<unsigned long long> raised{0};
+  return launch_vec(k_rms_backward_vec<T, NV, R, SAVED>, raised, p, R * NV * (a.residual && a.y ? 3 : 2), grid, device, st, a);
 }
 
 bool vec_ok(const void* p, long long stride, int dtype) {
@@ -608,9 +901,15 @@ extern "C" int psgd_rmsnorm_forward(psgd_rmsnorm* h, const void* x, psgd_dtype d
       e = cudaGetLastError();
       return;
     }
+    if (vec) {
+      by_vec_plan<T, 4>(p, rows <= 4LL * h->sms * p.groups, [&](auto nv, auto r) {
+        e = forward_vec<T, decltype(nv)::value, decltype(r)::value>(a, p, h->sms, h->device, st);
+      });
+      return;
+    }
     const unsigned grid = (unsigned)std::min<long long>(units(rows, p.groups), h->sms * kCtasPerSm);
-    by_plan<T>(vec, p, [&](auto v, auto nv) {
-      e = launch_early(k_rms_forward<T, decltype(v)::value, decltype(nv)::value>, grid, dim3(p.threads, p.groups), 0, 1, st, a);
+    by_any_plan(p, [&](auto nv) {
+      e = launch_early(k_rms_forward<T, 1, decltype(nv)::value>, grid, dim3(p.threads, p.groups), 0, 1, st, a);
     });
   });
   return e == cudaSuccess ? PSGD_OK : cuda_fail(who.c_str(), e);
@@ -676,12 +975,20 @@ extern "C" int psgd_rmsnorm_backward(psgd_rmsnorm* h, const void* grad, psgd_dty
         }
         return;
       }
+      if (vec && p.nv < 4) {  // (three arrays of four units have no room for their turns)
+        by_vec_plan<T, 2>(p, rows <= 4LL * h->sms * p.groups, [&](auto nv, auto r) {
+          constexpr int NV = decltype(nv)::value, R = decltype(r)::value;
+          parts = (int)turns_of(p, R, rows, h->sms);
+          e = codes ? backward_vec<T, NV, R, true>(a, p, parts, h->device, st) : backward_vec<T, NV, R, false>(a, p, parts, h->device, st);
+        });
+        return;
+      }
       parts = (int)std::min<long long>(units(rows, p.groups), h->max_ctas);
       const size_t smem = p.groups > 1 ? (size_t)dim * 4 : 0;
-      by_plan<T>(vec, p, [&](auto v, auto nv) {
+      by_any_plan(p, [&](auto nv) {
         auto go = [&](auto saved) {
-          e = launch_early(k_rms_backward<T, decltype(v)::value, decltype(nv)::value, decltype(saved)::value>, (unsigned)parts,
-                           dim3(p.threads, p.groups), smem, 1, st, a);
+          e = launch_early(k_rms_backward<T, 1, decltype(nv)::value, decltype(saved)::value>, (unsigned)parts, dim3(p.threads, p.groups), smem, 1,
+                           st, a);
         };
         if (codes) go(std::true_type());
         else go(std::false_type());
