@@ -21,66 +21,98 @@ struct EightArgs {
   unsigned char* codes;
   float* scales;
   long long rows;
-  long long pieces;  // blocks of all rows
+  unsigned pieces;   // blocks of all rows
+  unsigned long long by;  // 2^64 / blocks, rounded up (0: one block a row)
   int dim, blocks;
   int e5;
 };
 
-// A thread takes U units of E elements: unit i of thread t is lane t % LANES of block (t / LANES) + i * step.
-template <typename T, int V, int U> __global__ void __launch_bounds__(kThreads8) k_save(EightArgs a) {
-  constexpr int E = V == 1 ? 4 : V, LANES = kBlock8 / E;
+// piece / blocks without a division (exact for 32-bit numbers).
+__device__ __forceinline__ long long row_of(const EightArgs& a, unsigned piece) {
+  return a.rows == 1 ? 0 : a.by ? (long long)__umul64hi(piece, a.by) : piece;
+}
+
+// The largest magnitude's bits, as fp32, among 16 bytes of elements: of 16-bit types two at a time.
+template <typename T> __device__ __forceinline__ unsigned magnitude(const uint4& u) {
+  if constexpr (sizeof(T) == 4) {
+    return max(max(u.x & 0x7fffffffu, u.y & 0x7fffffffu), max(u.z & 0x7fffffffu, u.w & 0x7fffffffu));
+  } else {
+    const unsigned k = 0x7fff7fffu;
+    return __vmaxu2(__vmaxu2(u.x & k, u.y & k), __vmaxu2(u.z & k, u.w & k));
+  }
+}
+template <typename T> __device__ __forceinline__ unsigned wider(unsigned a, unsigned b) {
+  if constexpr (sizeof(T) == 4) return max(a, b);
+  else return __vmaxu2(a, b);
+}
+template <typename T> __device__ __forceinline__ unsigned as_f32(unsigned m) {
+  if constexpr (sizeof(T) == 4) return m;
+  const unsigned short h = (unsigned short)max(m & 0xffffu, m >> 16);
+  if constexpr (std::is_same_v<T, __half>) return __float_as_uint(__half2float(__ushort_as_half(h)));
+  else return (unsigned)h << 16;
+}
+
+// Rows of whole 16-byte units.  A thread takes U of them: unit i of thread t is lane t % LANES of block (t / LANES) +
+// i * step.  What is under way waits in its own type, and the largest magnitude of a block is found in it.  Bound by
+// HBM: 16384 x 4096 bf16 31 us (6.5 TB/s; 55 us with sums and maxima in fp32 and a division a unit).
+template <typename T, bool E5, int U> __global__ void __launch_bounds__(kThreads8) k_save_vec(EightArgs a) {
+  constexpr int E = Vec16<T>::N, LANES = kBlock8 / E;
   const int lane = threadIdx.x & (LANES - 1);
   const long long first = ((long long)blockIdx.x * kThreads8 + threadIdx.x) / LANES;
   const long long step = (long long)gridDim.x * (kThreads8 / LANES);
   after_previous();
   next_may_launch();
-  float v[U][E];
-  long long row[U];
-  int block[U];
+  uint4 raw[U];
 #pragma unroll
   for (int i = 0; i < U; ++i) {
     const long long piece = first + i * step;
-    row[i] = piece < a.pieces ? piece / a.blocks : a.rows;
-    block[i] = (int)(piece - row[i] * a.blocks);
-    const T* src = (const T*)a.x + row[i] * a.xs;
-    const int c = block[i] * kBlock8 + (V == 1 ? lane : lane * E);
-#pragma unroll
-    for (int e = 0; e < E; ++e) v[i][e] = 0.f;
-    if (row[i] == a.rows) continue;
-    if constexpr (V == 1) {
-#pragma unroll
-      for (int e = 0; e < E; ++e)
-        if (c + 32 * e < a.dim) v[i][e] = to_f(__ldg(src + c + 32 * e));
-    } else if (c < a.dim) {
-      const uint4 q = __ldg(reinterpret_cast<const uint4*>(src + c));
-      F2 p[E / 2];
-      to_pairs<T>(q, p);
-#pragma unroll
-      for (int e = 0; e < E / 2; ++e) split(p[e], v[i][2 * e], v[i][2 * e + 1]);
-    }
+    raw[i] = make_uint4(0, 0, 0, 0);
+    if (piece >= a.pieces) continue;
+    const long long row = row_of(a, (unsigned)piece);
+    const int c = (int)(piece - row * a.blocks) * kBlock8 + lane * E;
+    if (c < a.dim) raw[i] = __ldg(reinterpret_cast<const uint4*>((const T*)a.x + row * a.xs + c));
   }
 #pragma unroll
   for (int i = 0; i < U; ++i) {
+    unsigned top = magnitude<T>(raw[i]);
+#pragma unroll
+    for (int o = LANES / 2; o > 0; o >>= 1) top = wider<T>(top, __shfl_xor_sync(0xffffffffu, top, o));
+    top = as_f32<T>(top);
+    F2 p[E / 2];
+    to_pairs<T>(raw[i], p);
     unsigned code[E / 4];
     float scale;
-    encode<E, LANES>(a.e5, v[i], code, scale);
-    if (row[i] == a.rows) continue;
-    unsigned char* dst = a.codes + row[i] * a.dim;
-    const int c = block[i] * kBlock8 + (V == 1 ? lane : lane * E);
-    if constexpr (V == 1) {
+    if (top < 0x7f800000u) {
+      const int e = scale_exponent<E5>(top);
+      const float inv = power2(-e);
+      scale = power2(e);
 #pragma unroll
-      for (int e = 0; e < E; ++e)
-        if (c + 32 * e < a.dim) dst[c + 32 * e] = (unsigned char)(code[0] >> (8 * e));
-    } else if (c < a.dim) {
-      if constexpr (E == 8) *reinterpret_cast<uint2*>(dst + c) = make_uint2(code[0], code[1]);
-      else *reinterpret_cast<unsigned*>(dst + c) = code[0];
+      for (int k = 0; k < E / 4; ++k) {
+        float v[4];
+        split(mul(p[2 * k], f2(inv, inv)), v[0], v[1]);
+        split(mul(p[2 * k + 1], f2(inv, inv)), v[2], v[3]);
+        code[k] = codes2<E5>(v[0], v[1]) | codes2<E5>(v[2], v[3]) << 16;
+      }
+    } else {  // something infinite or NaN (for all lanes of the block)
+      float v[E];
+#pragma unroll
+      for (int k = 0; k < E / 2; ++k) split(p[k], v[2 * k], v[2 * k + 1]);
+      encode_special<E, LANES, E5>(v, code, scale);
     }
-    if (lane == 0) a.scales[row[i] * a.blocks + block[i]] = scale;
+    const long long piece = first + i * step;
+    if (piece >= a.pieces) continue;
+    const long long row = row_of(a, (unsigned)piece);
+    const int block = (int)(piece - row * a.blocks), c = block * kBlock8 + lane * E;
+    if (c >= a.dim) continue;
+    unsigned char* dst = a.codes + row * a.dim + c;
+    if constexpr (E == 8) *reinterpret_cast<uint2*>(dst) = make_uint2(code[0], code[1]);
+    else *reinterpret_cast<unsigned*>(dst) = code[0];
+    if (lane == 0) a.scales[row * a.blocks + block] = scale;
   }
 }
 
-template <typename T, int V, int U> __global__ void __launch_bounds__(kThreads8) k_restore(EightArgs a) {
-  constexpr int E = V == 1 ? 4 : V, LANES = kBlock8 / E;
+template <typename T, bool E5, int U> __global__ void __launch_bounds__(kThreads8) k_restore_vec(EightArgs a) {
+  constexpr int E = Vec16<T>::N, LANES = kBlock8 / E;
   const int lane = threadIdx.x & (LANES - 1);
   const long long first = ((long long)blockIdx.x * kThreads8 + threadIdx.x) / LANES;
   const long long step = (long long)gridDim.x * (kThreads8 / LANES);
@@ -88,49 +120,82 @@ template <typename T, int V, int U> __global__ void __launch_bounds__(kThreads8)
   next_may_launch();
   unsigned code[U][E / 4];
   float scale[U];
-  long long row[U];
-  int block[U];
+  T* dst[U];
 #pragma unroll
   for (int i = 0; i < U; ++i) {
     const long long piece = first + i * step;
-    row[i] = piece < a.pieces ? piece / a.blocks : a.rows;
-    block[i] = (int)(piece - row[i] * a.blocks);
-    const unsigned char* src = a.codes + row[i] * a.dim;
-    const int c = block[i] * kBlock8 + (V == 1 ? lane : lane * E);
-#pragma unroll
-    for (int e = 0; e < E / 4; ++e) code[i][e] = 0;
-    scale[i] = 1.f;
-    if (row[i] == a.rows) continue;
-    scale[i] = __ldg(a.scales + row[i] * a.blocks + block[i]);
-    if constexpr (V == 1) {
-#pragma unroll
-      for (int e = 0; e < E; ++e)
-        if (c + 32 * e < a.dim) code[i][0] |= (unsigned)__ldg(src + c + 32 * e) << (8 * e);
-    } else if (c < a.dim) {
-      if constexpr (E == 8) {
-        const uint2 q = __ldg(reinterpret_cast<const uint2*>(src + c));
-        code[i][0] = q.x;
-        code[i][1] = q.y;
-      } else {
-        code[i][0] = __ldg(reinterpret_cast<const unsigned*>(src + c));
-      }
+    dst[i] = nullptr;
+    if (piece >= a.pieces) continue;
+    const long long row = row_of(a, (unsigned)piece);
+    const int block = (int)(piece - row * a.blocks), c = block * kBlock8 + lane * E;
+    if (c >= a.dim) continue;
+    dst[i] = (T*)const_cast<void*>(a.x) + row * a.xs + c;
+    scale[i] = __ldg(a.scales + row * a.blocks + block);
+    const unsigned char* src = a.codes + row * a.dim + c;
+    if constexpr (E == 8) {
+      const uint2 q = __ldg(reinterpret_cast<const uint2*>(src));
+      code[i][0] = q.x;
+      code[i][1] = q.y;
+    } else {
+      code[i][0] = __ldg(reinterpret_cast<const unsigned*>(src));
     }
   }
 #pragma unroll
   for (int i = 0; i < U; ++i) {
-    if (row[i] == a.rows) continue;
+    if (!dst[i]) continue;
     float f[E];
 #pragma unroll
-    for (int e = 0; e < E / 4; ++e) decode4(a.e5, code[i][e], scale[i], f + 4 * e);
-    T* dst = (T*)const_cast<void*>(a.x) + row[i] * a.xs;
-    const int c = block[i] * kBlock8 + (V == 1 ? lane : lane * E);
-    if constexpr (V == 1) {
+    for (int e = 0; e < E / 4; ++e) decode4(E5, code[i][e], scale[i], f + 4 * e);
+    store_pack<T, E>(dst[i], f);
+  }
+}
+
+// Rows of any length and alignment: a warp a block, lane by lane, U blocks of a warp.
+template <typename T, bool SAVE, int U> __global__ void __launch_bounds__(kThreads8) k_eight_any(EightArgs a) {
+  const int lane = threadIdx.x & 31;
+  const long long first = ((long long)blockIdx.x * kThreads8 + threadIdx.x) / 32, step = (long long)gridDim.x * (kThreads8 / 32);
+  after_previous();
+  next_may_launch();
+  T* x = (T*)const_cast<void*>(a.x);
+  float v[U][4];
+  unsigned code[U];
+  float scale[U];
+  long long row[U];
+  int c[U];
 #pragma unroll
-      for (int e = 0; e < E; ++e)
-        if (c + 32 * e < a.dim) dst[c + 32 * e] = from_f<T>(f[e]);
-    } else if (c < a.dim) {
-      store_pack<T, V>(dst + c, f);
+  for (int i = 0; i < U; ++i) {
+    const long long piece = first + i * step;
+    row[i] = piece < a.pieces ? row_of(a, (unsigned)piece) : -1;
+    const int block = (int)(piece - row[i] * a.blocks);
+    c[i] = block * kBlock8 + lane;
+    code[i] = 0;
+    scale[i] = 1.f;
+    if (!SAVE && row[i] >= 0) scale[i] = __ldg(a.scales + row[i] * a.blocks + block);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      v[i][e] = 0.f;
+      if (row[i] < 0 || c[i] + 32 * e >= a.dim) continue;
+      if constexpr (SAVE) v[i][e] = to_f(__ldg(x + row[i] * a.xs + c[i] + 32 * e));
+      else code[i] |= (unsigned)__ldg(a.codes + row[i] * a.dim + c[i] + 32 * e) << (8 * e);
     }
+  }
+#pragma unroll
+  for (int i = 0; i < U; ++i) {
+    if constexpr (SAVE) {
+      unsigned packed[1];
+      encode<4, 32>(a.e5, v[i], packed, scale[i]);
+      code[i] = packed[0];
+    } else {
+      decode4(a.e5, code[i], scale[i], v[i]);
+    }
+    if (row[i] < 0) continue;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      if (c[i] + 32 * e >= a.dim) continue;
+      if constexpr (SAVE) a.codes[row[i] * a.dim + c[i] + 32 * e] = (unsigned char)(code[i] >> (8 * e));
+      else x[row[i] * a.xs + c[i] + 32 * e] = from_f<T>(v[i][e]);
+    }
+    if (SAVE && lane == 0) a.scales[row[i] * a.blocks + c[i] / kBlock8] = scale[i];
   }
 }
 
@@ -150,13 +215,13 @@ int check(const std::string& who, const void* x, int32_t dtype, int64_t stride, 
   return PSGD_OK;
 }
 
-template <bool SAVE, typename T, int V>
-cudaError_t go(EightArgs a, cudaStream_t st) {
-  constexpr int E = V == 1 ? 4 : V, LANES = kBlock8 / E, U = 2;
-  const long long per = kThreads8 / LANES * U;
-  // (a grid of at most 2^31 - 1 CTAs holds 2^46 / 128 blocks of one CTA's 16 or 32)
-  const unsigned grid = (unsigned)units(a.pieces, per);
-  return launch_early(SAVE ? k_save<T, V, U> : k_restore<T, V, U>, grid, kThreads8, 0, 1, st, a);
+template <bool SAVE, typename T> cudaError_t go(const EightArgs& a, bool vec, cudaStream_t st) {
+  constexpr int U = 4;
+  const long long lanes = vec ? kBlock8 / Vec16<T>::N : 32;
+  const unsigned grid = (unsigned)units(a.pieces, kThreads8 / lanes * U);
+  if (!vec) return launch_early(k_eight_any<T, SAVE, U>, grid, kThreads8, 0, 1, st, a);
+  if constexpr (SAVE) return launch_early(a.e5 ? k_save_vec<T, true, U> : k_save_vec<T, false, U>, grid, kThreads8, 0, 1, st, a);
+  else return launch_early(a.e5 ? k_restore_vec<T, true, U> : k_restore_vec<T, false, U>, grid, kThreads8, 0, 1, st, a);
 }
 
 template <bool SAVE> int run(const std::string& who, const void* x, int32_t dtype, int64_t stride, int64_t rows, int64_t dim,
@@ -164,17 +229,23 @@ template <bool SAVE> int run(const std::string& who, const void* x, int32_t dtyp
   const int rc = check(who, x, dtype, stride, rows, dim, codes, code, scales, SAVE, device);
   if (rc) return rc;
   if (rows == 0) return PSGD_OK;
+  // rows without gaps of whole blocks are one long row
+  if (dim % kBlock8 == 0 && (stride == dim || rows == 1) && rows * dim < (1LL << 30)) {
+    dim *= rows;
+    rows = 1;
+    stride = dim;
+  }
   const long long blocks = blocks8(dim);
-  if (units(rows * blocks, 16) > 0x7fffffffLL) return fail(PSGD_EINVAL, who + ": too many elements");
+  if (rows * blocks > 0xffffffffLL) return fail(PSGD_EINVAL, who + ": too many elements");
   DeviceScope scope(device);
-  EightArgs a{x, stride, (unsigned char*)codes, scales, rows, rows * blocks, (int)dim, (int)blocks, code == PSGD_E5M2};
+  EightArgs a{x, stride, (unsigned char*)codes, scales, rows, (unsigned)(rows * blocks),
+              blocks == 1 ? 0 : ~0ull / (unsigned long long)blocks + 1, (int)dim, (int)blocks, code == PSGD_E5M2};
   const cudaStream_t st = (cudaStream_t)stream;
   const int full = 16 / dtype_size(dtype);
   const bool vec = dim % full == 0 && aligned16(x) && (stride * dtype_size(dtype)) % 16 == 0 && (uintptr_t)codes % full == 0;
-  cudaError_t e;
-  if (dtype == PSGD_F32) e = vec ? go<SAVE, float, 4>(a, st) : go<SAVE, float, 1>(a, st);
-  else if (dtype == PSGD_F16) e = vec ? go<SAVE, __half, 8>(a, st) : go<SAVE, __half, 1>(a, st);
-  else e = vec ? go<SAVE, __nv_bfloat16, 8>(a, st) : go<SAVE, __nv_bfloat16, 1>(a, st);
+  const cudaError_t e = dtype == PSGD_F32   ? go<SAVE, float>(a, vec, st)
+                        : dtype == PSGD_F16 ? go<SAVE, __half>(a, vec, st)
+                                            : go<SAVE, __nv_bfloat16>(a, vec, st);
   return e == cudaSuccess ? PSGD_OK : cuda_fail(who.c_str(), e);
 }
 

@@ -55,25 +55,11 @@ template <int LANES> __device__ __forceinline__ unsigned lanes_max(unsigned m) {
   return m;
 }
 
-// Codes of a block's N values (N = 4 or 8) of this lane, packed from the low byte on, and
-// the block's scale.  LANES lanes hold the block.
+// Codes of a block's N values (N = 4 or 8) of this lane, packed from the low byte on, and the block's scale, where
+// something in the block is infinite or NaN: the scale is that of the others.  All of the block's LANES lanes are here,
+// of a warp's other block perhaps none, so the lanes are named.
 template <int N, int LANES, bool E5>
-__device__ __forceinline__ void encode(const float (&v)[N], unsigned (&packed)[N / 4], float& scale) {
-  unsigned all = 0;
-#pragma unroll
-  for (int i = 0; i < N; ++i) all = max(all, __float_as_uint(v[i]) & 0x7fffffffu);
-  all = lanes_max<LANES>(all);
-  if (all < 0x7f800000u) {
-    const int e = scale_exponent<E5>(all);
-    const float inv = power2(-e);
-    scale = power2(e);
-#pragma unroll
-    for (int i = 0; i < N / 4; ++i)
-      packed[i] = codes2<E5>(v[4 * i] * inv, v[4 * i + 1] * inv) | codes2<E5>(v[4 * i + 2] * inv, v[4 * i + 3] * inv) << 16;
-    return;
-  }
-  // something infinite or NaN: the scale is that of the others.  All lanes of the block are here, of a warp's other
-  // block perhaps none, so the lanes are named
+__device__ __forceinline__ void encode_special(const float (&v)[N], unsigned (&packed)[N / 4], float& scale) {
   unsigned top = 0;
 #pragma unroll
   for (int i = 0; i < N; ++i) {
@@ -92,6 +78,25 @@ __device__ __forceinline__ void encode(const float (&v)[N], unsigned (&packed)[N
 #pragma unroll
     for (int k = 0; k < 4; ++k) packed[i] |= (unsigned)code_any<E5>(v[4 * i + k], inv) << (8 * k);
   }
+}
+
+// The same where all is finite, or perhaps not.
+template <int N, int LANES, bool E5>
+__device__ __forceinline__ void encode(const float (&v)[N], unsigned (&packed)[N / 4], float& scale) {
+  unsigned all = 0;
+#pragma unroll
+  for (int i = 0; i < N; ++i) all = max(all, __float_as_uint(v[i]) & 0x7fffffffu);
+  all = lanes_max<LANES>(all);
+  if (all >= 0x7f800000u) {
+    encode_special<N, LANES, E5>(v, packed, scale);
+    return;
+  }
+  const int e = scale_exponent<E5>(all);
+  const float inv = power2(-e);
+  scale = power2(e);
+#pragma unroll
+  for (int i = 0; i < N / 4; ++i)
+    packed[i] = codes2<E5>(v[4 * i] * inv, v[4 * i + 1] * inv) | codes2<E5>(v[4 * i + 2] * inv, v[4 * i + 3] * inv) << 16;
 }
 template <int N, int LANES>
 __device__ __forceinline__ void encode(bool e5, const float (&v)[N], unsigned (&packed)[N / 4], float& scale) {

@@ -313,9 +313,11 @@ __global__ void __launch_bounds__(kThreadsMost, (Unit<T, V>::E * NV < kElements 
 // of one reduction; the rows of the next two turns are copied ahead into shared memory, by the thread that will use
 // them, so that neither a register nor a barrier waits for what is under way.
 constexpr int kAhead = 3;  // turns: the one in use and those under way
+// CTAs of an SM: two where a turn's rows leave the room (and 64 registers a thread suffice).
+constexpr int ctas_of(int nv, int r) { return nv == 1 && r <= 2 ? 2 : 1; }
 
 template <typename T, int NV, int R>
-__global__ void __launch_bounds__(kThreadsMost, 1) k_rms_forward_vec(RmsArgs a) {
+__global__ void __launch_bounds__(kThreadsMost, ctas_of(NV, R)) k_rms_forward_vec(RmsArgs a) {
   constexpr int E = Vec16<T>::N, NP = E / 2;
   extern __shared__ __align__(16) uint4 staged[];
   __shared__ float red[2][kThreadsMost / 32 * R];
@@ -743,7 +745,7 @@ Plan plan_of(long long dim, int e) {
 // row where there are few; f(units) for any rows.
 template <typename T, int R1, typename F> void by_vec_plan(const Plan& p, bool few, F&& f) {
   if (p.nv == 1) few ? f(Int<1>(), Int<1>()) : f(Int<1>(), Int<R1>());
-  else if (p.nv == 2) f(Int<2>(), Int<R1 / 2>());
+  else if (p.nv == 2) f(Int<2>(), Int<(R1 + 1) / 2>());
   else if constexpr (Vec16<T>::N * 4 <= kElements) f(Int<4>(), Int<1>());
 }
 template <typename F> void by_any_plan(const Plan& p, F&& f) {
@@ -764,7 +766,7 @@ template <typename K> cudaError_t launch_vec(K kernel, std::atomic<unsigned long
 template <typename T, int NV, int R>
 cudaError_t forward_vec(const RmsArgs& a, const Plan& p, int sms, int device, cudaStream_t st) {
   static std::atomic<unsigned long long> raised{0};
-  return launch_vec(k_rms_forward_vec<T, NV, R>, raised, p, R * NV * (a.residual ? 2 : 1), turns_of(p, R, a.rows, sms), device, st, a);
+  return launch_vec(k_rms_forward_vec<T, NV, R>, raised, p, R * NV * (a.residual ? 2 : 1), turns_of(p, R, a.rows, sms * ctas_of(NV, R)), device, st, a);
 }
 template <typename T, int NV, int R, bool SAVED>
 cudaError_t backward_vec(const RmsArgs& a, const Plan& p, unsigned grid, int device, cudaStream_t st) {
@@ -902,7 +904,7 @@ extern "C" int psgd_rmsnorm_forward(psgd_rmsnorm* h, const void* x, psgd_dtype d
       return;
     }
     if (vec) {
-      by_vec_plan<T, 4>(p, rows <= 4LL * h->sms * p.groups, [&](auto nv, auto r) {
+      by_vec_plan<T, 2>(p, rows <= 4LL * h->sms * p.groups, [&](auto nv, auto r) {
         e = forward_vec<T, decltype(nv)::value, decltype(r)::value>(a, p, h->sms, h->device, st);
       });
       return;
