@@ -28,9 +28,10 @@
 struct psgd_linear_ce {
   int device = 0, pairs = 0;
   long long vocab = 0, dim = 0, most = 0;
-  long long dp = 0;          // row stride of h and W in the workspace: dim up to a multiple of 8
+  long long dp = 0;          // row stride of h, W and dh in the workspace
   long long cap = 0;         // rows of the workspace: max_tokens up to a multiple of 256
   long long piece = 0;       // columns of the vocabulary that G holds, a multiple of 256
+  long long gp = 0;          // row stride of G
   void *h = nullptr, *hs = nullptr;  // the tokens that count, and them times 2^(e - max e)
   void* w = nullptr;         // a piece of a weight that TMA cannot read in place
   void* g = nullptr;
@@ -448,11 +449,12 @@ extern "C" int psgd_linear_ce_create(int64_t vocab, int64_t dim, int64_t max_tok
   h->vocab = vocab;
   h->dim = dim;
   h->most = max_tokens;
-  h->dp = units(dim, 8) * 8;
+  h->dp = mma::row_stride(dim);
   h->cap = std::max(1LL, units(max_tokens, mma::kTile)) * mma::kTile;
   // equal pieces of whole tiles
   const long long tiles = units(vocab, mma::kTile), fit = std::max(1LL, kPieceBytes / (h->cap * mma::kTile * 2));
   h->piece = units(tiles, units(tiles, fit)) * mma::kTile;
+  h->gp = mma::row_stride(h->piece);
   e = mma::pairs_of(device, &h->pairs);
   const auto get = [&](auto** p, long long bytes) {
     if (e == cudaSuccess) e = cudaMalloc((void**)p, bytes);
@@ -462,7 +464,7 @@ extern "C" int psgd_linear_ce_create(int64_t vocab, int64_t dim, int64_t max_tok
   get(&h->h, h->cap * h->dp * 2);
   get(&h->hs, h->cap * h->dp * 2);
   get(&h->w, h->piece * h->dp * 2);
-  get(&h->g, h->cap * h->piece * 2);
+  get(&h->g, h->cap * h->gp * 2);
   get(&h->dh, h->cap * h->dp * 4);
   get(&h->slots, 2 * h->pairs * mma::kSlotFloats * 4);
   get(&h->part, (units(vocab, mma::kTile / 2) + units(vocab, h->piece)) * h->cap * 8);  // (tiles have 128 columns at least)
@@ -567,11 +569,11 @@ extern "C" int psgd_linear_ce_backward(psgd_linear_ce* h, const void* hidden, ps
     mma::Product z = c.logits(v0, n), dh{}, dw{};
     c.weight_map(mma::kGrad, z, &dh.b, v0, n);
     z.lse = h->lse, z.factor = h->factor;
-    if (c.e == cudaSuccess) c.e = mma::make_map(&z.store, h->g, h->cap, h->piece, h->piece, 32, c.bf16);
+    if (c.e == cudaSuccess) c.e = mma::make_map(&z.store, h->g, h->cap, h->piece, h->gp, 32, c.bf16);
     if (c.e == cudaSuccess && tokens > 0) c.e = mma::enqueue(mma::kGrad, z, h->device, h->pairs, c.st);
     if (dhidden && tokens > 0) {
-      if (c.e == cudaSuccess) c.e = mma::make_map(&dh.a, h->g, h->cap, h->piece, h->piece, mma::box_rows(false), c.bf16);
-      if (c.e == cudaSuccess) c.e = mma::make_map(&dh.a_few, h->g, h->cap, h->piece, h->piece, mma::kFew, c.bf16);
+      if (c.e == cudaSuccess) c.e = mma::make_map(&dh.a, h->g, h->cap, h->piece, h->gp, mma::box_rows(false), c.bf16);
+      if (c.e == cudaSuccess) c.e = mma::make_map(&dh.a_few, h->g, h->cap, h->piece, h->gp, mma::kFew, c.bf16);
       dh.m = (int)tokens, dh.n = (int)h->dim, dh.k = (int)n;
       dh.live = h->count, dh.live_is = 1;
       dh.b_m_rows = 1, dh.b_y0 = z.b_y0;
@@ -581,7 +583,7 @@ extern "C" int psgd_linear_ce_backward(psgd_linear_ce* h, const void* hidden, ps
       if (c.e == cudaSuccess) c.e = mma::enqueue(mma::kOut, dh, h->device, h->pairs, c.st);
     }
     if (dweight) {
-      if (c.e == cudaSuccess) c.e = mma::make_map(&dw.a, h->g, h->cap, h->piece, h->piece, mma::box_rows(true), c.bf16);
+      if (c.e == cudaSuccess) c.e = mma::make_map(&dw.a, h->g, h->cap, h->piece, h->gp, mma::box_rows(true), c.bf16);
       if (c.e == cudaSuccess) c.e = mma::make_map(&dw.b, h->hs, h->cap, h->dim, h->dp, mma::box_rows(true), c.bf16);
       dw.m = (int)n, dw.n = (int)h->dim, dw.k = (int)tokens;
       dw.live = h->count, dw.live_is = 2;

@@ -256,6 +256,10 @@ enum Epilogue { kLse = 0, kGrad = 1, kOut = 2 };
 cudaError_t make_map(CUtensorMap* map, const void* p, long long rows, long long cols, long long stride, int box_rows, bool bf16);
 inline int box_rows(bool m_rows) { return m_rows ? kStep : kHalf; }
 
+// Elements from row to row of a matrix of 16-bit elements in a workspace: an odd number of lines of 128 bytes, so that
+// the lines that a box of many rows reads lie in all parts of L2 (GPT-2-XL's gradients 2150 -> 2121 us, the product
+// over 300 tokens of BERT-large's vocabulary 46 -> 41).
+inline long long row_stride(long long cols) { return (ops::units(cols, 64) | 1) * 64; }
 // Pairs of CTAs that a device holds at once.
 cudaError_t pairs_of(int device, int* pairs);
 // Columns of the tiles of an LSE or GRAD product over n columns; B's boxes have half as many rows.
