@@ -328,19 +328,6 @@ __global__ void __launch_bounds__(kMaxThreads, 1) k_norm_backward_vec(RowsArgs a
 // instructions that takes: backward 30001 x 1023 fp16 45 us (4.1 TB/s), fp32 67 us
 // (5.5 TB/s).  A barrier of the group follows each wait, as a granule is used by
 // other threads than the one that copied it.
-//
-// How the warps of a group share the copies of `items` rows: warp w takes the
-// items first, first + step, ..., and of each the granules of part `part` of
-// `parts`.
-struct CopyShare {
-  int first, step, part, parts;
-  __device__ __forceinline__ CopyShare(int items, int warps, int warp) {
-    parts = warps >= items ? warps / items : 1;
-    first = parts > 1 ? warp / parts : warp;
-    part = parts > 1 ? warp - first * parts : 0;
-    step = parts > 1 ? items : warps;  // (with parts, warps that are left over have first >= items)
-  }
-};
 
 // `a` where `keep` is not 0, else 0 (not a product: what lies behind a row may
 // be anything).
@@ -351,14 +338,6 @@ __device__ __forceinline__ F2 only(F2 a, F2 keep) {
   return f2(k != 0.f ? x : 0.f, l != 0.f ? y : 0.f);
 }
 
-__device__ __forceinline__ void group_barrier(int group, int threads) {
-  asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "r"(threads) : "memory");
-}
-
-// Where in its first granule row `index` of an array begins, in bytes.
-__device__ __forceinline__ int row_phase(const void* base, int index, long long stride, int size) {
-  return ((unsigned)(uintptr_t)base + (unsigned)index * ((unsigned)stride * (unsigned)size)) & 15;
-}
 // Elements 0 and 32 from a place in a row in shared memory, as a pair; they may
 // lie behind the row's end, where the slot's last bytes are read.
 template <typename T> __device__ __forceinline__ F2 pair_at(const T* row) { return f2(to_f(row[0]), to_f(row[32])); }

@@ -33,7 +33,7 @@ namespace ops {
 namespace {
 
 constexpr int kThreadsMost = kRowThreads;  // of a CTA
-constexpr int kCtasPerSm = 2;      // at most; one where a thread holds 16 elements of a row
+constexpr int kPartsPerSm = 2;     // partial rows of dw, at most
 constexpr int kElements = 16;      // of a row that a thread holds, at most
 
 struct RmsArgs {
@@ -54,259 +54,28 @@ struct RmsArgs {
   float eps;
 };
 
-// How a thread's columns lie.  V > 1: unit j of thread t is the 16 bytes t + j * threads of a row.  V = 1, rows of
-// any alignment: a warp's unit is a block of 128 columns, lane by lane.  Either way the lanes of a block of 128 are
-// neighbours.
-template <typename T, int V> struct Unit {
-  static constexpr int E = V == 1 ? 4 : V;              // elements
-  static constexpr int LANES = kBlock8 / E;             // lanes of a block
-  int first;  // column of element 0 of unit 0
-  int step;   // columns between units
-  __device__ __forceinline__ Unit(int t, int threads)
-      : first(V == 1 ? (t >> 5) * kBlock8 + (t & 31) : t * V), step(V == 1 ? threads / 32 * kBlock8 : threads * V) {}
-  __device__ __forceinline__ int col(int j, int e) const { return first + j * step + (V == 1 ? 32 * e : e); }
-  // V > 1: a unit is in the row or not (a row is whole units)
-  __device__ __forceinline__ bool in(int j, int e, int dim) const { return col(j, V == 1 ? e : 0) < dim; }
-};
-
-// A unit's raw elements, so that a load may be under way while nothing waits for it.
-template <typename T, int V> struct Raw {
-  static constexpr int E = Unit<T, V>::E;
-  std::conditional_t<V == 1, T, uint4> v[V == 1 ? E : 1];
-  __device__ __forceinline__ void load(const T* row, const Unit<T, V>& u, int j, int dim) {
-    if constexpr (V == 1) {
+// Rows of any length and alignment: a warp's unit is a block of 128 columns, four a lane, 32 apart.
+__device__ __forceinline__ void load_unit(const void* w, int dtype, int c, int dim, float none, float (&f)[4]) {
 #pragma unroll
-      for (int e = 0; e < E; ++e)
-        if (u.in(j, e, dim)) v[e] = row[u.col(j, e)];
-        else v[e] = from_f<T>(0.f);
-    } else {
-      v[0] = u.in(j, 0, dim) ? *reinterpret_cast<const uint4*>(row + u.col(j, 0)) : make_uint4(0, 0, 0, 0);
-    }
-  }
-  __device__ __forceinline__ void get(float (&f)[E]) const {
-    if constexpr (V == 1) {
-#pragma unroll
-      for (int e = 0; e < E; ++e) f[e] = to_f(v[e]);
-    } else {
-      F2 p[E / 2];
-      to_pairs<T>(v[0], p);
-#pragma unroll
-      for (int i = 0; i < E / 2; ++i) split(p[i], f[2 * i], f[2 * i + 1]);
-    }
-  }
-};
-template <typename T, int V>
-__device__ __forceinline__ void put(T* row, const Unit<T, V>& u, int j, int dim, const float (&f)[Unit<T, V>::E]) {
-  if constexpr (V == 1) {
-#pragma unroll
-    for (int e = 0; e < 4; ++e)
-      if (u.in(j, e, dim)) row[u.col(j, e)] = from_f<T>(f[e]);
-  } else {
-    if (u.in(j, 0, dim)) store_pack<T, V>(row + u.col(j, 0), f);
-  }
+  for (int e = 0; e < 4; ++e) f[e] = c + 32 * e < dim ? (w ? load_any(w, dtype, c + 32 * e) : none) : 0.f;
 }
-// Codes of a unit: E bytes side by side (V > 1; the address is a multiple of E), or one by one.
-template <typename T, int V> struct RawCodes {
-  static constexpr int E = Unit<T, V>::E;
-  unsigned v[E / 4];
+template <typename T> __device__ __forceinline__ void load_unit(const T* row, int c, int dim, float (&f)[4]) {
+#pragma unroll
+  for (int e = 0; e < 4; ++e) f[e] = c + 32 * e < dim ? to_f(row[c + 32 * e]) : 0.f;
+}
+template <typename T> __device__ __forceinline__ void put_unit(T* row, int c, int dim, const float (&f)[4]) {
+#pragma unroll
+  for (int e = 0; e < 4; ++e)
+    if (c + 32 * e < dim) row[c + 32 * e] = from_f<T>(f[e]);
+}
+__device__ __forceinline__ void put_codes(unsigned char* row, float* scales, int c, int dim, bool e5, const float (&f)[4]) {
+  unsigned code[1];
   float scale;
-  __device__ __forceinline__ void load(const unsigned char* row, const float* scales, const Unit<T, V>& u, int j, int dim) {
-    scale = u.in(j, 0, dim) ? __ldg(scales + u.col(j, 0) / kBlock8) : 1.f;
-    if constexpr (V == 1) {
-      v[0] = 0;
+  encode<4, 32>(e5, f, code, scale);
 #pragma unroll
-      for (int e = 0; e < 4; ++e)
-        if (u.in(j, e, dim)) v[0] |= (unsigned)__ldg(row + u.col(j, e)) << (8 * e);
-    } else if constexpr (E == 8) {
-      const uint2 c = u.in(j, 0, dim) ? __ldg(reinterpret_cast<const uint2*>(row + u.col(j, 0))) : make_uint2(0, 0);
-      v[0] = c.x;
-      v[1] = c.y;
-    } else {
-      v[0] = u.in(j, 0, dim) ? __ldg(reinterpret_cast<const unsigned*>(row + u.col(j, 0))) : 0u;
-    }
-  }
-  __device__ __forceinline__ void get(bool e5, float (&f)[E]) const {
-#pragma unroll
-    for (int i = 0; i < E / 4; ++i) decode4(e5, v[i], scale, f + 4 * i);
-  }
-};
-template <typename T, int V>
-__device__ __forceinline__ void put_codes(unsigned char* row, float* scales, const Unit<T, V>& u, int j, int dim,
-                                          const unsigned (&c)[Unit<T, V>::E / 4], float scale) {
-  if constexpr (V == 1) {
-#pragma unroll
-    for (int e = 0; e < 4; ++e)
-      if (u.in(j, e, dim)) row[u.col(j, e)] = (unsigned char)(c[0] >> (8 * e));
-  } else if (u.in(j, 0, dim)) {
-    if constexpr (Unit<T, V>::E == 8) *reinterpret_cast<uint2*>(row + u.col(j, 0)) = make_uint2(c[0], c[1]);
-    else *reinterpret_cast<unsigned*>(row + u.col(j, 0)) = c[0];
-  }
-  if ((threadIdx.x & (Unit<T, V>::LANES - 1)) == 0 && u.in(j, 0, dim)) scales[u.col(j, 0) / kBlock8] = scale;
-}
-// A unit of a parameter of any type and alignment (`none` where there is no parameter).
-template <typename T, int V>
-__device__ __forceinline__ void load_weight(const void* w, int dtype, const Unit<T, V>& u, int j, int dim, float (&f)[Unit<T, V>::E]) {
-#pragma unroll
-  for (int e = 0; e < Unit<T, V>::E; ++e) f[e] = u.in(j, e, dim) ? (w ? load_any(w, dtype, u.col(j, e)) : 1.f) : 0.f;
-}
-
-// The sum of v over a group's threads, returned to all of them.  `buf` holds a float per warp of the group; the
-// caller alternates between two of them, so that one barrier a call suffices.
-__device__ __forceinline__ float row_sum(float v, float* buf, int warps, int warp, int lane, int group, int threads) {
-  v = warp_sum(v);
-  if (warps == 1) return v;
-  if (lane == 0) buf[warp] = v;
-  asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "r"(threads) : "memory");
-  return warp_sum(lane < warps ? buf[lane] : 0.f);
-}
-
-template <typename T, int V, int NV>
-__global__ void __launch_bounds__(kThreadsMost, (Unit<T, V>::E * NV < kElements ? kCtasPerSm : 1)) k_rms_forward(RmsArgs a) {
-  constexpr int E = Unit<T, V>::E;
-  __shared__ float red[2][kThreadsMost / 32];
-  const int t = threadIdx.x, group = threadIdx.y, threads = blockDim.x;
-  const int warps = threads / 32, warp = t >> 5, lane = t & 31;
-  const Unit<T, V> u(t, threads);
-  const float inv = 1.f / (float)a.dim;
-  const long long step = (long long)gridDim.x * blockDim.y;
-  long long row = (long long)blockIdx.x * blockDim.y + group;
-  Raw<T, V> x[NV], res[NV];
-  auto fetch = [&](long long r) {
-#pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      x[j].load((const T*)a.x + r * a.xs, u, j, a.dim);
-      if (a.residual) res[j].load((const T*)a.residual + r * a.rs, u, j, a.dim);
-    }
-  };
-  after_previous();
-  next_may_launch();
-  if (row < a.rows) fetch(row);
-  float w[NV][E];
-#pragma unroll
-  for (int j = 0; j < NV; ++j) load_weight<T, V>(a.w, a.pdtype, u, j, a.dim, w[j]);
-  int flip = 0;
-  for (; row < a.rows; row += step, flip ^= 1) {
-    float s[NV][E], sum = 0.f;
-#pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      x[j].get(s[j]);
-      if (a.residual) {
-        float r[E];
-        res[j].get(r);
-#pragma unroll
-        for (int e = 0; e < E; ++e) s[j][e] = to_f(from_f<T>(s[j][e] + r[e]));
-      }
-#pragma unroll
-      for (int e = 0; e < E; ++e) sum = fmaf(s[j][e], s[j][e], sum);
-    }
-    if (row + step < a.rows) fetch(row + step);
-    if (a.summed) {
-#pragma unroll
-      for (int j = 0; j < NV; ++j) put<T, V>((T*)a.summed + row * a.ss, u, j, a.dim, s[j]);
-    }
-    sum = row_sum(sum, red[flip] + group * warps, warps, warp, lane, group, threads);
-    const float rstd = rsqrtf(fmaf(sum, inv, a.eps));
-    if (t == 0) a.rstd[row] = rstd;
-#pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      float y[E];
-#pragma unroll
-      for (int e = 0; e < E; ++e) y[e] = s[j][e] * rstd * w[j][e];
-      if (a.codes) {
-        unsigned c[E / 4];
-        float scale;
-        encode<E, Unit<T, V>::LANES>(a.e5, y, c, scale);
-        put_codes<T, V>(a.codes + row * a.dim, a.scales + row * a.blocks, u, j, a.dim, c, scale);
-      } else {
-        put<T, V>((T*)a.y + row * a.ys, u, j, a.dim, y);
-      }
-    }
-  }
-}
-
-template <typename T, int V, int NV, bool SAVED>
-__global__ void __launch_bounds__(kThreadsMost, (Unit<T, V>::E * NV < kElements ? kCtasPerSm : 1)) k_rms_backward(RmsArgs a) {
-  constexpr int E = Unit<T, V>::E;
-  extern __shared__ float cols[];
-  __shared__ float red[2][kThreadsMost / 32];
-  const int t = threadIdx.x, group = threadIdx.y, threads = blockDim.x;
-  const int warps = threads / 32, warp = t >> 5, lane = t & 31;
-  const Unit<T, V> u(t, threads);
-  const float inv = 1.f / (float)a.dim;
-  const long long step = (long long)gridDim.x * blockDim.y;
-  long long row = (long long)blockIdx.x * blockDim.y + group;
-  Raw<T, V> g[NV], gs[NV];
-  std::conditional_t<SAVED, RawCodes<T, V>, Raw<T, V>> x[NV];
-  float rstd = 0.f;
-  auto fetch = [&](long long r) {
-#pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      g[j].load((const T*)a.g + r * a.gs, u, j, a.dim);
-      if constexpr (SAVED) x[j].load(a.codes + r * a.dim, a.scales + r * a.blocks, u, j, a.dim);
-      else x[j].load((const T*)a.x + r * a.xs, u, j, a.dim);
-    }
-    rstd = __ldg(a.rstd + r);
-  };
-  after_previous();
-  if (row < a.rows) fetch(row);
-  float w[NV][E], dw[NV][E];
-#pragma unroll
-  for (int j = 0; j < NV; ++j) {
-    load_weight<T, V>(a.w, a.pdtype, u, j, a.dim, w[j]);
-#pragma unroll
-    for (int e = 0; e < E; ++e) dw[j][e] = 0.f;
-  }
-  int flip = 0;
-  for (; row < a.rows; row += step, flip ^= 1) {
-    float xh[NV][E], ga[NV][E], sum = 0.f;
-    const float rs = rstd;
-    if (a.residual && a.y) {
-#pragma unroll
-      for (int j = 0; j < NV; ++j) gs[j].load((const T*)a.residual + row * a.rs, u, j, a.dim);
-    }
-#pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      if constexpr (SAVED) x[j].get(a.e5, xh[j]);
-      else x[j].get(xh[j]);
-      g[j].get(ga[j]);
-#pragma unroll
-      for (int e = 0; e < E; ++e) {
-        xh[j][e] *= rs;
-        dw[j][e] = fmaf(ga[j][e], xh[j][e], dw[j][e]);
-        ga[j][e] *= w[j][e];
-        sum = fmaf(ga[j][e], xh[j][e], sum);
-      }
-    }
-    if (row + step < a.rows) fetch(row + step);
-    if (!a.y) continue;
-    sum = row_sum(sum, red[flip] + group * warps, warps, warp, lane, group, threads);
-    const float m = -sum * inv;
-#pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      float d[E], add[E];
-      if (a.residual) gs[j].get(add);
-#pragma unroll
-      for (int e = 0; e < E; ++e) {
-        d[e] = fmaf(xh[j][e], m, ga[j][e]) * rs;
-        if (a.residual) d[e] += add[e];
-      }
-      put<T, V>((T*)a.y + row * a.ys, u, j, a.dim, d);
-    }
-  }
-  next_may_launch();
-  if (!a.part) return;
-  // the groups' sums in group order
-  float* out = a.part + (long long)blockIdx.x * a.dim;
-  for (int y = 0; y < (int)blockDim.y; ++y) {
-    __syncthreads();
-    if (group != y) continue;
-    float* dst = y + 1 < (int)blockDim.y ? cols : out;
-#pragma unroll
-    for (int j = 0; j < NV; ++j)
-#pragma unroll
-      for (int e = 0; e < E; ++e)
-        if (u.in(j, e, a.dim)) dst[u.col(j, e)] = (y ? cols[u.col(j, e)] : 0.f) + dw[j][e];
-  }
+  for (int e = 0; e < 4; ++e)
+    if (c + 32 * e < dim) row[c + 32 * e] = (unsigned char)(code[0] >> (8 * e));
+  if (c % kBlock8 == 0 && c < dim) scales[c / kBlock8] = scale;
 }
 
 // The kernels for rows of whole 16-byte units.  A group takes R rows at a time, which share the barriers and shuffles
@@ -579,6 +348,216 @@ __global__ void __launch_bounds__(kThreadsMost, 1) k_rms_backward_vec(RmsArgs a)
   }
 }
 
+// The kernels for rows of any length and alignment.  The rows' aligned 16-byte granules are copied ahead into shared
+// memory, at the rows' own places within their first granules, and read from there element by element; a barrier of the
+// group follows each wait, as a granule is used by other threads than the one that copied it.
+// Bytes of one turn of a group: R rows of `arrays` arrays, and (backward) the rows' scales.
+__host__ __device__ inline int any_turn(int r, int arrays, int slot, int blocks) { return r * (arrays * slot + units(blocks, 4) * 16); }
+
+template <typename T, int NB, int R>
+__global__ void __launch_bounds__(kThreadsMost, 1) k_rms_forward_any(RmsArgs a) {
+  extern __shared__ __align__(16) unsigned char slots[];
+  __shared__ float red[2][kThreadsMost / 32 * R];
+  const int t = threadIdx.x, group = threadIdx.y, threads = blockDim.x;
+  const int warps = threads / 32, warp = t >> 5, lane = t & 31;
+  const int arrays = a.residual ? 2 : 1, slot = slot_bytes(warps * NB * kBlock8, sizeof(T)), turn = R * arrays * slot;
+  unsigned char* mine = slots + group * kAhead * turn;
+  const int first = warp * NB * kBlock8 + lane;
+  const float inv = 1.f / (float)a.dim;
+  const int step = gridDim.x * blockDim.y * R;
+  int row = ((int)blockIdx.x * blockDim.y + group) * R, ahead = row;
+  const CopyShare share(R * arrays, warps, warp);
+  auto issue = [&](int stage) {
+    for (int i = share.first; i < R * arrays; i += share.step) {
+      const bool second = i >= R;
+      const int r = ahead + (second ? i - R : i);
+      if (r < (int)a.rows)
+        copy_row(mine + stage * turn + i * slot, (const T*)(second ? a.residual : a.x), r, second ? a.rs : a.xs, a.dim,
+                 share.part * 32 + lane, share.parts * 32);
+    }
+    commit_copies();
+    ahead = ahead < (int)a.rows ? ahead + step : ahead;
+  };
+  after_previous();
+  next_may_launch();
+#pragma unroll
+  for (int k = 0; k < kAhead - 1; ++k) issue(k);
+  float w[NB][4];
+#pragma unroll
+  for (int b = 0; b < NB; ++b) load_unit(a.w, a.pdtype, first + b * kBlock8, a.dim, 1.f, w[b]);
+  int stage = 0, flip = 0;
+  for (; row < (int)a.rows; row += step, flip ^= 1) {
+    asm volatile("cp.async.wait_group %0;" ::"n"(kAhead - 2) : "memory");
+    group_barrier(group, threads);
+    issue(stage == 0 ? kAhead - 1 : stage - 1);
+    const int rows = min(R, (int)a.rows - row);
+    float s[R][NB][4], sum[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      sum[r] = 0.f;
+      const unsigned char* at = mine + stage * turn + r * slot;
+      const T* x = (const T*)(at + row_phase(a.x, row + r, a.xs, sizeof(T)));
+      const T* res = (const T*)(at + R * slot + row_phase(a.residual, row + r, a.rs, sizeof(T)));
+#pragma unroll
+      for (int b = 0; b < NB; ++b) {
+        const int c = first + b * kBlock8;
+        load_unit(x, c, r < rows ? a.dim : 0, s[r][b]);
+        if (a.residual) {
+          float more[4];
+          load_unit(res, c, r < rows ? a.dim : 0, more);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) s[r][b][e] = to_f(from_f<T>(s[r][b][e] + more[e]));
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) sum[r] = fmaf(s[r][b][e], s[r][b][e], sum[r]);
+        if (a.summed && r < rows) put_unit((T*)a.summed + (row + r) * a.ss, c, a.dim, s[r][b]);
+      }
+    }
+    stage = stage + 1 == kAhead ? 0 : stage + 1;
+    group_sum<R>(sum, red[flip] + group * warps * R, warps, warp, lane, group, threads);
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      if (r >= rows) break;
+      const float rstd = rsqrtf(fmaf(sum[r], inv, a.eps));
+      if (t == 0) a.rstd[row + r] = rstd;
+#pragma unroll
+      for (int b = 0; b < NB; ++b) {
+        const int c = first + b * kBlock8;
+        float y[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) y[e] = s[r][b][e] * rstd * w[b][e];
+        if (a.codes) put_codes(a.codes + (long long)(row + r) * a.dim, a.scales + (long long)(row + r) * a.blocks, c, a.dim, a.e5, y);
+        else put_unit((T*)a.y + (row + r) * a.ys, c, a.dim, y);
+      }
+    }
+  }
+}
+
+template <typename T, int NB, int R, bool SAVED>
+__global__ void __launch_bounds__(kThreadsMost, 1) k_rms_backward_any(RmsArgs a) {
+  extern __shared__ __align__(16) unsigned char slots[];
+  __shared__ float red[2][kThreadsMost / 32 * R];
+  __shared__ float stats[kAhead][kThreadsMost / 32][R];  // each warp's own copy of the rows' rstd
+  const int t = threadIdx.x, group = threadIdx.y, threads = blockDim.x;
+  const int warps = threads / 32, warp = t >> 5, lane = t & 31, cta_warp = group * warps + warp;
+  const int arrays = a.residual && a.y ? 3 : 2, slot = slot_bytes(warps * NB * kBlock8, sizeof(T));
+  const int turn = any_turn(R, arrays, slot, SAVED ? a.blocks : 0);
+  unsigned char* mine = slots + group * kAhead * turn;
+  const int first = warp * NB * kBlock8 + lane;
+  const float inv = 1.f / (float)a.dim;
+  const int step = gridDim.x * blockDim.y * R;
+  int row = ((int)blockIdx.x * blockDim.y + group) * R, ahead = row;
+  const CopyShare share(R * arrays, warps, warp);
+  auto scales_of = [&](int stage, int r) { return reinterpret_cast<float*>(mine + stage * turn + R * arrays * slot) + r * (int)units(a.blocks, 4) * 4; };
+  auto issue = [&](int stage) {
+    for (int i = share.first; i < R * arrays; i += share.step) {
+      const int array = i / R, r = ahead + i - array * R;
+      if (r >= (int)a.rows) continue;
+      unsigned char* to = mine + stage * turn + i * slot;
+      const int u = share.part * 32 + lane, by = share.parts * 32;
+      if (SAVED && array == 1) copy_row(to, (const unsigned char*)a.codes, r, a.dim, a.dim, u, by);
+      else copy_row(to, (const T*)(array == 0 ? a.g : array == 1 ? a.x : a.residual), r, array == 0 ? a.gs : array == 1 ? a.xs : a.rs, a.dim, u, by);
+    }
+    if constexpr (SAVED)
+      for (int r = 0; r < R; ++r)
+        for (int b = t; b < a.blocks; b += threads)
+          if (ahead + r < (int)a.rows) copy4(scales_of(stage, r) + b, a.scales + (long long)(ahead + r) * a.blocks + b);
+    if (lane < R && ahead + lane < (int)a.rows) copy4(&stats[stage][cta_warp][lane], a.rstd + ahead + lane);
+    commit_copies();
+    ahead = ahead < (int)a.rows ? ahead + step : ahead;
+  };
+  after_previous();
+#pragma unroll
+  for (int k = 0; k < kAhead - 1; ++k) issue(k);
+  float w[NB][4], dw[NB][4];
+#pragma unroll
+  for (int b = 0; b < NB; ++b) {
+    load_unit(a.w, a.pdtype, first + b * kBlock8, a.dim, 1.f, w[b]);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) dw[b][e] = 0.f;
+  }
+  int stage = 0, flip = 0;
+  for (; row < (int)a.rows; row += step, flip ^= 1) {
+    asm volatile("cp.async.wait_group %0;" ::"n"(kAhead - 2) : "memory");
+    group_barrier(group, threads);
+    issue(stage == 0 ? kAhead - 1 : stage - 1);
+    const int rows = min(R, (int)a.rows - row);
+    const unsigned char* data = mine + stage * turn;
+    float xh[R][NB][4], ga[R][NB][4], sum[R], rstd[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      sum[r] = 0.f;
+      rstd[r] = stats[stage][cta_warp][r];
+      const int dim = r < rows ? a.dim : 0;
+      const T* g = (const T*)(data + r * slot + row_phase(a.g, row + r, a.gs, sizeof(T)));
+      const unsigned char* kept = data + (R + r) * slot;
+      kept += SAVED ? row_phase(a.codes, row + r, a.dim, 1) : row_phase(a.x, row + r, a.xs, sizeof(T));
+#pragma unroll
+      for (int b = 0; b < NB; ++b) {
+        const int c = first + b * kBlock8;
+        load_unit(g, c, dim, ga[r][b]);
+        if constexpr (SAVED) {
+          unsigned code = 0;
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (c + 32 * e < dim) code |= (unsigned)kept[c + 32 * e] << (8 * e);
+          decode4(a.e5, code, c < dim ? scales_of(stage, r)[c / kBlock8] : 1.f, xh[r][b]);
+        } else {
+          load_unit((const T*)kept, c, dim, xh[r][b]);
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          // (a row that is none: its rstd may be anything)
+          xh[r][b][e] = r < rows ? xh[r][b][e] * rstd[r] : 0.f;
+          dw[b][e] = fmaf(ga[r][b][e], xh[r][b][e], dw[b][e]);
+          ga[r][b][e] *= w[b][e];
+          sum[r] = fmaf(ga[r][b][e], xh[r][b][e], sum[r]);
+        }
+      }
+    }
+    if (a.y) {
+      group_sum<R>(sum, red[flip] + group * warps * R, warps, warp, lane, group, threads);
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        if (r >= rows) break;
+        const float m = -sum[r] * inv;
+        const T* more = (const T*)(data + (2 * R + r) * slot + row_phase(a.residual, row + r, a.rs, sizeof(T)));
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+          const int c = first + b * kBlock8;
+          float d[4], f[4];
+          if (arrays == 3) load_unit(more, c, a.dim, f);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            d[e] = fmaf(xh[r][b][e], m, ga[r][b][e]) * rstd[r];
+            if (arrays == 3) d[e] += f[e];
+          }
+          put_unit((T*)a.y + (row + r) * a.ys, c, a.dim, d);
+        }
+      }
+    }
+    stage = stage + 1 == kAhead ? 0 : stage + 1;
+  }
+  next_may_launch();
+  if (!a.part) return;
+  // the groups' sums in group order, through the rows' memory
+  float* out = a.part + (long long)blockIdx.x * a.dim;
+  float* cols = reinterpret_cast<float*>(slots);
+  asm volatile("cp.async.wait_group 0;" ::: "memory");
+  for (int y = 0; y < (int)blockDim.y; ++y) {
+    __syncthreads();
+    if (group != y) continue;
+    float* dst = y + 1 < (int)blockDim.y ? cols : out;
+#pragma unroll
+    for (int b = 0; b < NB; ++b)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int c = first + b * kBlock8 + 32 * e;
+        if (c < a.dim) dst[c] = (y ? cols[c] : 0.f) + dw[b][e];
+      }
+  }
+}
+
 // Rows too long for registers: one CTA a row, a warp a block of 128 at a time; read again (from L2) for the result.
 __device__ __forceinline__ float cta_sum(float v, float* buf) {
   v = warp_sum(v);
@@ -589,74 +568,58 @@ __device__ __forceinline__ float cta_sum(float v, float* buf) {
 }
 template <typename T> __global__ void __launch_bounds__(kThreadsMost) k_rms_forward_long(RmsArgs a) {
   __shared__ float buf[kThreadsMost / 32];
-  const Unit<T, 1> u(threadIdx.x, blockDim.x);
-  const int rounds = (a.blocks + (int)blockDim.x / 32 - 1) / ((int)blockDim.x / 32);
-  auto sum_of = [&](long long row, int j, float (&s)[4]) {
-    Raw<T, 1> x;
-    x.load((const T*)a.x + row * a.xs, u, j, a.dim);
-    x.get(s);
+  const int first = ((int)threadIdx.x >> 5) * kBlock8 + (threadIdx.x & 31), step = (int)blockDim.x / 32 * kBlock8;
+  // (all lanes of a warp take part in a block or none does: encode() is a matter of the warp)
+  const int end = a.blocks * kBlock8;
+  auto sum_of = [&](long long row, int c, float (&s)[4]) {
+    load_unit((const T*)a.x + row * a.xs, c, a.dim, s);
     if (!a.residual) return;
     float r[4];
-    x.load((const T*)a.residual + row * a.rs, u, j, a.dim);
-    x.get(r);
+    load_unit((const T*)a.residual + row * a.rs, c, a.dim, r);
 #pragma unroll
     for (int e = 0; e < 4; ++e) s[e] = to_f(from_f<T>(s[e] + r[e]));
   };
   for (long long row = blockIdx.x; row < a.rows; row += gridDim.x) {
     float sum = 0.f;
-    for (int j = 0; j < rounds; ++j) {
+    for (int c = first; c < end; c += step) {
       float s[4];
-      sum_of(row, j, s);
+      sum_of(row, c, s);
 #pragma unroll
       for (int e = 0; e < 4; ++e) sum = fmaf(s[e], s[e], sum);
     }
     const float rstd = rsqrtf(fmaf(cta_sum(sum, buf), 1.f / (float)a.dim, a.eps));
     if (threadIdx.x == 0) a.rstd[row] = rstd;
-    for (int j = 0; j < rounds; ++j) {
+    for (int c = first; c < end; c += step) {
       float s[4], w[4], y[4];
-      sum_of(row, j, s);  // before the sum is written: it may take x's or the residual's place
-      if (a.summed) put<T, 1>((T*)a.summed + row * a.ss, u, j, a.dim, s);
-      load_weight<T, 1>(a.w, a.pdtype, u, j, a.dim, w);
+      sum_of(row, c, s);  // before the sum is written: it may take x's or the residual's place
+      if (a.summed) put_unit((T*)a.summed + row * a.ss, c, a.dim, s);
+      load_unit(a.w, a.pdtype, c, a.dim, 1.f, w);
 #pragma unroll
       for (int e = 0; e < 4; ++e) y[e] = s[e] * rstd * w[e];
-      if (a.codes) {
-        unsigned c[1];
-        float scale;
-        encode<4, 32>(a.e5, y, c, scale);
-        put_codes<T, 1>(a.codes + row * a.dim, a.scales + row * a.blocks, u, j, a.dim, c, scale);
-      } else {
-        put<T, 1>((T*)a.y + row * a.ys, u, j, a.dim, y);
-      }
+      if (a.codes) put_codes(a.codes + row * a.dim, a.scales + row * a.blocks, c, a.dim, a.e5, y);
+      else put_unit((T*)a.y + row * a.ys, c, a.dim, y);
     }
-  }
-}
-template <typename T> __device__ __forceinline__ void kept(const RmsArgs& a, long long row, const Unit<T, 1>& u, int j, float (&s)[4]) {
-  if (a.codes) {
-    RawCodes<T, 1> c;
-    c.load(a.codes + row * a.dim, a.scales + row * a.blocks, u, j, a.dim);
-    c.get(a.e5, s);
-  } else {
-    Raw<T, 1> x;
-    x.load((const T*)a.x + row * a.xs, u, j, a.dim);
-    x.get(s);
   }
 }
 template <typename T> __global__ void __launch_bounds__(kThreadsMost) k_rms_dx_long(RmsArgs a) {
   __shared__ float buf[kThreadsMost / 32];
-  const Unit<T, 1> u(threadIdx.x, blockDim.x);
-  const int rounds = (a.blocks + (int)blockDim.x / 32 - 1) / ((int)blockDim.x / 32);
+  const int first = ((int)threadIdx.x >> 5) * kBlock8 + (threadIdx.x & 31), step = (int)blockDim.x / 32 * kBlock8;
   for (long long row = blockIdx.x; row < a.rows; row += gridDim.x) {
     const float rs = a.rstd[row];
     float sum = 0.f;
     for (int pass = 0; pass < 2; ++pass) {
       const float m = -sum / (float)a.dim;
-      for (int j = 0; j < rounds; ++j) {
+      for (int c = first; c < a.dim; c += step) {
         float s[4], g[4], w[4];
-        Raw<T, 1> raw;
-        kept<T>(a, row, u, j, s);
-        raw.load((const T*)a.g + row * a.gs, u, j, a.dim);
-        raw.get(g);
-        load_weight<T, 1>(a.w, a.pdtype, u, j, a.dim, w);
+        if (a.codes) {
+          const float scale = a.scales[row * a.blocks + c / kBlock8];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) s[e] = c + 32 * e < a.dim ? decode1(a.e5, a.codes[row * a.dim + c + 32 * e], scale) : 0.f;
+        } else {
+          load_unit((const T*)a.x + row * a.xs, c, a.dim, s);
+        }
+        load_unit((const T*)a.g + row * a.gs, c, a.dim, g);
+        load_unit(a.w, a.pdtype, c, a.dim, 1.f, w);
         if (pass == 0) {
 #pragma unroll
           for (int e = 0; e < 4; ++e) sum = fmaf(g[e] * w[e], s[e] * rs, sum);
@@ -666,13 +629,12 @@ template <typename T> __global__ void __launch_bounds__(kThreadsMost) k_rms_dx_l
 #pragma unroll
         for (int e = 0; e < 4; ++e) d[e] = fmaf(s[e] * rs, m, g[e] * w[e]) * rs;
         if (a.residual) {
-          float add[4];
-          raw.load((const T*)a.residual + row * a.rs, u, j, a.dim);
-          raw.get(add);
+          float more[4];
+          load_unit((const T*)a.residual + row * a.rs, c, a.dim, more);
 #pragma unroll
-          for (int e = 0; e < 4; ++e) d[e] += add[e];
+          for (int e = 0; e < 4; ++e) d[e] += more[e];
         }
-        put<T, 1>((T*)a.y + row * a.ys, u, j, a.dim, d);
+        put_unit((T*)a.y + row * a.ys, c, a.dim, d);
       }
       if (pass == 0) sum = cta_sum(sum, buf);
     }
@@ -702,8 +664,10 @@ __global__ void __launch_bounds__(32 * kColumnWarps) k_rms_columns(const float* 
   after_previous();
   next_may_launch();
   float sum = 0.f;
-  if (c < dim)
+  if (c < dim) {
+#pragma unroll 4
     for (int p = warp; p < parts; p += kColumnWarps) sum += __ldcg(part + p * dim + c);
+  }
   sums[warp][lane] = sum;
   __syncthreads();
   if (warp || c >= dim) return;
@@ -748,10 +712,21 @@ template <typename T, int R1, typename F> void by_vec_plan(const Plan& p, bool f
   else if (p.nv == 2) f(Int<2>(), Int<(R1 + 1) / 2>());
   else if constexpr (Vec16<T>::N * 4 <= kElements) f(Int<4>(), Int<1>());
 }
-template <typename F> void by_any_plan(const Plan& p, F&& f) {
-  if (p.nv == 1) f(Int<1>());
-  else if (p.nv == 2) f(Int<2>());
-  else f(Int<4>());
+// f(units of a thread, rows of a turn) for any rows, whose `arrays` (and scales) have to fit into shared memory; false
+// where not even one row of each does.
+template <typename F> bool by_any_plan(const Plan& p, bool few, int size, int arrays, int blocks, int& bytes, F&& f) {
+  const int slot = slot_bytes(p.threads / 32 * p.nv * kBlock8, size);
+  const auto fits = [&](int r) {
+    bytes = p.groups * kAhead * any_turn(r, arrays, slot, blocks);
+    return bytes <= kMostStaged;
+  };
+  if (p.nv == 1 && !few && fits(4)) f(Int<1>(), Int<4>());
+  else if (p.nv == 2 && !few && fits(2)) f(Int<2>(), Int<2>());
+  else if (!fits(1)) return false;
+  else if (p.nv == 1) f(Int<1>(), Int<1>());
+  else if (p.nv == 2) f(Int<2>(), Int<1>());
+  else f(Int<4>(), Int<1>());
+  return true;
 }
 // Rows in one turn of a launch of one CTA an SM, and its CTAs.
 unsigned turns_of(const Plan& p, int r, long long rows, int sms) {
@@ -762,6 +737,21 @@ template <typename K> cudaError_t launch_vec(K kernel, std::atomic<unsigned long
   const cudaError_t e = raise_smem(kernel, raised, device, kMostStaged);
   if (e != cudaSuccess) return e;
   return launch_early(kernel, grid, dim3(p.threads, p.groups), (size_t)kAhead * stage_units * kThreadsMost * 16, 1, st, a);
+}
+template <typename K> cudaError_t launch_any(K kernel, std::atomic<unsigned long long>& raised, const Plan& p, int bytes, unsigned grid, int device,
+                                             cudaStream_t st, const RmsArgs& a) {
+  const cudaError_t e = raise_smem(kernel, raised, device, kMostStaged);
+  return e != cudaSuccess ? e : launch_early(kernel, grid, dim3(p.threads, p.groups), bytes, 1, st, a);
+}
+template <typename T, int NB, int R>
+cudaError_t forward_any(const RmsArgs& a, const Plan& p, int bytes, int sms, int device, cudaStream_t st) {
+  static std::atomic<unsigned long long> raised{0};
+  return launch_any(k_rms_forward_any<T, NB, R>, raised, p, bytes, turns_of(p, R, a.rows, sms), device, st, a);
+}
+template <typename T, int NB, int R, bool SAVED>
+cudaError_t backward_any(const RmsArgs& a, const Plan& p, int bytes, unsigned grid, int device, cudaStream_t st) {
+  static std::atomic<unsigned long long> raised{0};
+  return launch_any(k_rms_backward_any<T, NB, R, SAVED>, raised, p, bytes, grid, device, st, a);
 }
 template <typename T, int NV, int R>
 cudaError_t forward_vec(const RmsArgs& a, const Plan& p, int sms, int device, cudaStream_t st) {
@@ -830,7 +820,7 @@ extern "C" int psgd_rmsnorm_create(int64_t dim, int32_t device, psgd_rmsnorm** o
   h->dim = dim;
   e = cudaDeviceGetAttribute(&h->sms, cudaDevAttrMultiProcessorCount, device);
   if (e == cudaSuccess) {
-    h->max_ctas = h->sms * kCtasPerSm;
+    h->max_ctas = h->sms * kPartsPerSm;
     h->bytes = (size_t)h->max_ctas * dim * 4;
     e = cudaMalloc((void**)&h->part, h->bytes);
   }
@@ -898,21 +888,18 @@ extern "C" int psgd_rmsnorm_forward(psgd_rmsnorm* h, const void* x, psgd_dtype d
   cudaError_t e = cudaSuccess;
   by_dtype(dtype, [&](auto* tt) {
     using T = std::remove_pointer_t<decltype(tt)>;
-    if (p.nv == 0) {
-      k_rms_forward_long<T><<<(unsigned)std::min<long long>(rows, h->sms * 4), kThreadsMost, 0, st>>>(a);
-      e = cudaGetLastError();
-      return;
-    }
-    if (vec) {
-      by_vec_plan<T, 2>(p, rows <= 4LL * h->sms * p.groups, [&](auto nv, auto r) {
+    const bool few = rows <= 4LL * h->sms * std::max(p.groups, 1);
+    int bytes = 0;
+    if (p.nv && vec) {
+      by_vec_plan<T, 2>(p, few, [&](auto nv, auto r) {
         e = forward_vec<T, decltype(nv)::value, decltype(r)::value>(a, p, h->sms, h->device, st);
       });
-      return;
+    } else if (!p.nv || !by_any_plan(p, few, sizeof(T), residual ? 2 : 1, 0, bytes, [&](auto nb, auto r) {
+                 e = forward_any<T, decltype(nb)::value, decltype(r)::value>(a, p, bytes, h->sms, h->device, st);
+               })) {
+      k_rms_forward_long<T><<<(unsigned)std::min<long long>(rows, h->sms * 4), kThreadsMost, 0, st>>>(a);
+      e = cudaGetLastError();
     }
-    const unsigned grid = (unsigned)std::min<long long>(units(rows, p.groups), h->sms * kCtasPerSm);
-    by_any_plan(p, [&](auto nv) {
-      e = launch_early(k_rms_forward<T, 1, decltype(nv)::value>, grid, dim3(p.threads, p.groups), 0, 1, st, a);
-    });
   });
   return e == cudaSuccess ? PSGD_OK : cuda_fail(who.c_str(), e);
 }
@@ -964,7 +951,20 @@ extern "C" int psgd_rmsnorm_backward(psgd_rmsnorm* h, const void* grad, psgd_dty
   if (rows > 0)
     by_dtype(dtype, [&](auto* tt) {
       using T = std::remove_pointer_t<decltype(tt)>;
-      if (p.nv == 0) {
+      const bool few = rows <= 4LL * h->sms * std::max(p.groups, 1);
+      int bytes = 0;
+      if (vec && p.nv && p.nv < 4) {  // (three arrays of four units have no room for their turns)
+        by_vec_plan<T, 2>(p, few, [&](auto nv, auto r) {
+          constexpr int NV = decltype(nv)::value, R = decltype(r)::value;
+          parts = (int)turns_of(p, R, rows, h->sms);
+          e = codes ? backward_vec<T, NV, R, true>(a, p, parts, h->device, st) : backward_vec<T, NV, R, false>(a, p, parts, h->device, st);
+        });
+      } else if (!p.nv || !by_any_plan(p, few, sizeof(T), grad_summed && dx ? 3 : 2, codes ? a.blocks : 0, bytes, [&](auto nb, auto r) {
+                   constexpr int NB = decltype(nb)::value, R = decltype(r)::value;
+                   parts = (int)turns_of(p, R, rows, h->sms);
+                   e = codes ? backward_any<T, NB, R, true>(a, p, bytes, parts, h->device, st)
+                             : backward_any<T, NB, R, false>(a, p, bytes, parts, h->device, st);
+                 })) {
         // (dx may take g's place: dw first)
         if (dweight) {
           parts = (int)std::min<long long>(units(rows, 32), h->max_ctas);
@@ -975,26 +975,7 @@ extern "C" int psgd_rmsnorm_backward(psgd_rmsnorm* h, const void* grad, psgd_dty
           k_rms_dx_long<T><<<(unsigned)std::min<long long>(rows, h->sms * 4), kThreadsMost, 0, st>>>(a);
           e = cudaGetLastError();
         }
-        return;
       }
-      if (vec && p.nv < 4) {  // (three arrays of four units have no room for their turns)
-        by_vec_plan<T, 2>(p, rows <= 4LL * h->sms * p.groups, [&](auto nv, auto r) {
-          constexpr int NV = decltype(nv)::value, R = decltype(r)::value;
-          parts = (int)turns_of(p, R, rows, h->sms);
-          e = codes ? backward_vec<T, NV, R, true>(a, p, parts, h->device, st) : backward_vec<T, NV, R, false>(a, p, parts, h->device, st);
-        });
-        return;
-      }
-      parts = (int)std::min<long long>(units(rows, p.groups), h->max_ctas);
-      const size_t smem = p.groups > 1 ? (size_t)dim * 4 : 0;
-      by_any_plan(p, [&](auto nv) {
-        auto go = [&](auto saved) {
-          e = launch_early(k_rms_backward<T, 1, decltype(nv)::value, decltype(saved)::value>, (unsigned)parts, dim3(p.threads, p.groups), smem, 1,
-                           st, a);
-        };
-        if (codes) go(std::true_type());
-        else go(std::false_type());
-      });
     });
   if (e == cudaSuccess && dweight)
     e = launch_early(k_rms_columns, (unsigned)units(dim, 32), 32 * kColumnWarps, 0, 1, st, h->part, parts, dim, dweight,

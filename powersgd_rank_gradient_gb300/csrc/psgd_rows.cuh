@@ -82,5 +82,26 @@ template <int NE> __device__ __forceinline__ void load_param(const void* w, int 
   for (int h = 0; h < NE; ++h) f[h] = f2(v[2 * h], v[2 * h + 1]);
 }
 
+// How the warps of a group share the copies of `items` rows: warp w takes the
+// items first, first + step, ..., and of each the granules of part `part` of
+// `parts`.
+struct CopyShare {
+  int first, step, part, parts;
+  __device__ __forceinline__ CopyShare(int items, int warps, int warp) {
+    parts = warps >= items ? warps / items : 1;
+    first = parts > 1 ? warp / parts : warp;
+    part = parts > 1 ? warp - first * parts : 0;
+    step = parts > 1 ? items : warps;  // (with parts, warps that are left over have first >= items)
+  }
+};
+
+__device__ __forceinline__ void group_barrier(int group, int threads) {
+  asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "r"(threads) : "memory");
+}
+
+// Where in its first granule row `index` of an array begins, in bytes.
+__device__ __forceinline__ int row_phase(const void* base, int index, long long stride, int size) {
+  return ((unsigned)(uintptr_t)base + (unsigned)index * ((unsigned)stride * (unsigned)size)) & 15;
+}
 }  // namespace ops
 }  // namespace psgd
