@@ -9,6 +9,7 @@
 // fp32, so a bucket in fp32 gets an fp32 gradient.
 #include <algorithm>
 #include <new>
+#include <type_traits>
 
 #include "psgd_mma.cuh"
 
@@ -30,14 +31,22 @@ namespace {
 
 constexpr long long kMostRows = 1 << 24;
 
-// Rows of any stride and alignment into rows of `to` elements.
-template <typename T> __global__ void __launch_bounds__(256) k_align(const T* src, long long stride, long long rows, int cols, T* dst, long long to) {
+// Rows of any stride into rows of `to` words: a CTA takes runs of 2048 words of a row, eight words a thread under way.
+template <typename W> __global__ void __launch_bounds__(256) k_align(const W* src, long long stride, long long rows, int cols, W* dst, long long to, int runs) {
   after_previous();
   next_may_launch();
-  for (long long r = blockIdx.y; r < rows; r += gridDim.y) {
-    const T* s = src + r * stride;
-    T* d = dst + r * to;
-    for (int c = blockIdx.x * 256 + threadIdx.x; c < cols; c += gridDim.x * 256) d[c] = s[c];
+  for (long long i = blockIdx.x; i < rows * runs; i += gridDim.x) {
+    const long long r = runs == 1 ? i : i / runs;
+    const int first = (int)(i - r * runs) * 2048 + threadIdx.x;
+    const W* s = src + r * stride;
+    W* d = dst + r * to;
+    W x[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      if (first + 256 * k < cols) x[k] = s[first + 256 * k];
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      if (first + 256 * k < cols) d[first + 256 * k] = x[k];
   }
 }
 
@@ -45,8 +54,15 @@ template <typename T> __global__ void __launch_bounds__(256) k_align(const T* sr
 
 cudaError_t psgd::mma::align_rows(const void* src, long long stride, long long rows, long long cols, void* dst, long long to, cudaStream_t st) {
   if (rows == 0) return cudaSuccess;
-  const dim3 grid((unsigned)std::min<long long>(units(cols, 256), 16), (unsigned)std::min<long long>(rows, 4096));
-  return launch_early(k_align<uint16_t>, grid, 256, 0, 1, st, (const uint16_t*)src, stride, rows, (int)cols, (uint16_t*)dst, to);
+  const auto go = [&](auto* w, int by) {
+    using W = std::remove_pointer_t<decltype(w)>;
+    const long long runs = units(cols / by, 2048);
+    return launch_early(k_align<W>, (unsigned)std::min<long long>(rows * runs, 152 * 16), 256, 0, 1, st, (const W*)src, stride / by, rows,
+                        (int)(cols / by), (W*)dst, to / by, (int)runs);
+  };
+  // two elements at a time where all rows begin and end between words of two
+  if ((uintptr_t)src % 4 == 0 && stride % 2 == 0 && cols % 2 == 0) return go((uint32_t*)nullptr, 2);
+  return go((uint16_t*)nullptr, 1);
 }
 
 extern "C" int psgd_wgrad_create(int64_t outs, int64_t ins, int64_t max_rows, int32_t device, psgd_wgrad** out) {
