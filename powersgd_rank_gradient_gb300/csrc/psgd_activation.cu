@@ -29,8 +29,26 @@ struct EightArgs {
 
 // piece / blocks without a division (exact for 32-bit numbers).
 __device__ __forceinline__ long long row_of(const EightArgs& a, unsigned piece) {
-  return a.rows == 1 ? 0 : a.by ? (long long)__umul64hi(piece, a.by) : piece;
+  return a.by ? (long long)__umul64hi(piece, a.by) : piece;
 }
+// Where a piece's elements of this lane are: its row and column.  ONE: of one row, all in 32 bits.
+template <bool ONE> struct Place {
+  std::conditional_t<ONE, int, long long> row, scale;
+  int c;
+  bool in;
+  __device__ __forceinline__ Place(const EightArgs& a, long long piece, int lane, int e) {
+    if constexpr (ONE) {
+      row = 0;
+      scale = (int)piece;
+      c = (int)piece * kBlock8 + lane * e;
+    } else {
+      row = row_of(a, (unsigned)piece);
+      scale = piece;  // (scales have no gaps)
+      c = (int)(piece - row * a.blocks) * kBlock8 + lane * e;
+    }
+    in = piece < a.pieces && c < a.dim;
+  }
+};
 
 // The largest magnitude's bits, as fp32, among 16 bytes of elements: of 16-bit types two at a time.
 template <typename T> __device__ __forceinline__ unsigned magnitude(const uint4& u) {
@@ -53,9 +71,10 @@ template <typename T> __device__ __forceinline__ unsigned as_f32(unsigned m) {
 }
 
 // Rows of whole 16-byte units.  A thread takes U of them: unit i of thread t is lane t % LANES of block (t / LANES) +
-// i * step.  What is under way waits in its own type, and the largest magnitude of a block is found in it.  Bound by
-// HBM: 16384 x 4096 bf16 31 us (6.5 TB/s; 55 us with sums and maxima in fp32 and a division a unit).
-template <typename T, bool E5, int U> __global__ void __launch_bounds__(kThreads8) k_save_vec(EightArgs a) {
+// i * step.  What is under way waits in its own type, and the largest magnitude of a block is found in it.  16384 x 4096
+// bf16 saved and restored: 61 us, 404 MB at 6.6 TB/s (90 us with maxima in fp32 and a division a unit, 74 with a
+// multiplication in its place and places in 64 bits): bound by HBM.
+template <typename T, bool E5, int U, bool ONE> __global__ void __launch_bounds__(kThreads8) k_save_vec(EightArgs a) {
   constexpr int E = Vec16<T>::N, LANES = kBlock8 / E;
   const int lane = threadIdx.x & (LANES - 1);
   const long long first = ((long long)blockIdx.x * kThreads8 + threadIdx.x) / LANES;
@@ -66,11 +85,8 @@ template <typename T, bool E5, int U> __global__ void __launch_bounds__(kThreads
 #pragma unroll
   for (int i = 0; i < U; ++i) {
     const long long piece = first + i * step;
-    raw[i] = make_uint4(0, 0, 0, 0);
-    if (piece >= a.pieces) continue;
-    const long long row = row_of(a, (unsigned)piece);
-    const int c = (int)(piece - row * a.blocks) * kBlock8 + lane * E;
-    if (c < a.dim) raw[i] = __ldg(reinterpret_cast<const uint4*>((const T*)a.x + row * a.xs + c));
+    const Place<ONE> at(a, piece, lane, E);
+    raw[i] = at.in ? __ldg(reinterpret_cast<const uint4*>((const T*)a.x + at.row * a.xs + at.c)) : make_uint4(0, 0, 0, 0);
   }
 #pragma unroll
   for (int i = 0; i < U; ++i) {
@@ -99,19 +115,16 @@ template <typename T, bool E5, int U> __global__ void __launch_bounds__(kThreads
       for (int k = 0; k < E / 2; ++k) split(p[k], v[2 * k], v[2 * k + 1]);
       encode_special<E, LANES, E5>(v, code, scale);
     }
-    const long long piece = first + i * step;
-    if (piece >= a.pieces) continue;
-    const long long row = row_of(a, (unsigned)piece);
-    const int block = (int)(piece - row * a.blocks), c = block * kBlock8 + lane * E;
-    if (c >= a.dim) continue;
-    unsigned char* dst = a.codes + row * a.dim + c;
+    const Place<ONE> at(a, first + i * step, lane, E);
+    if (!at.in) continue;
+    unsigned char* dst = a.codes + (long long)at.row * a.dim + at.c;
     if constexpr (E == 8) *reinterpret_cast<uint2*>(dst) = make_uint2(code[0], code[1]);
     else *reinterpret_cast<unsigned*>(dst) = code[0];
-    if (lane == 0) a.scales[row * a.blocks + block] = scale;
+    if (lane == 0) a.scales[at.scale] = scale;
   }
 }
 
-template <typename T, bool E5, int U> __global__ void __launch_bounds__(kThreads8) k_restore_vec(EightArgs a) {
+template <typename T, bool E5, int U, bool ONE> __global__ void __launch_bounds__(kThreads8) k_restore_vec(EightArgs a) {
   constexpr int E = Vec16<T>::N, LANES = kBlock8 / E;
   const int lane = threadIdx.x & (LANES - 1);
   const long long first = ((long long)blockIdx.x * kThreads8 + threadIdx.x) / LANES;
@@ -123,15 +136,12 @@ template <typename T, bool E5, int U> __global__ void __launch_bounds__(kThreads
   T* dst[U];
 #pragma unroll
   for (int i = 0; i < U; ++i) {
-    const long long piece = first + i * step;
+    const Place<ONE> at(a, first + i * step, lane, E);
     dst[i] = nullptr;
-    if (piece >= a.pieces) continue;
-    const long long row = row_of(a, (unsigned)piece);
-    const int block = (int)(piece - row * a.blocks), c = block * kBlock8 + lane * E;
-    if (c >= a.dim) continue;
-    dst[i] = (T*)const_cast<void*>(a.x) + row * a.xs + c;
-    scale[i] = __ldg(a.scales + row * a.blocks + block);
-    const unsigned char* src = a.codes + row * a.dim + c;
+    if (!at.in) continue;
+    dst[i] = (T*)const_cast<void*>(a.x) + at.row * a.xs + at.c;
+    scale[i] = __ldg(a.scales + at.scale);
+    const unsigned char* src = a.codes + (long long)at.row * a.dim + at.c;
     if constexpr (E == 8) {
       const uint2 q = __ldg(reinterpret_cast<const uint2*>(src));
       code[i][0] = q.x;
@@ -222,8 +232,12 @@ template <bool SAVE, typename T> cudaError_t go(const EightArgs& a, bool vec, cu
     constexpr int U = decltype(u)::value;
     const unsigned grid = (unsigned)units(a.pieces, per * U);
     if (!vec) return launch_early(k_eight_any<T, SAVE, U>, grid, kThreads8, 0, 1, st, a);
-    if constexpr (SAVE) return launch_early(a.e5 ? k_save_vec<T, true, U> : k_save_vec<T, false, U>, grid, kThreads8, 0, 1, st, a);
-    else return launch_early(a.e5 ? k_restore_vec<T, true, U> : k_restore_vec<T, false, U>, grid, kThreads8, 0, 1, st, a);
+    const auto of = [&](auto one) {
+      constexpr bool ONE = decltype(one)::value;
+      if constexpr (SAVE) return launch_early(a.e5 ? k_save_vec<T, true, U, ONE> : k_save_vec<T, false, U, ONE>, grid, kThreads8, 0, 1, st, a);
+      else return launch_early(a.e5 ? k_restore_vec<T, true, U, ONE> : k_restore_vec<T, false, U, ONE>, grid, kThreads8, 0, 1, st, a);
+    };
+    return a.rows == 1 ? of(std::true_type()) : of(std::false_type());
   };
   return a.pieces > per * 4 * 512 ? with(std::integral_constant<int, 4>()) : with(std::integral_constant<int, 1>());
 }

@@ -7,8 +7,7 @@
 //
 // One group of threads takes a whole row, which stays in registers between its
 // sum and its result, so every operand is read once and every result written
-// once.  While a row is summed, the loads of the group's next row are under way.
-// In the backward pass a thread owns the same columns of every row it meets and
+// once.  In the backward pass a thread owns the same columns of every row it meets and
 // keeps their dw sums in fp32 registers; a CTA leaves one partial row and a
 // second kernel adds the partial rows in a fixed order.
 #include <algorithm>
@@ -80,7 +79,10 @@ __device__ __forceinline__ void put_codes(unsigned char* row, float* scales, int
 
 // The kernels for rows of whole 16-byte units.  A group takes R rows at a time, which share the barriers and shuffles
 // of one reduction; the rows of the next two turns are copied ahead into shared memory, by the thread that will use
-// them, so that neither a register nor a barrier waits for what is under way.
+// them, so that neither a register nor a barrier waits for what is under way.  Forward 32768 x 1600 bf16 with a residual
+// 73 us (5.8 TB/s, 85 % of the copy rate; 77 with plain loads a row ahead), 16384 x 1024 into 8 bits 23: HBM, and
+// instructions at 58 % of the issue slots.  Backward 65536 x 1600 bf16 from 8 bits with a residual's gradient 134 us
+// (5.5 TB/s; 246 with plain loads, 144 with one row a turn and two CTAs an SM).
 constexpr int kAhead = 3;  // turns: the one in use and those under way
 // CTAs of an SM: two where a turn's rows leave the room (and 64 registers a thread suffice).
 constexpr int ctas_of(int nv, int r) { return nv == 1 && r <= 2 ? 2 : 1; }
@@ -350,7 +352,8 @@ __global__ void __launch_bounds__(kThreadsMost, 1) k_rms_backward_vec(RmsArgs a)
 
 // The kernels for rows of any length and alignment.  The rows' aligned 16-byte granules are copied ahead into shared
 // memory, at the rows' own places within their first granules, and read from there element by element; a barrier of the
-// group follows each wait, as a granule is used by other threads than the one that copied it.
+// group follows each wait, as a granule is used by other threads than the one that copied it.  Backward 4099 x 1023 f16
+// 13.5 us with the columns' sums (17.0 with plain loads): latency of seven turns, two launches.
 // Bytes of one turn of a group: R rows of `arrays` arrays, and (backward) the rows' scales.
 __host__ __device__ inline int any_turn(int r, int arrays, int slot, int blocks) { return r * (arrays * slot + units(blocks, 4) * 16); }
 
