@@ -796,7 +796,7 @@ int psgd_wgrad_status(psgd_wgrad* w, void* stream);
  *
  * The handle holds the tokens that count, a bounded piece of the logits' gradient
  * (256 MB, or 256 columns of the vocabulary where those take more) and partial
- * sums; calls on one handle must not overlap on the GPU.
+ * sums (eight bytes for every 128 logits); calls on one handle must not overlap on the GPU.
  */
 typedef struct psgd_linear_ce psgd_linear_ce; /* opaque, library-owned */
 

@@ -7,8 +7,8 @@
 // made (psgd_gemm.cu): the forward pass leaves the largest logit and the sum of
 // exponentials of every tile's columns of a row, the backward pass makes them again
 // and leaves G, rounded to 16 bits, for a piece of the vocabulary at a time; both
-// gradients are products of that piece.  No memory grows with tokens x vocabulary
-// but those pieces, which are bounded.
+// gradients are products of that piece.  Those pieces are bounded; what grows with
+// tokens x vocabulary are eight bytes for every 128 logits.
 //
 // Tokens that count (a target in the vocabulary, a weight that is not 0) are moved
 // together first, so that padding costs nothing, and what its rows hold touches
@@ -364,7 +364,7 @@ struct Call {
   Call(psgd_linear_ce* h_, const void* hidden_, int dtype, long long hs, const void* weight_, long long ws, const void* targets, int bits,
        const float* weights, long long tokens, void* stream)
       : h(h_), hidden(hidden_), hidden_stride(hs), weight(weight_), weight_stride(ws), bf16(dtype == PSGD_BF16),
-        in_place(aligned16(weight_) && ws % 8 == 0 && ws >= h_->dim), t{targets, bits, weights, (int)tokens, h_->vocab},
+        in_place(mma::in_place(weight_, ws, h_->dim)), t{targets, bits, weights, (int)tokens, h_->vocab},
         st((cudaStream_t)stream) {}
 
   // The tokens that count, side by side.

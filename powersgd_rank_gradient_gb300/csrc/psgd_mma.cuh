@@ -254,6 +254,11 @@ enum Epilogue { kLse = 0, kGrad = 1, kOut = 2 };
 // with the 128-byte swizzle; what lies outside reads as zero.  The address is a multiple of 16 bytes, stride of 8
 // elements.
 cudaError_t make_map(CUtensorMap* map, const void* p, long long rows, long long cols, long long stride, int box_rows, bool bf16);
+// Whether a map can have rows of `cols` elements, `stride` apart, as they lie (rows that overlap, a broadcast operand's, it
+// cannot, nor strides of 2^40 bytes).
+inline bool in_place(const void* p, long long stride, long long cols) {
+  return ops::aligned16(p) && stride % 8 == 0 && stride >= cols && stride < (1LL << 39);
+}
 inline int box_rows(bool m_rows) { return m_rows ? kStep : kHalf; }
 
 // Elements from row to row of a matrix of 16-bit elements in a workspace: an odd number of lines of 128 bytes, so that

@@ -144,8 +144,8 @@ extern "C" int psgd_wgrad_backward(psgd_wgrad* h, const void* grad, psgd_dtype d
   if (rows > 0) {
     const int rc = psgd_activation_restore(codes, code, scales, rows, h->ins, h->x, dtype, h->ip, h->device, stream);
     if (rc) return rc;
-    // (a stride of 0, a broadcast gradient, is none that a tensor map has)
-    if (!aligned16(grad) || grad_stride % 8 != 0 || (rows > 1 && grad_stride < h->outs)) {
+    if (rows == 1 && aligned16(grad)) grad_stride = h->op;  // of one row no stride counts
+    if (!mma::in_place(grad, grad_stride, h->outs)) {
       e = mma::align_rows(grad, grad_stride, rows, h->outs, h->g, h->op, st);
       grad = h->g;
       grad_stride = h->op;
@@ -154,7 +154,6 @@ extern "C" int psgd_wgrad_backward(psgd_wgrad* h, const void* grad, psgd_dtype d
     grad = h->g;
     grad_stride = h->op;
   }
-  if (rows == 1) grad_stride = h->op;  // of one row no stride counts
   mma::Product p{};
   const bool bf16 = dtype == PSGD_BF16;
   if (e == cudaSuccess) e = mma::make_map(&p.a, grad, rows, h->outs, grad_stride, mma::box_rows(true), bf16);

@@ -236,6 +236,15 @@ class Activation8:
             return _bind.activation_restore(self.codes, self.scales, dtype, out)
 
 
+def _eight(a, what):
+    """(codes, scales) of ``a``, which must be an ``Activation8`` (or None: None of each)."""
+    if a is None:
+        return None, None
+    if not isinstance(a, Activation8):
+        raise ValueError(f"{what} must be an Activation8, got {type(a).__name__}")
+    return a.codes, a.scales
+
+
 def _index_of(t, stream):
     return t.get_device() if isinstance(t, torch.Tensor) and t.is_cuda else stream.device.index
 
@@ -247,7 +256,7 @@ def save_activation(x, dtype=torch.float8_e4m3fn, out=None, stream=None):
     A block of 128 elements of a row has one scale, the least power of two that
     brings its largest value within the format; a code is its element, rounded
     once.  Infinities and NaN become NaN (e5m2 keeps infinities)."""
-    codes, scales = (None, None) if out is None else (out.codes, out.scales)
+    codes, scales = _eight(out, "out")
     if stream is None:
         codes, scales = _bind.activation_save(x, dtype, codes, scales)
     else:
@@ -295,7 +304,7 @@ class RMSNorm:
 
     def forward8(self, x, weight=None, residual=None, dtype=torch.float8_e4m3fn, out=None, summed=None, stream=None):
         """(y, summed, rstd) with y an ``Activation8`` of ``dtype`` (a new one, or ``out``)."""
-        codes, scales = (None, None) if out is None else (out.codes, out.scales)
+        codes, scales = _eight(out, "out")
         if stream is None:
             codes, scales, summed, rstd = _bind.rmsnorm_forward(self._spec, x, weight, residual, None, summed, dtype, codes, scales)
         else:
@@ -357,10 +366,13 @@ class LinearWeightGrad:
         """``grad^T x`` with grad (..., out_features) in float16 or bfloat16 and x the values of
         ``activation`` (an ``Activation8`` of (..., in_features)) in grad's type, into ``out``
         (default: a new fp32 tensor), over what it holds or, with ``accumulate``, added to it."""
+        if activation is None:
+            raise ValueError("activation must be an Activation8, got NoneType")
+        codes, scales = _eight(activation, "activation")
         if stream is None:
-            return _bind.wgrad_backward(self._spec, grad, activation.codes, activation.scales, out, accumulate)
+            return _bind.wgrad_backward(self._spec, grad, codes, scales, out, accumulate)
         with _on(stream, self.device.index):
-            return _bind.wgrad_backward(self._spec, grad, activation.codes, activation.scales, out, accumulate)
+            return _bind.wgrad_backward(self._spec, grad, codes, scales, out, accumulate)
 
     def status(self, stream=None):
         """Synchronises; raises PsgdError if a bounded wait on the GPU gave up since the last status()."""

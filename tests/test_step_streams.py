@@ -54,3 +54,14 @@ def handle(cls):
 def test_streams_of_another_device(training, call):
     with pytest.raises(ValueError, match="stream must be on cuda:0"):
         call(training, types.SimpleNamespace(device=torch.device("cuda", 1), cuda_stream=0))
+
+
+@pytest.mark.parametrize("call,what", [
+    (lambda t, x: t.save_activation(x, out=x), "out"),
+    (lambda t, x: handle(t.RMSNorm).forward8(x, out=x), "out"),
+    (lambda t, x: handle(t.LinearWeightGrad).backward(x, x), "activation"),
+    (lambda t, x: handle(t.LinearWeightGrad).backward(x, None), "activation"),
+])
+def test_what_is_no_checkpoint_is_refused(training, call, what):
+    with pytest.raises(ValueError, match=f"^{what} must be an Activation8"):
+        call(training, cuda_tensor())
