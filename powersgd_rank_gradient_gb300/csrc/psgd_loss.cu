@@ -20,6 +20,7 @@
 #include <limits.h>
 
 #include <algorithm>
+#include <atomic>
 #include <new>
 #include <type_traits>
 
@@ -41,7 +42,7 @@ struct psgd_linear_ce {
   float *lse = nullptr, *factor = nullptr, *at_target = nullptr;
   int *row = nullptr, *target = nullptr, *exponent = nullptr;  // of the tokens that count
   int* place = nullptr;      // of a token among them, or -1
-  int* count = nullptr;      // [0]: tokens that count, [1]: largest exponent, [2]: error
+  int* count = nullptr;      // [0]: tokens that count, [1]: largest exponent, [2]: error, [3]: CTAs that are done
   float* scale = nullptr;    // [0]: dW's, [1]: a row of dh's without its power of two
   size_t bytes = 0;
 };
@@ -267,6 +268,136 @@ __global__ void __launch_bounds__(1024) k_plan_gather(Tokens t, int* place, int*
   gather_rows<T, V>(a, threadIdx.x >> 5, 32, threadIdx.x & 31, 32);
 }
 
+// Two entries of largest logit and sum of exponentials as one.  (An entry without a logit above -infinity has a sum of 0,
+// or NaN, which stays.)
+__device__ __forceinline__ float2 merge(float2 a, float2 b) {
+  const float now = fmaxf(a.x, b.x);
+  return make_float2(now, a.y * (a.x == -INFINITY ? 0.f : __expf(a.x - now)) + b.y * (b.x == -INFINITY ? 0.f : __expf(b.x - now)));
+}
+// (loss without its weight, lse) from the others' entry and the target's logit.
+__device__ __forceinline__ float2 loss_of(float2 others, float z) {
+  if (z >= others.x) {  // of a target that is nearly certain the loss is what the others add
+    const float rest = z == INFINITY ? NAN : log1pf(others.y * __expf(others.x - z));
+    return make_float2(rest, z + rest);
+  }
+  const float r = logf(others.y + __expf(z - others.x));
+  return make_float2((others.x - z) + r, others.x + r);
+}
+
+// The forward pass of at most N tokens, in one launch and without the tensor cores: a tile's 256 rows would be idle, and
+// what comes before and after a product would take half as long as it does.  A warp reads whole rows of the weight, four
+// at a time (one token over 50257 x 1600 bf16: 33 us, 4.9 TB/s), and keeps its own largest logit and sum of exponentials for
+// each token; the CTA that is done last adds the CTAs' entries up, always in the same order.
+constexpr int kFewDim = 8192;
+template <typename T, int N>
+__global__ void __launch_bounds__(256, N == 1 ? 4 : 2) k_losses_few(Tokens t, const T* hidden, long long hidden_stride, const T* weight, long long stride,
+                                                                    int dim, float2* part, float* at_target, int* done, float* losses, float* lses) {
+  extern __shared__ __align__(16) uint4 tokens[];  // N rows of dim / 8
+  __shared__ float2 all[8][N];
+  __shared__ int last;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, units8 = dim / 8, vocab = (int)t.vocab;
+  after_previous();
+  next_may_launch();
+  int own[N];  // the target of a token that counts, else -1
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const long long y = i < t.tokens ? target_of(t, i) : -1;
+    own[i] = y >= 0 && y < t.vocab && weight_of(t, i) != 0.f ? (int)y : -1;
+    for (int c = threadIdx.x; c < dim; c += 256)
+      reinterpret_cast<T*>(tokens)[i * dim + c] = own[i] >= 0 ? hidden[i * hidden_stride + c] : from_f<T>(0.f);
+  }
+  float2 mine[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) mine[i] = make_float2(-INFINITY, 0.f);
+  __syncthreads();
+  for (int row = (blockIdx.x * 8 + warp) * 4; row < vocab; row += gridDim.x * 32) {
+    F2 acc[N][4];
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) acc[i][r] = f2(0.f, 0.f);
+    const T* from[4];  // (rows behind the last: the last again)
+#pragma unroll
+    for (int r = 0; r < 4; ++r) from[r] = weight + min(row + r, vocab - 1) * stride;
+#pragma unroll 2
+    for (int u = lane; u < units8; u += 32) {
+      uint4 raw[4];
+#pragma unroll
+      for (int r = 0; r < 4; ++r) raw[r] = __ldg(reinterpret_cast<const uint4*>(from[r]) + u);
+      F2 x[N][4];
+#pragma unroll
+      for (int i = 0; i < N; ++i) to_pairs<T>(tokens[i * units8 + u], x[i]);
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        F2 w[4];
+        to_pairs<T>(raw[r], w);
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) acc[i][r] = fma(w[k], x[i][k], acc[i][r]);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      float z[4], most = -INFINITY;
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        float u, v;
+        split(acc[i][r], u, v);
+        z[r] = warp_sum(u + v);
+        if (row + r == own[i]) {
+          if (lane == 0) __stcg(at_target + i, z[r]);
+          z[r] = -INFINITY;
+        }
+        if (row + r >= vocab) z[r] = -INFINITY;
+        most = fmaxf(most, z[r]);
+      }
+      const float from0 = most == -INFINITY ? 0.f : most;
+      mine[i] = merge(mine[i], make_float2(most, (__expf(z[0] - from0) + __expf(z[1] - from0)) + (__expf(z[2] - from0) + __expf(z[3] - from0))));
+    }
+  }
+  if (lane == 0)
+#pragma unroll
+    for (int i = 0; i < N; ++i) all[warp][i] = mine[i];
+  __syncthreads();
+  if (threadIdx.x < N) {
+    float2 x = all[0][threadIdx.x];
+    for (int w = 1; w < 8; ++w) x = merge(x, all[w][threadIdx.x]);
+    __stcg(part + (long long)blockIdx.x * N + threadIdx.x, x);
+  }
+  __threadfence();
+  __syncthreads();
+  if (threadIdx.x == 0) last = atomicAdd(done, 1) == (int)gridDim.x - 1;
+  __syncthreads();
+  if (!last) return;
+  __threadfence();
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    float2 x = make_float2(-INFINITY, 0.f);
+    for (int p = threadIdx.x; p < (int)gridDim.x; p += 256) x = merge(x, __ldcg(part + (long long)p * N + i));
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      const float2 y = make_float2(__shfl_down_sync(0xffffffffu, x.x, o), __shfl_down_sync(0xffffffffu, x.y, o));
+      x = merge(x, y);
+    }
+    if (lane == 0) all[warp][i] = x;
+  }
+  __syncthreads();
+  const int i = threadIdx.x;
+  if (i == 0) *done = 0;
+  if (i >= t.tokens || i >= N) return;
+  const long long y = target_of(t, i);
+  float2 r = make_float2(0.f, 0.f);
+  if (y >= 0 && y < t.vocab && weight_of(t, i) != 0.f) {
+    float2 x = all[0][i];
+    for (int w = 1; w < 8; ++w) x = merge(x, all[w][i]);
+    r = loss_of(x, __ldcg(at_target + i));
+    r.x *= weight_of(t, i);
+  }
+  losses[i] = r.x;
+  lses[i] = r.y;
+}
+
 // Losses and log-sum-exps of 32 tokens a CTA from the tiles, whose order the warps share, and the targets' logits.
 __global__ void __launch_bounds__(1024) k_losses(Tokens t, const int* place, const float2* part, long long part_rows, int parts,
                                                  const float* at_target, float* losses, float* lses) {
@@ -275,41 +406,26 @@ __global__ void __launch_bounds__(1024) k_losses(Tokens t, const int* place, con
   after_previous();
   next_may_launch();
   const int at = i < t.tokens ? place[i] : -1;
-  float top = -INFINITY, sum = 0.f;
-  const auto add = [&](float2 x) {
-    const float now = fmaxf(top, x.x);
-    // a piece without a logit above -infinity has a sum of 0 (or NaN, which stays)
-    sum = sum * (top == -INFINITY ? 0.f : __expf(top - now)) + x.y * (x.x == -INFINITY ? 0.f : __expf(x.x - now));
-    top = now;
-  };
+  float2 mine = make_float2(-INFINITY, 0.f);
   if (at >= 0)
     for (int p = warp; p < parts; p += 32 * 8) {  // eight reads under way
       float2 x[8];
 #pragma unroll
       for (int k = 0; k < 8; ++k) x[k] = p + 32 * k < parts ? __ldcg(part + (p + 32 * k) * part_rows + at) : make_float2(-INFINITY, 0.f);
 #pragma unroll
-      for (int k = 0; k < 8; ++k) add(x[k]);
+      for (int k = 0; k < 8; ++k) mine = merge(mine, x[k]);
     }
-  all[warp][lane] = make_float2(top, sum);
+  all[warp][lane] = mine;
   __syncthreads();
   if (warp || i >= t.tokens) return;
-  float loss = 0.f, lse = 0.f;
+  float2 r = make_float2(0.f, 0.f);
   if (at >= 0) {
-    for (int w = 1; w < 32; ++w) add(all[w][lane]);
-    const float z = at_target[at];
-    float rest;
-    if (z >= top) {  // of a target that is nearly certain the loss is what the others add
-      rest = z == INFINITY ? NAN : log1pf(sum * __expf(top - z));
-      lse = z + rest;
-    } else {
-      const float r = logf(sum + __expf(z - top));
-      rest = (top - z) + r;
-      lse = top + r;
-    }
-    loss = weight_of(t, i) * rest;
+    for (int w = 1; w < 32; ++w) mine = merge(mine, all[w][lane]);
+    r = loss_of(mine, at_target[at]);
+    r.x *= weight_of(t, i);
   }
-  losses[i] = loss;
-  lses[i] = lse;
+  losses[i] = r.x;
+  lses[i] = r.y;
 }
 
 // dh of every token: its row of the sums times its power of two, 0 for a token that does not count.
@@ -519,6 +635,28 @@ extern "C" int psgd_linear_ce_forward(psgd_linear_ce* h, const void* hidden, psg
   if (tokens == 0) return PSGD_OK;
   DeviceScope scope(h->device);
   Call c(h, hidden, dtype, hidden_stride, weight, weight_stride, targets, target_bits, weights, tokens, stream);
+  // few tokens: one launch.  In place of the products, over 50257 x 1600 bf16 one token 34 us (48), four 53 (50); over
+  // 30522 x 1024 18 (28) and 26 (29), over 5000 x 256 7 (15) and 12 (15).
+  if (tokens <= 4 && c.in_place && h->dim % 8 == 0 && h->dim <= kFewDim) {
+    const unsigned grid = (unsigned)std::min<long long>(units(h->vocab, mma::kTile / 2), h->pairs * 2 * (tokens == 1 ? 4 : 2));
+    const auto go = [&](auto* tt, auto count) {
+      using T = std::remove_pointer_t<decltype(tt)>;
+      constexpr int N = decltype(count)::value;
+      static std::atomic<unsigned long long> raised{0};
+      c.e = raise_smem(k_losses_few<T, N>, raised, h->device, N * kFewDim * 2);
+      if (c.e == cudaSuccess)
+        c.e = launch_early(k_losses_few<T, N>, grid, 256, (size_t)N * h->dim * 2, 1, c.st, c.t, (const T*)hidden, hidden_stride, (const T*)weight,
+                           weight_stride, (int)h->dim, h->part, h->at_target, h->count + 3, losses, lse);
+    };
+    const auto by_count = [&](auto* tt) {
+      if (tokens == 1) go(tt, std::integral_constant<int, 1>());
+      else if (tokens == 2) go(tt, std::integral_constant<int, 2>());
+      else go(tt, std::integral_constant<int, 4>());
+    };
+    if (c.bf16) by_count((__nv_bfloat16*)nullptr);
+    else by_count((__half*)nullptr);
+    return c.e == cudaSuccess ? PSGD_OK : cuda_fail(who.c_str(), c.e);
+  }
   c.gather(false, nullptr, 1.f);
   const long long step = c.in_place ? h->vocab : h->piece;
   int parts = 0;

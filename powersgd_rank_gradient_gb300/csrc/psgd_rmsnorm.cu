@@ -81,8 +81,8 @@ __device__ __forceinline__ void put_codes(unsigned char* row, float* scales, int
 // of one reduction; the rows of the next two turns are copied ahead into shared memory, by the thread that will use
 // them, so that neither a register nor a barrier waits for what is under way.  Forward 32768 x 1600 bf16 with a residual
 // 73 us (5.8 TB/s, 85 % of the copy rate; 77 with plain loads a row ahead), 16384 x 1024 into 8 bits 23: HBM, and
-// instructions at 58 % of the issue slots.  Backward 65536 x 1600 bf16 from 8 bits with a residual's gradient 134 us
-// (5.5 TB/s; 246 with plain loads, 144 with one row a turn and two CTAs an SM).
+// instructions at 58 % of the issue slots.  Backward 65536 x 1600 bf16 from 8 bits with a residual's gradient 131 us
+// (5.6 TB/s; 246 with plain loads, 144 with one row a turn and two CTAs an SM).
 constexpr int kAhead = 3;  // turns: the one in use and those under way
 // CTAs of an SM: two where a turn's rows leave the room (and 64 registers a thread suffice).
 constexpr int ctas_of(int nv, int r) { return nv == 1 && r <= 2 ? 2 : 1; }
@@ -275,7 +275,8 @@ __global__ void __launch_bounds__(kThreadsMost, 1) k_rms_backward_vec(RmsArgs a)
         }
         to_pairs<T>(src[0], ga[r][j]);
         if constexpr (SAVED) {
-          const float scale = scales[stage][r * NV + j][mine_8];
+          // (a scale is a power of two: its product with rstd is exact, and one multiplication an element does for both)
+          const float scale = scales[stage][r * NV + j][mine_8] * rstd[r];
           float f[E];
           const unsigned* code = reinterpret_cast<const unsigned*>(src + kThreadsMost);
 #pragma unroll
@@ -284,10 +285,11 @@ __global__ void __launch_bounds__(kThreadsMost, 1) k_rms_backward_vec(RmsArgs a)
           for (int h = 0; h < NP; ++h) xh[r][j][h] = f2(f[2 * h], f[2 * h + 1]);
         } else {
           to_pairs<T>(src[kThreadsMost], xh[r][j]);
+#pragma unroll
+          for (int h = 0; h < NP; ++h) xh[r][j][h] = mul(xh[r][j][h], rs);
         }
 #pragma unroll
         for (int h = 0; h < NP; ++h) {
-          xh[r][j][h] = mul(xh[r][j][h], rs);
           dw[j][h] = fma(ga[r][j][h], xh[r][j][h], dw[j][h]);
           ga[r][j][h] = mul(ga[r][j][h], w[j][h]);
           along = fma(ga[r][j][h], xh[r][j][h], along);

@@ -104,6 +104,23 @@ def test_few_tokens_and_a_long_vocabulary():
     run(handle(50257, 200, 5), *batch(5, 50257, 200, BF16, 13, masked=0.0))
 
 
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("tokens,vocab,dim", [(1, 50257, 1600), (2, 1001, 8), (3, 4099, 328), (4, 130, 8192), (4, 5000, 8200), (1, 3, 64)])
+def test_tokens_one_by_one(tokens, vocab, dim, dtype):
+    """Four tokens at most, with and without rows that are read whole."""
+    hidden, weight, targets = batch(tokens, vocab, dim, dtype, 71, masked=0.0)
+    h = handle(vocab, dim, 300)
+    run(h, hidden, weight, targets)
+    targets[tokens // 2] = -100
+    run(h, hidden, weight, targets)
+    hidden[0], weight[vocab // 2, 3] = torch.nan, torch.inf
+    losses, _ = h.forward(hidden, weight, targets)
+    # (an infinite weight's logit is -infinity, which has no mass, where the hidden value is negative)
+    z, live = hidden.double() @ weight.double().t(), targets >= 0
+    bad = torch.isnan(z).any(1) | (z == torch.inf).any(1)
+    assert torch.equal(~torch.isfinite(losses[live]), bad[live]) and not bool(losses[~live].any())
+
+
 def test_sums_that_are_cut():
     run(handle(300, 264, 5000), *batch(5000, 300, 264, F16, 17))
 
