@@ -188,8 +188,8 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) k_produ
       uint32_t phase = 0;
       for (int i = 0; run_of(p, plan, pairs, pair, i, run); ++i) {
         const int row = run.tm * kTile + (int)rank * kHalf, col = run.tn * p.bn + (int)rank * (run.width / 2);
-        // Of A with K rows, no more than the rows that there are: what bounds products of few rows is the lines of 128
-        // bytes that an SM can have under way (some 350).  What lies in the others' place gives rows that nobody takes.
+        // Of A with K rows, no more than the rows that there are: fewer bytes into the SMs, and room for more stages.  What lies in the
+        // others' place gives rows that nobody takes.
         const int rows_here = min(kHalf, m - row), rows_0 = min(kHalf, m - run.tm * kTile), rows_1 = min(kHalf, m - run.tm * kTile - kHalf);
         const bool few = !p.a_m_rows && rows_1 < kHalf;
         const int boxes = (max(rows_here, 0) + kFew - 1) / kFew;
@@ -539,7 +539,7 @@ cudaError_t pairs_of(int device, int* pairs) {
 // Columns of an OUT product's tiles.  A step costs about as long as its lines take into an SM, 0.33 us for 256 + 256
 // rows and columns, and what is drained after a pair's last step, 2.5 us for 256 columns, is waited for.  So where the tiles
 // do not occupy the pairs (and cannot be cut along k), narrower ones end earlier: 1024 x 1024 from 509 rows, 16 tiles of 256
-// columns 12.2 us, 64 of 64 columns 10.0.
+// columns 12.2 us, 64 of 64 columns 11.4.
 static int columns_of(const Product& p, int pairs) {
   int best = kTile;
   double least = 1e30;
