@@ -268,7 +268,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) k_produ
       const int col0 = run.tn * p.bn + group * kCols;
       // (loaded while the tile is summed)
       int tgt = -1;
-      float lse = 0.f, factor = 0.f;
+      float lse = 0.f, factor = 0.f, own = 0.f;  // own: exp(z - lse) - 1 at the target
       if constexpr (KIND != kOut) {
         if (row < m) tgt = p.target[row] - p.column0 - col0;
       }
@@ -276,6 +276,8 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) k_produ
         if (row < m) {
           lse = p.lse[row];
           factor = p.factor[row];
+          // not from the sum in tensor memory, whose drift is larger than 1 - p of a likely target (see Gather)
+          if (tgt >= 0 && tgt < kCols) own = expm1f(p.at_target[row] - lse);
         }
       }
       float v[kCols];  // this lane's row, 64 columns of it
@@ -374,7 +376,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) k_produ
             for (int k = 0; k < 2; ++k) {
               const int at = 8 * i + 2 * e + k;
               // a row or column that is none: 0 whatever was summed there
-              g[k] = at < left ? (exp_of(v[at] - lse) - (at == tgt ? 1.f : 0.f)) * factor : 0.f;
+              g[k] = at < left ? (at == tgt ? own : exp_of(v[at] - lse)) * factor : 0.f;
             }
             w[e] = ops::pack2<T>(g[0], g[1]);
           }

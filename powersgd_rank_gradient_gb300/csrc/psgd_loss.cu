@@ -167,13 +167,13 @@ __device__ void plan(const Tokens& t, int* place, int* row, int* target, float* 
   }
 }
 
-// A warp's product of two rows of 16-bit elements, of any alignment.
+// A warp's product of two rows of 16-bit elements, of any alignment, in the order of k_losses_few.
 template <typename T> __device__ __forceinline__ float warp_dot(const T* a, const T* b, int dim, bool vec) {
   const int lane = threadIdx.x & 31;
-  float sum = 0.f;
+  F2 s = f2(0.f, 0.f);
 #pragma unroll 4
   for (int c = lane * 8; c < dim; c += 256) {
-    F2 x[4], y[4], s = f2(0.f, 0.f);
+    F2 x[4], y[4];
     if (vec) {
       to_pairs<T>(*reinterpret_cast<const uint4*>(a + c), x);
       to_pairs<T>(*reinterpret_cast<const uint4*>(b + c), y);
@@ -187,17 +187,17 @@ template <typename T> __device__ __forceinline__ float warp_dot(const T* a, cons
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i) s = fma(x[i], y[i], s);
-    float u, v;
-    split(s, u, v);
-    sum += u + v;
   }
-  return warp_sum(sum);
+  float u, v;
+  split(s, u, v);
+  return warp_sum(u + v);
 }
 
-// The rows of the tokens that count, side by side.  Forward: and their targets' logits, which are summed here, in rounded
-// fp32: where a target is likely, its logit is by far the largest, the loss is the small rest, and the tensor cores'
-// drift on a large sum (2e-6 of it) would be most of it.  Backward: and the rows times 2^(e - max e), then rows of zeros
-// up to a whole step of the sum over tokens, and the tokens' lse.
+// The rows of the tokens that count, side by side, and their targets' logits, which are summed here, in rounded fp32:
+// where a target is likely, its logit is by far the largest, the loss and 1 - p are the small rest, and the tensor cores'
+// drift on a large sum (1e-5 of it at 1600 elements of one sign) would be more than it is.  Both passes sum it in one
+// order, so that z - lse, of which 1 - p is made, has lost no more than lse's own rounding.  Backward: and the rows times
+// 2^(e - max e), then rows of zeros up to a whole step of the sum over tokens, and the tokens' lse.
 template <typename T> struct Gather {
   const T* src;
   long long stride;
@@ -207,7 +207,7 @@ template <typename T> struct Gather {
   long long dp;
   const float* lse_of;
   float* lse;
-  const T* weight;  // forward
+  const T* weight;
   long long weight_stride;
   int vec_dot;
   float* at_target;
@@ -239,16 +239,22 @@ template <typename T, int V> __device__ __forceinline__ void gather_rows(const G
         }
       }
     }
-    if (a.weight && thread < 32) {  // (the first warp of the row's threads)
-      const float z = warp_dot(from, a.weight + a.target[r] * a.weight_stride, a.dim, a.vec_dot);
-      if (thread == 0) a.at_target[r] = z;
-    }
   }
 }
-template <typename T, int V> __global__ void __launch_bounds__(128) k_gather(Gather<T> a) {
+// by whole warps
+template <typename T> __device__ __forceinline__ void gather_logits(const Gather<T>& a, int first, int step) {
+  const int n = a.count[0];
+  for (int r = first; r < n; r += step) {
+    const float z = warp_dot(a.src + (long long)a.row[r] * a.stride, a.weight + a.target[r] * a.weight_stride, a.dim, a.vec_dot);
+    if ((threadIdx.x & 31) == 0) a.at_target[r] = z;
+  }
+}
+// Four warps copy a row while the fifth sums its target's logit.
+template <typename T, int V> __global__ void __launch_bounds__(160) k_gather(Gather<T> a) {
   after_previous();
   next_may_launch();
-  gather_rows<T, V>(a, blockIdx.x, gridDim.x, threadIdx.x, 128);
+  if (threadIdx.x < 128) gather_rows<T, V>(a, blockIdx.x, gridDim.x, threadIdx.x, 128);
+  else gather_logits(a, blockIdx.x, gridDim.x);
 }
 __global__ void __launch_bounds__(1024) k_plan(Tokens t, int* place, int* row, int* target, float* factor, int* exponent, int* count,
                                                float* scale, float grad_scale, int shift) {
@@ -266,6 +272,7 @@ __global__ void __launch_bounds__(1024) k_plan_gather(Tokens t, int* place, int*
   plan(t, place, row, target, factor, exponent, count, scale, grad_scale, shift);
   __syncthreads();
   gather_rows<T, V>(a, threadIdx.x >> 5, 32, threadIdx.x & 31, 32);
+  gather_logits(a, threadIdx.x >> 5, 32);
 }
 
 // Two entries of largest logit and sum of exponentials as one.  (An entry without a logit above -infinity has a sum of 0,
@@ -495,13 +502,13 @@ struct Call {
       using T = std::remove_pointer_t<decltype(tt)>;
       constexpr int V = decltype(v)::value;
       const Gather<T> a{(const T*)hidden, hidden_stride, (int)h->dim, h->row, h->target, h->exponent, h->count, (T*)h->h,
-                        backward ? (T*)h->hs : nullptr, h->dp, lse, backward ? h->lse : nullptr, backward ? nullptr : (const T*)weight,
-                        weight_stride, vec && in_place, h->at_target};
+                        backward ? (T*)h->hs : nullptr, h->dp, lse, backward ? h->lse : nullptr, (const T*)weight, weight_stride,
+                        vec && in_place, h->at_target};
       if (few)
         e = launch_early(k_plan_gather<T, V>, 1, 1024, 0, 1, st, t, h->place, h->row, h->target, h->factor, h->exponent, h->count, h->scale,
                          grad_scale, shift, a);
       else
-        e = launch_early(k_gather<T, V>, (unsigned)std::min(t.tokens + mma::kStep, 4096), 128, 0, 1, st, a);
+        e = launch_early(k_gather<T, V>, (unsigned)std::min(t.tokens + mma::kStep, 4096), 160, 0, 1, st, a);
     };
     using One = std::integral_constant<int, 1>;
     using Eight = std::integral_constant<int, 8>;
@@ -706,7 +713,7 @@ extern "C" int psgd_linear_ce_backward(psgd_linear_ce* h, const void* hidden, ps
     const long long n = std::min(h->piece, h->vocab - v0);
     mma::Product z = c.logits(v0, n), dh{}, dw{};
     c.weight_map(mma::kGrad, z, &dh.b, v0, n);
-    z.lse = h->lse, z.factor = h->factor;
+    z.lse = h->lse, z.factor = h->factor, z.at_target = h->at_target;
     if (c.e == cudaSuccess) c.e = mma::make_map(&z.store, h->g, h->cap, h->piece, h->gp, 32, c.bf16);
     if (c.e == cudaSuccess && tokens > 0) c.e = mma::enqueue(mma::kGrad, z, h->device, h->pairs, c.st);
     if (dhidden && tokens > 0) {
