@@ -725,6 +725,7 @@ extern "C" int psgd_linear_ce_backward(psgd_linear_ce* h, const void* hidden, ps
       dh.bf16 = c.bf16, dh.error = h->count + 2;
       dh.out = h->dh, dh.ldo = h->dp, dh.dtype = PSGD_F32, dh.accumulate = v0 > 0;
       dh.slots = h->slots;
+      dh.chunk = mma::chunk_of(n, dtype);  // (dhidden's type: the workspace is rounded to it)
       if (c.e == cudaSuccess) c.e = mma::enqueue(mma::kOut, dh, h->device, h->pairs, c.st);
     }
     if (dweight) {
@@ -737,6 +738,7 @@ extern "C" int psgd_linear_ce_backward(psgd_linear_ce* h, const void* hidden, ps
       dw.out = (char*)dweight + v0 * dweight_stride * dtype_size(dweight_dtype), dw.ldo = dweight_stride;
       dw.dtype = dweight_dtype, dw.accumulate = accumulate != 0, dw.scale = h->scale;
       dw.slots = h->slots;
+      dw.chunk = mma::chunk_of(tokens, dweight_dtype);
       if (c.e == cudaSuccess) c.e = mma::enqueue(mma::kOut, dw, h->device, h->pairs, c.st);
     }
   }

@@ -165,7 +165,7 @@ extern "C" int psgd_wgrad_backward(psgd_wgrad* h, const void* grad, psgd_dtype d
   p.error = h->error;
   p.out = dweight, p.ldo = dweight_stride, p.dtype = dweight_dtype, p.accumulate = accumulate != 0;
   p.slots = h->slots;
-  p.chunk = dweight_dtype == PSGD_F32 ? 16 : 0;  // (with 32, sums of 2048 rows were 1.6e-6 off; a 16-bit result shows nothing of it)
+  p.chunk = mma::chunk_of(rows, dweight_dtype);
   e = mma::enqueue(mma::kOut, p, h->device, h->pairs, st);
   return e == cudaSuccess ? PSGD_OK : cuda_fail(who.c_str(), e);
 }
