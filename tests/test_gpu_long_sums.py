@@ -93,3 +93,26 @@ def test_weight_gradient_of_many_rows(rows, sign, dtype):
     h.status()
     want = grad.double().t() @ kept.restore(F32).double()
     assert float((got.double() - want).norm() / want.norm()) < 1e-6
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("dim", [8192, 65536])
+def test_logits_of_long_rows(dim, dtype):
+    """Losses and lse where no target is likely and all products have one sign."""
+    from powersgd_rank_gradient_gb300 import LinearCrossEntropy
+
+    tokens, vocab = 40, 2000
+    c = LinearCrossEntropy(vocab, dim, tokens, device=DEV)
+    hidden = positive((tokens, dim), dtype, 7)
+    weight = (positive((vocab, dim), F32, 8) * (48 / dim)).to(dtype)
+    targets = torch.randint(0, vocab, (tokens,), device=DEV, generator=torch.Generator(device=DEV).manual_seed(9))
+    losses, lse = c.forward(hidden, weight, targets)
+    c.status()
+    z = hidden.double() @ weight.double().t()
+    want = torch.logsumexp(z, 1)
+    ez = (CUT + (dim / 1024 + 4) * u) * float(z.max())
+    # a target's own logit: 4 dim / 256 products of a lane in a chain, then 6 additions
+    et = (dim / 64 + 6) * u * float(z.max())
+    el = ez + (200 + vocab / 128 / 32) * u + 3 * u * want
+    su.check(lse, want, el)
+    su.check(losses, want - z.gather(1, targets[:, None])[:, 0], el + et + 6 * u * want)
