@@ -196,8 +196,8 @@ template <typename T> __device__ __forceinline__ float warp_dot(const T* a, cons
 // The rows of the tokens that count, side by side, and their targets' logits, which are summed here, in rounded fp32:
 // where a target is likely, its logit is by far the largest, the loss and 1 - p are the small rest, and the tensor cores'
 // drift on a large sum (1e-5 of it at 1600 elements of one sign) would be more than it is.  Both passes sum it in one
-// order, so that z - lse, of which 1 - p is made, has lost no more than lse's own rounding.  Backward: and the rows times
-// 2^(e - max e), then rows of zeros up to a whole step of the sum over tokens, and the tokens' lse.
+// order, so that z - lse, of which 1 - p is made, has lost no more than lse's own rounding.  Backward: exp(z - lse) - 1 of it,
+// and the rows times 2^(e - max e), then rows of zeros up to a whole step of the sum over tokens, and the tokens' lse.
 template <typename T> struct Gather {
   const T* src;
   long long stride;
@@ -210,7 +210,7 @@ template <typename T> struct Gather {
   const T* weight;
   long long weight_stride;
   int vec_dot;
-  float* at_target;
+  float* at_target;  // forward: the target's logit, backward: exp(it - lse) - 1
 };
 template <typename T, int V> __device__ __forceinline__ void gather_rows(const Gather<T>& a, int first, int step, int thread, int threads) {
   const int n = a.count[0], end = a.hs ? (n + mma::kStep - 1) / mma::kStep * mma::kStep : n;
@@ -246,7 +246,7 @@ template <typename T> __device__ __forceinline__ void gather_logits(const Gather
   const int n = a.count[0];
   for (int r = first; r < n; r += step) {
     const float z = warp_dot(a.src + (long long)a.row[r] * a.stride, a.weight + a.target[r] * a.weight_stride, a.dim, a.vec_dot);
-    if ((threadIdx.x & 31) == 0) a.at_target[r] = z;
+    if ((threadIdx.x & 31) == 0) a.at_target[r] = a.hs ? expm1f(z - a.lse_of[a.row[r]]) : z;
   }
 }
 // Four warps copy a row while the fifth sums its target's logit.

@@ -199,7 +199,7 @@ struct Product {
   long long part_rows;       // rows between parts
   const float* lse;          // GRAD
   const float* factor;       // GRAD: multiplies a row's gradient
-  const float* at_target;    // GRAD: a row's logit at its target
+  const float* at_target;    // GRAD: a row's exp(z - lse) - 1 at its target
 };
 
 // How a product's tiles go to pairs of CTAs: whole tiles in turns of one for each pair; the tiles of a last turn that
