@@ -794,9 +794,13 @@ int psgd_wgrad_status(psgd_wgrad* w, void* stream);
 /*
  * Softmax cross entropy of a linear output layer, without its logits.
  *
- * The handle holds the tokens that count, a bounded piece of the logits' gradient
- * (256 MB, or 256 columns of the vocabulary where those take more) and partial
- * sums (eight bytes for every 128 logits); calls on one handle must not overlap on the GPU.
+ * The handle holds
+ *   the tokens that count, twice in their type and once in fp32 (8 bytes for max_tokens x dim),
+ *   a piece of the logits' gradient of at most 256 MB (or 256 columns of the vocabulary where those take more),
+ *   a piece of a weight that TMA cannot read where it lies (an address or row stride that is no multiple of 16
+ *   bytes, rows that overlap): at most 32 MB, or 256 MB where dim is no multiple of 8 (or 256 rows),
+ *   partial sums: 512 KB for every two SMs, and eight bytes for every 128 logits;
+ * 80 MB for one token of 50257 x 1600, 402 MB for 8192.  Calls on one handle must not overlap on the GPU.
  */
 typedef struct psgd_linear_ce psgd_linear_ce; /* opaque, library-owned */
 

@@ -360,7 +360,8 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) k_produ
         }
         flip ^= 1;
       } else {
-        if (group * kCols >= run.width) continue;
+        // (rows of zeros up to a whole step of the sum over tokens, and none behind them)
+        if (group * kCols >= run.width || row0 >= (m + kStep - 1) / kStep * kStep) continue;
         const int left = row < m ? p.vocab - p.column0 - col0 : 0;
         if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");  // the staging's last box is out
         __syncwarp();

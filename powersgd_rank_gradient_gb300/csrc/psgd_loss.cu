@@ -30,10 +30,11 @@ struct psgd_linear_ce {
   int device = 0, pairs = 0;
   long long vocab = 0, dim = 0, most = 0;
   long long dp = 0;          // row stride of h, W and dh in the workspace
-  long long cap = 0;         // rows of the workspace: max_tokens up to a multiple of 256
+  long long cap = 0;         // rows of the workspace: max_tokens up to a multiple of 64
   long long piece = 0;       // columns of the vocabulary that G holds, a multiple of 256
   long long gp = 0;          // row stride of G
   void *h = nullptr, *hs = nullptr;  // the tokens that count, and them times 2^(e - max e)
+  long long copied = 0;      // rows that w holds, a multiple of 256 and at most `piece`
   void* w = nullptr;         // a piece of a weight that TMA cannot read in place
   void* g = nullptr;
   float* dh = nullptr;       // cap x dp
@@ -53,6 +54,10 @@ namespace {
 
 constexpr long long kMostTokens = 1 << 20, kMostVocab = 1 << 24;
 constexpr long long kPieceBytes = 256LL << 20;  // of G
+// Of a weight that TMA cannot read in place.  Rows of whole 16-byte units seldom need it, and a handle for one token should
+// not hold a table; others mostly do (50257 x 1601 in pieces of 32 MB: 8 tokens' losses 166 us, 128 whole, 2458 tokens'
+// gradients 1445 and 1075).
+constexpr long long kCopyBytes = 32LL << 20, kOddCopyBytes = 256LL << 20;
 constexpr int kF16Shift = 14;  // G's values are at most 2 in size: 2^15 with it
 
 struct Tokens {
@@ -577,11 +582,15 @@ extern "C" int psgd_linear_ce_create(int64_t vocab, int64_t dim, int64_t max_tok
   h->dim = dim;
   h->most = max_tokens;
   h->dp = mma::row_stride(dim);
-  h->cap = std::max(1LL, units(max_tokens, mma::kTile)) * mma::kTile;
+  h->cap = std::max(1LL, units(max_tokens, mma::kStep)) * mma::kStep;
   // equal pieces of whole tiles
-  const long long tiles = units(vocab, mma::kTile), fit = std::max(1LL, kPieceBytes / (h->cap * mma::kTile * 2));
-  h->piece = units(tiles, units(tiles, fit)) * mma::kTile;
+  const auto pieces_of = [](long long columns, long long fit) {
+    const long long tiles = units(columns, mma::kTile);
+    return units(tiles, units(tiles, std::max(1LL, fit))) * mma::kTile;
+  };
+  h->piece = pieces_of(vocab, kPieceBytes / (h->cap * mma::kTile * 2));
   h->gp = mma::row_stride(h->piece);
+  h->copied = pieces_of(h->piece, (dim % 8 ? kOddCopyBytes : kCopyBytes) / (mma::kTile * h->dp * 2));
   e = mma::pairs_of(device, &h->pairs);
   const auto get = [&](auto** p, long long bytes) {
     if (e == cudaSuccess) e = cudaMalloc((void**)p, bytes);
@@ -590,11 +599,11 @@ extern "C" int psgd_linear_ce_create(int64_t vocab, int64_t dim, int64_t max_tok
   };
   get(&h->h, h->cap * h->dp * 2);
   get(&h->hs, h->cap * h->dp * 2);
-  get(&h->w, h->piece * h->dp * 2);
+  get(&h->w, h->copied * h->dp * 2);
   get(&h->g, h->cap * h->gp * 2);
   get(&h->dh, h->cap * h->dp * 4);
   get(&h->slots, 2 * h->pairs * mma::kSlotFloats * 4);
-  get(&h->part, (units(vocab, mma::kTile / 2) + units(vocab, h->piece)) * h->cap * 8);  // (tiles have 128 columns at least)
+  get(&h->part, (units(vocab, mma::kTile / 2) + units(vocab, h->copied)) * h->cap * 8);  // (tiles have 128 columns at least)
   for (float** p : {&h->lse, &h->factor, &h->at_target}) get(p, h->cap * 4);
   for (int** p : {&h->row, &h->target, &h->exponent, &h->place}) get(p, h->cap * 4);
   get(&h->count, 16);
@@ -669,7 +678,7 @@ extern "C" int psgd_linear_ce_forward(psgd_linear_ce* h, const void* hidden, psg
     return c.e == cudaSuccess ? PSGD_OK : cuda_fail(who.c_str(), c.e);
   }
   c.gather(false, nullptr, 1.f);
-  const long long step = c.in_place ? h->vocab : h->piece;
+  const long long step = c.in_place ? h->vocab : h->copied;
   int parts = 0;
   for (long long v0 = 0; v0 < h->vocab && c.e == cudaSuccess; v0 += step) {
     const long long n = std::min(step, h->vocab - v0);
@@ -713,8 +722,9 @@ extern "C" int psgd_linear_ce_backward(psgd_linear_ce* h, const void* hidden, ps
   Call c(h, hidden, dtype, hidden_stride, weight, weight_stride, targets, target_bits, weights, tokens, stream);
   const int shift = c.bf16 ? 0 : kF16Shift;
   c.gather(true, lse, grad_scale);
-  for (long long v0 = 0; v0 < h->vocab && c.e == cudaSuccess; v0 += h->piece) {
-    const long long n = std::min(h->piece, h->vocab - v0);
+  const long long step = c.in_place ? h->piece : h->copied;
+  for (long long v0 = 0; v0 < h->vocab && c.e == cudaSuccess; v0 += step) {
+    const long long n = std::min(step, h->vocab - v0);
     mma::Product z = c.logits(v0, n), dh{}, dw{};
     c.weight_map(mma::kGrad, z, &dh.b, v0, n);
     z.lse = h->lse, z.factor = h->factor, z.at_target = h->at_target;

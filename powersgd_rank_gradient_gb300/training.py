@@ -389,8 +389,9 @@ class LinearCrossEntropy:
     of ``vocab`` rows of ``dim`` elements, without the logits: they are made tile by
     tile and used where they are made, in the backward pass again.
 
-    ``max_tokens`` bounds the tokens of one call (the handle holds them, a bounded piece of the
-    logits' gradient and partial sums).  Calls on one handle must not overlap on the GPU.
+    ``max_tokens`` bounds the tokens of one call (the handle holds them, bounded pieces of the
+    logits' gradient and of a weight that begins between two 16-byte units, and partial sums: see
+    ``workspace_bytes()``).  Calls on one handle must not overlap on the GPU.
 
     ``hidden`` (..., dim) and ``weight`` (vocab, dim) are float16 or bfloat16, of one
     type; ``targets`` (...) int32 or int64; ``weights`` (...) float32, multiplied into
