@@ -758,8 +758,10 @@ int psgd_rmsnorm_backward(psgd_rmsnorm* n, const void* grad, psgd_dtype dtype, i
 
 /*
  * The weight gradient of a linear layer y = x W^T from its input's 8-bit
- * checkpoint, on the tensor cores.  The handle holds the restored checkpoint and a
- * product's partial sums; calls on one handle must not overlap on the GPU.
+ * checkpoint, on the tensor cores.  The handle holds the restored checkpoint
+ * (2 bytes for max_rows x ins), a piece of a gradient that TMA cannot read where it lies (an address or row stride
+ * that is no multiple of 16 bytes, rows that overlap): at most 32 MB, or 512 MB where outs is no multiple of 8 (or 256 columns),
+ * and a product's partial sums (512 KB for every two SMs).  Calls on one handle must not overlap on the GPU.
  */
 typedef struct psgd_wgrad psgd_wgrad; /* opaque, library-owned */
 

@@ -16,9 +16,10 @@
 struct psgd_wgrad {
   int device = 0, pairs = 0;
   long long outs = 0, ins = 0, most = 0;
-  long long op = 0, ip = 0;         // row strides: multiples of 8 elements
+  long long ip = 0;                 // row stride of x: a multiple of 8 elements
+  long long copied = 0, gp = 0;     // columns that g holds, a multiple of 256 or all; its row stride, a multiple of 8
   void* x = nullptr;                // most x ip, the checkpoint restored
-  void* g = nullptr;                // most x op, a gradient that TMA cannot read in place
+  void* g = nullptr;                // most x gp, a piece of a gradient that TMA cannot read in place
   float* slots = nullptr;
   int* error = nullptr;
   size_t bytes = 0;
@@ -30,6 +31,9 @@ using namespace psgd::ops;
 namespace {
 
 constexpr long long kMostRows = 1 << 24;
+// Of a gradient that TMA cannot read in place.  Rows of whole 16-byte units seldom need it (16384 x 6400 x 1600 in pieces of
+// 32 MB 462 us, whole 323, read in place 226), others mostly do (32768 x 6399 x 256 in two pieces 300 us, whole 274).
+constexpr long long kCopyBytes = 32LL << 20, kOddCopyBytes = 512LL << 20;
 
 // Rows of any stride into rows of `to` words: a CTA takes runs of 2048 words of a row, eight words a thread under way.
 template <typename W> __global__ void __launch_bounds__(256) k_align(const W* src, long long stride, long long rows, int cols, W* dst, long long to, int runs) {
@@ -83,8 +87,12 @@ extern "C" int psgd_wgrad_create(int64_t outs, int64_t ins, int64_t max_rows, in
   h->outs = outs;
   h->ins = ins;
   h->most = max_rows;
-  h->op = units(outs, 8) * 8;
   h->ip = units(ins, 8) * 8;
+  // equal pieces of whole tiles
+  const long long tiles = units(outs, mma::kTile);
+  const long long fit = std::max(1LL, (outs % 8 ? kOddCopyBytes : kCopyBytes) / (std::max<long long>(max_rows, 1) * mma::kTile * 2));
+  h->copied = std::min<long long>(outs, units(tiles, units(tiles, fit)) * mma::kTile);
+  h->gp = units(h->copied, 8) * 8;
   e = mma::pairs_of(device, &h->pairs);
   const auto get = [&](auto** p, long long bytes) {
     bytes = std::max(bytes, 16LL);
@@ -93,7 +101,7 @@ extern "C" int psgd_wgrad_create(int64_t outs, int64_t ins, int64_t max_rows, in
     else *p = nullptr;
   };
   get(&h->x, max_rows * h->ip * 2);
-  get(&h->g, max_rows * h->op * 2);
+  get(&h->g, max_rows * h->gp * 2);
   get(&h->slots, 2 * h->pairs * mma::kSlotFloats * 4);
   get(&h->error, 4);
   if (e == cudaSuccess) e = cudaMemset(h->error, 0, 4);
@@ -140,33 +148,39 @@ extern "C" int psgd_wgrad_backward(psgd_wgrad* h, const void* grad, psgd_dtype d
     return fail(PSGD_EINVAL, who + ": dweight overlaps another operand");
   DeviceScope scope(h->device);
   const cudaStream_t st = (cudaStream_t)stream;
-  cudaError_t e = cudaSuccess;
+  long long piece = h->outs;  // columns of the gradient that a product takes
+  bool copy = false;
   if (rows > 0) {
     const int rc = psgd_activation_restore(codes, code, scales, rows, h->ins, h->x, dtype, h->ip, h->device, stream);
     if (rc) return rc;
-    if (rows == 1 && aligned16(grad)) grad_stride = h->op;  // of one row no stride counts
-    if (!mma::in_place(grad, grad_stride, h->outs)) {
-      e = mma::align_rows(grad, grad_stride, rows, h->outs, h->g, h->op, st);
-      grad = h->g;
-      grad_stride = h->op;
-    }
-  } else {
-    grad = h->g;
-    grad_stride = h->op;
+    if (rows == 1 && aligned16(grad)) grad_stride = units(h->outs, 8) * 8;  // of one row no stride counts
+    copy = !mma::in_place(grad, grad_stride, h->outs);
+    if (copy) piece = h->copied;
+  } else {  // (a map needs an address, which nothing is read from)
+    grad = h->x;
+    grad_stride = units(h->outs, 8) * 8;
   }
   mma::Product p{};
-  const bool bf16 = dtype == PSGD_BF16;
-  if (e == cudaSuccess) e = mma::make_map(&p.a, grad, rows, h->outs, grad_stride, mma::box_rows(true), bf16);
-  if (e == cudaSuccess) e = mma::make_map(&p.b, h->x, rows, h->ins, h->ip, mma::box_rows(true), bf16);
-  if (e != cudaSuccess) return cuda_fail(who.c_str(), e);
-  p.m = (int)h->outs, p.n = (int)h->ins, p.k = (int)rows;
+  p.bf16 = dtype == PSGD_BF16;
+  p.n = (int)h->ins, p.k = (int)rows;
   p.a_m_rows = p.b_m_rows = 1;
-  p.bf16 = bf16;
   p.error = h->error;
-  p.out = dweight, p.ldo = dweight_stride, p.dtype = dweight_dtype, p.accumulate = accumulate != 0;
+  p.ldo = dweight_stride, p.dtype = dweight_dtype, p.accumulate = accumulate != 0;
   p.slots = h->slots;
   p.chunk = mma::chunk_of(rows, dweight_dtype);
-  e = mma::enqueue(mma::kOut, p, h->device, h->pairs, st);
+  cudaError_t e = mma::make_map(&p.b, h->x, rows, h->ins, h->ip, mma::box_rows(true), p.bf16);
+  for (long long first = 0; first < h->outs && e == cudaSuccess; first += piece) {
+    const long long n = std::min(piece, h->outs - first);
+    const void* from = (const char*)grad + first * 2;
+    if (copy) {
+      e = mma::align_rows(from, grad_stride, rows, n, h->g, h->gp, st);
+      from = h->g;
+    }
+    if (e == cudaSuccess) e = mma::make_map(&p.a, from, rows, n, copy ? h->gp : grad_stride, mma::box_rows(true), p.bf16);
+    p.m = (int)n;
+    p.out = (char*)dweight + first * dweight_stride * dtype_size(dweight_dtype);
+    if (e == cudaSuccess) e = mma::enqueue(mma::kOut, p, h->device, h->pairs, st);
+  }
   return e == cudaSuccess ? PSGD_OK : cuda_fail(who.c_str(), e);
 }
 

@@ -336,7 +336,8 @@ class LinearWeightGrad:
     of ``in_features`` elements, from an 8-bit checkpoint of x.
 
     ``max_tokens`` bounds the rows of one call (the handle holds the restored
-    checkpoint and a product's partial sums; layers of one shape may share it).
+    checkpoint, a bounded piece of a gradient that begins between two 16-byte units and a
+    product's partial sums; layers of one shape may share it).
     Calls on one handle must not overlap on the GPU."""
 
     def __init__(self, out_features, in_features, max_tokens, device=None):

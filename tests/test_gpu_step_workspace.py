@@ -74,3 +74,31 @@ def test_a_handle_of_just_so_many_tokens(tokens):
         (wh, ww), (eh, ew) = su.loss_backward(hidden[:n], weight, targets[:n], lse, None)
         su.check_out(dh, wh, eh, BF16)
         su.check_out(dw, ww, ew, F32)
+
+
+@pytest.mark.parametrize("outs,ins,rows", [(6400, 1600, 16384), (1024, 1024, 509), (2048, 64, 300000)])
+def test_a_weight_gradient_holds_no_gradient(outs, ins, rows):
+    from powersgd_rank_gradient_gb300 import LinearWeightGrad
+
+    h = LinearWeightGrad(outs, ins, rows, device=DEV)
+    # the checkpoint restored, a copied piece (256 columns at least), partial sums
+    assert h.workspace_bytes() <= rows * ins * 2 + max(32 * MB, rows * 512) + sums() + 64
+    h.close()
+
+
+@pytest.mark.parametrize("odtype,accumulate", [(F32, False), (BF16, True)])
+@pytest.mark.parametrize("rows,outs,ins", [(9000, 3000, 72), (30000, 1096, 200)])
+def test_gradients_that_are_copied_in_pieces(rows, outs, ins, odtype, accumulate):
+    """Rows of whole units that begin between two of them: more than 32 MB."""
+    from powersgd_rank_gradient_gb300 import LinearWeightGrad, save_activation
+
+    gen = torch.Generator(device=DEV).manual_seed(outs)
+    grad = torch.randn(rows * outs + 3, device=DEV, generator=gen).to(BF16)[3:].view(rows, outs)
+    kept = save_activation(torch.randn((rows, ins), device=DEV, generator=gen).to(BF16))
+    before = torch.randn((outs, ins), device=DEV, generator=gen).to(odtype)
+    h = LinearWeightGrad(outs, ins, rows, device=DEV)
+    assert h.workspace_bytes() < rows * ins * 2 + grad.numel() * 2 + sums()
+    out = h.backward(grad, kept, out=before.clone(), accumulate=accumulate)
+    h.status()
+    want, err = su.product(grad, kept.restore(F32), before=before if accumulate else None)
+    su.check(out, want, su.out_tol(err, want, odtype))
