@@ -89,12 +89,14 @@ struct Items {  // eight tokens' targets (-1 for a token that does not count) an
     for (int k = 0; k < kPlanItems; ++k) target[k] = y[k] >= 0 && y[k] < t.vocab && weight[k] != 0.f ? (int)y[k] : -1;
   }
 };
-__device__ void plan(const Tokens& t, int* place, int* row, int* target, float* factor, int* exponent, int* count, float* scale,
-                     float grad_scale, int shift) {
+__global__ void __launch_bounds__(1024) k_plan(Tokens t, int* place, int* row, int* target, float* factor, int* exponent, int* count,
+                                               float* scale, float grad_scale, int shift) {
   __shared__ int sums[32];
   __shared__ float most[32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   constexpr int kTurn = 1024 * kPlanItems;
+  after_previous();
+  next_may_launch();
   // the largest weight
   Items mine(t, (int)threadIdx.x * kPlanItems);
   float top = 0.f;
@@ -217,14 +219,26 @@ template <typename T> struct Gather {
   int vec_dot;
   float* at_target;  // forward: the target's logit, backward: exp(it - lse) - 1
 };
-template <typename T, int V> __device__ __forceinline__ void gather_rows(const Gather<T>& a, int first, int step, int thread, int threads) {
-  const int n = a.count[0], end = a.hs ? (n + mma::kStep - 1) / mma::kStep * mma::kStep : n;
-  for (int r = first; r < end; r += step) {
+// Four warps copy a row while the fifth sums its target's logit.
+constexpr int kGatherThreads = 160;
+template <typename T, int V> __global__ void __launch_bounds__(kGatherThreads) k_gather(Gather<T> a) {
+  after_previous();
+  next_may_launch();
+  const int n = a.count[0], thread = threadIdx.x;
+  if (thread >= 128) {
+    for (int r = blockIdx.x; r < n; r += gridDim.x) {
+      const float z = warp_dot(a.src + (long long)a.row[r] * a.stride, a.weight + a.target[r] * a.weight_stride, a.dim, a.vec_dot);
+      if (thread == 128) a.at_target[r] = a.hs ? expm1f(z - a.lse_of[a.row[r]]) : z;
+    }
+    return;
+  }
+  const int end = a.hs ? (n + mma::kStep - 1) / mma::kStep * mma::kStep : n;
+  for (int r = blockIdx.x; r < end; r += gridDim.x) {
     const bool in = r < n;
     const T* from = a.src + (in ? (long long)a.row[r] * a.stride : 0);
     const float f = in && a.hs ? scalbnf(1.f, max(a.exponent[r] - a.count[1], -200)) : 1.f;
     if (a.lse && in && thread == 0) a.lse[r] = a.lse_of[a.row[r]];
-    for (int c = thread * V; c < a.dim; c += threads * V) {
+    for (int c = thread * V; c < a.dim; c += 128 * V) {
       if constexpr (V == 1) {
         const T x = in ? from[c] : from_f<T>(0.f);
         a.h[r * a.dp + c] = x;
@@ -245,39 +259,6 @@ template <typename T, int V> __device__ __forceinline__ void gather_rows(const G
       }
     }
   }
-}
-// by whole warps
-template <typename T> __device__ __forceinline__ void gather_logits(const Gather<T>& a, int first, int step) {
-  const int n = a.count[0];
-  for (int r = first; r < n; r += step) {
-    const float z = warp_dot(a.src + (long long)a.row[r] * a.stride, a.weight + a.target[r] * a.weight_stride, a.dim, a.vec_dot);
-    if ((threadIdx.x & 31) == 0) a.at_target[r] = a.hs ? expm1f(z - a.lse_of[a.row[r]]) : z;
-  }
-}
-// Four warps copy a row while the fifth sums its target's logit.
-template <typename T, int V> __global__ void __launch_bounds__(160) k_gather(Gather<T> a) {
-  after_previous();
-  next_may_launch();
-  if (threadIdx.x < 128) gather_rows<T, V>(a, blockIdx.x, gridDim.x, threadIdx.x, 128);
-  else gather_logits(a, blockIdx.x, gridDim.x);
-}
-__global__ void __launch_bounds__(1024) k_plan(Tokens t, int* place, int* row, int* target, float* factor, int* exponent, int* count,
-                                               float* scale, float grad_scale, int shift) {
-  after_previous();
-  next_may_launch();
-  plan(t, place, row, target, factor, exponent, count, scale, grad_scale, shift);
-}
-// Both in one launch, where the rows are few enough for one CTA, a warp a row.
-constexpr int kFewTokens = 32;
-template <typename T, int V>
-__global__ void __launch_bounds__(1024) k_plan_gather(Tokens t, int* place, int* row, int* target, float* factor, int* exponent, int* count,
-                                                      float* scale, float grad_scale, int shift, Gather<T> a) {
-  after_previous();
-  next_may_launch();
-  plan(t, place, row, target, factor, exponent, count, scale, grad_scale, shift);
-  __syncthreads();
-  gather_rows<T, V>(a, threadIdx.x >> 5, 32, threadIdx.x & 31, 32);
-  gather_logits(a, threadIdx.x >> 5, 32);
 }
 
 // Two entries of largest logit and sum of exponentials as one.  (An entry without a logit above -infinity has a sum of 0,
@@ -499,9 +480,7 @@ struct Call {
   void gather(bool backward, const float* lse, float grad_scale) {
     const int shift = bf16 ? 0 : kF16Shift;
     const bool vec = h->dim % 8 == 0 && aligned16(hidden) && hidden_stride % 8 == 0;
-    const bool few = t.tokens <= kFewTokens;
-    if (!few)
-      e = launch_early(k_plan, 1, 1024, 0, 1, st, t, h->place, h->row, h->target, h->factor, h->exponent, h->count, h->scale, grad_scale, shift);
+    e = launch_early(k_plan, 1, 1024, 0, 1, st, t, h->place, h->row, h->target, h->factor, h->exponent, h->count, h->scale, grad_scale, shift);
     if (e != cudaSuccess) return;
     const auto go = [&](auto* tt, auto v) {
       using T = std::remove_pointer_t<decltype(tt)>;
@@ -509,11 +488,7 @@ struct Call {
       const Gather<T> a{(const T*)hidden, hidden_stride, (int)h->dim, h->row, h->target, h->exponent, h->count, (T*)h->h,
                         backward ? (T*)h->hs : nullptr, h->dp, lse, backward ? h->lse : nullptr, (const T*)weight, weight_stride,
                         vec && in_place, h->at_target};
-      if (few)
-        e = launch_early(k_plan_gather<T, V>, 1, 1024, 0, 1, st, t, h->place, h->row, h->target, h->factor, h->exponent, h->count, h->scale,
-                         grad_scale, shift, a);
-      else
-        e = launch_early(k_gather<T, V>, (unsigned)std::min(t.tokens + mma::kStep, 4096), 160, 0, 1, st, a);
+      e = launch_early(k_gather<T, V>, (unsigned)std::min(t.tokens + mma::kStep, 4096), kGatherThreads, 0, 1, st, a);
     };
     using One = std::integral_constant<int, 1>;
     using Eight = std::integral_constant<int, 8>;
