@@ -279,9 +279,10 @@ __device__ __forceinline__ float2 loss_of(float2 others, float z) {
 
 // The forward pass of at most N tokens, in one launch and without the tensor cores: a tile's 256 rows would be idle, and
 // what comes before and after a product would take half as long as it does.  A warp reads whole rows of the weight, four
-// at a time (one token over 50257 x 1600 bf16: 33 us, 4.9 TB/s), and keeps its own largest logit and sum of exponentials for
+// at a time (one token over 50257 x 1600 bf16: 35 us from call to call, 4.6 TB/s), and keeps its own largest logit and sum of exponentials for
 // each token; the CTA that is done last adds the CTAs' entries up, always in the same order.
 constexpr int kFewDim = 8192;
+constexpr long long kFewTable = 1 << 25;  // elements, for more than two tokens
 template <typename T, int N>
 __global__ void __launch_bounds__(256, N == 1 ? 4 : 2) k_losses_few(Tokens t, const T* hidden, long long hidden_stride, const T* weight, long long stride,
                                                                     int dim, float2* part, float* at_target, int* done, float* losses, float* lses) {
@@ -630,9 +631,10 @@ extern "C" int psgd_linear_ce_forward(psgd_linear_ce* h, const void* hidden, psg
   if (tokens == 0) return PSGD_OK;
   DeviceScope scope(h->device);
   Call c(h, hidden, dtype, hidden_stride, weight, weight_stride, targets, target_bits, weights, tokens, stream);
-  // few tokens: one launch.  In place of the products, over 50257 x 1600 bf16 one token 34 us (48), four 53 (50); over
-  // 30522 x 1024 18 (28) and 26 (29), over 5000 x 256 7 (15) and 12 (15).
-  if (tokens <= 4 && c.in_place && h->dim % 8 == 0 && h->dim <= kFewDim) {
+  // Few tokens: one launch in place of a product's four.  Over 50257 x 1600 bf16 one token 35 us (47 by products), two 39 (47), three and
+  // four 53 and 55 (47); over 30522 x 1024 19 (29), 19 (29), 27 and 28 (29); over 5000 x 256 7 (15), 8 (15), 12 and 13 (15): with
+  // three or four tokens a row's arithmetic takes longer than its bytes, and only small tables gain.
+  if (tokens <= (h->vocab * h->dim <= kFewTable ? 4 : 2) && c.in_place && h->dim % 8 == 0 && h->dim <= kFewDim) {
     const unsigned grid = (unsigned)std::min<long long>(units(h->vocab, mma::kTile / 2), h->pairs * 2 * (tokens == 1 ? 4 : 2));
     const auto go = [&](auto* tt, auto count) {
       using T = std::remove_pointer_t<decltype(tt)>;
