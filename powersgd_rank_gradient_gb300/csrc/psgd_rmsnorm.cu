@@ -710,15 +710,16 @@ Plan plan_of(long long dim, int e) {
   }
   return p;
 }
-// f(units of a thread, rows of a turn) for rows of whole units: `r1` rows where a thread has one unit of each, or one
-// row where there are few; f(units) for any rows.
+// f(units of a thread, rows of a turn) for rows of whole units: `r1` rows where a thread has one unit of each, or one row
+// where there are few, that is, no more than groups on all SMs: 300 x 1024 bf16 forward 2.1 us (two rows 2.5), backward 4.6
+// (4.9), but 1216 x 1600 3.3 with two rows (3.6 with one), backward 7.0 (7.8), and 9728 x 1600 backward 23.7 (28.5).
 template <typename T, int R1, typename F> void by_vec_plan(const Plan& p, bool few, F&& f) {
   if (p.nv == 1) few ? f(Int<1>(), Int<1>()) : f(Int<1>(), Int<R1>());
   else if (p.nv == 2) f(Int<2>(), Int<(R1 + 1) / 2>());
   else if constexpr (Vec16<T>::N * 4 <= kElements) f(Int<4>(), Int<1>());
 }
-// f(units of a thread, rows of a turn) for any rows, whose `arrays` (and scales) have to fit into shared memory; false
-// where not even one row of each does.
+// The same for any rows (300 x 1023 bf16 forward 3.0 us one row a turn, 4.3 four, backward 6.1 and 6.5; 1216 rows 5.8 and 4.4, 10.3
+// and 7.1), whose `arrays` (and scales) have to fit into shared memory; false where not even one row of each does.
 template <typename F> bool by_any_plan(const Plan& p, bool few, int size, int arrays, int blocks, int& bytes, F&& f) {
   const int slot = slot_bytes(p.threads / 32 * p.nv * kBlock8, size);
   const auto fits = [&](int r) {
@@ -893,7 +894,7 @@ extern "C" int psgd_rmsnorm_forward(psgd_rmsnorm* h, const void* x, psgd_dtype d
   cudaError_t e = cudaSuccess;
   by_dtype(dtype, [&](auto* tt) {
     using T = std::remove_pointer_t<decltype(tt)>;
-    const bool few = rows <= 4LL * h->sms * std::max(p.groups, 1);
+    const bool few = rows <= (long long)h->sms * std::max(p.groups, 1);
     int bytes = 0;
     if (p.nv && vec) {
       by_vec_plan<T, 2>(p, few, [&](auto nv, auto r) {
@@ -956,7 +957,7 @@ extern "C" int psgd_rmsnorm_backward(psgd_rmsnorm* h, const void* grad, psgd_dty
   if (rows > 0)
     by_dtype(dtype, [&](auto* tt) {
       using T = std::remove_pointer_t<decltype(tt)>;
-      const bool few = rows <= 4LL * h->sms * std::max(p.groups, 1);
+      const bool few = rows <= (long long)h->sms * std::max(p.groups, 1);
       int bytes = 0;
       if (vec && p.nv && p.nv < 4) {  // (three arrays of four units have no room for their turns)
         by_vec_plan<T, 2>(p, few, [&](auto nv, auto r) {
