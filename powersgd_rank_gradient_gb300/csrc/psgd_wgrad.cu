@@ -35,7 +35,8 @@ constexpr long long kMostRows = 1 << 24;
 // 32 MB 462 us, whole 323, read in place 226), others mostly do (32768 x 6399 x 256 in two pieces 300 us, whole 274).
 constexpr long long kCopyBytes = 32LL << 20, kOddCopyBytes = 512LL << 20;
 
-// Rows of any stride into rows of `to` words: a CTA takes runs of 2048 words of a row, eight words a thread under way.
+// Rows of any stride into rows of `to` words: a CTA takes runs of 2048 words of a row, eight words a thread under way (a
+// weight gradient from 4961 x 5114 43 us, with four 42, with sixteen 40; from 16384 x 1001 31, 31 and 39).
 template <typename W> __global__ void __launch_bounds__(256) k_align(const W* src, long long stride, long long rows, int cols, W* dst, long long to, int runs) {
   after_previous();
   next_may_launch();
