@@ -777,8 +777,8 @@ size_t psgd_wgrad_workspace_bytes(const psgd_wgrad* w);
  * (psgd_activation_save) rounded to grad's type (exact in bf16; in f16 while it is in
  * range).
  *
- *   grad          : `rows` rows of outs elements, F16 or BF16 (the tensor cores
- *                   multiply 16-bit operands; sums are fp32).
+ *   grad          : `rows` rows of outs elements, F16 or BF16 (the products are of
+ *                   16-bit operands; sums are fp32).
  *   codes, scales : `rows` rows of ins elements.
  *   dweight       : outs rows of ins elements, dweight_stride apart, at any
  *                   element offset.  Without rows it becomes 0 (unchanged with
@@ -817,8 +817,8 @@ size_t psgd_linear_ce_workspace_bytes(const psgd_linear_ce* c);
  *   lse_t    = log sum_v exp(z_tv),
  *   losses_t = w_t (lse_t - z_t,target).
  *
- *   hidden  : `tokens` rows of dim elements, F16 or BF16 (the tensor cores
- *             multiply 16-bit operands; sums are fp32).
+ *   hidden  : `tokens` rows of dim elements, F16 or BF16 (the products are of
+ *             16-bit operands; sums are fp32).
  *   weight  : vocab rows of dim elements of the same type.
  *   targets : target_bits (32 or 64) bit signed integers, without gaps.
  *   weights : w, one float a token; NULL: 1.
@@ -839,7 +839,8 @@ int psgd_linear_ce_forward(psgd_linear_ce* c, const void* hidden, psgd_dtype dty
  * The logits are computed again.  exp(z - lse) - [v = target], times r_t, is rounded
  * once to the operands' type before both products, where w_t = s r_t 2^e with s the
  * significand of the largest weight and 1 <= |r_t| < 2; hidden_t takes the power of two,
- * relative to the largest.
+ * relative to the largest.  At the target it is exp(z - lse) - 1 without a cancellation but that of lse's own
+ * rounding (z is the forward pass's), so a likely target's 1 - p is there to 2^-24 |lse|.
  *
  *   hidden, weight, targets, weights : as in the forward pass; lse: its output.
  *   dhidden : out, rows of the operands' type; may be NULL.  0 for a token that

@@ -2,7 +2,7 @@
 // in the same kernel: the pieces of a log-sum-exp, the gradient of a softmax cross
 // entropy, or the sums' rounding into a bucket.
 //
-// Persistent pairs of CTAs.  In each, one thread loads (TMA, five stages of 32 KB),
+// Persistent pairs of CTAs.  In each, one thread loads (TMA, 160 KB in five stages, or up to ten of fewer rows or columns),
 // one thread of the first CTA multiplies (tcgen05, both CTAs' tensor memory), and
 // sixteen warps take finished tiles, 32 rows of 64 columns each, out of tensor
 // memory while the next tile is summed in its other half.
@@ -31,7 +31,7 @@ struct Run {
   int tm, tn, k0, k1, slot, width;
 };
 // A pair's i-th run; false behind the last.  The schedule is in shared memory: in the registers of the warps that drain
-// it pushed some of their 64 sums out into local memory, which cost up to 10 us a tile.
+// it pushed some of their 64 sums out into local memory, which cost up to 10 us a tile (one word of an OUT kernel still is).
 __device__ __forceinline__ bool run_of(const Product& p, const Schedule& s, int pairs, int pair, int i, Run& r) {
   int tile = pair + i * pairs;
   r.k0 = 0;
@@ -562,8 +562,8 @@ static int columns_of(const Product& p, int pairs) {
   return best;
 }
 
-// A step costs as its rows and columns; the last turn's pairs without a tile idle.  For a token over 50257 columns, 197 tiles
-// of 256 on 76 pairs are 3 turns, 225 of 224 as many.  GRAD leaves boxes of 64 columns.
+// A step costs as its rows and columns; the last turn's pairs without a tile idle.  For up to 256 tokens over 50257 columns,
+// 197 tiles of 256 on 76 pairs are 3 turns, 225 of 224 as many.  GRAD leaves boxes of 64 columns.
 int logits_columns(Epilogue kind, long long rows, long long n, int pairs) {
   int best = kTile;
   long long least = 0;
@@ -578,9 +578,8 @@ int logits_columns(Epilogue kind, long long rows, long long n, int pairs) {
 }
 
 cudaError_t enqueue(Epilogue kind, Product p, int device, int pairs, cudaStream_t st) {
-  // (the others' columns go by 128)
-  if (kind == kOut) p.bn = columns_of(p, pairs);
-  if (kind == kOut) {
+  if (kind == kOut) {  // (the others' callers know theirs, of which B's boxes have half)
+    p.bn = columns_of(p, pairs);
     const int size = 4 * ops::dtype_size(p.dtype);
     p.vec = (uintptr_t)p.out % size == 0 && (p.ldo % 4 == 0 || p.m == 1);
   }

@@ -6,7 +6,7 @@
 // bf16 exactly: 4 significant bits times a power of two), and the product runs
 // on the tensor cores with both operands as they lie, the summed dimension being
 // the rows (psgd_gemm.cu).  Products of 16-bit values are exact in fp32 and the sums
-// fp32, so a bucket in fp32 gets an fp32 gradient.
+// fp32, taken out of the tensor cores where they are long, so a bucket in fp32 gets an fp32 gradient.
 #include <algorithm>
 #include <new>
 #include <type_traits>
