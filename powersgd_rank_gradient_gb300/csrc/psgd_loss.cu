@@ -524,7 +524,7 @@ struct Call {
     p.column0 = (int)v0, p.vocab = (int)h->vocab;
     p.target = h->target;
     // a logit of one sign loses 1e-7 of itself for every 16 elements of a row (see chunk_of): rows of 2048 1.3e-5, as library
-    // products with sums on the tensor cores do, longer ones 4e-6 and no more.  (For 1600 elements it would cost 4 %: the
+    // products with sums on the tensor cores do, longer ones 6e-6 and no more.  (For 1600 elements it would cost 4 %: the
     // losses of 8192 tokens of GPT-2-XL 774 -> 805 us.)
     p.chunk = h->dim > 2048 ? 16 : 0;
     if (e == cudaSuccess) e = mma::make_map(&p.a, h->h, h->cap, h->dim, h->dp, mma::box_rows(false), bf16);

@@ -249,8 +249,8 @@ __host__ __device__ inline int width_of(int n, int bn, int tn) {
 
 // Steps of the summed dimension (of k elements) that the tensor cores sum by themselves, 0: all.  They cut sums off where
 // fp32 would round them: a sum of one sign with operands of 11 bits loses 1e-7 of itself for every 16 elements (16384
-// rows 5e-5; gradients of both signs with 8-bit activations 8e-6).  Taken out every 1024 elements and added in
-// rounded fp32 it loses 3e-6 however long it is (7e-7).  So for fp32 results always; for results of 16 bits where a sum of one
+// rows 1e-4; gradients of both signs with 8-bit activations 8e-6).  Taken out every 1024 elements and added in
+// rounded fp32 it loses 6e-6 however long it is (7e-7).  So for fp32 results always; for results of 16 bits where a sum of one
 // sign could lose an eighth of half a step of theirs (2^-12 and 2^-9) otherwise: sums that are taken out cost GPT-2-XL's
 // gradients 2 % (2050 -> 2100 us) and 16384 rows' bf16 weight gradient as much (263 -> 267).
 inline int chunk_of(long long k, int dtype) {
